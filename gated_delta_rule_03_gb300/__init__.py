@@ -4,6 +4,8 @@ The compute path is the C-ABI library `libgdr.so` (hand-written sm_103a CUDA,
 declared in include/gdr.h). This package is a thin binding over it:
 
     from gated_delta_rule_03_gb300 import chunk_fwd, decode_step
+    from gated_delta_rule_03_gb300 import linattn_fwd, linattn_bwd, linattn_step
+    from gated_delta_rule_03_gb300 import block_norm_fwd, block_norm_bwd
 
 Importing the package loads nothing; the first call loads the library and
 raises if it is missing. There is no CPU fallback. The submodule `inputs`
@@ -11,12 +13,16 @@ raises if it is missing. There is no CPU fallback. The submodule `inputs`
 """
 _OPS = ("GdrError", "chunk_fwd", "chunk_fwd_workspace_size", "decode_step", "library_path",
         "read_device_status", "status_string")
+_LINATTN = ("linattn_fwd", "linattn_fwd_workspace_size", "linattn_bwd", "linattn_bwd_workspace_size",
+            "linattn_step")
+_BLOCK_NORM = ("block_norm_fwd", "block_norm_bwd", "block_norm_bwd_workspace_size")
 
-__all__ = list(_OPS)
+__all__ = list(_OPS + _LINATTN + _BLOCK_NORM)
 
 
 def __getattr__(name):
-    if name in _OPS:
-        from . import ops
-        return getattr(ops, name)
+    for names, module in ((_OPS, "ops"), (_LINATTN, "linattn"), (_BLOCK_NORM, "block_norm")):
+        if name in names:
+            from importlib import import_module
+            return getattr(import_module("." + module, __name__), name)
     raise AttributeError(name)

@@ -1,0 +1,165 @@
+// linattn.cuh -- what the kernels of linear attention with a constant decay per head share.
+//
+// With lam = exp(log_decay[h]), per sequence and head:
+//   S_t = lam S_{t-1} + k_t v_t^T,   o_t = scale S_t^T q_t.
+// Backward, with D_t the gradient of S_t (D_T = dS_final for the last token T):
+//   D_t = lam D_{t+1} + scale q_t do_t^T,   dq_t = scale S_t do_t,
+//   dk_t = D_t v_t,   dv_t = D_t^T k_t,   dS0 = lam D_1.
+//
+// All four are one "mix" of rows x, y (d_x entries) and z (d_z entries) around a state
+// E [d_x][d_z]. A chunk of n tokens (rows r = 0 .. n-1), entered with E, gives
+//   out_r = s_intra sum_i M_ri lam^|r-i| (x_r.y_i) z_i + s_inter w_out(r) x_r E
+//   E    <- lam^n E + s_state sum_r w_upd(r) y_r z_r^T
+// with
+//                 x    y    z    state    order    M_ri     w_out      w_upd
+//   o             q    k    v    S        first    i <= r   lam^(r+1)  lam^(n-1-r)
+//   dq            do   v    k    S^T      to last  i <= r   lam^(r+1)  lam^(n-1-r)
+//   dv            k    q    do   E        last     i >= r   lam^(n-1-r) lam^(r+1)
+//   dk            v    do   q    E^T      to first i >= r   lam^(n-1-r) lam^(r+1)
+// where E = lam D_{t+1} is the state carried backwards (so that its start value is
+// dS_final and its last value dS0), and s_intra = scale; s_inter, s_state = scale, 1 from
+// first to last and 1, scale from last to first. Every power of lam has an exponent >= 0.
+//
+// Segments. Without a gate that depends on the tokens, the state after a run of tokens is
+// lam^n times the state before it plus a sum that does not depend on that state. A sequence
+// is cut into segments of `seg` tokens (the last one shorter). A first launch computes every
+// segment's own sum R_f; in the second every segment starts from
+//   first to last:  lam^(f seg) S0 + sum_{g<f} lam^((f-1-g) seg) R_g
+//   last to first:  lam^(tokens behind f) dS_final + sum_{g>f} lam^((g-1-f) seg) R_g
+// and all segments run at once. With one segment per sequence the first launch is left out.
+#pragma once
+
+#include "internal.h"
+
+namespace gdr {
+namespace linattn {
+
+constexpr int kTile = 128;        // segments are a multiple of this many tokens
+constexpr float kLog2e = 1.4426950408889634f;
+
+// One mix of a launch.
+struct Mix {
+    const void *x, *y, *z;
+    int64_t xs, ys, zs;     // elements from one token's rows to the next token's
+    int xg, yg, zg;         // heads of the state that share one head of x, y, z
+    void *out;              // [total_tokens, H, d_z], or null (state only)
+    bool out_f32;           // out in fp32 whatever the input type (partial sums)
+    int dx, dz;
+    bool turned;            // the state in memory is [d_z][d_x] (S^T, E^T)
+    bool backward;          // from the last token to the first
+    float s_intra, s_inter, s_state;
+    const float *start;     // S0 or dS_final, [num_seqs, H] matrices, or null
+    float *end;             // S_final or dS0, or null
+    const float *R;         // the segments' own sums, [item, H] matrices (null: one segment)
+    float *R_out;           // state only: where they go
+};
+
+// The sequences and segments of a call.
+struct Plan {
+    const int32_t *cu_seqlens;  // null: equal lengths
+    int64_t num_seqs, total_tokens;
+    int64_t seg;                // tokens per segment (a multiple of kTile)
+    int64_t seq_len;            // equal lengths
+    int segs;                   // segments per sequence (equal lengths)
+    int64_t items;              // segments in all (packed: an upper bound)
+    int H;
+    const float *log_decay;
+    int32_t *status;            // the workspace's status word
+    bool first;                 // the call's first launch: it sets the status word
+};
+
+struct Segment {
+    int seq;        // -1: nothing to do
+    int f, n;       // this segment's number and the sequence's count
+    int64_t begin;  // first token of the segment
+    int64_t tokens; // its tokens
+    int64_t behind; // tokens of the sequence behind it
+    int64_t item0;  // the sequence's first item
+};
+
+// Which segment item `item` is; called by the whole block (a barrier inside). With
+// cu_seqlens every block checks all of it (offsets from 0, not decreasing, at most
+// total_tokens); where it is not so, no block does anything and `bad` is set.
+__device__ __forceinline__ Segment locate(const Plan &p, int64_t item, Segment *shared, bool *bad) {
+    *bad = false;
+    auto fill = [&](int seq, int f, int n, int64_t first, int64_t len, int64_t item0) {
+        Segment s;
+        s.seq = seq;
+        s.f = f;
+        s.n = n;
+        s.begin = first + (int64_t)f * p.seg;
+        const int64_t rest = len - (int64_t)f * p.seg;
+        s.tokens = rest < p.seg ? rest : p.seg;
+        s.behind = rest - s.tokens;
+        s.item0 = item0;
+        return s;
+    };
+    if (!p.cu_seqlens) {
+        const int seq = (int)(item / p.segs), f = (int)(item % p.segs);
+        return fill(seq, f, p.segs, (int64_t)seq * p.seq_len, p.seq_len, item - f);
+    }
+    __shared__ int64_t warp_sum[32];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = (blockDim.x + 31) >> 5;
+    if (tid == 0) shared->seq = -1;
+    int64_t carry = 0;
+    int wrong = 0;
+    for (int64_t base = 0; base < p.num_seqs; base += blockDim.x) {
+        const int64_t n = base + tid;
+        int64_t a = 0, len = 0, count = 0;
+        if (n < p.num_seqs) {
+            a = p.cu_seqlens[n];
+            len = (int64_t)p.cu_seqlens[n + 1] - a;
+            if (len < 0 || a < 0 || a + len > p.total_tokens || (n == 0 && a != 0)) {
+                wrong = 1;
+            } else {
+                count = (len + p.seg - 1) / p.seg;
+                if (count < 1) count = 1;  // an empty sequence still hands on its state
+            }
+        }
+        int64_t sum = count;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const int64_t up = __shfl_up_sync(0xffffffffu, sum, off);
+            if (lane >= off) sum += up;
+        }
+        if (lane == 31) warp_sum[warp] = sum;
+        __syncthreads();
+        int64_t before = 0, total = 0;
+        for (int w = 0; w < warps; ++w) {
+            if (w < warp) before += warp_sum[w];
+            total += warp_sum[w];
+        }
+        const int64_t first_item = carry + before + sum - count;
+        if (count > 0 && item >= first_item && item < first_item + count)
+            *shared = fill((int)n, (int)(item - first_item), (int)count, a, len, first_item);
+        carry += total;
+        __syncthreads();
+    }
+    *bad = __syncthreads_or(wrong) != 0;
+    return *shared;
+}
+
+// log2 of the decay, held finite so that 0 * log2(lam) is 0 for lam = 0 (-inf); NaN stays.
+__device__ __forceinline__ float log2_decay(float log_decay) {
+    return log_decay < -1e30f ? -1e30f : log_decay * kLog2e;
+}
+// lam^n for n >= 0. The product's rounding shifts the result by |n log2 lam| 2^-24 of
+// itself at most, where the power itself has shrunk to 2^-|n log2 lam|.
+__device__ __forceinline__ float decay_pow(float l2, float n) { return exp2f(l2 * n); }
+
+// Element (a, b) of a state matrix [d_x][d_z], or of its transpose in memory.
+__device__ __forceinline__ int64_t state_at(const Mix &m, int a, int b) {
+    return m.turned ? (int64_t)b * m.dx + a : (int64_t)a * m.dz + b;
+}
+
+int launch_mix_exact(const Plan &p, const Mix *mixes, int count, int dtype, cudaStream_t stream);
+// Sums the heads that share one head: in fp32 [rows, H, d] -> out [rows, H / g, d]. Rows
+// behind the last sequence are left as they are.
+int launch_share(const Plan &p, const float *in, void *out, int g, int d, int dtype,
+                 cudaStream_t stream);
+int launch_step(const void *q, const void *k, const void *v, const float *log_decay, float *S,
+                void *o, int64_t N, int H, int qg, int kg, int vg, int dk, int dv, int dtype,
+                float scale, int64_t qs, int64_t ks, int64_t vs, cudaStream_t stream);
+
+}  // namespace linattn
+}  // namespace gdr

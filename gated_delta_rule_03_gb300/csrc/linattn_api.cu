@@ -1,0 +1,333 @@
+// linattn_api.cu -- C ABI of linear attention with a constant decay per head: checks of the
+// arguments, the segments of a call, the workspace and the launches.
+#include <math.h>
+#include <string.h>
+
+#include "linattn.cuh"
+
+namespace gdr {
+namespace linattn {
+namespace {
+
+size_t align_up(size_t x) { return (x + 255) / 256 * 256; }
+
+struct Call {
+    int64_t N, T;
+    int H, qh, kh, vh, dk, dv, dtype;
+    float scale;
+    int64_t qs, ks, vs;
+    size_t e;  // bytes per element
+    size_t state() const { return (size_t)N * H * dk * dv * sizeof(float); }
+};
+
+int check_stride(int64_t given, int heads, int d, size_t e, int64_t *out) {
+    const int64_t dense = (int64_t)heads * d;
+    *out = given == 0 ? dense : given;
+    if (*out < dense || *out > INT32_MAX) return GDR_ERR_INVALID_ARG;
+    return (*out * (int64_t)e) % 16 == 0 ? GDR_OK : GDR_ERR_ALIGNMENT;
+}
+
+int check_shape(const gdr_linattn_shape *s, Call *c) {
+    if (!s || s->num_seqs < 1 || s->total_tokens < 0 || s->H < 1) return GDR_ERR_INVALID_ARG;
+    if (s->total_tokens > INT32_MAX || s->num_seqs > INT32_MAX / 2) return GDR_ERR_INVALID_ARG;
+    if (s->q_heads < 1 || s->k_heads < 1 || s->v_heads < 1) return GDR_ERR_INVALID_ARG;
+    if (s->H % s->q_heads || s->H % s->k_heads || s->H % s->v_heads) return GDR_ERR_INVALID_ARG;
+    if (s->dtype != GDR_F32 && s->dtype != GDR_BF16) return GDR_ERR_UNSUPPORTED;
+    if ((s->d_k != 64 && s->d_k != 128) || (s->d_v != 64 && s->d_v != 128 && s->d_v != 256))
+        return GDR_ERR_UNSUPPORTED;
+    if (!isfinite(s->scale)) return GDR_ERR_INVALID_ARG;
+    c->N = s->num_seqs;
+    c->T = s->total_tokens;
+    c->H = s->H;
+    c->qh = s->q_heads;
+    c->kh = s->k_heads;
+    c->vh = s->v_heads;
+    c->dk = s->d_k;
+    c->dv = s->d_v;
+    c->dtype = s->dtype;
+    c->scale = s->scale;
+    c->e = s->dtype == GDR_F32 ? 4 : 2;
+    // blocks of a launch: at most (tiles + sequences) x heads x slices
+    if ((c->T / kTile + c->N) > (int64_t)(INT32_MAX / 16) / c->H) return GDR_ERR_INVALID_ARG;
+    int st = check_stride(s->q_stride, c->qh, c->dk, c->e, &c->qs);
+    if (st == GDR_OK) st = check_stride(s->k_stride, c->kh, c->dk, c->e, &c->ks);
+    if (st == GDR_OK) st = check_stride(s->v_stride, c->vh, c->dv, c->e, &c->vs);
+    return st;
+}
+
+// Tokens per segment. `cols`: blocks per segment and head. The model: a launch takes
+// rounds x tiles per segment, a segment's own sum about half of what its mix takes, and the
+// second launch and the reading of the sums some tiles' worth more.
+int64_t segment_tokens(const Call &c, bool packed, int cols) {
+    const int64_t tiles = (c.T + kTile - 1) / kTile;
+    const int64_t m = packed ? tiles : (c.T / c.N + kTile - 1) / kTile;  // longest possible
+    if (m <= 1) return kTile;
+    const int64_t sms = 152;
+    int64_t best = m;
+    double best_cost = 1e300;
+    for (int64_t n = 1; n <= m && n <= 256; ++n) {
+        const int64_t len = (m + n - 1) / n;
+        const int64_t items = packed ? tiles / len + c.N : c.N * ((m + len - 1) / len);
+        const int64_t rounds = (items * c.H * cols + sms - 1) / sms;
+        double cost = (double)rounds * len;
+        if (n > 1) cost = 1.5 * cost + 3 + 0.5 * n;
+        if (cost < best_cost) {
+            best_cost = cost;
+            best = len;
+        }
+    }
+    return best * kTile;
+}
+
+Plan make_plan(const Call &c, const float *log_decay, const int32_t *cu, int cols, void *ws) {
+    Plan p = {};
+    p.cu_seqlens = cu;
+    p.num_seqs = c.N;
+    p.total_tokens = c.T;
+    p.H = c.H;
+    p.log_decay = log_decay;
+    p.status = (int32_t *)ws;
+    p.seg = segment_tokens(c, cu != nullptr, cols);
+    if (cu) {
+        p.items = c.T / p.seg + c.N;
+    } else {
+        p.seq_len = c.T / c.N;
+        p.segs = (int)((p.seq_len + p.seg - 1) / p.seg);
+        if (p.segs < 1) p.segs = 1;
+        p.items = c.N * p.segs;
+    }
+    return p;
+}
+bool segmented(const Plan &p) { return p.cu_seqlens ? p.total_tokens > p.seg : p.segs > 1; }
+
+// Workspace: status word; a copy of S0 where S_final is to be written over it; the
+// segments' own sums (backward: those of both directions, and fp32 gradients of heads that
+// share one).
+struct Layout {
+    size_t copy, R, R2, part[3], total;
+};
+Layout layout(const Call &c, int64_t items, bool backward) {
+    Layout L = {};
+    size_t off = 256;
+    const size_t sums = (size_t)items * c.H * c.dk * c.dv * sizeof(float);
+    L.copy = off;
+    if (!backward) off = align_up(off + c.state());
+    L.R = off;
+    off = align_up(off + sums);
+    L.R2 = off;
+    if (backward) {
+        off = align_up(off + sums);
+        const int heads[3] = {c.qh, c.kh, c.vh}, d[3] = {c.dk, c.dk, c.dv};
+        for (int i = 0; i < 3; ++i) {
+            L.part[i] = off;
+            if (heads[i] != c.H) off = align_up(off + (size_t)c.T * c.H * d[i] * sizeof(float));
+        }
+    }
+    L.total = off;
+    return L;
+}
+// The larger of what equal and packed lengths take.
+size_t workspace_bytes_for(const Call &c, bool backward) {
+    static const int32_t some = 0;
+    const int cols = backward ? c.dk / 64 : c.dv / 64;
+    int64_t items = make_plan(c, nullptr, &some, cols, nullptr).items;
+    if (c.T % c.N == 0) {
+        const int64_t equal = make_plan(c, nullptr, nullptr, cols, nullptr).items;
+        if (equal > items) items = equal;
+    }
+    return layout(c, items, backward).total;
+}
+
+struct Span {
+    const void *p;
+    size_t n;
+};
+Span rows(const void *p, const Call &c, int64_t stride, int heads, int d) {
+    return {p, c.T == 0 ? 0 : ((size_t)(c.T - 1) * stride + (size_t)heads * d) * c.e};
+}
+bool overlap(const Span &a, const Span &b) {
+    if (!a.p || !b.p || !a.n || !b.n) return false;
+    const char *x = (const char *)a.p, *y = (const char *)b.p;
+    return x < y + b.n && y < x + a.n;
+}
+int check_spans(const Span *in, int ni, const Span *out, int no) {
+    for (int i = 0; i < ni; ++i)
+        if ((uintptr_t)in[i].p & 15u) return GDR_ERR_ALIGNMENT;
+    for (int i = 0; i < no; ++i) {
+        if ((uintptr_t)out[i].p & 15u) return GDR_ERR_ALIGNMENT;
+        for (int j = 0; j < ni; ++j)
+            if (overlap(out[i], in[j])) return GDR_ERR_INVALID_ARG;
+        for (int j = 0; j < i; ++j)
+            if (overlap(out[i], out[j])) return GDR_ERR_INVALID_ARG;
+    }
+    return GDR_OK;
+}
+
+Mix mix_of(const Call &c, const void *x, int64_t xs, int xh, const void *y, int64_t ys, int yh,
+           const void *z, int64_t zs, int zh, int dx, int dz) {
+    Mix m = {};
+    m.x = x; m.y = y; m.z = z;
+    m.xs = xs; m.ys = ys; m.zs = zs;
+    m.xg = c.H / xh; m.yg = c.H / yh; m.zg = c.H / zh;
+    m.dx = dx; m.dz = dz;
+    m.s_intra = m.s_inter = c.scale;
+    m.s_state = 1.f;
+    return m;
+}
+
+}  // namespace
+}  // namespace linattn
+}  // namespace gdr
+
+using namespace gdr;
+using namespace gdr::linattn;
+
+extern "C" {
+
+size_t gdr_linattn_fwd_workspace_size(const gdr_linattn_shape *shape) {
+    Call c;
+    return check_shape(shape, &c) == GDR_OK ? workspace_bytes_for(c, false) : 0;
+}
+
+size_t gdr_linattn_bwd_workspace_size(const gdr_linattn_shape *shape) {
+    Call c;
+    return check_shape(shape, &c) == GDR_OK ? workspace_bytes_for(c, true) : 0;
+}
+
+int gdr_linattn_fwd(const gdr_linattn_shape *shape, const void *q, const void *k, const void *v,
+                    const float *log_decay, const float *S0, const int32_t *cu_seqlens, void *o,
+                    float *S_final, void *workspace, size_t workspace_bytes, gdr_stream_t stream) {
+    Call c;
+    int st = check_shape(shape, &c);
+    if (st != GDR_OK) return st;
+    if (!cu_seqlens && c.T % c.N != 0) return GDR_ERR_INVALID_ARG;
+    if (!workspace) return GDR_ERR_WORKSPACE;
+    if (!log_decay || (c.T > 0 && (!q || !k || !v || !o))) return GDR_ERR_INVALID_ARG;
+    if (((uintptr_t)log_decay | (uintptr_t)cu_seqlens) & 3u) return GDR_ERR_ALIGNMENT;
+    const size_t need = workspace_bytes_for(c, false);
+    if (workspace_bytes < need) return GDR_ERR_WORKSPACE;
+    const Span in[] = {rows(q, c, c.qs, c.qh, c.dk), rows(k, c, c.ks, c.kh, c.dk),
+                       rows(v, c, c.vs, c.vh, c.dv), {S0 == S_final ? nullptr : S0, c.state()}};
+    const Span out[] = {rows(o, c, (int64_t)c.H * c.dv, c.H, c.dv), {S_final, c.state()}, {workspace, need}};
+    if ((st = check_spans(in, 4, out, 3)) != GDR_OK) return st;
+    const Span small[] = {{log_decay, (size_t)c.H * 4}, {cu_seqlens, (size_t)(c.N + 1) * 4}};
+    for (const Span &s : out)
+        if (overlap(s, small[0]) || overlap(s, small[1])) return GDR_ERR_INVALID_ARG;
+
+    Plan p = make_plan(c, log_decay, cu_seqlens, c.dv / 64, workspace);
+    const Layout L = layout(c, p.items, false);
+    char *ws = (char *)workspace;
+    const cudaStream_t s = (cudaStream_t)stream;
+    Mix m = mix_of(c, q, c.qs, c.qh, k, c.ks, c.kh, v, c.vs, c.vh, c.dk, c.dv);
+    p.first = true;
+    if (segmented(p)) {
+        // (the first segment of a sequence reads S0 while its last one may write S_final)
+        if (S0 && S0 == S_final) {
+            if (cudaMemcpyAsync(ws + L.copy, S0, c.state(), cudaMemcpyDeviceToDevice, s) != cudaSuccess)
+                return GDR_ERR_CUDA;
+            S0 = (const float *)(ws + L.copy);
+        }
+        Mix sums = m;
+        sums.R_out = (float *)(ws + L.R);
+        if ((st = launch_mix_exact(p, &sums, 1, c.dtype, s)) != GDR_OK) return st;
+        m.R = sums.R_out;
+        p.first = false;
+    }
+    m.start = S0;
+    m.end = S_final;
+    m.out = c.T > 0 ? o : (void *)workspace;  // (no rows: nothing is written to it)
+    return launch_mix_exact(p, &m, 1, c.dtype, s);
+}
+
+int gdr_linattn_bwd(const gdr_linattn_shape *shape, const void *d_o, const void *q, const void *k,
+                    const void *v, const float *log_decay, const float *S0, const float *dS_final,
+                    const int32_t *cu_seqlens, void *dq, void *dk, void *dv, float *dS0,
+                    void *workspace, size_t workspace_bytes, gdr_stream_t stream) {
+    Call c;
+    int st = check_shape(shape, &c);
+    if (st != GDR_OK) return st;
+    if (!cu_seqlens && c.T % c.N != 0) return GDR_ERR_INVALID_ARG;
+    if (!workspace) return GDR_ERR_WORKSPACE;
+    if (!log_decay || (c.T > 0 && (!d_o || !q || !k || !v || !dq || !dk || !dv))) return GDR_ERR_INVALID_ARG;
+    if (((uintptr_t)log_decay | (uintptr_t)cu_seqlens) & 3u) return GDR_ERR_ALIGNMENT;
+    const size_t need = workspace_bytes_for(c, true);
+    if (workspace_bytes < need) return GDR_ERR_WORKSPACE;
+    const int64_t os = (int64_t)c.H * c.dv;
+    const Span in[] = {rows(q, c, c.qs, c.qh, c.dk), rows(k, c, c.ks, c.kh, c.dk), rows(v, c, c.vs, c.vh, c.dv),
+                       rows(d_o, c, os, c.H, c.dv), {S0, c.state()}, {dS_final, c.state()}};
+    const Span out[] = {rows(dq, c, (int64_t)c.qh * c.dk, c.qh, c.dk), rows(dk, c, (int64_t)c.kh * c.dk, c.kh, c.dk),
+                        rows(dv, c, (int64_t)c.vh * c.dv, c.vh, c.dv), {dS0, c.state()}, {workspace, need}};
+    if ((st = check_spans(in, 6, out, 5)) != GDR_OK) return st;
+    const Span small[] = {{log_decay, (size_t)c.H * 4}, {cu_seqlens, (size_t)(c.N + 1) * 4}};
+    for (const Span &s : out)
+        if (overlap(s, small[0]) || overlap(s, small[1])) return GDR_ERR_INVALID_ARG;
+
+    Plan p = make_plan(c, log_decay, cu_seqlens, c.dk / 64, workspace);
+    const Layout L = layout(c, p.items, true);
+    char *ws = (char *)workspace;
+    const cudaStream_t s = (cudaStream_t)stream;
+    Mix q_, k_, v_;  // dq, dk, dv
+    q_ = mix_of(c, d_o, os, c.H, v, c.vs, c.vh, k, c.ks, c.kh, c.dv, c.dk);
+    q_.turned = true;
+    k_ = mix_of(c, v, c.vs, c.vh, d_o, os, c.H, q, c.qs, c.qh, c.dv, c.dk);
+    k_.turned = true;
+    v_ = mix_of(c, k, c.ks, c.kh, q, c.qs, c.qh, d_o, os, c.H, c.dk, c.dv);
+    k_.backward = v_.backward = true;
+    k_.s_inter = v_.s_inter = 1.f;
+    k_.s_state = v_.s_state = c.scale;
+    p.first = true;
+    if (segmented(p)) {
+        Mix sums[2];
+        sums[0] = mix_of(c, nullptr, 0, c.H, k, c.ks, c.kh, v, c.vs, c.vh, c.dk, c.dv);
+        sums[0].R_out = (float *)(ws + L.R);
+        sums[1] = v_;
+        sums[1].R_out = (float *)(ws + L.R2);
+        if ((st = launch_mix_exact(p, sums, 2, c.dtype, s)) != GDR_OK) return st;
+        q_.R = sums[0].R_out;
+        k_.R = v_.R = sums[1].R_out;
+        p.first = false;
+    }
+    q_.start = S0;
+    k_.start = v_.start = dS_final;
+    v_.end = dS0;
+    Mix all[3] = {q_, k_, v_};
+    void *to[3] = {dq, dk, dv};
+    const int heads[3] = {c.qh, c.kh, c.vh};
+    for (int i = 0; i < 3; ++i) {
+        all[i].out_f32 = heads[i] != c.H;
+        all[i].out = all[i].out_f32 ? (void *)(ws + L.part[i]) : to[i];
+        if (c.T == 0) all[i].out = workspace;  // (no rows: nothing is written to it)
+    }
+    if ((st = launch_mix_exact(p, all, 3, c.dtype, s)) != GDR_OK) return st;
+    for (int i = 0; i < 3 && c.T > 0; ++i)
+        if (all[i].out_f32) {
+            st = launch_share(p, (const float *)all[i].out, to[i], c.H / heads[i], i == 2 ? c.dv : c.dk, c.dtype, s);
+            if (st != GDR_OK) return st;
+        }
+    return GDR_OK;
+}
+
+int gdr_linattn_step(const gdr_linattn_shape *shape, const void *q, const void *k, const void *v,
+                     const float *log_decay, float *S, void *o, gdr_stream_t stream) {
+    if (shape && shape->num_seqs == 0 && shape->total_tokens == 0) {
+        gdr_linattn_shape one = *shape;
+        one.num_seqs = 1;
+        Call c;
+        return check_shape(&one, &c);
+    }
+    Call c;
+    int st = check_shape(shape, &c);
+    if (st != GDR_OK) return st;
+    if (c.T != c.N || c.N > INT32_MAX / 8 / c.H) return GDR_ERR_INVALID_ARG;
+    if (!q || !k || !v || !log_decay || !S || !o) return GDR_ERR_INVALID_ARG;
+    if ((uintptr_t)log_decay & 3u) return GDR_ERR_ALIGNMENT;
+    const Span in[] = {rows(q, c, c.qs, c.qh, c.dk), rows(k, c, c.ks, c.kh, c.dk), rows(v, c, c.vs, c.vh, c.dv)};
+    const Span out[] = {rows(o, c, (int64_t)c.H * c.dv, c.H, c.dv), {S, c.state()}};
+    if ((st = check_spans(in, 3, out, 2)) != GDR_OK) return st;
+    const Span decay = {log_decay, (size_t)c.H * 4};
+    if (overlap(out[0], decay) || overlap(out[1], decay)) return GDR_ERR_INVALID_ARG;
+    return launch_step(q, k, v, log_decay, S, o, c.N, c.H, c.H / c.qh, c.H / c.kh, c.H / c.vh, c.dk,
+                       c.dv, c.dtype, c.scale, c.qs, c.ks, c.vs, (cudaStream_t)stream);
+}
+
+}  // extern "C"

@@ -1,0 +1,201 @@
+"""Linear attention with one constant decay per head: binding of gdr_linattn_* (gdr.h).
+
+S_t = lam S_{t-1} + k_t v_t^T, o_t = scale S_t^T q_t with lam = exp(log_decay[h]). q, k and v
+are [T, heads, d] in bf16 or fp32, each with a head count that divides H (the length of
+log_decay). They may be views with a token stride of their own, as the parts of one fused
+projection are; everything else is dense. Argument marshalling only: there is no autograd
+here, `linattn_bwd` returns the gradients.
+"""
+import ctypes
+import functools
+
+import torch
+
+from . import ops
+from .ops import _DTYPES, _check, _need, _stream_handle
+
+
+class LinattnShape(ctypes.Structure):
+    """struct gdr_linattn_shape of gdr.h."""
+    _fields_ = [("num_seqs", ctypes.c_int64), ("total_tokens", ctypes.c_int64),
+                ("H", ctypes.c_int), ("q_heads", ctypes.c_int), ("k_heads", ctypes.c_int),
+                ("v_heads", ctypes.c_int), ("d_k", ctypes.c_int), ("d_v", ctypes.c_int),
+                ("dtype", ctypes.c_int), ("scale", ctypes.c_float),
+                ("q_stride", ctypes.c_int64), ("k_stride", ctypes.c_int64),
+                ("v_stride", ctypes.c_int64)]
+
+
+@functools.lru_cache(maxsize=256)
+def _shape(*fields):
+    return LinattnShape(*fields)
+
+
+@functools.lru_cache(maxsize=256)
+def _workspace_bytes(backward, *fields):
+    lib = ops._load()
+    f = lib.gdr_linattn_bwd_workspace_size if backward else lib.gdr_linattn_fwd_workspace_size
+    return int(f(ctypes.byref(_shape(*fields))))
+
+
+def _rows(t, name, dtype, device, tokens=None):
+    """Checks a [tokens, heads, d] tensor whose heads are contiguous; its token stride."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if t.dim() != 3:
+        raise ValueError(f"{name} must have shape [tokens, heads, d]")
+    n, heads, d = t.shape
+    if tokens is not None and n != tokens:
+        raise ValueError(f"{name} has {n} tokens, expected {tokens}")
+    s0, s1, s2 = t.stride()
+    if (d > 1 and s2 != 1) or (heads > 1 and s1 != d):
+        raise ValueError(f"{name}: the heads of a token must be contiguous")
+    if n > 1 and s0 < heads * d:
+        raise ValueError(f"{name}: the token stride must be at least heads * d")
+    return s0 if n > 1 else heads * d
+
+
+def _fields(q, k, v, log_decay, n, scale):
+    _rows_of = functools.partial(_rows, device=q.device)
+    if not isinstance(q, torch.Tensor) or q.dtype not in _DTYPES:
+        raise TypeError(f"unsupported dtype {q.dtype}")
+    qs = _rows_of(q, "q", q.dtype)
+    T = q.shape[0]
+    ks = _rows_of(k, "k", q.dtype, tokens=T)
+    vs = _rows_of(v, "v", q.dtype, tokens=T)
+    if k.shape[2] != q.shape[2]:
+        raise ValueError(f"k has heads of {k.shape[2]}, q of {q.shape[2]}")
+    _need(log_decay, "log_decay", torch.float32, q.device)
+    if log_decay.dim() != 1:
+        raise ValueError("log_decay must have shape [H]")
+    return (n, T, log_decay.numel(), q.shape[1], k.shape[1], v.shape[1], q.shape[2], v.shape[2],
+            _DTYPES[q.dtype], float(scale), qs, ks, vs)
+
+
+def _seqs(cu_seqlens, num_seqs, device):
+    if cu_seqlens is None:
+        return 1 if num_seqs is None else int(num_seqs)
+    _need(cu_seqlens, "cu_seqlens", torch.int32, device)
+    n = cu_seqlens.numel() - 1
+    if num_seqs is not None and int(num_seqs) != n:
+        raise ValueError(f"num_seqs is {num_seqs}, cu_seqlens has {n} sequences")
+    return n
+
+
+def _dense(t, name, shape, dtype, device):
+    """A given output, checked, or a new one."""
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    _need(t, name, dtype, device)
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    return t
+
+
+def _given(t, name, shape, dtype, device):
+    if t is not None:
+        _dense(t, name, shape, dtype, device)
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+def linattn_fwd_workspace_size(num_seqs, total_tokens, H, dk, dv, dtype=torch.bfloat16,
+                               q_heads=None, k_heads=None, v_heads=None):
+    """Workspace bytes of linattn_fwd (0 if the sizes are unsupported)."""
+    return _workspace_bytes(False, int(num_seqs), int(total_tokens), H, q_heads or H, k_heads or H,
+                            v_heads or H, dk, dv, _DTYPES[dtype], 1.0, 0, 0, 0)
+
+
+def linattn_bwd_workspace_size(num_seqs, total_tokens, H, dk, dv, dtype=torch.bfloat16,
+                               q_heads=None, k_heads=None, v_heads=None):
+    """Workspace bytes of linattn_bwd (0 if the sizes are unsupported)."""
+    return _workspace_bytes(True, int(num_seqs), int(total_tokens), H, q_heads or H, k_heads or H,
+                            v_heads or H, dk, dv, _DTYPES[dtype], 1.0, 0, 0, 0)
+
+
+def _workspace(workspace, backward, fields, device):
+    if workspace is None:
+        return torch.empty(max(_workspace_bytes(backward, *fields), 256), dtype=torch.uint8, device=device)
+    _need(workspace, "workspace", device=device)
+    return workspace
+
+
+def linattn_fwd(q, k, v, log_decay, S0=None, cu_seqlens=None, num_seqs=None, scale=1.0,
+                final_state=True, o=None, S_final=None, workspace=None, stream=None):
+    """Prompts (gdr_linattn_fwd): q [T, q_heads, dk], k [T, k_heads, dk], v [T, v_heads, dv];
+    log_decay [H] fp32; S0 [num_seqs, H, dk, dv] fp32 or None; cu_seqlens [num_seqs + 1]
+    int32 or None (then `num_seqs` equal sequences, default 1). Returns (o [T, H, dv],
+    S_final [num_seqs, H, dk, dv] fp32, or None with final_state=False). Preallocated o,
+    S_final (which may be S0) and workspace (uint8) are used as given."""
+    lib = ops._load()
+    n = _seqs(cu_seqlens, num_seqs, q.device)
+    fields = _fields(q, k, v, log_decay, n, scale)
+    dev, (T, H, dk, dv) = q.device, (fields[1], fields[2], fields[6], fields[7])
+    _given(S0, "S0", (n, H, dk, dv), torch.float32, dev)
+    o = _dense(o, "o", (T, H, dv), q.dtype, dev)
+    if final_state or S_final is not None:
+        S_final = _dense(S_final, "S_final", (n, H, dk, dv), torch.float32, dev)
+    ws = _workspace(workspace, False, fields, dev)
+    with torch.cuda.device(dev):
+        st = lib.gdr_linattn_fwd(ctypes.byref(_shape(*fields)), q.data_ptr(), k.data_ptr(),
+                                 v.data_ptr(), log_decay.data_ptr(), _addr(S0), _addr(cu_seqlens),
+                                 o.data_ptr(), _addr(S_final), ws.data_ptr(),
+                                 ws.numel() * ws.element_size(), _stream_handle(stream, dev))
+    _check(st, "gdr_linattn_fwd")
+    return o, S_final
+
+
+def linattn_bwd(do, q, k, v, log_decay, S0=None, dS_final=None, cu_seqlens=None, num_seqs=None,
+                scale=1.0, dq=None, dk=None, dv=None, dS0=None, workspace=None, stream=None):
+    """Gradients of linattn_fwd (gdr_linattn_bwd) from do [T, H, dv] and the gradient
+    dS_final of S_final (None for zero). Returns (dq, dk, dv, dS0), each like its tensor but
+    dense; dS0 is None unless S0 or dS0 is given."""
+    lib = ops._load()
+    n = _seqs(cu_seqlens, num_seqs, q.device)
+    fields = _fields(q, k, v, log_decay, n, scale)
+    dev, (T, H, d_k, d_v) = q.device, (fields[1], fields[2], fields[6], fields[7])
+    state = (n, H, d_k, d_v)
+    _given(S0, "S0", state, torch.float32, dev)
+    _given(dS_final, "dS_final", state, torch.float32, dev)
+    if do is None:
+        raise TypeError("do must be a torch.Tensor")
+    _given(do, "do", (T, H, d_v), q.dtype, dev)
+    dq = _dense(dq, "dq", q.shape, q.dtype, dev)
+    dk = _dense(dk, "dk", k.shape, q.dtype, dev)
+    dv = _dense(dv, "dv", v.shape, q.dtype, dev)
+    if S0 is not None or dS0 is not None:
+        dS0 = _dense(dS0, "dS0", state, torch.float32, dev)
+    ws = _workspace(workspace, True, fields, dev)
+    with torch.cuda.device(dev):
+        st = lib.gdr_linattn_bwd(ctypes.byref(_shape(*fields)), do.data_ptr(), q.data_ptr(),
+                                 k.data_ptr(), v.data_ptr(), log_decay.data_ptr(), _addr(S0),
+                                 _addr(dS_final), _addr(cu_seqlens), dq.data_ptr(), dk.data_ptr(),
+                                 dv.data_ptr(), _addr(dS0), ws.data_ptr(),
+                                 ws.numel() * ws.element_size(), _stream_handle(stream, dev))
+    _check(st, "gdr_linattn_bwd")
+    return dq, dk, dv, dS0
+
+
+def linattn_step(q, k, v, log_decay, S, scale=1.0, o=None, stream=None):
+    """The next token of N sequences (gdr_linattn_step): q [N, q_heads, dk], k [N, k_heads,
+    dk], v [N, v_heads, dv]; S [N, H, dk, dv] fp32 updated in place. Returns o [N, H, dv]."""
+    lib = ops._load()
+    fields = _fields(q, k, v, log_decay, q.shape[0], scale)
+    dev, (N, H, dk, dv) = q.device, (fields[1], fields[2], fields[6], fields[7])
+    if S is None:
+        raise TypeError("S must be a torch.Tensor")
+    _given(S, "S", (N, H, dk, dv), torch.float32, dev)
+    o = _dense(o, "o", (N, H, dv), q.dtype, dev)
+    with torch.cuda.device(dev):
+        st = lib.gdr_linattn_step(ctypes.byref(_shape(*fields)), q.data_ptr(), k.data_ptr(),
+                                  v.data_ptr(), log_decay.data_ptr(), S.data_ptr(), o.data_ptr(),
+                                  _stream_handle(stream, dev))
+    _check(st, "gdr_linattn_step")
+    return o

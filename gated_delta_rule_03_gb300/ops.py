@@ -133,6 +133,18 @@ def _load():
     lib.gdr_chunk_fwd_schedule_model.argtypes = [i64, i64, c_int, c_int, c_int, c_int, c_int, c_int,
                                                  c_int, c_int]
     lib.gdr_chunk_fwd_schedule_model.restype = c_int
+    size_t = ctypes.c_size_t
+    for name, res, args in (
+            ("gdr_linattn_fwd_workspace_size", size_t, [vp]),
+            ("gdr_linattn_bwd_workspace_size", size_t, [vp]),
+            ("gdr_linattn_fwd", c_int, [vp] * 10 + [size_t, vp]),
+            ("gdr_linattn_bwd", c_int, [vp] * 14 + [size_t, vp]),
+            ("gdr_linattn_step", c_int, [vp] * 8),
+            ("gdr_block_norm_fwd", c_int, [vp] * 9),
+            ("gdr_block_norm_bwd_workspace_size", size_t, [vp]),
+            ("gdr_block_norm_bwd", c_int, [vp] * 14 + [size_t, vp])):
+        getattr(lib, name).restype = res
+        getattr(lib, name).argtypes = args
     lib.gdr_read_device_status.argtypes = [vp, ctypes.POINTER(c_int), vp]
     lib.gdr_read_device_status.restype = c_int
     _lib = lib

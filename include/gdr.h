@@ -407,6 +407,147 @@ int gdr_chunk_fwd_schedule(int64_t num_seqs, int64_t total_tokens, int H, int d_
  */
 int gdr_read_device_status(const void *workspace, int *status, gdr_stream_t stream);
 
+/*
+ * Linear attention with one constant decay per head (retention).
+ *
+ * With lam_h = exp(log_decay[h]), per sequence and head, from S_0 (zero if S0 is NULL):
+ *     S_t = lam_h S_{t-1} + k_t v_t^T,     o_t = scale S_t^T q_t
+ * the decayed additive write above (GDR_RULE_ADDITIVE) with alpha_t = lam_h for every
+ * token and beta_t = 1. Without gates that depend on the tokens it needs neither gate
+ * tensors nor a solve, its segments run side by side, and it has a backward pass. The
+ * decay is a constant of the head, not a learned weight: it gets no gradient.
+ *
+ * Shape of a call (a HOST struct):
+ *   num_seqs, total_tokens   sequences (>= 1) and rows of the packed tensors
+ *   H                        heads of the state and of o
+ *   q_heads, k_heads, v_heads  heads of q, k and v; each divides H, and head h reads head
+ *                            h / (H / q_heads) of q, and so on (keys and values shared by
+ *                            groups of query heads, or queries and keys by groups of
+ *                            value heads)
+ *   d_k                      64 or 128;   d_v  64, 128 or 256
+ *   dtype                    gdr_dtype of q, k, v, o and their gradients
+ *   scale                    finite
+ *   q_stride, k_stride, v_stride  elements from a token's first head to the next token's
+ *                            first head (for views of one fused projection); 0 means
+ *                            dense, heads x d. A multiple of 16 bytes, at least dense.
+ *                            The heads of one token are contiguous.
+ */
+typedef struct gdr_linattn_shape {
+    int64_t num_seqs, total_tokens;
+    int H, q_heads, k_heads, v_heads, d_k, d_v, dtype;
+    float scale;
+    int64_t q_stride, k_stride, v_stride;
+} gdr_linattn_shape;
+
+/*
+ * Bytes of device workspace of gdr_linattn_fwd and gdr_linattn_bwd for a shape (host-only,
+ * no CUDA call); 0 for shapes that the calls reject.
+ */
+size_t gdr_linattn_fwd_workspace_size(const gdr_linattn_shape *shape);
+size_t gdr_linattn_bwd_workspace_size(const gdr_linattn_shape *shape);
+
+/*
+ * Prompts: o for every token and the state after the last token of every sequence.
+ *   q [total_tokens, q_heads, d_k], k [.., k_heads, d_k], v [.., v_heads, d_v]  dtype,
+ *               token strides as in the shape, 16-byte aligned
+ *   log_decay   [H] fp32, <= 0; 0 keeps everything, -inf (lam = 0) forgets everything. Not
+ *               checked (it is device memory). A NaN makes that head's results NaN.
+ *   S0          [num_seqs, H, d_k, d_v] fp32 or NULL for zero
+ *   cu_seqlens  [num_seqs + 1] int32 offsets from 0, non-decreasing, the last at most
+ *               total_tokens: rows behind it are neither read nor written (a padded batch).
+ *               Or NULL for num_seqs sequences of total_tokens / num_seqs tokens each.
+ *               Checked on the device: a violation leaves GDR_ERR_BAD_SEQLENS in the
+ *               workspace's status word (gdr_read_device_status) and nothing else is
+ *               written. A sequence of no tokens hands its S0 on.
+ *   o           [total_tokens, H, d_v] dtype, dense (written)
+ *   S_final     [num_seqs, H, d_k, d_v] fp32 (written), or NULL. It may be S0's buffer;
+ *               any other overlap of an output is rejected.
+ *   workspace   as for gdr_chunk_fwd; calls that share one must be ordered on one stream
+ * A value that is not finite in a token's q, k or v stays within its sequence and head,
+ * but may reach other tokens of it, before the token too (up to 127 of them: products are
+ * taken over blocks of tokens).
+ */
+int gdr_linattn_fwd(const gdr_linattn_shape *shape, const void *q, const void *k, const void *v,
+                    const float *log_decay, const float *S0, const int32_t *cu_seqlens, void *o,
+                    float *S_final, void *workspace, size_t workspace_bytes, gdr_stream_t stream);
+
+/*
+ * Gradients of gdr_linattn_fwd: from d_o [total_tokens, H, d_v] (dtype, dense) and the
+ * gradient dS_final of S_final (fp32, NULL for zero)
+ *   dq [total_tokens, q_heads, d_k], dk [.., k_heads, d_k], dv [.., v_heads, d_v]  dtype,
+ *   dense (written; a head shared by several gets the sum, added in fp32 and rounded once)
+ *   dS0 [num_seqs, H, d_k, d_v] fp32 (written), or NULL.
+ * q, k, v, log_decay, S0 and cu_seqlens as in the forward call (nothing is kept from it).
+ * Rows behind the last sequence are left as they were. No output may overlap another
+ * argument. Results are the same bits every time.
+ */
+int gdr_linattn_bwd(const gdr_linattn_shape *shape, const void *d_o, const void *q, const void *k,
+                    const void *v, const float *log_decay, const float *S0, const float *dS_final,
+                    const int32_t *cu_seqlens, void *dq, void *dk, void *dv, float *dS0,
+                    void *workspace, size_t workspace_bytes, gdr_stream_t stream);
+
+/*
+ * The next token of num_seqs sequences (total_tokens = num_seqs, one row each): S
+ * [num_seqs, H, d_k, d_v] fp32 is read and overwritten, o [num_seqs, H, d_v] written.
+ * num_seqs = 0 enqueues nothing.
+ */
+int gdr_linattn_step(const gdr_linattn_shape *shape, const void *q, const void *k, const void *v,
+                     const float *log_decay, float *S, void *o, gdr_stream_t stream);
+
+/*
+ * The norms before and after a block, fused with the block's gate and the residual scale.
+ *
+ * Per row of D entries, with rms(a) = sqrt(mean a_j^2 + eps):
+ *     t  = y / rms(y) * w_post      (post_norm; else t = y)
+ *     x' = x + res_scale * act(gate) * t        (no gate: act = 1)
+ *     h  = x' / rms(x') * w_pre     (pre_norm)
+ * x is the residual stream, y the block's output, h the next block's input. h is taken
+ * from x' before x' is rounded. y NULL: h = x / rms(x) * w_pre only (the first block).
+ *
+ * Shape of a call (a HOST struct):
+ *   rows >= 0, D in [1, 8192]
+ *   dtype      gdr_dtype of y, gate, h and their gradients
+ *   x_dtype    gdr_dtype of x, x' and their gradients: dtype, or GDR_F32
+ *   post_norm, pre_norm   nonzero: the norm is taken
+ *   gate_act   GDR_GATE_IDENTITY, GDR_GATE_SILU (g sigmoid(g)) or GDR_GATE_SIGMOID
+ *   gate_rows  0: no gate; 1: one row for all; rows: one per row
+ *   res_scale  finite;  eps >= 0, finite (0 means 1e-6)
+ */
+enum { GDR_GATE_IDENTITY = 0, GDR_GATE_SILU = 1, GDR_GATE_SIGMOID = 2 };
+typedef struct gdr_block_norm_shape {
+    int64_t rows;
+    int D, dtype, x_dtype, post_norm, pre_norm, gate_act;
+    int64_t gate_rows;
+    float res_scale, eps;
+} gdr_block_norm_shape;
+
+/*
+ *   x [rows, D], y [rows, D] or NULL, gate [gate_rows, D] or NULL
+ *   w_post, w_pre  [D] fp32, NULL for ones (and only with their norm)
+ *   x_out  [rows, D] x_dtype (written; may be x; NULL without y)
+ *   h      [rows, D] dtype (written; NULL without pre_norm)
+ * Every pointer is 16-byte aligned; any overlap of an output but x_out = x is rejected.
+ */
+int gdr_block_norm_fwd(const gdr_block_norm_shape *shape, const void *x, const void *y,
+                       const void *gate, const float *w_post, const float *w_pre, void *x_out,
+                       void *h, gdr_stream_t stream);
+
+/*
+ * Its gradients, from dh (with pre_norm) and dx_out, the gradient that the stream behind
+ * the block hands to x' (NULL for zero, with pre_norm only). x_out is the stored x' (x if
+ * there was no y).
+ *   dx [rows, D] x_dtype (written; may be dx_out), dy [rows, D] dtype (with y)
+ *   dgate [gate_rows, D] dtype, dw_post, dw_pre [D] fp32: written, or NULL. The sums over
+ *   rows are added in fp32 in a fixed order; with no rows they are zero.
+ *   workspace  gdr_block_norm_bwd_workspace_size bytes, 16-byte aligned; may be NULL when
+ *              no sum over rows is asked for
+ */
+size_t gdr_block_norm_bwd_workspace_size(const gdr_block_norm_shape *shape);
+int gdr_block_norm_bwd(const gdr_block_norm_shape *shape, const void *dx_out, const void *dh,
+                       const void *x_out, const void *y, const void *gate, const float *w_post,
+                       const float *w_pre, void *dx, void *dy, void *dgate, float *dw_post,
+                       float *dw_pre, void *workspace, size_t workspace_bytes, gdr_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -18,7 +18,7 @@ BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libgdr.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 SOURCES = ["gdr_api.cu", "decode.cu", "prefill_exact.cu", "solve_tc.cu", "prefill_tc.cu", "channel_tc.cu", "noalloc.cu",
-           "epilogue.cu", "linattn_api.cu", "linattn_exact.cu", "linattn_step.cu", "block_norm.cu"]
+           "epilogue.cu", "linattn_api.cu", "linattn_exact.cu", "linattn_tc.cu", "linattn_step.cu", "block_norm.cu"]
 
 
 def nvcc():

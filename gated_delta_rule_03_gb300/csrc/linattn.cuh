@@ -153,9 +153,11 @@ __device__ __forceinline__ int64_t state_at(const Mix &m, int a, int b) {
 }
 
 int launch_mix_exact(const Plan &p, const Mix *mixes, int count, int dtype, cudaStream_t stream);
-// Sums the heads that share one head: in fp32 [rows, H, d] -> out [rows, H / g, d]. Rows
+int launch_mix_tc(const Plan &p, const Mix *mixes, int count, int d_v, bool sums, bool wide_state,
+                  cudaStream_t stream);
+// Sums the g parts of every head: in fp32 [rows, heads g, d] -> out [rows, heads, d]. Rows
 // behind the last sequence are left as they are.
-int launch_share(const Plan &p, const float *in, void *out, int g, int d, int dtype,
+int launch_share(const Plan &p, const float *in, void *out, int heads, int g, int d, int dtype,
                  cudaStream_t stream);
 int launch_step(const void *q, const void *k, const void *v, const float *log_decay, float *S,
                 void *o, int64_t N, int H, int qg, int kg, int vg, int dk, int dv, int dtype,

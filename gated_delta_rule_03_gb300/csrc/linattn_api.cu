@@ -79,6 +79,15 @@ int64_t segment_tokens(const Call &c, bool packed, int cols) {
     return best * kTile;
 }
 
+// bf16 goes to the tensor cores (a call without tokens has nothing for them).
+bool on_tensor_cores(const Call &c) { return c.dtype == GDR_BF16 && c.T > 0; }
+// Slices of d_v: a tensor-core block takes 128 of its columns.
+int slices(const Call &c) { return on_tensor_cores(c) && c.dv > 128 ? c.dv / 128 : 1; }
+int columns(const Call &c, bool backward) {
+    if (on_tensor_cores(c)) return (backward ? 3 : 1) * slices(c);
+    return backward ? c.dk / 64 : c.dv / 64;
+}
+
 Plan make_plan(const Call &c, const float *log_decay, const int32_t *cu, int cols, void *ws) {
     Plan p = {};
     p.cu_seqlens = cu;
@@ -105,6 +114,7 @@ bool segmented(const Plan &p) { return p.cu_seqlens ? p.total_tokens > p.seg : p
 // share one).
 struct Layout {
     size_t copy, R, R2, part[3], total;
+    int parts[3];  // heads and slices whose gradients add up to one head's of dq, dk, dv
 };
 Layout layout(const Call &c, int64_t items, bool backward) {
     Layout L = {};
@@ -120,7 +130,8 @@ Layout layout(const Call &c, int64_t items, bool backward) {
         const int heads[3] = {c.qh, c.kh, c.vh}, d[3] = {c.dk, c.dk, c.dv};
         for (int i = 0; i < 3; ++i) {
             L.part[i] = off;
-            if (heads[i] != c.H) off = align_up(off + (size_t)c.T * c.H * d[i] * sizeof(float));
+            L.parts[i] = c.H / heads[i] * (i < 2 ? slices(c) : 1);
+            if (L.parts[i] > 1) off = align_up(off + (size_t)c.T * heads[i] * L.parts[i] * d[i] * sizeof(float));
         }
     }
     L.total = off;
@@ -129,7 +140,7 @@ Layout layout(const Call &c, int64_t items, bool backward) {
 // The larger of what equal and packed lengths take.
 size_t workspace_bytes_for(const Call &c, bool backward) {
     static const int32_t some = 0;
-    const int cols = backward ? c.dk / 64 : c.dv / 64;
+    const int cols = columns(c, backward);
     int64_t items = make_plan(c, nullptr, &some, cols, nullptr).items;
     if (c.T % c.N == 0) {
         const int64_t equal = make_plan(c, nullptr, nullptr, cols, nullptr).items;
@@ -175,6 +186,13 @@ Mix mix_of(const Call &c, const void *x, int64_t xs, int xh, const void *y, int6
     return m;
 }
 
+int launch(const Call &c, const Plan &p, const Mix *mixes, int count, bool sums, cudaStream_t s) {
+    if (!on_tensor_cores(c)) return launch_mix_exact(p, mixes, count, c.dtype, s);
+    bool end = false;
+    for (int i = 0; i < count; ++i) end |= mixes[i].end != nullptr;
+    return launch_mix_tc(p, mixes, count, c.dv, sums, end, s);
+}
+
 }  // namespace
 }  // namespace linattn
 }  // namespace gdr
@@ -214,7 +232,7 @@ int gdr_linattn_fwd(const gdr_linattn_shape *shape, const void *q, const void *k
     for (const Span &s : out)
         if (overlap(s, small[0]) || overlap(s, small[1])) return GDR_ERR_INVALID_ARG;
 
-    Plan p = make_plan(c, log_decay, cu_seqlens, c.dv / 64, workspace);
+    Plan p = make_plan(c, log_decay, cu_seqlens, columns(c, false), workspace);
     const Layout L = layout(c, p.items, false);
     char *ws = (char *)workspace;
     const cudaStream_t s = (cudaStream_t)stream;
@@ -229,14 +247,14 @@ int gdr_linattn_fwd(const gdr_linattn_shape *shape, const void *q, const void *k
         }
         Mix sums = m;
         sums.R_out = (float *)(ws + L.R);
-        if ((st = launch_mix_exact(p, &sums, 1, c.dtype, s)) != GDR_OK) return st;
+        if ((st = launch(c, p, &sums, 1, true, s)) != GDR_OK) return st;
         m.R = sums.R_out;
         p.first = false;
     }
     m.start = S0;
     m.end = S_final;
     m.out = c.T > 0 ? o : (void *)workspace;  // (no rows: nothing is written to it)
-    return launch_mix_exact(p, &m, 1, c.dtype, s);
+    return launch(c, p, &m, 1, false, s);
 }
 
 int gdr_linattn_bwd(const gdr_linattn_shape *shape, const void *d_o, const void *q, const void *k,
@@ -262,7 +280,7 @@ int gdr_linattn_bwd(const gdr_linattn_shape *shape, const void *d_o, const void 
     for (const Span &s : out)
         if (overlap(s, small[0]) || overlap(s, small[1])) return GDR_ERR_INVALID_ARG;
 
-    Plan p = make_plan(c, log_decay, cu_seqlens, c.dk / 64, workspace);
+    Plan p = make_plan(c, log_decay, cu_seqlens, columns(c, true), workspace);
     const Layout L = layout(c, p.items, true);
     char *ws = (char *)workspace;
     const cudaStream_t s = (cudaStream_t)stream;
@@ -282,7 +300,7 @@ int gdr_linattn_bwd(const gdr_linattn_shape *shape, const void *d_o, const void 
         sums[0].R_out = (float *)(ws + L.R);
         sums[1] = v_;
         sums[1].R_out = (float *)(ws + L.R2);
-        if ((st = launch_mix_exact(p, sums, 2, c.dtype, s)) != GDR_OK) return st;
+        if ((st = launch(c, p, sums, 2, true, s)) != GDR_OK) return st;
         q_.R = sums[0].R_out;
         k_.R = v_.R = sums[1].R_out;
         p.first = false;
@@ -294,14 +312,14 @@ int gdr_linattn_bwd(const gdr_linattn_shape *shape, const void *d_o, const void 
     void *to[3] = {dq, dk, dv};
     const int heads[3] = {c.qh, c.kh, c.vh};
     for (int i = 0; i < 3; ++i) {
-        all[i].out_f32 = heads[i] != c.H;
+        all[i].out_f32 = L.parts[i] > 1;
         all[i].out = all[i].out_f32 ? (void *)(ws + L.part[i]) : to[i];
         if (c.T == 0) all[i].out = workspace;  // (no rows: nothing is written to it)
     }
-    if ((st = launch_mix_exact(p, all, 3, c.dtype, s)) != GDR_OK) return st;
+    if ((st = launch(c, p, all, 3, false, s)) != GDR_OK) return st;
     for (int i = 0; i < 3 && c.T > 0; ++i)
         if (all[i].out_f32) {
-            st = launch_share(p, (const float *)all[i].out, to[i], c.H / heads[i], i == 2 ? c.dv : c.dk, c.dtype, s);
+            st = launch_share(p, (const float *)all[i].out, to[i], heads[i], L.parts[i], i == 2 ? c.dv : c.dk, c.dtype, s);
             if (st != GDR_OK) return st;
         }
     return GDR_OK;

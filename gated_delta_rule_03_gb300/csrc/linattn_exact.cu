@@ -261,10 +261,10 @@ template <typename T> int launch_t(const Plan &p, const Mix &m, cudaStream_t str
 
 template <typename T>
 __global__ void __launch_bounds__(256)
-share_kernel(const Plan p, const float *__restrict__ in, T *__restrict__ out, int g, int d) {
+share_kernel(const Plan p, const float *__restrict__ in, T *__restrict__ out, int heads, int g, int d) {
     const int64_t rows = p.cu_seqlens ? p.cu_seqlens[p.num_seqs] : p.total_tokens;
     if (p.status[0] != GDR_OK) return;
-    const int heads = p.H / g, quads = d / 4;
+    const int quads = d / 4;
     const int64_t total = rows * heads * quads;
     for (int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x; e < total; e += (int64_t)gridDim.x * 256) {
         const int j = (int)(e % quads) * 4;
@@ -288,15 +288,15 @@ int launch_mix_exact(const Plan &p, const Mix *mixes, int count, int dtype, cuda
     return GDR_OK;
 }
 
-int launch_share(const Plan &p, const float *in, void *out, int g, int d, int dtype,
+int launch_share(const Plan &p, const float *in, void *out, int heads, int g, int d, int dtype,
                  cudaStream_t stream) {
-    const int64_t quads = p.total_tokens * (p.H / g) * (d / 4);
+    const int64_t quads = p.total_tokens * heads * (d / 4);
     const int64_t blocks = (quads + 255) / 256;
     const unsigned grid = (unsigned)(blocks < 152 * 16 ? blocks : 152 * 16);
     if (dtype == GDR_BF16)
-        share_kernel<<<grid, 256, 0, stream>>>(p, in, (__nv_bfloat16 *)out, g, d);
+        share_kernel<<<grid, 256, 0, stream>>>(p, in, (__nv_bfloat16 *)out, heads, g, d);
     else
-        share_kernel<<<grid, 256, 0, stream>>>(p, in, (float *)out, g, d);
+        share_kernel<<<grid, 256, 0, stream>>>(p, in, (float *)out, heads, g, d);
     return cuda_status(cudaGetLastError());
 }
 

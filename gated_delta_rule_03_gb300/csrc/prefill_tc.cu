@@ -215,6 +215,13 @@ bool make_map_thd(CUtensorMap *map, const void *base, int d, int H, int64_t T) {
     return encode_3d(map, base, dims, strides, box);
 }
 
+bool make_map_rows(CUtensorMap *map, const void *base, int d, int heads, int64_t stride, int64_t T) {
+    const cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)heads, (cuuint64_t)T};
+    const cuuint64_t strides[2] = {(cuuint64_t)d * 2, (cuuint64_t)stride * 2};
+    const cuuint32_t box[3] = {64, 1, 128};
+    return encode_3d(map, base, dims, strides, box);
+}
+
 bool make_map_rows_f32(CUtensorMap *map, const float *base, int d, int H, int64_t T) {
     const cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)H, (cuuint64_t)T};
     const cuuint64_t strides[2] = {(cuuint64_t)d * 4, (cuuint64_t)d * H * 4};

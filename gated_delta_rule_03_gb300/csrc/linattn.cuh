@@ -153,8 +153,7 @@ __device__ __forceinline__ int64_t state_at(const Mix &m, int a, int b) {
 }
 
 int launch_mix_exact(const Plan &p, const Mix *mixes, int count, int dtype, cudaStream_t stream);
-int launch_mix_tc(const Plan &p, const Mix *mixes, int count, int d_v, bool sums, bool wide_state,
-                  cudaStream_t stream);
+int launch_mix_tc(const Plan &p, const Mix *mixes, int count, int d_v, bool sums, cudaStream_t stream);
 // Sums the g parts of every head: in fp32 [rows, heads g, d] -> out [rows, heads, d]. Rows
 // behind the last sequence are left as they are.
 int launch_share(const Plan &p, const float *in, void *out, int heads, int g, int d, int dtype,

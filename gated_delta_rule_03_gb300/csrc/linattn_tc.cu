@@ -3,28 +3,37 @@
 //
 // One CTA per (segment, head, 128 columns of d_v) walks its segment in chunks of C = 128
 // tokens. Per chunk, with the decay weights of linattn.cuh:
-//   P  = X Y^T            masked and weighted into bf16, kept in TMEM as an A operand
-//   Oi = X E              E: the state entering the chunk, as bf16 in shared memory
-//   Oa = P Z
-//   U  = Yw^T Z           Yw: the rows of Y times w_upd
-//   out = s_inter w_out Oi + Oa,   E <- lam^n E + U
-// Nothing that the tensor cores compute for a chunk depends on the state but Oi: the state
-// itself lives in fp32 registers, so that the sequential part of a chunk is one fused
-// multiply-add per element and its copy to shared memory. Every weight is at most 1.
+//   P  = X Y^T           masked and weighted into bf16, kept in TMEM as an A operand
+//   O  = P Z + X E       E: the state entering the chunk, as bf16 in shared memory
+//   U  = Yw^T Z          Yw: the rows of Y times w_upd, turned into TMEM as an A operand
+//   out_r = s_inter f_r O_r,   E <- lam^n E + U
+// Nothing that the tensor cores compute for a chunk depends on the state but X E: the
+// state itself lives in fp32 registers, so that the sequential part of a chunk is one fused
+// multiply-add per element and its copy to shared memory.
 //
-// Rounding. X, Y and Z are used as they are. P and the copy of E that Oi reads are rounded
-// to bf16 once each, as a product's operand has to be; either costs an output element
-// 2^-8 of the sum of its terms' sizes at most, like the output's own rounding. Yw is kept
-// as two bf16 parts, 16 bits: a term of the state is off by 2^-16 at most, where one part
-// would cost the outputs as much again as E's own rounding. U is summed chunk by chunk and
-// added to E in fp32: a sum over a whole segment in the tensor cores would lose more.
+// One accumulator for both halves of O: a row's factor f_r = max(w_out(r), 2^-60) is taken
+// out of it, so P's weights are lam^|r-i| / f_r. Where w_out is below 2^-60 the state's
+// part of that row counts for 2^-60 of its size instead of less: nothing, next to P Z in fp32.
 //
-// Shared memory: a ring of five 32 KB tiles for X, Y, Z (TMA, 128-byte swizzle), E in bf16,
-// 32 KB for the lower part of Yw. The upper part overwrites Y once P has been taken.
+// Rounding. X, Y and Z are used as they are. P and the copy of E are rounded to bf16 once
+// each, as a product's operand has to be; either costs an output element 2^-8 of the sum
+// of its terms' sizes at most, like the output's own rounding. Yw is kept as two bf16
+// parts, 16 bits: a term of the state is off by 2^-16 at most, where one part would cost the
+// outputs as much again as E's own rounding. U is summed chunk by chunk and added to E in
+// fp32: a sum over a whole segment in the tensor cores would lose more.
 //
-// Warps 0-7: P into TMEM, then the output rows. Warps 8-15: Yw, the state (64 registers of a
-// thread's 96 hold it). Warp 16: the loads. Warp 17: the MMAs, in the order P, Oi, U of the first 64 tokens, Oa, U of the
-// others: each conversion runs behind products that do not need it.
+// What bounds it: a product of two operands in shared memory reads them at all of shared
+// memory's bandwidth (128 x 128 x 16: 8 KB in 64 cycles), and loads, conversions and copies
+// use the same. So P and Yw are A operands in TMEM (512 columns: P, O, U, Yw of 128 each),
+// and Yw goes there straight from Y (ldmatrix turns it) instead of through shared memory.
+//
+// Shared memory: X, Y and Z tiles of two chunks (TMA, 128-byte swizzle), E in bf16.
+// Warp 17 issues the MMAs in the order P Z, X E, P of the next chunk, U. Warps 0-15 all do
+// the same work on a sixteenth each (a lane quarter by 32 columns or tokens), in the order
+// in which the products end: the output rows, P's weights of the next chunk, the state, Yw of
+// the next chunk. Warp 16: the loads. With 96 registers a thread nothing may spill (shared
+// memory leaves no first-level cache to spill to): hence 16 columns at a time, and
+// what would be worked out ahead of the loop made opaque.
 #include "linattn.cuh"
 #include "tc_common.cuh"
 
@@ -37,13 +46,11 @@ using tc::pack_bf16x2;
 
 constexpr int C = 128;
 constexpr uint32_t TILE = 32768, BLOCK = 16384;  // a tile: two blocks of 64 columns
-constexpr int kSlots = 5;
-constexpr uint32_t OFF_E = kSlots * TILE, OFF_LOW = OFF_E + TILE, OFF_END = OFF_LOW + TILE;
-constexpr uint32_t kSmem = OFF_END + 1024;  // slack for the 1024-byte alignment
-constexpr uint32_t TM_P = 0, TM_OA = 128, TM_OI = 256, TM_U = 384, TM_COLS = 512;
-constexpr int kRowWarps = 8, kStateWarps = 8, kThreads = 32 * (kRowWarps + kStateWarps + 2);
-constexpr int kRowThreads = 32 * kRowWarps, kStateThreads = 32 * kStateWarps;
-constexpr int kLoadWarp = kRowWarps + kStateWarps;
+constexpr int kSlots = 6;
+constexpr uint32_t OFF_E = kSlots * TILE, kSmem = OFF_E + TILE;
+constexpr uint32_t TM_P = 0, TM_O = 128, TM_U = 256, TM_Y = 384, TM_COLS = 512;
+constexpr int kWorkers = 16, kWorkThreads = 32 * kWorkers, kLoadWarp = kWorkers;
+constexpr int kThreads = kWorkThreads + 64;
 
 struct TcMix {
     int mx, my, mz;              // maps
@@ -54,12 +61,13 @@ struct TcMix {
     int64_t out_row, out_h, out_s;  // elements from one token, head, slice to the next
     bool out_f32, turned, backward;
     int astep, bstep;            // rows and columns of the state from one slice to the next
-    float s_intra, s_inter, s_state;
+    float s_intra, s_inter, s_state;  // (s_intra: relative to s_inter)
     const float *start, *R;
     float *end, *R_out;
 };
 struct TcArgs {
-    CUtensorMap maps[4];
+    CUtensorMap maps[4];  // q, k, v, do
+    CUtensorMap outs[3];  // the mixes' outputs (bf16)
     Plan p;
     TcMix mix[3];
     int count, slices;
@@ -104,53 +112,104 @@ __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
     return d;
 }
 
-// The weights of a chunk's rows, for n tokens, as two bf16 parts each (the larger in the
-// low half); rows behind the last token get 0. By 256 threads, which meet at barrier 1.
-__device__ __forceinline__ void row_weights(uint32_t *table, int n, bool backward, float l2, float s, int id) {
-    asm volatile("bar.sync 1, 256;" ::: "memory");  // the table before has been used
-    if (id < C) {
-        const float x = id < n ? s * decay_pow(l2, (float)(backward ? id + 1 : n - 1 - id)) : 0.f;
-        table[id] = pack_bf16x2(x, x - __bfloat162float(__float2bfloat16_rn(x)));
-    }
-    asm volatile("bar.sync 1, 256;" ::: "memory");
+// The weights of the 32 tokens that a warp weighs, of a chunk of n, as two bf16 parts:
+// table[i] holds the larger parts of tokens 32 sub + 2i and the one after, then the smaller
+// ones. Each warp has a table of its own.
+__device__ __forceinline__ void row_weights(uint2 *table, int n, bool backward, float l2, float s, int sub, int lane) {
+    __syncwarp();
+    const int r = 32 * sub + 2 * (lane & 15);
+    const float x = s * decay_pow(l2, (float)(backward ? r + 1 : max(n - 1 - r, 0)));
+    const float y = s * decay_pow(l2, (float)(backward ? r + 2 : max(n - 2 - r, 0)));
+    const float hx = __bfloat162float(__float2bfloat16_rn(x)), hy = __bfloat162float(__float2bfloat16_rn(y));
+    if (lane < 16) table[lane] = make_uint2(pack_bf16x2(hx, hy), pack_bf16x2(x - hx, y - hy));
+    __syncwarp();
 }
 
-// Rows [64 half, 64 half + 64) of the Y tile times their weights, as two bf16 parts: the
-// larger in place, the other to `low` (the same places in a tile of its own). With the
-// weight w = wh + wl (bf16 each), hi = round(y wh), lo = y wh - hi (exact: what is left of
-// 16 bits) + y wl. `id` of 256 threads.
-template <int HALF>
-__device__ __forceinline__ void weigh_half(unsigned char *y, unsigned char *low, int blocks, int n,
-                                           const uint32_t *table, int id) {
-    const uint32_t at = (64 * HALF + (id >> 3)) * 128 + (id & 7) * 16;
+__device__ __forceinline__ void ldmatrix_x4_trans(uint32_t (&r)[4], uint32_t at) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(at)
+                 : "memory");
+}
+// 16 TMEM lanes x 8 columns: register 2j + e of thread t is lane 8e + t/4, column 4j + t%4.
+__device__ __forceinline__ void tmem_store_16x128b_x2(uint32_t taddr, const uint32_t (&r)[4]) {
+    asm volatile("tcgen05.st.sync.aligned.16x128b.x2.b32 [%0], {%1, %2, %3, %4};" ::"r"(taddr), "r"(r[0]),
+                 "r"(r[1]), "r"(r[2]), "r"(r[3])
+                 : "memory");
+}
+// 16 columns of this thread's TMEM lane on their way; tmem_arrived names them, so that no use
+// comes before it. (It waits for every load of the thread.)
+__device__ __forceinline__ void tmem_fetch16(uint32_t taddr, uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr)
+        : "memory");
+}
+__device__ __forceinline__ void tmem_arrived(uint32_t (&r)[16]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                   "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]),
+                   "+r"(r[15])::"memory");
+}
+__device__ __forceinline__ void tmem_store8_nowait(uint32_t taddr, const uint32_t (&r)[8]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr),
+                 "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                 : "memory");
+}
+__device__ __forceinline__ void tmem_store_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// Yw of 32 tokens into TMEM: lane = column of Y, TMEM column = two tokens, the larger parts
+// at `taddr`, the smaller ones 64 columns on. With a weight w = wh + wl (bf16 each),
+// hi = round(y wh), lo = y wh - hi (exact: what is left of 16 bits) + y wl. A warp takes the
+// 32 columns of its lane quarter and the tokens 32 sub ..; ldmatrix hands each thread two
+// tokens of one column, as the store wants them.
+__device__ __forceinline__ void weigh(uint32_t y, uint32_t taddr, int quarter, int sub, int n,
+                                      const uint2 *table, int lane) {
+    const int mat = lane >> 3;
+    const int token = 32 * sub + (mat >> 1) * 8 + (lane & 7);
+#pragma unroll 1
+    for (int mb = 0; mb < 2; ++mb) {
+        const int m0 = 32 * quarter + 16 * mb, chunk = ((m0 & 63) >> 3) + (mat & 1);
+        const uint32_t at = y + (m0 >> 6) * BLOCK + token * 128 + (((chunk ^ lane) & 7) << 4);
+        const uint32_t to = taddr + ((uint32_t)m0 << 16) + 16 * sub;
+        uint32_t r[2][4];
+        ldmatrix_x4_trans(r[0], at);
+        ldmatrix_x4_trans(r[1], at + 2048);  // 16 tokens further on
+        if (n < C) {  // whatever lies behind the last token
 #pragma unroll
-    for (int it = 0; it < 2; ++it) {
-        const int r = 64 * HALF + 32 * it + (id >> 3);
-        const __nv_bfloat162 w = reinterpret_cast<const __nv_bfloat162 &>(table[r]);
-        const __nv_bfloat162 wh = __low2bfloat162(w), wl = __high2bfloat162(w);
+            for (int i = 0; i < 4; ++i) {
+                const int t = 32 * sub + 8 * i + 2 * (lane & 3);
+                const uint32_t keep = t + 1 < n ? 0xffffffffu : (t < n ? 0xffffu : 0u);
+                r[i >> 1][2 * (i & 1)] &= keep;
+                r[i >> 1][2 * (i & 1) + 1] &= keep;
+            }
+        }
 #pragma unroll
-        for (int b = 0; b < 2; ++b) {
-            if (b >= blocks) break;
-            uint4 lo, in = *reinterpret_cast<const uint4 *>(y + b * BLOCK + at + it * 4096);
-            if (r >= n) in = make_uint4(0, 0, 0, 0);  // (whatever lies behind the last token)
-            uint32_t *pi = &in.x, *pl = &lo.x;
+        for (int jj = 0; jj < 2; ++jj) {
+            uint32_t hi[4], lo[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                const __nv_bfloat162 k = reinterpret_cast<const __nv_bfloat162 &>(pi[e]);
-                const __nv_bfloat162 h = __hmul2_rn(k, wh);
-                const __nv_bfloat162 l = __hfma2(k, wl, __hfma2(k, wh, __hneg2(h)));
-                pi[e] = reinterpret_cast<const uint32_t &>(h);
-                pl[e] = reinterpret_cast<const uint32_t &>(l);
+                const uint2 w = table[8 * jj + 4 * (e >> 1) + (lane & 3)];  // of two tokens
+                const __nv_bfloat162 v = reinterpret_cast<const __nv_bfloat162 &>(r[jj][e]);
+                const __nv_bfloat162 wh = reinterpret_cast<const __nv_bfloat162 &>(w.x);
+                const __nv_bfloat162 wl = reinterpret_cast<const __nv_bfloat162 &>(w.y);
+                const __nv_bfloat162 h = __hmul2_rn(v, wh);
+                const __nv_bfloat162 l = __hfma2(v, wl, __hfma2(v, wh, __hneg2(h)));
+                hi[e] = reinterpret_cast<const uint32_t &>(h);
+                lo[e] = reinterpret_cast<const uint32_t &>(l);
             }
-            *reinterpret_cast<uint4 *>(y + b * BLOCK + at + it * 4096) = in;
-            *reinterpret_cast<uint4 *>(low + b * BLOCK + at + it * 4096) = lo;
+            tmem_store_16x128b_x2(to + 8 * jj, hi);
+            tmem_store_16x128b_x2(to + 64 + 8 * jj, lo);
         }
     }
 }
 
 // Rows n .. 127 of a tile become zero.
 __device__ __forceinline__ void clear_behind(unsigned char *tile, int blocks, int n, int id) {
-    for (int e = id; e < (C - n) * 8 * blocks; e += kStateThreads) {
+    for (int e = id; e < (C - n) * 8 * blocks; e += kWorkThreads) {
         const int b = e / ((C - n) * 8), r = n + e / 8 % (C - n);
         *reinterpret_cast<uint4 *>(tile + b * BLOCK + r * 128 + (e & 7) * 16) = make_uint4(0, 0, 0, 0);
     }
@@ -184,89 +243,70 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t db, uint
         : "memory");
 }
 
-// The MMAs of U over 64 tokens, the smaller part first. Descriptors of the whole tiles.
-__device__ __forceinline__ void issue_update(uint32_t d, uint32_t y, uint32_t low, uint32_t z, int half,
-                                             uint32_t idesc) {
+// The MMAs of U: the smaller part first.
+__device__ __forceinline__ void issue_update(uint32_t d, uint32_t y, uint32_t z, uint32_t idesc) {
 #pragma unroll
     for (int i = 1; i >= 0; --i)
 #pragma unroll
-        for (int kk = 0; kk < 4; ++kk) {
-            const uint32_t at = (4 * half + kk) * 2048;
-            mma_ss(d, i ? low : y, at, z, at, idesc, !(half == 0 && i == 1 && kk == 0));
-        }
+        for (int kk = 0; kk < 8; ++kk) mma_ts(d, y + 64 * i + 8 * kk, z, kk * 2048, idesc, i == 0 || kk > 0);
 }
 
-// E <- w E + 64 columns of this thread's TMEM lane.
-__device__ __forceinline__ void add_update(float2 (&E)[32], float w, uint32_t taddr) {
+// E <- w E + 32 columns of this thread's TMEM lane.
+__device__ __forceinline__ void add_update(float2 (&E)[16], float w, uint32_t taddr) {
     const float2 w2 = make_float2(w, w);
+    uint32_t u[2][16];
+    tmem_fetch16(taddr, u[0]);
+    tmem_fetch16(taddr + 16, u[1]);
+    tmem_arrived(u[0]);
+    tmem_arrived(u[1]);
 #pragma unroll
-    for (int part = 0; part < 4; ++part) {  // (16 at a time: registers)
-        float u[16];
-        tmem_load16(taddr + 16 * part, u);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) E[8 * part + j] = fma2(w2, E[8 * part + j], make_float2(u[2 * j], u[2 * j + 1]));
-    }
+    for (int j = 0; j < 16; ++j)
+        E[j] = fma2(w2, E[j], make_float2(__uint_as_float(u[j >> 3][2 * j & 15]), __uint_as_float(u[j >> 3][(2 * j & 15) + 1])));
 }
 
-// Four lanes that hold 64 bytes each of a row of their own: afterwards bytes 16 i .. of lane
-// q's registers are bytes 16 q .. of lane i's row.
-__device__ __forceinline__ void turn_four(uint32_t (&p)[16], int lane) {
-#pragma unroll
-    for (int step = 1; step < 4; step *= 2) {
-        const bool up = lane & step;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            if (i & step) continue;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                // the lower lane sends its part i + step, the upper one its part i
-                const uint32_t mine = up ? p[4 * i + e] : p[4 * (i + step) + e];
-                const uint32_t other = __shfl_xor_sync(0xffffffffu, mine, step);
-                if (up) p[4 * i + e] = other;
-                else p[4 * (i + step) + e] = other;
-            }
-        }
-    }
-}
-
-// A thread's 64 columns of state row a, from or to memory.
+// A thread's 32 columns of state row a, from or to memory.
 struct StateAt {
-    int64_t first, step;  // element of column 0, elements from one column to the next
+    int64_t first;  // element of column 0
+    int step;       // elements from one column to the next
 };
 __device__ __forceinline__ StateAt state_row(const TcArgs &A, const TcMix &m, int slice, int a, int b) {
     const int64_t aa = a + m.astep * slice, bb = b + m.bstep * slice;
     return m.turned ? StateAt{bb * A.pitch + aa, A.pitch} : StateAt{aa * A.pitch + bb, 1};
 }
-__device__ __forceinline__ void read_state(float2 (&E)[32], const float *S, const StateAt &at, float w) {
+// (pointers are opaque after every step: 32 places worked out ahead would take 64 registers)
+// Eight of the columns, from column 8 part on, times w added to `sum`.
+__device__ __forceinline__ void read_state(float (&sum)[8], const float *S, const StateAt &at, int part, float w) {
+    const float *p = S + at.first + (int64_t)(8 * part) * at.step;
     if (at.step == 1) {
 #pragma unroll
-        for (int j = 0; j < 32; j += 2) {
-            if (j % 8 == 0) asm volatile("" ::: "memory");  // (four loads at a time: registers)
-            const float4 x = *reinterpret_cast<const float4 *>(S + at.first + 2 * j);
-            E[j].x = fmaf(w, x.x, E[j].x);
-            E[j].y = fmaf(w, x.y, E[j].y);
-            E[j + 1].x = fmaf(w, x.z, E[j + 1].x);
-            E[j + 1].y = fmaf(w, x.w, E[j + 1].y);
+        for (int j = 0; j < 8; j += 4) {
+            const float4 x = *reinterpret_cast<const float4 *>(p + j);
+            sum[j] = fmaf(w, x.x, sum[j]);
+            sum[j + 1] = fmaf(w, x.y, sum[j + 1]);
+            sum[j + 2] = fmaf(w, x.z, sum[j + 2]);
+            sum[j + 3] = fmaf(w, x.w, sum[j + 3]);
         }
     } else {
 #pragma unroll
-        for (int j = 0; j < 32; ++j) {
-            if (j % 8 == 0) asm volatile("" ::: "memory");
-            E[j].x = fmaf(w, S[at.first + 2 * j * at.step], E[j].x);
-            E[j].y = fmaf(w, S[at.first + (2 * j + 1) * at.step], E[j].y);
+        for (int j = 0; j < 8; ++j) {
+            sum[j] = fmaf(w, *p, sum[j]);
+            p += at.step;
+            asm volatile("" : "+l"(p));
         }
     }
 }
-__device__ __forceinline__ void write_state(const float2 (&E)[32], float *S, const StateAt &at) {
-    if (at.step == 1) {
+__device__ __forceinline__ void write_state(const float2 (&E)[16], float *p, int step) {
+    if (step == 1) {
 #pragma unroll
-        for (int j = 0; j < 32; j += 2)
-            *reinterpret_cast<float4 *>(S + at.first + 2 * j) = make_float4(E[j].x, E[j].y, E[j + 1].x, E[j + 1].y);
+        for (int j = 0; j < 16; j += 2)
+            *reinterpret_cast<float4 *>(p + 2 * j) = make_float4(E[j].x, E[j].y, E[j + 1].x, E[j + 1].y);
     } else {
 #pragma unroll
-        for (int j = 0; j < 32; ++j) {
-            S[at.first + 2 * j * at.step] = E[j].x;
-            S[at.first + (2 * j + 1) * at.step] = E[j].y;
+        for (int j = 0; j < 16; ++j) {
+            p[0] = E[j].x;
+            p[step] = E[j].y;
+            p += 2 * step;
+            asm volatile("" : "+l"(p));
         }
     }
 }
@@ -278,19 +318,22 @@ struct Work {
     int64_t item;
 };
 
-enum { B_FULL = 0, B_EMPTY = kSlots, B_P = 2 * kSlots, B_PREADY, B_Y0, B_Y1, B_U, B_EREADY,
-       B_O, B_OFREE, B_DRAIN, B_COUNT };
+enum { B_FULL = 0, B_EMPTY = kSlots, B_P = 2 * kSlots, B_PREADY, B_A, B_YREADY, B_U, B_EREADY,
+       B_O, B_OFREE, B_STAGED, B_DRAIN, B_COUNT };
 
+// One body for both directions, its loops kept rolled where they can be: the warps of a
+// block run far apart in the code, and a copy of it per direction or role costs more in
+// instruction fetches than the selects do (gradients: 2.5 times the time with three copies).
 __global__ void __launch_bounds__(kThreads, 1) mix_tc_kernel(const __grid_constant__ TcArgs A) {
-    extern __shared__ __align__(1024) unsigned char smem_raw[];
-    unsigned char *sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    extern __shared__ __align__(1024) unsigned char sm[];
     const uint32_t base = smem_u32(sm);
     __shared__ Segment found;
     __shared__ __align__(8) uint64_t bars[B_COUNT];
     __shared__ uint32_t tmem_slot;
     __shared__ int gave_up;
-    __shared__ uint32_t row_w[C];
-    __shared__ __align__(16) float step_pow[32];  // lam^(31-j), or lam^j from last to first
+    __shared__ Work kept;  // (for the end, in no register meanwhile)
+    __shared__ uint2 weights[kWorkers][16];
+    __shared__ __align__(16) float pow_of[32];  // lam^(31-j), or lam^j from last to first
     auto bar = [&](int i) { return smem_u32(&bars[i]); };
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
@@ -305,36 +348,43 @@ __global__ void __launch_bounds__(kThreads, 1) mix_tc_kernel(const __grid_consta
     if (blockIdx.x == 0 && tid == 0 && A.p.first) A.p.status[0] = bad ? GDR_ERR_BAD_SEQLENS : GDR_OK;
     if (bad || w.s.seq < 0) return;
     const TcMix &m = A.mix[w.role];
-    const float l2 = log2_decay(A.p.log_decay[w.h]);
+    const bool back = m.backward;
+    const float l2_of_head = log2_decay(A.p.log_decay[w.h]);
     const int chunks = (int)((w.s.tokens + C - 1) / C);
-    const bool ends = m.end && w.s.f == (m.backward ? 0 : w.s.n - 1);
-    auto chunk_of = [&](int cc) { return m.backward ? chunks - 1 - cc : cc; };
-    auto tokens_of = [&](int c) {
-        const int64_t r = w.s.tokens - (int64_t)c * C;
-        return (int)(r < C ? r : C);
-    };
-    auto slot = [&](int t) { return base + (uint32_t)(t % kSlots) * TILE; };
-    auto slot_p = [&](int t) { return sm + (uint32_t)(t % kSlots) * TILE; };
+    const bool ends = m.end && w.s.f == (back ? 0 : w.s.n - 1);
+    auto chunk_of = [&](int cc) { return back ? chunks - 1 - cc : cc; };
+    const int tail = (int)(w.s.tokens - (int64_t)(chunks - 1) * C);  // tokens of the last chunk
+    auto tokens_of = [&](int c) { return c == chunks - 1 ? tail : C; };
+    // tile i (X, Y, Z) of chunk cc: its slot, and the phase of the slot's barriers
+    auto slot = [&](int cc, int i) { return 3 * (cc & 1) + i; };
+    auto phase = [&](int cc) { return cc >> 1; };
 
     if (tid == 0) {
-        for (int i = 0; i < 2 * kSlots; ++i) mbar_init(bar(i), 1);
+        // (X, Y, Z, X, Y, Z: Y is freed by the warps that weigh it, X by the output that has
+        // left it)
+        for (int i = 0; i < kSlots; ++i) {
+            mbar_init(bar(B_FULL + i), 1);
+            mbar_init(bar(B_EMPTY + i), i % 3 == 1 ? kWorkers : 1);
+        }
         mbar_init(bar(B_P), 1);
-        mbar_init(bar(B_PREADY), kRowThreads);
-        mbar_init(bar(B_Y0), kStateThreads);
-        mbar_init(bar(B_Y1), kStateThreads);
+        mbar_init(bar(B_PREADY), kWorkers);
+        mbar_init(bar(B_A), 1);
+        mbar_init(bar(B_YREADY), kWorkers);
         mbar_init(bar(B_U), 1);
-        mbar_init(bar(B_EREADY), kStateThreads);
+        mbar_init(bar(B_EREADY), kWorkers);
         mbar_init(bar(B_O), 1);
-        mbar_init(bar(B_OFREE), kRowThreads);
+        mbar_init(bar(B_OFREE), kWorkers);
+        mbar_init(bar(B_STAGED), kWorkers);
         mbar_init(bar(B_DRAIN), 1);
         fence_mbar_init();
         gave_up = 0;
+        kept = w;
         prefetch_tensormap(&A.maps[m.mx]);
         prefetch_tensormap(&A.maps[m.my]);
         prefetch_tensormap(&A.maps[m.mz]);
     }
     if (tid < 32) {
-        step_pow[tid] = decay_pow(l2, (float)(m.backward ? tid : 31 - tid));
+        pow_of[tid] = decay_pow(l2_of_head, (float)(back ? tid : 31 - tid));
         tmem_alloc(smem_u32(&tmem_slot), TM_COLS);
         tmem_relinquish();
     }
@@ -361,250 +411,310 @@ __global__ void __launch_bounds__(kThreads, 1) mix_tc_kernel(const __grid_consta
     // by a whole warp: converged again, and of one mind
     auto warp_wait = [&](int b, int phase) -> bool { return __all_sync(0xffffffffu, wait(b, phase)); };
 
-    if (warp < kRowWarps) {
-        // ------------------------------------------------ P, then the output rows
-        // two warps per lane quarter, each with half of the columns
-        const int quarter = warp & 3, side = warp >> 2;
-        const uint32_t lanes = tmem + ((uint32_t)(32 * quarter) << 16);
-        const int t = 32 * quarter + lane;  // row of the chunk
-        // lam^(t-i) = lam^(t - 32b - 31) lam^(31 - (i - 32b)): the first is at most 1 off the
-        // diagonal block and at most lam^-31 on it, a float unless lam < 1/16 (`steep`)
-        const bool steep = l2 < -4.f;
-        float2 far[2];
+    if (warp < kWorkers) {
+        int quarter = warp & 3, sub = warp >> 2;
+        int lane = tid & 31;
+        float l2 = l2_of_head;
+        uint32_t lanes = tmem + ((uint32_t)(32 * quarter) << 16);
+        int t = 32 * quarter + lane;  // row of the chunk, and of the state
+        int col = 32 * sub;          // this warp's columns of P, O and the state
+        const bool has_z = col < 64 * m.zb;
+        // an arrival for the warp, after what its lanes have written
+        auto arrive = [&](int b) {
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(b));
+        };
+
+        // ---- the state: row t, columns col ..
+        const StateAt st = state_row(A, m, w.slice, t, col);
+        const bool mine = t < 64 * m.xb && has_z;
+        float2 E[16];
 #pragma unroll
-        for (int bb = 0; bb < 2; ++bb) {
-            const int b = 2 * side + bb;
-            far[bb].x = far[bb].y = m.s_intra * ex2(l2 * (float)(m.backward ? 32 * b - t : t - 32 * b - 31));
+        for (int j = 0; j < 16; ++j) E[j] = make_float2(0.f, 0.f);
+        if (mine && (m.start || m.R)) {
+            const float *const S = m.start ? m.start + ((int64_t)w.s.seq * A.p.H + w.h) * A.mat : nullptr;
+            const float ws = decay_pow(l2, (float)(back ? w.s.behind : (int64_t)w.s.f * A.p.seg));
+            const float *const R = m.R ? m.R + (w.s.item0 * A.p.H + w.h) * A.mat : nullptr;
+            const int64_t next = A.p.H * A.mat;  // from one segment's sum to the next one's
+#pragma unroll
+            for (int part = 0; part < 4; ++part) {
+                float sum[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) sum[i] = 0.f;
+                if (S) read_state(sum, S, st, part, ws);
+#pragma unroll 1
+                for (int g = back ? w.s.f + 1 : 0; R && g < (back ? w.s.n : w.s.f); ++g) {
+                    const int apart = back ? g - 1 - w.s.f : w.s.f - 1 - g;
+                    read_state(sum, R + g * next, st, part, decay_pow(l2, (float)(apart * A.p.seg)));
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) E[4 * part + i] = make_float2(sum[2 * i], sum[2 * i + 1]);
+            }
         }
-        for (int cc = 0; cc < chunks; ++cc) {
-            const int c = chunk_of(cc), n = tokens_of(c);
-            if (!warp_wait(B_P, cc)) break;
+        // rows of E as the K rows of a B operand
+        auto publish = [&]() {
+            if (has_z) {
+                unsigned char *row = sm + OFF_E + (sub >> 1) * BLOCK + t * 128;
+#pragma unroll
+                for (int j = 0; j < 16; j += 4)
+                    *reinterpret_cast<uint4 *>(row + ((((4 * sub + (j >> 2)) ^ t) & 7) << 4)) =
+                        make_uint4(pack_bf16x2(E[j].x, E[j].y), pack_bf16x2(E[j + 1].x, E[j + 1].y),
+                                   pack_bf16x2(E[j + 2].x, E[j + 2].y), pack_bf16x2(E[j + 3].x, E[j + 3].y));
+            }
+            fence_async_smem();
+            arrive(B_EREADY);
+        };
+
+        // ---- Yw
+        int weighed = 0;  // the length that the weights are for
+        auto weigh_chunk = [&](int cc) -> bool {
+            const int n = tokens_of(chunk_of(cc)), sy = slot(cc, 1);
+            if (n != weighed) row_weights(weights[warp], weighed = n, back, l2, m.s_state, sub, lane);
+            if (!warp_wait(B_FULL + sy, phase(cc))) return false;
+            if (quarter < 2 * m.xb) weigh(base + sy * TILE, tmem + TM_Y, quarter, sub, n, weights[warp], lane);
+            tmem_store_wait();
+            tc_fence_before();
+            arrive(B_EMPTY + sy);
+            if (lane == 0) mbar_arrive(bar(B_YREADY));
+            return true;
+        };
+
+        // ---- P's weights lam^|t-i| / f_t: 2^60 at most
+        auto row_factor = [&](int n) {  // log2 f_t
+            return fmaxf(l2 * (float)(back ? max(n - 1 - t, 0) : t + 1), -60.f);
+        };
+        auto weigh_scores = [&](int cc) -> bool {
+            const int n = tokens_of(chunk_of(cc)), sz = slot(cc, 2);
+            if (n < C) {  // Z's rows behind the last token meet P's zeros
+                if (!warp_wait(B_FULL + sz, phase(cc))) return false;
+                clear_behind(sm + sz * TILE, m.zb, n, tid);
+                fence_async_smem();
+            }
+            if (!warp_wait(B_P, cc)) return false;
             tc_fence_after();
+            const float f = row_factor(n);
+            // 16 columns at a time, the next ones on their way meanwhile
+            const bool diagonal = sub == quarter;
+            if (back ? sub < quarter : sub > quarter) {
+                const uint32_t none[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+                tmem_store8_nowait(lanes + TM_P + col, none);
+                tmem_store8_nowait(lanes + TM_P + col + 8, none);
+            } else {
+                uint32_t ahead[16];
+                tmem_fetch16(lanes + TM_P + col, ahead);
+                // off the diagonal: the way to the block's near column, times the way on to column j
+                const float far = m.s_intra * ex2(l2 * (float)(back ? col - t : t - col - 31) - f);
+                const float2 far2 = make_float2(far, far);
+                const float l2s = back ? -l2 : l2;
+                const int lo = back && diagonal ? lane : 0, hi = back ? n - 1 - col : (diagonal ? lane : 31);
 #pragma unroll
-            for (int bb = 0; bb < 2; ++bb) {
-                const int b = 2 * side + bb;
-                uint32_t out[16];
-                if (m.backward ? b < quarter : b > quarter) {
+                for (int half = 0; half < 2; ++half) {
+                    tmem_arrived(ahead);
+                    float v[16];
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) out[j] = 0;
-                } else {
-                    float v[32];
-                    tmem_load32(lanes + TM_P + 32 * b, v);
-                    if (steep && b == quarter) {
+                    for (int j = 0; j < 16; ++j) v[j] = __uint_as_float(ahead[j]);
+                    if (half == 0) tmem_fetch16(lanes + TM_P + col + 16, ahead);
+                    if (diagonal) {  // each distance by itself
+                        // (the distance itself: 0 has to meet -inf's stand-in as 0)
+                        const float from = (float)(lane - 16 * half);
 #pragma unroll
-                        for (int j = 0; j < 32; ++j)
-                            v[j] *= m.s_intra * ex2(l2 * (float)(m.backward ? j - lane : lane - j));
+                        for (int j = 0; j < 16; ++j) v[j] *= m.s_intra * ex2(fmaf(l2s, from - (float)j, -f));
                     } else {
 #pragma unroll
-                        for (int j = 0; j < 32; j += 4) {
-                            const float4 g = *reinterpret_cast<const float4 *>(&step_pow[j]);
-                            const float2 x = mul2(make_float2(v[j], v[j + 1]), mul2(far[bb], make_float2(g.x, g.y)));
-                            const float2 z = mul2(make_float2(v[j + 2], v[j + 3]), mul2(far[bb], make_float2(g.z, g.w)));
+                        for (int j = 0; j < 16; j += 4) {
+                            const float4 g = *reinterpret_cast<const float4 *>(&pow_of[16 * half + j]);
+                            const float2 x = mul2(make_float2(v[j], v[j + 1]), mul2(far2, make_float2(g.x, g.y)));
+                            const float2 z = mul2(make_float2(v[j + 2], v[j + 3]), mul2(far2, make_float2(g.z, g.w)));
                             v[j] = x.x;
                             v[j + 1] = x.y;
                             v[j + 2] = z.x;
                             v[j + 3] = z.y;
                         }
                     }
-                    // columns beyond the diagonal; from last to first, columns behind the last token
-                    const int first = m.backward ? t - 32 * b : 0, last = m.backward ? n - 1 - 32 * b : t - 32 * b;
-                    if (b == quarter || (m.backward && 32 * b + 32 > n)) {
+                    if (diagonal || hi < 31) {  // beyond the diagonal, or behind the last token
 #pragma unroll
-                        for (int j = 0; j < 32; ++j) v[j] = j >= first && j <= last ? v[j] : 0.f;
+                        for (int j = 0; j < 16; ++j) v[j] = 16 * half + j >= lo && 16 * half + j <= hi ? v[j] : 0.f;
                     }
+                    uint32_t out[8];
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) out[j] = pack_bf16x2(v[2 * j], v[2 * j + 1]);
+                    for (int j = 0; j < 8; ++j) out[j] = pack_bf16x2(v[2 * j], v[2 * j + 1]);
+                    // the bf16 copy goes to the first half of the block's own columns: those of
+                    // the second half's copy have been read by now
+                    tmem_store8_nowait(lanes + TM_P + col + 8 * half, out);
                 }
-                // the bf16 copy of a block overwrites the first half of its own columns
-                tmem_store16(lanes + TM_P + 32 * b, out);
             }
+            tmem_store_wait();
             tc_fence_before();
-            mbar_arrive(bar(B_PREADY));
-            if (!warp_wait(B_O, cc)) break;
-            tc_fence_after();
-            const float wo = m.s_inter * decay_pow(l2, (float)(m.backward ? (t < n ? n - 1 - t : 0) : t + 1));
-            const float2 wo2 = make_float2(wo, wo);
-            // rows leave four at a time, 16 bytes of a row per lane
-            const int r0 = 32 * quarter + (lane & ~3);
-            const int64_t at = (w.s.begin + (int64_t)c * C + r0) * m.out_row + w.h * m.out_h + w.slice * m.out_s;
-#pragma unroll 1
-            for (int b = m.zb * side; b < m.zb * side + m.zb; ++b) {
-                float oi[32], oa[32];
-                tmem_load32(lanes + TM_OA + 32 * b, oa);
-                tmem_load32(lanes + TM_OI + 32 * b, oi);
-                if (b == m.zb * side + m.zb - 1) {
-                    tc_fence_before();
-                    mbar_arrive(bar(B_OFREE));
-                }
-#pragma unroll
-                for (int j = 0; j < 32; j += 2) {
-                    const float2 x = fma2(wo2, make_float2(oi[j], oi[j + 1]), make_float2(oa[j], oa[j + 1]));
-                    oa[j] = x.x;
-                    oa[j + 1] = x.y;
-                }
-                if (m.out_f32) {
-                    float *o = (float *)m.out + at + 32 * b;
-#pragma unroll
-                    for (int half = 0; half < 2; ++half) {
-                        uint32_t p[16];
-#pragma unroll
-                        for (int j = 0; j < 16; ++j) p[j] = __float_as_uint(oa[16 * half + j]);
-                        turn_four(p, lane);
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            if (r0 + i < n)
-                                *reinterpret_cast<uint4 *>(o + i * m.out_row + 16 * half + 4 * (lane & 3)) =
-                                    make_uint4(p[4 * i], p[4 * i + 1], p[4 * i + 2], p[4 * i + 3]);
-                    }
-                } else {
-                    uint32_t p[16];
-#pragma unroll
-                    for (int j = 0; j < 16; ++j) p[j] = pack_bf16x2(oa[2 * j], oa[2 * j + 1]);
-                    turn_four(p, lane);
-                    __nv_bfloat16 *o = (__nv_bfloat16 *)m.out + at + 32 * b;
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        if (r0 + i < n)
-                            *reinterpret_cast<uint4 *>(o + i * m.out_row + 8 * (lane & 3)) =
-                                make_uint4(p[4 * i], p[4 * i + 1], p[4 * i + 2], p[4 * i + 3]);
-                }
-                __syncwarp();
-            }
-        }
-    } else if (warp < kLoadWarp) {
-        // ------------------------------------------------ Yw and the state
-        const int id = tid - kRowThreads;
-        const int a = 32 * (warp & 3) + lane, b0 = 64 * (id / 128);  // this thread's row and columns
-        const bool mine = a < 64 * m.xb && b0 < 64 * m.zb;
-        const uint32_t lanes = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
-        const StateAt st = state_row(A, m, w.slice, a, b0);
-        float2 E[32];
-#pragma unroll
-        for (int j = 0; j < 32; ++j) E[j] = make_float2(0.f, 0.f);
-        if (mine) {
-            if (m.start) {
-                const int64_t dist = m.backward ? w.s.behind : (int64_t)w.s.f * A.p.seg;
-                read_state(E, m.start + ((int64_t)w.s.seq * A.p.H + w.h) * A.mat, st, decay_pow(l2, (float)dist));
-            }
-            for (int g = m.backward ? w.s.f + 1 : 0; m.R && g < (m.backward ? w.s.n : w.s.f); ++g) {
-                const int apart = m.backward ? g - 1 - w.s.f : w.s.f - 1 - g;
-                read_state(E, m.R + ((w.s.item0 + g) * A.p.H + w.h) * A.mat, st, decay_pow(l2, (float)(apart * A.p.seg)));
-            }
-        }
-        // rows a of E as the K rows of a B operand: columns b0 .. b0 + 63, one swizzled block
-        auto publish = [&]() {
-            if (b0 < 64 * m.zb) {
-                unsigned char *row = sm + OFF_E + (b0 / 64) * BLOCK + a * 128;
-#pragma unroll
-                for (int j = 0; j < 32; j += 4)
-                    *reinterpret_cast<uint4 *>(row + ((((j >> 2) ^ a) & 7) << 4)) =
-                        make_uint4(pack_bf16x2(E[j].x, E[j].y), pack_bf16x2(E[j + 1].x, E[j + 1].y),
-                                   pack_bf16x2(E[j + 2].x, E[j + 2].y), pack_bf16x2(E[j + 3].x, E[j + 3].y));
-            }
-            fence_async_smem();
-            mbar_arrive(bar(B_EREADY));
+            arrive(B_PREADY);
+            return true;
         };
-        if (chunks > 0) publish();
-        int weighed = 0;  // the length that the weights are for
-        unsigned char *low = sm + OFF_LOW;
-        for (int cc = 0; cc < chunks; ++cc) {
+
+        // ---- the output rows, 32 columns of row t: by way of the chunk's X tile, which has been
+        // used, and TMA (by rows of their own the stores would take the load/store unit 2000
+        // cycles a chunk); what is not a whole tile of bf16, straight to its place
+        int pitch = (int)m.out_row * (m.out_f32 ? 4 : 2);
+        char *out0 = (char *)m.out + ((w.s.begin + t) * m.out_row + w.h * m.out_h + w.slice * m.out_s + col) * (m.out_f32 ? 4 : 2);
+        auto store_rows = [&](int cc) -> bool {
             const int c = chunk_of(cc), n = tokens_of(c);
-            const bool need = cc + 1 < chunks || ends;
-            if (!warp_wait(B_P, cc)) break;  // P has been taken: Y may be overwritten
-            if (!warp_wait(B_FULL + (3 * cc + 1) % kSlots, (3 * cc + 1) / kSlots)) break;
-            if (n < C) {
-                if (!warp_wait(B_FULL + (3 * cc + 2) % kSlots, (3 * cc + 2) / kSlots)) break;
-                clear_behind(slot_p(3 * cc + 2), m.zb, n, id);
-            }
-            unsigned char *y = slot_p(3 * cc + 1);
-            if (n != weighed) row_weights(row_w, weighed = n, m.backward, l2, m.s_state, id);
-            if (need) weigh_half<0>(y, low, m.xb, n, row_w, id);
-            fence_async_smem();
-            mbar_arrive(bar(B_Y0));
-            if (!need) continue;  // (the last chunk)
-            weigh_half<1>(y, low, m.xb, n, row_w, id);
-            fence_async_smem();
-            mbar_arrive(bar(B_Y1));
-            if (!warp_wait(B_U, cc)) break;
+            if (!warp_wait(B_O, cc)) return false;
             tc_fence_after();
-            if (b0 < 64 * m.zb) add_update(E, decay_pow(l2, (float)n), lanes + TM_U + b0);
+            uint32_t o[2][16];
+            tmem_fetch16(lanes + TM_O + col, o[0]);
+            tmem_fetch16(lanes + TM_O + col + 16, o[1]);
+            tmem_arrived(o[0]);
+            tmem_arrived(o[1]);
             tc_fence_before();
-            if (cc + 1 < chunks) publish();
-        }
-        if (ends && mine && !*stop)
-            write_state(E, m.end + ((int64_t)w.s.seq * A.p.H + w.h) * A.mat, st);
-    } else if (warp == kLoadWarp) {
-        // ------------------------------------------------ the loads
-        if (lane == 0) {
-            int issued = 0;
-            for (int cc = 0; cc < chunks; ++cc) {
-                const int t0 = (int)(w.s.begin + (int64_t)chunk_of(cc) * C);
-                bool ok = true;
-                for (int i = 0; i < 3 && ok; ++i) {
-                    const int t = 3 * cc + i;
-                    if (t >= kSlots && !(ok = wait(B_EMPTY + t % kSlots, t / kSlots - 1))) break;
-                    const CUtensorMap *map = &A.maps[i == 0 ? m.mx : (i == 1 ? m.my : m.mz)];
-                    const int col = w.slice * (i == 0 ? m.xstep : (i == 1 ? m.ystep : m.zstep));
-                    const int head = w.h / (i == 0 ? m.xg : (i == 1 ? m.yg : m.zg));
-                    const int blocks = i == 2 ? m.zb : m.xb;
-                    const uint32_t full = bar(B_FULL + t % kSlots);
-                    mbar_arrive_expect_tx(full, blocks * BLOCK);
-                    for (int b = 0; b < blocks; ++b)
-                        tma_load_3d(slot(t) + b * BLOCK, map, full, col + 64 * b, head, t0);
-                    ++issued;
+            arrive(B_OFREE);
+            const float wo = m.s_inter * ex2(row_factor(n));
+            const float2 wo2 = make_float2(wo, wo);
+            const bool tile = n == C && !m.out_f32;
+            unsigned char *row = sm + slot(cc, 0) * TILE + (sub >> 1) * BLOCK + t * 128;
+            char *to = out0 + (int64_t)c * C * pitch;
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                uint32_t p[8];
+                float2 x[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    x[j] = mul2(wo2, make_float2(__uint_as_float(o[half][2 * j]), __uint_as_float(o[half][2 * j + 1])));
+                    p[j] = pack_bf16x2(x[j].x, x[j].y);
                 }
-                if (!ok) break;
+                if (!has_z) {
+                } else if (tile) {
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
+                        *reinterpret_cast<uint4 *>(row + (((4 * sub + 2 * half + i) ^ t) & 7) * 16) =
+                            make_uint4(p[4 * i], p[4 * i + 1], p[4 * i + 2], p[4 * i + 3]);
+                } else if (t < n && m.out_f32) {
+#pragma unroll
+                    for (int j = 0; j < 8; j += 2)
+                        *reinterpret_cast<float4 *>(to + 64 * half + 8 * j) = make_float4(x[j].x, x[j].y, x[j + 1].x, x[j + 1].y);
+                } else if (t < n) {
+                    *reinterpret_cast<uint4 *>(to + 32 * half) = make_uint4(p[0], p[1], p[2], p[3]);
+                    *reinterpret_cast<uint4 *>(to + 32 * half + 16) = make_uint4(p[4], p[5], p[6], p[7]);
+                }
             }
+            fence_async_smem();
+            arrive(B_STAGED);
+            return true;
+        };
+        // (nothing needs the state behind the last chunk unless it goes out)
+        auto need = [&](int cc) { return cc + 1 < chunks || ends; };
+        // (one place for each step, the first chunk's included: the code is fetched as it runs)
+        bool ok = true;
+        for (int cc = -1; cc < chunks; ++cc) {
+            // opaque in every round: what follows from them, worked out ahead of the loop,
+            // would take more registers than there are
+            asm volatile("" : "+r"(pitch), "+l"(out0), "+r"(lane), "+r"(t), "+f"(l2), "+r"(quarter), "+r"(sub), "+r"(col), "+r"(lanes));
+            const bool more = cc + 1 < chunks;
+            if (cc >= 0 && !(ok = store_rows(cc))) break;
+            if (more && !(ok = weigh_scores(cc + 1))) break;
+            if (cc >= 0 && need(cc)) {
+                if (!(ok = warp_wait(B_U, cc))) break;
+                tc_fence_after();
+                if (has_z) add_update(E, decay_pow(l2, (float)tokens_of(chunk_of(cc))), lanes + TM_U + col);
+                tc_fence_before();
+            }
+            if (!more) break;
+            publish();
+            if (need(cc + 1) && !(ok = weigh_chunk(cc + 1))) break;
+        }
+        if (ends && ok && t < 64 * m.xb && has_z) {
+            const StateAt to = state_row(A, m, kept.slice, t, col);
+            write_state(E, m.end + ((int64_t)kept.s.seq * A.p.H + kept.h) * A.mat + to.first, to.step);
+        }
+    } else if (warp == kLoadWarp) {
+        // ------------------------------------------------ the loads, and the outputs' stores
+        if (lane == 0) {
+            int issued[3] = {0, 0, 0};
+            auto load = [&](int cc, int i) {
+                const int to = slot(cc, i);
+                const CUtensorMap *map = &A.maps[i == 0 ? m.mx : (i == 1 ? m.my : m.mz)];
+                const int at = w.slice * (i == 0 ? m.xstep : (i == 1 ? m.ystep : m.zstep));
+                const int head = w.h / (i == 0 ? m.xg : (i == 1 ? m.yg : m.zg));
+                const int blocks = i == 2 ? m.zb : m.xb, t0 = (int)(w.s.begin + (int64_t)chunk_of(cc) * C);
+                const uint32_t full = bar(B_FULL + to);
+                mbar_arrive_expect_tx(full, blocks * BLOCK);
+                for (int b = 0; b < blocks; ++b) tma_load_3d(base + to * TILE + b * BLOCK, map, full, at + 64 * b, head, t0);
+                ++issued[i];
+            };
+            for (int cc = 0; cc < 2 && cc < chunks; ++cc)
+                for (int i = 0; i < 3; ++i) load(cc, i);
+            const CUtensorMap *out = &A.outs[w.role];
+            const int out_col = m.out_s ? w.slice * (int)m.out_s : 0;
+            for (int cc = 0; cc < chunks; ++cc) {
+                const bool more = cc + 2 < chunks;
+                if (more) {
+                    if (!wait(B_EMPTY + slot(cc, 1), phase(cc))) break;
+                    load(cc + 2, 1);
+                }
+                if (!wait(B_STAGED, cc)) break;
+                if (tokens_of(chunk_of(cc)) == C && !m.out_f32) {
+                    for (int b = 0; b < m.zb; ++b)
+                        tma_store_3d(out, base + slot(cc, 0) * TILE + b * BLOCK, out_col + 64 * b, w.h,
+                                     (int)(w.s.begin + (int64_t)chunk_of(cc) * C));
+                    bulk_commit_group();
+                    bulk_wait_group_read<0>();
+                }
+                if (more) {
+                    load(cc + 2, 0);
+                    if (!wait(B_EMPTY + slot(cc, 2), phase(cc))) break;
+                    load(cc + 2, 2);
+                }
+            }
+            bulk_wait_group_all();
             // after a wait gave up: every load issued has landed before the block ends
-            for (int t = issued > kSlots ? issued - kSlots : 0; *stop && t < issued; ++t)
-                mbar_wait_for(bar(B_FULL + t % kSlots), (t / kSlots) & 1, A.wait_cycles);
+            for (int i = 0; *stop && i < 3; ++i)
+                for (int cc = issued[i] > 2 ? issued[i] - 2 : 0; cc < issued[i]; ++cc)
+                    mbar_wait_for(bar(B_FULL + slot(cc, i)), phase(cc) & 1, A.wait_cycles);
         }
     } else if (lane == 0) {
         // ------------------------------------------------ the MMAs
         const uint32_t id_pp = idesc_bf16(128, 128, 0, 0);           // A and B K-major
         const uint32_t id_o = idesc_bf16(128, 64 * m.zb, 0, 1);      // B with rows of z along K
-        const uint32_t id_u = idesc_bf16(128, 64 * m.zb, 1, 1);      // A turned: rows of y along K
+        const uint32_t id_u = id_o;                                  // A in TMEM as for O
         const bool wide = m.xb == 2;
-        for (int cc = 0; cc < chunks; ++cc) {
-            const bool need = cc + 1 < chunks || ends;
-            const int tx = 3 * cc, ty = tx + 1, tz = tx + 2;
-            uint32_t x = desc_k(slot(tx)), y = desc_k(slot(ty)), yt = desc_mn(slot(ty)), z = desc_mn(slot(tz));
-            uint32_t E = desc_mn(base + OFF_E), low = desc_mn(base + OFF_LOW);
-            // (kept from being added up ahead of the loop: registers)
-            asm volatile("" : "+r"(x), "+r"(y), "+r"(yt), "+r"(z), "+r"(E), "+r"(low));
-            if (!wait(B_FULL + tx % kSlots, tx / kSlots) || !wait(B_FULL + ty % kSlots, ty / kSlots)) break;
-            if (cc > 0 && !wait(B_O, cc - 1)) break;  // P's columns have been read
+        const uint32_t E = desc_mn(base + OFF_E);
+        auto scores = [&](int cc) -> bool {  // P of chunk cc
+            const int sx = slot(cc, 0), sy = slot(cc, 1);
+            if (!wait(B_FULL + sx, phase(cc)) || !wait(B_FULL + sy, phase(cc))) return false;
+            if (cc > 0 && !wait(B_A, cc - 1)) return false;  // P's columns have been used
             tc_fence_after();
+            const uint32_t x = desc_k(base + sx * TILE), y = desc_k(base + sy * TILE);
 #pragma unroll
             for (int kk = 0; kk < 8; ++kk) {
                 const uint32_t at = (kk >> 2) * BLOCK + (kk & 3) * 32;
                 if (kk < 4 || wide) mma_ss(tmem + TM_P, x, at, y, at, id_pp, kk > 0);
             }
             mma_commit(bar(B_P));
-            if (!wait(B_EREADY, cc) || (cc > 0 && !wait(B_OFREE, cc - 1))) break;
+            return true;
+        };
+        bool ok = chunks == 0 || scores(0);
+        for (int cc = 0; ok && cc < chunks; ++cc) {
+            const bool need = cc + 1 < chunks || ends;
+            const int sx = slot(cc, 0), sz = slot(cc, 2);
+            const uint32_t x = desc_k(base + sx * TILE), z = desc_mn(base + sz * TILE);
+            ok = wait(B_FULL + sz, phase(cc)) && wait(B_PREADY, cc) && (cc == 0 || wait(B_OFREE, cc - 1));
+            if (!ok) break;
             tc_fence_after();
 #pragma unroll
             for (int kk = 0; kk < 8; ++kk)
-                if (kk < 4 || wide)
-                    mma_ss(tmem + TM_OI, x, (kk >> 2) * BLOCK + (kk & 3) * 32, E, kk * 2048, id_o, kk > 0);
-            mma_commit(bar(B_EMPTY + tx % kSlots));
-            if (!wait(B_FULL + tz % kSlots, tz / kSlots) || !wait(B_Y0, cc)) break;
-            tc_fence_after();
-            if (need) issue_update(tmem + TM_U, yt, low, z, 0, id_u);
-            if (!wait(B_PREADY, cc)) break;
+                mma_ts(tmem + TM_O, tmem + TM_P + 32 * (kk >> 1) + 8 * (kk & 1), z, kk * 2048, id_o, kk > 0);
+            mma_commit(bar(B_A));
+            if (!(ok = wait(B_EREADY, cc))) break;
             tc_fence_after();
 #pragma unroll
             for (int kk = 0; kk < 8; ++kk)
-                mma_ts(tmem + TM_OA, tmem + TM_P + 32 * (kk >> 1) + 8 * (kk & 1), z, kk * 2048, id_o, kk > 0);
+                if (kk < 4 || wide) mma_ss(tmem + TM_O, x, (kk >> 2) * BLOCK + (kk & 3) * 32, E, kk * 2048, id_o, true);
             mma_commit(bar(B_O));
+            if (cc + 1 < chunks && !(ok = scores(cc + 1))) break;
             if (need) {
-                if (!wait(B_Y1, cc)) break;
+                if (!(ok = wait(B_YREADY, cc))) break;
                 tc_fence_after();
-                issue_update(tmem + TM_U, yt, low, z, 1, id_u);
+                issue_update(tmem + TM_U, tmem + TM_Y, z, id_u);
                 mma_commit(bar(B_U));
             }
-            mma_commit(bar(B_EMPTY + ty % kSlots));
-            mma_commit(bar(B_EMPTY + tz % kSlots));
+            mma_commit(bar(B_EMPTY + sz));
         }
         mma_commit(bar(B_DRAIN));
         mbar_wait_for(bar(B_DRAIN), 0, A.wait_cycles);
@@ -617,25 +727,23 @@ __global__ void __launch_bounds__(kThreads, 1) mix_tc_kernel(const __grid_consta
 
 // ---------------------------------------------------------------- the segments' own sums
 
-constexpr int kSumWeighWarps = 8, kSumStateWarps = 8, kSumThreads = 32 * (kSumWeighWarps + kSumStateWarps + 2);
-constexpr int kSumLoadWarp = kSumWeighWarps + kSumStateWarps;
-constexpr uint32_t OFF_STAGE = kSlots * TILE, kSumSmem = OFF_STAGE + 2 * TILE + 1024;
-constexpr uint32_t kSumCols = 256;
+constexpr int kSumThreads = kWorkThreads + 64;
+constexpr uint32_t kSumSmem = kSlots * TILE;
+constexpr uint32_t TM_SUM_Y = 256;  // two buffers of U, then of Yw
 enum { S_FULL = 0, S_EMPTY = kSlots, S_READY = 2 * kSlots, S_U = S_READY + 2,
        S_UFREE = S_U + 2, S_DRAIN = S_UFREE + 2, S_COUNT };
 
 // R_f of every segment but the last from the side that the state comes from: U chunk by
-// chunk as in the mix, with two accumulators and two tiles for Yw's lower part, so that weighing, products and sums of neighbouring chunks run at once. Bound by
-// reading Y and Z.
+// chunk as in the mix, with two buffers each of U and Yw, so that a chunk is weighed while
+// the products of the one before it run. Bound by reading Y and Z.
 __global__ void __launch_bounds__(kSumThreads, 1) sum_tc_kernel(const __grid_constant__ TcArgs A) {
-    extern __shared__ __align__(1024) unsigned char smem_raw[];
-    unsigned char *sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    extern __shared__ __align__(1024) unsigned char sm[];
     const uint32_t base = smem_u32(sm);
     __shared__ Segment found;
     __shared__ __align__(8) uint64_t bars[S_COUNT];
     __shared__ uint32_t tmem_slot;
     __shared__ int gave_up;
-    __shared__ uint32_t row_w[C];
+    __shared__ uint2 weights[kWorkers][16];
     auto bar = [&](int i) { return smem_u32(&bars[i]); };
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     Work w;
@@ -658,18 +766,22 @@ __global__ void __launch_bounds__(kSumThreads, 1) sum_tc_kernel(const __grid_con
         return (int)(r < C ? r : C);
     };
     if (tid == 0) {
-        for (int i = 0; i < 2 * kSlots; ++i) mbar_init(bar(i), 1);
+        // (Y in the even slots: freed by the threads that weigh it)
+        for (int i = 0; i < kSlots; ++i) {
+            mbar_init(bar(S_FULL + i), 1);
+            mbar_init(bar(S_EMPTY + i), i % 2 == 0 ? kWorkers : 1);
+        }
         for (int i = 0; i < 2; ++i) {
-            mbar_init(bar(S_READY + i), kStateThreads);
+            mbar_init(bar(S_READY + i), kWorkers);
             mbar_init(bar(S_U + i), 1);
-            mbar_init(bar(S_UFREE + i), kStateThreads);
+            mbar_init(bar(S_UFREE + i), kWorkers);
         }
         mbar_init(bar(S_DRAIN), 1);
         fence_mbar_init();
         gave_up = 0;
     }
     if (tid < 32) {
-        tmem_alloc(smem_u32(&tmem_slot), kSumCols);
+        tmem_alloc(smem_u32(&tmem_slot), TM_COLS);
         tmem_relinquish();
     }
     tc_fence_before();
@@ -692,42 +804,53 @@ __global__ void __launch_bounds__(kSumThreads, 1) sum_tc_kernel(const __grid_con
     };
     auto warp_wait = [&](int b, int phase) -> bool { return __all_sync(0xffffffffu, wait(b, phase)); };
     auto slot = [&](int t) { return (uint32_t)(t % kSlots) * TILE; };
-    auto stage = [&](int i) { return OFF_STAGE + (uint32_t)(i & 1) * TILE; };
 
-    if (warp < kSumWeighWarps) {
-        int weighed = 0;
-        for (int cc = 0; cc < chunks; ++cc) {
-            const int n = tokens_of(chunk_of(cc)), ty = 2 * cc, tz = ty + 1;
-            bool ok = warp_wait(S_FULL + ty % kSlots, ty / kSlots);
-            if (ok && n < C) {
-                ok = warp_wait(S_FULL + tz % kSlots, tz / kSlots);
-                if (ok) clear_behind(sm + slot(tz), m.zb, n, tid);
-            }
-            if (ok && cc >= 2) ok = warp_wait(S_U + (cc & 1), (cc >> 1) - 1);  // the tile is free
-            if (!ok) break;
-            if (n != weighed) row_weights(row_w, weighed = n, m.backward, l2, m.s_state, tid);
-            weigh_half<0>(sm + slot(ty), sm + stage(cc), m.xb, n, row_w, tid);
-            weigh_half<1>(sm + slot(ty), sm + stage(cc), m.xb, n, row_w, tid);
-            fence_async_smem();
-            mbar_arrive(bar(S_READY + (cc & 1)));
-        }
-    } else if (warp < kSumLoadWarp) {
-        const int id = tid - 32 * kSumWeighWarps;
-        const int a = 32 * (warp & 3) + lane, b0 = 64 * (id / 128);
-        const uint32_t lanes = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
-        float2 E[32];
+    if (warp < kWorkers) {
+        const int quarter = warp & 3, sub = warp >> 2;
+        const int t = 32 * quarter + lane, col = 32 * sub;  // row and columns of the state
+        const bool has_z = col < 64 * m.zb;
+        const uint32_t lanes = tmem + ((uint32_t)(32 * quarter) << 16);
+        auto arrive = [&](int b) {
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(b));
+        };
+        float2 E[16];
 #pragma unroll
-        for (int j = 0; j < 32; ++j) E[j] = make_float2(0.f, 0.f);
-        for (int cc = 0; cc < chunks; ++cc) {
-            if (!warp_wait(S_U + (cc & 1), cc >> 1)) break;
+        for (int j = 0; j < 16; ++j) E[j] = make_float2(0.f, 0.f);
+        int weighed = 0;
+        bool ok = true;
+        for (int cc = 0; ok && cc <= chunks; ++cc) {
+            if (cc < chunks) {
+                const int n = tokens_of(chunk_of(cc)), ty = 2 * cc, tz = ty + 1;
+                if (n != weighed) row_weights(weights[warp], weighed = n, m.backward, l2, m.s_state, sub, lane);
+                    if (!(ok = warp_wait(S_FULL + ty % kSlots, ty / kSlots))) break;
+                if (n < C) {
+                    if (!(ok = warp_wait(S_FULL + tz % kSlots, tz / kSlots))) break;
+                    clear_behind(sm + slot(tz), m.zb, n, tid);
+                    fence_async_smem();
+                }
+                // (the buffer is free: U of chunk cc - 2 has been read below)
+                if (quarter < 2 * m.xb)
+                    weigh(base + slot(ty), tmem + TM_SUM_Y + 128 * (cc & 1), quarter, sub, n, weights[warp], lane);
+                tmem_store_wait();
+                tc_fence_before();
+                arrive(S_EMPTY + ty % kSlots);
+                if (lane == 0) mbar_arrive(bar(S_READY + (cc & 1)));
+            }
+            if (cc == 0) continue;
+            const int b = cc - 1;  // the chunk before: its U
+            if (!(ok = warp_wait(S_U + (b & 1), b >> 1))) break;
             tc_fence_after();
-            if (b0 < 64 * m.zb) add_update(E, decay_pow(l2, (float)tokens_of(chunk_of(cc))), lanes + 128 * (cc & 1) + b0);
+            if (has_z) add_update(E, decay_pow(l2, (float)tokens_of(chunk_of(b))), lanes + 128 * (b & 1) + col);
             tc_fence_before();
-            mbar_arrive(bar(S_UFREE + (cc & 1)));
+            arrive(S_UFREE + (b & 1));
         }
-        if (a < 64 * m.xb && b0 < 64 * m.zb && !*stop)
-            write_state(E, m.R_out + (w.item * A.p.H + w.h) * A.mat, state_row(A, m, w.slice, a, b0));
-    } else if (warp == kSumLoadWarp) {
+        if (ok && t < 64 * m.xb && has_z)
+            {
+            const StateAt st = state_row(A, m, w.slice, t, col);
+            write_state(E, m.R_out + (w.item * A.p.H + w.h) * A.mat + st.first, st.step);
+        }
+    } else if (warp == kLoadWarp) {
         if (lane == 0) {
             int issued = 0;
             for (int cc = 0; cc < chunks; ++cc) {
@@ -750,19 +873,15 @@ __global__ void __launch_bounds__(kSumThreads, 1) sum_tc_kernel(const __grid_con
                 mbar_wait_for(bar(S_FULL + t % kSlots), (t / kSlots) & 1, A.wait_cycles);
         }
     } else if (lane == 0) {
-        const uint32_t id_u = idesc_bf16(128, 64 * m.zb, 1, 1);
-        bool ok = true;
-        for (int cc = 0; cc < chunks && ok; ++cc) {
-            const int ty = 2 * cc, tz = ty + 1;
-            if (!(ok = wait(S_FULL + tz % kSlots, tz / kSlots))) break;
-            if (cc >= 2 && !(ok = wait(S_UFREE + (cc & 1), (cc >> 1) - 1))) break;
-            if (!(ok = wait(S_READY + (cc & 1), cc >> 1))) break;
+        const uint32_t id_u = idesc_bf16(128, 64 * m.zb, 0, 1);
+        for (int cc = 0; cc < chunks; ++cc) {
+            const int tz = 2 * cc + 1;
+            if (!wait(S_FULL + tz % kSlots, tz / kSlots)) break;
+            if (cc >= 2 && !wait(S_UFREE + (cc & 1), (cc >> 1) - 1)) break;
+            if (!wait(S_READY + (cc & 1), cc >> 1)) break;
             tc_fence_after();
-            for (int half = 0; half < 2; ++half)
-                issue_update(tmem + 128 * (cc & 1), desc_mn(base + slot(ty)), desc_mn(base + stage(cc)),
-                             desc_mn(base + slot(tz)), half, id_u);
+            issue_update(tmem + 128 * (cc & 1), tmem + TM_SUM_Y + 128 * (cc & 1), desc_mn(base + slot(tz)), id_u);
             mma_commit(bar(S_U + (cc & 1)));
-            mma_commit(bar(S_EMPTY + ty % kSlots));
             mma_commit(bar(S_EMPTY + tz % kSlots));
         }
         mma_commit(bar(S_DRAIN));
@@ -771,7 +890,7 @@ __global__ void __launch_bounds__(kSumThreads, 1) sum_tc_kernel(const __grid_con
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (warp == 0) tmem_dealloc(tmem, kSumCols);
+    if (warp == 0) tmem_dealloc(tmem, TM_COLS);
 }
 
 template <typename K> int run(K kernel, const TcArgs &A, int threads, uint32_t smem, cudaStream_t stream) {
@@ -824,6 +943,8 @@ int launch_mix_tc(const Plan &p, const Mix *mixes, int count, int d_v, bool sums
         m.zstep = m.bstep = s.dz > 128 ? 128 : 0;
         m.out = s.out;
         m.out_f32 = s.out_f32;
+        if (!sums && !s.out_f32 && !tc::make_map_rows(&A.outs[i], s.out, s.dz, p.H, (int64_t)p.H * s.dz, p.total_tokens))
+            return GDR_ERR_CUDA;
         // slices of z lie side by side; of x they are sums of their own
         const int parts = s.dx > 128 ? A.slices : 1;
         m.out_s = s.dz > 128 ? 128 : (parts > 1 ? s.dz : 0);
@@ -831,7 +952,10 @@ int launch_mix_tc(const Plan &p, const Mix *mixes, int count, int d_v, bool sums
         m.out_row = (int64_t)p.H * m.out_h;
         m.turned = s.turned;
         m.backward = s.backward;
-        m.s_intra = s.s_intra; m.s_inter = s.s_inter; m.s_state = s.s_state;
+        // from first to last both are the scale, from last to first s_inter is 1
+        m.s_intra = s.backward ? s.s_intra : 1.f;
+        m.s_inter = s.s_inter;
+        m.s_state = s.s_state;
         m.start = s.start; m.end = s.end; m.R = s.R; m.R_out = s.R_out;
     }
     if (sums) return run(sum_tc_kernel, A, kSumThreads, kSumSmem, stream);

@@ -170,6 +170,9 @@ __device__ __forceinline__ void weigh(uint32_t y, uint32_t taddr, int quarter, i
                                       const uint2 *table, int lane) {
     const int mat = lane >> 3;
     const int token = 32 * sub + (mat >> 1) * 8 + (lane & 7);
+    uint2 w[4];  // of two tokens each
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = table[4 * i + (lane & 3)];
 #pragma unroll 1
     for (int mb = 0; mb < 2; ++mb) {
         const int m0 = 32 * quarter + 16 * mb, chunk = ((m0 & 63) >> 3) + (mat & 1);
@@ -192,10 +195,9 @@ __device__ __forceinline__ void weigh(uint32_t y, uint32_t taddr, int quarter, i
             uint32_t hi[4], lo[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                const uint2 w = table[8 * jj + 4 * (e >> 1) + (lane & 3)];  // of two tokens
                 const __nv_bfloat162 v = reinterpret_cast<const __nv_bfloat162 &>(r[jj][e]);
-                const __nv_bfloat162 wh = reinterpret_cast<const __nv_bfloat162 &>(w.x);
-                const __nv_bfloat162 wl = reinterpret_cast<const __nv_bfloat162 &>(w.y);
+                const __nv_bfloat162 wh = reinterpret_cast<const __nv_bfloat162 &>(w[2 * jj + (e >> 1)].x);
+                const __nv_bfloat162 wl = reinterpret_cast<const __nv_bfloat162 &>(w[2 * jj + (e >> 1)].y);
                 const __nv_bfloat162 h = __hmul2_rn(v, wh);
                 const __nv_bfloat162 l = __hfma2(v, wl, __hfma2(v, wh, __hneg2(h)));
                 hi[e] = reinterpret_cast<const uint32_t &>(h);
@@ -333,7 +335,8 @@ __global__ void __launch_bounds__(kThreads, 1) mix_tc_kernel(const __grid_consta
     __shared__ int gave_up;
     __shared__ Work kept;  // (for the end, in no register meanwhile)
     __shared__ uint2 weights[kWorkers][16];
-    __shared__ __align__(16) float pow_of[32];  // lam^(31-j), or lam^j from last to first
+    __shared__ __align__(16) float step_of[32];  // lam^(31-j), or lam^j from last to first
+    __shared__ float pow_of[63];                  // lam^(i-31), 0 for i < 31
     auto bar = [&](int i) { return smem_u32(&bars[i]); };
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
@@ -384,7 +387,9 @@ __global__ void __launch_bounds__(kThreads, 1) mix_tc_kernel(const __grid_consta
         prefetch_tensormap(&A.maps[m.mz]);
     }
     if (tid < 32) {
-        pow_of[tid] = decay_pow(l2_of_head, (float)(back ? tid : 31 - tid));
+        step_of[tid] = decay_pow(l2_of_head, (float)(back ? tid : 31 - tid));
+        pow_of[31 + tid] = decay_pow(l2_of_head, (float)tid);
+        if (tid < 31) pow_of[tid] = 0.f;
         tmem_alloc(smem_u32(&tmem_slot), TM_COLS);
         tmem_relinquish();
     }
@@ -502,42 +507,49 @@ __global__ void __launch_bounds__(kThreads, 1) mix_tc_kernel(const __grid_consta
             } else {
                 uint32_t ahead[16];
                 tmem_fetch16(lanes + TM_P + col, ahead);
-                // off the diagonal: the way to the block's near column, times the way on to column j
-                const float far = m.s_intra * ex2(l2 * (float)(back ? col - t : t - col - 31) - f);
+                // off the diagonal: the way to the block's near column, times the way on to column
+                // j; on it each distance by itself, 0 beyond it
+                const float far = m.s_intra * ex2(diagonal ? -f : fmaf(l2, (float)(back ? col - t : t - col - 31), -f));
                 const float2 far2 = make_float2(far, far);
-                const float l2s = back ? -l2 : l2;
+                const float *g = pow_of + (back ? 31 - lane : 31 + lane);
                 const int lo = back && diagonal ? lane : 0, hi = back ? n - 1 - col : (diagonal ? lane : 31);
 #pragma unroll
                 for (int half = 0; half < 2; ++half) {
                     tmem_arrived(ahead);
-                    float v[16];
+                    float2 v[8];
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) v[j] = __uint_as_float(ahead[j]);
+                    for (int j = 0; j < 8; ++j) v[j] = make_float2(__uint_as_float(ahead[2 * j]), __uint_as_float(ahead[2 * j + 1]));
                     if (half == 0) tmem_fetch16(lanes + TM_P + col + 16, ahead);
-                    if (diagonal) {  // each distance by itself
-                        // (the distance itself: 0 has to meet -inf's stand-in as 0)
-                        const float from = (float)(lane - 16 * half);
+                    if (diagonal) {
+                        const float *gh = back ? g + 16 * half : g - 16 * half;
+                        if (back) {
 #pragma unroll
-                        for (int j = 0; j < 16; ++j) v[j] *= m.s_intra * ex2(fmaf(l2s, from - (float)j, -f));
+                            for (int j = 0; j < 8; ++j) v[j] = mul2(v[j], make_float2(gh[2 * j], gh[2 * j + 1]));
+                        } else {
+#pragma unroll
+                            for (int j = 0; j < 8; ++j) v[j] = mul2(v[j], make_float2(gh[-2 * j], gh[-2 * j - 1]));
+                        }
                     } else {
 #pragma unroll
-                        for (int j = 0; j < 16; j += 4) {
-                            const float4 g = *reinterpret_cast<const float4 *>(&pow_of[16 * half + j]);
-                            const float2 x = mul2(make_float2(v[j], v[j + 1]), mul2(far2, make_float2(g.x, g.y)));
-                            const float2 z = mul2(make_float2(v[j + 2], v[j + 3]), mul2(far2, make_float2(g.z, g.w)));
-                            v[j] = x.x;
-                            v[j + 1] = x.y;
-                            v[j + 2] = z.x;
-                            v[j + 3] = z.y;
+                        for (int j = 0; j < 8; j += 2) {
+                            const float4 w4 = *reinterpret_cast<const float4 *>(&step_of[16 * half + 2 * j]);
+                            v[j] = mul2(v[j], make_float2(w4.x, w4.y));
+                            v[j + 1] = mul2(v[j + 1], make_float2(w4.z, w4.w));
                         }
                     }
-                    if (diagonal || hi < 31) {  // beyond the diagonal, or behind the last token
 #pragma unroll
-                        for (int j = 0; j < 16; ++j) v[j] = 16 * half + j >= lo && 16 * half + j <= hi ? v[j] : 0.f;
+                    for (int j = 0; j < 8; ++j) v[j] = mul2(v[j], far2);
+                    if (n < C) {  // what lies behind the last token may be anything
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) {
+                            const int i = 16 * half + 2 * j;
+                            v[j].x = i >= lo && i <= hi ? v[j].x : 0.f;
+                            v[j].y = i + 1 >= lo && i + 1 <= hi ? v[j].y : 0.f;
+                        }
                     }
                     uint32_t out[8];
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) out[j] = pack_bf16x2(v[2 * j], v[2 * j + 1]);
+                    for (int j = 0; j < 8; ++j) out[j] = pack_bf16x2(v[j].x, v[j].y);
                     // the bf16 copy goes to the first half of the block's own columns: those of
                     // the second half's copy have been read by now
                     tmem_store8_nowait(lanes + TM_P + col + 8 * half, out);
@@ -612,7 +624,7 @@ __global__ void __launch_bounds__(kThreads, 1) mix_tc_kernel(const __grid_consta
             if (cc >= 0 && need(cc)) {
                 if (!(ok = warp_wait(B_U, cc))) break;
                 tc_fence_after();
-                if (has_z) add_update(E, decay_pow(l2, (float)tokens_of(chunk_of(cc))), lanes + TM_U + col);
+                if (has_z) add_update(E, ex2(l2 * (float)tokens_of(chunk_of(cc))), lanes + TM_U + col);
                 tc_fence_before();
             }
             if (!more) break;

@@ -13,7 +13,7 @@ import torch
 
 from . import ops
 from .linattn import _addr, _dense, _given
-from .ops import _DTYPES, _check, _need, _stream_handle
+from .ops import _DTYPES, _launch, _need
 
 # the gate's function (gdr_block_norm_shape.gate_act)
 ACTS = {"identity": 0, "silu": 1, "sigmoid": 2}
@@ -28,13 +28,14 @@ class BlockNormShape(ctypes.Structure):
 
 
 @functools.lru_cache(maxsize=256)
-def _shape(*fields):
-    return BlockNormShape(*fields)
+def _shape(fields):
+    """A reference to the struct of these fields."""
+    return ctypes.byref(BlockNormShape(*fields))
 
 
 @functools.lru_cache(maxsize=256)
-def _workspace_bytes(*fields):
-    return int(ops._load().gdr_block_norm_bwd_workspace_size(ctypes.byref(_shape(*fields))))
+def _workspace_bytes(fields):
+    return int(ops._load().gdr_block_norm_bwd_workspace_size(_shape(fields)))
 
 
 def _fields(x, y, gate, act, w_post, w_pre, post_norm, pre_norm, res_scale, eps, dtype):
@@ -88,17 +89,14 @@ def block_norm_fwd(x, y=None, gate=None, act="silu", w_post=None, w_pre=None, po
         h = _dense(h, "h", x.shape, dt, dev)
     elif h is not None:
         raise ValueError("h needs pre_norm")
-    with torch.cuda.device(dev):
-        st = lib.gdr_block_norm_fwd(ctypes.byref(_shape(*fields)), x.data_ptr(), _addr(y), _addr(gate),
-                                    _addr(w_post), _addr(w_pre), _addr(x_out), _addr(h),
-                                    _stream_handle(stream, dev))
-    _check(st, "gdr_block_norm_fwd")
+    _launch(lib.gdr_block_norm_fwd, "gdr_block_norm_fwd", dev, stream, _shape(fields), x.data_ptr(), _addr(y),
+            _addr(gate), _addr(w_post), _addr(w_pre), _addr(x_out), _addr(h))
     return (x if y is None else x_out), h
 
 
 def block_norm_bwd_workspace_size(rows, D, dtype=torch.bfloat16, x_dtype=None):
     """Workspace bytes of block_norm_bwd (0 if the sizes are unsupported)."""
-    return _workspace_bytes(int(rows), int(D), _DTYPES[dtype], _DTYPES[x_dtype or dtype], 1, 1, 0, 0, 1.0, 0.0)
+    return _workspace_bytes((int(rows), int(D), _DTYPES[dtype], _DTYPES[x_dtype or dtype], 1, 1, 0, 0, 1.0, 0.0))
 
 
 def block_norm_bwd(dx_out, dh, x_out, y=None, gate=None, act="silu", w_post=None, w_pre=None,
@@ -137,14 +135,9 @@ def block_norm_bwd(dx_out, dh, x_out, y=None, gate=None, act="silu", w_post=None
         if given is not None and has is None:
             raise ValueError(f"{name} has no input")
     if workspace is None:
-        workspace = torch.empty(_workspace_bytes(*fields), dtype=torch.uint8, device=dev)
+        workspace = torch.empty(_workspace_bytes(fields), dtype=torch.uint8, device=dev)
     _need(workspace, "workspace", device=dev)
-    with torch.cuda.device(dev):
-        st = lib.gdr_block_norm_bwd(ctypes.byref(_shape(*fields)), _addr(dx_out), _addr(dh),
-                                    x_out.data_ptr(), _addr(y), _addr(gate), _addr(w_post),
-                                    _addr(w_pre), dx.data_ptr(), _addr(dy), _addr(dgate),
-                                    _addr(dw_post), _addr(dw_pre), workspace.data_ptr(),
-                                    workspace.numel() * workspace.element_size(),
-                                    _stream_handle(stream, dev))
-    _check(st, "gdr_block_norm_bwd")
+    _launch(lib.gdr_block_norm_bwd, "gdr_block_norm_bwd", dev, stream, _shape(fields), _addr(dx_out), _addr(dh),
+            x_out.data_ptr(), _addr(y), _addr(gate), _addr(w_post), _addr(w_pre), dx.data_ptr(), _addr(dy),
+            _addr(dgate), _addr(dw_post), _addr(dw_pre), workspace.data_ptr(), workspace.nbytes)
     return dx, dy, dgate, dw_post, dw_pre

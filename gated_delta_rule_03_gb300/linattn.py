@@ -12,7 +12,7 @@ import functools
 import torch
 
 from . import ops
-from .ops import _DTYPES, _check, _need, _stream_handle
+from .ops import _DTYPES, _launch, _need
 
 
 class LinattnShape(ctypes.Structure):
@@ -26,18 +26,19 @@ class LinattnShape(ctypes.Structure):
 
 
 @functools.lru_cache(maxsize=256)
-def _shape(*fields):
-    return LinattnShape(*fields)
+def _shape(fields):
+    """A reference to the struct of these fields."""
+    return ctypes.byref(LinattnShape(*fields))
 
 
 @functools.lru_cache(maxsize=256)
-def _workspace_bytes(backward, *fields):
+def _workspace_bytes(backward, fields):
     lib = ops._load()
     f = lib.gdr_linattn_bwd_workspace_size if backward else lib.gdr_linattn_fwd_workspace_size
-    return int(f(ctypes.byref(_shape(*fields))))
+    return int(f(_shape(fields)))
 
 
-def _rows(t, name, dtype, device, tokens=None):
+def _rows(t, name, dtype, device, tokens):
     """Checks a [tokens, heads, d] tensor whose heads are contiguous; its token stride."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
@@ -50,31 +51,35 @@ def _rows(t, name, dtype, device, tokens=None):
     if t.dim() != 3:
         raise ValueError(f"{name} must have shape [tokens, heads, d]")
     n, heads, d = t.shape
-    if tokens is not None and n != tokens:
+    if n != tokens:
         raise ValueError(f"{name} has {n} tokens, expected {tokens}")
     s0, s1, s2 = t.stride()
     if (d > 1 and s2 != 1) or (heads > 1 and s1 != d):
         raise ValueError(f"{name}: the heads of a token must be contiguous")
-    if n > 1 and s0 < heads * d:
+    if n <= 1:
+        return heads * d
+    if s0 < heads * d:
         raise ValueError(f"{name}: the token stride must be at least heads * d")
-    return s0 if n > 1 else heads * d
+    return s0
 
 
 def _fields(q, k, v, log_decay, n, scale):
-    _rows_of = functools.partial(_rows, device=q.device)
     if not isinstance(q, torch.Tensor) or q.dtype not in _DTYPES:
-        raise TypeError(f"unsupported dtype {q.dtype}")
-    qs = _rows_of(q, "q", q.dtype)
-    T = q.shape[0]
-    ks = _rows_of(k, "k", q.dtype, tokens=T)
-    vs = _rows_of(v, "v", q.dtype, tokens=T)
-    if k.shape[2] != q.shape[2]:
-        raise ValueError(f"k has heads of {k.shape[2]}, q of {q.shape[2]}")
-    _need(log_decay, "log_decay", torch.float32, q.device)
+        raise TypeError(f"unsupported q: {getattr(q, 'dtype', type(q))}")
+    dtype, device = q.dtype, q.device
+    T = len(q) if q.dim() else 0
+    qs = _rows(q, "q", dtype, device, T)
+    ks = _rows(k, "k", dtype, device, T)
+    vs = _rows(v, "v", dtype, device, T)
+    _, q_heads, d_k = q.shape
+    _, k_heads, d = k.shape
+    _, v_heads, d_v = v.shape
+    if d != d_k:
+        raise ValueError(f"k has heads of {d}, q of {d_k}")
+    _need(log_decay, "log_decay", torch.float32, device)
     if log_decay.dim() != 1:
         raise ValueError("log_decay must have shape [H]")
-    return (n, T, log_decay.numel(), q.shape[1], k.shape[1], v.shape[1], q.shape[2], v.shape[2],
-            _DTYPES[q.dtype], float(scale), qs, ks, vs)
+    return (n, T, log_decay.numel(), q_heads, k_heads, v_heads, d_k, d_v, _DTYPES[dtype], float(scale), qs, ks, vs)
 
 
 def _seqs(cu_seqlens, num_seqs, device):
@@ -92,7 +97,7 @@ def _dense(t, name, shape, dtype, device):
     if t is None:
         return torch.empty(shape, dtype=dtype, device=device)
     _need(t, name, dtype, device)
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     return t
 
@@ -109,20 +114,20 @@ def _addr(t):
 def linattn_fwd_workspace_size(num_seqs, total_tokens, H, dk, dv, dtype=torch.bfloat16,
                                q_heads=None, k_heads=None, v_heads=None):
     """Workspace bytes of linattn_fwd (0 if the sizes are unsupported)."""
-    return _workspace_bytes(False, int(num_seqs), int(total_tokens), H, q_heads or H, k_heads or H,
-                            v_heads or H, dk, dv, _DTYPES[dtype], 1.0, 0, 0, 0)
+    return _workspace_bytes(False, (int(num_seqs), int(total_tokens), H, q_heads or H, k_heads or H,
+                            v_heads or H, dk, dv, _DTYPES[dtype], 1.0, 0, 0, 0))
 
 
 def linattn_bwd_workspace_size(num_seqs, total_tokens, H, dk, dv, dtype=torch.bfloat16,
                                q_heads=None, k_heads=None, v_heads=None):
     """Workspace bytes of linattn_bwd (0 if the sizes are unsupported)."""
-    return _workspace_bytes(True, int(num_seqs), int(total_tokens), H, q_heads or H, k_heads or H,
-                            v_heads or H, dk, dv, _DTYPES[dtype], 1.0, 0, 0, 0)
+    return _workspace_bytes(True, (int(num_seqs), int(total_tokens), H, q_heads or H, k_heads or H,
+                            v_heads or H, dk, dv, _DTYPES[dtype], 1.0, 0, 0, 0))
 
 
 def _workspace(workspace, backward, fields, device):
     if workspace is None:
-        return torch.empty(max(_workspace_bytes(backward, *fields), 256), dtype=torch.uint8, device=device)
+        return torch.empty(max(_workspace_bytes(backward, fields), 256), dtype=torch.uint8, device=device)
     _need(workspace, "workspace", device=device)
     return workspace
 
@@ -143,12 +148,9 @@ def linattn_fwd(q, k, v, log_decay, S0=None, cu_seqlens=None, num_seqs=None, sca
     if final_state or S_final is not None:
         S_final = _dense(S_final, "S_final", (n, H, dk, dv), torch.float32, dev)
     ws = _workspace(workspace, False, fields, dev)
-    with torch.cuda.device(dev):
-        st = lib.gdr_linattn_fwd(ctypes.byref(_shape(*fields)), q.data_ptr(), k.data_ptr(),
-                                 v.data_ptr(), log_decay.data_ptr(), _addr(S0), _addr(cu_seqlens),
-                                 o.data_ptr(), _addr(S_final), ws.data_ptr(),
-                                 ws.numel() * ws.element_size(), _stream_handle(stream, dev))
-    _check(st, "gdr_linattn_fwd")
+    _launch(lib.gdr_linattn_fwd, "gdr_linattn_fwd", dev, stream, _shape(fields), q.data_ptr(), k.data_ptr(),
+            v.data_ptr(), log_decay.data_ptr(), _addr(S0), _addr(cu_seqlens), o.data_ptr(), _addr(S_final),
+            ws.data_ptr(), ws.nbytes)
     return o, S_final
 
 
@@ -173,13 +175,9 @@ def linattn_bwd(do, q, k, v, log_decay, S0=None, dS_final=None, cu_seqlens=None,
     if S0 is not None or dS0 is not None:
         dS0 = _dense(dS0, "dS0", state, torch.float32, dev)
     ws = _workspace(workspace, True, fields, dev)
-    with torch.cuda.device(dev):
-        st = lib.gdr_linattn_bwd(ctypes.byref(_shape(*fields)), do.data_ptr(), q.data_ptr(),
-                                 k.data_ptr(), v.data_ptr(), log_decay.data_ptr(), _addr(S0),
-                                 _addr(dS_final), _addr(cu_seqlens), dq.data_ptr(), dk.data_ptr(),
-                                 dv.data_ptr(), _addr(dS0), ws.data_ptr(),
-                                 ws.numel() * ws.element_size(), _stream_handle(stream, dev))
-    _check(st, "gdr_linattn_bwd")
+    _launch(lib.gdr_linattn_bwd, "gdr_linattn_bwd", dev, stream, _shape(fields), do.data_ptr(), q.data_ptr(),
+            k.data_ptr(), v.data_ptr(), log_decay.data_ptr(), _addr(S0), _addr(dS_final), _addr(cu_seqlens),
+            dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), _addr(dS0), ws.data_ptr(), ws.nbytes)
     return dq, dk, dv, dS0
 
 
@@ -187,15 +185,12 @@ def linattn_step(q, k, v, log_decay, S, scale=1.0, o=None, stream=None):
     """The next token of N sequences (gdr_linattn_step): q [N, q_heads, dk], k [N, k_heads,
     dk], v [N, v_heads, dv]; S [N, H, dk, dv] fp32 updated in place. Returns o [N, H, dv]."""
     lib = ops._load()
-    fields = _fields(q, k, v, log_decay, q.shape[0], scale)
+    fields = _fields(q, k, v, log_decay, len(q), scale)
     dev, (N, H, dk, dv) = q.device, (fields[1], fields[2], fields[6], fields[7])
     if S is None:
         raise TypeError("S must be a torch.Tensor")
     _given(S, "S", (N, H, dk, dv), torch.float32, dev)
     o = _dense(o, "o", (N, H, dv), q.dtype, dev)
-    with torch.cuda.device(dev):
-        st = lib.gdr_linattn_step(ctypes.byref(_shape(*fields)), q.data_ptr(), k.data_ptr(),
-                                  v.data_ptr(), log_decay.data_ptr(), S.data_ptr(), o.data_ptr(),
-                                  _stream_handle(stream, dev))
-    _check(st, "gdr_linattn_step")
+    _launch(lib.gdr_linattn_step, "gdr_linattn_step", dev, stream, _shape(fields), q.data_ptr(), k.data_ptr(),
+            v.data_ptr(), log_decay.data_ptr(), S.data_ptr(), o.data_ptr())
     return o

@@ -169,6 +169,27 @@ def _stream_handle(stream, device):
     return ctypes.c_void_p(s.cuda_stream)
 
 
+# the current stream's handle without a Stream object around it (2 us of a small call)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _launch(f, what, device, stream, *args):
+    """Calls f(*args, stream) with `device` current; raises GdrError for its status."""
+    if stream is not None:
+        handle = stream.cuda_stream
+    elif _raw_stream is not None:
+        handle = _raw_stream(device.index)
+    else:
+        handle = torch.cuda.current_stream(device).cuda_stream
+    if torch.cuda.current_device() == device.index:
+        status = f(*args, handle)
+    else:
+        with torch.cuda.device(device):
+            status = f(*args, handle)
+    if status != 0:
+        raise GdrError(status, what)
+
+
 def _need(t, name, dtype=None, device=None):
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")

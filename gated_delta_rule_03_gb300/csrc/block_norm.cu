@@ -20,224 +20,412 @@ namespace {
 
 constexpr int kSms = 152;
 
-// VEC consecutive entries (VEC divides D), read 16 bytes at a time where they are that many.
+// VEC consecutive entries (VEC divides D) in 32-bit words, read 16 bytes at a time where they
+// are that many; a bf16 unpacks by a shift or a mask, a pair packs in one conversion.
 template <typename T, int VEC> struct alignas(sizeof(T) * VEC < 16 ? sizeof(T) * VEC : 16) Pack {
-    T v[VEC];
+    uint32_t w[sizeof(T) * VEC / 4];
+    __device__ __forceinline__ void zero() {
+#pragma unroll
+        for (uint32_t &x : w) x = 0;
+    }
+    __device__ __forceinline__ float get(int i) const {
+        if constexpr (sizeof(T) == 4) return __uint_as_float(w[i]);
+        else return __uint_as_float(i & 1 ? w[i / 2] & 0xffff0000u : w[i / 2] << 16);
+    }
+    __device__ __forceinline__ void set(int i, float a, float b) {  // entries i, i + 1 (i even)
+        if constexpr (sizeof(T) == 4) {
+            w[i] = __float_as_uint(a);
+            if (VEC > 1) w[i + 1 < VEC ? i + 1 : i] = __float_as_uint(VEC > 1 ? b : a);
+        } else {
+            const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+            w[i / 2] = reinterpret_cast<const uint32_t &>(v);
+        }
+    }
+};
+template <> struct Pack<__nv_bfloat16, 1> {  // (odd widths)
+    __nv_bfloat16 v;
+    __device__ __forceinline__ void zero() { v = __float2bfloat16_rn(0.f); }
+    __device__ __forceinline__ float get(int) const { return __bfloat162float(v); }
+    __device__ __forceinline__ void set(int, float a, float) { v = __float2bfloat16_rn(a); }
+};
+template <typename T, int VEC> __device__ __forceinline__ void pack_all(Pack<T, VEC> &p, const float *x) {
+#pragma unroll
+    for (int i = 0; i < VEC; i += 2) p.set(i, x[i], x[VEC > 1 ? i + 1 : i]);
+}
+
+// A thread's PER entries of a row as they are in memory: VEC at a time, blockDim.x VEC apart.
+// Entries behind the row's end (and whole rows behind the last, D = 0) are zero.
+template <typename T, int VEC, int PER> struct Raw {
+    Pack<T, VEC> p[PER / VEC];
+    __device__ __forceinline__ void load(const T *row, int D) {
+#pragma unroll
+        for (int j = 0; j < PER / VEC; ++j) {
+            const int e = (threadIdx.x + blockDim.x * j) * VEC;
+            if (e < D) p[j] = *reinterpret_cast<const Pack<T, VEC> *>(row + e);
+            else p[j].zero();
+        }
+    }
+    __device__ __forceinline__ float operator[](int i) const { return p[i / VEC].get(i % VEC); }
 };
 
 template <typename T, int VEC, int PER>
-__device__ __forceinline__ void load_row(const T *p, int D, float (&x)[PER]) {
+__device__ __forceinline__ void store_row(T *row, int D, const float (&x)[PER]) {
 #pragma unroll
     for (int j = 0; j < PER / VEC; ++j) {
         const int e = (threadIdx.x + blockDim.x * j) * VEC;
-        if (e < D) {
-            const Pack<T, VEC> a = *reinterpret_cast<const Pack<T, VEC> *>(p + e);
-#pragma unroll
-            for (int i = 0; i < VEC; ++i) x[j * VEC + i] = to_f32(a.v[i]);
-        } else {
-#pragma unroll
-            for (int i = 0; i < VEC; ++i) x[j * VEC + i] = 0.f;
-        }
+        Pack<T, VEC> a;
+        pack_all(a, x + j * VEC);
+        if (e < D) *reinterpret_cast<Pack<T, VEC> *>(row + e) = a;
     }
 }
 
-template <typename T, int VEC, int PER>
-__device__ __forceinline__ void store_row(T *p, int D, const float (&x)[PER]) {
+// A weight of a thread's entries, read where it is used (it stays in the first-level cache).
+template <int VEC> struct Weight {
+    float v[VEC];
+};
+template <int VEC> __device__ __forceinline__ Weight<VEC> weight_of(const float *w, int j, int D) {
+    Weight<VEC> a;
+    const int e = (threadIdx.x + blockDim.x * j) * VEC;
+    Pack<float, VEC> p;
 #pragma unroll
-    for (int j = 0; j < PER / VEC; ++j) {
-        const int e = (threadIdx.x + blockDim.x * j) * VEC;
-        if (e < D) {
-            Pack<T, VEC> a;
+    for (int i = 0; i < VEC; ++i) p.w[i] = 0x3f800000u;
+    if (w && e < D) p = *reinterpret_cast<const Pack<float, VEC> *>(w + e);
 #pragma unroll
-            for (int i = 0; i < VEC; ++i) a.v[i] = from_f32<T>(x[j * VEC + i]);
-            *reinterpret_cast<Pack<T, VEC> *>(p + e) = a;
-        }
-    }
+    for (int i = 0; i < VEC; ++i) a.v[i] = p.get(i);
+    return a;
 }
 
-template <int VEC, int PER>
-__device__ __forceinline__ void load_weight(const float *w, int D, float (&x)[PER]) {
-    if (w) {
-        load_row<float, VEC>(w, D, x);
-    } else {
+// Sums of K values over the blockDim.x threads of a row: within the warp, then over the row's
+// warps (at most 16) by every warp for itself. `buf` has 2 x 16 x 3 floats; calls take its
+// halves in turn, so that one barrier per sum is enough.
+template <int K> __device__ __forceinline__ void row_sum(float (&s)[K], float *buf, int turn) {
 #pragma unroll
-        for (int i = 0; i < PER; ++i) x[i] = 1.f;
-    }
-}
-
-// Sums of K values over the blockDim.x threads of a row; `buf` has K floats per warp.
-template <int K> __device__ __forceinline__ void row_sum(float (&s)[K], float *buf) {
+    for (int off = 16; off > 0; off >>= 1)
 #pragma unroll
-    for (int k = 0; k < K; ++k)
-#pragma unroll
-        for (int off = 16; off > 0; off >>= 1) s[k] += __shfl_xor_sync(0xffffffffu, s[k], off);
-    const int warps = blockDim.x >> 5;
+        for (int k = 0; k < K; ++k) s[k] += __shfl_xor_sync(0xffffffffu, s[k], off);
+    const int warps = blockDim.x >> 5, lane = threadIdx.x & 31;
     if (warps == 1) return;
-    const int warp = threadIdx.x >> 5;
-    float *row = buf + threadIdx.y * warps * K;
-    __syncthreads();  // the values of the sum before have been read
-    if ((threadIdx.x & 31) == 0) {
+    float *row = buf + (turn & 1) * 48 + threadIdx.y * warps * K;
+    if (lane == 0) {
 #pragma unroll
-        for (int k = 0; k < K; ++k) row[warp * K + k] = s[k];
+        for (int k = 0; k < K; ++k) row[k * warps + (threadIdx.x >> 5)] = s[k];
     }
     __syncthreads();
 #pragma unroll
-    for (int k = 0; k < K; ++k) {
-        float t = 0.f;
-        for (int w = 0; w < warps; ++w) t += row[w * K + k];
-        s[k] = t;
-    }
+    for (int k = 0; k < K; ++k) s[k] = (lane & 15) < warps ? row[k * warps + (lane & 15)] : 0.f;
+#pragma unroll
+    for (int off = 8; off > 0; off >>= 1)
+#pragma unroll
+        for (int k = 0; k < K; ++k) s[k] += __shfl_xor_sync(0xffffffffu, s[k], off);
 }
 
-__device__ __forceinline__ float sigmoid(float g) { return 1.f / (1.f + __expf(-g)); }
+// sigmoid by the hardware's exponential and reciprocal (a few units in the last place).
+__device__ __forceinline__ float sigmoid(float g) {
+    float e, r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(g * -1.4426950408889634f));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
+    return r;
+}
+// The gate's function of VEC entries, and with kDeriv its derivative; one branch for all.
+template <bool kDeriv, typename T, int VEC>
+__device__ __forceinline__ void gate_of(int act, const Pack<T, VEC> &g, float (&a)[VEC], float (&da)[VEC]) {
+    if (act == GDR_GATE_IDENTITY) {
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+            a[e] = g.get(e);
+            if (kDeriv) da[e] = 1.f;
+        }
+    } else if (act == GDR_GATE_SILU) {
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+            const float x = g.get(e), s = sigmoid(x);
+            a[e] = x * s;
+            if (kDeriv) da[e] = fmaf(a[e], 1.f - s, s);
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+            a[e] = sigmoid(g.get(e));
+            if (kDeriv) da[e] = a[e] * (1.f - a[e]);
+        }
+    }
+}
 
 struct NormParams {
     int64_t rows;
     int D;
     int post, pre, act;
     int64_t gate_stride;  // 0: one row for all
-    float s, eps;
+    float s, eps, inv_D;
     const float *w_post, *w_pre;
 };
 
+// One row per blockDim.x threads, 16 entries each where the row is wide enough: few threads
+// with many loads in flight each, so that the two sums over a row cost little. (16384 x 2048
+// bf16: 8, 16, 32 entries 100, 72, 93 us.)
 template <typename T, typename TX, int VEC, int PER>
 __global__ void __launch_bounds__(512)
 block_norm_fwd_kernel(const NormParams p, const TX *x, const T *y, const T *gate, TX *x_out, T *h) {
-    __shared__ float buf[32];
+    __shared__ float buf[96];
     const int64_t row = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
-    const bool live = row < p.rows;
-    const int D = live ? p.D : 0;  // a row behind the last loads and stores nothing
+    const int D = row < p.rows ? p.D : 0;  // a row behind the last loads and stores nothing
     const int64_t at = row * p.D;
-    float xv[PER], yv[PER], gv[PER];
-    load_row<TX, VEC>(x + at, D, xv);
+    Raw<TX, VEC, PER> xr;
+    float v[PER];
+    xr.load(x + at, D);
     if (y) {
-        load_row<T, VEC>(y + at, D, yv);
-        if (gate) load_row<T, VEC>(gate + row * p.gate_stride, D, gv);
-        float w[PER];
+        Raw<T, VEC, PER> yr, gr;
+        yr.load(y + at, D);
+        if (gate) gr.load(gate + row * p.gate_stride, D);
+        float r = 1.f;
         if (p.post) {
             float ss[1] = {0.f};
 #pragma unroll
-            for (int i = 0; i < PER; ++i) ss[0] = fmaf(yv[i], yv[i], ss[0]);
-            row_sum(ss, buf);
-            const float r = rsqrtf(ss[0] / p.D + p.eps);
-            load_weight<VEC>(p.w_post, D, w);
-#pragma unroll
-            for (int i = 0; i < PER; ++i) yv[i] *= r * w[i];
+            for (int i = 0; i < PER; ++i) ss[0] = fmaf(yr[i], yr[i], ss[0]);
+            row_sum(ss, buf, 0);
+            r = rsqrtf(ss[0] * p.inv_D + p.eps);
         }
-        if (gate) {
+        const float *w = p.post ? p.w_post : nullptr;
 #pragma unroll
-            for (int i = 0; i < PER; ++i) {
-                const float a = p.act == GDR_GATE_IDENTITY ? gv[i] : sigmoid(gv[i]) * (p.act == GDR_GATE_SILU ? gv[i] : 1.f);
-                yv[i] *= a;
+        for (int j = 0; j < PER / VEC; ++j) {
+            const Weight<VEC> wj = weight_of<VEC>(w, j, D);
+            float a[VEC], none[VEC];
+            if (gate) {
+                gate_of<false>(p.act, gr.p[j], a, none);
+            } else {
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) a[e] = 1.f;
+            }
+            const float rs = r * p.s;
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) {
+                const int i = j * VEC + e;
+                v[i] = fmaf(yr[i] * a[e], rs * wj.v[e], xr[i]);
             }
         }
+        store_row<TX, VEC>(x_out + at, D, v);
+    } else {
 #pragma unroll
-        for (int i = 0; i < PER; ++i) xv[i] = fmaf(p.s, yv[i], xv[i]);
-        store_row<TX, VEC>(x_out + at, D, xv);
+        for (int i = 0; i < PER; ++i) v[i] = xr[i];
     }
     if (!h) return;
-    float ss[1] = {0.f}, w[PER];
+    float ss[1] = {0.f};
 #pragma unroll
-    for (int i = 0; i < PER; ++i) ss[0] = fmaf(xv[i], xv[i], ss[0]);
-    row_sum(ss, buf);
-    const float r = rsqrtf(ss[0] / p.D + p.eps);
-    load_weight<VEC>(p.w_pre, D, w);
+    for (int i = 0; i < PER; ++i) ss[0] = fmaf(v[i], v[i], ss[0]);
+    row_sum(ss, buf, 1);
+    const float r = rsqrtf(ss[0] * p.inv_D + p.eps);
 #pragma unroll
-    for (int i = 0; i < PER; ++i) xv[i] *= r * w[i];
-    store_row<T, VEC>(h + at, D, xv);
+    for (int j = 0; j < PER / VEC; ++j) {
+        const Weight<VEC> wj = weight_of<VEC>(p.w_pre, j, D);
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) v[j * VEC + e] *= r * wj.v[e];
+    }
+    store_row<T, VEC>(h + at, D, v);
 }
 
-// Sums over this block's rows go to part[which][blockIdx.x * blockDim.y + threadIdx.y][D].
-template <typename T, typename TX, int VEC, int PER>
-__global__ void __launch_bounds__(512)
+__device__ __forceinline__ uint32_t smem_at(const void *p) { return (uint32_t)__cvta_generic_to_shared(p); }
+
+// A thread's 8 entries of a row on their way to shared memory, to slots that it alone uses (no
+// barrier), 16 bytes of every thread side by side; zeros behind the row's end.
+template <typename T> __device__ __forceinline__ void fetch8(uint32_t slot, const T *from, bool live, int threads) {
+#pragma unroll
+    for (int u = 0; u < (int)sizeof(T) / 2; ++u)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(slot + u * 16 * threads),
+                     "l"((const char *)from + 16 * u), "r"(live ? 16 : 0)
+                     : "memory");
+}
+template <typename T> __device__ __forceinline__ void read8(Pack<T, 8> &p, const char *slot, int threads) {
+#pragma unroll
+    for (int u = 0; u < (int)sizeof(T) / 2; ++u) {
+        const uint4 x = *reinterpret_cast<const uint4 *>(slot + u * 16 * threads);
+        p.w[4 * u] = x.x;
+        p.w[4 * u + 1] = x.y;
+        p.w[4 * u + 2] = x.z;
+        p.w[4 * u + 3] = x.w;
+    }
+}
+
+// What a block of the backward kernel keeps of its rows' inputs.
+template <typename T, typename TX, int PER> __host__ __device__ constexpr int row_bytes() {
+    return PER * (2 * (int)sizeof(TX) + 3 * (int)sizeof(T));
+}
+template <typename T, int VEC, int PER> __host__ __device__ constexpr bool fetches_ahead() { return PER == 8 && VEC == 8; }
+
+// Sums over this block's rows go to part[which][blockIdx.x * blockDim.y + threadIdx.y][D]. The
+// next row's inputs are on their way to shared memory while a row is worked on (in registers
+// they would halve the warps, and the instructions per entry, about 45, need the warps).
+// Rows wider than 4096 keep their columns' sums in shared memory instead.
+template <typename T, typename TX, int VEC, int PER, int THREADS>
+__global__ void __launch_bounds__(THREADS, THREADS > 256 ? 1 : (fetches_ahead<T, VEC, PER>() ? 3 : 2))
 block_norm_bwd_kernel(const NormParams p, const TX *dx_out, const T *dh, const TX *x, const T *y,
                       const T *gate, TX *dx, T *dy, T *dgate, float *part_post, float *part_pre,
                       float *part_gate) {
+    constexpr bool kWide = PER > 8, kAhead = fetches_ahead<T, VEC, PER>();
     __shared__ float buf[96];
-    float a_post[PER], a_pre[PER], a_gate[PER];
+    extern __shared__ __align__(16) char dynamic[];
+    float *wide = reinterpret_cast<float *>(dynamic);  // [3][D], each thread its own columns
+    float a_post[kWide ? 1 : PER], a_pre[kWide ? 1 : PER], a_gate[kWide ? 1 : PER];
 #pragma unroll
-    for (int i = 0; i < PER; ++i) a_post[i] = a_pre[i] = a_gate[i] = 0.f;
+    for (int i = 0; i < (kWide ? 1 : PER); ++i) a_post[i] = a_pre[i] = a_gate[i] = 0.f;
+    if (kWide) {
+        for (int e = threadIdx.x; e < 3 * p.D; e += blockDim.x) wide[e] = 0.f;
+        __syncthreads();
+    }
+    auto column = [&](int i) { return (threadIdx.x + blockDim.x * (i / VEC)) * VEC + i % VEC; };
+    auto add = [&](float (&a)[kWide ? 1 : PER], int which, int i, float x) {
+        if (!kWide) a[kWide ? 0 : i] += x;
+        else if (column(i) < p.D) wide[which * p.D + column(i)] += x;
+    };
     const int64_t step = (int64_t)gridDim.x * blockDim.y;
     const int64_t rounds = (p.rows + step - 1) / step;  // the same for every thread: barriers inside
-    for (int64_t round = 0; round < rounds; ++round) {
-        const int64_t row = round * step + (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
+    int64_t row = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
+    const int threads = blockDim.x * blockDim.y, id = threadIdx.y * blockDim.x + threadIdx.x;
+    // a round's inputs, this thread's slots: dx_out, x, then dh, y, gate
+    constexpr int kX = 8 * (int)sizeof(TX), kT = 8 * (int)sizeof(T), kRound = 2 * kX + 3 * kT;
+    char *const mine_at = dynamic + 16 * id;
+    const int e8 = threadIdx.x * 8;
+    auto fetch = [&](int64_t round, int64_t at_row) {
+        if constexpr (kAhead) {
+            const bool live = at_row < p.rows && e8 < p.D;
+            const int64_t at = live ? at_row * p.D + e8 : 0;
+            const uint32_t to = smem_at(mine_at) + (round & 1 ? kRound * threads : 0);
+            if (dx_out) fetch8(to, dx_out + at, live, threads);
+            if (dh) {
+                fetch8(to + kX * threads, x + at, live, threads);
+                fetch8(to + 2 * kX * threads, dh + at, live, threads);
+            }
+            if (y) fetch8(to + (2 * kX + kT) * threads, y + at, live, threads);
+            if (gate)
+                fetch8(to + (2 * kX + 2 * kT) * threads, gate + (p.gate_stride ? at : (live ? e8 : 0)), live, threads);
+            asm volatile("cp.async.commit_group;" ::: "memory");
+        }
+    };
+    fetch(0, row);
+    for (int64_t round = 0; round < rounds; ++round, row += step) {
         const int D = row < p.rows ? p.D : 0;
         const int64_t at = row * p.D;
-        float dv[PER], hv[PER], xv[PER], yv[PER], gv[PER], w[PER];
-        if (dx_out) {
-            load_row<TX, VEC>(dx_out + at, D, dv);
-        } else {
-#pragma unroll
-            for (int i = 0; i < PER; ++i) dv[i] = 0.f;
+        if (kAhead) {
+            if (round + 1 < rounds) {
+                fetch(round + 1, row + step);
+                asm volatile("cp.async.wait_group 1;" ::: "memory");
+            } else {
+                asm volatile("cp.async.wait_group 0;" ::: "memory");
+            }
         }
-        if (dh) {
-            load_row<T, VEC>(dh + at, D, hv);
-            load_row<TX, VEC>(x + at, D, xv);
-        }
-        if (y) load_row<T, VEC>(y + at, D, yv);
-        if (gate) load_row<T, VEC>(gate + row * p.gate_stride, D, gv);
+        const char *const here = mine_at + (round & 1 ? kRound * threads : 0);
+        float dv[PER];
         float sums[3] = {0.f, 0.f, 0.f};
+        Raw<TX, VEC, PER> xr;
+        Raw<T, VEC, PER> hr, yr, gr;
+        Raw<TX, VEC, PER> dr;
+        if constexpr (!kAhead) {  // (from shared memory they are read where they are used)
+            dr.load(dx_out + at, dx_out ? D : 0);
+            gr.load(gate + row * p.gate_stride, gate ? D : 0);
+        }
         if (dh) {
-            load_weight<VEC>(p.w_pre, D, w);
+            if constexpr (kAhead) {
+                read8(xr.p[0], here + kX * threads, threads);
+                read8(hr.p[0], here + 2 * kX * threads, threads);
+            } else {
+                xr.load(x + at, D);
+                hr.load(dh + at, D);
+            }
+        }
+        if (y) {
+            if constexpr (kAhead) read8(yr.p[0], here + (2 * kX + kT) * threads, threads);
+            else yr.load(y + at, D);
+        }
+        if (dh) {
 #pragma unroll
-            for (int i = 0; i < PER; ++i) {
-                sums[0] = fmaf(xv[i], xv[i], sums[0]);
-                sums[1] = fmaf(hv[i] * w[i], xv[i], sums[1]);
+            for (int j = 0; j < PER / VEC; ++j) {
+                const Weight<VEC> w = weight_of<VEC>(p.w_pre, j, D);
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) {
+                    const int i = j * VEC + e;
+                    const float xv = xr[i];
+                    dv[i] = hr[i] * w.v[e];
+                    sums[0] = fmaf(xv, xv, sums[0]);
+                    sums[1] = fmaf(dv[i], xv, sums[1]);
+                }
             }
         }
         if (p.post) {
 #pragma unroll
-            for (int i = 0; i < PER; ++i) sums[2] = fmaf(yv[i], yv[i], sums[2]);
+            for (int i = 0; i < PER; ++i) sums[2] = fmaf(yr[i], yr[i], sums[2]);
         }
-        if (dh || p.post) row_sum(sums, buf);
-        if (dh) {
-            const float r = rsqrtf(sums[0] / p.D + p.eps), m = r * r * (sums[1] / p.D);
+        if (dh || p.post) row_sum(sums, buf, 0);
+        {
+            if constexpr (kAhead)
+                if (dx_out) read8(dr.p[0], here, threads);
+            const float r = rsqrtf(sums[0] * p.inv_D + p.eps), m = r * r * (sums[1] * p.inv_D);
 #pragma unroll
             for (int i = 0; i < PER; ++i) {
-                a_pre[i] = fmaf(hv[i], xv[i] * r, a_pre[i]);
-                dv[i] = fmaf(r, hv[i] * w[i] - xv[i] * m, dv[i]);
+                const float d = dx_out ? dr[i] : 0.f;
+                if (dh) {
+                    const float xv = xr[i];
+                    add(a_pre, 1, i, hr[i] * (xv * r));
+                    dv[i] = fmaf(r, dv[i] - xv * m, d);
+                } else {
+                    dv[i] = d;
+                }
             }
         }
         store_row<TX, VEC>(dx + at, D, dv);
         if (!y) continue;
-        const float r = p.post ? rsqrtf(sums[2] / p.D + p.eps) : 1.f;
-        if (p.post) {
-            load_weight<VEC>(p.w_post, D, w);
-        } else {
-#pragma unroll
-            for (int i = 0; i < PER; ++i) w[i] = 1.f;
-        }
+        const float r = p.post ? rsqrtf(sums[2] * p.inv_D + p.eps) : 1.f;
+        const float *w_post = p.post ? p.w_post : nullptr;
         float dot[1] = {0.f};
+        if constexpr (kAhead)
+            if (gate) read8(gr.p[0], here + (2 * kX + 2 * kT) * threads, threads);
 #pragma unroll
-        for (int i = 0; i < PER; ++i) {
-            float dz = p.s * dv[i];
+        for (int j = 0; j < PER / VEC; ++j) {
+            const Weight<VEC> w = weight_of<VEC>(w_post, j, D);
+            float a[VEC], dg[VEC];
             if (gate) {
-                const float g = gv[i], sg = sigmoid(g);
-                const float a = p.act == GDR_GATE_IDENTITY ? g : (p.act == GDR_GATE_SILU ? g * sg : sg);
-                const float da = p.act == GDR_GATE_IDENTITY ? 1.f
-                                 : (p.act == GDR_GATE_SILU ? sg * (1.f + g * (1.f - sg)) : sg * (1.f - sg));
-                gv[i] = dz * (yv[i] * r * w[i]) * da;
-                a_gate[i] += gv[i];
-                dz *= a;
-            }
-            a_post[i] = fmaf(dz, yv[i] * r, a_post[i]);
-            dz *= w[i];
-            dot[0] = fmaf(dz, yv[i], dot[0]);
-            dv[i] = dz;
-        }
-        if (gate && p.gate_stride && dgate) store_row<T, VEC>(dgate + at, D, gv);
-        if (p.post) {
-            row_sum(dot, buf);
-            const float m = r * r * (dot[0] / p.D);
+                gate_of<true>(p.act, gr.p[j], a, dg);
+            } else {
 #pragma unroll
-            for (int i = 0; i < PER; ++i) dv[i] = r * (dv[i] - yv[i] * m);
+                for (int e = 0; e < VEC; ++e) a[e] = 1.f;
+            }
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) {
+                const int i = j * VEC + e;
+                const float yv = yr[i], yn = yv * r, dz = p.s * dv[i];
+                if (gate) {
+                    dg[e] *= dz * (yn * w.v[e]);
+                    if (part_gate) add(a_gate, 2, i, dg[e]);
+                }
+                const float da = dz * a[e];
+                add(a_post, 0, i, da * yn);
+                dv[i] = da * w.v[e];
+                dot[0] = fmaf(dv[i], yv, dot[0]);
+            }
+            if (gate && p.gate_stride && dgate) {
+                const int e0 = (threadIdx.x + blockDim.x * j) * VEC;
+                Pack<T, VEC> out;
+                pack_all(out, dg);
+                if (e0 < D) *reinterpret_cast<Pack<T, VEC> *>(dgate + at + e0) = out;
+            }
+        }
+        if (p.post) {
+            row_sum(dot, buf, 1);
+            const float m = r * r * (dot[0] * p.inv_D);
+#pragma unroll
+            for (int i = 0; i < PER; ++i) dv[i] = r * (dv[i] - yr[i] * m);
         }
         store_row<T, VEC>(dy + at, D, dv);
     }
     const int64_t mine = ((int64_t)blockIdx.x * blockDim.y + threadIdx.y) * p.D;
-    if (part_post) store_row<float, VEC>(part_post + mine, p.D, a_post);
-    if (part_pre) store_row<float, VEC>(part_pre + mine, p.D, a_pre);
-    if (part_gate) store_row<float, VEC>(part_gate + mine, p.D, a_gate);
+    if constexpr (kWide) {
+        __syncthreads();
+        float *const part[3] = {part_post, part_pre, part_gate};
+        for (int i = 0; i < 3; ++i)
+            for (int e = threadIdx.x; part[i] && e < p.D; e += blockDim.x) part[i][mine + e] = wide[i * p.D + e];
+    } else {
+        if (part_post) store_row<float, VEC>(part_post + mine, p.D, a_post);
+        if (part_pre) store_row<float, VEC>(part_pre + mine, p.D, a_pre);
+        if (part_gate) store_row<float, VEC>(part_gate + mine, p.D, a_gate);
+    }
 }
 
 struct Sum {
@@ -269,24 +457,26 @@ __global__ void __launch_bounds__(256) column_sum_kernel(const Sums s, int parts
     }
 }
 
-// Threads per row, rows per block and (backward) blocks: a row's entries spread over whole
-// warps, PER each; narrow rows share a block of up to 128 threads.
+// Entries per thread, entries per access, threads per row and rows per block: a row's entries
+// spread over whole warps, narrow rows share a block of up to 128 threads. Forward 16 entries
+// per thread; backward 8 (16 beyond D = 4096), as a thread also holds the sums of its columns.
 struct Shape2 {
     int per, vec;
     dim3 block;
 };
-Shape2 shape_of(int D) {
+Shape2 shape_of(int D, bool backward) {
     Shape2 s;
-    s.per = D <= 4096 ? 8 : 16;
+    s.per = backward ? (D <= 4096 ? 8 : 16) : (D <= 1024 ? 8 : 16);
     s.vec = D % 8 == 0 ? 8 : (D % 2 == 0 ? 2 : 1);
     const int tpr = ((D + s.per - 1) / s.per + 31) / 32 * 32;
     s.block = dim3((unsigned)tpr, (unsigned)(tpr >= 128 ? 1 : 128 / tpr));
     return s;
 }
+// Blocks of a backward call: 768 threads on an SM where a block has at most 256, else one block.
 int bwd_blocks(int64_t rows, const Shape2 &s) {
     const int threads = (int)(s.block.x * s.block.y);
     const int64_t need = (rows + s.block.y - 1) / s.block.y;
-    const int64_t most = (int64_t)kSms * (threads <= 512 ? 512 / threads : 1);
+    const int64_t most = (int64_t)kSms * (threads <= 256 ? 768 / threads : 1);
     return (int)(need < most ? need : most);
 }
 
@@ -303,37 +493,45 @@ template <typename T, typename TX> struct Run {
     static int bwd(const NormParams &p, const Shape2 &s, int blocks, const void *dx_out, const void *dh,
                    const void *x, const void *y, const void *gate, void *dx, void *dy, void *dgate,
                    float *pp, float *pn, float *pg, cudaStream_t stream) {
-        block_norm_bwd_kernel<T, TX, VEC, PER><<<(unsigned)blocks, s.block, 0, stream>>>(
+        const int threads = (int)(s.block.x * s.block.y);
+        const size_t bytes = PER > 8 ? 3 * (size_t)p.D * sizeof(float)
+                             : (fetches_ahead<T, VEC, PER>() ? 2 * (size_t)row_bytes<T, TX, PER>() * threads : 0);
+        auto kernel = PER > 8 || threads > 256 ? block_norm_bwd_kernel<T, TX, VEC, PER, 512>
+                                               : block_norm_bwd_kernel<T, TX, VEC, PER, (PER > 8 ? 512 : 256)>;
+        if (bytes > 48 * 1024 &&
+            cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) != cudaSuccess)
+            return GDR_ERR_CUDA;
+        kernel<<<(unsigned)blocks, s.block, bytes, stream>>>(
             p, (const TX *)dx_out, (const T *)dh, (const TX *)x, (const T *)y, (const T *)gate,
             (TX *)dx, (T *)dy, (T *)dgate, pp, pn, pg);
         return cuda_status(cudaGetLastError());
     }
 };
 
-#define GDR_NORM_BY_SHAPE(R, what, ...)                                        \
+#define GDR_NORM_BY_SHAPE(R, what, A, B, ...)                                   \
     do {                                                                       \
-        if (s.per == 8) {                                                      \
-            if (s.vec == 8) return R::template what<8, 8>(__VA_ARGS__);        \
-            if (s.vec == 2) return R::template what<2, 8>(__VA_ARGS__);        \
-            return R::template what<1, 8>(__VA_ARGS__);                        \
+        if (s.per == A) {                                                      \
+            if (s.vec == 8) return R::template what<8, A>(__VA_ARGS__);        \
+            if (s.vec == 2) return R::template what<2, A>(__VA_ARGS__);        \
+            return R::template what<1, A>(__VA_ARGS__);                        \
         }                                                                      \
-        if (s.vec == 8) return R::template what<8, 16>(__VA_ARGS__);           \
-        if (s.vec == 2) return R::template what<2, 16>(__VA_ARGS__);           \
-        return R::template what<1, 16>(__VA_ARGS__);                           \
+        if (s.vec == 8) return R::template what<8, B>(__VA_ARGS__);            \
+        if (s.vec == 2) return R::template what<2, B>(__VA_ARGS__);            \
+        return R::template what<1, B>(__VA_ARGS__);                            \
     } while (0)
 
 template <typename T, typename TX>
 int run_fwd(const NormParams &p, const Shape2 &s, const void *x, const void *y, const void *gate,
             void *x_out, void *h, cudaStream_t stream) {
     using R = Run<T, TX>;
-    GDR_NORM_BY_SHAPE(R, fwd, p, s, x, y, gate, x_out, h, stream);
+    GDR_NORM_BY_SHAPE(R, fwd, 8, 16, p, s, x, y, gate, x_out, h, stream);
 }
 template <typename T, typename TX>
 int run_bwd(const NormParams &p, const Shape2 &s, int blocks, const void *dx_out, const void *dh,
             const void *x, const void *y, const void *gate, void *dx, void *dy, void *dgate,
             float *pp, float *pn, float *pg, cudaStream_t stream) {
     using R = Run<T, TX>;
-    GDR_NORM_BY_SHAPE(R, bwd, p, s, blocks, dx_out, dh, x, y, gate, dx, dy, dgate, pp, pn, pg, stream);
+    GDR_NORM_BY_SHAPE(R, bwd, 8, 16, p, s, blocks, dx_out, dh, x, y, gate, dx, dy, dgate, pp, pn, pg, stream);
 }
 
 size_t elem(int dtype) { return dtype == GDR_F32 ? 4 : 2; }
@@ -354,6 +552,7 @@ int check_shape(const gdr_block_norm_shape *s, NormParams *p) {
     if (!(s->res_scale > -3.0e38f && s->res_scale < 3.0e38f)) return GDR_ERR_INVALID_ARG;
     p->rows = s->rows;
     p->D = s->D;
+    p->inv_D = 1.f / s->D;
     p->post = s->post_norm != 0;
     p->pre = s->pre_norm != 0;
     p->act = s->gate_act;
@@ -400,7 +599,7 @@ int gdr_block_norm_fwd(const gdr_block_norm_shape *shape, const void *x, const v
     if (!apart(x, nx, h, nt)) return GDR_ERR_INVALID_ARG;
     p.w_post = w_post;
     p.w_pre = w_pre;
-    const Shape2 s = shape_of(p.D);
+    const Shape2 s = shape_of(p.D, false);
     const cudaStream_t stm = (cudaStream_t)stream;
     if (shape->dtype == GDR_F32) return run_fwd<float, float>(p, s, x, y, gate, x_out, h, stm);
     if (shape->x_dtype == GDR_F32) return run_fwd<__nv_bfloat16, float>(p, s, x, y, gate, x_out, h, stm);
@@ -410,7 +609,7 @@ int gdr_block_norm_fwd(const gdr_block_norm_shape *shape, const void *x, const v
 size_t gdr_block_norm_bwd_workspace_size(const gdr_block_norm_shape *shape) {
     NormParams p;
     if (check_shape(shape, &p) != GDR_OK) return 0;
-    const Shape2 s = shape_of(p.D);
+    const Shape2 s = shape_of(p.D, true);
     const size_t parts = (size_t)bwd_blocks(p.rows, s) * s.block.y;
     return 256 + 3 * parts * ((size_t)(p.D + 3) / 4 * 4) * sizeof(float);
 }
@@ -450,7 +649,7 @@ int gdr_block_norm_bwd(const gdr_block_norm_shape *shape, const void *dx_out, co
     }
     p.w_post = w_post;
     p.w_pre = w_pre;
-    const Shape2 s = shape_of(p.D);
+    const Shape2 s = shape_of(p.D, true);
     const cudaStream_t stm = (cudaStream_t)stream;
     const int blocks = bwd_blocks(p.rows, s);
     const int parts = blocks * (int)s.block.y;

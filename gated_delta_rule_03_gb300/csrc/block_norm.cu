@@ -66,6 +66,7 @@ template <typename T, int VEC, int PER> struct Raw {
         }
     }
     __device__ __forceinline__ float operator[](int i) const { return p[i / VEC].get(i % VEC); }
+    __device__ __forceinline__ float2 two(int i) const { return make_float2((*this)[i], (*this)[i + 1]); }
 };
 
 template <typename T, int VEC, int PER>
@@ -119,6 +120,24 @@ template <int K> __device__ __forceinline__ void row_sum(float (&s)[K], float *b
         for (int k = 0; k < K; ++k) s[k] += __shfl_xor_sync(0xffffffffu, s[k], off);
 }
 
+// Two fp32 at a time.
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    float2 d;
+    asm("mul.rn.f32x2 %0, %1, %2;"
+        : "=l"(reinterpret_cast<uint64_t &>(d))
+        : "l"(reinterpret_cast<const uint64_t &>(a)), "l"(reinterpret_cast<const uint64_t &>(b)));
+    return d;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    float2 d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;"
+        : "=l"(reinterpret_cast<uint64_t &>(d))
+        : "l"(reinterpret_cast<const uint64_t &>(a)), "l"(reinterpret_cast<const uint64_t &>(b)),
+          "l"(reinterpret_cast<const uint64_t &>(c)));
+    return d;
+}
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
+
 // sigmoid by the hardware's exponential and reciprocal (a few units in the last place).
 __device__ __forceinline__ float sigmoid(float g) {
     float e, r;
@@ -126,28 +145,33 @@ __device__ __forceinline__ float sigmoid(float g) {
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
     return r;
 }
-// The gate's function of VEC entries, and with kDeriv its derivative; one branch for all.
-template <bool kDeriv, typename T, int VEC>
-__device__ __forceinline__ void gate_of(int act, const Pack<T, VEC> &g, float (&a)[VEC], float (&da)[VEC]) {
+// The gate's function of N entries; one branch for all.
+template <int N> __device__ __forceinline__ void gate_of(int act, const float (&g)[N], float (&a)[N]) {
     if (act == GDR_GATE_IDENTITY) {
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-            a[e] = g.get(e);
-            if (kDeriv) da[e] = 1.f;
-        }
+        for (int e = 0; e < N; ++e) a[e] = g[e];
     } else if (act == GDR_GATE_SILU) {
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-            const float x = g.get(e), s = sigmoid(x);
-            a[e] = x * s;
-            if (kDeriv) da[e] = fmaf(a[e], 1.f - s, s);
-        }
+        for (int e = 0; e < N; ++e) a[e] = g[e] * sigmoid(g[e]);
     } else {
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-            a[e] = sigmoid(g.get(e));
-            if (kDeriv) da[e] = a[e] * (1.f - a[e]);
-        }
+        for (int e = 0; e < N; ++e) a[e] = sigmoid(g[e]);
+    }
+}
+// The same of two entries with the derivative.
+__device__ __forceinline__ void gate_both(int act, float2 g, float2 &a, float2 &da) {
+    if (act == GDR_GATE_IDENTITY) {
+        a = g;
+        da = both(1.f);
+        return;
+    }
+    const float2 s = make_float2(sigmoid(g.x), sigmoid(g.y)), rest = fma2(s, both(-1.f), both(1.f));
+    if (act == GDR_GATE_SILU) {
+        a = mul2(g, s);
+        da = fma2(a, rest, s);
+    } else {
+        a = s;
+        da = mul2(s, rest);
     }
 }
 
@@ -189,9 +213,11 @@ block_norm_fwd_kernel(const NormParams p, const TX *x, const T *y, const T *gate
 #pragma unroll
         for (int j = 0; j < PER / VEC; ++j) {
             const Weight<VEC> wj = weight_of<VEC>(w, j, D);
-            float a[VEC], none[VEC];
+            float a[VEC], g[VEC];
             if (gate) {
-                gate_of<false>(p.act, gr.p[j], a, none);
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) g[e] = gr[j * VEC + e];
+                gate_of(p.act, g, a);
             } else {
 #pragma unroll
                 for (int e = 0; e < VEC; ++e) a[e] = 1.f;
@@ -264,17 +290,22 @@ block_norm_bwd_kernel(const NormParams p, const TX *dx_out, const T *dh, const T
     __shared__ float buf[96];
     extern __shared__ __align__(16) char dynamic[];
     float *wide = reinterpret_cast<float *>(dynamic);  // [3][D], each thread its own columns
-    float a_post[kWide ? 1 : PER], a_pre[kWide ? 1 : PER], a_gate[kWide ? 1 : PER];
+    constexpr int kSums = kWide ? 1 : PER / 2;
+    float2 a_post[kSums], a_pre[kSums], a_gate[kSums];
 #pragma unroll
-    for (int i = 0; i < (kWide ? 1 : PER); ++i) a_post[i] = a_pre[i] = a_gate[i] = 0.f;
+    for (int i = 0; i < kSums; ++i) a_post[i] = a_pre[i] = a_gate[i] = both(0.f);
     if (kWide) {
         for (int e = threadIdx.x; e < 3 * p.D; e += blockDim.x) wide[e] = 0.f;
         __syncthreads();
     }
     auto column = [&](int i) { return (threadIdx.x + blockDim.x * (i / VEC)) * VEC + i % VEC; };
-    auto add = [&](float (&a)[kWide ? 1 : PER], int which, int i, float x) {
-        if (!kWide) a[kWide ? 0 : i] += x;
-        else if (column(i) < p.D) wide[which * p.D + column(i)] += x;
+    auto add = [&](float2 (&a)[kSums], int which, int i, float2 x) {  // entries i, i + 1
+        if (!kWide) {
+            a[kWide ? 0 : i / 2] = fma2(x, both(1.f), a[kWide ? 0 : i / 2]);
+        } else {
+            if (column(i) < p.D) wide[which * p.D + column(i)] += x.x;
+            if (column(i + 1) < p.D) wide[which * p.D + column(i + 1)] += x.y;
+        }
     };
     const int64_t step = (int64_t)gridDim.x * blockDim.y;
     const int64_t rounds = (p.rows + step - 1) / step;  // the same for every thread: barriers inside
@@ -313,28 +344,24 @@ block_norm_bwd_kernel(const NormParams p, const TX *dx_out, const T *dh, const T
             }
         }
         const char *const here = mine_at + (round & 1 ? kRound * threads : 0);
-        float dv[PER];
-        float sums[3] = {0.f, 0.f, 0.f};
-        Raw<TX, VEC, PER> xr;
+        Raw<TX, VEC, PER> xr, dr;
         Raw<T, VEC, PER> hr, yr, gr;
-        Raw<TX, VEC, PER> dr;
-        if constexpr (!kAhead) {  // (from shared memory they are read where they are used)
-            dr.load(dx_out + at, dx_out ? D : 0);
-            gr.load(gate + row * p.gate_stride, gate ? D : 0);
-        }
-        if (dh) {
-            if constexpr (kAhead) {
+        if constexpr (kAhead) {  // (dx_out and gate are read where they are used)
+            if (dh) {
                 read8(xr.p[0], here + kX * threads, threads);
                 read8(hr.p[0], here + 2 * kX * threads, threads);
-            } else {
-                xr.load(x + at, D);
-                hr.load(dh + at, D);
             }
+            if (y) read8(yr.p[0], here + (2 * kX + kT) * threads, threads);
+        } else {
+            dr.load(dx_out + at, dx_out ? D : 0);
+            xr.load(x + at, dh ? D : 0);
+            hr.load(dh + at, dh ? D : 0);
+            yr.load(y + at, y ? D : 0);
+            gr.load(gate + row * p.gate_stride, gate ? D : 0);
         }
-        if (y) {
-            if constexpr (kAhead) read8(yr.p[0], here + (2 * kX + kT) * threads, threads);
-            else yr.load(y + at, D);
-        }
+        // entries in pairs throughout
+        float2 dv[PER / 2];
+        float2 xx = both(0.f), hx = xx, yy = xx;
         if (dh) {
 #pragma unroll
             for (int j = 0; j < PER / VEC; ++j) {
@@ -342,78 +369,88 @@ block_norm_bwd_kernel(const NormParams p, const TX *dx_out, const T *dh, const T
 #pragma unroll
                 for (int e = 0; e < VEC; ++e) {
                     const int i = j * VEC + e;
-                    const float xv = xr[i];
-                    dv[i] = hr[i] * w.v[e];
-                    sums[0] = fmaf(xv, xv, sums[0]);
-                    sums[1] = fmaf(dv[i], xv, sums[1]);
+                    (i & 1 ? dv[i / 2].y : dv[i / 2].x) = w.v[e];
                 }
+            }
+#pragma unroll
+            for (int i = 0; i < PER; i += 2) {
+                const float2 xv = xr.two(i);
+                dv[i / 2] = mul2(dv[i / 2], hr.two(i));
+                xx = fma2(xv, xv, xx);
+                hx = fma2(dv[i / 2], xv, hx);
             }
         }
         if (p.post) {
 #pragma unroll
-            for (int i = 0; i < PER; ++i) sums[2] = fmaf(yr[i], yr[i], sums[2]);
+            for (int i = 0; i < PER; i += 2) yy = fma2(yr.two(i), yr.two(i), yy);
         }
+        float sums[3] = {xx.x + xx.y, hx.x + hx.y, yy.x + yy.y};
         if (dh || p.post) row_sum(sums, buf, 0);
-        {
-            if constexpr (kAhead)
-                if (dx_out) read8(dr.p[0], here, threads);
+        if constexpr (kAhead)
+            if (dx_out) read8(dr.p[0], here, threads);
+        if (dh) {
             const float r = rsqrtf(sums[0] * p.inv_D + p.eps), m = r * r * (sums[1] * p.inv_D);
 #pragma unroll
-            for (int i = 0; i < PER; ++i) {
-                const float d = dx_out ? dr[i] : 0.f;
-                if (dh) {
-                    const float xv = xr[i];
-                    add(a_pre, 1, i, hr[i] * (xv * r));
-                    dv[i] = fmaf(r, dv[i] - xv * m, d);
-                } else {
-                    dv[i] = d;
-                }
+            for (int i = 0; i < PER; i += 2) {
+                const float2 xv = xr.two(i);
+                add(a_pre, 1, i, mul2(hr.two(i), mul2(xv, both(r))));
+                dv[i / 2] = fma2(both(r), fma2(xv, both(-m), dv[i / 2]), dx_out ? dr.two(i) : both(0.f));
             }
+        } else {
+#pragma unroll
+            for (int i = 0; i < PER; i += 2) dv[i / 2] = dr.two(i);
         }
-        store_row<TX, VEC>(dx + at, D, dv);
+        store_row<TX, VEC>(dx + at, D, reinterpret_cast<const float(&)[PER]>(dv));
         if (!y) continue;
         const float r = p.post ? rsqrtf(sums[2] * p.inv_D + p.eps) : 1.f;
         const float *w_post = p.post ? p.w_post : nullptr;
-        float dot[1] = {0.f};
+        float2 yd = both(0.f), wt[PER / 2];
         if constexpr (kAhead)
             if (gate) read8(gr.p[0], here + (2 * kX + 2 * kT) * threads, threads);
 #pragma unroll
         for (int j = 0; j < PER / VEC; ++j) {
             const Weight<VEC> w = weight_of<VEC>(w_post, j, D);
-            float a[VEC], dg[VEC];
-            if (gate) {
-                gate_of<true>(p.act, gr.p[j], a, dg);
-            } else {
-#pragma unroll
-                for (int e = 0; e < VEC; ++e) a[e] = 1.f;
-            }
 #pragma unroll
             for (int e = 0; e < VEC; ++e) {
                 const int i = j * VEC + e;
-                const float yv = yr[i], yn = yv * r, dz = p.s * dv[i];
-                if (gate) {
-                    dg[e] *= dz * (yn * w.v[e]);
-                    if (part_gate) add(a_gate, 2, i, dg[e]);
-                }
-                const float da = dz * a[e];
-                add(a_post, 0, i, da * yn);
-                dv[i] = da * w.v[e];
-                dot[0] = fmaf(dv[i], yv, dot[0]);
-            }
-            if (gate && p.gate_stride && dgate) {
-                const int e0 = (threadIdx.x + blockDim.x * j) * VEC;
-                Pack<T, VEC> out;
-                pack_all(out, dg);
-                if (e0 < D) *reinterpret_cast<Pack<T, VEC> *>(dgate + at + e0) = out;
+                (i & 1 ? wt[i / 2].y : wt[i / 2].x) = w.v[e];
             }
         }
+        if (gate) {
+            float2 dg[PER / 2];
+#pragma unroll
+            for (int i = 0; i < PER; i += 2) {
+                float2 a, da;
+                gate_both(p.act, gr.two(i), a, da);
+                const float2 dz = mul2(both(p.s), dv[i / 2]);
+                dg[i / 2] = mul2(mul2(dz, da), mul2(mul2(yr.two(i), both(r)), wt[i / 2]));
+                dv[i / 2] = mul2(dz, a);
+            }
+            if (p.gate_stride) {
+                if (dgate) store_row<T, VEC>(dgate + at, D, reinterpret_cast<const float(&)[PER]>(dg));
+            } else if (part_gate) {
+#pragma unroll
+                for (int i = 0; i < PER; i += 2) add(a_gate, 2, i, dg[i / 2]);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < PER; i += 2) dv[i / 2] = mul2(both(p.s), dv[i / 2]);
+        }
+#pragma unroll
+        for (int i = 0; i < PER; i += 2) {
+            const float2 yv = yr.two(i);
+            add(a_post, 0, i, mul2(dv[i / 2], mul2(yv, both(r))));
+            dv[i / 2] = mul2(dv[i / 2], wt[i / 2]);
+            yd = fma2(dv[i / 2], yv, yd);
+        }
         if (p.post) {
+            float dot[1] = {yd.x + yd.y};
             row_sum(dot, buf, 1);
             const float m = r * r * (dot[0] * p.inv_D);
 #pragma unroll
-            for (int i = 0; i < PER; ++i) dv[i] = r * (dv[i] - yr[i] * m);
+            for (int i = 0; i < PER; i += 2) dv[i / 2] = mul2(both(r), fma2(yr.two(i), both(-m), dv[i / 2]));
         }
-        store_row<T, VEC>(dy + at, D, dv);
+        store_row<T, VEC>(dy + at, D, reinterpret_cast<const float(&)[PER]>(dv));
     }
     const int64_t mine = ((int64_t)blockIdx.x * blockDim.y + threadIdx.y) * p.D;
     if constexpr (kWide) {
@@ -422,9 +459,9 @@ block_norm_bwd_kernel(const NormParams p, const TX *dx_out, const T *dh, const T
         for (int i = 0; i < 3; ++i)
             for (int e = threadIdx.x; part[i] && e < p.D; e += blockDim.x) part[i][mine + e] = wide[i * p.D + e];
     } else {
-        if (part_post) store_row<float, VEC>(part_post + mine, p.D, a_post);
-        if (part_pre) store_row<float, VEC>(part_pre + mine, p.D, a_pre);
-        if (part_gate) store_row<float, VEC>(part_gate + mine, p.D, a_gate);
+        if (part_post) store_row<float, VEC>(part_post + mine, p.D, reinterpret_cast<const float(&)[PER]>(a_post));
+        if (part_pre) store_row<float, VEC>(part_pre + mine, p.D, reinterpret_cast<const float(&)[PER]>(a_pre));
+        if (part_gate) store_row<float, VEC>(part_gate + mine, p.D, reinterpret_cast<const float(&)[PER]>(a_gate));
     }
 }
 

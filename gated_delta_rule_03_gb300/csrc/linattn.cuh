@@ -27,6 +27,7 @@
 //   first to last:  lam^(f seg) S0 + sum_{g<f} lam^((f-1-g) seg) R_g
 //   last to first:  lam^(tokens behind f) dS_final + sum_{g>f} lam^((g-1-f) seg) R_g
 // and all segments run at once. With one segment per sequence the first launch is left out.
+// Where the sums alone would leave SMs idle, they are taken over parts of a segment.
 #pragma once
 
 #include "internal.h"
@@ -34,7 +35,6 @@
 namespace gdr {
 namespace linattn {
 
-constexpr int kTile = 128;        // segments are a multiple of this many tokens
 constexpr float kLog2e = 1.4426950408889634f;
 
 // One mix of a launch.
@@ -50,7 +50,7 @@ struct Mix {
     float s_intra, s_inter, s_state;
     const float *start;     // S0 or dS_final, [num_seqs, H] matrices, or null
     float *end;             // S_final or dS0, or null
-    const float *R;         // the segments' own sums, [item, H] matrices (null: one segment)
+    const float *R;         // the segments' own sums (null: one segment)
     float *R_out;           // state only: where they go
 };
 
@@ -58,10 +58,12 @@ struct Mix {
 struct Plan {
     const int32_t *cu_seqlens;  // null: equal lengths
     int64_t num_seqs, total_tokens;
-    int64_t seg;                // tokens per segment (a multiple of kTile)
+    int64_t seg;                // tokens per segment (a multiple of a block's chunk)
     int64_t seq_len;            // equal lengths
     int segs;                   // segments per sequence (equal lengths)
     int64_t items;              // segments in all (packed: an upper bound)
+    int split;                  // parts of a segment that are summed by themselves (each seg / split
+                                // tokens): R has [item, split, H] matrices
     int H;
     const float *log_decay;
     int32_t *status;            // the workspace's status word

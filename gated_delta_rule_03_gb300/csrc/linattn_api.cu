@@ -47,36 +47,12 @@ int check_shape(const gdr_linattn_shape *s, Call *c) {
     c->dtype = s->dtype;
     c->scale = s->scale;
     c->e = s->dtype == GDR_F32 ? 4 : 2;
-    // blocks of a launch: at most (tiles + sequences) x heads x slices
-    if ((c->T / kTile + c->N) > (int64_t)(INT32_MAX / 16) / c->H) return GDR_ERR_INVALID_ARG;
+    // blocks of a launch: at most (tiles of 64 + sequences) x heads x slices (4) or parts (4) x mixes (3)
+    if ((c->T / 64 + c->N) > (int64_t)(INT32_MAX / 16) / c->H) return GDR_ERR_INVALID_ARG;
     int st = check_stride(s->q_stride, c->qh, c->dk, c->e, &c->qs);
     if (st == GDR_OK) st = check_stride(s->k_stride, c->kh, c->dk, c->e, &c->ks);
     if (st == GDR_OK) st = check_stride(s->v_stride, c->vh, c->dv, c->e, &c->vs);
     return st;
-}
-
-// Tokens per segment. `cols`: blocks per segment and head. The model: a launch takes
-// rounds x tiles per segment, a segment's own sum about half of what its mix takes, and the
-// second launch and the reading of the sums some tiles' worth more.
-int64_t segment_tokens(const Call &c, bool packed, int cols) {
-    const int64_t tiles = (c.T + kTile - 1) / kTile;
-    const int64_t m = packed ? tiles : (c.T / c.N + kTile - 1) / kTile;  // longest possible
-    if (m <= 1) return kTile;
-    const int64_t sms = 152;
-    int64_t best = m;
-    double best_cost = 1e300;
-    for (int64_t n = 1; n <= m && n <= 256; ++n) {
-        const int64_t len = (m + n - 1) / n;
-        const int64_t items = packed ? tiles / len + c.N : c.N * ((m + len - 1) / len);
-        const int64_t rounds = (items * c.H * cols + sms - 1) / sms;
-        double cost = (double)rounds * len;
-        if (n > 1) cost = 1.5 * cost + 3 + 0.5 * n;
-        if (cost < best_cost) {
-            best_cost = cost;
-            best = len;
-        }
-    }
-    return best * kTile;
 }
 
 // bf16 goes to the tensor cores (a call without tokens has nothing for them).
@@ -88,6 +64,52 @@ int columns(const Call &c, bool backward) {
     return backward ? c.dk / 64 : c.dv / 64;
 }
 
+// Tokens per segment, by a model of the time in microseconds. `cols`: blocks per segment and
+// head; a launch takes rounds of 152 blocks. Tensor cores: a tile of 128 tokens takes 2.5 us
+// in a mix and 1.2 in a sum, a block 8 to start and end, and reads a sum in 1; the second
+// launch costs 4. fp32 arithmetic: tiles of 64 tokens, 9 and 4 us, 3 to start, 2 a sum.
+// (4 x 4096 x 16 heads: 1, 2, 3, 4 segments 92, 89, 105, 111 us; 65536 x 16 chains: 5, 7, 9, 10
+// segments 411, 313, 263, 368 us.)
+struct Cost {
+    int tile;
+    double mix, sum, start, read;
+};
+Cost cost_of(const Call &c) {
+    if (on_tensor_cores(c)) return {128, 2.5, 1.2, 8, 1};
+    return {64, 9, 4, 3, 2};
+}
+int64_t segment_tokens(const Call &c, bool packed, int cols, int *split) {
+    *split = 1;
+    const Cost k = cost_of(c);
+    const int64_t tiles = (c.T + k.tile - 1) / k.tile;
+    const int64_t m = packed ? tiles : (c.T / c.N + k.tile - 1) / k.tile;  // longest possible
+    if (m <= 1) return k.tile;
+    const int64_t sms = 152;
+    int64_t best = m;
+    double best_cost = 1e300;
+    for (int64_t n = 1; n <= m && n <= 256; ++n) {
+        const int64_t len = (m + n - 1) / n;
+        const int64_t items = packed ? tiles / len + c.N : c.N * ((m + len - 1) / len);
+        const int64_t rounds = (items * c.H * cols + sms - 1) / sms;
+        // (the sums in 1, 2 or 4 parts of a segment, on the tensor cores)
+        for (int parts = 1; parts <= (n > 1 && on_tensor_cores(c) ? 4 : 1); parts *= 2) {
+            if (len % parts) break;
+            double cost = (double)rounds * (len * k.mix + k.start);
+            if (n > 1) {
+                const int64_t blocks = (items * (n - 1) + n - 1) / n * c.H * cols * parts;
+                cost += 4 + (double)((blocks + sms - 1) / sms) * ((double)len / parts * k.sum + k.start) +
+                        (double)(n - 1) * parts * k.read;
+            }
+            if (cost < best_cost) {
+                best_cost = cost;
+                best = len;
+                *split = parts;
+            }
+        }
+    }
+    return best * k.tile;
+}
+
 Plan make_plan(const Call &c, const float *log_decay, const int32_t *cu, int cols, void *ws) {
     Plan p = {};
     p.cu_seqlens = cu;
@@ -96,7 +118,7 @@ Plan make_plan(const Call &c, const float *log_decay, const int32_t *cu, int col
     p.H = c.H;
     p.log_decay = log_decay;
     p.status = (int32_t *)ws;
-    p.seg = segment_tokens(c, cu != nullptr, cols);
+    p.seg = segment_tokens(c, cu != nullptr, cols, &p.split);
     if (cu) {
         p.items = c.T / p.seg + c.N;
     } else {
@@ -116,10 +138,11 @@ struct Layout {
     size_t copy, R, R2, part[3], total;
     int parts[3];  // heads and slices whose gradients add up to one head's of dq, dk, dv
 };
-Layout layout(const Call &c, int64_t items, bool backward) {
+// `sums_each`: matrices of the segments' own sums per head and direction.
+Layout layout(const Call &c, int64_t sums_each, bool backward) {
     Layout L = {};
     size_t off = 256;
-    const size_t sums = (size_t)items * c.H * c.dk * c.dv * sizeof(float);
+    const size_t sums = (size_t)sums_each * c.H * c.dk * c.dv * sizeof(float);
     L.copy = off;
     if (!backward) off = align_up(off + c.state());
     L.R = off;
@@ -137,16 +160,17 @@ Layout layout(const Call &c, int64_t items, bool backward) {
     L.total = off;
     return L;
 }
+int64_t sums_of(const Plan &p) { return segmented(p) ? p.items * p.split : 0; }
 // The larger of what equal and packed lengths take.
 size_t workspace_bytes_for(const Call &c, bool backward) {
     static const int32_t some = 0;
     const int cols = columns(c, backward);
-    int64_t items = make_plan(c, nullptr, &some, cols, nullptr).items;
+    int64_t sums = sums_of(make_plan(c, nullptr, &some, cols, nullptr));
     if (c.T % c.N == 0) {
-        const int64_t equal = make_plan(c, nullptr, nullptr, cols, nullptr).items;
-        if (equal > items) items = equal;
+        const int64_t equal = sums_of(make_plan(c, nullptr, nullptr, cols, nullptr));
+        if (equal > sums) sums = equal;
     }
-    return layout(c, items, backward).total;
+    return layout(c, sums, backward).total;
 }
 
 struct Span {
@@ -231,7 +255,7 @@ int gdr_linattn_fwd(const gdr_linattn_shape *shape, const void *q, const void *k
         if (overlap(s, small[0]) || overlap(s, small[1])) return GDR_ERR_INVALID_ARG;
 
     Plan p = make_plan(c, log_decay, cu_seqlens, columns(c, false), workspace);
-    const Layout L = layout(c, p.items, false);
+    const Layout L = layout(c, sums_of(p), false);
     char *ws = (char *)workspace;
     const cudaStream_t s = (cudaStream_t)stream;
     Mix m = mix_of(c, q, c.qs, c.qh, k, c.ks, c.kh, v, c.vs, c.vh, c.dk, c.dv);
@@ -279,7 +303,7 @@ int gdr_linattn_bwd(const gdr_linattn_shape *shape, const void *d_o, const void 
         if (overlap(s, small[0]) || overlap(s, small[1])) return GDR_ERR_INVALID_ARG;
 
     Plan p = make_plan(c, log_decay, cu_seqlens, columns(c, true), workspace);
-    const Layout L = layout(c, p.items, true);
+    const Layout L = layout(c, sums_of(p), true);
     char *ws = (char *)workspace;
     const cudaStream_t s = (cudaStream_t)stream;
     Mix q_, k_, v_;  // dq, dk, dv

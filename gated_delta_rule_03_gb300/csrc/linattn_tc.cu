@@ -275,25 +275,32 @@ __device__ __forceinline__ StateAt state_row(const TcArgs &A, const TcMix &m, in
     const int64_t aa = a + m.astep * slice, bb = b + m.bstep * slice;
     return m.turned ? StateAt{bb * A.pitch + aa, A.pitch} : StateAt{aa * A.pitch + bb, 1};
 }
-// (pointers are opaque after every step: 32 places worked out ahead would take 64 registers)
-// Eight of the columns, from column 8 part on, times w added to `sum`.
-__device__ __forceinline__ void read_state(float (&sum)[8], const float *S, const StateAt &at, int part, float w) {
-    const float *p = S + at.first + (int64_t)(8 * part) * at.step;
+// E += w times them. (Pointers are opaque after some steps: 32 places worked out ahead would
+// take 64 registers.)
+__device__ __forceinline__ void read_state(float2 (&E)[16], const float *S, const StateAt &at, float w) {
+    const float *p = S + at.first;
+    const float2 w2 = make_float2(w, w);
     if (at.step == 1) {
+        float4 x[8];
 #pragma unroll
-        for (int j = 0; j < 8; j += 4) {
-            const float4 x = *reinterpret_cast<const float4 *>(p + j);
-            sum[j] = fmaf(w, x.x, sum[j]);
-            sum[j + 1] = fmaf(w, x.y, sum[j + 1]);
-            sum[j + 2] = fmaf(w, x.z, sum[j + 2]);
-            sum[j + 3] = fmaf(w, x.w, sum[j + 3]);
+        for (int j = 0; j < 8; ++j) x[j] = reinterpret_cast<const float4 *>(p)[j];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            E[2 * j] = fma2(w2, make_float2(x[j].x, x[j].y), E[2 * j]);
+            E[2 * j + 1] = fma2(w2, make_float2(x[j].z, x[j].w), E[2 * j + 1]);
         }
     } else {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            sum[j] = fmaf(w, *p, sum[j]);
-            p += at.step;
-            asm volatile("" : "+l"(p));
+        for (int part = 0; part < 2; ++part) {
+            float x[16];
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+                x[j] = *p;
+                p += at.step;
+                if (j % 4 == 3) asm volatile("" : "+l"(p));
+            }
+#pragma unroll
+            for (int j = 0; j < 8; ++j) E[8 * part + j] = fma2(w2, make_float2(x[2 * j], x[2 * j + 1]), E[8 * part + j]);
         }
     }
 }
@@ -436,24 +443,20 @@ __global__ void __launch_bounds__(kThreads, 1) mix_tc_kernel(const __grid_consta
         float2 E[16];
 #pragma unroll
         for (int j = 0; j < 16; ++j) E[j] = make_float2(0.f, 0.f);
-        if (mine && (m.start || m.R)) {
-            const float *const S = m.start ? m.start + ((int64_t)w.s.seq * A.p.H + w.h) * A.mat : nullptr;
-            const float ws = decay_pow(l2, (float)(back ? w.s.behind : (int64_t)w.s.f * A.p.seg));
-            const float *const R = m.R ? m.R + (w.s.item0 * A.p.H + w.h) * A.mat : nullptr;
-            const int64_t next = A.p.H * A.mat;  // from one segment's sum to the next one's
-#pragma unroll
-            for (int part = 0; part < 4; ++part) {
-                float sum[8];
-#pragma unroll
-                for (int i = 0; i < 8; ++i) sum[i] = 0.f;
-                if (S) read_state(sum, S, st, part, ws);
+        griddep_wait();  // the segments' sums are there (the loads began before)
+        if (mine) {
+            if (m.start)
+                read_state(E, m.start + ((int64_t)w.s.seq * A.p.H + w.h) * A.mat, st,
+                           decay_pow(l2, (float)(back ? w.s.behind : (int64_t)w.s.f * A.p.seg)));
+            if (m.R) {
+                const int part = (int)(A.p.seg / A.p.split);
+                const float *R = m.R + (w.s.item0 * A.p.split * A.p.H + w.h) * A.mat;
+                const int first = back ? (w.s.f + 1) * A.p.split : 0, end = (back ? w.s.n : w.s.f) * A.p.split;
 #pragma unroll 1
-                for (int g = back ? w.s.f + 1 : 0; R && g < (back ? w.s.n : w.s.f); ++g) {
-                    const int apart = back ? g - 1 - w.s.f : w.s.f - 1 - g;
-                    read_state(sum, R + g * next, st, part, decay_pow(l2, (float)(apart * A.p.seg)));
+                for (int i = first; i < end; ++i) {
+                    const int apart = back ? i - first : end - 1 - i;
+                    read_state(E, R + (int64_t)i * A.p.H * A.mat, st, decay_pow(l2, (float)apart * (float)part));
                 }
-#pragma unroll
-                for (int i = 0; i < 4; ++i) E[4 * part + i] = make_float2(sum[2 * i], sum[2 * i + 1]);
             }
         }
         // rows of E as the K rows of a B operand
@@ -763,12 +766,17 @@ __global__ void __launch_bounds__(kSumThreads, 1) sum_tc_kernel(const __grid_con
     const int64_t rest = blockIdx.x / A.count;
     w.slice = (int)(rest % A.slices);
     w.h = (int)(rest / A.slices % A.p.H);
-    w.item = rest / A.slices / A.p.H;
+    w.item = rest / A.slices / A.p.H;  // of the parts
+    const int part = (int)(w.item % A.p.split);
+    griddep_launch_dependents();
     bool bad;
-    w.s = locate(A.p, w.item, &found, &bad);
+    w.s = locate(A.p, w.item / A.p.split, &found, &bad);
     if (blockIdx.x == 0 && tid == 0 && A.p.first) A.p.status[0] = bad ? GDR_ERR_BAD_SEQLENS : GDR_OK;
     if (bad || w.s.seq < 0) return;
     const TcMix &m = A.mix[w.role];
+    const int64_t part_len = A.p.seg / A.p.split;
+    w.s.begin += part * part_len;
+    w.s.tokens = max((int64_t)0, min(part_len, w.s.tokens - part * part_len));  // (none: a sum of zero)
     if (w.s.f == (m.backward ? 0 : w.s.n - 1)) return;  // hands nothing on
     const float l2 = log2_decay(A.p.log_decay[w.h]);
     const int chunks = (int)((w.s.tokens + C - 1) / C);
@@ -905,12 +913,23 @@ __global__ void __launch_bounds__(kSumThreads, 1) sum_tc_kernel(const __grid_con
     if (warp == 0) tmem_dealloc(tmem, TM_COLS);
 }
 
-template <typename K> int run(K kernel, const TcArgs &A, int threads, uint32_t smem, cudaStream_t stream) {
+// `after_sums`: may start while the sums' launch ahead of it ends (it waits for it before it
+// reads them).
+template <typename K>
+int run(K kernel, const TcArgs &A, int64_t items, int threads, uint32_t smem, bool after_sums, cudaStream_t stream) {
     if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
         return GDR_ERR_CUDA;
-    const int64_t blocks = A.p.items * A.p.H * A.slices * A.count;
-    kernel<<<(unsigned)blocks, threads, smem, stream>>>(A);
-    return cuda_status(cudaGetLastError());
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(items * A.p.H * A.slices * A.count));
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = after_sums ? 1 : 0;
+    return cuda_status(cudaLaunchKernelEx(&cfg, kernel, A));
 }
 
 }  // namespace
@@ -970,8 +989,8 @@ int launch_mix_tc(const Plan &p, const Mix *mixes, int count, int d_v, bool sums
         m.s_state = s.s_state;
         m.start = s.start; m.end = s.end; m.R = s.R; m.R_out = s.R_out;
     }
-    if (sums) return run(sum_tc_kernel, A, kSumThreads, kSumSmem, stream);
-    return run(mix_tc_kernel, A, kThreads, kSmem, stream);
+    if (sums) return run(sum_tc_kernel, A, p.items * p.split, kSumThreads, kSumSmem, false, stream);
+    return run(mix_tc_kernel, A, p.items, kThreads, kSmem, !p.first, stream);
 }
 
 }  // namespace linattn

@@ -61,7 +61,7 @@ struct Plan {
     int64_t seg;                // tokens per segment (a multiple of a block's chunk)
     int64_t seq_len;            // equal lengths
     int segs;                   // segments per sequence (equal lengths)
-    int64_t items;              // segments in all (packed: an upper bound)
+    int64_t items, handing;     // segments in all, and those that hand a sum on (packed: upper bounds)
     int split;                  // parts of a segment that are summed by themselves (each seg / split
                                 // tokens): R has [item, split, H] matrices
     int H;
@@ -79,11 +79,14 @@ struct Segment {
     int64_t item0;  // the sequence's first item
 };
 
-// Which segment item `item` is; called by the whole block (a barrier inside). With
+// What item `item` of a launch is: the segments in order, or (`handing` 1 or 2) those that hand
+// a sum on, all of a sequence but its last (1) or its first (2). Called by the whole block (a barrier inside). With
 // cu_seqlens every block checks all of it (offsets from 0, not decreasing, at most
 // total_tokens); where it is not so, no block does anything and `bad` is set.
-__device__ __forceinline__ Segment locate(const Plan &p, int64_t item, Segment *shared, bool *bad) {
+__device__ __forceinline__ Segment locate(const Plan &p, int64_t item, int handing, Segment *shared, bool *bad) {
     *bad = false;
+    const int skip = handing == 2;  // segments in front of the first item's
+    const int less = handing != 0;
     auto fill = [&](int seq, int f, int n, int64_t first, int64_t len, int64_t item0) {
         Segment s;
         s.seq = seq;
@@ -97,8 +100,9 @@ __device__ __forceinline__ Segment locate(const Plan &p, int64_t item, Segment *
         return s;
     };
     if (!p.cu_seqlens) {
-        const int seq = (int)(item / p.segs), f = (int)(item % p.segs);
-        return fill(seq, f, p.segs, (int64_t)seq * p.seq_len, p.seq_len, item - f);
+        const int each = p.segs - less;
+        const int seq = (int)(item / each), f = (int)(item % each) + skip;
+        return fill(seq, f, p.segs, (int64_t)seq * p.seq_len, p.seq_len, (int64_t)seq * p.segs);
     }
     __shared__ int64_t warp_sum[32];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = (blockDim.x + 31) >> 5;
@@ -116,6 +120,7 @@ __device__ __forceinline__ Segment locate(const Plan &p, int64_t item, Segment *
             } else {
                 count = (len + p.seg - 1) / p.seg;
                 if (count < 1) count = 1;  // an empty sequence still hands on its state
+                count -= less;
             }
         }
         int64_t sum = count;
@@ -133,7 +138,7 @@ __device__ __forceinline__ Segment locate(const Plan &p, int64_t item, Segment *
         }
         const int64_t first_item = carry + before + sum - count;
         if (count > 0 && item >= first_item && item < first_item + count)
-            *shared = fill((int)n, (int)(item - first_item), (int)count, a, len, first_item);
+            *shared = fill((int)n, (int)(item - first_item) + skip, (int)count + less, a, len, first_item + n * less);
         carry += total;
         __syncthreads();
     }
@@ -158,8 +163,12 @@ int launch_mix_exact(const Plan &p, const Mix *mixes, int count, int dtype, cuda
 int launch_mix_tc(const Plan &p, const Mix *mixes, int count, int d_v, bool sums, cudaStream_t stream);
 // Sums the g parts of every head: in fp32 [rows, heads g, d] -> out [rows, heads, d]. Rows
 // behind the last sequence are left as they are.
-int launch_share(const Plan &p, const float *in, void *out, int heads, int g, int d, int dtype,
-                 cudaStream_t stream);
+struct Share {
+    const float *in;
+    void *out;
+    int heads, g, d;
+};
+int launch_share(const Plan &p, const Share *shares, int count, int dtype, cudaStream_t stream);
 int launch_step(const void *q, const void *k, const void *v, const float *log_decay, float *S,
                 void *o, int64_t N, int H, int qg, int kg, int vg, int dk, int dv, int dtype,
                 float scale, int64_t qs, int64_t ks, int64_t vs, cudaStream_t stream);

@@ -68,8 +68,12 @@ int columns(const Call &c, bool backward) {
 // head; a launch takes rounds of 152 blocks. Tensor cores: a tile of 128 tokens takes 2.5 us
 // in a mix and 1.2 in a sum, a block 8 to start and end, and reads a sum in 1; the second
 // launch costs 4. fp32 arithmetic: tiles of 64 tokens, 9 and 4 us, 3 to start, 2 a sum.
-// (4 x 4096 x 16 heads: 1, 2, 3, 4 segments 92, 89, 105, 111 us; 65536 x 16 chains: 5, 7, 9, 10
-// segments 411, 313, 263, 368 us.)
+// Blocks of different lengths filling up an SM take 1.2 times their sum, and half a block's
+// time is lost at the end. (4 x 4096 x 16 heads: 1, 2, 3, 4 segments 92, 89, 105, 111 us; 65536
+// x 16 chains: 5, 7, 9, 10 segments 411, 313, 263, 368 us. Eight packed sequences, 40,000
+// tokens, 16 heads, segments of 24 and of 72 tiles: all equal 192 and 143 us, the longest 1.6
+// times the mean 237 and 187, twice 234 and 230, 4 times 191 and 257; with 4 heads 11 tiles 82
+// us, 72 tiles 171.)
 struct Cost {
     int tile;
     double mix, sum, start, read;
@@ -82,22 +86,36 @@ int64_t segment_tokens(const Call &c, bool packed, int cols, int *split) {
     *split = 1;
     const Cost k = cost_of(c);
     const int64_t tiles = (c.T + k.tile - 1) / k.tile;
-    const int64_t m = packed ? tiles : (c.T / c.N + k.tile - 1) / k.tile;  // longest possible
+    const int64_t mean = (c.T / c.N + k.tile - 1) / k.tile;
+    // The longest sequence. Of packed ones the host knows no lengths, and takes 7/4 of the mean
+    // (to a multiple of 4); a longer one is cut there, with its sums in four parts.
+    int64_t m = mean;
+    if (packed) {
+        m = ((7 * mean + 3) / 4 + 3) / 4 * 4;
+        if (c.N == 1 || m > tiles) m = tiles;
+    }
     if (m <= 1) return k.tile;
-    const int64_t sms = 152;
+    const double sms = 152;
+    // blocks one after the other on every SM: equal ones in rounds, others filling up
+    auto time = [&](double blocks, double longest, double total, double start) {
+        if (blocks <= sms) return longest + start;
+        if (!packed) return ceil(blocks / sms) * (longest + start);
+        return 1.2 * (total + blocks * start) / sms + 0.5 * (longest + start);
+    };
     int64_t best = m;
     double best_cost = 1e300;
+    const double all = (double)(packed ? tiles : c.N * mean) * c.H * cols;  // tiles of a mix
     for (int64_t n = 1; n <= m && n <= 256; ++n) {
         const int64_t len = (m + n - 1) / n;
-        const int64_t items = packed ? tiles / len + c.N : c.N * ((m + len - 1) / len);
-        const int64_t rounds = (items * c.H * cols + sms - 1) / sms;
+        const double items = packed ? (double)tiles / len + 0.5 * c.N : (double)(c.N * ((m + len - 1) / len));
+        const double blocks = (items < c.N ? c.N : items) * c.H * cols;
         // (the sums in 1, 2 or 4 parts of a segment, on the tensor cores)
         for (int parts = 1; parts <= (n > 1 && on_tensor_cores(c) ? 4 : 1); parts *= 2) {
             if (len % parts) break;
-            double cost = (double)rounds * (len * k.mix + k.start);
+            double cost = time(blocks, len * k.mix, all * k.mix, k.start);
             if (n > 1) {
-                const int64_t blocks = (items * (n - 1) + n - 1) / n * c.H * cols * parts;
-                cost += 4 + (double)((blocks + sms - 1) / sms) * ((double)len / parts * k.sum + k.start) +
+                const double handing_on = (blocks - (double)c.N * c.H * cols) / blocks;
+                cost += 4 + time(blocks * handing_on * parts, (double)len / parts * k.sum, all * handing_on * k.sum, k.start) +
                         (double)(n - 1) * parts * k.read;
             }
             if (cost < best_cost) {
@@ -107,6 +125,7 @@ int64_t segment_tokens(const Call &c, bool packed, int cols, int *split) {
             }
         }
     }
+    if (packed && best == m && m < tiles && on_tensor_cores(c)) *split = 4;
     return best * k.tile;
 }
 
@@ -120,12 +139,14 @@ Plan make_plan(const Call &c, const float *log_decay, const int32_t *cu, int col
     p.status = (int32_t *)ws;
     p.seg = segment_tokens(c, cu != nullptr, cols, &p.split);
     if (cu) {
-        p.items = c.T / p.seg + c.N;
+        p.handing = c.T / p.seg;
+        p.items = p.handing + c.N;
     } else {
         p.seq_len = c.T / c.N;
         p.segs = (int)((p.seq_len + p.seg - 1) / p.seg);
         if (p.segs < 1) p.segs = 1;
         p.items = c.N * p.segs;
+        p.handing = p.items - c.N;
     }
     return p;
 }
@@ -339,11 +360,11 @@ int gdr_linattn_bwd(const gdr_linattn_shape *shape, const void *d_o, const void 
         if (c.T == 0) all[i].out = workspace;  // (no rows: nothing is written to it)
     }
     if ((st = launch(c, p, all, 3, false, s)) != GDR_OK) return st;
+    Share shares[3];
+    int n = 0;
     for (int i = 0; i < 3 && c.T > 0; ++i)
-        if (all[i].out_f32) {
-            st = launch_share(p, (const float *)all[i].out, to[i], heads[i], L.parts[i], i == 2 ? c.dv : c.dk, c.dtype, s);
-            if (st != GDR_OK) return st;
-        }
+        if (all[i].out_f32) shares[n++] = {(const float *)all[i].out, to[i], heads[i], L.parts[i], i == 2 ? c.dv : c.dk};
+    if (n > 0) return launch_share(p, shares, n, c.dtype, s);
     return GDR_OK;
 }
 

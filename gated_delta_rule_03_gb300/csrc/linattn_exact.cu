@@ -62,11 +62,9 @@ __global__ void __launch_bounds__(kThreads, 1) mix_exact_kernel(const Plan p, co
     const int slice = (int)(block % slices), h = (int)(block / slices % p.H);
     const int64_t item = block / slices / p.H;
     bool bad;
-    const Segment s = locate(p, item, &found, &bad);
+    const Segment s = locate(p, item, kOut ? 0 : 1 + m.backward, &found, &bad);
     if (block == 0 && tid == 0 && p.first) p.status[0] = bad ? GDR_ERR_BAD_SEQLENS : GDR_OK;
     if (bad || s.seq < 0) return;
-    // the last segment from the side that the state comes from hands nothing on
-    if (!kOut && s.f == (m.backward ? 0 : s.n - 1)) return;
 
     const float l2 = log2_decay(p.log_decay[h]);
     for (int i = tid; i <= C; i += kThreads) pw[i] = decay_pow(l2, (float)i);
@@ -221,7 +219,7 @@ __global__ void __launch_bounds__(kThreads, 1) mix_exact_kernel(const Plan p, co
     }
 
     float *to = nullptr;
-    if (!kOut) to = m.R_out + (item * p.H + h) * mat;
+    if (!kOut) to = m.R_out + ((s.item0 + s.f) * p.H + h) * mat;
     else if (m.end && s.f == (m.backward ? 0 : s.n - 1)) to = m.end + ((int64_t)s.seq * p.H + h) * mat;
     if (!to) return;
 #pragma unroll
@@ -244,7 +242,7 @@ int launch_one(const Plan &p, const Mix &m, cudaStream_t stream) {
     if (cudaFuncSetAttribute(mix_exact_kernel<T, DX, kOut>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              (int)bytes) != cudaSuccess)
         return GDR_ERR_CUDA;
-    const int64_t blocks = p.items * p.H * (m.dz / NZ);
+    const int64_t blocks = (kOut ? p.items : p.handing) * p.H * (m.dz / NZ);
     mix_exact_kernel<T, DX, kOut><<<(unsigned)blocks, kThreads, bytes, stream>>>(p, m);
     return cuda_status(cudaGetLastError());
 }
@@ -259,19 +257,23 @@ template <typename T> int launch_t(const Plan &p, const Mix &m, cudaStream_t str
     return GDR_ERR_UNSUPPORTED;
 }
 
-template <typename T>
-__global__ void __launch_bounds__(256)
-share_kernel(const Plan p, const float *__restrict__ in, T *__restrict__ out, int heads, int g, int d) {
-    const int64_t rows = p.cu_seqlens ? p.cu_seqlens[p.num_seqs] : p.total_tokens;
+struct Shares {
+    Share v[3];
+};
+// Bound by its reads: g fp32 per value written, 16 bytes at a time.
+template <typename T> __global__ void __launch_bounds__(256) share_kernel(const Plan p, const Shares shares) {
+    const Share &m = shares.v[blockIdx.y];
     if (p.status[0] != GDR_OK) return;
-    const int quads = d / 4;
-    const int64_t total = rows * heads * quads;
+    const int64_t rows = p.cu_seqlens ? p.cu_seqlens[p.num_seqs] : p.total_tokens;
+    const int quads = m.d / 4;
+    const int64_t total = rows * m.heads * quads;
     for (int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x; e < total; e += (int64_t)gridDim.x * 256) {
         const int j = (int)(e % quads) * 4;
-        const int64_t rh = e / quads;  // row * heads + head: the g heads behind it are in[rh g ..]
-        float4 sum = load4(in + rh * g * d + j);
-        for (int i = 1; i < g; ++i) fma4(sum, 1.f, load4(in + (rh * g + i) * d + j));
-        store4(out + rh * d + j, sum);
+        const int64_t rh = e / quads;  // row * heads + head: its g parts are in[rh g ..]
+        const float *in = m.in + rh * m.g * m.d + j;
+        float4 sum = load4(in);
+        for (int i = 1; i < m.g; ++i) fma4(sum, 1.f, load4(in + i * m.d));
+        store4((T *)m.out + rh * m.d + j, sum);
     }
 }
 
@@ -288,15 +290,18 @@ int launch_mix_exact(const Plan &p, const Mix *mixes, int count, int dtype, cuda
     return GDR_OK;
 }
 
-int launch_share(const Plan &p, const float *in, void *out, int heads, int g, int d, int dtype,
-                 cudaStream_t stream) {
-    const int64_t quads = p.total_tokens * heads * (d / 4);
+int launch_share(const Plan &p, const Share *shares, int count, int dtype, cudaStream_t stream) {
+    Shares all = {};
+    int64_t quads = 0;
+    for (int i = 0; i < count; ++i) {
+        all.v[i] = shares[i];
+        const int64_t q = p.total_tokens * shares[i].heads * (shares[i].d / 4);
+        if (q > quads) quads = q;
+    }
     const int64_t blocks = (quads + 255) / 256;
-    const unsigned grid = (unsigned)(blocks < 152 * 16 ? blocks : 152 * 16);
-    if (dtype == GDR_BF16)
-        share_kernel<<<grid, 256, 0, stream>>>(p, in, (__nv_bfloat16 *)out, heads, g, d);
-    else
-        share_kernel<<<grid, 256, 0, stream>>>(p, in, (float *)out, heads, g, d);
+    const dim3 grid((unsigned)(blocks < 152 * 16 ? blocks : 152 * 16), (unsigned)count);
+    if (dtype == GDR_BF16) share_kernel<__nv_bfloat16><<<grid, 256, 0, stream>>>(p, all);
+    else share_kernel<float><<<grid, 256, 0, stream>>>(p, all);
     return cuda_status(cudaGetLastError());
 }
 

@@ -266,6 +266,27 @@ __device__ __forceinline__ void add_update(float2 (&E)[16], float w, uint32_t ta
         E[j] = fma2(w2, E[j], make_float2(__uint_as_float(u[j >> 3][2 * j & 15]), __uint_as_float(u[j >> 3][(2 * j & 15) + 1])));
 }
 
+// Four lanes that hold 32 words each of a row of their own (8 words per part): afterwards part
+// i of lane q is part q of lane i's row.
+__device__ __forceinline__ void turn_four(float (&p)[32], int lane) {
+#pragma unroll
+    for (int step = 1; step < 4; step *= 2) {
+        const bool up = lane & step;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if (i & step) continue;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                // the lower lane sends its part i + step, the upper one its part i
+                const float mine = up ? p[8 * i + e] : p[8 * (i + step) + e];
+                const float other = __shfl_xor_sync(0xffffffffu, mine, step);
+                if (up) p[8 * i + e] = other;
+                else p[8 * (i + step) + e] = other;
+            }
+        }
+    }
+}
+
 // A thread's 32 columns of state row a, from or to memory.
 struct StateAt {
     int64_t first;  // element of column 0
@@ -354,7 +375,7 @@ __global__ void __launch_bounds__(kThreads, 1) mix_tc_kernel(const __grid_consta
     w.h = (int)(rest / A.slices % A.p.H);
     w.item = rest / A.slices / A.p.H;
     bool bad;
-    w.s = locate(A.p, w.item, &found, &bad);
+    w.s = locate(A.p, w.item, 0, &found, &bad);
     if (blockIdx.x == 0 && tid == 0 && A.p.first) A.p.status[0] = bad ? GDR_ERR_BAD_SEQLENS : GDR_OK;
     if (bad || w.s.seq < 0) return;
     const TcMix &m = A.mix[w.role];
@@ -585,28 +606,42 @@ __global__ void __launch_bounds__(kThreads, 1) mix_tc_kernel(const __grid_consta
             const bool tile = n == C && !m.out_f32;
             unsigned char *row = sm + slot(cc, 0) * TILE + (sub >> 1) * BLOCK + t * 128;
             char *to = out0 + (int64_t)c * C * pitch;
+            if (m.out_f32) {
+                // four rows at a time, 32 bytes of one per lane
+                float p[32];
 #pragma unroll
-            for (int half = 0; half < 2; ++half) {
-                uint32_t p[8];
-                float2 x[8];
+                for (int j = 0; j < 32; ++j) p[j] = wo * __uint_as_float(o[j >> 4][j & 15]);
+                turn_four(p, lane);
+                const int live = has_z ? n - (t & ~3) : 0;  // rows of the four to be written
+                char *at = to + (32 - pitch) * (lane & 3);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    x[j] = mul2(wo2, make_float2(__uint_as_float(o[half][2 * j]), __uint_as_float(o[half][2 * j + 1])));
-                    p[j] = pack_bf16x2(x[j].x, x[j].y);
+                for (int i = 0; i < 4; ++i) {
+                    if (i < live) {
+                        *reinterpret_cast<float4 *>(at) = make_float4(p[8 * i], p[8 * i + 1], p[8 * i + 2], p[8 * i + 3]);
+                        *reinterpret_cast<float4 *>(at + 16) =
+                            make_float4(p[8 * i + 4], p[8 * i + 5], p[8 * i + 6], p[8 * i + 7]);
+                    }
+                    at += pitch;
                 }
-                if (!has_z) {
-                } else if (tile) {
+            } else {
 #pragma unroll
-                    for (int i = 0; i < 2; ++i)
-                        *reinterpret_cast<uint4 *>(row + (((4 * sub + 2 * half + i) ^ t) & 7) * 16) =
-                            make_uint4(p[4 * i], p[4 * i + 1], p[4 * i + 2], p[4 * i + 3]);
-                } else if (t < n && m.out_f32) {
+                for (int half = 0; half < 2; ++half) {
+                    uint32_t p[8];
 #pragma unroll
-                    for (int j = 0; j < 8; j += 2)
-                        *reinterpret_cast<float4 *>(to + 64 * half + 8 * j) = make_float4(x[j].x, x[j].y, x[j + 1].x, x[j + 1].y);
-                } else if (t < n) {
-                    *reinterpret_cast<uint4 *>(to + 32 * half) = make_uint4(p[0], p[1], p[2], p[3]);
-                    *reinterpret_cast<uint4 *>(to + 32 * half + 16) = make_uint4(p[4], p[5], p[6], p[7]);
+                    for (int j = 0; j < 8; ++j) {
+                        const float2 x = mul2(wo2, make_float2(__uint_as_float(o[half][2 * j]), __uint_as_float(o[half][2 * j + 1])));
+                        p[j] = pack_bf16x2(x.x, x.y);
+                    }
+                    if (!has_z) {
+                    } else if (tile) {
+#pragma unroll
+                        for (int i = 0; i < 2; ++i)
+                            *reinterpret_cast<uint4 *>(row + (((4 * sub + 2 * half + i) ^ t) & 7) * 16) =
+                                make_uint4(p[4 * i], p[4 * i + 1], p[4 * i + 2], p[4 * i + 3]);
+                    } else if (t < n) {
+                        *reinterpret_cast<uint4 *>(to + 32 * half) = make_uint4(p[0], p[1], p[2], p[3]);
+                        *reinterpret_cast<uint4 *>(to + 32 * half + 16) = make_uint4(p[4], p[5], p[6], p[7]);
+                    }
                 }
             }
             fence_async_smem();
@@ -770,14 +805,14 @@ __global__ void __launch_bounds__(kSumThreads, 1) sum_tc_kernel(const __grid_con
     const int part = (int)(w.item % A.p.split);
     griddep_launch_dependents();
     bool bad;
-    w.s = locate(A.p, w.item / A.p.split, &found, &bad);
+    w.s = locate(A.p, w.item / A.p.split, 1 + A.mix[w.role].backward, &found, &bad);
     if (blockIdx.x == 0 && tid == 0 && A.p.first) A.p.status[0] = bad ? GDR_ERR_BAD_SEQLENS : GDR_OK;
     if (bad || w.s.seq < 0) return;
     const TcMix &m = A.mix[w.role];
     const int64_t part_len = A.p.seg / A.p.split;
     w.s.begin += part * part_len;
     w.s.tokens = max((int64_t)0, min(part_len, w.s.tokens - part * part_len));  // (none: a sum of zero)
-    if (w.s.f == (m.backward ? 0 : w.s.n - 1)) return;  // hands nothing on
+    w.item = (w.s.item0 + w.s.f) * A.p.split + part;  // of R
     const float l2 = log2_decay(A.p.log_decay[w.h]);
     const int chunks = (int)((w.s.tokens + C - 1) / C);
     auto chunk_of = [&](int cc) { return m.backward ? chunks - 1 - cc : cc; };
@@ -989,7 +1024,7 @@ int launch_mix_tc(const Plan &p, const Mix *mixes, int count, int d_v, bool sums
         m.s_state = s.s_state;
         m.start = s.start; m.end = s.end; m.R = s.R; m.R_out = s.R_out;
     }
-    if (sums) return run(sum_tc_kernel, A, p.items * p.split, kSumThreads, kSumSmem, false, stream);
+    if (sums) return run(sum_tc_kernel, A, p.handing * p.split, kSumThreads, kSumSmem, false, stream);
     return run(mix_tc_kernel, A, p.items, kThreads, kSmem, !p.first, stream);
 }
 

@@ -12,7 +12,7 @@ import functools
 import torch
 
 from . import ops
-from .linattn import _addr, _dense, _given
+from .linattn import _addr, _dense, _given, _new
 from .ops import _DTYPES, _launch, _need
 
 # the gate's function (gdr_block_norm_shape.gate_act)
@@ -82,11 +82,11 @@ def block_norm_fwd(x, y=None, gate=None, act="silu", w_post=None, w_pre=None, po
     dev = x.device
     dt = y.dtype if y is not None else (dtype or x.dtype)
     if y is not None:
-        x_out = _dense(x_out, "x_out", x.shape, x.dtype, dev)
+        x_out = _dense(x_out, "x_out", x.shape, x.dtype, dev, stream)
     elif x_out is not None:
         raise ValueError("x_out needs y")
     if pre_norm:
-        h = _dense(h, "h", x.shape, dt, dev)
+        h = _dense(h, "h", x.shape, dt, dev, stream)
     elif h is not None:
         raise ValueError("h needs pre_norm")
     _launch(lib.gdr_block_norm_fwd, "gdr_block_norm_fwd", dev, stream, _shape(fields), x.data_ptr(), _addr(y),
@@ -121,21 +121,21 @@ def block_norm_bwd(dx_out, dh, x_out, y=None, gate=None, act="silu", w_post=None
         _given(dh, "dh", x_out.shape, dtype, dev)
     elif dh is not None:
         raise ValueError("dh needs pre_norm")
-    dx = _dense(dx, "dx", x_out.shape, x_out.dtype, dev)
+    dx = _dense(dx, "dx", x_out.shape, x_out.dtype, dev, stream)
     if y is not None:
-        dy = _dense(dy, "dy", y.shape, dtype, dev)
+        dy = _dense(dy, "dy", y.shape, dtype, dev, stream)
     if gate is not None:
-        dgate = _dense(dgate, "dgate", gate.shape, dtype, dev)
+        dgate = _dense(dgate, "dgate", gate.shape, dtype, dev, stream)
     if w_post is not None:
-        dw_post = _dense(dw_post, "dw_post", (D,), torch.float32, dev)
+        dw_post = _dense(dw_post, "dw_post", (D,), torch.float32, dev, stream)
     if w_pre is not None:
-        dw_pre = _dense(dw_pre, "dw_pre", (D,), torch.float32, dev)
+        dw_pre = _dense(dw_pre, "dw_pre", (D,), torch.float32, dev, stream)
     for name, given, has in (("dy", dy, y), ("dgate", dgate, gate), ("dw_post", dw_post, w_post),
                              ("dw_pre", dw_pre, w_pre)):
         if given is not None and has is None:
             raise ValueError(f"{name} has no input")
     if workspace is None:
-        workspace = torch.empty(_workspace_bytes(fields), dtype=torch.uint8, device=dev)
+        workspace = _new(_workspace_bytes(fields), torch.uint8, dev, stream)
     _need(workspace, "workspace", device=dev)
     _launch(lib.gdr_block_norm_bwd, "gdr_block_norm_bwd", dev, stream, _shape(fields), _addr(dx_out), _addr(dh),
             x_out.data_ptr(), _addr(y), _addr(gate), _addr(w_post), _addr(w_pre), dx.data_ptr(), _addr(dy),

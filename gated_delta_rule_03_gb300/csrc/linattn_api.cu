@@ -29,6 +29,7 @@ int check_stride(int64_t given, int heads, int d, size_t e, int64_t *out) {
 
 int check_shape(const gdr_linattn_shape *s, Call *c) {
     if (!s || s->num_seqs < 1 || s->total_tokens < 0 || s->H < 1) return GDR_ERR_INVALID_ARG;
+    if (s->H > 1 << 16) return GDR_ERR_INVALID_ARG;  // a row of outputs stays below 2^31 bytes
     if (s->total_tokens > INT32_MAX || s->num_seqs > INT32_MAX / 2) return GDR_ERR_INVALID_ARG;
     if (s->q_heads < 1 || s->k_heads < 1 || s->v_heads < 1) return GDR_ERR_INVALID_ARG;
     if (s->H % s->q_heads || s->H % s->k_heads || s->H % s->v_heads) return GDR_ERR_INVALID_ARG;

@@ -377,7 +377,10 @@ __global__ void __launch_bounds__(kThreads, 1) mix_tc_kernel(const __grid_consta
     bool bad;
     w.s = locate(A.p, w.item, 0, &found, &bad);
     if (blockIdx.x == 0 && tid == 0 && A.p.first) A.p.status[0] = bad ? GDR_ERR_BAD_SEQLENS : GDR_OK;
-    if (bad || w.s.seq < 0) return;
+    if (bad || w.s.seq < 0) {
+        griddep_wait();  // no launch ends before the one ahead of it
+        return;
+    }
     const TcMix &m = A.mix[w.role];
     const bool back = m.backward;
     const float l2_of_head = log2_decay(A.p.log_decay[w.h]);

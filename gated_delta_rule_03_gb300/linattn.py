@@ -92,10 +92,19 @@ def _seqs(cu_seqlens, num_seqs, device):
     return n
 
 
-def _dense(t, name, shape, dtype, device):
+def _new(shape, dtype, device, stream):
+    """A tensor to be written on `stream`: memory of that stream, so that what the current
+    stream still does with memory it has given back does not run into it."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _dense(t, name, shape, dtype, device, stream=None):
     """A given output, checked, or a new one."""
     if t is None:
-        return torch.empty(shape, dtype=dtype, device=device)
+        return _new(shape, dtype, device, stream)
     _need(t, name, dtype, device)
     if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
@@ -125,9 +134,9 @@ def linattn_bwd_workspace_size(num_seqs, total_tokens, H, dk, dv, dtype=torch.bf
                             v_heads or H, dk, dv, _DTYPES[dtype], 1.0, 0, 0, 0))
 
 
-def _workspace(workspace, backward, fields, device):
+def _workspace(workspace, backward, fields, device, stream):
     if workspace is None:
-        return torch.empty(max(_workspace_bytes(backward, fields), 256), dtype=torch.uint8, device=device)
+        return _new(max(_workspace_bytes(backward, fields), 256), torch.uint8, device, stream)
     _need(workspace, "workspace", device=device)
     return workspace
 
@@ -144,10 +153,10 @@ def linattn_fwd(q, k, v, log_decay, S0=None, cu_seqlens=None, num_seqs=None, sca
     fields = _fields(q, k, v, log_decay, n, scale)
     dev, (T, H, dk, dv) = q.device, (fields[1], fields[2], fields[6], fields[7])
     _given(S0, "S0", (n, H, dk, dv), torch.float32, dev)
-    o = _dense(o, "o", (T, H, dv), q.dtype, dev)
+    o = _dense(o, "o", (T, H, dv), q.dtype, dev, stream)
     if final_state or S_final is not None:
-        S_final = _dense(S_final, "S_final", (n, H, dk, dv), torch.float32, dev)
-    ws = _workspace(workspace, False, fields, dev)
+        S_final = _dense(S_final, "S_final", (n, H, dk, dv), torch.float32, dev, stream)
+    ws = _workspace(workspace, False, fields, dev, stream)
     _launch(lib.gdr_linattn_fwd, "gdr_linattn_fwd", dev, stream, _shape(fields), q.data_ptr(), k.data_ptr(),
             v.data_ptr(), log_decay.data_ptr(), _addr(S0), _addr(cu_seqlens), o.data_ptr(), _addr(S_final),
             ws.data_ptr(), ws.nbytes)
@@ -169,12 +178,12 @@ def linattn_bwd(do, q, k, v, log_decay, S0=None, dS_final=None, cu_seqlens=None,
     if do is None:
         raise TypeError("do must be a torch.Tensor")
     _given(do, "do", (T, H, d_v), q.dtype, dev)
-    dq = _dense(dq, "dq", q.shape, q.dtype, dev)
-    dk = _dense(dk, "dk", k.shape, q.dtype, dev)
-    dv = _dense(dv, "dv", v.shape, q.dtype, dev)
+    dq = _dense(dq, "dq", q.shape, q.dtype, dev, stream)
+    dk = _dense(dk, "dk", k.shape, q.dtype, dev, stream)
+    dv = _dense(dv, "dv", v.shape, q.dtype, dev, stream)
     if S0 is not None or dS0 is not None:
-        dS0 = _dense(dS0, "dS0", state, torch.float32, dev)
-    ws = _workspace(workspace, True, fields, dev)
+        dS0 = _dense(dS0, "dS0", state, torch.float32, dev, stream)
+    ws = _workspace(workspace, True, fields, dev, stream)
     _launch(lib.gdr_linattn_bwd, "gdr_linattn_bwd", dev, stream, _shape(fields), do.data_ptr(), q.data_ptr(),
             k.data_ptr(), v.data_ptr(), log_decay.data_ptr(), _addr(S0), _addr(dS_final), _addr(cu_seqlens),
             dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), _addr(dS0), ws.data_ptr(), ws.nbytes)
@@ -190,7 +199,7 @@ def linattn_step(q, k, v, log_decay, S, scale=1.0, o=None, stream=None):
     if S is None:
         raise TypeError("S must be a torch.Tensor")
     _given(S, "S", (N, H, dk, dv), torch.float32, dev)
-    o = _dense(o, "o", (N, H, dv), q.dtype, dev)
+    o = _dense(o, "o", (N, H, dv), q.dtype, dev, stream)
     _launch(lib.gdr_linattn_step, "gdr_linattn_step", dev, stream, _shape(fields), q.data_ptr(), k.data_ptr(),
             v.data_ptr(), log_decay.data_ptr(), S.data_ptr(), o.data_ptr())
     return o

@@ -419,7 +419,7 @@ int gdr_read_device_status(const void *workspace, int *status, gdr_stream_t stre
  *
  * Shape of a call (a HOST struct):
  *   num_seqs, total_tokens   sequences (>= 1) and rows of the packed tensors
- *   H                        heads of the state and of o
+ *   H                        heads of the state and of o, at most 65536
  *   q_heads, k_heads, v_heads  heads of q, k and v; each divides H, and head h reads head
  *                            h / (H / q_heads) of q, and so on (keys and values shared by
  *                            groups of query heads, or queries and keys by groups of

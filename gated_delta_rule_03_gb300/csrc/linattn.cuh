@@ -60,8 +60,10 @@ struct Plan {
     int64_t num_seqs, total_tokens;
     int64_t seg;                // tokens per segment (a multiple of a block's chunk)
     int64_t seq_len;            // equal lengths
-    int segs;                   // segments per sequence (equal lengths)
-    int64_t items, handing;     // segments in all, and those that hand a sum on (packed: upper bounds)
+    int segs;                   // segments per sequence (equal lengths) ..
+    int64_t whole;              // .. of all but the first `whole` (sequence, head) pairs: they stay whole
+    int64_t items;              // segments of all sequences (packed: an upper bound)
+    int64_t units, handing;     // (segment, head) pairs, and those that hand a sum on (packed: likewise)
     int split;                  // parts of a segment that are summed by themselves (each seg / split
                                 // tokens): R has [item, split, H] matrices
     int H;
@@ -77,33 +79,45 @@ struct Segment {
     int64_t tokens; // its tokens
     int64_t behind; // tokens of the sequence behind it
     int64_t item0;  // the sequence's first item
+    int h;          // head
 };
 
-// What item `item` of a launch is: the segments in order, or (`handing` 1 or 2) those that hand
-// a sum on, all of a sequence but its last (1) or its first (2). Called by the whole block (a barrier inside). With
-// cu_seqlens every block checks all of it (offsets from 0, not decreasing, at most
-// total_tokens); where it is not so, no block does anything and `bad` is set.
-__device__ __forceinline__ Segment locate(const Plan &p, int64_t item, int handing, Segment *shared, bool *bad) {
-    *bad = false;
+// What unit `unit` of a launch is, a segment and a head: all of them, or (`handing` 1 or 2)
+// those that hand a sum on, all of a sequence but its last (1) or its first (2). Equal
+// lengths: first the pairs that stay whole, then the segments one after the other. Called
+// by the whole block (a barrier inside). With cu_seqlens every block checks all of it (offsets from 0, not decreasing, at most
+// total_tokens); where it is not so, no block does anything: false.
+__device__ __forceinline__ bool locate(const Plan &p, int64_t unit, int handing, Segment *shared) {
     const int skip = handing == 2;  // segments in front of the first item's
     const int less = handing != 0;
-    auto fill = [&](int seq, int f, int n, int64_t first, int64_t len, int64_t item0) {
+    auto fill = [&](int seq, int h, int f, int n, int64_t first, int64_t len, int64_t item0) {
         Segment s;
         s.seq = seq;
         s.f = f;
         s.n = n;
         s.begin = first + (int64_t)f * p.seg;
         const int64_t rest = len - (int64_t)f * p.seg;
-        s.tokens = rest < p.seg ? rest : p.seg;
+        s.tokens = n == 1 || rest < p.seg ? rest : p.seg;
         s.behind = rest - s.tokens;
         s.item0 = item0;
-        return s;
+        s.h = h;
+        *shared = s;
     };
     if (!p.cu_seqlens) {
-        const int each = p.segs - less;
-        const int seq = (int)(item / each), f = (int)(item % each) + skip;
-        return fill(seq, f, p.segs, (int64_t)seq * p.seq_len, p.seq_len, (int64_t)seq * p.segs);
+        int64_t pair = unit;
+        int f = 0, n = 1;
+        if (less || unit >= p.whole) {
+            const int64_t r = less ? unit : unit - p.whole, left = p.num_seqs * p.H - p.whole;
+            pair = p.whole + r % left;
+            f = (int)(r / left) + skip;
+            n = p.segs;
+        }
+        const int64_t seq = pair / p.H;
+        if (threadIdx.x == 0) fill((int)seq, (int)(pair % p.H), f, n, seq * p.seq_len, p.seq_len, seq * p.segs);
+        __syncthreads();
+        return true;
     }
+    const int64_t item = unit / p.H;
     __shared__ int64_t warp_sum[32];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = (blockDim.x + 31) >> 5;
     if (tid == 0) shared->seq = -1;
@@ -138,12 +152,11 @@ __device__ __forceinline__ Segment locate(const Plan &p, int64_t item, int handi
         }
         const int64_t first_item = carry + before + sum - count;
         if (count > 0 && item >= first_item && item < first_item + count)
-            *shared = fill((int)n, (int)(item - first_item) + skip, (int)count + less, a, len, first_item + n * less);
+            fill((int)n, (int)(unit % p.H), (int)(item - first_item) + skip, (int)count + less, a, len, first_item + n * less);
         carry += total;
         __syncthreads();
     }
-    *bad = __syncthreads_or(wrong) != 0;
-    return *shared;
+    return __syncthreads_or(wrong) == 0;
 }
 
 // log2 of the decay, held finite so that 0 * log2(lam) is 0 for lam = 0 (-inf); NaN stays.

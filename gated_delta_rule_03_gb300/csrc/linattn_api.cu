@@ -65,8 +65,7 @@ int columns(const Call &c, bool backward) {
     return backward ? c.dk / 64 : c.dv / 64;
 }
 
-// Tokens per segment, by a model of the time in microseconds. `cols`: blocks per segment and
-// head; a launch takes rounds of 152 blocks. Tensor cores: a tile of 128 tokens takes 2.5 us
+// How sequences are cut, by a model of the time in microseconds: a launch takes rounds of 152 blocks. Tensor cores: a tile of 128 tokens takes 2.5 us
 // in a mix and 1.2 in a sum, a block 8 to start and end, and reads a sum in 1; the second
 // launch costs 4. fp32 arithmetic: tiles of 64 tokens, 9 and 4 us, 3 to start, 2 a sum.
 // Blocks of different lengths filling up an SM take 1.2 times their sum, and half a block's
@@ -83,9 +82,15 @@ Cost cost_of(const Call &c) {
     if (on_tensor_cores(c)) return {128, 2.5, 1.2, 8, 1};
     return {64, 9, 4, 3, 2};
 }
-int64_t segment_tokens(const Call &c, bool packed, int cols, int *split) {
-    *split = 1;
+struct Cut {
+    int64_t seg;    // tokens per segment
+    int split;      // parts of one that are summed by themselves
+    int64_t whole;  // (sequence, head) pairs that are not cut
+};
+Cut cut(const Call &c, bool packed, bool backward) {
     const Cost k = cost_of(c);
+    const bool tc = on_tensor_cores(c);
+    const int cols = columns(c, backward), sum_cols = tc && backward ? cols / 3 * 2 : cols;
     const int64_t tiles = (c.T + k.tile - 1) / k.tile;
     const int64_t mean = (c.T / c.N + k.tile - 1) / k.tile;
     // The longest sequence. Of packed ones the host knows no lengths, and takes 7/4 of the mean
@@ -95,42 +100,49 @@ int64_t segment_tokens(const Call &c, bool packed, int cols, int *split) {
         m = ((7 * mean + 3) / 4 + 3) / 4 * 4;
         if (c.N == 1 || m > tiles) m = tiles;
     }
-    if (m <= 1) return k.tile;
+    if (m <= 1) return {k.tile, 1, 0};
     const double sms = 152;
+    const int64_t pairs = c.N * c.H;
     // blocks one after the other on every SM: equal ones in rounds, others filling up
-    auto time = [&](double blocks, double longest, double total, double start) {
-        if (blocks <= sms) return longest + start;
-        if (!packed) return ceil(blocks / sms) * (longest + start);
-        return 1.2 * (total + blocks * start) / sms + 0.5 * (longest + start);
+    auto time = [&](double blocks, double longest, double total) {
+        if (blocks <= sms) return longest + k.start;
+        if (!packed) return ceil(blocks / sms) * (longest + k.start);
+        return 1.2 * (total + blocks * k.start) / sms + 0.5 * (longest + k.start);
     };
-    int64_t best = m;
+    Cut best = {m, 1, 0};
     double best_cost = 1e300;
-    const double all = (double)(packed ? tiles : c.N * mean) * c.H * cols;  // tiles of a mix
+    // Pairs of equal lengths that fill whole rounds may stay whole, and only the rest is cut.
+    const int64_t full = packed || pairs * cols < sms ? 0 : (int64_t)sms * (pairs * cols / (int64_t)sms) / cols;
     for (int64_t n = 1; n <= m && n <= 256; ++n) {
-        const int64_t len = (m + n - 1) / n;
-        const double items = packed ? (double)tiles / len + 0.5 * c.N : (double)(c.N * ((m + len - 1) / len));
-        const double blocks = (items < c.N ? c.N : items) * c.H * cols;
-        // (the sums in 1, 2 or 4 parts of a segment, on the tensor cores)
-        for (int parts = 1; parts <= (n > 1 && on_tensor_cores(c) ? 4 : 1); parts *= 2) {
-            if (len % parts) break;
-            double cost = time(blocks, len * k.mix, all * k.mix, k.start);
-            if (n > 1) {
-                const double handing_on = (blocks - (double)c.N * c.H * cols) / blocks;
-                cost += 4 + time(blocks * handing_on * parts, (double)len / parts * k.sum, all * handing_on * k.sum, k.start) +
-                        (double)(n - 1) * parts * k.read;
-            }
-            if (cost < best_cost) {
-                best_cost = cost;
-                best = len;
-                *split = parts;
+        const int64_t len = (m + n - 1) / n, segs = (m + len - 1) / len;
+        for (int64_t whole : {(int64_t)0, full}) {
+            if (whole && (n == 1 || whole == pairs)) break;
+            const int64_t cuts = pairs - whole;
+            double items = (double)(cuts * segs);
+            if (packed) items = fmax(((double)tiles / len + 0.5 * c.N) * c.H, (double)pairs);
+            const double all = (double)(packed ? tiles * c.H : cuts * m);  // tiles of a mix
+            const double handing = (items - cuts) / items;
+            // (the sums in 1, 2 or 4 parts of a segment, on the tensor cores)
+            for (int parts = 1; parts <= (n > 1 && tc ? 4 : 1); parts *= 2) {
+                if (len % parts) break;
+                double cost = time(items * cols, len * k.mix, all * cols * k.mix);
+                if (whole) cost += time((double)(whole * cols), m * k.mix, 0);
+                if (n > 1)
+                    cost += 4 + time(items * handing * sum_cols * parts, (double)len / parts * k.sum, all * handing * sum_cols * k.sum) +
+                            (double)(n - 1) * parts * k.read;
+                if (cost < best_cost) {
+                    best_cost = cost;
+                    best = {len, parts, whole};
+                }
             }
         }
     }
-    if (packed && best == m && m < tiles && on_tensor_cores(c)) *split = 4;
-    return best * k.tile;
+    if (packed && best.seg == m && m < tiles && tc) best.split = 4;
+    best.seg *= k.tile;
+    return best;
 }
 
-Plan make_plan(const Call &c, const float *log_decay, const int32_t *cu, int cols, void *ws) {
+Plan make_plan(const Call &c, const float *log_decay, const int32_t *cu, bool backward, void *ws) {
     Plan p = {};
     p.cu_seqlens = cu;
     p.num_seqs = c.N;
@@ -138,16 +150,21 @@ Plan make_plan(const Call &c, const float *log_decay, const int32_t *cu, int col
     p.H = c.H;
     p.log_decay = log_decay;
     p.status = (int32_t *)ws;
-    p.seg = segment_tokens(c, cu != nullptr, cols, &p.split);
+    const Cut at = cut(c, cu != nullptr, backward);
+    p.seg = at.seg;
+    p.split = at.split;
     if (cu) {
-        p.handing = c.T / p.seg;
-        p.items = p.handing + c.N;
+        p.items = c.T / p.seg + c.N;
+        p.units = p.items * c.H;
+        p.handing = c.T / p.seg * c.H;
     } else {
         p.seq_len = c.T / c.N;
         p.segs = (int)((p.seq_len + p.seg - 1) / p.seg);
         if (p.segs < 1) p.segs = 1;
+        p.whole = p.segs > 1 ? at.whole : 0;
         p.items = c.N * p.segs;
-        p.handing = p.items - c.N;
+        p.handing = (c.N * c.H - p.whole) * (p.segs - 1);
+        p.units = c.N * c.H + p.handing;
     }
     return p;
 }
@@ -186,10 +203,9 @@ int64_t sums_of(const Plan &p) { return segmented(p) ? p.items * p.split : 0; }
 // The larger of what equal and packed lengths take.
 size_t workspace_bytes_for(const Call &c, bool backward) {
     static const int32_t some = 0;
-    const int cols = columns(c, backward);
-    int64_t sums = sums_of(make_plan(c, nullptr, &some, cols, nullptr));
+    int64_t sums = sums_of(make_plan(c, nullptr, &some, backward, nullptr));
     if (c.T % c.N == 0) {
-        const int64_t equal = sums_of(make_plan(c, nullptr, nullptr, cols, nullptr));
+        const int64_t equal = sums_of(make_plan(c, nullptr, nullptr, backward, nullptr));
         if (equal > sums) sums = equal;
     }
     return layout(c, sums, backward).total;
@@ -276,7 +292,7 @@ int gdr_linattn_fwd(const gdr_linattn_shape *shape, const void *q, const void *k
     for (const Span &s : out)
         if (overlap(s, small[0]) || overlap(s, small[1])) return GDR_ERR_INVALID_ARG;
 
-    Plan p = make_plan(c, log_decay, cu_seqlens, columns(c, false), workspace);
+    Plan p = make_plan(c, log_decay, cu_seqlens, false, workspace);
     const Layout L = layout(c, sums_of(p), false);
     char *ws = (char *)workspace;
     const cudaStream_t s = (cudaStream_t)stream;
@@ -324,7 +340,7 @@ int gdr_linattn_bwd(const gdr_linattn_shape *shape, const void *d_o, const void 
     for (const Span &s : out)
         if (overlap(s, small[0]) || overlap(s, small[1])) return GDR_ERR_INVALID_ARG;
 
-    Plan p = make_plan(c, log_decay, cu_seqlens, columns(c, true), workspace);
+    Plan p = make_plan(c, log_decay, cu_seqlens, true, workspace);
     const Layout L = layout(c, sums_of(p), true);
     char *ws = (char *)workspace;
     const cudaStream_t s = (cudaStream_t)stream;

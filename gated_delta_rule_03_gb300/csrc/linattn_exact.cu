@@ -59,10 +59,10 @@ __global__ void __launch_bounds__(kThreads, 1) mix_exact_kernel(const Plan p, co
     const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
     const int slices = m.dz / NZ;
     const int64_t block = blockIdx.x;
-    const int slice = (int)(block % slices), h = (int)(block / slices % p.H);
-    const int64_t item = block / slices / p.H;
-    bool bad;
-    const Segment s = locate(p, item, kOut ? 0 : 1 + m.backward, &found, &bad);
+    const int slice = (int)(block % slices);
+    const bool bad = !locate(p, block / slices, kOut ? 0 : 1 + m.backward, &found);
+    const Segment s = found;
+    const int h = s.h;
     if (block == 0 && tid == 0 && p.first) p.status[0] = bad ? GDR_ERR_BAD_SEQLENS : GDR_OK;
     if (bad || s.seq < 0) return;
 
@@ -242,7 +242,7 @@ int launch_one(const Plan &p, const Mix &m, cudaStream_t stream) {
     if (cudaFuncSetAttribute(mix_exact_kernel<T, DX, kOut>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              (int)bytes) != cudaSuccess)
         return GDR_ERR_CUDA;
-    const int64_t blocks = (kOut ? p.items : p.handing) * p.H * (m.dz / NZ);
+    const int64_t blocks = (kOut ? p.units : p.handing) * (m.dz / NZ);
     mix_exact_kernel<T, DX, kOut><<<(unsigned)blocks, kThreads, bytes, stream>>>(p, m);
     return cuda_status(cudaGetLastError());
 }

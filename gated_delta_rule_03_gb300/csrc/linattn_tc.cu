@@ -341,13 +341,6 @@ __device__ __forceinline__ void write_state(const float2 (&E)[16], float *p, int
     }
 }
 
-// What a block of either kernel works on.
-struct Work {
-    Segment s;
-    int role, slice, h, chunks;
-    int64_t item;
-};
-
 enum { B_FULL = 0, B_EMPTY = kSlots, B_P = 2 * kSlots, B_PREADY, B_A, B_YREADY, B_U, B_EREADY,
        B_O, B_OFREE, B_STAGED, B_DRAIN, B_COUNT };
 
@@ -361,33 +354,29 @@ __global__ void __launch_bounds__(kThreads, 1) mix_tc_kernel(const __grid_consta
     __shared__ __align__(8) uint64_t bars[B_COUNT];
     __shared__ uint32_t tmem_slot;
     __shared__ int gave_up;
-    __shared__ Work kept;  // (for the end, in no register meanwhile)
+    __shared__ int kept_slice;  // (for the end, in no register meanwhile)
     __shared__ uint2 weights[kWorkers][16];
     __shared__ __align__(16) float step_of[32];  // lam^(31-j), or lam^j from last to first
     __shared__ float pow_of[63];                  // lam^(i-31), 0 for i < 31
     auto bar = [&](int i) { return smem_u32(&bars[i]); };
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
-    Work w;
-    w.role = (int)(blockIdx.x % A.count);
+    const int role = (int)(blockIdx.x % A.count);
     const int64_t rest = blockIdx.x / A.count;
-    w.slice = (int)(rest % A.slices);
-    w.h = (int)(rest / A.slices % A.p.H);
-    w.item = rest / A.slices / A.p.H;
-    bool bad;
-    w.s = locate(A.p, w.item, 0, &found, &bad);
+    const int slice = (int)(rest % A.slices);
+    const bool bad = !locate(A.p, rest / A.slices, 0, &found);
     if (blockIdx.x == 0 && tid == 0 && A.p.first) A.p.status[0] = bad ? GDR_ERR_BAD_SEQLENS : GDR_OK;
-    if (bad || w.s.seq < 0) {
+    if (bad || found.seq < 0) {
         griddep_wait();  // no launch ends before the one ahead of it
         return;
     }
-    const TcMix &m = A.mix[w.role];
+    const TcMix &m = A.mix[role];
     const bool back = m.backward;
-    const float l2_of_head = log2_decay(A.p.log_decay[w.h]);
-    const int chunks = (int)((w.s.tokens + C - 1) / C);
-    const bool ends = m.end && w.s.f == (back ? 0 : w.s.n - 1);
+    const float l2_of_head = log2_decay(A.p.log_decay[found.h]);
+    const int chunks = (int)((found.tokens + C - 1) / C);
+    const bool ends = m.end && found.f == (back ? 0 : found.n - 1);
     auto chunk_of = [&](int cc) { return back ? chunks - 1 - cc : cc; };
-    const int tail = (int)(w.s.tokens - (int64_t)(chunks - 1) * C);  // tokens of the last chunk
+    const int tail = (int)(found.tokens - (int64_t)(chunks - 1) * C);  // tokens of the last chunk
     auto tokens_of = [&](int c) { return c == chunks - 1 ? tail : C; };
     // tile i (X, Y, Z) of chunk cc: its slot, and the phase of the slot's barriers
     auto slot = [&](int cc, int i) { return 3 * (cc & 1) + i; };
@@ -412,7 +401,7 @@ __global__ void __launch_bounds__(kThreads, 1) mix_tc_kernel(const __grid_consta
         mbar_init(bar(B_DRAIN), 1);
         fence_mbar_init();
         gave_up = 0;
-        kept = w;
+        kept_slice = slice;
         prefetch_tensormap(&A.maps[m.mx]);
         prefetch_tensormap(&A.maps[m.my]);
         prefetch_tensormap(&A.maps[m.mz]);
@@ -462,20 +451,20 @@ __global__ void __launch_bounds__(kThreads, 1) mix_tc_kernel(const __grid_consta
         };
 
         // ---- the state: row t, columns col ..
-        const StateAt st = state_row(A, m, w.slice, t, col);
+        const StateAt st = state_row(A, m, slice, t, col);
         const bool mine = t < 64 * m.xb && has_z;
         float2 E[16];
 #pragma unroll
         for (int j = 0; j < 16; ++j) E[j] = make_float2(0.f, 0.f);
-        griddep_wait();  // the segments' sums are there (the loads began before)
+        if (found.n > 1) griddep_wait();  // the segments' sums are there (the loads began before)
         if (mine) {
             if (m.start)
-                read_state(E, m.start + ((int64_t)w.s.seq * A.p.H + w.h) * A.mat, st,
-                           decay_pow(l2, (float)(back ? w.s.behind : (int64_t)w.s.f * A.p.seg)));
+                read_state(E, m.start + ((int64_t)found.seq * A.p.H + found.h) * A.mat, st,
+                           decay_pow(l2, (float)(back ? found.behind : (int64_t)found.f * A.p.seg)));
             if (m.R) {
                 const int part = (int)(A.p.seg / A.p.split);
-                const float *R = m.R + (w.s.item0 * A.p.split * A.p.H + w.h) * A.mat;
-                const int first = back ? (w.s.f + 1) * A.p.split : 0, end = (back ? w.s.n : w.s.f) * A.p.split;
+                const float *R = m.R + (found.item0 * A.p.split * A.p.H + found.h) * A.mat;
+                const int first = back ? (found.f + 1) * A.p.split : 0, end = (back ? found.n : found.f) * A.p.split;
 #pragma unroll 1
                 for (int i = first; i < end; ++i) {
                     const int apart = back ? i - first : end - 1 - i;
@@ -592,7 +581,7 @@ __global__ void __launch_bounds__(kThreads, 1) mix_tc_kernel(const __grid_consta
         // used, and TMA (by rows of their own the stores would take the load/store unit 2000
         // cycles a chunk); what is not a whole tile of bf16, straight to its place
         int pitch = (int)m.out_row * (m.out_f32 ? 4 : 2);
-        char *out0 = (char *)m.out + ((w.s.begin + t) * m.out_row + w.h * m.out_h + w.slice * m.out_s + col) * (m.out_f32 ? 4 : 2);
+        char *out0 = (char *)m.out + ((found.begin + t) * m.out_row + found.h * m.out_h + slice * m.out_s + col) * (m.out_f32 ? 4 : 2);
         auto store_rows = [&](int cc) -> bool {
             const int c = chunk_of(cc), n = tokens_of(c);
             if (!warp_wait(B_O, cc)) return false;
@@ -673,8 +662,8 @@ __global__ void __launch_bounds__(kThreads, 1) mix_tc_kernel(const __grid_consta
             if (need(cc + 1) && !(ok = weigh_chunk(cc + 1))) break;
         }
         if (ends && ok && t < 64 * m.xb && has_z) {
-            const StateAt to = state_row(A, m, kept.slice, t, col);
-            write_state(E, m.end + ((int64_t)kept.s.seq * A.p.H + kept.h) * A.mat + to.first, to.step);
+            const StateAt to = state_row(A, m, kept_slice, t, col);
+            write_state(E, m.end + ((int64_t)found.seq * A.p.H + found.h) * A.mat + to.first, to.step);
         }
     } else if (warp == kLoadWarp) {
         // ------------------------------------------------ the loads, and the outputs' stores
@@ -683,9 +672,9 @@ __global__ void __launch_bounds__(kThreads, 1) mix_tc_kernel(const __grid_consta
             auto load = [&](int cc, int i) {
                 const int to = slot(cc, i);
                 const CUtensorMap *map = &A.maps[i == 0 ? m.mx : (i == 1 ? m.my : m.mz)];
-                const int at = w.slice * (i == 0 ? m.xstep : (i == 1 ? m.ystep : m.zstep));
-                const int head = w.h / (i == 0 ? m.xg : (i == 1 ? m.yg : m.zg));
-                const int blocks = i == 2 ? m.zb : m.xb, t0 = (int)(w.s.begin + (int64_t)chunk_of(cc) * C);
+                const int at = slice * (i == 0 ? m.xstep : (i == 1 ? m.ystep : m.zstep));
+                const int head = found.h / (i == 0 ? m.xg : (i == 1 ? m.yg : m.zg));
+                const int blocks = i == 2 ? m.zb : m.xb, t0 = (int)(found.begin + (int64_t)chunk_of(cc) * C);
                 const uint32_t full = bar(B_FULL + to);
                 mbar_arrive_expect_tx(full, blocks * BLOCK);
                 for (int b = 0; b < blocks; ++b) tma_load_3d(base + to * TILE + b * BLOCK, map, full, at + 64 * b, head, t0);
@@ -693,8 +682,8 @@ __global__ void __launch_bounds__(kThreads, 1) mix_tc_kernel(const __grid_consta
             };
             for (int cc = 0; cc < 2 && cc < chunks; ++cc)
                 for (int i = 0; i < 3; ++i) load(cc, i);
-            const CUtensorMap *out = &A.outs[w.role];
-            const int out_col = m.out_s ? w.slice * (int)m.out_s : 0;
+            const CUtensorMap *out = &A.outs[role];
+            const int out_col = m.out_s ? slice * (int)m.out_s : 0;
             for (int cc = 0; cc < chunks; ++cc) {
                 const bool more = cc + 2 < chunks;
                 if (more) {
@@ -704,8 +693,8 @@ __global__ void __launch_bounds__(kThreads, 1) mix_tc_kernel(const __grid_consta
                 if (!wait(B_STAGED, cc)) break;
                 if (tokens_of(chunk_of(cc)) == C && !m.out_f32) {
                     for (int b = 0; b < m.zb; ++b)
-                        tma_store_3d(out, base + slot(cc, 0) * TILE + b * BLOCK, out_col + 64 * b, w.h,
-                                     (int)(w.s.begin + (int64_t)chunk_of(cc) * C));
+                        tma_store_3d(out, base + slot(cc, 0) * TILE + b * BLOCK, out_col + 64 * b, found.h,
+                                     (int)(found.begin + (int64_t)chunk_of(cc) * C));
                     bulk_commit_group();
                     bulk_wait_group_read<0>();
                 }
@@ -775,6 +764,7 @@ __global__ void __launch_bounds__(kThreads, 1) mix_tc_kernel(const __grid_consta
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    griddep_wait();  // no launch ends before the one ahead of it
     if (warp == 0) tmem_dealloc(tmem, TM_COLS);
 }
 
@@ -799,28 +789,26 @@ __global__ void __launch_bounds__(kSumThreads, 1) sum_tc_kernel(const __grid_con
     __shared__ uint2 weights[kWorkers][16];
     auto bar = [&](int i) { return smem_u32(&bars[i]); };
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    Work w;
-    w.role = (int)(blockIdx.x % A.count);
+    const int role = (int)(blockIdx.x % A.count);
     const int64_t rest = blockIdx.x / A.count;
-    w.slice = (int)(rest % A.slices);
-    w.h = (int)(rest / A.slices % A.p.H);
-    w.item = rest / A.slices / A.p.H;  // of the parts
-    const int part = (int)(w.item % A.p.split);
+    const int slice = (int)(rest % A.slices);
+    const int part = (int)(rest / A.slices / A.p.handing);
     griddep_launch_dependents();
-    bool bad;
-    w.s = locate(A.p, w.item / A.p.split, 1 + A.mix[w.role].backward, &found, &bad);
+    const bool bad = !locate(A.p, rest / A.slices % A.p.handing, 1 + A.mix[role].backward, &found);
+    Segment s = found;
+    const int h = s.h;
     if (blockIdx.x == 0 && tid == 0 && A.p.first) A.p.status[0] = bad ? GDR_ERR_BAD_SEQLENS : GDR_OK;
-    if (bad || w.s.seq < 0) return;
-    const TcMix &m = A.mix[w.role];
+    if (bad || s.seq < 0) return;
+    const TcMix &m = A.mix[role];
     const int64_t part_len = A.p.seg / A.p.split;
-    w.s.begin += part * part_len;
-    w.s.tokens = max((int64_t)0, min(part_len, w.s.tokens - part * part_len));  // (none: a sum of zero)
-    w.item = (w.s.item0 + w.s.f) * A.p.split + part;  // of R
-    const float l2 = log2_decay(A.p.log_decay[w.h]);
-    const int chunks = (int)((w.s.tokens + C - 1) / C);
+    s.begin += part * part_len;
+    s.tokens = max((int64_t)0, min(part_len, s.tokens - part * part_len));  // (none: a sum of zero)
+    const int64_t item = (s.item0 + s.f) * A.p.split + part;
+    const float l2 = log2_decay(A.p.log_decay[h]);
+    const int chunks = (int)((s.tokens + C - 1) / C);
     auto chunk_of = [&](int cc) { return m.backward ? chunks - 1 - cc : cc; };
     auto tokens_of = [&](int c) {
-        const int64_t r = w.s.tokens - (int64_t)c * C;
+        const int64_t r = s.tokens - (int64_t)c * C;
         return (int)(r < C ? r : C);
     };
     if (tid == 0) {
@@ -905,14 +893,14 @@ __global__ void __launch_bounds__(kSumThreads, 1) sum_tc_kernel(const __grid_con
         }
         if (ok && t < 64 * m.xb && has_z)
             {
-            const StateAt st = state_row(A, m, w.slice, t, col);
-            write_state(E, m.R_out + (w.item * A.p.H + w.h) * A.mat + st.first, st.step);
+            const StateAt st = state_row(A, m, slice, t, col);
+            write_state(E, m.R_out + (item * A.p.H + h) * A.mat + st.first, st.step);
         }
     } else if (warp == kLoadWarp) {
         if (lane == 0) {
             int issued = 0;
             for (int cc = 0; cc < chunks; ++cc) {
-                const int t0 = (int)(w.s.begin + (int64_t)chunk_of(cc) * C);
+                const int t0 = (int)(s.begin + (int64_t)chunk_of(cc) * C);
                 bool ok = true;
                 for (int i = 0; i < 2 && ok; ++i) {
                     const int t = 2 * cc + i;
@@ -922,7 +910,7 @@ __global__ void __launch_bounds__(kSumThreads, 1) sum_tc_kernel(const __grid_con
                     mbar_arrive_expect_tx(full, blocks * BLOCK);
                     for (int b = 0; b < blocks; ++b)
                         tma_load_3d(base + slot(t) + b * BLOCK, &A.maps[i ? m.mz : m.my], full,
-                                    w.slice * (i ? m.zstep : m.ystep) + 64 * b, w.h / (i ? m.zg : m.yg), t0);
+                                    slice * (i ? m.zstep : m.ystep) + 64 * b, h / (i ? m.zg : m.yg), t0);
                     ++issued;
                 }
                 if (!ok) break;
@@ -954,11 +942,11 @@ __global__ void __launch_bounds__(kSumThreads, 1) sum_tc_kernel(const __grid_con
 // `after_sums`: may start while the sums' launch ahead of it ends (it waits for it before it
 // reads them).
 template <typename K>
-int run(K kernel, const TcArgs &A, int64_t items, int threads, uint32_t smem, bool after_sums, cudaStream_t stream) {
+int run(K kernel, const TcArgs &A, int64_t units, int threads, uint32_t smem, bool after_sums, cudaStream_t stream) {
     if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
         return GDR_ERR_CUDA;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(items * A.p.H * A.slices * A.count));
+    cfg.gridDim = dim3((unsigned)(units * A.slices * A.count));
     cfg.blockDim = dim3((unsigned)threads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
@@ -1028,7 +1016,7 @@ int launch_mix_tc(const Plan &p, const Mix *mixes, int count, int d_v, bool sums
         m.start = s.start; m.end = s.end; m.R = s.R; m.R_out = s.R_out;
     }
     if (sums) return run(sum_tc_kernel, A, p.handing * p.split, kSumThreads, kSumSmem, false, stream);
-    return run(mix_tc_kernel, A, p.items, kThreads, kSmem, !p.first, stream);
+    return run(mix_tc_kernel, A, p.units, kThreads, kSmem, !p.first, stream);
 }
 
 }  // namespace linattn

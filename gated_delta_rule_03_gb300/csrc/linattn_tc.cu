@@ -669,12 +669,14 @@ __global__ void __launch_bounds__(kThreads, 1) mix_tc_kernel(const __grid_consta
         // ------------------------------------------------ the loads, and the outputs' stores
         if (lane == 0) {
             int issued[3] = {0, 0, 0};
+            const int h = found.h;
+            const int64_t begin = found.begin;
             auto load = [&](int cc, int i) {
                 const int to = slot(cc, i);
                 const CUtensorMap *map = &A.maps[i == 0 ? m.mx : (i == 1 ? m.my : m.mz)];
                 const int at = slice * (i == 0 ? m.xstep : (i == 1 ? m.ystep : m.zstep));
-                const int head = found.h / (i == 0 ? m.xg : (i == 1 ? m.yg : m.zg));
-                const int blocks = i == 2 ? m.zb : m.xb, t0 = (int)(found.begin + (int64_t)chunk_of(cc) * C);
+                const int head = h / (i == 0 ? m.xg : (i == 1 ? m.yg : m.zg));
+                const int blocks = i == 2 ? m.zb : m.xb, t0 = (int)(begin + (int64_t)chunk_of(cc) * C);
                 const uint32_t full = bar(B_FULL + to);
                 mbar_arrive_expect_tx(full, blocks * BLOCK);
                 for (int b = 0; b < blocks; ++b) tma_load_3d(base + to * TILE + b * BLOCK, map, full, at + 64 * b, head, t0);
@@ -693,8 +695,8 @@ __global__ void __launch_bounds__(kThreads, 1) mix_tc_kernel(const __grid_consta
                 if (!wait(B_STAGED, cc)) break;
                 if (tokens_of(chunk_of(cc)) == C && !m.out_f32) {
                     for (int b = 0; b < m.zb; ++b)
-                        tma_store_3d(out, base + slot(cc, 0) * TILE + b * BLOCK, out_col + 64 * b, found.h,
-                                     (int)(found.begin + (int64_t)chunk_of(cc) * C));
+                        tma_store_3d(out, base + slot(cc, 0) * TILE + b * BLOCK, out_col + 64 * b, h,
+                                     (int)(begin + (int64_t)chunk_of(cc) * C));
                     bulk_commit_group();
                     bulk_wait_group_read<0>();
                 }

@@ -474,21 +474,24 @@ struct Sums {
     Sum v[3];
 };
 
-// out[c] = sum over the parts of column c: 32 columns per block, 8 threads each take every
-// eighth part, the eight added in order.
+// out[c] = sum over the parts of column c: 32 columns per block, 32 threads each take every
+// 32nd part, the 32 added in order. Bound by the loads' latency, one behind the other.
+constexpr int kSumRows = 32;
 template <typename T>
-__global__ void __launch_bounds__(256) column_sum_kernel(const Sums s, int parts, int D) {
-    __shared__ float buf[8][33];
+__global__ void __launch_bounds__(32 * kSumRows) column_sum_kernel(const Sums s, int parts, int D) {
+    __shared__ float buf[kSumRows][33];
     const Sum &m = s.v[blockIdx.y];
     const int c = blockIdx.x * 32 + threadIdx.x;
     float t = 0.f;
-    if (c < D)
-        for (int r = threadIdx.y; r < parts; r += 8) t += m.part[(int64_t)r * D + c];
+    if (c < D) {
+#pragma unroll 8
+        for (int r = threadIdx.y; r < parts; r += kSumRows) t += m.part[(int64_t)r * D + c];
+    }
     buf[threadIdx.y][threadIdx.x] = t;
     __syncthreads();
     if (threadIdx.y == 0 && c < D) {
 #pragma unroll
-        for (int r = 1; r < 8; ++r) t += buf[r][threadIdx.x];
+        for (int r = 1; r < kSumRows; ++r) t += buf[r][threadIdx.x];
         if (m.f32) ((float *)m.out)[c] = t;
         else ((T *)m.out)[c] = from_f32<T>(t);
     }
@@ -709,7 +712,7 @@ int gdr_block_norm_bwd(const gdr_block_norm_shape *shape, const void *dx_out, co
     if (dw_pre) sums.v[n++] = {pn, dw_pre, 1};
     if (dgate && shape->gate_rows == 1 && p.gate_stride == 0) sums.v[n++] = {pg, dgate, shape->dtype == GDR_F32};
     if (n == 0) return GDR_OK;
-    const dim3 grid((unsigned)((p.D + 31) / 32), (unsigned)n), block(32, 8);
+    const dim3 grid((unsigned)((p.D + 31) / 32), (unsigned)n), block(32, kSumRows);
     if (shape->dtype == GDR_F32) column_sum_kernel<float><<<grid, block, 0, stm>>>(sums, parts, p.D);
     else column_sum_kernel<__nv_bfloat16><<<grid, block, 0, stm>>>(sums, parts, p.D);
     return cuda_status(cudaGetLastError());

@@ -24,5 +24,6 @@ def __getattr__(name):
     for names, module in ((_OPS, "ops"), (_LINATTN, "linattn"), (_BLOCK_NORM, "block_norm")):
         if name in names:
             from importlib import import_module
-            return getattr(import_module("." + module, __name__), name)
+            globals()[name] = found = getattr(import_module("." + module, __name__), name)
+            return found  # (kept: the next look-up does not come here, 3 us of a small call)
     raise AttributeError(name)

@@ -64,10 +64,11 @@ def _rows(t, name, dtype, device, tokens):
 
 
 def _fields(q, k, v, log_decay, n, scale):
+    """The fields of LinattnShape; n: sequences, None for one per token."""
     if not isinstance(q, torch.Tensor) or q.dtype not in _DTYPES:
         raise TypeError(f"unsupported q: {getattr(q, 'dtype', type(q))}")
     dtype, device = q.dtype, q.device
-    T = len(q) if q.dim() else 0
+    T = q.shape[0] if q.dim() else 0
     qs = _rows(q, "q", dtype, device, T)
     ks = _rows(k, "k", dtype, device, T)
     vs = _rows(v, "v", dtype, device, T)
@@ -79,7 +80,7 @@ def _fields(q, k, v, log_decay, n, scale):
     _need(log_decay, "log_decay", torch.float32, device)
     if log_decay.dim() != 1:
         raise ValueError("log_decay must have shape [H]")
-    return (n, T, log_decay.numel(), q_heads, k_heads, v_heads, d_k, d_v, _DTYPES[dtype], float(scale), qs, ks, vs)
+    return (T if n is None else n, T, log_decay.numel(), q_heads, k_heads, v_heads, d_k, d_v, _DTYPES[dtype], float(scale), qs, ks, vs)
 
 
 def _seqs(cu_seqlens, num_seqs, device):
@@ -194,7 +195,7 @@ def linattn_step(q, k, v, log_decay, S, scale=1.0, o=None, stream=None):
     """The next token of N sequences (gdr_linattn_step): q [N, q_heads, dk], k [N, k_heads,
     dk], v [N, v_heads, dv]; S [N, H, dk, dv] fp32 updated in place. Returns o [N, H, dv]."""
     lib = ops._load()
-    fields = _fields(q, k, v, log_decay, len(q), scale)
+    fields = _fields(q, k, v, log_decay, None, scale)
     dev, (N, H, dk, dv) = q.device, (fields[1], fields[2], fields[6], fields[7])
     if S is None:
         raise TypeError("S must be a torch.Tensor")

@@ -280,7 +280,8 @@ template <typename T, int VEC, int PER> __host__ __device__ constexpr bool fetch
 // Sums over this block's rows go to part[which][blockIdx.x * blockDim.y + threadIdx.y][D]. The
 // next row's inputs are on their way to shared memory while a row is worked on (in registers
 // they would halve the warps, and the instructions per entry, about 45, need the warps).
-// Rows wider than 4096 keep their columns' sums in shared memory instead.
+// Rows wider than 4096 keep their columns' sums in shared memory instead. One gate row for all:
+// with A = the sum over rows of s dx' n, dw_post is act(gate) A and dgate is act'(gate) w_post A.
 template <typename T, typename TX, int VEC, int PER, int THREADS>
 __global__ void __launch_bounds__(THREADS, THREADS > 256 ? 1 : (fetches_ahead<T, VEC, PER>() ? 3 : 2))
 block_norm_bwd_kernel(const NormParams p, const TX *dx_out, const T *dh, const TX *x, const T *y,
@@ -289,13 +290,13 @@ block_norm_bwd_kernel(const NormParams p, const TX *dx_out, const T *dh, const T
     constexpr bool kWide = PER > 8, kAhead = fetches_ahead<T, VEC, PER>();
     __shared__ float buf[96];
     extern __shared__ __align__(16) char dynamic[];
-    float *wide = reinterpret_cast<float *>(dynamic);  // [3][D], each thread its own columns
+    float *wide = reinterpret_cast<float *>(dynamic);  // [2][D], each thread its own columns
     constexpr int kSums = kWide ? 1 : PER / 2;
-    float2 a_post[kSums], a_pre[kSums], a_gate[kSums];
+    float2 a_post[kSums], a_pre[kSums];
 #pragma unroll
-    for (int i = 0; i < kSums; ++i) a_post[i] = a_pre[i] = a_gate[i] = both(0.f);
+    for (int i = 0; i < kSums; ++i) a_post[i] = a_pre[i] = both(0.f);
     if (kWide) {
-        for (int e = threadIdx.x; e < 3 * p.D; e += blockDim.x) wide[e] = 0.f;
+        for (int e = threadIdx.x; e < 2 * p.D; e += blockDim.x) wide[e] = 0.f;
         __syncthreads();
     }
     auto column = [&](int i) { return (threadIdx.x + blockDim.x * (i / VEC)) * VEC + i % VEC; };
@@ -307,6 +308,7 @@ block_norm_bwd_kernel(const NormParams p, const TX *dx_out, const T *dh, const T
             if (column(i + 1) < p.D) wide[which * p.D + column(i + 1)] += x.y;
         }
     };
+    const bool one_gate = gate && !p.gate_stride;
     const int64_t step = (int64_t)gridDim.x * blockDim.y;
     const int64_t rounds = (p.rows + step - 1) / step;  // the same for every thread: barriers inside
     int64_t row = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
@@ -422,26 +424,23 @@ block_norm_bwd_kernel(const NormParams p, const TX *dx_out, const T *dh, const T
             for (int i = 0; i < PER; i += 2) {
                 float2 a, da;
                 gate_both(p.act, gr.two(i), a, da);
-                const float2 dz = mul2(both(p.s), dv[i / 2]);
-                dg[i / 2] = mul2(mul2(dz, da), mul2(mul2(yr.two(i), both(r)), wt[i / 2]));
+                const float2 dz = mul2(both(p.s), dv[i / 2]), n = mul2(yr.two(i), both(r));
+                dg[i / 2] = mul2(mul2(dz, da), mul2(n, wt[i / 2]));
                 dv[i / 2] = mul2(dz, a);
+                add(a_post, 0, i, mul2(one_gate ? dz : dv[i / 2], n));
             }
-            if (p.gate_stride) {
-                if (dgate) store_row<T, VEC>(dgate + at, D, reinterpret_cast<const float(&)[PER]>(dg));
-            } else if (part_gate) {
-#pragma unroll
-                for (int i = 0; i < PER; i += 2) add(a_gate, 2, i, dg[i / 2]);
-            }
+            if (p.gate_stride && dgate) store_row<T, VEC>(dgate + at, D, reinterpret_cast<const float(&)[PER]>(dg));
         } else {
 #pragma unroll
-            for (int i = 0; i < PER; i += 2) dv[i / 2] = mul2(both(p.s), dv[i / 2]);
+            for (int i = 0; i < PER; i += 2) {
+                dv[i / 2] = mul2(both(p.s), dv[i / 2]);
+                add(a_post, 0, i, mul2(dv[i / 2], mul2(yr.two(i), both(r))));
+            }
         }
 #pragma unroll
         for (int i = 0; i < PER; i += 2) {
-            const float2 yv = yr.two(i);
-            add(a_post, 0, i, mul2(dv[i / 2], mul2(yv, both(r))));
             dv[i / 2] = mul2(dv[i / 2], wt[i / 2]);
-            yd = fma2(dv[i / 2], yv, yd);
+            yd = fma2(dv[i / 2], yr.two(i), yd);
         }
         if (p.post) {
             float dot[1] = {yd.x + yd.y};
@@ -453,15 +452,41 @@ block_norm_bwd_kernel(const NormParams p, const TX *dx_out, const T *dh, const T
         store_row<T, VEC>(dy + at, D, reinterpret_cast<const float(&)[PER]>(dv));
     }
     const int64_t mine = ((int64_t)blockIdx.x * blockDim.y + threadIdx.y) * p.D;
+    const float *w_end = p.post ? p.w_post : nullptr;
     if constexpr (kWide) {
         __syncthreads();
-        float *const part[3] = {part_post, part_pre, part_gate};
-        for (int i = 0; i < 3; ++i)
-            for (int e = threadIdx.x; part[i] && e < p.D; e += blockDim.x) part[i][mine + e] = wide[i * p.D + e];
+        for (int e = threadIdx.x; e < p.D; e += blockDim.x) {
+            float2 a = both(1.f), da = a;
+            if (one_gate) gate_both(p.act, both((float)gate[e]), a, da);
+            if (part_post) part_post[mine + e] = wide[e] * a.x;
+            if (part_pre) part_pre[mine + e] = wide[p.D + e];
+            if (part_gate) part_gate[mine + e] = wide[e] * (w_end ? w_end[e] : 1.f) * da.x;
+        }
     } else {
-        if (part_post) store_row<float, VEC>(part_post + mine, p.D, reinterpret_cast<const float(&)[PER]>(a_post));
         if (part_pre) store_row<float, VEC>(part_pre + mine, p.D, reinterpret_cast<const float(&)[PER]>(a_pre));
-        if (part_gate) store_row<float, VEC>(part_gate + mine, p.D, reinterpret_cast<const float(&)[PER]>(a_gate));
+        if (one_gate) {
+            Raw<T, VEC, PER> gr;
+            gr.load(gate, p.D);
+            float2 a_gate[kSums];
+#pragma unroll
+            for (int j = 0; j < PER / VEC; ++j) {
+                const Weight<VEC> w = weight_of<VEC>(w_end, j, p.D);
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) {
+                    const int i = j * VEC + e;
+                    (i & 1 ? a_gate[i / 2].y : a_gate[i / 2].x) = w.v[e];
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < PER; i += 2) {
+                float2 a, da;
+                gate_both(p.act, gr.two(i), a, da);
+                a_gate[i / 2] = mul2(mul2(a_post[i / 2], a_gate[i / 2]), da);
+                a_post[i / 2] = mul2(a_post[i / 2], a);
+            }
+            if (part_gate) store_row<float, VEC>(part_gate + mine, p.D, reinterpret_cast<const float(&)[PER]>(a_gate));
+        }
+        if (part_post) store_row<float, VEC>(part_post + mine, p.D, reinterpret_cast<const float(&)[PER]>(a_post));
     }
 }
 
@@ -534,7 +559,7 @@ template <typename T, typename TX> struct Run {
                    const void *x, const void *y, const void *gate, void *dx, void *dy, void *dgate,
                    float *pp, float *pn, float *pg, cudaStream_t stream) {
         const int threads = (int)(s.block.x * s.block.y);
-        const size_t bytes = PER > 8 ? 3 * (size_t)p.D * sizeof(float)
+        const size_t bytes = PER > 8 ? 2 * (size_t)p.D * sizeof(float)
                              : (fetches_ahead<T, VEC, PER>() ? 2 * (size_t)row_bytes<T, TX, PER>() * threads : 0);
         auto kernel = PER > 8 || threads > 256 ? block_norm_bwd_kernel<T, TX, VEC, PER, 512>
                                                : block_norm_bwd_kernel<T, TX, VEC, PER, (PER > 8 ? 512 : 256)>;

@@ -27,7 +27,8 @@
 //   first to last:  lam^(f seg) S0 + sum_{g<f} lam^((f-1-g) seg) R_g
 //   last to first:  lam^(tokens behind f) dS_final + sum_{g>f} lam^((g-1-f) seg) R_g
 // and all segments run at once. With one segment per sequence the first launch is left out.
-// Where the sums alone would leave SMs idle, they are taken over parts of a segment.
+// Where the sums alone would leave SMs idle, they are taken over parts of a segment. Of equal
+// sequences only those may be cut that whole rounds of the SMs leave over.
 #pragma once
 
 #include "internal.h"
@@ -85,8 +86,9 @@ struct Segment {
 // What unit `unit` of a launch is, a segment and a head: all of them, or (`handing` 1 or 2)
 // those that hand a sum on, all of a sequence but its last (1) or its first (2). Equal
 // lengths: first the pairs that stay whole, then the segments one after the other. Called
-// by the whole block (a barrier inside). With cu_seqlens every block checks all of it (offsets from 0, not decreasing, at most
-// total_tokens); where it is not so, no block does anything: false.
+// by the whole block (a barrier inside). With cu_seqlens every block checks all of it (offsets
+// from 0, not decreasing, at most total_tokens); where it is not so, no block does anything:
+// false.
 __device__ __forceinline__ bool locate(const Plan &p, int64_t unit, int handing, Segment *shared) {
     const int skip = handing == 2;  // segments in front of the first item's
     const int less = handing != 0;

@@ -65,15 +65,17 @@ int columns(const Call &c, bool backward) {
     return backward ? c.dk / 64 : c.dv / 64;
 }
 
-// How sequences are cut, by a model of the time in microseconds: a launch takes rounds of 152 blocks. Tensor cores: a tile of 128 tokens takes 2.5 us
-// in a mix and 1.2 in a sum, a block 8 to start and end, and reads a sum in 1; the second
-// launch costs 4. fp32 arithmetic: tiles of 64 tokens, 9 and 4 us, 3 to start, 2 a sum.
-// Blocks of different lengths filling up an SM take 1.2 times their sum, and half a block's
-// time is lost at the end. (4 x 4096 x 16 heads: 1, 2, 3, 4 segments 92, 89, 105, 111 us; 65536
-// x 16 chains: 5, 7, 9, 10 segments 411, 313, 263, 368 us. Eight packed sequences, 40,000
-// tokens, 16 heads, segments of 24 and of 72 tiles: all equal 192 and 143 us, the longest 1.6
-// times the mean 237 and 187, twice 234 and 230, 4 times 191 and 257; with 4 heads 11 tiles 82
-// us, 72 tiles 171.)
+// How sequences are cut, by a model of the time in microseconds: a launch takes rounds of 152
+// blocks. Tensor cores: a tile of 128 tokens takes 2.5 us in a mix and 1.2 in a sum, a block 8 to
+// start and end, and reads a sum in 1; the second launch costs 4. fp32 arithmetic: tiles of 64
+// tokens, 9 and 4 us, 3 to start, 2 a sum. Blocks of different lengths filling up an SM take
+// 1.2 times their sum, and half a block's time is lost at the end. Measured:
+//   4 x 4096 x 16 heads: 1, 2, 3, 4 segments 92, 89, 105, 111 us
+//   65536 x 16 chains: 5, 7, 9, 10 segments 411, 313, 263, 368 us
+//   192 chains of 4096 (a backward call): all whole 179 us, 150 of them whole and 42 in three 150
+//   eight packed sequences, 40,000 tokens, 16 heads, segments of 24 and of 72 tiles: all equal 192
+//   and 143 us, the longest 1.6 times the mean 237 and 187, twice 234 and 230, 4 times 191 and
+//   257; with 4 heads 11 tiles 82 us, 72 tiles 171
 struct Cost {
     int tile;
     double mix, sum, start, read;

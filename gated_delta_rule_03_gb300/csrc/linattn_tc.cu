@@ -34,6 +34,11 @@
 // the next chunk. Warp 16: the loads. With 96 registers a thread nothing may spill (shared
 // memory leaves no first-level cache to spill to): hence 16 columns at a time, and
 // what would be worked out ahead of the loop made opaque.
+//
+// Measured: 4 sequences of 4096 tokens, 16 heads, d_k = d_v = 128 (273 MB, two segments each)
+// in 83 us with the sums, 3.3 TB/s: a chunk takes 2.5 us, the chain of its products and what lies
+// between them, with the tensor cores busy 37 % of the time and the schedulers 46 %. Where all
+// 152 SMs run and every tile comes from DRAM (128 KB a chunk) memory bounds it: 2.9 us.
 #include "linattn.cuh"
 #include "tc_common.cuh"
 
@@ -780,7 +785,8 @@ enum { S_FULL = 0, S_EMPTY = kSlots, S_READY = 2 * kSlots, S_U = S_READY + 2,
 
 // R_f of every segment but the last from the side that the state comes from: U chunk by
 // chunk as in the mix, with two buffers each of U and Yw, so that a chunk is weighed while
-// the products of the one before it run. Bound by reading Y and Z.
+// the products of the one before it run. 1.2 us a chunk: bound by reading Y and Z, 64 KB, where
+// all SMs run.
 __global__ void __launch_bounds__(kSumThreads, 1) sum_tc_kernel(const __grid_constant__ TcArgs A) {
     extern __shared__ __align__(1024) unsigned char sm[];
     const uint32_t base = smem_u32(sm);

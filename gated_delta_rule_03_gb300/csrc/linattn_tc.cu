@@ -271,9 +271,9 @@ __device__ __forceinline__ void add_update(float2 (&E)[16], float w, uint32_t ta
         E[j] = fma2(w2, E[j], make_float2(__uint_as_float(u[j >> 3][2 * j & 15]), __uint_as_float(u[j >> 3][(2 * j & 15) + 1])));
 }
 
-// Four lanes that hold 32 words each of a row of their own (8 words per part): afterwards part
+// Four lanes that hold 16 words each of a row of their own (4 words per part): afterwards part
 // i of lane q is part q of lane i's row.
-__device__ __forceinline__ void turn_four(float (&p)[32], int lane) {
+__device__ __forceinline__ void turn_four(float (&p)[16], int lane) {
 #pragma unroll
     for (int step = 1; step < 4; step *= 2) {
         const bool up = lane & step;
@@ -281,12 +281,12 @@ __device__ __forceinline__ void turn_four(float (&p)[32], int lane) {
         for (int i = 0; i < 4; ++i) {
             if (i & step) continue;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
+            for (int e = 0; e < 4; ++e) {
                 // the lower lane sends its part i + step, the upper one its part i
-                const float mine = up ? p[8 * i + e] : p[8 * (i + step) + e];
+                const float mine = up ? p[4 * i + e] : p[4 * (i + step) + e];
                 const float other = __shfl_xor_sync(0xffffffffu, mine, step);
-                if (up) p[8 * i + e] = other;
-                else p[8 * (i + step) + e] = other;
+                if (up) p[4 * i + e] = other;
+                else p[4 * (i + step) + e] = other;
             }
         }
     }
@@ -604,21 +604,21 @@ __global__ void __launch_bounds__(kThreads, 1) mix_tc_kernel(const __grid_consta
             unsigned char *row = sm + slot(cc, 0) * TILE + (sub >> 1) * BLOCK + t * 128;
             char *to = out0 + (int64_t)c * C * pitch;
             if (m.out_f32) {
-                // four rows at a time, 32 bytes of one per lane
-                float p[32];
-#pragma unroll
-                for (int j = 0; j < 32; ++j) p[j] = wo * __uint_as_float(o[j >> 4][j & 15]);
-                turn_four(p, lane);
+                // four rows at a time, 16 bytes of one per lane: whole sectors of 32
                 const int live = has_z ? n - (t & ~3) : 0;  // rows of the four to be written
-                char *at = to + (32 - pitch) * (lane & 3);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    if (i < live) {
-                        *reinterpret_cast<float4 *>(at) = make_float4(p[8 * i], p[8 * i + 1], p[8 * i + 2], p[8 * i + 3]);
-                        *reinterpret_cast<float4 *>(at + 16) =
-                            make_float4(p[8 * i + 4], p[8 * i + 5], p[8 * i + 6], p[8 * i + 7]);
+                for (int half = 0; half < 2; ++half) {
+                    float p[16];
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) p[j] = wo * __uint_as_float(o[half][j]);
+                    turn_four(p, lane);
+                    char *at = to + (16 - pitch) * (lane & 3) + 64 * half;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        if (i < live)
+                            *reinterpret_cast<float4 *>(at) = make_float4(p[4 * i], p[4 * i + 1], p[4 * i + 2], p[4 * i + 3]);
+                        at += pitch;
                     }
-                    at += pitch;
                 }
             } else {
 #pragma unroll

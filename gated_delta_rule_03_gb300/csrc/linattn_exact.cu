@@ -268,11 +268,11 @@ template <typename T> __global__ void __launch_bounds__(256) share_kernel(const 
     const Share &m = shares.v[blockIdx.y];
     if (p.status[0] != GDR_OK) return;
     const int64_t rows = p.cu_seqlens ? p.cu_seqlens[p.num_seqs] : p.total_tokens;
-    const int quads = m.d / 4;
-    const int64_t total = rows * m.heads * quads;
+    const int shift = 29 - __clz(m.d);  // d / 4 quads, a power of two
+    const int64_t total = rows * m.heads << shift;
     for (int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x; e < total; e += (int64_t)gridDim.x * 256) {
-        const int j = (int)(e % quads) * 4;
-        const int64_t rh = e / quads;  // row * heads + head: its g parts are in[rh g ..]
+        const int j = (int)(e & ((1 << shift) - 1)) * 4;
+        const int64_t rh = e >> shift;  // row * heads + head: its g parts are in[rh g ..]
         const float *in = m.in + rh * m.g * m.d + j;
         float4 sum = load4(in);
         for (int i = 1; i < m.g; ++i) fma4(sum, 1.f, load4(in + i * m.d));

@@ -39,6 +39,8 @@
 // in 83 us with the sums, 3.3 TB/s: a chunk takes 2.5 us, the chain of its products and what lies
 // between them, with the tensor cores busy 37 % of the time and the schedulers 46 %. Where all
 // 152 SMs run and every tile comes from DRAM (128 KB a chunk) memory bounds it: 2.9 us.
+#include <mutex>
+
 #include "linattn.cuh"
 #include "tc_common.cuh"
 
@@ -947,6 +949,27 @@ __global__ void __launch_bounds__(kSumThreads, 1) sum_tc_kernel(const __grid_con
     if (warp == 0) tmem_dealloc(tmem, TM_COLS);
 }
 
+// Tensor map over a [T, heads, d] bf16 tensor whose tokens are `stride` elements apart, with
+// 64 (features) x 1 (head) x 128 (tokens) boxes, 128-byte swizzle; 256 bytes of L2 at a time.
+bool make_map_rows(CUtensorMap *map, const void *base, int d, int heads, int64_t stride, int64_t T) {
+    static decltype(&cuTensorMapEncodeTiled) encode = nullptr;
+    static std::once_flag once;
+    std::call_once(once, [] {
+        cudaDriverEntryPointQueryResult found;
+        void *f = nullptr;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &found) == cudaSuccess &&
+            found == cudaDriverEntryPointSuccess)
+            encode = reinterpret_cast<decltype(encode)>(f);
+    });
+    if (!encode) return false;
+    const cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)heads, (cuuint64_t)T};
+    const cuuint64_t strides[2] = {(cuuint64_t)d * 2, (cuuint64_t)stride * 2};
+    const cuuint32_t box[3] = {64, 1, 128}, each[3] = {1, 1, 1};
+    return encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides, box, each,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // `after_sums`: may start while the sums' launch ahead of it ends (it waits for it before it
 // reads them).
 template <typename K>
@@ -992,7 +1015,7 @@ int launch_mix_tc(const Plan &p, const Mix *mixes, int count, int d_v, bool sums
         if (n == 4) return false;
         *at = n;
         have[n] = {base, stride, group, d};
-        return tc::make_map_rows(&A.maps[n++], base, d, p.H / group, stride, p.total_tokens);
+        return make_map_rows(&A.maps[n++], base, d, p.H / group, stride, p.total_tokens);
     };
     for (int i = 0; i < count; ++i) {
         const Mix &s = mixes[i];
@@ -1008,7 +1031,7 @@ int launch_mix_tc(const Plan &p, const Mix *mixes, int count, int d_v, bool sums
         m.zstep = m.bstep = s.dz > 128 ? 128 : 0;
         m.out = s.out;
         m.out_f32 = s.out_f32;
-        if (!sums && !s.out_f32 && !tc::make_map_rows(&A.outs[i], s.out, s.dz, p.H, (int64_t)p.H * s.dz, p.total_tokens))
+        if (!sums && !s.out_f32 && !make_map_rows(&A.outs[i], s.out, s.dz, p.H, (int64_t)p.H * s.dz, p.total_tokens))
             return GDR_ERR_CUDA;
         // slices of z lie side by side; of x they are sums of their own
         const int parts = s.dx > 128 ? A.slices : 1;

@@ -78,9 +78,6 @@ __device__ __forceinline__ ChunkScan chunk_scan(float a0, float a1, int lane) {
 // Tensor map over a packed [T, H, d] bf16 tensor with 64 (features) x 1 (head) x 64
 // (tokens) boxes, 128-byte swizzle.
 bool make_map_thd(CUtensorMap *map, const void *base, int d, int H, int64_t T);
-// Tensor map over a [T, heads, d] bf16 tensor whose tokens are `stride` elements apart, with
-// 64 (features) x 1 (head) x 128 (tokens) boxes, 128-byte swizzle.
-bool make_map_rows(CUtensorMap *map, const void *base, int d, int heads, int64_t stride, int64_t T);
 // Tensor map over [units][64][64] bf16 matrices, one whole matrix per box, 128-byte swizzle.
 bool make_map_units(CUtensorMap *map, const void *base, int64_t units);
 // Tensor map over a packed [T, H, d] fp32 tensor with d (features) x 1 (head) x 64 (tokens)

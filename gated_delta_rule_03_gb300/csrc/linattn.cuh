@@ -63,10 +63,10 @@ struct Plan {
     int64_t seq_len;            // equal lengths
     int segs;                   // segments per sequence (equal lengths) ..
     int64_t whole;              // .. of all but the first `whole` (sequence, head) pairs: they stay whole
-    int64_t items;              // segments of all sequences (packed: an upper bound)
-    int64_t units, handing;     // (segment, head) pairs, and those that hand a sum on (packed: likewise)
+    int64_t sums;               // segments that hand a sum on, those of whole pairs too (packed: a bound)
+    int64_t units, handing;     // (segment, head) pairs, and those that hand a sum on (packed: bounds)
     int split;                  // parts of a segment that are summed by themselves (each seg / split
-                                // tokens): R has [item, split, H] matrices
+                                // tokens): R has [sums, split, H] matrices
     int H;
     const float *log_decay;
     int32_t *status;            // the workspace's status word
@@ -79,7 +79,7 @@ struct Segment {
     int64_t begin;  // first token of the segment
     int64_t tokens; // its tokens
     int64_t behind; // tokens of the sequence behind it
-    int64_t item0;  // the sequence's first item
+    int64_t sum0;   // its sequence's first sum in R: one per segment but the last (or the first)
     int h;          // head
 };
 
@@ -92,7 +92,7 @@ struct Segment {
 __device__ __forceinline__ bool locate(const Plan &p, int64_t unit, int handing, Segment *shared) {
     const int skip = handing == 2;  // segments in front of the first item's
     const int less = handing != 0;
-    auto fill = [&](int seq, int h, int f, int n, int64_t first, int64_t len, int64_t item0) {
+    auto fill = [&](int seq, int h, int f, int n, int64_t first, int64_t len, int64_t sum0) {
         Segment s;
         s.seq = seq;
         s.f = f;
@@ -101,7 +101,7 @@ __device__ __forceinline__ bool locate(const Plan &p, int64_t unit, int handing,
         const int64_t rest = len - (int64_t)f * p.seg;
         s.tokens = n == 1 || rest < p.seg ? rest : p.seg;
         s.behind = rest - s.tokens;
-        s.item0 = item0;
+        s.sum0 = sum0;
         s.h = h;
         *shared = s;
     };
@@ -115,7 +115,7 @@ __device__ __forceinline__ bool locate(const Plan &p, int64_t unit, int handing,
             n = p.segs;
         }
         const int64_t seq = pair / p.H;
-        if (threadIdx.x == 0) fill((int)seq, (int)(pair % p.H), f, n, seq * p.seq_len, p.seq_len, seq * p.segs);
+        if (threadIdx.x == 0) fill((int)seq, (int)(pair % p.H), f, n, seq * p.seq_len, p.seq_len, seq * (p.segs - 1));
         __syncthreads();
         return true;
     }
@@ -154,7 +154,7 @@ __device__ __forceinline__ bool locate(const Plan &p, int64_t unit, int handing,
         }
         const int64_t first_item = carry + before + sum - count;
         if (count > 0 && item >= first_item && item < first_item + count)
-            fill((int)n, (int)(unit % p.H), (int)(item - first_item) + skip, (int)count + less, a, len, first_item + n * less);
+            fill((int)n, (int)(unit % p.H), (int)(item - first_item) + skip, (int)count + less, a, len, first_item - (less ? 0 : n));
         carry += total;
         __syncthreads();
     }

@@ -115,7 +115,9 @@ Cut cut(const Call &c, bool packed, bool backward) {
     double best_cost = 1e300;
     // Pairs of equal lengths that fill whole rounds may stay whole, and only the rest is cut.
     const int64_t full = packed || pairs * cols < sms ? 0 : (int64_t)sms * (pairs * cols / (int64_t)sms) / cols;
-    for (int64_t n = 1; n <= m && n <= 256; ++n) {
+    // Segments per sequence: each count up to 16, then in steps of an eighth, and those that
+    // fill one to four rounds.
+    auto consider = [&](int64_t n) {
         const int64_t len = (m + n - 1) / n, segs = (m + len - 1) / len;
         for (int64_t whole : {(int64_t)0, full}) {
             if (whole && (n == 1 || whole == pairs)) break;
@@ -138,6 +140,11 @@ Cut cut(const Call &c, bool packed, bool backward) {
                 }
             }
         }
+    };
+    for (int64_t n = 1; n <= m && n <= 256; n += n < 16 ? 1 : n / 8) consider(n);
+    for (int64_t r = 1; r <= 4; ++r) {
+        const int64_t n = r * (int64_t)sms / (pairs * cols);
+        if (n > 16 && n <= m && n <= 256) consider(n);
     }
     if (packed && best.seg == m && m < tiles && tc) best.split = 4;
     best.seg *= k.tile;
@@ -156,15 +163,15 @@ Plan make_plan(const Call &c, const float *log_decay, const int32_t *cu, bool ba
     p.seg = at.seg;
     p.split = at.split;
     if (cu) {
-        p.items = c.T / p.seg + c.N;
-        p.units = p.items * c.H;
-        p.handing = c.T / p.seg * c.H;
+        p.sums = c.T / p.seg;
+        p.handing = p.sums * c.H;
+        p.units = p.handing + c.N * c.H;
     } else {
         p.seq_len = c.T / c.N;
         p.segs = (int)((p.seq_len + p.seg - 1) / p.seg);
         if (p.segs < 1) p.segs = 1;
         p.whole = p.segs > 1 ? at.whole : 0;
-        p.items = c.N * p.segs;
+        p.sums = c.N * (p.segs - 1);
         p.handing = (c.N * c.H - p.whole) * (p.segs - 1);
         p.units = c.N * c.H + p.handing;
     }
@@ -201,16 +208,22 @@ Layout layout(const Call &c, int64_t sums_each, bool backward) {
     L.total = off;
     return L;
 }
-int64_t sums_of(const Plan &p) { return segmented(p) ? p.items * p.split : 0; }
-// The larger of what equal and packed lengths take.
-size_t workspace_bytes_for(const Call &c, bool backward) {
+int64_t sums_of(const Plan &p) { return segmented(p) ? p.sums * p.split : 0; }
+// What a call needs, the larger of what equal and packed lengths take; its plan in *p.
+size_t plan_call(const Call &c, bool backward, const float *log_decay, const int32_t *cu, void *ws, Plan *p) {
     static const int32_t some = 0;
-    int64_t sums = sums_of(make_plan(c, nullptr, &some, backward, nullptr));
-    if (c.T % c.N == 0) {
-        const int64_t equal = sums_of(make_plan(c, nullptr, nullptr, backward, nullptr));
-        if (equal > sums) sums = equal;
+    *p = make_plan(c, log_decay, cu, backward, ws);
+    int64_t sums = sums_of(*p);
+    if (!cu || c.T % c.N == 0) {
+        const int64_t other = sums_of(make_plan(c, log_decay, cu ? nullptr : &some, backward, ws));
+        if (other > sums) sums = other;
     }
     return layout(c, sums, backward).total;
+}
+size_t workspace_bytes_for(const Call &c, bool backward) {
+    static const int32_t some = 0;
+    Plan p;
+    return plan_call(c, backward, nullptr, &some, nullptr, &p);
 }
 
 struct Span {
@@ -284,7 +297,8 @@ int gdr_linattn_fwd(const gdr_linattn_shape *shape, const void *q, const void *k
     if (!workspace) return GDR_ERR_WORKSPACE;
     if (!log_decay || (c.T > 0 && (!q || !k || !v || !o))) return GDR_ERR_INVALID_ARG;
     if (((uintptr_t)log_decay | (uintptr_t)cu_seqlens) & 3u) return GDR_ERR_ALIGNMENT;
-    const size_t need = workspace_bytes_for(c, false);
+    Plan p;
+    const size_t need = plan_call(c, false, log_decay, cu_seqlens, workspace, &p);
     if (workspace_bytes < need) return GDR_ERR_WORKSPACE;
     const Span in[] = {rows(q, c, c.qs, c.qh, c.dk), rows(k, c, c.ks, c.kh, c.dk),
                        rows(v, c, c.vs, c.vh, c.dv), {S0 == S_final ? nullptr : S0, c.state()}};
@@ -294,7 +308,6 @@ int gdr_linattn_fwd(const gdr_linattn_shape *shape, const void *q, const void *k
     for (const Span &s : out)
         if (overlap(s, small[0]) || overlap(s, small[1])) return GDR_ERR_INVALID_ARG;
 
-    Plan p = make_plan(c, log_decay, cu_seqlens, false, workspace);
     const Layout L = layout(c, sums_of(p), false);
     char *ws = (char *)workspace;
     const cudaStream_t s = (cudaStream_t)stream;
@@ -330,7 +343,8 @@ int gdr_linattn_bwd(const gdr_linattn_shape *shape, const void *d_o, const void 
     if (!workspace) return GDR_ERR_WORKSPACE;
     if (!log_decay || (c.T > 0 && (!d_o || !q || !k || !v || !dq || !dk || !dv))) return GDR_ERR_INVALID_ARG;
     if (((uintptr_t)log_decay | (uintptr_t)cu_seqlens) & 3u) return GDR_ERR_ALIGNMENT;
-    const size_t need = workspace_bytes_for(c, true);
+    Plan p;
+    const size_t need = plan_call(c, true, log_decay, cu_seqlens, workspace, &p);
     if (workspace_bytes < need) return GDR_ERR_WORKSPACE;
     const int64_t os = (int64_t)c.H * c.dv;
     const Span in[] = {rows(q, c, c.qs, c.qh, c.dk), rows(k, c, c.ks, c.kh, c.dk), rows(v, c, c.vs, c.vh, c.dv),
@@ -342,7 +356,6 @@ int gdr_linattn_bwd(const gdr_linattn_shape *shape, const void *d_o, const void 
     for (const Span &s : out)
         if (overlap(s, small[0]) || overlap(s, small[1])) return GDR_ERR_INVALID_ARG;
 
-    Plan p = make_plan(c, log_decay, cu_seqlens, true, workspace);
     const Layout L = layout(c, sums_of(p), true);
     char *ws = (char *)workspace;
     const cudaStream_t s = (cudaStream_t)stream;

@@ -94,9 +94,9 @@ __global__ void __launch_bounds__(kThreads, 1) mix_exact_kernel(const Plan p, co
             const int64_t dist = m.backward ? s.behind : (int64_t)s.f * p.seg;
             add_state(m.start + ((int64_t)s.seq * p.H + h) * mat, decay_pow(l2, (float)dist));
         }
-        for (int g = m.backward ? s.f + 1 : 0; m.R && g < (m.backward ? s.n : s.f); ++g) {
-            const int apart = m.backward ? g - 1 - s.f : s.f - 1 - g;
-            add_state(m.R + ((s.item0 + g) * p.H + h) * mat, decay_pow(l2, (float)(apart * p.seg)));
+        for (int g = m.backward ? s.f : 0; m.R && g < (m.backward ? s.n - 1 : s.f); ++g) {
+            const int apart = m.backward ? g - s.f : s.f - 1 - g;
+            add_state(m.R + ((s.sum0 + g) * p.H + h) * mat, decay_pow(l2, (float)(apart * p.seg)));
         }
     }
 
@@ -222,7 +222,7 @@ __global__ void __launch_bounds__(kThreads, 1) mix_exact_kernel(const Plan p, co
     }
 
     float *to = nullptr;
-    if (!kOut) to = m.R_out + ((s.item0 + s.f) * p.H + h) * mat;
+    if (!kOut) to = m.R_out + ((s.sum0 + s.f - m.backward) * p.H + h) * mat;
     else if (m.end && s.f == (m.backward ? 0 : s.n - 1)) to = m.end + ((int64_t)s.seq * p.H + h) * mat;
     if (!to) return;
 #pragma unroll

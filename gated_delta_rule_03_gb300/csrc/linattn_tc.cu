@@ -470,8 +470,8 @@ __global__ void __launch_bounds__(kThreads, 1) mix_tc_kernel(const __grid_consta
                            decay_pow(l2, (float)(back ? found.behind : (int64_t)found.f * A.p.seg)));
             if (m.R) {
                 const int part = (int)(A.p.seg / A.p.split);
-                const float *R = m.R + (found.item0 * A.p.split * A.p.H + found.h) * A.mat;
-                const int first = back ? (found.f + 1) * A.p.split : 0, end = (back ? found.n : found.f) * A.p.split;
+                const float *R = m.R + (found.sum0 * A.p.split * A.p.H + found.h) * A.mat;
+                const int first = back ? found.f * A.p.split : 0, end = (back ? found.n - 1 : found.f) * A.p.split;
 #pragma unroll 1
                 for (int i = first; i < end; ++i) {
                     const int apart = back ? i - first : end - 1 - i;
@@ -813,7 +813,7 @@ __global__ void __launch_bounds__(kSumThreads, 1) sum_tc_kernel(const __grid_con
     const int64_t part_len = A.p.seg / A.p.split;
     s.begin += part * part_len;
     s.tokens = max((int64_t)0, min(part_len, s.tokens - part * part_len));  // (none: a sum of zero)
-    const int64_t item = (s.item0 + s.f) * A.p.split + part;
+    const int64_t sum = (s.sum0 + s.f - m.backward) * A.p.split + part;
     const float l2 = log2_decay(A.p.log_decay[h]);
     const int chunks = (int)((s.tokens + C - 1) / C);
     auto chunk_of = [&](int cc) { return m.backward ? chunks - 1 - cc : cc; };
@@ -879,7 +879,7 @@ __global__ void __launch_bounds__(kSumThreads, 1) sum_tc_kernel(const __grid_con
             if (cc < chunks) {
                 const int n = tokens_of(chunk_of(cc)), ty = 2 * cc, tz = ty + 1;
                 if (n != weighed) row_weights(weights[warp], weighed = n, m.backward, l2, m.s_state, sub, lane);
-                    if (!(ok = warp_wait(S_FULL + ty % kSlots, ty / kSlots))) break;
+                if (!(ok = warp_wait(S_FULL + ty % kSlots, ty / kSlots))) break;
                 if (n < C) {
                     if (!(ok = warp_wait(S_FULL + tz % kSlots, tz / kSlots))) break;
                     clear_behind(sm + slot(tz), m.zb, n, tid);
@@ -901,10 +901,9 @@ __global__ void __launch_bounds__(kSumThreads, 1) sum_tc_kernel(const __grid_con
             tc_fence_before();
             arrive(S_UFREE + (b & 1));
         }
-        if (ok && t < 64 * m.xb && has_z)
-            {
+        if (ok && t < 64 * m.xb && has_z) {
             const StateAt st = state_row(A, m, slice, t, col);
-            write_state(E, m.R_out + (item * A.p.H + h) * A.mat + st.first, st.step);
+            write_state(E, m.R_out + (sum * A.p.H + h) * A.mat + st.first, st.step);
         }
     } else if (warp == kLoadWarp) {
         if (lane == 0) {

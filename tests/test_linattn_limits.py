@@ -55,6 +55,17 @@ def test_cut_sequences(case, dtype):
 
 @gpu
 @pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
+def test_more_sequences_than_a_block_has_threads(dtype):
+    """The offsets are scanned a block's width at a time; one sequence behind the first
+    width is cut."""
+    c = make([1, 0, 2] * 230 + [2100] + [3, 1] * 60, 1, 1, 1, 1, 64, 64, dtype, "retention", s0=True, behind=3, seed=11)
+    assert len(c["lens"]) > 576
+    check_fwd(c, *run_fwd(c))
+    check_bwd(c)
+
+
+@gpu
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
 @pytest.mark.parametrize("n,T,H", [(2, 1700, 1), (3, 640, 2), (1, 2177, 2)])
 def test_equal_lengths_forward_and_backward(n, T, H, dtype):
     c = make([T] * n, H, H, H, H, 128, 128, dtype, "retention", s0=True, seed=4)
@@ -241,3 +252,15 @@ def test_the_workspace_size_holds_for_packed_and_for_equal_lengths():
                 assert lib.gdr_linattn_fwd(s, *(fake(i) for i in range(4)), None, cu, fake(5), fake(6), fake(7), fwd - 1, None) == -4
                 assert lib.gdr_linattn_bwd(s, *(fake(i) for i in range(5)), None, None, cu, fake(6), fake(7), fake(8),
                                            None, fake(9), bwd - 1, None) == -4
+
+
+def test_the_workspace_does_not_grow_with_short_sequences():
+    """A sum is kept for a segment that hands one on: at most T / 128 of them, in four parts."""
+    from gated_delta_rule_03_gb300 import ops
+    lib = ops._load()
+    matrix = 4 * 128 * 128 * 4  # heads, d_k, d_v, bytes
+    for n, T in [(64, 6400), (4096, 40960), (1000, 1000)]:
+        s = ctypes.byref(shape(num_seqs=n, total_tokens=T, k_heads=4, v_heads=4))
+        sums = 4 * (T // 128) * matrix
+        assert lib.gdr_linattn_fwd_workspace_size(s) <= n * matrix + sums + 1024
+        assert lib.gdr_linattn_bwd_workspace_size(s) <= 2 * sums + 1024

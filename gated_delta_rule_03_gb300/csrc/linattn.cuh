@@ -88,8 +88,13 @@ struct Segment {
 // lengths: first the pairs that stay whole, then the segments one after the other. Called
 // by the whole block (a barrier inside). With cu_seqlens every block checks all of it (offsets
 // from 0, not decreasing, at most total_tokens); where it is not so, no block does anything:
-// false.
-__device__ __forceinline__ bool locate(const Plan &p, int64_t unit, int handing, Segment *shared) {
+// false. Up to kOrdered sequences are taken longest first, so that short ones fill up the end
+// of the launch (a sequence's place takes a look at every other, hence the limit). In this and
+// in the order of memory: 8 of 1,611 to 7,848 tokens, shortest first, 32 heads 267 and 300 us; 31
+// of 900 and one of 6,000, 16 heads 173 and 215, backward with 32 heads 800 and 755. `scratch`:
+// 2 kOrdered ints of shared memory.
+constexpr int kOrdered = 64;
+__device__ __forceinline__ bool locate(const Plan &p, int64_t unit, int handing, Segment *shared, int *scratch) {
     const int skip = handing == 2;  // segments in front of the first item's
     const int less = handing != 0;
     auto fill = [&](int seq, int h, int f, int n, int64_t first, int64_t len, int64_t sum0) {
@@ -123,12 +128,26 @@ __device__ __forceinline__ bool locate(const Plan &p, int64_t unit, int handing,
     __shared__ int64_t warp_sum[32];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = (blockDim.x + 31) >> 5;
     if (tid == 0) shared->seq = -1;
+    const bool ordered = p.num_seqs <= kOrdered;
+    if (ordered) {
+        int *lens = scratch + kOrdered;
+        const int mine = tid < p.num_seqs ? p.cu_seqlens[tid + 1] - p.cu_seqlens[tid] : 0;
+        if (tid < p.num_seqs) lens[tid] = mine;
+        __syncthreads();
+        if (tid < p.num_seqs) {
+            int rank = 0;
+            for (int j = 0; j < (int)p.num_seqs; ++j) rank += lens[j] > mine || (lens[j] == mine && j < tid);
+            scratch[rank] = tid;
+        }
+        __syncthreads();
+    }
     int64_t carry = 0;
     int wrong = 0;
     for (int64_t base = 0; base < p.num_seqs; base += blockDim.x) {
-        const int64_t n = base + tid;
-        int64_t a = 0, len = 0, count = 0;
-        if (n < p.num_seqs) {
+        const int64_t i = base + tid;  // place in the order
+        int64_t n = i, a = 0, len = 0, count = 0;
+        if (i < p.num_seqs) {
+            if (ordered) n = scratch[i];
             a = p.cu_seqlens[n];
             len = (int64_t)p.cu_seqlens[n + 1] - a;
             if (len < 0 || a < 0 || a + len > p.total_tokens || (n == 0 && a != 0)) {
@@ -154,7 +173,7 @@ __device__ __forceinline__ bool locate(const Plan &p, int64_t unit, int handing,
         }
         const int64_t first_item = carry + before + sum - count;
         if (count > 0 && item >= first_item && item < first_item + count)
-            fill((int)n, (int)(unit % p.H), (int)(item - first_item) + skip, (int)count + less, a, len, first_item - (less ? 0 : n));
+            fill((int)n, (int)(unit % p.H), (int)(item - first_item) + skip, (int)count + less, a, len, first_item - (less ? 0 : i));
         carry += total;
         __syncthreads();
     }

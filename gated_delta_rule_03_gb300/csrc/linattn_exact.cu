@@ -63,7 +63,7 @@ __global__ void __launch_bounds__(kThreads, 1) mix_exact_kernel(const Plan p, co
     const int slices = m.dz / NZ;
     const int64_t block = blockIdx.x;
     const int slice = (int)(block % slices);
-    const bool bad = !locate(p, block / slices, kOut ? 0 : 1 + m.backward, &found);
+    const bool bad = !locate(p, block / slices, kOut ? 0 : 1 + m.backward, &found, (int *)smem);
     const Segment s = found;
     const int h = s.h;
     if (block == 0 && tid == 0 && p.first) p.status[0] = bad ? GDR_ERR_BAD_SEQLENS : GDR_OK;

@@ -371,7 +371,7 @@ __global__ void __launch_bounds__(kThreads, 1) mix_tc_kernel(const __grid_consta
     const int role = (int)(blockIdx.x % A.count);
     const int64_t rest = blockIdx.x / A.count;
     const int slice = (int)(rest % A.slices);
-    const bool bad = !locate(A.p, rest / A.slices, 0, &found);
+    const bool bad = !locate(A.p, rest / A.slices, 0, &found, (int *)weights);
     if (blockIdx.x == 0 && tid == 0 && A.p.first) A.p.status[0] = bad ? GDR_ERR_BAD_SEQLENS : GDR_OK;
     if (bad || found.seq < 0) {
         griddep_wait();  // no launch ends before the one ahead of it
@@ -804,7 +804,7 @@ __global__ void __launch_bounds__(kSumThreads, 1) sum_tc_kernel(const __grid_con
     const int slice = (int)(rest % A.slices);
     const int part = (int)(rest / A.slices / A.p.handing);
     griddep_launch_dependents();
-    const bool bad = !locate(A.p, rest / A.slices % A.p.handing, 1 + A.mix[role].backward, &found);
+    const bool bad = !locate(A.p, rest / A.slices % A.p.handing, 1 + A.mix[role].backward, &found, (int *)weights);
     Segment s = found;
     const int h = s.h;
     if (blockIdx.x == 0 && tid == 0 && A.p.first) A.p.status[0] = bad ? GDR_ERR_BAD_SEQLENS : GDR_OK;

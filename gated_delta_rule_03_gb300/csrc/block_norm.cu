@@ -96,28 +96,39 @@ template <int VEC> __device__ __forceinline__ Weight<VEC> weight_of(const float 
     return a;
 }
 
-// Sums of K values over the blockDim.x threads of a row: within the warp, then over the row's
-// warps (at most 16) by every warp for itself. `buf` has 2 x 16 x 3 floats; calls take its
-// halves in turn, so that one barrier per sum is enough.
+// Sums of K values (1 or 3) over the blockDim.x threads of a row: within the warp, then over the
+// row's warps (at most 16) by every warp for itself. Of three values each half of the warp goes
+// on with its own after an exchange: 6 shuffles instead of 15. `buf` has 2 x 16 x 3 floats; calls
+// take its halves in turn, so that one barrier per sum is enough.
 template <int K> __device__ __forceinline__ void row_sum(float (&s)[K], float *buf, int turn) {
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1)
-#pragma unroll
-        for (int k = 0; k < K; ++k) s[k] += __shfl_xor_sync(0xffffffffu, s[k], off);
+    static_assert(K == 1 || K == 3, "");
+    const unsigned all = 0xffffffffu;
     const int warps = blockDim.x >> 5, lane = threadIdx.x & 31;
-    if (warps == 1) return;
-    float *row = buf + (turn & 1) * 48 + threadIdx.y * warps * K;
-    if (lane == 0) {
-#pragma unroll
-        for (int k = 0; k < K; ++k) row[k * warps + (threadIdx.x >> 5)] = s[k];
+    float v = s[0];
+    if (K == 3) {  // lanes 0-7 go on with value 0, 16-23 with 1, the others with 2
+        const bool high = lane & 16, last = lane & 8;
+        const float x = (high ? s[1] : s[0]) + __shfl_xor_sync(all, high ? s[0] : s[1], 16);
+        const float y = s[2] + __shfl_xor_sync(all, s[2], 16);
+        v = (last ? y : x) + __shfl_xor_sync(all, last ? x : y, 8);
     }
-    __syncthreads();
 #pragma unroll
-    for (int k = 0; k < K; ++k) s[k] = (lane & 15) < warps ? row[k * warps + (lane & 15)] : 0.f;
+    for (int off = K == 3 ? 4 : 16; off > 0; off >>= 1) v += __shfl_xor_sync(all, v, off);
+    if (warps > 1) {
+        float *row = buf + (turn & 1) * 48 + threadIdx.y * warps * K;
+        const int which = K == 3 ? (lane & 8 ? 2 : lane >> 4) : 0;
+        if ((lane & (K == 3 ? 7 : 31)) == 0) row[which * warps + (threadIdx.x >> 5)] = v;
+        __syncthreads();
+        const int w = lane & 7;
+        v = w < warps ? row[which * warps + w] : 0.f;
+        if (w + 8 < warps) v += row[which * warps + w + 8];
 #pragma unroll
-    for (int off = 8; off > 0; off >>= 1)
-#pragma unroll
-        for (int k = 0; k < K; ++k) s[k] += __shfl_xor_sync(0xffffffffu, s[k], off);
+        for (int off = 4; off > 0; off >>= 1) v += __shfl_xor_sync(all, v, off);
+    }
+    s[0] = K == 3 ? __shfl_sync(all, v, 0) : v;
+    if (K == 3) {
+        s[K / 2] = __shfl_sync(all, v, 16);
+        s[K - 1] = __shfl_sync(all, v, 8);
+    }
 }
 
 // Two fp32 at a time.

@@ -291,7 +291,8 @@ template <typename T, int VEC, int PER> __host__ __device__ constexpr bool fetch
 // Sums over this block's rows go to part[which][blockIdx.x * blockDim.y + threadIdx.y][D]. The
 // next row's inputs are on their way to shared memory while a row is worked on (in registers
 // they would halve the warps, and the instructions per entry, about 45, need the warps).
-// Bound by its instructions: 16384 x 2048 bf16, 537 MB, in 120 us, 4.5 TB/s, and 8 for the sums.
+// Bound by its instructions, 690 per warp and 256 entries: 16384 x 2048 bf16, 537 MB, in 127 us
+// with the column sums, 4.2 TB/s.
 // Rows wider than 4096 keep their columns' sums in shared memory instead. One gate row for all:
 // with A = the sum over rows of s dx' n, dw_post is act(gate) A and dgate is act'(gate) w_post A.
 template <typename T, typename TX, int VEC, int PER, int THREADS>
@@ -554,7 +555,7 @@ Shape2 shape_of(int D, bool backward) {
 }
 // Blocks of a backward call: 768 threads on an SM where a block has at most 256, else one block;
 // all of them are resident at once (the kernel's bounds above). 4099 x 1030 fp32: 38 us; with
-// a third of the blocks left for a second round 47 us.
+// a third of the blocks left for a second round 47 us (before three sums took 12 shuffles: 36).
 int bwd_blocks(int64_t rows, const Shape2 &s) {
     const int threads = (int)(s.block.x * s.block.y);
     const int64_t need = (rows + s.block.y - 1) / s.block.y;

@@ -74,6 +74,33 @@ def test_equal_lengths_forward_and_backward(n, T, H, dtype):
 
 
 @gpu
+@pytest.mark.parametrize("N,T,H,dtype", [(9, 2560, 17, BF16), (3, 2500, 18, BF16), (7, 650, 11, F32)],
+                         ids=["forward-bf16", "backward-bf16", "f32"])
+def test_some_pairs_whole_and_the_rest_cut(N, T, H, dtype):
+    """A few chains more than the GPU has SMs (153, 162 and 154 of them): most (sequence, head)
+    pairs stay whole, the last ones are cut. Corners against the definition, all pairs written."""
+    from gated_delta_rule_03_gb300 import linattn_bwd
+    c = make([T] * N, H, H, H, H, 128, 128, dtype, "retention", s0=True, seed=12)
+    o, S = run_fwd(c, cu=None)
+    outs = [torch.full_like(c[n], math.nan) for n in ("q", "k", "v", "S0")]
+    linattn_bwd(c["do"], c["q"], c["k"], c["v"], c["ld"], S0=c["S0"], dS_final=c["dS"], num_seqs=N,
+                scale=c["scale"], dq=outs[0], dk=outs[1], dv=outs[2], dS0=outs[3])
+    assert all(bool(torch.isfinite(t).all()) for t in (o, S, *outs))
+    terms = ref.f32_terms(T, 128, 128, 1)
+    for n, h in [(0, 0), (N - 2, H - 1), (N - 1, 0), (N - 1, H - 2), (N - 1, H - 1)]:
+        rows = slice(n * T, (n + 1) * T)
+        q, k, v, do = (ref.f64(c[x][rows, h:h + 1]) for x in ("q", "k", "v", "do"))
+        ld, S0, dS = ref.f64(c["ld"][h:h + 1]), ref.f64(c["S0"][n:n + 1, h:h + 1]), ref.f64(c["dS"][n:n + 1, h:h + 1])
+        want_o, want_S, abs_o, abs_S = ref.forward(q, k, v, ld, [T], S0, c["scale"])
+        ref.check("o", o[rows, h:h + 1], want_o, abs_o, dtype, terms)
+        ref.check("S_final", S[n:n + 1, h:h + 1], want_S, abs_S, F32, terms)
+        want = ref.backward(do, q, k, v, ld, [T], S0, dS, c["scale"])
+        for name, t in zip(("dq", "dk", "dv"), outs):
+            ref.check(name, t[rows, h:h + 1], *want[name], dtype, terms)
+        ref.check("dS0", outs[3][n:n + 1, h:h + 1], *want["dS0"], F32, terms)
+
+
+@gpu
 @pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
 def test_one_tensor_as_query_key_and_value(dtype):
     c = make([500, 77], 2, 2, 2, 2, 128, 128, dtype, "retention", s0=True, seed=5)

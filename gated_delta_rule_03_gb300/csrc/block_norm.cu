@@ -98,9 +98,12 @@ template <int VEC> __device__ __forceinline__ Weight<VEC> weight_of(const float 
 
 // Sums of K values (1 or 3) over the blockDim.x threads of a row: within the warp, then over the
 // row's warps (at most 16) by every warp for itself. Of three values each half of the warp goes
-// on with its own after an exchange: 6 shuffles instead of 15. `buf` has 2 x 16 x 3 floats; calls
-// take its halves in turn, so that one barrier per sum is enough.
-template <int K> __device__ __forceinline__ void row_sum(float (&s)[K], float *buf, int turn) {
+// on with its own after an exchange: 6 shuffles instead of 15. `buf` has 2 x 16 x 3 floats. One
+// barrier per sum is enough where every call takes the other half than the call before it, in a
+// loop's next round too: a warp then comes back to a half only past the barrier of the sum between,
+// which all warps reach after they have read that half. So the half is kept here, in `turn`, of
+// which a block has one (0 at first) for all its sums.
+template <int K> __device__ __forceinline__ void row_sum(float (&s)[K], float *buf, int &turn) {
     static_assert(K == 1 || K == 3, "");
     const unsigned all = 0xffffffffu;
     const int warps = blockDim.x >> 5, lane = threadIdx.x & 31;
@@ -114,7 +117,8 @@ template <int K> __device__ __forceinline__ void row_sum(float (&s)[K], float *b
 #pragma unroll
     for (int off = K == 3 ? 4 : 16; off > 0; off >>= 1) v += __shfl_xor_sync(all, v, off);
     if (warps > 1) {
-        float *row = buf + (turn & 1) * 48 + threadIdx.y * warps * K;
+        float *row = buf + turn * 48 + threadIdx.y * warps * K;
+        turn ^= 1;
         const int which = K == 3 ? (lane & 8 ? 2 : lane >> 4) : 0;
         if ((lane & (K == 3 ? 7 : 31)) == 0) row[which * warps + (threadIdx.x >> 5)] = v;
         __syncthreads();
@@ -202,6 +206,7 @@ template <typename T, typename TX, int VEC, int PER>
 __global__ void __launch_bounds__(512)
 block_norm_fwd_kernel(const NormParams p, const TX *x, const T *y, const T *gate, TX *x_out, T *h) {
     __shared__ float buf[96];
+    int turn = 0;
     const int64_t row = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
     const int D = row < p.rows ? p.D : 0;  // a row behind the last loads and stores nothing
     const int64_t at = row * p.D;
@@ -217,7 +222,7 @@ block_norm_fwd_kernel(const NormParams p, const TX *x, const T *y, const T *gate
             float ss[1] = {0.f};
 #pragma unroll
             for (int i = 0; i < PER; ++i) ss[0] = fmaf(yr[i], yr[i], ss[0]);
-            row_sum(ss, buf, 0);
+            row_sum(ss, buf, turn);
             r = rsqrtf(ss[0] * p.inv_D + p.eps);
         }
         const float *w = p.post ? p.w_post : nullptr;
@@ -249,7 +254,7 @@ block_norm_fwd_kernel(const NormParams p, const TX *x, const T *y, const T *gate
     float ss[1] = {0.f};
 #pragma unroll
     for (int i = 0; i < PER; ++i) ss[0] = fmaf(v[i], v[i], ss[0]);
-    row_sum(ss, buf, 1);
+    row_sum(ss, buf, turn);
     const float r = rsqrtf(ss[0] * p.inv_D + p.eps);
 #pragma unroll
     for (int j = 0; j < PER / VEC; ++j) {
@@ -302,6 +307,7 @@ block_norm_bwd_kernel(const NormParams p, const TX *dx_out, const T *dh, const T
                       float *part_gate) {
     constexpr bool kWide = PER > 8, kAhead = fetches_ahead<T, VEC, PER>();
     __shared__ float buf[96];
+    int turn = 0;
     extern __shared__ __align__(16) char dynamic[];
     float *wide = reinterpret_cast<float *>(dynamic);  // [2][D], each thread its own columns
     constexpr int kSums = kWide ? 1 : PER / 2;
@@ -400,7 +406,7 @@ block_norm_bwd_kernel(const NormParams p, const TX *dx_out, const T *dh, const T
             for (int i = 0; i < PER; i += 2) yy = fma2(yr.two(i), yr.two(i), yy);
         }
         float sums[3] = {xx.x + xx.y, hx.x + hx.y, yy.x + yy.y};
-        if (dh || p.post) row_sum(sums, buf, 0);
+        if (dh || p.post) row_sum(sums, buf, turn);
         if constexpr (kAhead)
             if (dx_out) read8(dr.p[0], here, threads);
         if (dh) {
@@ -457,7 +463,7 @@ block_norm_bwd_kernel(const NormParams p, const TX *dx_out, const T *dh, const T
         }
         if (p.post) {
             float dot[1] = {yd.x + yd.y};
-            row_sum(dot, buf, 1);
+            row_sum(dot, buf, turn);
             const float m = r * r * (dot[0] * p.inv_D);
 #pragma unroll
             for (int i = 0; i < PER; i += 2) dv[i / 2] = mul2(both(r), fma2(yr.two(i), both(-m), dv[i / 2]));

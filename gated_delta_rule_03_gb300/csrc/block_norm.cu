@@ -559,13 +559,24 @@ Shape2 shape_of(int D, bool backward) {
     s.block = dim3((unsigned)tpr, (unsigned)(tpr >= 128 ? 1 : 128 / tpr));
     return s;
 }
-// Blocks of a backward call: 768 threads on an SM where a block has at most 256, else one block;
-// all of them are resident at once (the kernel's bounds above). 4099 x 1030 fp32: 38 us; with
-// a third of the blocks left for a second round 47 us (before three sums took 12 shuffles: 36).
-int bwd_blocks(int64_t rows, const Shape2 &s) {
+size_t elem(int dtype) { return dtype == GDR_F32 ? 4 : 2; }
+
+// Blocks of a backward call: all of them are resident at once. Where a block has at most 256
+// threads an SM takes 768 (registers: the kernel's bounds above) and what its 228 KB of shared memory
+// hold (each block the rows that it fetches ahead, its buffer, and 1 KB of the system's), else one
+// block. fp32 in widths of eights is where shared memory decides.
+// With a third of the blocks left for a second round: 4099 x 1030 fp32 47 us, now 35; 8192 x 2048
+// fp32 216 us, now 180.
+int bwd_blocks(int64_t rows, const Shape2 &s, const gdr_block_norm_shape *shape) {
     const int threads = (int)(s.block.x * s.block.y);
     const int64_t need = (rows + s.block.y - 1) / s.block.y;
-    const int64_t most = (int64_t)kSms * (threads <= 256 ? 768 / threads : 1);
+    int per_sm = threads <= 256 ? 768 / threads : 1;
+    if (s.per == 8 && s.vec == 8) {  // fetches_ahead
+        const int ahead = 2 * s.per * (int)(2 * elem(shape->x_dtype) + 3 * elem(shape->dtype)) * threads;
+        const int fit = 228 * 1024 / (ahead + 96 * (int)sizeof(float) + 1024);
+        if (fit < per_sm) per_sm = fit;
+    }
+    const int64_t most = (int64_t)kSms * per_sm;
     return (int)(need < most ? need : most);
 }
 
@@ -623,7 +634,6 @@ int run_bwd(const NormParams &p, const Shape2 &s, int blocks, const void *dx_out
     GDR_NORM_BY_SHAPE(R, bwd, 8, 16, p, s, blocks, dx_out, dh, x, y, gate, dx, dy, dgate, pp, pn, pg, stream);
 }
 
-size_t elem(int dtype) { return dtype == GDR_F32 ? 4 : 2; }
 bool apart(const void *a, size_t an, const void *b, size_t bn) {
     if (!a || !b || !an || !bn) return true;
     const char *pa = (const char *)a, *pb = (const char *)b;
@@ -699,7 +709,7 @@ size_t gdr_block_norm_bwd_workspace_size(const gdr_block_norm_shape *shape) {
     NormParams p;
     if (check_shape(shape, &p) != GDR_OK) return 0;
     const Shape2 s = shape_of(p.D, true);
-    const size_t parts = (size_t)bwd_blocks(p.rows, s) * s.block.y;
+    const size_t parts = (size_t)bwd_blocks(p.rows, s, shape) * s.block.y;
     return 256 + 3 * parts * ((size_t)(p.D + 3) / 4 * 4) * sizeof(float);
 }
 
@@ -740,7 +750,7 @@ int gdr_block_norm_bwd(const gdr_block_norm_shape *shape, const void *dx_out, co
     p.w_pre = w_pre;
     const Shape2 s = shape_of(p.D, true);
     const cudaStream_t stm = (cudaStream_t)stream;
-    const int blocks = bwd_blocks(p.rows, s);
+    const int blocks = bwd_blocks(p.rows, s, shape);
     const int parts = blocks * (int)s.block.y;
     const size_t one = (size_t)parts * ((size_t)(p.D + 3) / 4 * 4);
     float *base = (float *)((char *)workspace + 256);

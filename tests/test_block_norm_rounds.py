@@ -16,7 +16,7 @@ import numpy as np
 import pytest
 import torch
 
-from tests.test_block_norm import BF16, EPS, F32, U, backward, f64, make, rstd
+from tests.test_block_norm import BF16, EPS, F32, U, backward, f64, lib, make, rstd, shape  # noqa: F401
 
 gpu = pytest.mark.gpu
 u = 2.0 ** -24
@@ -122,3 +122,23 @@ def test_many_rows_without_the_norm_after_the_block(D, rows, dt, xdt):
 @pytest.mark.parametrize("D,rows", ROUNDS)
 def test_many_rows_of_the_first_block(D, rows, dt, xdt):
     check_backward(rows, D, dt, xdt, "none", "silu", "no", "weight", 1.0, repeats=20, first=True)
+
+
+# ------------------------------------------------------------------ without a GPU
+
+@pytest.mark.parametrize("D", [8, 104, 256, 512, 768, 1024, 1280, 1536, 1792, 2048, 2056, 4096])
+@pytest.mark.parametrize("dtype,x_dtype", [(0, 0), (1, 1), (1, 0)], ids=TYPE_IDS)
+def test_the_blocks_of_a_backward_call_fit_the_gpu_at_once(lib, dtype, x_dtype, D):  # noqa: F811
+    # widths in eights up to 4096: two rows' five inputs in shared memory, 8 entries a thread
+    threads = (D + 255) // 256 * 32
+    rows_at_once = 1 if threads >= 128 else 128 // threads
+    threads *= rows_at_once
+    size = {0: 4, 1: 2}
+    block = 2 * 8 * (2 * size[x_dtype] + 3 * size[dtype]) * threads + 96 * 4 + 1024  # (1 KB each is the system's)
+    held = lib.gdr_block_norm_bwd_workspace_size(shape(rows=1 << 20, D=D, dtype=dtype, x_dtype=x_dtype, gate_rows=0)) - 256
+    blocks, left = divmod(held, 3 * D * 4 * rows_at_once)
+    assert left == 0 and blocks % 152 == 0
+    per_sm = blocks // 152
+    assert per_sm * block <= 228 * 1024 and per_sm * threads <= 768
+    # and as many as fit: one block more would be too much for either
+    assert (per_sm + 1) * block > 228 * 1024 or (per_sm + 1) * threads > 768 or threads > 256

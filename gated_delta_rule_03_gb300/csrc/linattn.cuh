@@ -193,7 +193,8 @@ __device__ __forceinline__ int64_t state_at(const Mix &m, int a, int b) {
     return m.turned ? (int64_t)b * m.dx + a : (int64_t)a * m.dz + b;
 }
 
-int launch_mix_exact(const Plan &p, const Mix *mixes, int count, int dtype, cudaStream_t stream);
+// (rows in fp32, or none)
+int launch_mix_exact(const Plan &p, const Mix *mixes, int count, cudaStream_t stream);
 int launch_mix_tc(const Plan &p, const Mix *mixes, int count, int d_v, bool sums, cudaStream_t stream);
 // Sums the g parts of every head: in fp32 [rows, heads g, d] -> out [rows, heads, d]. Rows
 // behind the last sequence are left as they are.

@@ -268,7 +268,7 @@ Mix mix_of(const Call &c, const void *x, int64_t xs, int xh, const void *y, int6
 }
 
 int launch(const Call &c, const Plan &p, const Mix *mixes, int count, bool sums, cudaStream_t s) {
-    if (!on_tensor_cores(c)) return launch_mix_exact(p, mixes, count, c.dtype, s);
+    if (!on_tensor_cores(c)) return launch_mix_exact(p, mixes, count, s);
     return launch_mix_tc(p, mixes, count, c.dv, sums, s);
 }
 

@@ -1,5 +1,6 @@
 // linattn_exact.cu -- the mix of linear attention (linattn.cuh) in fp32 arithmetic, for fp32
-// inputs and for the sizes that the tensor-core kernel does not take.
+// inputs. A bf16 call without tokens comes here too: it only hands on its states, which are
+// fp32, and no row of any type is read or written. And the sum of gradients of shared heads.
 //
 // One CTA per (segment, head, 64 columns of z) walks its segment in chunks of C tokens. The
 // state lives in registers (thread (ty, tx): rows ty R .. + R - 1, columns 4 tx .. + 3) and
@@ -23,16 +24,7 @@ template <int DX> struct Cfg {
     static constexpr size_t floats = 2 * C * LX + C * LZ + DX * LZ + C * LP + C + 1;
 };
 
-template <typename T> __device__ __forceinline__ float4 load4(const T *p);
-template <> __device__ __forceinline__ float4 load4<float>(const float *p) {
-    return *reinterpret_cast<const float4 *>(p);
-}
-template <> __device__ __forceinline__ float4 load4<__nv_bfloat16>(const __nv_bfloat16 *p) {
-    const uint2 u = *reinterpret_cast<const uint2 *>(p);
-    const float2 lo = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&u.x));
-    const float2 hi = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&u.y));
-    return make_float4(lo.x, lo.y, hi.x, hi.y);
-}
+__device__ __forceinline__ float4 load4(const float *p) { return *reinterpret_cast<const float4 *>(p); }
 __device__ __forceinline__ void store4(float *p, float4 x) { *reinterpret_cast<float4 *>(p) = x; }
 __device__ __forceinline__ void store4(__nv_bfloat16 *p, float4 x) {
     __nv_bfloat162 lo = __floats2bfloat162_rn(x.x, x.y), hi = __floats2bfloat162_rn(x.z, x.w);
@@ -49,7 +41,7 @@ __device__ __forceinline__ void fma4(float4 &a, float s, const float4 &b) {
 }
 
 // kOut: the mix itself; otherwise only the segment's own sum R.
-template <typename T, int DX, bool kOut>
+template <int DX, bool kOut>
 __global__ void __launch_bounds__(kThreads, 1) mix_exact_kernel(const Plan p, const Mix m) {
     constexpr int C = Cfg<DX>::C, LX = Cfg<DX>::LX, LZ = Cfg<DX>::LZ, LP = Cfg<DX>::LP;
     constexpr int R = DX / 16;          // state rows per thread
@@ -100,9 +92,9 @@ __global__ void __launch_bounds__(kThreads, 1) mix_exact_kernel(const Plan p, co
         }
     }
 
-    const T *x = (const T *)m.x + (int64_t)(h / m.xg) * m.dx;
-    const T *y = (const T *)m.y + (int64_t)(h / m.yg) * m.dx;
-    const T *z = (const T *)m.z + (int64_t)(h / m.zg) * m.dz + slice * NZ;
+    const float *x = (const float *)m.x + (int64_t)(h / m.xg) * m.dx;
+    const float *y = (const float *)m.y + (int64_t)(h / m.yg) * m.dx;
+    const float *z = (const float *)m.z + (int64_t)(h / m.zg) * m.dz + slice * NZ;
     const int chunks = (int)((s.tokens + C - 1) / C);
     for (int cc = 0; cc < chunks; ++cc) {
         const int c = m.backward ? chunks - 1 - cc : cc;
@@ -196,8 +188,7 @@ __global__ void __launch_bounds__(kThreads, 1) mix_exact_kernel(const Plan p, co
                 const int r = ty + 16 * a;
                 if (r >= n) continue;
                 const int64_t at = ((t0 + r) * p.H + h) * m.dz + z0;
-                if (m.out_f32) store4((float *)m.out + at, o[a]);
-                else store4((T *)m.out + at, o[a]);
+                store4((float *)m.out + at, o[a]);
             }
         } else {
             __syncthreads();
@@ -238,24 +229,24 @@ __global__ void __launch_bounds__(kThreads, 1) mix_exact_kernel(const Plan p, co
     }
 }
 
-template <typename T, int DX, bool kOut>
+template <int DX, bool kOut>
 int launch_one(const Plan &p, const Mix &m, cudaStream_t stream) {
     constexpr size_t bytes = Cfg<DX>::floats * sizeof(float);
     static_assert(bytes <= 232448 - 512, "shared memory");
-    if (cudaFuncSetAttribute(mix_exact_kernel<T, DX, kOut>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    if (cudaFuncSetAttribute(mix_exact_kernel<DX, kOut>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              (int)bytes) != cudaSuccess)
         return GDR_ERR_CUDA;
     const int64_t blocks = (kOut ? p.units : p.handing) * (m.dz / NZ);
-    mix_exact_kernel<T, DX, kOut><<<(unsigned)blocks, kThreads, bytes, stream>>>(p, m);
+    mix_exact_kernel<DX, kOut><<<(unsigned)blocks, kThreads, bytes, stream>>>(p, m);
     return cuda_status(cudaGetLastError());
 }
 
-template <typename T> int launch_t(const Plan &p, const Mix &m, cudaStream_t stream) {
+int launch_of(const Plan &p, const Mix &m, cudaStream_t stream) {
     const bool out = m.out != nullptr;
     switch (m.dx) {
-        case 64: return out ? launch_one<T, 64, true>(p, m, stream) : launch_one<T, 64, false>(p, m, stream);
-        case 128: return out ? launch_one<T, 128, true>(p, m, stream) : launch_one<T, 128, false>(p, m, stream);
-        case 256: return out ? launch_one<T, 256, true>(p, m, stream) : launch_one<T, 256, false>(p, m, stream);
+        case 64: return out ? launch_one<64, true>(p, m, stream) : launch_one<64, false>(p, m, stream);
+        case 128: return out ? launch_one<128, true>(p, m, stream) : launch_one<128, false>(p, m, stream);
+        case 256: return launch_one<256, true>(p, m, stream);  // (sums have rows of d_k, 128 at most)
     }
     return GDR_ERR_UNSUPPORTED;
 }
@@ -282,12 +273,11 @@ template <typename T> __global__ void __launch_bounds__(256) share_kernel(const 
 
 }  // namespace
 
-int launch_mix_exact(const Plan &p, const Mix *mixes, int count, int dtype, cudaStream_t stream) {
+int launch_mix_exact(const Plan &p, const Mix *mixes, int count, cudaStream_t stream) {
     for (int i = 0; i < count; ++i) {
         Plan pi = p;
         pi.first = p.first && i == 0;
-        const int st = dtype == GDR_BF16 ? launch_t<__nv_bfloat16>(pi, mixes[i], stream)
-                                         : launch_t<float>(pi, mixes[i], stream);
+        const int st = launch_of(pi, mixes[i], stream);
         if (st != GDR_OK) return st;
     }
     return GDR_OK;

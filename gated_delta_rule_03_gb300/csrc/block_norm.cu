@@ -103,6 +103,7 @@ template <int VEC> __device__ __forceinline__ Weight<VEC> weight_of(const float 
 // loop's next round too: a warp then comes back to a half only past the barrier of the sum between,
 // which all warps reach after they have read that half. So the half is kept here, in `turn`, of
 // which a block has one (0 at first) for all its sums.
+constexpr int kBufBytes = 2 * 16 * 3 * (int)sizeof(float);
 template <int K> __device__ __forceinline__ void row_sum(float (&s)[K], float *buf, int &turn) {
     static_assert(K == 1 || K == 3, "");
     const unsigned all = 0xffffffffu;
@@ -205,7 +206,7 @@ struct NormParams {
 template <typename T, typename TX, int VEC, int PER>
 __global__ void __launch_bounds__(512)
 block_norm_fwd_kernel(const NormParams p, const TX *x, const T *y, const T *gate, TX *x_out, T *h) {
-    __shared__ float buf[96];
+    __shared__ float buf[kBufBytes / sizeof(float)];
     int turn = 0;
     const int64_t row = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
     const int D = row < p.rows ? p.D : 0;  // a row behind the last loads and stores nothing
@@ -306,7 +307,7 @@ block_norm_bwd_kernel(const NormParams p, const TX *dx_out, const T *dh, const T
                       const T *gate, TX *dx, T *dy, T *dgate, float *part_post, float *part_pre,
                       float *part_gate) {
     constexpr bool kWide = PER > 8, kAhead = fetches_ahead<T, VEC, PER>();
-    __shared__ float buf[96];
+    __shared__ float buf[kBufBytes / sizeof(float)];
     int turn = 0;
     extern __shared__ __align__(16) char dynamic[];
     float *wide = reinterpret_cast<float *>(dynamic);  // [2][D], each thread its own columns
@@ -573,7 +574,7 @@ int bwd_blocks(int64_t rows, const Shape2 &s, const gdr_block_norm_shape *shape)
     int per_sm = threads <= 256 ? 768 / threads : 1;
     if (s.per == 8 && s.vec == 8) {  // fetches_ahead
         const int ahead = 2 * s.per * (int)(2 * elem(shape->x_dtype) + 3 * elem(shape->dtype)) * threads;
-        const int fit = 228 * 1024 / (ahead + 96 * (int)sizeof(float) + 1024);
+        const int fit = 228 * 1024 / (ahead + kBufBytes + 1024);
         if (fit < per_sm) per_sm = fit;
     }
     const int64_t most = (int64_t)kSms * per_sm;
@@ -598,7 +599,8 @@ template <typename T, typename TX> struct Run {
                              : (fetches_ahead<T, VEC, PER>() ? 2 * (size_t)row_bytes<T, TX, PER>() * threads : 0);
         auto kernel = PER > 8 || threads > 256 ? block_norm_bwd_kernel<T, TX, VEC, PER, 512>
                                                : block_norm_bwd_kernel<T, TX, VEC, PER, (PER > 8 ? 512 : 256)>;
-        if (bytes > 48 * 1024 &&
+        // (48 KB without asking, the kernel's own 384 bytes among them: D = 6144 has to ask)
+        if (bytes + kBufBytes > 48 * 1024 &&
             cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) != cudaSuccess)
             return GDR_ERR_CUDA;
         kernel<<<(unsigned)blocks, s.block, bytes, stream>>>(

@@ -124,6 +124,14 @@ def test_many_rows_of_the_first_block(D, rows, dt, xdt):
     check_backward(rows, D, dt, xdt, "none", "silu", "no", "weight", 1.0, repeats=20, first=True)
 
 
+@gpu
+@pytest.mark.parametrize("dt,xdt", TYPES, ids=TYPE_IDS)
+@pytest.mark.parametrize("D", [6096, 6097, 6120, 6143, 6144, 6145])
+def test_widths_whose_column_sums_take_just_48_kb(D, dt, xdt):
+    # (what a kernel has without asking for more, its own buffer among it)
+    check_backward(155, D, dt, xdt, "one", "silu", "weight", "weight", 1.0, repeats=1)
+
+
 # ------------------------------------------------------------------ without a GPU
 
 @pytest.mark.parametrize("D", [8, 104, 256, 512, 768, 1024, 1280, 1536, 1792, 2048, 2056, 4096])

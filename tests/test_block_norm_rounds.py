@@ -16,7 +16,7 @@ import numpy as np
 import pytest
 import torch
 
-from tests.test_block_norm import BF16, EPS, F32, U, backward, f64, lib, make, rstd, shape  # noqa: F401
+from tests.test_block_norm import BF16, EPS, F32, U, backward, f64, forward, lib, make, rstd, shape  # noqa: F401
 
 gpu = pytest.mark.gpu
 u = 2.0 ** -24
@@ -67,6 +67,26 @@ def bounds(want, c, rows, post, kind, gate):
         else:
             out["dgate"] = (KX + 1 + KN + 3 + DGATE) * u * size
     return out
+
+
+def check_forward(rows, D, dt, xdt, gate, kind, post, pre, s, seed=12):
+    from gated_delta_rule_03_gb300 import block_norm_fwd
+    c = make(rows, D, dt, xdt, gate, post, pre, seed=seed)
+    got_x, got_h = block_norm_fwd(c["x"], c["y"], gate=c["gate"], act=kind, w_post=c["w_post"], w_pre=c["w_pre"],
+                                  post_norm=post != "no", pre_norm=pre != "no", res_scale=s, eps=EPS)
+    x, y, g, wp, wn = (f64(c[n]) for n in ("x", "y", "gate", "w_post", "w_pre"))
+    want_x, want_h = forward(x, y, g, wp, wn, post != "no", pre != "no", kind, s)
+    # x + (y act) (r s) w: the gate, r, three products; the addition
+    may = u * ((GATE + RS + 3) * np.abs(want_x - x) + np.abs(want_x))
+    compare("x", got_x, want_x, may, xdt)
+    if pre == "no":
+        assert got_h is None
+        return
+    # x' w r: what x' is off by, itself and in its mean square; r and two products
+    r = rstd(want_x)
+    shift = np.sqrt((may * may).mean(-1, keepdims=True)) * r
+    may = may * r * (1 if wn is None else np.abs(wn)) + np.abs(want_h) * (shift + (RS + 2) * u)
+    compare("h", got_h, want_h, may, dt)
 
 
 def compare(name, got, want, may, dtype):
@@ -130,6 +150,38 @@ def test_many_rows_of_the_first_block(D, rows, dt, xdt):
 def test_widths_whose_column_sums_take_just_48_kb(D, dt, xdt):
     # (what a kernel has without asking for more, its own buffer among it)
     check_backward(155, D, dt, xdt, "one", "silu", "weight", "weight", 1.0, repeats=1)
+
+
+# rows, D, type, stream's type, gate, act, norm after, norm before, scale: wide rows, each access
+# width (eights, pairs, single entries) below and above the 4096 columns where the forms change
+WIDE = [
+    (700, 8192, F32, F32, "rows", "silu", "weight", "weight", 1.0),
+    (330, 8190, F32, F32, "one", "sigmoid", "weight", "weight", 0.5),
+    (160, 8191, F32, F32, "one", "silu", "weight", "ones", 1.0),
+    (400, 5120, BF16, F32, "rows", "silu", "weight", "weight", -1.0),
+    (170, 7168, BF16, BF16, "one", "silu", "ones", "weight", 1.0),
+    (200, 4100, BF16, F32, "none", "silu", "weight", "no", 1.0),
+    (333, 6143, BF16, BF16, "rows", "identity", "no", "weight", 0.25),
+    (1100, 4096, F32, F32, "one", "silu", "weight", "weight", 0.5),
+    (900, 2048, F32, F32, "rows", "silu", "weight", "weight", 1.0),
+    (1500, 1536, F32, F32, "rows", "sigmoid", "weight", "weight", 1.0),
+    (2000, 1024, BF16, F32, "one", "identity", "weight", "weight", 1.0),
+    (1300, 1030, F32, F32, "rows", "silu", "weight", "weight", 0.25),
+    (900, 1999, F32, F32, "none", "silu", "weight", "weight", 1.0),
+    (5000, 136, F32, F32, "one", "silu", "weight", "weight", 1.0),
+]
+
+
+@gpu
+@pytest.mark.parametrize("case", WIDE, ids=[f"{c[0]}x{c[1]}" for c in WIDE])
+def test_forward_rounds_as_often_as_its_sums_are_deep(case):
+    check_forward(*case)
+
+
+@gpu
+@pytest.mark.parametrize("case", WIDE, ids=[f"{c[0]}x{c[1]}" for c in WIDE])
+def test_gradients_round_as_often_as_their_sums_are_deep(case):
+    check_backward(*case, repeats=2)
 
 
 # ------------------------------------------------------------------ without a GPU

@@ -71,6 +71,7 @@ struct Plan {
     const float *log_decay;
     int32_t *status;            // the workspace's status word
     bool first;                 // the call's first launch: it sets the status word
+    bool fine;                  // a state goes out: its terms keep fp32's bits
 };
 
 struct Segment {

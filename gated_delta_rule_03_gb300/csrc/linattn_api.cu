@@ -317,6 +317,7 @@ int gdr_linattn_fwd(const gdr_linattn_shape *shape, const void *q, const void *k
     const cudaStream_t s = (cudaStream_t)stream;
     Mix m = mix_of(c, q, c.qs, c.qh, k, c.ks, c.kh, v, c.vs, c.vh, c.dk, c.dv);
     p.first = true;
+    p.fine = S_final != nullptr;
     if (segmented(p)) {
         // (the first segment of a sequence reads S0 while its last one may write S_final)
         if (S0 && S0 == S_final) {
@@ -373,6 +374,7 @@ int gdr_linattn_bwd(const gdr_linattn_shape *shape, const void *d_o, const void 
     k_.s_inter = v_.s_inter = 1.f;
     k_.s_state = v_.s_state = c.scale;
     p.first = true;
+    p.fine = dS0 != nullptr;
     if (segmented(p)) {
         Mix sums[2];
         sums[0] = mix_of(c, nullptr, 0, c.H, k, c.ks, c.kh, v, c.vs, c.vh, c.dk, c.dv);

@@ -17,28 +17,33 @@
 //
 // Rounding. X, Y and Z are used as they are. P and the copy of E are rounded to bf16 once
 // each, as a product's operand has to be; either costs an output element 2^-8 of the sum
-// of its terms' sizes at most, like the output's own rounding. Yw is kept as two bf16
-// parts, 16 bits: a term of the state is off by 2^-16 at most, where one part would cost the
-// outputs as much again as E's own rounding. U is summed chunk by chunk and added to E in
-// fp32: a sum over a whole segment in the tensor cores would lose more.
+// of its terms' sizes at most, like the output's own rounding. Yw is rounded to fp32 and kept
+// as three bf16 parts, which hold that exactly, so that a state that goes out (S_final, dS0) is
+// off by 1 to 5e-7 in norm, like a sum in fp32. Where none goes out, two parts, 16 bits: a term
+// of the state is then off by 2^-16 at most, and only bf16 outputs see it (one part would cost
+// them as much again as E's own rounding). The third part's products take 7 to 22 us of 91 to 302
+// (figures below): 4 x 4096 tokens 84 us with two parts, eight packed prompts 177, 65536 tokens 270.
+// U is summed chunk by chunk and added to E in fp32: a sum over a whole segment in the tensor
+// cores would lose more.
 //
 // What bounds it: a product of two operands in shared memory reads them at all of shared
 // memory's bandwidth (128 x 128 x 16: 8 KB in 64 cycles), and loads, conversions and copies
-// use the same. So P and Yw are A operands in TMEM (512 columns: P, O, U, Yw of 128 each),
-// and Yw goes there straight from Y (ldmatrix turns it) instead of through shared memory.
+// use the same. So P and Yw are A operands in TMEM (512 columns: P, O, U, Yw of 128 each; Yw's
+// third part in columns of O and U that the chunk leaves free), and Yw goes there straight from
+// Y (ldmatrix turns it) instead of through shared memory.
 //
 // Shared memory: X, Y and Z tiles of two chunks (TMA, 128-byte swizzle), E in bf16.
 // Warp 17 issues the MMAs in the order P Z, X E, P of the next chunk, U. Warps 0-15 all do
 // the same work on a sixteenth each (a lane quarter by 32 columns or tokens), in the order
 // in which the products end: the output rows, P's weights of the next chunk, the state, Yw of
-// the next chunk. Warp 16: the loads. With 96 registers a thread nothing may spill (shared
+// the next chunk. Warp 16: the loads. With 96 registers a thread next to nothing may spill (shared
 // memory leaves no first-level cache to spill to): hence 16 columns at a time, and
-// what would be worked out ahead of the loop made opaque.
+// what would be worked out ahead of the loop made opaque. (8 bytes do, outside the loop.)
 //
 // Measured: 4 sequences of 4096 tokens, 16 heads, d_k = d_v = 128 (273 MB, two segments each)
-// in 83 us with the sums, 3.3 TB/s: a chunk takes 2.5 us, the chain of its products and what lies
-// between them, with the tensor cores busy 37 % of the time and the schedulers 46 %. Where all
-// 152 SMs run and every tile comes from DRAM (128 KB a chunk) memory bounds it: 2.9 us.
+// in 91 us with the sums, 3.0 TB/s: a chunk takes 2.8 us (2.5 with two parts), the chain of its
+// products and what lies between them, with neither the tensor cores nor the schedulers busy half
+// of the time. Where all 152 SMs run and every tile comes from DRAM (128 KB a chunk) it takes 3.1.
 #include <mutex>
 
 #include "linattn.cuh"
@@ -119,16 +124,19 @@ __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
     return d;
 }
 
-// The weights of the 32 tokens that a warp weighs, of a chunk of n, as two bf16 parts:
-// table[i] holds the larger parts of tokens 32 sub + 2i and the one after, then the smaller
-// ones. Each warp has a table of its own.
+// The weights of the 32 tokens that a warp weighs, of a chunk of n: table[i] holds those of tokens
+// 32 sub + 2i and the one after, in fp32 (kFine) or as two bf16 parts, the larger ones of both
+// tokens, then the smaller ones. Each warp has a table of its own.
+template <bool kFine>
 __device__ __forceinline__ void row_weights(uint2 *table, int n, bool backward, float l2, float s, int sub, int lane) {
     __syncwarp();
     const int r = 32 * sub + 2 * (lane & 15);
     const float x = s * decay_pow(l2, (float)(backward ? r + 1 : max(n - 1 - r, 0)));
     const float y = s * decay_pow(l2, (float)(backward ? r + 2 : max(n - 2 - r, 0)));
     const float hx = __bfloat162float(__float2bfloat16_rn(x)), hy = __bfloat162float(__float2bfloat16_rn(y));
-    if (lane < 16) table[lane] = make_uint2(pack_bf16x2(hx, hy), pack_bf16x2(x - hx, y - hy));
+    if (lane < 16)
+        table[lane] = kFine ? make_uint2(__float_as_uint(x), __float_as_uint(y))
+                            : make_uint2(pack_bf16x2(hx, hy), pack_bf16x2(x - hx, y - hy));
     __syncwarp();
 }
 
@@ -168,13 +176,31 @@ __device__ __forceinline__ void tmem_store8_nowait(uint32_t taddr, const uint32_
 }
 __device__ __forceinline__ void tmem_store_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
+// Two bf16 minus two fp32.
+__device__ __forceinline__ float2 minus(uint32_t a, float2 x) {
+    float2 d;
+    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\t"
+        "sub.rn.f32.bf16 %0, l, %3;\n\tsub.rn.f32.bf16 %1, h, %4;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "r"(a), "f"(x.x), "f"(x.y));
+    return d;
+}
+// Two fp32 cut to their upper halves, bf16.
+__device__ __forceinline__ uint32_t cut_bf16x2(float2 x) {
+    return __byte_perm(__float_as_uint(x.x), __float_as_uint(x.y), 0x7632);
+}
+
 // Yw of 32 tokens into TMEM: lane = column of Y, TMEM column = two tokens, the larger parts
 // at `taddr`, the smaller ones 64 columns on. With a weight w = wh + wl (bf16 each),
-// hi = round(y wh), lo = y wh - hi (exact: what is left of 16 bits) + y wl. A warp takes the
-// 32 columns of its lane quarter and the tokens 32 sub ..; ldmatrix hands each thread two
-// tokens of one column, as the store wants them.
+// hi = round(y wh), lo = y wh - hi (exact: what is left of 16 bits) + y wl. kFine: y w, rounded
+// to fp32, is cut into three parts of 8 bits each that hold it exactly: hi, minus lo, and the
+// rest at `third`. (The mixed-precision subtractions keep the ALU free for the cuts; with masks
+// instead, eight packed prompts took 211 us, not 200.) A warp takes the 32 columns of its lane
+// quarter and the tokens 32 sub ..; ldmatrix hands each thread two tokens of one column, as the
+// store wants them.
+template <bool kFine>
 __device__ __forceinline__ void weigh(uint32_t y, uint32_t taddr, int quarter, int sub, int n,
-                                      const uint2 *table, int lane) {
+                                      const uint2 *table, int lane, uint32_t third) {
     const int mat = lane >> 3;
     const int token = 32 * sub + (mat >> 1) * 8 + (lane & 7);
     uint2 w[4];  // of two tokens each
@@ -200,15 +226,31 @@ __device__ __forceinline__ void weigh(uint32_t y, uint32_t taddr, int quarter, i
 #pragma unroll
         for (int jj = 0; jj < 2; ++jj) {
             uint32_t hi[4], lo[4];
+            if constexpr (kFine) {
+                uint32_t rest[4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const __nv_bfloat162 v = reinterpret_cast<const __nv_bfloat162 &>(r[jj][e]);
-                const __nv_bfloat162 wh = reinterpret_cast<const __nv_bfloat162 &>(w[2 * jj + (e >> 1)].x);
-                const __nv_bfloat162 wl = reinterpret_cast<const __nv_bfloat162 &>(w[2 * jj + (e >> 1)].y);
-                const __nv_bfloat162 h = __hmul2_rn(v, wh);
-                const __nv_bfloat162 l = __hfma2(v, wl, __hfma2(v, wh, __hneg2(h)));
-                hi[e] = reinterpret_cast<const uint32_t &>(h);
-                lo[e] = reinterpret_cast<const uint32_t &>(l);
+                for (int e = 0; e < 4; ++e) {
+                    const uint2 we = w[2 * jj + (e >> 1)];
+                    float2 x = make_float2(__uint_as_float(r[jj][e] << 16), __uint_as_float(r[jj][e] & 0xffff0000u));
+                    x = mul2(x, make_float2(__uint_as_float(we.x), __uint_as_float(we.y)));
+                    hi[e] = cut_bf16x2(x);
+                    x = minus(hi[e], x);  // minus what is left ..
+                    lo[e] = cut_bf16x2(x);
+                    x = minus(lo[e], x);  // .. and what is left after that
+                    rest[e] = cut_bf16x2(x);
+                }
+                tmem_store_16x128b_x2(third + ((uint32_t)m0 << 16) + 8 * jj, rest);
+            } else {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const __nv_bfloat162 v = reinterpret_cast<const __nv_bfloat162 &>(r[jj][e]);
+                    const __nv_bfloat162 wh = reinterpret_cast<const __nv_bfloat162 &>(w[2 * jj + (e >> 1)].x);
+                    const __nv_bfloat162 wl = reinterpret_cast<const __nv_bfloat162 &>(w[2 * jj + (e >> 1)].y);
+                    const __nv_bfloat162 h = __hmul2_rn(v, wh);
+                    const __nv_bfloat162 l = __hfma2(v, wl, __hfma2(v, wh, __hneg2(h)));
+                    hi[e] = reinterpret_cast<const uint32_t &>(h);
+                    lo[e] = reinterpret_cast<const uint32_t &>(l);
+                }
             }
             tmem_store_16x128b_x2(to + 8 * jj, hi);
             tmem_store_16x128b_x2(to + 64 + 8 * jj, lo);
@@ -252,12 +294,28 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t db, uint
         : "memory");
 }
 
-// The MMAs of U: the smaller part first.
-__device__ __forceinline__ void issue_update(uint32_t d, uint32_t y, uint32_t z, uint32_t idesc) {
+// The MMAs of U: the smaller parts first. kFine: three parts, the smallest at `third`, in 16 columns
+// of every kApart, and minus the middle one (kNegateA, in the instruction's descriptor).
+constexpr uint32_t kNegateA = 1u << 13;
+template <bool kFine, int kApart>
+__device__ __forceinline__ void issue_update(uint32_t d, uint32_t y, uint32_t z, uint32_t idesc, uint32_t third) {
+    if (kFine) {
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk) mma_ts(d, third + kApart * (kk >> 1) + 8 * (kk & 1), z, kk * 2048, idesc, kk > 0);
+    }
 #pragma unroll
     for (int i = 1; i >= 0; --i)
 #pragma unroll
-        for (int kk = 0; kk < 8; ++kk) mma_ts(d, y + 64 * i + 8 * kk, z, kk * 2048, idesc, i == 0 || kk > 0);
+        for (int kk = 0; kk < 8; ++kk)
+            mma_ts(d, y + 64 * i + 8 * kk, z, kk * 2048, kFine && i == 1 ? idesc | kNegateA : idesc, kFine || i == 0 || kk > 0);
+}
+
+// lam^n for n tokens that a state is carried over, rounded once where it is near 1: the hardware's
+// exponential is off by 2^-22, the same way every time, which adds up over the chunks of a long
+// sequence (65536 tokens: states off by 1.4e-6 with it).
+__device__ __forceinline__ float carried(float l2, int n) {
+    const float x = l2 * (float)n;
+    return x > -0.5f ? 1.f + expm1f(x * 0.69314718056f) : exp2f(x);
 }
 
 // E <- w E + 32 columns of this thread's TMEM lane.
@@ -353,8 +411,11 @@ enum { B_FULL = 0, B_EMPTY = kSlots, B_P = 2 * kSlots, B_PREADY, B_A, B_YREADY, 
 
 // One body for both directions, its loops kept rolled where they can be: the warps of a
 // block run far apart in the code, and a copy of it per direction or role costs more in
-// instruction fetches than the selects do (gradients: 2.5 times the time with three copies).
-__global__ void __launch_bounds__(kThreads, 1) mix_tc_kernel(const __grid_constant__ TcArgs A) {
+// instruction fetches than the selects do (gradients: 2.5 times the time with three copies). kFine:
+// a state goes out, Yw has three parts. Two loops in one kernel, the second with three parts for the
+// chunks near the end alone, were slower than three parts throughout (prompts of 4 x 4096 120 us,
+// 91), and so was a choice chunk by chunk (97).
+template <bool kFine> __global__ void __launch_bounds__(kThreads, 1) mix_tc_kernel(const __grid_constant__ TcArgs A) {
     extern __shared__ __align__(1024) unsigned char sm[];
     const uint32_t base = smem_u32(sm);
     __shared__ Segment found;
@@ -362,6 +423,7 @@ __global__ void __launch_bounds__(kThreads, 1) mix_tc_kernel(const __grid_consta
     __shared__ uint32_t tmem_slot;
     __shared__ int gave_up;
     __shared__ int kept_slice;  // (for the end, in no register meanwhile)
+    __shared__ float shrink[2];  // kFine: lam^n over a whole chunk and the last one
     __shared__ uint2 weights[kWorkers][16];
     __shared__ __align__(16) float step_of[32];  // lam^(31-j), or lam^j from last to first
     __shared__ float pow_of[63];                  // lam^(i-31), 0 for i < 31
@@ -416,7 +478,9 @@ __global__ void __launch_bounds__(kThreads, 1) mix_tc_kernel(const __grid_consta
     if (tid < 32) {
         step_of[tid] = decay_pow(l2_of_head, (float)(back ? tid : 31 - tid));
         pow_of[31 + tid] = decay_pow(l2_of_head, (float)tid);
+        if (kFine && tid < 2) shrink[tid] = carried(l2_of_head, tid ? tail : C);
         if (tid < 31) pow_of[tid] = 0.f;
+        __syncwarp();
         tmem_alloc(smem_u32(&tmem_slot), TM_COLS);
         tmem_relinquish();
     }
@@ -424,6 +488,10 @@ __global__ void __launch_bounds__(kThreads, 1) mix_tc_kernel(const __grid_consta
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = tmem_slot;
+    // kFine: O and U of a chunk share columns, in turn the two halves of TM_O and TM_U: U starts when
+    // O has been read. The half of the other chunks is free then, and holds Yw's smallest part.
+    auto o_at = [](int cc) -> uint32_t { return kFine ? TM_O + 128 * (cc & 1) : TM_O; };
+    auto u_at = [&](int cc) -> uint32_t { return kFine ? o_at(cc) : TM_U; };
     // A bounded wait: the first that runs out ends the others too.
     volatile int *stop = &gave_up;
     auto wait = [&](int b, int phase) -> bool {
@@ -497,9 +565,11 @@ __global__ void __launch_bounds__(kThreads, 1) mix_tc_kernel(const __grid_consta
         int weighed = 0;  // the length that the weights are for
         auto weigh_chunk = [&](int cc) -> bool {
             const int n = tokens_of(chunk_of(cc)), sy = slot(cc, 1);
-            if (n != weighed) row_weights(weights[warp], weighed = n, back, l2, m.s_state, sub, lane);
+            if (n != weighed) row_weights<kFine>(weights[warp], weighed = n, back, l2, m.s_state, sub, lane);
             if (!warp_wait(B_FULL + sy, phase(cc))) return false;
-            if (quarter < 2 * m.xb) weigh(base + sy * TILE, tmem + TM_Y, quarter, sub, n, weights[warp], lane);
+            // (the smallest part: into this warp's own block of U of the chunk before, which it has read)
+            if (quarter < 2 * m.xb)
+                weigh<kFine>(base + sy * TILE, tmem + TM_Y, quarter, sub, n, weights[warp], lane, tmem + o_at(cc + 1) + col);
             tmem_store_wait();
             tc_fence_before();
             arrive(B_EMPTY + sy);
@@ -594,8 +664,8 @@ __global__ void __launch_bounds__(kThreads, 1) mix_tc_kernel(const __grid_consta
             if (!warp_wait(B_O, cc)) return false;
             tc_fence_after();
             uint32_t o[2][16];
-            tmem_fetch16(lanes + TM_O + col, o[0]);
-            tmem_fetch16(lanes + TM_O + col + 16, o[1]);
+            tmem_fetch16(lanes + o_at(cc) + col, o[0]);
+            tmem_fetch16(lanes + o_at(cc) + col + 16, o[1]);
             tmem_arrived(o[0]);
             tmem_arrived(o[1]);
             tc_fence_before();
@@ -661,7 +731,8 @@ __global__ void __launch_bounds__(kThreads, 1) mix_tc_kernel(const __grid_consta
             if (cc >= 0 && need(cc)) {
                 if (!(ok = warp_wait(B_U, cc))) break;
                 tc_fence_after();
-                if (has_z) add_update(E, ex2(l2 * (float)tokens_of(chunk_of(cc))), lanes + TM_U + col);
+                const int n = tokens_of(chunk_of(cc));
+                if (has_z) add_update(E, kFine ? shrink[n < C] : ex2(l2 * (float)n), lanes + u_at(cc) + col);
                 tc_fence_before();
             }
             if (!more) break;
@@ -745,24 +816,27 @@ __global__ void __launch_bounds__(kThreads, 1) mix_tc_kernel(const __grid_consta
             const bool need = cc + 1 < chunks || ends;
             const int sx = slot(cc, 0), sz = slot(cc, 2);
             const uint32_t x = desc_k(base + sx * TILE), z = desc_mn(base + sz * TILE);
-            ok = wait(B_FULL + sz, phase(cc)) && wait(B_PREADY, cc) && (cc == 0 || wait(B_OFREE, cc - 1));
+            // (the accumulator is free: O of the chunk before has been read, or (kFine) U of the chunk
+            // before, whose smallest part lay there, is complete)
+            ok = wait(B_FULL + sz, phase(cc)) && wait(B_PREADY, cc) && (cc == 0 || wait(kFine ? B_U : B_OFREE, cc - 1));
             if (!ok) break;
+            const uint32_t o = tmem + o_at(cc);
             tc_fence_after();
 #pragma unroll
             for (int kk = 0; kk < 8; ++kk)
-                mma_ts(tmem + TM_O, tmem + TM_P + 32 * (kk >> 1) + 8 * (kk & 1), z, kk * 2048, id_o, kk > 0);
+                mma_ts(o, tmem + TM_P + 32 * (kk >> 1) + 8 * (kk & 1), z, kk * 2048, id_o, kk > 0);
             mma_commit(bar(B_A));
             if (!(ok = wait(B_EREADY, cc))) break;
             tc_fence_after();
 #pragma unroll
             for (int kk = 0; kk < 8; ++kk)
-                if (kk < 4 || wide) mma_ss(tmem + TM_O, x, (kk >> 2) * BLOCK + (kk & 3) * 32, E, kk * 2048, id_o, true);
+                if (kk < 4 || wide) mma_ss(o, x, (kk >> 2) * BLOCK + (kk & 3) * 32, E, kk * 2048, id_o, true);
             mma_commit(bar(B_O));
             if (cc + 1 < chunks && !(ok = scores(cc + 1))) break;
             if (need) {
-                if (!(ok = wait(B_YREADY, cc))) break;
+                if (!(ok = wait(B_YREADY, cc) && (!kFine || wait(B_OFREE, cc)))) break;
                 tc_fence_after();
-                issue_update(tmem + TM_U, tmem + TM_Y, z, id_u);
+                issue_update<kFine, 32>(tmem + u_at(cc), tmem + TM_Y, z, id_u, tmem + o_at(cc + 1));
                 mma_commit(bar(B_U));
             }
             mma_commit(bar(B_EMPTY + sz));
@@ -781,15 +855,15 @@ __global__ void __launch_bounds__(kThreads, 1) mix_tc_kernel(const __grid_consta
 
 constexpr int kSumThreads = kWorkThreads + 64;
 constexpr uint32_t kSumSmem = kSlots * TILE;
-constexpr uint32_t TM_SUM_Y = 256;  // two buffers of U, then of Yw
 enum { S_FULL = 0, S_EMPTY = kSlots, S_READY = 2 * kSlots, S_U = S_READY + 2,
        S_UFREE = S_U + 2, S_DRAIN = S_UFREE + 2, S_COUNT };
 
 // R_f of every segment but the last from the side that the state comes from: U chunk by
-// chunk as in the mix, with two buffers each of U and Yw, so that a chunk is weighed while
-// the products of the one before it run. 1.2 us a chunk: bound by reading Y and Z, 64 KB, where
-// all SMs run.
-__global__ void __launch_bounds__(kSumThreads, 1) sum_tc_kernel(const __grid_constant__ TcArgs A) {
+// chunk as in the mix, with two buffers of Yw, so that a chunk is weighed while the products of
+// the one before it run, and two of U. With three parts of Yw (kFine) there are columns for one U:
+// its products wait until the one before has been read. 1.2 us a chunk: bound by reading Y and Z,
+// 64 KB, where all SMs run; with three parts 1.6.
+template <bool kFine> __global__ void __launch_bounds__(kSumThreads, 1) sum_tc_kernel(const __grid_constant__ TcArgs A) {
     extern __shared__ __align__(1024) unsigned char sm[];
     const uint32_t base = smem_u32(sm);
     __shared__ Segment found;
@@ -797,6 +871,7 @@ __global__ void __launch_bounds__(kSumThreads, 1) sum_tc_kernel(const __grid_con
     __shared__ uint32_t tmem_slot;
     __shared__ int gave_up;
     __shared__ uint2 weights[kWorkers][16];
+    __shared__ float shrink[2];
     auto bar = [&](int i) { return smem_u32(&bars[i]); };
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int role = (int)(blockIdx.x % A.count);
@@ -816,6 +891,8 @@ __global__ void __launch_bounds__(kSumThreads, 1) sum_tc_kernel(const __grid_con
     const int64_t sum = (s.sum0 + s.f - m.backward) * A.p.split + part;
     const float l2 = log2_decay(A.p.log_decay[h]);
     const int chunks = (int)((s.tokens + C - 1) / C);
+    auto u_at = [&](int cc) -> uint32_t { return kFine ? 0 : 128 * (cc & 1); };
+    auto y_at = [&](int cc) -> uint32_t { return kFine ? 128 + 192 * (cc & 1) : 256 + 128 * (cc & 1); };
     auto chunk_of = [&](int cc) { return m.backward ? chunks - 1 - cc : cc; };
     auto tokens_of = [&](int c) {
         const int64_t r = s.tokens - (int64_t)c * C;
@@ -837,6 +914,8 @@ __global__ void __launch_bounds__(kSumThreads, 1) sum_tc_kernel(const __grid_con
         gave_up = 0;
     }
     if (tid < 32) {
+        if (kFine && tid < 2) shrink[tid] = carried(l2, tid ? tokens_of(chunks - 1) : C);
+        __syncwarp();
         tmem_alloc(smem_u32(&tmem_slot), TM_COLS);
         tmem_relinquish();
     }
@@ -878,7 +957,7 @@ __global__ void __launch_bounds__(kSumThreads, 1) sum_tc_kernel(const __grid_con
         for (int cc = 0; ok && cc <= chunks; ++cc) {
             if (cc < chunks) {
                 const int n = tokens_of(chunk_of(cc)), ty = 2 * cc, tz = ty + 1;
-                if (n != weighed) row_weights(weights[warp], weighed = n, m.backward, l2, m.s_state, sub, lane);
+                if (n != weighed) row_weights<kFine>(weights[warp], weighed = n, m.backward, l2, m.s_state, sub, lane);
                 if (!(ok = warp_wait(S_FULL + ty % kSlots, ty / kSlots))) break;
                 if (n < C) {
                     if (!(ok = warp_wait(S_FULL + tz % kSlots, tz / kSlots))) break;
@@ -887,7 +966,8 @@ __global__ void __launch_bounds__(kSumThreads, 1) sum_tc_kernel(const __grid_con
                 }
                 // (the buffer is free: U of chunk cc - 2 has been read below)
                 if (quarter < 2 * m.xb)
-                    weigh(base + slot(ty), tmem + TM_SUM_Y + 128 * (cc & 1), quarter, sub, n, weights[warp], lane);
+                    weigh<kFine>(base + slot(ty), tmem + y_at(cc), quarter, sub, n, weights[warp], lane,
+                                 tmem + y_at(cc) + 128 + 16 * sub);
                 tmem_store_wait();
                 tc_fence_before();
                 arrive(S_EMPTY + ty % kSlots);
@@ -897,7 +977,8 @@ __global__ void __launch_bounds__(kSumThreads, 1) sum_tc_kernel(const __grid_con
             const int b = cc - 1;  // the chunk before: its U
             if (!(ok = warp_wait(S_U + (b & 1), b >> 1))) break;
             tc_fence_after();
-            if (has_z) add_update(E, decay_pow(l2, (float)tokens_of(chunk_of(b))), lanes + 128 * (b & 1) + col);
+            const int n = tokens_of(chunk_of(b));
+            if (has_z) add_update(E, kFine ? shrink[n < C] : decay_pow(l2, (float)n), lanes + u_at(b) + col);
             tc_fence_before();
             arrive(S_UFREE + (b & 1));
         }
@@ -932,10 +1013,11 @@ __global__ void __launch_bounds__(kSumThreads, 1) sum_tc_kernel(const __grid_con
         for (int cc = 0; cc < chunks; ++cc) {
             const int tz = 2 * cc + 1;
             if (!wait(S_FULL + tz % kSlots, tz / kSlots)) break;
-            if (cc >= 2 && !wait(S_UFREE + (cc & 1), (cc >> 1) - 1)) break;
+            const int reader = cc - (kFine ? 1 : 2);  // the chunk whose U has to have been read
+            if (reader >= 0 && !wait(S_UFREE + (reader & 1), reader >> 1)) break;
             if (!wait(S_READY + (cc & 1), cc >> 1)) break;
             tc_fence_after();
-            issue_update(tmem + 128 * (cc & 1), tmem + TM_SUM_Y + 128 * (cc & 1), desc_mn(base + slot(tz)), id_u);
+            issue_update<kFine, 16>(tmem + u_at(cc), tmem + y_at(cc), desc_mn(base + slot(tz)), id_u, tmem + y_at(cc) + 128);
             mma_commit(bar(S_U + (cc & 1)));
             mma_commit(bar(S_EMPTY + tz % kSlots));
         }
@@ -1045,8 +1127,9 @@ int launch_mix_tc(const Plan &p, const Mix *mixes, int count, int d_v, bool sums
         m.s_state = s.s_state;
         m.start = s.start; m.end = s.end; m.R = s.R; m.R_out = s.R_out;
     }
-    if (sums) return run(sum_tc_kernel, A, p.handing * p.split, kSumThreads, kSumSmem, false, stream);
-    return run(mix_tc_kernel, A, p.units, kThreads, kSmem, !p.first, stream);
+    if (sums)
+        return run(p.fine ? sum_tc_kernel<true> : sum_tc_kernel<false>, A, p.handing * p.split, kSumThreads, kSumSmem, false, stream);
+    return run(p.fine ? mix_tc_kernel<true> : mix_tc_kernel<false>, A, p.units, kThreads, kSmem, !p.first, stream);
 }
 
 }  // namespace linattn

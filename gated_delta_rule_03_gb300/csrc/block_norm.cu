@@ -296,9 +296,12 @@ template <typename T, int VEC, int PER> __host__ __device__ constexpr bool fetch
 
 // Sums over this block's rows go to part[which][blockIdx.x * blockDim.y + threadIdx.y][D]. The
 // next row's inputs are on their way to shared memory while a row is worked on (in registers
-// they would halve the warps, and the instructions, 86 per thread and entry, need the warps).
-// Bound by its instructions, 690 per warp and 256 entries: 16384 x 2048 bf16, 537 MB, in 127 us
-// with the column sums, 4.2 TB/s.
+// they would halve the warps, and the instructions, 89 per thread and entry, need the warps).
+// 16384 x 2048 bf16, 537 MB, takes 127 us with the column sums, 4.2 TB/s, with two thirds of the
+// issue slots and half of DRAM in use: the row's sums and the reads from shared memory leave
+// gaps that 24 warps on an SM do not fill. With 80 registers 16 bytes are spilled (64 would take
+// a fourth block and spill more: 151 us, 130 at that time). In fp32 shared memory
+// holds 16 warps on an SM: 8192 x 2048, 537 MB, in 180 us, 3.0 TB/s.
 // Rows wider than 4096 keep their columns' sums in shared memory instead. One gate row for all:
 // with A = the sum over rows of s dx' n, dw_post is act(gate) A and dgate is act'(gate) w_post A.
 template <typename T, typename TX, int VEC, int PER, int THREADS>

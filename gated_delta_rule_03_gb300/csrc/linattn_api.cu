@@ -67,15 +67,16 @@ int columns(const Call &c, bool backward) {
 
 // How sequences are cut, by a model of the time in microseconds: a launch takes rounds of 152
 // blocks. Tensor cores: a tile of 128 tokens takes 2.5 us in a mix and 1.2 in a sum, a block 8 to
-// start and end, and reads a sum in 1; the second launch costs 4. fp32 arithmetic: tiles of 64
+// start and end, and reads a sum in 1; the second launch costs 4. (Where a state goes out both
+// take 0.3 longer; the choice is the same.) fp32 arithmetic: tiles of 64
 // tokens, 9 and 4 us, 3 to start, 2 a sum. Blocks of different lengths filling up an SM take
-// 1.2 times their sum, and half a block's time is lost at the end. Measured:
-//   4 x 4096 x 16 heads: 1, 2, 3, 4 segments 92, 89, 105, 111 us
-//   65536 x 16 chains: 5, 7, 9, 10 segments 411, 313, 263, 368 us
-//   192 chains of 4096 (a backward call): all whole 179 us, 150 of them whole and 42 in three 150
-//   eight packed sequences, 40,000 tokens, 16 heads, segments of 24 and of 72 tiles: all equal 192
-//   and 143 us, the longest 1.6 times the mean 237 and 187, twice 234 and 230, 4 times 191 and
-//   257; with 4 heads 11 tiles 82 us, 72 tiles 171
+// 1.2 times their sum, and half a block's time is lost at the end. Measured, with the state:
+//   4 x 4096 x 16 heads: 1, 2, 3, 4 segments 104, 90, 114, 121 us (without it 89, 80, 100, 107)
+//   65536 x 16 chains: 5, 7, 9, 10 segments 477, 360, 301, 428 us (414, 317, 267, 376)
+//   192 chains of 4096 (a backward call): all whole 180 us, 150 of them whole and 42 in three 150
+//   eight packed sequences, 40,000 tokens, 16 heads, segments of 24 and of 72 tiles: all equal 208
+//   and 145 us, the longest 1.6 times the mean 210 and 206, twice 256 and 284, 4 times 210 and
+//   285; with 4 heads 11 tiles 76 us, 72 tiles 129
 struct Cost {
     int tile;
     double mix, sum, start, read;

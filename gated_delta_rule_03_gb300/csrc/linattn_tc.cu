@@ -38,7 +38,7 @@
 // in which the products end: the output rows, P's weights of the next chunk, the state, Yw of
 // the next chunk. Warp 16: the loads. With 96 registers a thread next to nothing may spill (shared
 // memory leaves no first-level cache to spill to): hence 16 columns at a time, and
-// what would be worked out ahead of the loop made opaque. (8 bytes do, outside the loop.)
+// what would be worked out ahead of the loop made opaque. (8 bytes do.)
 //
 // Measured: 4 sequences of 4096 tokens, 16 heads, d_k = d_v = 128 (273 MB, two segments each)
 // in 91 us with the sums, 3.0 TB/s: a chunk takes 2.8 us (2.5 with two parts), the chain of its

@@ -463,6 +463,10 @@ size_t gdr_linattn_bwd_workspace_size(const gdr_linattn_shape *shape);
  *   S_final     [num_seqs, H, d_k, d_v] fp32 (written), or NULL. It may be S0's buffer;
  *               any other overlap of an output is rejected.
  *   workspace   as for gdr_chunk_fwd; calls that share one must be ordered on one stream
+ * All sums and states are fp32. bf16 inputs: the scores of a block of 128 tokens and the copy
+ * of the state that enters it are rounded to bf16 once each, as operands of a product; S_final
+ * (and dS0 of the backward call) keep the precision of fp32 sums. A state's part of an output
+ * that has decayed below 2^-60 within a block counts for up to 2^-60 of it instead.
  * A value that is not finite in a token's q, k or v stays within its sequence and head,
  * but may reach other tokens of it, before the token too (up to 127 of them: products are
  * taken over blocks of tokens).

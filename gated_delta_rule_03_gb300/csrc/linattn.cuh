@@ -70,7 +70,8 @@ struct Plan {
     int H;
     const float *log_decay;
     int32_t *status;            // the workspace's status word
-    bool first;                 // the call's first launch: it sets the status word
+    bool first;                 // the launch sets the status word (the call's first, unless `checked`)
+    bool checked;               // launch_check has run: the status word says whether the offsets are ones
     bool fine;                  // a state goes out: its terms keep fp32's bits
 };
 
@@ -89,12 +90,18 @@ struct Segment {
 // lengths: first the pairs that stay whole, then the segments one after the other. Called
 // by the whole block (a barrier inside). With cu_seqlens every block checks all of it (offsets
 // from 0, not decreasing, at most total_tokens); where it is not so, no block does anything:
-// false. Up to kOrdered sequences are taken longest first, so that short ones fill up the end
-// of the launch (a sequence's place takes a look at every other, hence the limit). In this and
-// in the order of memory: 8 of 1,611 to 7,848 tokens, shortest first, 32 heads 267 and 300 us; 31
-// of 900 and one of 6,000, 16 heads 173 and 215, backward with 32 heads 800 and 755. `scratch`:
-// 2 kOrdered ints of shared memory.
-constexpr int kOrdered = 64;
+// false. Beyond kChecked sequences a launch ahead has done that (launch_check). Up to kOrdered
+// sequences are taken longest first, so that short ones fill up the end of the launch (a
+// sequence's place takes a look at every other, hence the limit). In this and in the order of
+// memory: 8 of 1,611 to 7,848 tokens, shortest first, 32 heads 267 and 300 us; 31 of 900 and one of
+// 6,000, 16 heads 173 and 215, backward with 32 heads 800 and 755. Of more, sequence n has the
+// places from n + floor(cu[n] / seg) on (of those that hand a sum on: from floor(cu[n] / seg)): as
+// many as it needs or one more, up to where the next one's begin and the last one's at the launch's
+// end. So the pass that checks finds a place's sequence, and so does a search where there is no such
+// pass, without counting places up (20,000 sequences of one token, two heads 2.1 ms, with places
+// counted and offsets checked by every block 12.0; 1000 of 60, 16 heads 0.91 and 1.06).
+// `scratch`: 2 kOrdered ints of shared memory.
+constexpr int kOrdered = 64, kChecked = 2048;
 __device__ __forceinline__ bool locate(const Plan &p, int64_t unit, int handing, Segment *shared, int *scratch) {
     const int skip = handing == 2;  // segments in front of the first item's
     const int less = handing != 0;
@@ -126,58 +133,88 @@ __device__ __forceinline__ bool locate(const Plan &p, int64_t unit, int handing,
         return true;
     }
     const int64_t item = unit / p.H;
-    __shared__ int64_t warp_sum[32];
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = (blockDim.x + 31) >> 5;
+    const int tid = threadIdx.x;
     if (tid == 0) shared->seq = -1;
-    const bool ordered = p.num_seqs <= kOrdered;
-    if (ordered) {
-        int *lens = scratch + kOrdered;
-        const int mine = tid < p.num_seqs ? p.cu_seqlens[tid + 1] - p.cu_seqlens[tid] : 0;
-        if (tid < p.num_seqs) lens[tid] = mine;
-        __syncthreads();
-        if (tid < p.num_seqs) {
-            int rank = 0;
-            for (int j = 0; j < (int)p.num_seqs; ++j) rank += lens[j] > mine || (lens[j] == mine && j < tid);
-            scratch[rank] = tid;
-        }
-        __syncthreads();
-    }
-    int64_t carry = 0;
-    int wrong = 0;
-    for (int64_t base = 0; base < p.num_seqs; base += blockDim.x) {
-        const int64_t i = base + tid;  // place in the order
-        int64_t n = i, a = 0, len = 0, count = 0;
-        if (i < p.num_seqs) {
-            if (ordered) n = scratch[i];
-            a = p.cu_seqlens[n];
-            len = (int64_t)p.cu_seqlens[n + 1] - a;
-            if (len < 0 || a < 0 || a + len > p.total_tokens || (n == 0 && a != 0)) {
-                wrong = 1;
-            } else {
-                count = (len + p.seg - 1) / p.seg;
-                if (count < 1) count = 1;  // an empty sequence still hands on its state
-                count -= less;
+    if (p.num_seqs > kOrdered) {
+        int64_t n = -1;  // the sequence whose places `item` is among, in one thread
+        if (p.checked) {
+            if (__syncthreads_or(tid == 0 && *p.status != GDR_OK)) return false;
+            // the last one whose places begin at `item` or before it: every thread looks at one of as
+            // many, evenly apart, in each round
+            int64_t from = 0, left = p.num_seqs;
+            while (left > 1) {
+                const int64_t apart = (left + blockDim.x - 1) / blockDim.x, at = from + tid * apart;
+                bool begun = false;
+                if (at < from + left) {
+                    const int64_t place = item - (less ? 0 : at);  // floor(cu[at] / seg) <= place
+                    begun = place >= 0 && p.cu_seqlens[at] < (place + 1) * p.seg;
+                }
+                const int64_t last = __syncthreads_count(begun) - 1;
+                left = left - last * apart < apart ? left - last * apart : apart;
+                from += last * apart;
             }
+            if (tid == 0) n = from;
+        } else {
+            int wrong = 0;
+#pragma unroll 4
+            for (int64_t i = tid; i < p.num_seqs; i += blockDim.x) {
+                const int64_t a = p.cu_seqlens[i], b = p.cu_seqlens[i + 1];
+                if (b < a || a < 0 || b > p.total_tokens || (i == 0 && a != 0)) wrong = 1;
+                // floor(a / seg) <= place < floor(b / seg), or one more for each sequence
+                const int64_t place = item - (less ? 0 : i);
+                if (place >= 0 && a < (place + 1) * p.seg && b >= (place + less) * p.seg) n = i;
+            }
+            if (__syncthreads_or(wrong)) return false;
         }
-        int64_t sum = count;
-#pragma unroll
-        for (int off = 1; off < 32; off <<= 1) {
-            const int64_t up = __shfl_up_sync(0xffffffffu, sum, off);
-            if (lane >= off) sum += up;
+        if (n >= 0) {
+            const int64_t a = p.cu_seqlens[n], len = (int64_t)p.cu_seqlens[n + 1] - a, first = a / p.seg;
+            int64_t count = (len + p.seg - 1) / p.seg;
+            if (count < 1) count = 1;  // an empty sequence still hands on its state
+            const int64_t f = item - (less ? 0 : n) - first;
+            if (f < count - less) fill((int)n, (int)(unit % p.H), (int)f + skip, (int)count, a, len, first);
         }
-        if (lane == 31) warp_sum[warp] = sum;
         __syncthreads();
-        int64_t before = 0, total = 0;
-        for (int w = 0; w < warps; ++w) {
-            if (w < warp) before += warp_sum[w];
-            total += warp_sum[w];
-        }
-        const int64_t first_item = carry + before + sum - count;
-        if (count > 0 && item >= first_item && item < first_item + count)
-            fill((int)n, (int)(unit % p.H), (int)(item - first_item) + skip, (int)count + less, a, len, first_item - (less ? 0 : i));
-        carry += total;
-        __syncthreads();
+        return true;
     }
+    const int lane = tid & 31, warp = tid >> 5;
+    __shared__ int64_t warp_sum[32];
+    int *lens = scratch + kOrdered;
+    const int mine = tid < p.num_seqs ? p.cu_seqlens[tid + 1] - p.cu_seqlens[tid] : 0;
+    if (tid < p.num_seqs) lens[tid] = mine;
+    __syncthreads();
+    if (tid < p.num_seqs) {
+        int rank = 0;
+        for (int j = 0; j < (int)p.num_seqs; ++j) rank += lens[j] > mine || (lens[j] == mine && j < tid);
+        scratch[rank] = tid;
+    }
+    __syncthreads();
+    int wrong = 0;
+    int64_t n = tid, a = 0, len = 0, count = 0;  // of place tid in the order
+    if (tid < p.num_seqs) {
+        n = scratch[tid];
+        a = p.cu_seqlens[n];
+        len = (int64_t)p.cu_seqlens[n + 1] - a;
+        if (len < 0 || a < 0 || a + len > p.total_tokens || (n == 0 && a != 0)) {
+            wrong = 1;
+        } else {
+            count = (len + p.seg - 1) / p.seg;
+            if (count < 1) count = 1;
+            count -= less;
+        }
+    }
+    int64_t sum = count;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+        const int64_t up = __shfl_up_sync(0xffffffffu, sum, off);
+        if (lane >= off) sum += up;
+    }
+    if (lane == 31) warp_sum[warp] = sum;
+    __syncthreads();
+    int64_t before = 0;
+    for (int w = 0; w < warp; ++w) before += warp_sum[w];
+    const int64_t first_item = before + sum - count;
+    if (count > 0 && item >= first_item && item < first_item + count)
+        fill((int)n, (int)(unit % p.H), (int)(item - first_item) + skip, (int)count + less, a, len, first_item - (less ? 0 : tid));
     return __syncthreads_or(wrong) == 0;
 }
 
@@ -194,9 +231,12 @@ __device__ __forceinline__ int64_t state_at(const Mix &m, int a, int b) {
     return m.turned ? (int64_t)b * m.dx + a : (int64_t)a * m.dz + b;
 }
 
+// Sets the status word, by the offsets of cu_seqlens.
+int launch_check(const Plan &p, cudaStream_t stream);
 // (rows in fp32, or none)
 int launch_mix_exact(const Plan &p, const Mix *mixes, int count, cudaStream_t stream);
-int launch_mix_tc(const Plan &p, const Mix *mixes, int count, int d_v, bool sums, cudaStream_t stream);
+// `sums`: the segments' own sums; `after_sums`: the launch ahead is theirs.
+int launch_mix_tc(const Plan &p, const Mix *mixes, int count, int d_v, bool sums, bool after_sums, cudaStream_t stream);
 // Sums the g parts of every head: in fp32 [rows, heads g, d] -> out [rows, heads, d]. Rows
 // behind the last sequence are left as they are.
 struct Share {

@@ -270,7 +270,13 @@ Mix mix_of(const Call &c, const void *x, int64_t xs, int xh, const void *y, int6
 
 int launch(const Call &c, const Plan &p, const Mix *mixes, int count, bool sums, cudaStream_t s) {
     if (!on_tensor_cores(c)) return launch_mix_exact(p, mixes, count, s);
-    return launch_mix_tc(p, mixes, count, c.dv, sums, s);
+    return launch_mix_tc(p, mixes, count, c.dv, sums, !sums && segmented(p), s);
+}
+// Ahead of the first launch: it sets the status word, or a check of the offsets does.
+int begin(Plan *p, cudaStream_t s) {
+    p->checked = p->cu_seqlens && p->num_seqs > kChecked;
+    p->first = !p->checked;
+    return p->checked ? launch_check(*p, s) : GDR_OK;
 }
 
 }  // namespace
@@ -317,7 +323,7 @@ int gdr_linattn_fwd(const gdr_linattn_shape *shape, const void *q, const void *k
     char *ws = (char *)workspace;
     const cudaStream_t s = (cudaStream_t)stream;
     Mix m = mix_of(c, q, c.qs, c.qh, k, c.ks, c.kh, v, c.vs, c.vh, c.dk, c.dv);
-    p.first = true;
+    if ((st = begin(&p, s)) != GDR_OK) return st;
     p.fine = S_final != nullptr;
     if (segmented(p)) {
         // (the first segment of a sequence reads S0 while its last one may write S_final)
@@ -374,7 +380,7 @@ int gdr_linattn_bwd(const gdr_linattn_shape *shape, const void *d_o, const void 
     k_.backward = v_.backward = true;
     k_.s_inter = v_.s_inter = 1.f;
     k_.s_state = v_.s_state = c.scale;
-    p.first = true;
+    if ((st = begin(&p, s)) != GDR_OK) return st;
     p.fine = dS0 != nullptr;
     if (segmented(p)) {
         Mix sums[2];

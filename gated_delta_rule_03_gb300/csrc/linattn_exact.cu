@@ -271,7 +271,23 @@ template <typename T> __global__ void __launch_bounds__(256) share_kernel(const 
     }
 }
 
+// Bound by reading the offsets once.
+__global__ void __launch_bounds__(256) check_kernel(const Plan p) {
+    for (int64_t n = (int64_t)blockIdx.x * 256 + threadIdx.x; n < p.num_seqs; n += (int64_t)gridDim.x * 256) {
+        const int a = p.cu_seqlens[n], b = p.cu_seqlens[n + 1];
+        if (b < a || a < 0 || b > p.total_tokens || (n == 0 && a != 0)) p.status[0] = GDR_ERR_BAD_SEQLENS;
+    }
+}
+
 }  // namespace
+
+int launch_check(const Plan &p, cudaStream_t stream) {
+    static_assert(GDR_OK == 0, "");
+    if (cudaMemsetAsync(p.status, 0, sizeof(int32_t), stream) != cudaSuccess) return GDR_ERR_CUDA;
+    const int64_t blocks = (p.num_seqs + 255) / 256;
+    check_kernel<<<(unsigned)(blocks < 152 * 8 ? blocks : 152 * 8), 256, 0, stream>>>(p);
+    return cuda_status(cudaGetLastError());
+}
 
 int launch_mix_exact(const Plan &p, const Mix *mixes, int count, cudaStream_t stream) {
     for (int i = 0; i < count; ++i) {

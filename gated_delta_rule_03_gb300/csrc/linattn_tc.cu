@@ -1072,8 +1072,8 @@ int run(K kernel, const TcArgs &A, int64_t units, int threads, uint32_t smem, bo
 
 }  // namespace
 
-// Every mix of one launch has the same slices; `sums`: the segments' own sums.
-int launch_mix_tc(const Plan &p, const Mix *mixes, int count, int d_v, bool sums, cudaStream_t stream) {
+// Every mix of one launch has the same slices.
+int launch_mix_tc(const Plan &p, const Mix *mixes, int count, int d_v, bool sums, bool after_sums, cudaStream_t stream) {
     TcArgs A = {};
     A.p = p;
     A.count = count;
@@ -1129,7 +1129,7 @@ int launch_mix_tc(const Plan &p, const Mix *mixes, int count, int d_v, bool sums
     }
     if (sums)
         return run(p.fine ? sum_tc_kernel<true> : sum_tc_kernel<false>, A, p.handing * p.split, kSumThreads, kSumSmem, false, stream);
-    return run(p.fine ? mix_tc_kernel<true> : mix_tc_kernel<false>, A, p.units, kThreads, kSmem, !p.first, stream);
+    return run(p.fine ? mix_tc_kernel<true> : mix_tc_kernel<false>, A, p.units, kThreads, kSmem, after_sums, stream);
 }
 
 }  // namespace linattn

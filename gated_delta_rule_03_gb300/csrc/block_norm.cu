@@ -13,6 +13,7 @@
 //
 // One row per TPR = blockDim.x threads, PER entries per thread in registers, so that every
 // row is read once and written once; all arithmetic and every sum in fp32.
+#include "f32x2.cuh"
 #include "internal.h"
 
 namespace gdr {
@@ -136,22 +137,6 @@ template <int K> __device__ __forceinline__ void row_sum(float (&s)[K], float *b
     }
 }
 
-// Two fp32 at a time.
-__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
-    float2 d;
-    asm("mul.rn.f32x2 %0, %1, %2;"
-        : "=l"(reinterpret_cast<uint64_t &>(d))
-        : "l"(reinterpret_cast<const uint64_t &>(a)), "l"(reinterpret_cast<const uint64_t &>(b)));
-    return d;
-}
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
-    float2 d;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;"
-        : "=l"(reinterpret_cast<uint64_t &>(d))
-        : "l"(reinterpret_cast<const uint64_t &>(a)), "l"(reinterpret_cast<const uint64_t &>(b)),
-          "l"(reinterpret_cast<const uint64_t &>(c)));
-    return d;
-}
 __device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
 
 // sigmoid by the hardware's exponential and reciprocal (a few units in the last place).

@@ -46,6 +46,7 @@
 // of the time. Where all 152 SMs run and every tile comes from DRAM (128 KB a chunk) it takes 3.1.
 #include <mutex>
 
+#include "f32x2.cuh"
 #include "linattn.cuh"
 #include "tc_common.cuh"
 
@@ -105,23 +106,6 @@ __device__ __forceinline__ bool mbar_sleep(uint32_t bar, uint32_t parity) {
         : "r"(bar), "r"(parity), "r"(100000u)
         : "memory");
     return ok != 0;
-}
-
-// Two fp32 at a time.
-__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
-    float2 d;
-    asm("mul.rn.f32x2 %0, %1, %2;"
-        : "=l"(reinterpret_cast<uint64_t &>(d))
-        : "l"(reinterpret_cast<const uint64_t &>(a)), "l"(reinterpret_cast<const uint64_t &>(b)));
-    return d;
-}
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
-    float2 d;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;"
-        : "=l"(reinterpret_cast<uint64_t &>(d))
-        : "l"(reinterpret_cast<const uint64_t &>(a)), "l"(reinterpret_cast<const uint64_t &>(b)),
-          "l"(reinterpret_cast<const uint64_t &>(c)));
-    return d;
 }
 
 // The weights of the 32 tokens that a warp weighs, of a chunk of n: table[i] holds those of tokens

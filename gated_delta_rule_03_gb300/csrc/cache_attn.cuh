@@ -1,0 +1,128 @@
+// cache_attn.cuh -- shared parts of attention over a paged 8-bit cache.
+//
+// Weights. An entry of the cache is a code times the scale of its page and head, so with
+// t_j = log2(e) s_j + log2(vs_j) (vs_j: the value scale of token j's page) a row's results are
+//     o = sum_j w_j code_j / l,   w_j = 2^(t_j - ref),   l = sum_j w_j / vs_j,   lse = ln l + ref ln 2
+// for any reference: the codes enter the second product as they are (exact in fp16), and a
+// weight is relative to the largest contribution even where pages differ much in scale.
+// A row's ref follows its maximum, kSpan below it, and moves only when a weight would pass
+// 2^(kSpan + kSlack): moving it costs a pass over the row's outputs. Weights in fp16 keep their 11
+// bits down to 2^-21 of the largest and are dropped below 2^-32.
+#pragma once
+
+#include <cuda_fp16.h>
+#include <math.h>
+
+#include "codes.cuh"
+#include "internal.h"
+
+namespace gdr {
+namespace cattn {
+
+constexpr float kSpan = 7.f, kSlack = 8.f;
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+constexpr float kNoRef = -1e30f;  // of a row that has seen nothing
+
+struct Attn {
+    const void *q;
+    const uint8_t *kc, *vc;
+    const float *ks, *vs;
+    const int32_t *table, *kv_lens, *cu;
+    const float *slopes;
+    void *o;
+    float *lse;
+    int32_t *status;
+    int64_t num_seqs, tokens, max_q, width, qs, pages;
+    int heads, kv_heads, group, log_page, causal;
+    float scale, softcap;
+};
+
+// New tokens of request n: the first row and their number.
+__device__ __forceinline__ int2 rows_of(const Attn &a, int64_t n) {
+    if (a.cu) {
+        const int c = __ldg(a.cu + n);
+        return make_int2(c, __ldg(a.cu + n + 1) - c);
+    }
+    const int64_t len = a.max_q;
+    return make_int2((int)(n * len), (int)len);
+}
+__device__ __forceinline__ bool lengths_hold(const Attn &a, int64_t n) {
+    const int len = __ldg(a.kv_lens + n);
+    if (len < 0 || len > (a.width << a.log_page)) return false;
+    if (!a.cu) return true;
+    const int c = __ldg(a.cu + n), d = __ldg(a.cu + n + 1);
+    return (n > 0 || c == 0) && d >= c && d <= a.tokens && d - c <= a.max_q;
+}
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float lg2(float x) {
+    float y;
+    asm("lg2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// The score of a token in powers of two, from a product that is already scaled; away = |p - j|.
+// tanh(x) = 1 - 2 / (1 + e^2x) is off by some 1e-7 in all, and the cap times that in the score: enough
+// for bf16 results; fp32 ones take the library's.
+template <bool kExact> __device__ __forceinline__ float shaped(float z, float softcap, float slope, float away) {
+    if (softcap > 0.f) {
+        const float x = z / softcap;
+        z = softcap * (kExact ? tanhf(x) : 1.f - __fdividef(2.f, 1.f + ex2(2.f * kLog2e * x)));
+    }
+    return fmaf(-slope, away, z);
+}
+
+// 2^n that brings a row with this largest size (bits of an fp32 number) to 2^14 .. 2^15, so that
+// fp16 holds its entries (to 2^-39 of the largest, subnormal ones included); 0 for NaN and
+// infinity, which stay what they are.
+__device__ __forceinline__ int row_shift(uint32_t bits) {
+    const int e = (int)(bits >> 23);
+    return e == 255 ? 0 : min(14 - (e - 127), 126);
+}
+__device__ __forceinline__ float two_to(int n) { return __int_as_float((n + 127) << 23); }
+
+// Sum over the block and inclusive sums, kThreads threads.
+__device__ __forceinline__ int64_t warp_sums(int64_t x) {
+#pragma unroll
+    for (int d = 1; d < 32; d *= 2) {
+        const int64_t y = __shfl_up_sync(~0u, x, d);
+        if ((int)(threadIdx.x & 31) >= d) x += y;
+    }
+    return x;
+}
+template <int kThreads> __device__ int64_t block_sums(int64_t x, int64_t *sums, int64_t *total) {
+    const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    x = warp_sums(x);
+    __syncthreads();
+    if (lane == 31) sums[w] = x;
+    __syncthreads();
+    int64_t before = 0, all = 0;
+#pragma unroll
+    for (int i = 0; i < kThreads / 32; ++i) {
+        if (i < w) before += sums[i];
+        all += sums[i];
+    }
+    *total = all;
+    return x + before;
+}
+
+// A part of one item's keys, for a join of several: log2 of its sum, then its outputs (divided by it).
+// kRows rows.
+template <int kRows, int D> struct Part {
+    float lse2[kRows];
+    float o[kRows][D];
+};
+
+int launch_step64(const Attn &a, int codes, int dtype, void *ws, cudaStream_t s);
+int launch_step128(const Attn &a, int codes, int dtype, void *ws, cudaStream_t s);
+int launch_step256(const Attn &a, int codes, int dtype, void *ws, cudaStream_t s);
+size_t step_bytes64();
+size_t step_bytes128();
+size_t step_bytes256();
+
+}  // namespace cattn
+}  // namespace gdr

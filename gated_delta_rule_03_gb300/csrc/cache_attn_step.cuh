@@ -1,0 +1,584 @@
+// cache_attn_step.cuh -- attention over a paged 8-bit cache for few rows: single tokens.
+//
+// Rows. The queries of one request that share a head of the cache (its group of heads, times its
+// new tokens) are the rows of 16-row tiles: an item is (request, head of the cache, tile).
+//
+// Products. Warp-level 16x8x16 MMAs in fp16 with fp32 sums: a tile of 16 rows is what they take, and
+// their operands are registers, so codes go from the copy in shared memory to an operand without
+// a turn through it. The order of the contraction is free: thread c of a quad takes 16 consecutive
+// bytes of a key as the k indices of four steps (queries are laid out alike), and dims 16 g + u of a value as
+// column g of step u, which makes every copy 16 bytes wide.
+// The tensor cores are far from busy (a tenth at 8 heads a group); the 5th-generation ones would need
+// the codes converted through shared memory, rows filled up to 128, and the same bytes.
+//
+// Bound by memory: each cached byte is read once per 16 rows. A warp streams tiles of 16 tokens
+// through a ring of its own in shared memory (cp.async, kStages deep, each thread reads back only what
+// it copied: no barrier between warps until an item ends).
+//
+// Split. All items' keys, in units of kUnit tokens, are laid end to end and shared out equally
+// among the resident blocks, whatever the requests' lengths. A block that ends inside an
+// item leaves its part in the workspace; join_parts_kernel adds them in order.
+#pragma once
+
+#include "cache_attn.cuh"
+#include "sm100.cuh"
+
+namespace gdr {
+namespace cattn {
+
+constexpr int kStepWarps = 4;
+constexpr int kUnit = 16 * kStepWarps;  // tokens
+constexpr int kMinUnits = 4;            // a block's least share
+constexpr int kSms = 152;
+
+template <int D, int kParts> struct StepConfig {
+    static constexpr int kSteps = D / 16;                 // k steps of the first product
+    static constexpr int kStages = D == 64 ? 6 : (D == 256 ? (kParts == 2 ? 2 : 3) : 4);
+    static constexpr int kBlocks = D == 64 ? (kParts == 2 ? 3 : 4) : (D == 128 ? (kParts == 2 ? 2 : 3) : 2);  // per SM
+    static constexpr int kStage = 2 * 16 * D;             // bytes: keys, then values
+    static constexpr int kRing = kStepWarps * kStages * kStage;
+    static constexpr int kQ = kParts * kSteps * 32 * 16;
+    static constexpr bool kInRegs = D * kParts <= 128;    // queries stay in registers
+    static constexpr int kSmem = kRing + kQ;
+    static_assert(kStepWarps * 16 * D * 4 <= kRing, "outputs of the warps meet in the ring");
+};
+
+__device__ __forceinline__ void cp16(uint32_t dst, const void *src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp8(uint32_t dst, const void *src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+__device__ __forceinline__ float2 unpack_f16(uint32_t r) { return __half22float2(reinterpret_cast<const __half2 &>(r)); }
+
+struct StepPlan {
+    int32_t *tasks;  // [blocks][4]: the item whose parts begin with this block's: request (-1: none), head, tile, blocks
+    char *parts;     // [blocks][2] Part
+};
+
+// Where unit `u` lies: request n and the units before it.
+struct Share {
+    int64_t n, before, total;
+    bool ok;
+};
+__device__ __forceinline__ int64_t units_of(const Attn &a, int64_t n) {
+    return max((__ldg(a.kv_lens + n) + kUnit - 1) / kUnit, 1);
+}
+__device__ __forceinline__ int tiles_of(const Attn &a, int rows) { return (int)(((int64_t)rows * a.group + 15) / 16); }
+
+// The request of the first unit of this block's share, and the share itself.
+__device__ inline Share find_share(const Attn &a, int64_t *sums, int64_t *found, int64_t *per) {
+    constexpr int kThreads = kStepWarps * 32;
+    const int tid = threadIdx.x;
+    int64_t mine = 0;
+    bool ok = true;
+    auto weight = [&](int64_t n) { return (int64_t)a.kv_heads * tiles_of(a, rows_of(a, n).y) * units_of(a, n); };
+    for (int64_t n = tid; n < a.num_seqs; n += kThreads) {
+        if (lengths_hold(a, n)) mine += weight(n);
+        else ok = false;
+    }
+    Share s;
+    s.ok = __syncthreads_and(ok);
+    if (!s.ok) return s;
+    block_sums<kThreads>(mine, sums, &s.total);
+    *per = max((s.total + gridDim.x - 1) / gridDim.x, (int64_t)kMinUnits);
+    const int64_t u = (int64_t)blockIdx.x * *per;
+    s.n = s.before = 0;
+    if (u >= s.total) return s;
+    int64_t carry = 0;
+    for (int64_t n0 = 0; n0 < a.num_seqs; n0 += kThreads) {
+        const int64_t n = n0 + tid, w = n < a.num_seqs ? weight(n) : 0;
+        int64_t total;
+        const int64_t end = carry + block_sums<kThreads>(w, sums, &total);
+        if (u >= end - w && u < end) {
+            found[0] = n;
+            found[1] = end - w;
+        }
+        carry += total;
+        if (carry > u) break;
+    }
+    __syncthreads();
+    s.n = found[0];
+    s.before = found[1];
+    return s;
+}
+
+template <typename T, int D, int kCode, int kParts, bool kShaped>
+__global__ void __launch_bounds__(kStepWarps * 32, (StepConfig<D, kParts>::kBlocks)) attn_step_kernel(Attn a, StepPlan plan) {
+    using C = StepConfig<D, kParts>;
+    using P = Part<16, D>;
+    extern __shared__ __align__(16) char smem[];
+    __shared__ int64_t sums[kStepWarps], found[2];
+    __shared__ float2 scales[kStepWarps][C::kStages];
+    __shared__ float row_factor[16], row_slope[16];
+    __shared__ float warp_ref[kStepWarps][16], warp_sum[kStepWarps][16];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
+    const int in_page = (1 << a.log_page) - 1;
+
+    int64_t per;
+    const Share share = find_share(a, sums, found, &per);
+    if (blockIdx.x == 0 && tid == 0) *a.status = share.ok ? GDR_OK : GDR_ERR_BAD_SEQLENS;
+    int4 task = make_int4(-1, 0, 0, 0);
+    sm100::griddep_launch_dependents();
+    if (!share.ok) {
+        if (plan.tasks && tid == 0) ((int4 *)plan.tasks)[blockIdx.x] = task;
+        return;
+    }
+
+    char *const ring = smem + warp * C::kStages * C::kStage;
+    const uint32_t ring_s = sm100::smem_u32(ring) + lane * 16;
+    uint32_t *const qfrag = (uint32_t *)(smem + C::kRing);
+
+    int64_t u = (int64_t)blockIdx.x * per, n = share.n, before = share.before;
+    const int64_t end_u = min(share.total, u + per);
+    while (u < end_u) {
+        const int2 rows = rows_of(a, n);
+        const int tiles = tiles_of(a, rows.y);
+        const int len = __ldg(a.kv_lens + n);
+        const int64_t units = units_of(a, n), weight = (int64_t)a.kv_heads * tiles * units;
+        if (u >= before + weight) {  // (also a request without new tokens)
+            before += weight;
+            ++n;
+            continue;
+        }
+        const int64_t rel = u - before, item = rel / units;
+        const int ua = (int)(rel - item * units), ub = (int)min(units, ua + (end_u - u));
+        const int tile = (int)(item % tiles), head = (int)(item / tiles);
+        const int row0 = tile * 16, nrows = min(16, rows.y * a.group - row0);
+        // the tokens that the last row may see
+        const int past = len - rows.y;  // position of the first new token
+        const int far = a.causal ? max(0, min(len, past + (row0 + nrows - 1) / a.group + 1)) : len;
+        const int first = ua * kUnit, last = min(far, ub * kUnit);
+        const int count = last > first ? ((last - first + 15) / 16 - warp + kStepWarps - 1) / kStepWarps : 0;  // of this warp
+
+        // ---- the stream of tiles: page and scales of 32 tiles at a time, one per lane
+        int64_t page = 0;
+        float ks = 0.f, vs = 0.f;
+        auto look_up = [&](int i0) {
+            const int tok = first + (warp + (i0 + lane) * kStepWarps) * 16;
+            if (tok < last) {
+                const int p = __ldg(a.table + n * a.width + (tok >> a.log_page));
+                const bool good = p >= 0 && p < a.pages;
+                page = good ? p : 0;
+                ks = good ? __ldg(a.ks + page * a.kv_heads + head) : __int_as_float(0x7fffffff);
+                vs = good ? __ldg(a.vs + page * a.kv_heads + head) : __int_as_float(0x7fffffff);
+            }
+        };
+        auto fetch = [&](int i) {  // tile i of this warp
+            if (i < count) {
+                if ((i & 31) == 0) look_up(i);
+                const int64_t pg = __shfl_sync(~0u, page, i & 31);
+                const float k1 = __shfl_sync(~0u, ks, i & 31), v1 = __shfl_sync(~0u, vs, i & 31);
+                const int tok = first + (warp + i * kStepWarps) * 16;
+                const int64_t at = (((pg * a.kv_heads + head) << a.log_page) + (tok & in_page)) * D;
+                const int slot = i % C::kStages;
+                if (lane == 0) scales[warp][slot] = make_float2(k1, v1);
+                const uint32_t dst = ring_s + slot * C::kStage;
+#pragma unroll
+                for (int t = 0; t < 2; ++t)
+#pragma unroll
+                    for (int j = 0; j < D / 64; ++j)
+                        cp16(dst + (t * (D / 64) + j) * 512, a.kc + at + (8 * t + g) * D + 64 * j + 16 * c);
+#pragma unroll
+                for (int t = 0; t < 4; ++t) {
+                    const int row = 2 * c + (t & 1) + 8 * (t >> 1);
+                    if constexpr (D == 64) {
+                        cp8(dst - lane * 8 + 16 * D + t * 256, a.vc + at + row * D + 8 * g);
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < D / 128; ++j)
+                            cp16(dst + 16 * D + (t * (D / 128) + j) * 512, a.vc + at + row * D + 128 * j + 16 * g);
+                    }
+                }
+            }
+            asm volatile("cp.async.commit_group;" ::: "memory");
+        };
+#pragma unroll
+        for (int i = 0; i < C::kStages - 1; ++i) fetch(i);
+
+        // ---- queries: fp16 with a power of two per row, in the order of the first product
+        {
+            const int r = tid >> 3, part = tid & 7, at = row0 + r;
+            constexpr int kMine = D / 8;
+            float v[kMine];
+            uint32_t most = 0;
+            if (r < nrows) {
+                const int h = head * a.group + at % a.group;
+                const T *src = (const T *)a.q + (int64_t)(rows.x + at / a.group) * a.qs + (int64_t)h * D + part * kMine;
+                constexpr int kVec = 16 / sizeof(T);
+#pragma unroll
+                for (int i = 0; i < kMine; i += kVec) {
+                    const uint4 w = __ldg((const uint4 *)(src + i));
+                    const T *e = (const T *)&w;
+#pragma unroll
+                    for (int x = 0; x < kVec; ++x) v[i + x] = to_f32<T>(e[x]);
+                }
+#pragma unroll
+                for (int i = 0; i < kMine; ++i) most = max(most, __float_as_uint(v[i]) & 0x7fffffffu);
+                if (part == 0) row_slope[r] = kShaped && a.slopes ? __ldg(a.slopes + h) : 0.f;
+            } else {
+#pragma unroll
+                for (int i = 0; i < kMine; ++i) v[i] = 0.f;
+                if (part == 0) row_slope[r] = 0.f;
+            }
+#pragma unroll
+            for (int d = 1; d < 8; d *= 2) most = max(most, __shfl_xor_sync(~0u, most, d));
+            const int shift = row_shift(most);
+            const float up = two_to(shift);
+            if (part == 0) row_factor[r] = two_to(-shift) * a.scale;
+#pragma unroll
+            for (int i = 0; i < kMine; i += 2) {
+                const int d = part * kMine + i;
+                const int step = (d >> 6) * 4 + ((d & 15) >> 2), cc = (d & 63) >> 4, pair = (d & 3) >> 1;
+                uint32_t *const to = qfrag + (step * 32 + (r & 7) * 4 + cc) * 4 + (r >> 3) + 2 * pair;
+                const float x = v[i] * up, y = v[i + 1] * up;
+                const uint32_t hi = pack_f16(x, y);
+                *to = hi;
+                if (kParts == 2) {
+                    const float2 f = unpack_f16(hi);
+                    to[C::kSteps * 128] = pack_f16(x - f.x, y - f.y);
+                }
+            }
+        }
+        __syncthreads();
+        uint32_t qreg[C::kInRegs ? kParts * C::kSteps : 1][4];
+        if (C::kInRegs) {
+#pragma unroll
+            for (int s = 0; s < kParts * C::kSteps; ++s) {
+                const uint4 w = *(const uint4 *)(qfrag + (s * 32 + lane) * 4);
+                qreg[s][0] = w.x, qreg[s][1] = w.y, qreg[s][2] = w.z, qreg[s][3] = w.w;
+            }
+        }
+        const float f0 = row_factor[g], f1 = row_factor[g + 8], slope0 = row_slope[g], slope1 = row_slope[g + 8];
+        const int p0 = past + (row0 + g) / a.group, p1 = past + (row0 + g + 8) / a.group;
+        const int lim0 = a.causal ? min(len, p0 + 1) : len, lim1 = a.causal ? min(len, p1 + 1) : len;
+        const int sure = a.causal ? min(len, past + row0 / a.group + 1) : len;  // seen by every row
+
+        float ref0 = kNoRef, ref1 = kNoRef, l0 = 0.f, l1 = 0.f;
+        float acc[D / 8][4];
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
+
+        for (int i = 0; i < count; ++i) {
+            fetch(i + C::kStages - 1);
+            asm volatile("cp.async.wait_group %0;" ::"n"(C::kStages - 1) : "memory");
+            __syncwarp();  // (scales)
+            const int slot = i % C::kStages;
+            const char *const at = ring + slot * C::kStage;
+            const float2 sc = scales[warp][slot];
+            const int tok = first + (warp + i * kStepWarps) * 16;
+            float s[2][4];
+#pragma unroll
+            for (int t = 0; t < 2; ++t) s[t][0] = s[t][1] = s[t][2] = s[t][3] = 0.f;
+#pragma unroll
+            for (int j = 0; j < D / 64; ++j) {
+                uint4 k[2];
+#pragma unroll
+                for (int t = 0; t < 2; ++t) k[t] = *(const uint4 *)(at + (t * (D / 64) + j) * 512 + lane * 16);
+#pragma unroll
+                for (int w = 0; w < 4; ++w) {
+                    const int step = j * 4 + w;
+                    uint32_t q[kParts][4];
+#pragma unroll
+                    for (int x = 0; x < kParts; ++x) {
+                        if (C::kInRegs) {
+#pragma unroll
+                            for (int y = 0; y < 4; ++y) q[x][y] = qreg[x * C::kSteps + step][y];
+                        } else {
+                            const uint4 z = *(const uint4 *)(qfrag + ((x * C::kSteps + step) * 32 + lane) * 4);
+                            q[x][0] = z.x, q[x][1] = z.y, q[x][2] = z.z, q[x][3] = z.w;
+                        }
+                    }
+#pragma unroll
+                    for (int t = 0; t < 2; ++t) {
+                        const uint32_t word = w == 0 ? k[t].x : w == 1 ? k[t].y : w == 2 ? k[t].z : k[t].w;
+                        uint32_t lo, hi;
+                        codes::to_f16x4<kCode>(word, lo, hi);
+#pragma unroll
+                        for (int x = kParts - 1; x >= 0; --x) mma_f16(s[t], q[x], lo, hi);
+                    }
+                }
+            }
+            // scores in powers of two, with the value scale's
+            const float lv = lg2(sc.y), rv = __fdividef(1.f, sc.y);
+            const float m0 = f0 * sc.x, m1 = f1 * sc.x;
+#pragma unroll
+            for (int t = 0; t < 2; ++t)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int j = tok + 8 * t + 2 * c + (e & 1);
+                    float z = s[t][e] * (e < 2 ? m0 : m1);
+                    if (kShaped) z = shaped<kParts == 2>(z, a.softcap, e < 2 ? slope0 : slope1, fabsf((float)((e < 2 ? p0 : p1) - j)));
+                    s[t][e] = fmaf(z, kLog2e, lv);
+                }
+            const bool edge = tok + 16 > sure;
+            if (edge) {
+#pragma unroll
+                for (int t = 0; t < 2; ++t)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (tok + 8 * t + 2 * c + (e & 1) >= (e < 2 ? lim0 : lim1)) s[t][e] = -INFINITY;
+            }
+            const float top0 = fmaxf(fmaxf(s[0][0], s[0][1]), fmaxf(s[1][0], s[1][1]));
+            const float top1 = fmaxf(fmaxf(s[0][2], s[0][3]), fmaxf(s[1][2], s[1][3]));
+            if (__any_sync(~0u, top0 > ref0 + (kSpan + kSlack) || top1 > ref1 + (kSpan + kSlack))) {
+                float t0 = top0, t1 = top1;
+#pragma unroll
+                for (int d = 1; d < 4; d *= 2) {
+                    t0 = fmaxf(t0, __shfl_xor_sync(~0u, t0, d));
+                    t1 = fmaxf(t1, __shfl_xor_sync(~0u, t1, d));
+                }
+                const float n0 = t0 > ref0 + (kSpan + kSlack) ? t0 - kSpan : ref0, n1 = t1 > ref1 + (kSpan + kSlack) ? t1 - kSpan : ref1;
+                const float d0 = ex2(ref0 - n0), d1 = ex2(ref1 - n1);
+                ref0 = n0;
+                ref1 = n1;
+                l0 *= d0;
+                l1 *= d1;
+#pragma unroll
+                for (int x = 0; x < D / 8; ++x) {
+                    acc[x][0] *= d0;
+                    acc[x][1] *= d0;
+                    acc[x][2] *= d1;
+                    acc[x][3] *= d1;
+                }
+            }
+#pragma unroll
+            for (int t = 0; t < 2; ++t)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) s[t][e] = ex2(s[t][e] - (e < 2 ? ref0 : ref1));
+            if (edge && sc.y != sc.y) {  // (a page without a scale reaches only who looks at it)
+#pragma unroll
+                for (int t = 0; t < 2; ++t)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (tok + 8 * t + 2 * c + (e & 1) < (e < 2 ? lim0 : lim1)) (e < 2 ? l0 : l1) = sc.y;
+            } else {
+                l0 = fmaf((s[0][0] + s[0][1]) + (s[1][0] + s[1][1]), rv, l0);
+                l1 = fmaf((s[0][2] + s[0][3]) + (s[1][2] + s[1][3]), rv, l1);
+            }
+            uint32_t p[kParts][4];
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+                const float x0 = s[y >> 1][(y & 1) * 2], x1 = s[y >> 1][(y & 1) * 2 + 1];
+                p[0][y] = pack_f16(x0, x1);
+                if (kParts == 2) {
+                    const float2 f = unpack_f16(p[0][y]);
+                    p[kParts - 1][y] = pack_f16(x0 - f.x, x1 - f.y);
+                }
+            }
+            // bytes behind the last token, and those that stand in for a page that is none, may be anything
+            const bool unsure = tok + 16 > len || sc.y != sc.y;
+#pragma unroll
+            for (int j = 0; j < (D + 127) / 128; ++j) {
+                constexpr int kWords = D == 64 ? 2 : 4;
+                uint32_t v[4][kWords];
+#pragma unroll
+                for (int t = 0; t < 4; ++t) {
+                    if constexpr (D == 64) {
+                        const uint2 w = *(const uint2 *)(at + 16 * D + t * 256 + lane * 8);
+                        v[t][0] = w.x, v[t][1] = w.y;
+                    } else {
+                        const uint4 w = *(const uint4 *)(at + 16 * D + (t * (D / 128) + j) * 512 + lane * 16);
+                        v[t][0] = w.x, v[t][1] = w.y, v[t][2] = w.z, v[t][3] = w.w;
+                    }
+                    if (unsure && (sc.y != sc.y || tok + 2 * c + (t & 1) + 8 * (t >> 1) >= len)) {
+#pragma unroll
+                        for (int w = 0; w < kWords; ++w) v[t][w] = 0;
+                    }
+                }
+#pragma unroll
+                for (int w = 0; w < kWords; ++w) {
+                    uint32_t b[2][4];  // [token pair][dim of the word]
+#pragma unroll
+                    for (int t = 0; t < 2; ++t) {
+                        codes::to_f16x4<kCode>(__byte_perm(v[2 * t][w], v[2 * t + 1][w], 0x5140), b[t][0], b[t][1]);
+                        codes::to_f16x4<kCode>(__byte_perm(v[2 * t][w], v[2 * t + 1][w], 0x7362), b[t][2], b[t][3]);
+                    }
+#pragma unroll
+                    for (int x = 0; x < 4; ++x)
+#pragma unroll
+                        for (int y = kParts - 1; y >= 0; --y) mma_f16(acc[j * 4 * kWords + w * 4 + x], p[y], b[0][x], b[1][x]);
+                }
+            }
+        }
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
+
+        // ---- the warps' parts meet
+#pragma unroll
+        for (int d = 1; d < 4; d *= 2) {
+            l0 += __shfl_xor_sync(~0u, l0, d);
+            l1 += __shfl_xor_sync(~0u, l1, d);
+        }
+        if (c == 0) {
+            warp_ref[warp][g] = ref0;
+            warp_ref[warp][g + 8] = ref1;
+            warp_sum[warp][g] = l0;
+            warp_sum[warp][g + 8] = l1;
+        }
+        __syncthreads();
+        float *const outs = (float *)smem;  // [warp][16][D]
+        constexpr int kU = D == 64 ? 8 : 16;  // dims of a thread in a row of 8 groups
+#pragma unroll
+        for (int x = 0; x < D / 8; ++x) {
+            // column n of the MMA's 8 is dim (x / kU) 128 + kU n + x % kU
+            const int dim = (x / kU) * 128 + kU * (2 * c) + x % kU;
+            float *const to = outs + (warp * 16 + g) * D + dim;
+            to[0] = acc[x][0];
+            to[kU] = acc[x][1];
+            to[8 * D] = acc[x][2];
+            to[8 * D + kU] = acc[x][3];
+        }
+        __syncthreads();
+        const bool whole = ua == 0 && ub == units;
+        P *const part = whole ? nullptr : (P *)plan.parts + (2 * (int64_t)blockIdx.x + (ua == 0));
+        constexpr int kQuads = D / 4;
+        for (int x = tid; x < 16 * kQuads; x += kStepWarps * 32) {
+            const int r = x / kQuads, d = (x % kQuads) * 4;
+            if (r >= nrows) break;
+            float top = kNoRef;
+#pragma unroll
+            for (int w = 0; w < kStepWarps; ++w) top = fmaxf(top, warp_ref[w][r]);
+            float l = 0.f;
+            float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int w = 0; w < kStepWarps; ++w) {
+                const float f = ex2(warp_ref[w][r] - top);
+                const float4 y = *(const float4 *)(outs + (w * 16 + r) * D + d);
+                l = fmaf(warp_sum[w][r], f, l);
+                o.x = fmaf(y.x, f, o.x);
+                o.y = fmaf(y.y, f, o.y);
+                o.z = fmaf(y.z, f, o.z);
+                o.w = fmaf(y.w, f, o.w);
+            }
+            const float inv = l == 0.f ? 0.f : 1.f / l, sum2 = l == 0.f ? -INFINITY : log2f(l) + top;
+            o.x *= inv, o.y *= inv, o.z *= inv, o.w *= inv;
+            if (part) {
+                *(float4 *)&part->o[r][d] = o;
+                if (d == 0) part->lse2[r] = sum2;
+            } else {
+                const int64_t row = (int64_t)(rows.x + (row0 + r) / a.group) * a.heads + head * a.group + (row0 + r) % a.group;
+                T *const to = (T *)a.o + row * D + d;
+                if constexpr (sizeof(T) == 4) {
+                    *(float4 *)to = o;
+                } else {
+                    const __nv_bfloat162 lo = __floats2bfloat162_rn(o.x, o.y), hi = __floats2bfloat162_rn(o.z, o.w);
+                    *(uint2 *)to = make_uint2(reinterpret_cast<const uint32_t &>(lo), reinterpret_cast<const uint32_t &>(hi));
+                }
+                if (d == 0 && a.lse) a.lse[row] = sum2 * kLn2;
+            }
+        }
+        if (!whole && ua == 0) {
+            const int64_t stop = u - ua + units - 1;  // the item's last unit
+            task = make_int4((int)n, head, tile, (int)(stop / per - blockIdx.x + 1));
+        }
+        u += ub - ua;
+        __syncthreads();
+    }
+    if (plan.tasks && tid == 0) ((int4 *)plan.tasks)[blockIdx.x] = task;
+}
+
+// Adds the parts of items that several blocks worked on: a block for each that begins one, a
+// warp for each of its rows, the parts in order.
+template <typename T, int D> __global__ void __launch_bounds__(256) join_parts_kernel(Attn a, StepPlan plan) {
+    using P = Part<16, D>;
+    sm100::griddep_wait();
+    const int4 task = ((const int4 *)plan.tasks)[blockIdx.x];
+    if (task.x < 0) return;
+    const int64_t n = task.x;
+    const int head = task.y, row0 = task.z * 16, blocks = task.w;
+    const int2 rows = rows_of(a, n);
+    const int nrows = min(16, rows.y * a.group - row0);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const P *const parts = (const P *)plan.parts;
+    // the first block's part is its second one, that of the others their first
+    auto part = [&](int i) { return parts + 2 * ((int64_t)blockIdx.x + i) + (i == 0); };
+    for (int r = warp; r < nrows; r += 8) {
+        float top = -INFINITY, bad = 0.f;
+        for (int i = lane; i < blocks; i += 32) {
+            const float x = part(i)->lse2[r];
+            top = fmaxf(top, x);
+            if (x != x) bad = x;
+        }
+#pragma unroll
+        for (int d = 1; d < 32; d *= 2) {
+            top = fmaxf(top, __shfl_xor_sync(~0u, top, d));
+            bad += __shfl_xor_sync(~0u, bad, d);
+        }
+        const float base = top == -INFINITY ? 0.f : top;
+        float l = 0.f, o[D / 32];
+#pragma unroll
+        for (int x = 0; x < D / 32; ++x) o[x] = 0.f;
+#pragma unroll 4
+        for (int i = 0; i < blocks; ++i) {
+            const P *const p = part(i);
+            const float f = ex2(p->lse2[r] - base);
+            l += f;
+#pragma unroll
+            for (int x = 0; x < D / 32; ++x) o[x] = fmaf(p->o[r][x * 32 + lane], f, o[x]);
+        }
+        l += bad;
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+        const int64_t row = (int64_t)(rows.x + (row0 + r) / a.group) * a.heads + head * a.group + (row0 + r) % a.group;
+#pragma unroll
+        for (int x = 0; x < D / 32; ++x) ((T *)a.o)[row * D + x * 32 + lane] = from_f32<T>(o[x] * inv);
+        if (lane == 0 && a.lse) a.lse[row] = (l == 0.f ? -INFINITY : log2f(l) + base) * kLn2;
+    }
+}
+
+template <typename T, int D, int kCode, int kParts, bool kShaped>
+int launch_step_kernel(const Attn &a, const StepPlan &plan, bool join, cudaStream_t s) {
+    using C = StepConfig<D, kParts>;
+    constexpr int kBlocks = kSms * C::kBlocks;
+    const auto kernel = attn_step_kernel<T, D, kCode, kParts, kShaped>;
+    static const cudaError_t sized = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem) != cudaSuccess) return GDR_ERR_CUDA;
+    kernel<<<kBlocks, kStepWarps * 32, C::kSmem, s>>>(a, plan);
+    if (cudaGetLastError() != cudaSuccess) return GDR_ERR_CUDA;
+    if (!join) return GDR_OK;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(kBlocks);
+    cfg.blockDim = dim3(256);
+    cfg.stream = s;
+    cudaLaunchAttribute attr = {};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cuda_status(cudaLaunchKernelEx(&cfg, join_parts_kernel<T, D>, a, plan));
+}
+
+template <int D> int launch_step_d(const Attn &a, int codes, int dtype, void *ws, cudaStream_t s) {
+    // The least share of a block is kMinUnits: no request can have more, no item is split
+    const bool join = ((a.width << a.log_page) + kUnit - 1) / kUnit > 1;
+    StepPlan plan;
+    plan.tasks = join ? (int32_t *)ws : nullptr;
+    plan.parts = (char *)ws + ((size_t)kSms * 4 * sizeof(int4) + 255) / 256 * 256;
+    const bool shaped = a.softcap > 0.f || a.slopes;
+    const bool e4m3 = codes == GDR_CODE_E4M3;
+#define GDR_STEP(T, CODE, PARTS) \
+    return shaped ? launch_step_kernel<T, D, CODE, PARTS, true>(a, plan, join, s) : launch_step_kernel<T, D, CODE, PARTS, false>(a, plan, join, s)
+    if (dtype == GDR_F32) {
+        if (e4m3) GDR_STEP(float, GDR_CODE_E4M3, 2);
+        GDR_STEP(float, GDR_CODE_INT8, 2);
+    }
+    if (e4m3) GDR_STEP(__nv_bfloat16, GDR_CODE_E4M3, 1);
+    GDR_STEP(__nv_bfloat16, GDR_CODE_INT8, 1);
+#undef GDR_STEP
+}
+
+template <int D> size_t step_bytes_d() {
+    return ((size_t)kSms * 4 * sizeof(int4) + 255) / 256 * 256 + (size_t)kSms * StepConfig<D, 1>::kBlocks * 2 * sizeof(Part<16, D>);
+}
+
+}  // namespace cattn
+}  // namespace gdr

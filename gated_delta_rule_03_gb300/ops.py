@@ -142,7 +142,14 @@ def _load():
             ("gdr_linattn_step", c_int, [vp] * 8),
             ("gdr_block_norm_fwd", c_int, [vp] * 9),
             ("gdr_block_norm_bwd_workspace_size", size_t, [vp]),
-            ("gdr_block_norm_bwd", c_int, [vp] * 14 + [size_t, vp])):
+            ("gdr_block_norm_bwd", c_int, [vp] * 14 + [size_t, vp]),
+            ("gdr_rotary_fwd", c_int, [vp] * 8),
+            ("gdr_rotary_bwd", c_int, [vp] * 8),
+            ("gdr_page_plan", c_int, [vp] * 13),
+            ("gdr_page_release", c_int, [vp] * 7),
+            ("gdr_cache_append", c_int, [vp, i64, vp, i64, vp, i64] + [vp] * 6),
+            ("gdr_cache_attn_workspace_size", size_t, [vp]),
+            ("gdr_cache_attn", c_int, [vp] * 13 + [size_t, vp])):
         getattr(lib, name).restype = res
         getattr(lib, name).argtypes = args
     lib.gdr_read_device_status.argtypes = [vp, ctypes.POINTER(c_int), vp]

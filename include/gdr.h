@@ -64,7 +64,8 @@ enum {
     GDR_ERR_WORKSPACE = -4,      /* workspace missing or smaller than required */
     GDR_ERR_CUDA = -5,           /* a CUDA runtime call or kernel launch failed */
     GDR_ERR_DEVICE_TIMEOUT = -6, /* a device-side wait gave up (read via gdr_read_device_status) */
-    GDR_ERR_BAD_SEQLENS = -7     /* cu_seqlens not 0 ... total_tokens non-decreasing (device-checked) */
+    GDR_ERR_BAD_SEQLENS = -7     /* cu_seqlens not 0 ... total_tokens non-decreasing, or lengths that do
+                                    not fit their buffers (device-checked) */
 };
 
 /*
@@ -551,6 +552,189 @@ int gdr_block_norm_bwd(const gdr_block_norm_shape *shape, const void *dx_out, co
                        const void *x_out, const void *y, const void *gate, const float *w_post,
                        const float *w_pre, void *dx, void *dy, void *dgate, float *dw_post,
                        float *dw_pre, void *workspace, size_t workspace_bytes, gdr_stream_t stream);
+
+/*
+ * Rotary positions of queries and keys.
+ *
+ * The first rot_dim entries of a head are rot_dim / 2 pairs; pair i of a token at position p
+ * is turned by the angle 2 pi p rates[i] / 2^64 and scaled by `amplitude`:
+ *     (x, y) -> amplitude (x cos - y sin, x sin + y cos)
+ * the other entries are copied. Pair i is (x_i, x_{i + rot_dim/2}), or with `neighbours`
+ * (x_{2i}, x_{2i+1}).
+ *
+ * rates: turns per position in steps of 2^-64, modulo one turn. The product with the position
+ * is taken in 64-bit integers, whose overflow drops whole turns: the angle of any position
+ * is off by 2^-33 turns at most before it becomes an fp32 number, however far the position.
+ *
+ * Shape of a call (a HOST struct):
+ *   tokens          rows of every tensor (>= 0)
+ *   q_heads >= 1, k_heads >= 0 (0: no keys)
+ *   d               a multiple of 8 in [8, 256];  rot_dim even, in [2, d]
+ *   dtype           gdr_dtype of all tensors
+ *   neighbours      nonzero: a pair is two neighbours
+ *   amplitude       finite
+ *   *_stride        elements from a token's first head to the next token's (views of one
+ *                   fused projection); 0 means dense. A multiple of 16 bytes, at least dense.
+ */
+typedef struct gdr_rotary_shape {
+    int64_t tokens;
+    int q_heads, k_heads, d, rot_dim, dtype, neighbours;
+    float amplitude;
+    int64_t q_stride, k_stride, q_out_stride, k_out_stride;
+} gdr_rotary_shape;
+
+/*
+ *   q [tokens, q_heads, d], k [tokens, k_heads, d] or NULL (k_heads = 0)
+ *   positions [tokens] int32, any value;  rates [rot_dim / 2] int64
+ *   q_out, k_out   (written) like q and k; q_out may be q and k_out may be k, with the same
+ *                  stride. Any other element shared by an output and another argument is
+ *                  rejected; views of one buffer's rows side by side share none.
+ * gdr_rotary_bwd turns the gradients dq, dk of the outputs back into those of the inputs:
+ * the same call with the opposite angle.
+ */
+int gdr_rotary_fwd(const gdr_rotary_shape *shape, const void *q, const void *k,
+                   const int32_t *positions, const int64_t *rates, void *q_out, void *k_out,
+                   gdr_stream_t stream);
+int gdr_rotary_bwd(const gdr_rotary_shape *shape, const void *dq_out, const void *dk_out,
+                   const int32_t *positions, const int64_t *rates, void *dq, void *dk,
+                   gdr_stream_t stream);
+
+/*
+ * Pages for the new tokens of every request of a paged cache.
+ *
+ * Request n has kv_lens[n] tokens in the cache, in pages block_table[n, 0 ..] of `page` tokens,
+ * and is to get q_lens[n] more. The pages that it lacks are taken from the end of the list of
+ * free pages, free_pages[0 .. *free_count - 1], request by request. A request gets all that it
+ * asks for or nothing:
+ *   - refused if its new tokens end behind `rows`, or it would need more than `width` pages,
+ *     or its length is negative (a negative q_lens counts as 0);
+ *   - refused if it needs pages and the list does not hold those of all requests up to it
+ *     (those refused for the first reason aside).
+ * Results:
+ *   block_table  [num_seqs, width] int32: the new pages' entries are written, no others
+ *   kv_lens_out  [num_seqs] int32: lengths with the new tokens (may be kv_lens)
+ *   free_count_out [1] int32 (may be free_count)
+ *   cu_q         [num_seqs + 1] int32: offsets of the requests' new tokens, cut off at rows
+ *   start        [num_seqs] int32: position of a request's first new token, -1 if refused
+ *   positions    [rows] int32: every new token's position, 0 if there is none
+ *   slots        [rows] int32: page * (tokens per page) + place in it, -1 if there is none
+ * sizes: num_seqs >= 1, rows >= 0, width >= 1, page a power of two in [16, 128],
+ * num_pages * page < 2^31 (the caller's entries are not checked here; users of slots and block
+ * tables check theirs). One or two launches, no workspace; the same results every time.
+ */
+typedef struct gdr_page_shape {
+    int64_t num_seqs, width;   /* block_table [num_seqs, width] */
+    int64_t rows;              /* tokens of the packed batch, padding included */
+    int64_t num_pages;         /* entries of free_pages */
+    int page;
+} gdr_page_shape;
+int gdr_page_plan(const gdr_page_shape *shape, const int32_t *q_lens, const int32_t *kv_lens,
+                  const int32_t *free_pages, const int32_t *free_count, int32_t *block_table,
+                  int32_t *kv_lens_out, int32_t *free_count_out, int32_t *cu_q, int32_t *start,
+                  int32_t *positions, int32_t *slots, gdr_stream_t stream);
+
+/*
+ * Gives the pages of requests that have ended back: for every n with done[n] != 0 (bytes) the
+ * entries of its ceil(kv_lens[n] / page) pages are put behind the free list, in order, and
+ * become -1 in the table; kv_lens[n] becomes 0. In place; `rows` is not used. Pages that the
+ * list has no room for stay with their request.
+ */
+int gdr_page_release(const gdr_page_shape *shape, const uint8_t *done, int32_t *kv_lens,
+                     int32_t *block_table, int32_t *free_pages, int32_t *free_count,
+                     gdr_stream_t stream);
+
+/*
+ * A paged cache of keys and values held in 8 bits.
+ *
+ * k_cache, v_cache [num_pages, kv_heads, page, d] hold codes; k_scale, v_scale [num_pages,
+ * kv_heads] fp32 one scale for each page and head: an entry stands for code * scale.
+ * GDR_CODE_E4M3 codes are 8-bit floating numbers (4 exponent and 3 mantissa bits, largest
+ * 448), GDR_CODE_INT8 codes are integers of at most 127 in size.
+ * gdr_cache_append makes scales that are powers of two, 2^-60 to 2^60: rescaling a page then
+ * loses nothing of a floating code that stays normal, and one rounding of an integer one.
+ */
+enum { GDR_CODE_E4M3 = 0, GDR_CODE_INT8 = 1 };
+typedef struct gdr_cache_shape {
+    int64_t num_pages;
+    int kv_heads, page, d;     /* page a power of two in [16, 128]; d 64, 128 or 256 */
+    int codes;                 /* GDR_CODE_E4M3 or GDR_CODE_INT8 */
+    int dtype;                 /* gdr_dtype of keys, values, queries and outputs */
+} gdr_cache_shape;
+
+/*
+ * Puts new keys and values into their slots.
+ *   k, v   [tokens, kv_heads, d] dtype, token strides in elements (0: dense)
+ *   slots  [tokens] int32: page * (tokens per page) + place. A slot outside the cache (-1 for
+ *          padding) is skipped.
+ * Rows whose slots follow one another within a page form a run. A page gets one run per
+ * call (tokens of one request in order, as gdr_page_plan lays them out); two runs of a page, or a
+ * slot given twice, leave that page's codes and scale unspecified.
+ * A run that begins at a page's first place starts the page anew: its scale is the least power
+ * of two that holds the run's largest entry. A run behind older tokens may only raise the
+ * scale; the older codes are then rounded to the new one. Entries beyond what the largest
+ * scale holds become the largest code. An entry that is not finite makes the page's scale
+ * for that head NaN (the page then reads as NaN) until the page is started anew.
+ */
+int gdr_cache_append(const gdr_cache_shape *shape, int64_t tokens, const void *k, int64_t k_stride,
+                     const void *v, int64_t v_stride, const int32_t *slots, void *k_cache,
+                     void *v_cache, float *k_scale, float *v_scale, gdr_stream_t stream);
+
+/*
+ * Softmax attention of new tokens over the cache.
+ *
+ * Query head h reads head h / (heads / kv_heads) of the cache. For token i of the n_q new
+ * tokens of a request with len = kv_lens[n] tokens in the cache (the new ones among them, so
+ * that it stands at position p = len - n_q + i), over the cached tokens j < len, causal: j <= p:
+ *     s_j = scale q.k_j;   softcap > 0: s_j = softcap tanh(s_j / softcap);
+ *     slopes: s_j -= slopes[h] |p - j|
+ *     o = sum_j softmax(s)_j v_j,   lse = log sum_j exp(s_j)
+ * A token that sees nothing gets o = 0 and lse = -inf.
+ *
+ * Shape of a call (a HOST struct):
+ *   num_seqs, total_tokens   requests (>= 1) and rows of q
+ *   max_q     the most new tokens of one request (with cu_q; else total_tokens / num_seqs)
+ *   heads     a multiple of kv_heads, at most 65536
+ *   width     block_table [num_seqs, width]
+ *   q_stride  elements from a token's first head to the next token's; 0: dense
+ *   causal    nonzero: causal
+ *   scale     finite; softcap finite, >= 0 (0: none)
+ */
+typedef struct gdr_cache_attn_shape {
+    gdr_cache_shape cache;
+    int64_t num_seqs, total_tokens, max_q, width, q_stride;
+    int heads, causal;
+    float scale, softcap;
+} gdr_cache_attn_shape;
+/* Bytes of device workspace (host-only, no CUDA call); 0 for shapes that the call rejects. */
+size_t gdr_cache_attn_workspace_size(const gdr_cache_attn_shape *shape);
+
+/*
+ *   q            [total_tokens, heads, d] dtype, 16-byte aligned
+ *   caches and scales as above; scales positive and in 2^-60 .. 2^60, or NaN
+ *   block_table  [num_seqs, width] int32. Only the first ceil(len / page) entries of a row are
+ *                read. An entry outside the cache makes the results of the tokens that look at
+ *                that page NaN; no access leaves the cache.
+ *   kv_lens      [num_seqs] int32, 0 .. width * page
+ *   cu_q         [num_seqs + 1] int32 offsets from 0, non-decreasing, the last at most
+ *                total_tokens (rows behind it are neither read nor written), no request longer
+ *                than max_q; or NULL for total_tokens / num_seqs tokens each
+ *   slopes       [heads] fp32 or NULL
+ *   o            [total_tokens, heads, d] dtype, dense (written)
+ *   lse          [total_tokens, heads] fp32 (written), or NULL
+ *   workspace    16-byte aligned; calls that share one must be ordered on one stream
+ * kv_lens and cu_q are checked on the device: a violation leaves GDR_ERR_BAD_SEQLENS in the
+ * workspace's status word (gdr_read_device_status) and nothing else is written.
+ * Scores, maxima, sums and outputs are fp32 until o is rounded. bf16: a query is held in fp16
+ * with a power of two per row (exact for entries within 2^-24 of its largest), the weights of a
+ * tile in fp16 relative to a running maximum. fp32: both as two fp16 parts (22 bits).
+ * What is masked or behind len is never used: NaN there stays there. A NaN within a page reaches
+ * the tokens that look at the page's scale. The same results every time.
+ */
+int gdr_cache_attn(const gdr_cache_attn_shape *shape, const void *q, const void *k_cache,
+                   const void *v_cache, const float *k_scale, const float *v_scale,
+                   const int32_t *block_table, const int32_t *kv_lens, const int32_t *cu_q,
+                   const float *slopes, void *o, float *lse, void *workspace,
+                   size_t workspace_bytes, gdr_stream_t stream);
 
 #ifdef __cplusplus
 }

@@ -20,7 +20,7 @@ ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 SOURCES = ["gdr_api.cu", "decode.cu", "prefill_exact.cu", "solve_tc.cu", "prefill_tc.cu", "channel_tc.cu", "noalloc.cu",
            "epilogue.cu", "linattn_api.cu", "linattn_exact.cu", "linattn_tc.cu", "linattn_step.cu", "block_norm.cu",
            "rotary.cu", "pages.cu", "cache_append.cu", "cache_attn_api.cu", "cache_attn_step64.cu", "cache_attn_step128.cu",
-           "cache_attn_step256.cu"]
+           "cache_attn_step256.cu", "cache_attn_tc64.cu", "cache_attn_tc128.cu", "cache_attn_tc256.cu"]
 
 
 def nvcc():

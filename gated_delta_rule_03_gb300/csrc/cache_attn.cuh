@@ -123,6 +123,12 @@ int launch_step256(const Attn &a, int codes, int dtype, void *ws, cudaStream_t s
 size_t step_bytes64();
 size_t step_bytes128();
 size_t step_bytes256();
+int launch_tc64(const Attn &a, int codes, int dtype, void *ws, cudaStream_t s);
+int launch_tc128(const Attn &a, int codes, int dtype, void *ws, cudaStream_t s);
+int launch_tc256(const Attn &a, int codes, int dtype, void *ws, cudaStream_t s);
+size_t tc_bytes64(const Attn &a, int dtype);
+size_t tc_bytes128(const Attn &a, int dtype);
+size_t tc_bytes256(const Attn &a, int dtype);
 
 }  // namespace cattn
 }  // namespace gdr

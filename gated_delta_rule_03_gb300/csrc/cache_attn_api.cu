@@ -34,21 +34,31 @@ int check_shape(const gdr_cache_attn_shape *s, Call *c) {
     if ((st = row_stride(s->q_stride, (int64_t)s->heads * c->d, c->e, &a.qs)) != GDR_OK) return st;
     a.num_seqs = s->num_seqs;
     a.tokens = s->total_tokens;
-    a.max_q = s->max_q;
+    a.max_q = s->max_q < s->total_tokens ? s->max_q : s->total_tokens;
     a.width = s->width;
     a.pages = s->cache.num_pages;
     a.heads = s->heads;
     a.kv_heads = s->cache.kv_heads;
     a.group = s->heads / s->cache.kv_heads;
     a.causal = s->causal != 0;
+    if (a.max_q > (INT32_MAX - 256) / a.group) return GDR_ERR_INVALID_ARG;  // (rows of an item are 32-bit numbers)
     a.scale = s->scale;
     a.softcap = s->softcap;
     return GDR_OK;
 }
 
 constexpr size_t kHead = 256;  // the status word
+
+// Few rows share a head of the cache: at most a tile of the warp-level products. Single tokens are (up
+// to 16 heads a group); the other kernel fills its rows from 17 on.
+bool few_rows(const Attn &a) { return a.max_q * a.group <= 16; }
+
 size_t workspace_bytes(const Call &c) {
-    return kHead + (c.d == 64 ? step_bytes64() : c.d == 128 ? step_bytes128() : step_bytes256());
+    // (equal lengths without offsets may be shorter than max_q)
+    const size_t step = c.d == 64 ? step_bytes64() : c.d == 128 ? step_bytes128() : step_bytes256();
+    if (few_rows(c.a)) return kHead + step;
+    const size_t tc = c.d == 64 ? tc_bytes64(c.a, c.dtype) : c.d == 128 ? tc_bytes128(c.a, c.dtype) : tc_bytes256(c.a, c.dtype);
+    return kHead + (tc > step ? tc : step);
 }
 
 }  // namespace
@@ -111,8 +121,11 @@ int gdr_cache_attn(const gdr_cache_attn_shape *shape, const void *q, const void 
     if (!cu_q) a.max_q = a.tokens / a.num_seqs;
     void *const ws = (char *)workspace + kHead;
     const cudaStream_t s = (cudaStream_t)stream;
-    return c.d == 64 ? launch_step64(a, c.codes, c.dtype, ws, s)
-                     : c.d == 128 ? launch_step128(a, c.codes, c.dtype, ws, s) : launch_step256(a, c.codes, c.dtype, ws, s);
+    if (few_rows(a))
+        return c.d == 64 ? launch_step64(a, c.codes, c.dtype, ws, s)
+                         : c.d == 128 ? launch_step128(a, c.codes, c.dtype, ws, s) : launch_step256(a, c.codes, c.dtype, ws, s);
+    return c.d == 64 ? launch_tc64(a, c.codes, c.dtype, ws, s)
+                     : c.d == 128 ? launch_tc128(a, c.codes, c.dtype, ws, s) : launch_tc256(a, c.codes, c.dtype, ws, s);
 }
 
 }  // extern "C"

@@ -310,7 +310,7 @@ __global__ void __launch_bounds__(kStepWarps * 32, (StepConfig<D, kParts>::kBloc
                 }
             }
             // scores in powers of two, with the value scale's
-            const float lv = lg2(sc.y), rv = __fdividef(1.f, sc.y);
+            const float lv = lg2(sc.y), rv = sc.y == sc.y ? __fdividef(1.f, sc.y) : 1.f;  // (a weight there is NaN, or 0 if masked)
             const float m0 = f0 * sc.x, m1 = f1 * sc.x;
 #pragma unroll
             for (int t = 0; t < 2; ++t)
@@ -356,16 +356,8 @@ __global__ void __launch_bounds__(kStepWarps * 32, (StepConfig<D, kParts>::kBloc
             for (int t = 0; t < 2; ++t)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) s[t][e] = ex2(s[t][e] - (e < 2 ? ref0 : ref1));
-            if (edge && sc.y != sc.y) {  // (a page without a scale reaches only who looks at it)
-#pragma unroll
-                for (int t = 0; t < 2; ++t)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        if (tok + 8 * t + 2 * c + (e & 1) < (e < 2 ? lim0 : lim1)) (e < 2 ? l0 : l1) = sc.y;
-            } else {
-                l0 = fmaf((s[0][0] + s[0][1]) + (s[1][0] + s[1][1]), rv, l0);
-                l1 = fmaf((s[0][2] + s[0][3]) + (s[1][2] + s[1][3]), rv, l1);
-            }
+            l0 = fmaf((s[0][0] + s[0][1]) + (s[1][0] + s[1][1]), rv, l0);
+            l1 = fmaf((s[0][2] + s[0][3]) + (s[1][2] + s[1][3]), rv, l1);
             uint32_t p[kParts][4];
 #pragma unroll
             for (int y = 0; y < 4; ++y) {

@@ -1,0 +1,13 @@
+// cache_attn_tc256.cu -- the many-row kernels of cache_attn_tc.cuh for heads of 256.
+#include "cache_attn_tc.cuh"
+
+namespace gdr {
+namespace cattn {
+
+int launch_tc256(const Attn &a, int codes, int dtype, void *ws, cudaStream_t s) {
+    return launch_tc_d<256>(a, codes, dtype, ws, s);
+}
+size_t tc_bytes256(const Attn &a, int dtype) { return tc_bytes_d<256>(a, dtype); }
+
+}  // namespace cattn
+}  // namespace gdr

@@ -30,11 +30,12 @@ namespace cattn {
 using namespace sm100;
 
 constexpr int kTcThreads = 416;
-constexpr int kRing = 4;  // tiles of scales
+constexpr int kRing = 4;   // tiles of scales
+constexpr int kFlush = 4;  // tiles whose outputs are added up in TMEM (fp32)
 
 template <int D, int kParts> struct TcConfig {
     static constexpr int kTiles = kParts == 1 && D <= 128 ? 2 : 1;
-    static constexpr int kKeys = kParts == 2 && D == 256 ? 64 : 128;
+    static constexpr int kKeys = kParts == 2 ? 64 : 128;
     static constexpr int kRows = 128 * kTiles;
     static constexpr int kSoft = 128 * kTiles;         // threads
     static constexpr int kConv = 384 - kSoft;
@@ -44,9 +45,9 @@ template <int D, int kParts> struct TcConfig {
     static constexpr int kSmem = kTiles * kParts * kQ + 2 * kStages * kKv + 1024;
     // TMEM columns: scores of two slots (weights in their place), outputs, low parts of weights
     static constexpr uint32_t kS = kKeys, kO = 256;
-    static constexpr uint32_t kLow = D == 256 ? 128 : 384, kLowStep = kKeys / 2;
+    static constexpr uint32_t kLow = 128, kLowStep = kKeys / 2;
     static_assert(kSmem <= 232448 - 1024, "shared memory");
-    static_assert(kO + kTiles * D <= 512 && 2 * kKeys <= 256, "TMEM");
+    static_assert(kO + kTiles * D <= 512 && 2 * kKeys + (kParts == 2 ? 2 * kLowStep : 0) <= kO, "TMEM");
 };
 
 struct TcPlan {
@@ -61,6 +62,30 @@ template <int kRows, int D> struct TcPart {
 
 __host__ __device__ constexpr uint32_t idesc_f16(int M, int N, int b_mn) {
     return (1u << 4) | ((uint32_t)b_mn << 16) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+
+// Low words of shared-memory descriptors of 128-byte-swizzled tiles (sw128_desc), to which places within a
+// tile are added: K-major, and MN-major with `apart` bytes between 64-wide blocks. The high word is one for all.
+__device__ __forceinline__ uint32_t desc_k(uint32_t at) { return (at >> 4) | (1u << 16); }
+__device__ __forceinline__ uint32_t desc_mn(uint32_t at, uint32_t apart) { return (at >> 4) | ((apart >> 4) << 16); }
+constexpr uint32_t kDescHigh = (1024u >> 4) | (1u << 14) | (2u << 29);
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, bool add) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 x, y;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "mov.b64 x, {%1, %5};\n\tmov.b64 y, {%2, %5};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "r"(b), "r"(idesc), "r"((uint32_t)add), "r"(kDescHigh)
+        : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, bool add) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 y;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "mov.b64 y, {%2, %5};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "r"(b), "r"(idesc), "r"((uint32_t)add), "r"(kDescHigh)
+        : "memory");
 }
 
 // Where a block's rows are: request n, its rows from row0 on.
@@ -117,26 +142,74 @@ template <int kRows> __device__ inline bool find_tile(const Attn &a, int64_t x, 
     return true;
 }
 
-// 32 fp32 columns of this thread's TMEM lane, the wait apart (tmem_arrive).
-__device__ __forceinline__ void tmem_fetch32(uint32_t taddr, uint32_t (&r)[32]) {
+// 16 columns of this thread's TMEM lane, the wait apart; the wait names every register, so that no use
+// comes before it.
+__device__ __forceinline__ void tmem_fetch16(uint32_t taddr, uint32_t (&r)[16]) {
     asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
-        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
         : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]),
-          "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]),
-          "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]),
-          "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+          "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
         : "r"(taddr)
         : "memory");
 }
-__device__ __forceinline__ void tmem_arrive(uint32_t (&r)[32]) {
+__device__ __forceinline__ void tmem_arrive16(uint32_t (&r)[16]) {
 #pragma unroll
-    for (int i = 0; i < 32; i += 8)
+    for (int i = 0; i < 16; i += 8)
         asm volatile("tcgen05.wait::ld.sync.aligned;"
                      : "+r"(r[i]), "+r"(r[i + 1]), "+r"(r[i + 2]), "+r"(r[i + 3]), "+r"(r[i + 4]), "+r"(r[i + 5]), "+r"(r[i + 6]),
                        "+r"(r[i + 7])::"memory");
 }
+// 16 columns stored, the wait apart (tmem_stored).
+__device__ __forceinline__ void tmem_put16(uint32_t taddr, const uint32_t *r) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+        "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
+        "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        : "memory");
+}
+__device__ __forceinline__ void tmem_stored() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// What becomes of scores: nothing more, a cap, or a bias by distance with or without a cap.
+enum { kPlain = 0, kCapped = 1, kBiased = 2 };
+
+// Exponents of 16 keys' weights from products with their codes: m scales a product (log2(e) in it if
+// kPlain), off: log2 of the value scale less the row's reference, away: p - j of the first key.
+// tanh(x) = 1 - 2 / (1 + e^2x) as in cache_attn.cuh; of a capped score the rest folds into one multiply-add.
+template <int kMode, bool kExact> struct Shape {
+    float m, off, cap, slope, away, k;
+    __device__ __forceinline__ Shape(float m_, float off_, float cap_, float inv_cap, float slope_, float away_)
+        : m(m_), off(off_), cap(cap_), slope(slope_), away(away_), k(0.f) {
+        if (kMode == kCapped && !kExact) {
+            m = m_ * inv_cap * (2.f * kLog2e);
+            off = fmaf(cap_, kLog2e, off_);
+            k = -2.f * kLog2e * cap_;
+        } else if (kMode != kPlain && cap_ > 0.f) {
+            k = inv_cap;
+        }
+    }
+    static __device__ __forceinline__ float rcp(float x) {
+        float y;
+        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+        return y;
+    }
+    __device__ __forceinline__ float one(float z, int e) const {
+        z *= m;
+        if (cap > 0.f) z = cap * (kExact ? tanhf(z * k) : fmaf(-2.f, rcp(1.f + ex2(z * k * (2.f * kLog2e))), 1.f));
+        if (kMode == kBiased) z = fmaf(-slope, fabsf(away - (float)e), z);
+        return fmaf(z, kLog2e, off);
+    }
+    __device__ __forceinline__ float2 operator()(float2 z, int e) const {
+        if (kMode == kPlain) return fma2(z, make_float2(m, m), make_float2(off, off));
+        if (kMode == kCapped && !kExact) {
+            float2 x = mul2(z, make_float2(m, m));
+            x = add2(make_float2(ex2(x.x), ex2(x.y)), make_float2(1.f, 1.f));
+            return fma2(make_float2(rcp(x.x), rcp(x.y)), make_float2(k, k), make_float2(off, off));
+        }
+        return make_float2(one(z.x, e), one(z.y, e + 1));
+    }
+};
 
 __device__ __forceinline__ uint32_t f16_pair(float lo, float hi) {
     uint32_t r;
@@ -144,11 +217,17 @@ __device__ __forceinline__ uint32_t f16_pair(float lo, float hi) {
     return r;
 }
 __device__ __forceinline__ float2 f16_values(uint32_t r) { return __half22float2(reinterpret_cast<const __half2 &>(r)); }
+// Issued where it stands: a load that the compiler may move ends up next to its use.
+__device__ __forceinline__ uint4 ld_nc(const void *p) {
+    uint4 v;
+    asm volatile("ld.global.nc.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+    return v;
+}
 __device__ __forceinline__ void store16(uint32_t saddr, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
     asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(saddr), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
 }
 
-template <typename T, int D, int kParts, bool kShaped>
+template <typename T, int D, int kParts, int kMode>
 __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_constant__ Attn a, const TcPlan plan, const int code) {
     using C = TcConfig<D, kParts>;
     extern __shared__ unsigned char sm[];
@@ -203,42 +282,47 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_con
         const uint32_t to = sq + (r >> 7) * kParts * C::kQ;
         const bool live = r < nrows;
         const T *src = live ? (const T *)a.q + (int64_t)(item.first + at / a.group) * a.qs + (int64_t)(head * a.group + at % a.group) * D : nullptr;
+        // 256 bytes of the row at a time in registers, all of them under way together; longer rows come twice
+        constexpr int kPiece = 256 / sizeof(T), kPieces = (D + kPiece - 1) / kPiece, kVecs = (D < kPiece ? D : kPiece) * sizeof(T) / 16;
         constexpr int kVec = 16 / sizeof(T);
-        auto eight = [&](int d, float (&v)[8]) {
+        uint4 w[kVecs];
+        auto fetch = [&](int piece) {
 #pragma unroll
-            for (int i = 0; i < 8; i += kVec) {
-                const uint4 w = live ? __ldg((const uint4 *)(src + d + i)) : make_uint4(0, 0, 0, 0);
-                const T *e = (const T *)&w;
-#pragma unroll
-                for (int x = 0; x < kVec; ++x) v[i + x] = to_f32<T>(e[x]);
-            }
+            for (int i = 0; i < kVecs; ++i) w[i] = live ? ld_nc(src + piece * kPiece + i * kVec) : make_uint4(0, 0, 0, 0);
         };
         uint32_t most = 0;
-#pragma unroll 4
-        for (int d = 0; d < D; d += 8) {
-            float v[8];
-            eight(d, v);
+#pragma unroll 1
+        for (int piece = kPieces - 1; piece >= 0; --piece) {
+            fetch(piece);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) most = max(most, __float_as_uint(v[i]) & 0x7fffffffu);
+            for (int i = 0; i < kVecs; ++i) {
+                const T *e = (const T *)&w[i];
+#pragma unroll
+                for (int x = 0; x < kVec; ++x) most = max(most, __float_as_uint(to_f32<T>(e[x])) & 0x7fffffffu);
+            }
         }
         const int shift = row_shift(most);
         const float up = a.scale < 0.f ? -two_to(shift) : two_to(shift);
         row_up = two_to(-shift) * fabsf(a.scale);
-#pragma unroll 4
-        for (int d = 0; d < D; d += 8) {
-            float v[8];
-            eight(d, v);
-            uint32_t hi[4], lo[4];
+#pragma unroll 1
+        for (int piece = 0; piece < kPieces; ++piece) {
+            if (piece > 0) fetch(piece);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float x = v[2 * i] * up, y = v[2 * i + 1] * up;
-                hi[i] = f16_pair(x, y);
-                const float2 f = f16_values(hi[i]);
-                lo[i] = f16_pair(x - f.x, y - f.y);
+            for (int c = 0; c < kVecs * kVec; c += 8) {
+                uint32_t hi[4], lo[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int e = c + 2 * i;
+                    const float x = to_f32<T>(((const T *)&w[e / kVec])[e % kVec]) * up, y = to_f32<T>(((const T *)&w[(e + 1) / kVec])[(e + 1) % kVec]) * up;
+                    hi[i] = f16_pair(x, y);
+                    const float2 f = f16_values(hi[i]);
+                    lo[i] = f16_pair(x - f.x, y - f.y);
+                }
+                const int d = piece * kPiece + c;
+                const uint32_t dst = to + (d >> 6) * 16384 + sw128_offset(r & 127, d & 63);
+                store16(dst, hi[0], hi[1], hi[2], hi[3]);
+                if (kParts == 2) store16(dst + C::kQ, lo[0], lo[1], lo[2], lo[3]);
             }
-            const uint32_t dst = to + (d >> 6) * 16384 + sw128_offset(r & 127, d & 63);
-            store16(dst, hi[0], hi[1], hi[2], hi[3]);
-            if (kParts == 2) store16(dst + C::kQ, lo[0], lo[1], lo[2], lo[3]);
         }
         fence_async_smem();
     }
@@ -256,9 +340,37 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_con
         const int p = past + at / a.group, lim = a.causal ? min(len, p + 1) : len;
         const int sure = a.causal ? min(len, past + (row0 + tile * 128) / a.group + 1) : len;
         const uint32_t out = tmem + lanes + C::kO + tile * D;
-        const float slope = kShaped && a.slopes && tid < nrows ? __ldg(a.slopes + head * a.group + at % a.group) : 0.f;
-        float ref = kNoRef, l = 0.f;
-        const float up2 = row_up * (kShaped ? 1.f : kLog2e);
+        const bool live = tid < nrows;
+        const int64_t row = (int64_t)(item.first + at / a.group) * a.heads + head * a.group + at % a.group;
+        TcPart<C::kRows, D> *const part = (TcPart<C::kRows, D> *)plan.parts + (((int64_t)head * plan.tiles + blockIdx.x) * plan.splits + split);
+        float *const row_out = plan.splits > 1 ? part->o[tid] : (float *)a.o + row * D;  // (fp32 only without splits)
+        const float slope = kMode == kBiased && a.slopes && live ? __ldg(a.slopes + head * a.group + at % a.group) : 0.f;
+        const float cap = kMode == kPlain ? 0.f : a.softcap, inv_cap = cap > 0.f ? 1.f / cap : 0.f;
+        const float up2 = row_up * (kMode == kPlain ? kLog2e : 1.f);
+        float ref = 0.f, l = 0.f;
+        float sum_ref = 0.f, sum_l = 0.f;  // kParts == 2: of what has left TMEM
+
+        // The tensor cores cut the sums in TMEM instead of rounding them, some 2^-24 of them per step and always
+        // towards zero: fp32 results take the outputs of kFlush tiles at a time out and add them up in memory.
+        auto flush = [&] {
+            const bool some = sum_l != 0.f;
+            const float by = some ? ex2(sum_ref - ref) : 0.f;
+#pragma unroll 1
+            for (int c = 0; c < D; c += 32) {
+                float v[32];
+                tmem_load32(out + c, v);
+                if (!live) continue;
+#pragma unroll
+                for (int e = 0; e < 32; e += 4) {
+                    float4 o = some ? *(const float4 *)(row_out + c + e) : make_float4(0.f, 0.f, 0.f, 0.f);
+                    o = make_float4(fmaf(o.x, by, v[e]), fmaf(o.y, by, v[e + 1]), fmaf(o.z, by, v[e + 2]), fmaf(o.w, by, v[e + 3]));
+                    *(float4 *)(row_out + c + e) = o;
+                }
+            }
+            sum_l = fmaf(sum_l, by, l);
+            sum_ref = ref;
+            l = 0.f;
+        };
 
         for (int i = 0; i < count && fine; ++i) {
             const int slot = C::kTiles == 2 ? tile : i & 1, use = C::kTiles == 2 ? i : i >> 1;
@@ -267,118 +379,96 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_con
                 fine = false;
                 break;
             }
+            // The outputs of the tiles before. With two row tiles the scores' barrier says that they are there; with
+            // one it does so of the last but one tile, and the last has a barrier that even and odd tiles share in turn.
+            auto outputs_done = [&] {
+                if (C::kTiles == 1 && !mbar_wait(bar(O_DONE + ((i - 1) & 1)), ((i - 1) >> 1) & 1)) fine = false;
+                __syncwarp();
+                tc_fence_after();
+            };
             __syncwarp();
             tc_fence_after();
+            const bool anew = kParts == 2 && i % kFlush == 0;  // (this tile's product begins the outputs)
+            if (anew && i > 0) {
+                outputs_done();
+                if (!__all_sync(~0u, fine)) break;
+                flush();
+            }
             const int tok = (j0 + i) * C::kKeys;
             const float4 *const sc = scales[(j0 + i) % kRing];
             const bool edge = tok + C::kKeys > sure;
-            // a score in powers of two, with the value scale's
-            auto value = [&](float z, float f, float lv, int j) {
-                return kShaped ? fmaf(shaped<kParts == 2>(z * f, a.softcap, slope, fabsf((float)(p - j))), kLog2e, lv) : fmaf(z, f, lv);
-            };
-            float top = -INFINITY;
-            auto largest = [&](auto at_edge) {
+
+            // Weights with the row's reference as it is, 16 keys at a time, and the largest exponent. The first tile
+            // (a row that sees none of its keys sees no later ones), or an exponent that is too large, moves the
+            // reference, and the outputs so far with it; then the weights are taken again.
+            uint32_t hi[C::kKeys / 2], lo[kParts == 2 ? C::kKeys / 2 : 1];
+            float sum = 0.f, top = -INFINITY;
+            auto weigh = [&](auto at_edge) {
                 constexpr bool kEdge = decltype(at_edge)::value;
+                float2 all = make_float2(0.f, 0.f);
+                top = -INFINITY;
+                uint32_t x[2][16];
+                tmem_fetch16(s_at, x[0]);
 #pragma unroll
-                for (int c = 0; c < C::kKeys; c += 32) {
-                    uint32_t x[32];
-                    tmem_fetch32(s_at + c, x);
-                    tmem_arrive(x);
+                for (int g = 0; g < C::kKeys / 16; ++g) {
+                    uint32_t(&y)[16] = x[g & 1];
+                    tmem_arrive16(y);
+                    if (g + 1 < C::kKeys / 16) tmem_fetch16(s_at + 16 * (g + 1), x[(g + 1) & 1]);
+                    const float4 f = sc[g];
+                    const Shape<kMode, kParts == 2> shape(f.x * up2, f.y - ref, cap, inv_cap, slope, (float)(p - tok - 16 * g));
+                    float2 some = make_float2(0.f, 0.f);
 #pragma unroll
-                    for (int g = 0; g < 2; ++g) {
-                        const float4 f = sc[c / 16 + g];
-                        const float m = f.x * up2;
-                        float big = -INFINITY;
-                        if (kShaped && a.slopes) {
-#pragma unroll
-                            for (int e = 0; e < 16; ++e) {
-                                const int j = tok + c + 16 * g + e;
-                                const float z = value(__uint_as_float(x[16 * g + e]), m, f.y, j);
-                                big = fmaxf(big, kEdge && j >= lim ? -INFINITY : z);
-                            }
-                            top = fmaxf(top, big);
-                        } else {  // (the value rises with the score: factors are not negative)
-#pragma unroll
-                            for (int e = 0; e < 16; ++e) {
-                                const float z = __uint_as_float(x[16 * g + e]);
-                                big = fmaxf(big, kEdge && tok + c + 16 * g + e >= lim ? -INFINITY : z);
-                            }
-                            if (big > -INFINITY) top = fmaxf(top, value(big, m, f.y, 0));
+                    for (int e = 0; e < 16; e += 2) {
+                        float2 w = shape(make_float2(__uint_as_float(y[e]), __uint_as_float(y[e + 1])), e);
+                        if (kEdge) {
+                            const int j = tok + 16 * g + e;
+                            if (j >= lim) w.x = -INFINITY;
+                            if (j + 1 >= lim) w.y = -INFINITY;
+                        }
+                        top = fmaxf(top, fmaxf(w.x, w.y));
+                        w.x = ex2(w.x);
+                        w.y = ex2(w.y);
+                        some = add2(some, w);
+                        const int q = 8 * g + e / 2;
+                        hi[q] = f16_pair(w.x, w.y);
+                        if (kParts == 2) {
+                            const float2 v = f16_values(hi[q]);
+                            lo[q] = f16_pair(w.x - v.x, w.y - v.y);
                         }
                     }
+                    all = fma2(some, make_float2(f.z, f.z), all);
                 }
+                sum = all.x + all.y;
             };
-            if (edge) largest(std::true_type{});
-            else largest(std::false_type{});
-            const bool move = top > ref + (kSpan + kSlack);
-            if (__any_sync(~0u, move)) {
-                // The outputs so far have to be there. With two row tiles the scores' barrier says so; with one the
-                // last but one product does, and the last has a barrier that even and odd tiles share in turn.
-                if (C::kTiles == 1 && i > 0 && !mbar_wait(bar(O_DONE + ((i - 1) & 1)), ((i - 1) >> 1) & 1)) {
-                    fine = false;
-                    break;
-                }
-                tc_fence_after();
-                const float next = move ? top - kSpan : ref, by = ex2(ref - next);
-                ref = next;
-                l *= by;
+            for (bool settled = false;; settled = true) {
+                if (edge) weigh(std::true_type{});
+                else weigh(std::false_type{});
+                if (settled || (i > 0 && !__any_sync(~0u, top > kSpan + kSlack))) break;
+                const bool move = i == 0 ? top > -INFINITY : top > kSpan + kSlack;
+                if (move) ref += top - kSpan;
                 if (i > 0) {
+                    const float by = move ? ex2(kSpan - top) : 1.f;
+                    l *= by;
+                    if (!anew) {
+                        outputs_done();
 #pragma unroll 1
-                    for (int c = 0; c < D; c += 32) {
-                        float v[32];
-                        tmem_load32(out + c, v);
+                        for (int c = 0; c < D; c += 32) {
+                            float v[32];
+                            tmem_load32(out + c, v);
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) v[e] *= by;
-                        tmem_store32(out + c, v);
+                            for (int e = 0; e < 32; ++e) v[e] *= by;
+                            tmem_store32(out + c, v);
+                        }
                     }
                 }
             }
-            auto weigh = [&](auto at_edge) {
-                constexpr bool kEdge = decltype(at_edge)::value;
+            l += sum;
 #pragma unroll
-                for (int c = 0; c < C::kKeys; c += 32) {
-                    uint32_t x[32];
-                    tmem_fetch32(s_at + c, x);
-                    tmem_arrive(x);
-                    uint32_t hi[16], lo[kParts == 2 ? 16 : 1];
-#pragma unroll
-                    for (int g = 0; g < 2; ++g) {
-                        const float4 f = sc[c / 16 + g];
-                        const float m = f.x * up2, off = f.y - ref;
-                        float2 sum = make_float2(0.f, 0.f);
-#pragma unroll
-                        for (int e = 0; e < 16; e += 2) {
-                            const int j = tok + c + 16 * g + e;
-                            const float z0 = __uint_as_float(x[16 * g + e]), z1 = __uint_as_float(x[16 * g + e + 1]);
-                            float2 w;
-                            if (kShaped) {
-                                w = make_float2(ex2(value(z0, m, off, j)), ex2(value(z1, m, off, j + 1)));
-                            } else {
-                                w = fma2(make_float2(z0, z1), make_float2(m, m), make_float2(off, off));
-                                w.x = ex2(w.x);
-                                w.y = ex2(w.y);
-                            }
-                            if (kEdge) {
-                                if (j >= lim) w.x = 0.f;
-                                if (j + 1 >= lim) w.y = 0.f;
-                            }
-                            sum.x += w.x;
-                            sum.y += w.y;
-                            const int q = 8 * g + e / 2;
-                            hi[q] = f16_pair(w.x, w.y);
-                            if (kParts == 2) {
-                                const float2 v = f16_values(hi[q]);
-                                lo[q] = f16_pair(w.x - v.x, w.y - v.y);
-                            }
-                        }
-                        l = fmaf(sum.x + sum.y, f.z, l);
-                    }
-                    tmem_store16(s_at + c / 2, hi);
-                    if constexpr (kParts == 2) tmem_store16(tmem + lanes + C::kLow + slot * C::kLowStep + c / 2, lo);
-                }
-            };
-            if (edge) weigh(std::true_type{});
-            else weigh(std::false_type{});
+            for (int c = 0; c < C::kKeys / 2; c += 16) {
+                tmem_put16(s_at + c, hi + c);
+                if constexpr (kParts == 2) tmem_put16(tmem + lanes + C::kLow + slot * C::kLowStep + c, lo + c);
+            }
+            tmem_stored();
             tc_fence_before();
             mbar_arrive(bar(W_FULL + slot));
         }
@@ -388,22 +478,18 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_con
             __syncwarp();
             tc_fence_after();
         }
-        if (fine && tid < nrows) {
-            const bool some = l != 0.f;
-            const float inv = some ? 1.f / l : 0.f, sum2 = some ? log2f(l) + ref : -INFINITY;
-            const int64_t row = (int64_t)(item.first + at / a.group) * a.heads + head * a.group + at % a.group;
-            if (plan.splits > 1) {
-                const int64_t part = ((int64_t)head * plan.tiles + blockIdx.x) * plan.splits + split;
-                ((TcPart<C::kRows, D> *)plan.parts)[part].lse2[tid] = sum2;
-            } else if (a.lse) {
-                a.lse[row] = sum2 * kLn2;
-            }
-        }
         // (a warp reads its lanes together, whichever rows are live)
         if (__all_sync(~0u, fine)) {
-            const float inv = l != 0.f ? 1.f / l : 0.f;
-            const int64_t row = (int64_t)(item.first + at / a.group) * a.heads + head * a.group + at % a.group;
-            const int64_t part = ((int64_t)head * plan.tiles + blockIdx.x) * plan.splits + split;
+            const float by = kParts == 2 ? ex2(sum_ref - ref) : 0.f;
+            const bool older = kParts == 2 && sum_l != 0.f;
+            if (older) l = fmaf(sum_l, by, l);
+            const bool some = l != 0.f;
+            const float inv = some ? 1.f / l : 0.f;
+            if (live) {
+                const float sum2 = some ? log2f(l) + ref : -INFINITY;
+                if (plan.splits > 1) part->lse2[tid] = sum2;
+                else if (a.lse) a.lse[row] = sum2 * kLn2;
+            }
 #pragma unroll 1
             for (int c = 0; c < D; c += 32) {
                 float v[32];
@@ -413,13 +499,22 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_con
 #pragma unroll
                     for (int e = 0; e < 32; ++e) v[e] = 0.f;
                 }
-                if (tid >= nrows) continue;
+                if (!live) continue;
+                if (older) {
 #pragma unroll
-                for (int e = 0; e < 32; ++e) v[e] = l != 0.f ? v[e] * inv : 0.f;
+                    for (int e = 0; e < 32; e += 4) {
+                        const float4 o = *(const float4 *)(row_out + c + e);
+                        v[e] = fmaf(o.x, by, v[e]);
+                        v[e + 1] = fmaf(o.y, by, v[e + 1]);
+                        v[e + 2] = fmaf(o.z, by, v[e + 2]);
+                        v[e + 3] = fmaf(o.w, by, v[e + 3]);
+                    }
+                }
+#pragma unroll
+                for (int e = 0; e < 32; ++e) v[e] = some ? v[e] * inv : 0.f;
                 if (plan.splits > 1 || sizeof(T) == 4) {
-                    float *const to = plan.splits > 1 ? &((TcPart<C::kRows, D> *)plan.parts)[part].o[tid][c] : (float *)a.o + row * D + c;
 #pragma unroll
-                    for (int e = 0; e < 32; e += 4) *(float4 *)(to + e) = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
+                    for (int e = 0; e < 32; e += 4) *(float4 *)(row_out + c + e) = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
                 } else {
                     __nv_bfloat16 *const to = (__nv_bfloat16 *)a.o + row * D + c;
 #pragma unroll
@@ -445,22 +540,33 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_con
         // Eight lanes in turn write 16-byte chunks 2x of two rows, one even and one odd: no two in the same banks.
         const int x = lane & 3, blk = (lane >> 3) & (kBlocks - 1), row_lo = (lane >> 2) & 1;
         const int row = cw * kWarpRows + row_lo + 2 * (lane >> (3 + (kBlocks == 4 ? 2 : kBlocks == 2 ? 1 : 0)));
-        const int in_page = (1 << a.log_page) - 1;
-        // page of the 16 keys `lane & 7` of tile i: -1 behind the last token and outside the cache
-        auto pages_of = [&](int i) {
-            const int tok = (j0 + i) * C::kKeys + (lane & 7) * 16;
-            if (i >= count || (lane & 7) * 16 >= C::kKeys || tok >= len) return -1;
-            const int pg = __ldg(a.table + (int64_t)n * a.width + (tok >> a.log_page));
-            return pg >= 0 && pg < a.pages ? pg : -2;
+        const int in_page = (1 << a.log_page) - 1, lane_off = (row & 15) * D + blk * 64 + x * 16;
+        // Lane g < 8 knows 16 keys of a tile: their page (-1 behind the last token, -2 outside the cache), and
+        // where their codes begin.
+        struct Keys {
+            int page;
+            int64_t at;
         };
-        auto load = [&](const uint8_t *cache, int i, int pages, uint4 (&v)[kPasses]) {
+        auto keys_of = [&](int i) {
+            const int tok = (j0 + i) * C::kKeys + (lane & 7) * 16;
+            if (i >= count || (lane & 7) * 16 >= C::kKeys || tok >= len) return Keys{-1, 0};
+            int pg = __ldg(a.table + (int64_t)n * a.width + (tok >> a.log_page));
+            if (pg < 0 || pg >= a.pages) pg = -2;
+            return Keys{pg, (((int64_t)pg * a.kv_heads + head) * (in_page + 1) + (tok & in_page)) * D};
+        };
+        auto load = [&](const uint8_t *cache, int i, const Keys &keys, uint4 (&v)[kPasses]) {
+            const bool full = (j0 + i + 1) * C::kKeys <= len && __all_sync(~0u, keys.page >= 0 || (lane & 7) * 16 >= C::kKeys);
 #pragma unroll
             for (int ps = 0; ps < kPasses; ++ps) {
-                const int r = ps * kPass + row, tok = (j0 + i) * C::kKeys + r;
-                const int pg = __shfl_sync(~0u, pages, r >> 4);
-                v[ps] = make_uint4(0, 0, 0, 0);
-                if (pg >= 0 && tok < len)
-                    v[ps] = __ldg((const uint4 *)(cache + ((((int64_t)pg * a.kv_heads + head) << a.log_page) + (tok & in_page)) * D + blk * 64 + x * 16));
+                const int g = (ps * kPass + cw * kWarpRows) >> 4;  // (a warp's rows of a pass lie in one of the 16s)
+                const uint8_t *const from = cache + (__shfl_sync(~0u, keys.at, g) + lane_off);
+                if (full) {
+                    v[ps] = ld_nc(from);
+                } else {
+                    const int pg = __shfl_sync(~0u, keys.page, g);
+                    v[ps] = make_uint4(0, 0, 0, 0);
+                    if (pg >= 0 && (j0 + i) * C::kKeys + ps * kPass + row < len) v[ps] = ld_nc(from);
+                }
             }
         };
         auto put = [&](uint32_t to, const uint4 (&v)[kPasses]) {
@@ -482,18 +588,18 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_con
             }
             fence_async_smem();
         };
-        int pages = pages_of(0), next = pages_of(1);
+        Keys keys = keys_of(0), next = keys_of(1);
         uint4 k[kPasses], v[kPasses];
-        load(a.kc, 0, pages, k);
+        load(a.kc, 0, keys, k);
         for (int i = 0; i < count; ++i) {
             const int st = i % C::kStages, turn = (i / C::kStages) & 1;
-            load(a.vc, i, pages, v);
+            load(a.vc, i, keys, v);
             if (cw == 0 && lane < C::kKeys / 16) {
                 float4 f = make_float4(0.f, 0.f, 1.f, 0.f);  // (behind the last token: masked)
-                if (pages != -1) {
+                if (keys.page != -1) {
                     const float bad = __int_as_float(0x7fffffff);
-                    const float ks = pages < 0 ? bad : __ldg(a.ks + (int64_t)pages * a.kv_heads + head);
-                    const float vs = pages < 0 ? bad : __ldg(a.vs + (int64_t)pages * a.kv_heads + head);
+                    const float ks = keys.page < 0 ? bad : __ldg(a.ks + (int64_t)keys.page * a.kv_heads + head);
+                    const float vs = keys.page < 0 ? bad : __ldg(a.vs + (int64_t)keys.page * a.kv_heads + head);
                     f = make_float4(ks, lg2(vs), vs == vs ? __fdividef(1.f, vs) : 1.f, 0.f);
                 }
                 scales[(j0 + i) % kRing][lane] = f;
@@ -504,9 +610,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_con
             }
             put(sk + st * C::kKv, k);
             mbar_arrive(bar(K_FULL + st));
-            pages = next;
-            next = pages_of(i + 2);
-            load(a.kc, i + 1, pages, k);
+            keys = next;
+            next = keys_of(i + 2);
+            load(a.kc, i + 1, keys, k);
             if (!mbar_wait(bar(V_FREE + st), turn ^ 1)) {
                 fine = false;
                 break;
@@ -517,24 +623,26 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_con
     } else if (lane == 0) {
         // ---------------------------------------------------------------- products
         const uint32_t id_s = idesc_f16(128, C::kKeys, 0), id_o = idesc_f16(128, D, 1);
+        // (the low parts first: a sum is cut while it is small)
         auto scores = [&](int i, int tile, int slot) {
-            const uint32_t kt = sk + (i % C::kStages) * C::kKv;
+            const uint32_t kt = desc_k(sk + (i % C::kStages) * C::kKv), qt = desc_k(sq + tile * kParts * C::kQ);
 #pragma unroll
-            for (int x = 0; x < kParts; ++x)
+            for (int x = kParts - 1; x >= 0; --x)
 #pragma unroll
                 for (int kk = 0; kk < D / 16; ++kk)
-                    mma_bf16(tmem + slot * C::kS, sw128_desc(sq + (tile * kParts + x) * C::kQ + (kk >> 2) * 16384 + (kk & 3) * 32, 16, 1024),
-                             sw128_desc(kt + (kk >> 2) * (C::kKeys * 128) + (kk & 3) * 32, 16, 1024), id_s, x + kk > 0);
+                    mma_ss(tmem + slot * C::kS, qt + ((x * C::kQ + (kk >> 2) * 16384 + (kk & 3) * 32) >> 4),
+                           kt + (((kk >> 2) * (C::kKeys * 128) + (kk & 3) * 32) >> 4), id_s, x < kParts - 1 || kk > 0);
             mma_commit(bar(S_FULL + slot));
         };
         auto outputs = [&](int i, int tile, int slot) {
-            const uint32_t vt = sv + (i % C::kStages) * C::kKv;
+            const uint32_t vt = desc_mn(sv + (i % C::kStages) * C::kKv, C::kKeys * 128);
+            const bool add = (kParts == 2 ? i % kFlush : i) > 0;
 #pragma unroll
-            for (int x = 0; x < kParts; ++x)
+            for (int x = kParts - 1; x >= 0; --x)
 #pragma unroll
                 for (int kk = 0; kk < C::kKeys / 16; ++kk)
-                    mma_bf16_ta(tmem + C::kO + tile * D, (x == 0 ? tmem + slot * C::kS : tmem + C::kLow + slot * C::kLowStep) + 8 * kk,
-                                sw128_desc(vt + kk * 2048, C::kKeys * 128, 1024), id_o, i + x + kk > 0);
+                    mma_ts(tmem + C::kO + tile * D, (x == 0 ? tmem + slot * C::kS : tmem + C::kLow + slot * C::kLowStep) + 8 * kk,
+                           vt + ((kk * 2048) >> 4), id_o, add || x < kParts - 1 || kk > 0);
         };
         auto turn = [&](int i) { return (uint32_t)(i / C::kStages) & 1u; };
         auto wait = [&](int b, uint32_t parity) {
@@ -696,11 +804,11 @@ template <int D> size_t tc_bytes_d(const Attn &a, int dtype) {
     return most;
 }
 
-template <typename T, int D, int kParts, bool kShaped> int launch_tc_kernel(const Attn &a, int code, void *ws, cudaStream_t s) {
+template <typename T, int D, int kParts, int kMode> int launch_tc_kernel(const Attn &a, int code, void *ws, cudaStream_t s) {
     using C = TcConfig<D, kParts>;
     TcPlan plan = tc_plan<D, kParts>(a, a.cu != nullptr);
     plan.parts = (char *)ws;
-    const auto kernel = attn_tc_kernel<T, D, kParts, kShaped>;
+    const auto kernel = attn_tc_kernel<T, D, kParts, kMode>;
     if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem) != cudaSuccess) return GDR_ERR_CUDA;
     kernel<<<dim3((unsigned)plan.tiles, (unsigned)a.kv_heads, (unsigned)plan.splits), kTcThreads, C::kSmem, s>>>(a, plan, code);
     if (cudaGetLastError() != cudaSuccess) return GDR_ERR_CUDA;
@@ -710,10 +818,14 @@ template <typename T, int D, int kParts, bool kShaped> int launch_tc_kernel(cons
 }
 
 template <int D> int launch_tc_d(const Attn &a, int code, int dtype, void *ws, cudaStream_t s) {
-    const bool shaped = a.softcap > 0.f || a.slopes;
+    const int mode = a.slopes ? kBiased : a.softcap > 0.f ? kCapped : kPlain;
     if (dtype == GDR_F32)
-        return shaped ? launch_tc_kernel<float, D, 2, true>(a, code, ws, s) : launch_tc_kernel<float, D, 2, false>(a, code, ws, s);
-    return shaped ? launch_tc_kernel<__nv_bfloat16, D, 1, true>(a, code, ws, s) : launch_tc_kernel<__nv_bfloat16, D, 1, false>(a, code, ws, s);
+        return mode == kPlain    ? launch_tc_kernel<float, D, 2, kPlain>(a, code, ws, s)
+               : mode == kCapped ? launch_tc_kernel<float, D, 2, kCapped>(a, code, ws, s)
+                                 : launch_tc_kernel<float, D, 2, kBiased>(a, code, ws, s);
+    return mode == kPlain    ? launch_tc_kernel<__nv_bfloat16, D, 1, kPlain>(a, code, ws, s)
+           : mode == kCapped ? launch_tc_kernel<__nv_bfloat16, D, 1, kCapped>(a, code, ws, s)
+                             : launch_tc_kernel<__nv_bfloat16, D, 1, kBiased>(a, code, ws, s);
 }
 
 }  // namespace cattn

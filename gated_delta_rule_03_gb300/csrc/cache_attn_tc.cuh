@@ -11,9 +11,10 @@
 // Loads of codes go to registers a tile ahead, as they have to pass through them.
 //
 // Roles (416 threads): kTiles groups of 128 threads for the softmax, a row to a thread; the rest of
-// 384 convert; one thread of the last warp issues the products. With two row tiles one's softmax runs
-// under the other's products; with one (wide heads, fp32) the scores have two buffers and the next
-// tile's product runs under the softmax.
+// 384 convert; one thread of the last warp issues the products. Scores have two buffers, so that the next
+// tile's are there when a tile's weights are done. A block stays and goes from item to item: the next
+// item's queries and first keys are on their way while the outputs of the last leave. (A block for each
+// item took 32 thousand cycles more per item, as much as six tiles of 128 keys.)
 //
 // fp32: queries and weights as two fp16 parts, hi + lo, whose products are added in the same TMEM sums.
 #pragma once
@@ -30,29 +31,34 @@ namespace cattn {
 using namespace sm100;
 
 constexpr int kTcThreads = 416;
-constexpr int kRing = 4;   // tiles of scales
+constexpr int kRing = 8;   // tiles of scales
 constexpr int kFlush = 4;  // tiles whose outputs are added up in TMEM (fp32)
 
 template <int D, int kParts> struct TcConfig {
     static constexpr int kTiles = kParts == 1 && D <= 128 ? 2 : 1;
-    static constexpr int kKeys = kParts == 2 ? 64 : 128;
+    // Two row tiles leave TMEM for scores of 4 x 64 keys. (128 keys and one buffer for each: every softmax waits
+    // for its products, 376 us for 4 x 4096 tokens, 16 heads.)
+    static constexpr int kKeys = 64;
     static constexpr int kRows = 128 * kTiles;
     static constexpr int kSoft = 128 * kTiles;         // threads
     static constexpr int kConv = 384 - kSoft;
+    // Registers of a thread: 13 warps are launched with 128 each; what the converters give up the softmax
+    // gets (kSoft kSoftRegs + kConv kConvRegs = 384 x 128).
+    static constexpr int kConvRegs = 112, kSoftRegs = kTiles == 2 ? 136 : 160;
+    static_assert(kSoft * kSoftRegs + kConv * kConvRegs <= 384 * 128, "registers of the launch");
     static constexpr int kQ = 128 * D * 2;             // bytes of a part of a row tile
     static constexpr int kKv = kKeys * D * 2;          // of a tile of keys or values
-    static constexpr int kStages = D == 256 ? 1 : 2;
+    static constexpr int kStages = D == 256 ? (kParts == 2 ? 1 : 2) : 4;
     static constexpr int kSmem = kTiles * kParts * kQ + 2 * kStages * kKv + 1024;
-    // TMEM columns: scores of two slots (weights in their place), outputs, low parts of weights
-    static constexpr uint32_t kS = kKeys, kO = 256;
-    static constexpr uint32_t kLow = 128, kLowStep = kKeys / 2;
-    static_assert(kSmem <= 232448 - 1024, "shared memory");
-    static_assert(kO + kTiles * D <= 512 && 2 * kKeys + (kParts == 2 ? 2 * kLowStep : 0) <= kO, "TMEM");
+    // TMEM columns: scores of two slots per row tile (weights in their place), low parts of weights, outputs
+    static constexpr uint32_t kLow = 128, kLowStep = kKeys / 2, kO = 256;
+    static_assert(kSmem <= 232448 - 2048, "shared memory");
+    static_assert(kO + kTiles * D <= 512 && kTiles * 2 * kKeys + (kParts == 2 ? 2 * kLowStep : 0) <= kO, "TMEM");
 };
 
 struct TcPlan {
-    char *parts;   // fp32 outputs and sums of the splits: [item][split] TcPart
-    int tiles;     // row tiles that the grid has per head of the cache
+    char *parts;   // fp32 outputs and sums of the splits: [tile][head][split] TcPart
+    int64_t tiles; // row tiles, empty ones among them, for each head of the cache
     int splits;    // of each item's keys
 };
 template <int kRows, int D> struct TcPart {
@@ -88,57 +94,59 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint3
         : "memory");
 }
 
-// Where a block's rows are: request n, its rows from row0 on.
+// Row tiles are numbered request by request; packed ones from floor(first row / kRows) + n on, a bound that needs
+// no sum over the requests and leaves a tile empty here and there.
+template <int kRows> __device__ __forceinline__ int64_t first_tile(const Attn &a, int64_t n) {
+    if (!a.cu) return n * ((a.max_q * a.group + kRows - 1) / kRows);
+    return (int64_t)__ldg(a.cu + n) * a.group / kRows + n;
+}
+
 struct TcItem {
-    int n, row0, first, len, nq;  // first: the request's first token; nq: its new tokens
+    int n, first, len, past;   // request: its first row of q, tokens in the cache, those before the new ones
+    int row0, rows;            // of the tile
+    int head, j0, count;       // head of the cache; tiles of keys
+    int64_t part;
 };
 
-// Finds tile `x` (the last ones first: they see the most keys). Every thread of the block; false if there
-// is no such tile, *ok whether the lengths hold.
-template <int kRows> __device__ inline bool find_tile(const Attn &a, int64_t x, int64_t *sums, TcItem *found, bool *ok) {
-    const int tid = threadIdx.x;
-    auto tiles = [&](int64_t n) { return ((int64_t)rows_of(a, n).y * a.group + kRows - 1) / kRows; };
-    bool good = true;
-    int64_t mine = 0;
-    for (int64_t n = tid; n < a.num_seqs; n += kTcThreads) {
-        if (lengths_hold(a, n)) mine += tiles(n);
-        else good = false;
-    }
-    *ok = __syncthreads_and(good);
-    if (!*ok) return false;
-    if (!a.cu) {  // equal lengths: the last tiles of all requests first
-        const int64_t each = tiles(0);
-        if (x >= each * a.num_seqs) return false;
-        if (tid == 0) {
-            found->n = (int)(x % a.num_seqs);
-            found->row0 = (int)((each - 1 - x / a.num_seqs) * kRows);
-        }
+// Item k of this block, false behind the last. Those that see the most keys come first, and the blocks take
+// them to and fro. An empty one has rows = 0.
+template <int kRows, int kKeys> __device__ __forceinline__ bool get_item(const Attn &a, const TcPlan &plan, int64_t k, TcItem &t) {
+    const int64_t each = (int64_t)a.kv_heads * plan.splits;
+    const int64_t idx = k * gridDim.x + (k & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+    if (idx >= plan.tiles * each) return false;
+    const int64_t y = idx / each;
+    const int rest = (int)(idx - y * each), split = rest / a.kv_heads;
+    t.head = rest - split * a.kv_heads;
+    int64_t x, tile;
+    if (!a.cu) {
+        const int64_t per = plan.tiles / a.num_seqs;
+        t.n = (int)(y % a.num_seqs);
+        tile = per - 1 - y / a.num_seqs;
+        x = t.n * per + tile;
     } else {
-        int64_t total;
-        block_sums<kTcThreads>(mine, sums, &total);
-        if (x >= total) return false;
-        const int64_t want = total - 1 - x;
-        int64_t carry = 0;
-        for (int64_t n0 = 0; n0 < a.num_seqs; n0 += kTcThreads) {
-            const int64_t n = n0 + tid, w = n < a.num_seqs ? tiles(n) : 0;
-            int64_t all;
-            const int64_t end = carry + block_sums<kTcThreads>(w, sums, &all);
-            if (want >= end - w && want < end) {
-                found->n = (int)n;
-                found->row0 = (int)((want - (end - w)) * kRows);
-            }
-            carry += all;
-            if (carry > want) break;
+        x = plan.tiles - 1 - y;
+        int64_t lo = 0, hi = a.num_seqs - 1;  // the last request whose tiles begin at x or before
+        while (lo < hi) {
+            const int64_t mid = (lo + hi + 1) / 2;
+            if (first_tile<kRows>(a, mid) <= x) lo = mid;
+            else hi = mid - 1;
         }
+        t.n = (int)lo;
+        tile = x - first_tile<kRows>(a, lo);
     }
-    __syncthreads();
-    if (tid == 0) {
-        const int2 r = rows_of(a, found->n);
-        found->first = r.x;
-        found->nq = r.y;
-        found->len = __ldg(a.kv_lens + found->n);
-    }
-    __syncthreads();
+    const int2 r = rows_of(a, t.n);
+    t.first = r.x;
+    t.len = __ldg(a.kv_lens + t.n);
+    t.past = t.len - r.y;
+    const int64_t left = (int64_t)r.y * a.group - tile * kRows;
+    t.row0 = (int)(tile * kRows);
+    t.rows = left <= 0 ? 0 : (int)(left < kRows ? left : kRows);
+    // keys that the last row sees, and this split's tiles of them
+    const int far = a.causal ? max(0, min(t.len, t.past + (t.row0 + t.rows - 1) / a.group + 1)) : t.len;
+    const int all = t.rows ? (far + kKeys - 1) / kKeys : 0, per = (all + plan.splits - 1) / plan.splits;
+    t.j0 = min(all, split * per);
+    t.count = min(all, t.j0 + per) - t.j0;
+    t.part = (x * a.kv_heads + t.head) * plan.splits + split;
     return true;
 }
 
@@ -168,6 +176,11 @@ __device__ __forceinline__ void tmem_put16(uint32_t taddr, const uint32_t *r) {
         "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
         "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
         : "memory");
+}
+__device__ __forceinline__ void tmem_put8(uint32_t taddr, const uint32_t (&r)[8]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "r"(r[0]), "r"(r[1]),
+                 "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                 : "memory");
 }
 __device__ __forceinline__ void tmem_stored() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
@@ -227,39 +240,32 @@ __device__ __forceinline__ void store16(uint32_t saddr, uint32_t x, uint32_t y, 
     asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(saddr), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
 }
 
-template <typename T, int D, int kParts, int kMode>
-__global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_constant__ Attn a, const TcPlan plan, const int code) {
+__device__ __forceinline__ bool elect() {
+    uint32_t one;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(one));
+    return one != 0;
+}
+template <int kRegs> __device__ __forceinline__ void set_registers_up() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs)); }
+template <int kRegs> __device__ __forceinline__ void set_registers_down() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs)); }
+
+template <typename T, int D, int kParts, int kMode, int kCode>
+__global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_constant__ Attn a, const __grid_constant__ TcPlan plan) {
     using C = TcConfig<D, kParts>;
     extern __shared__ unsigned char sm[];
     const uint32_t base = (smem_u32(sm) + 1023u) & ~1023u;
     const uint32_t sq = base, sk = base + C::kTiles * kParts * C::kQ, sv = sk + C::kStages * C::kKv;
-    __shared__ int64_t sums[kTcThreads / 32];
-    __shared__ TcItem item;
-    __shared__ float4 scales[kRing][8];  // of 16 keys: score factor, log2 and reciprocal of the value scale
+    __shared__ float4 scales[kRing][8];  // of 16 keys: key scale, log2 and reciprocal of the value scale
     __shared__ uint32_t tmem_slot;
     __shared__ int gave_up;
-    enum { K_FULL = 0, K_FREE = 2, V_FULL = 4, V_FREE = 6, S_FULL = 8, W_FULL = 10, O_DONE = 12, O_LAST = 14, BARS = 15 };
+    // Of the stages of keys and values; of the scores' slots (2 tile + parity of the key tile); per row tile; one
+    enum { K_FULL = 0, K_FREE = 4, V_FULL = 8, V_FREE = 12, S_FULL = 16, W_FULL = 20, O_DONE = 24, Q_FULL = 28, O_FREE = 30, O_LAST = 32, BARS = 33 };
     __shared__ __align__(8) uint64_t bars[BARS];
     auto bar = [&](int i) { return smem_u32(&bars[i]); };
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
-    bool ok;
-    const int split = blockIdx.z, head = blockIdx.y;
-    const bool mine = find_tile<C::kRows>(a, blockIdx.x, sums, &item, &ok);
-    if (tid == 0 && blockIdx.x == 0 && head == 0 && split == 0) *a.status = ok ? GDR_OK : GDR_ERR_BAD_SEQLENS;
-    if (!mine) return;
-
-    const int n = item.n, row0 = item.row0, len = item.len, past = len - item.nq;
-    const int nrows = min(C::kRows, (int)min((int64_t)item.nq * a.group - row0, (int64_t)C::kRows));
-    // keys that the last row sees, and this split's tiles of them
-    const int far = a.causal ? max(0, min(len, past + (row0 + nrows - 1) / a.group + 1)) : len;
-    const int all_tiles = (far + C::kKeys - 1) / C::kKeys;
-    const int each = (all_tiles + plan.splits - 1) / plan.splits;
-    const int j0 = min(all_tiles, split * each), j1 = min(all_tiles, j0 + each), count = j1 - j0;
-
     if (tid == 0) {
         gave_up = 0;
-        for (int s = 0; s < 2; ++s) {
+        for (int s = 0; s < 4; ++s) {
             mbar_init(bar(K_FULL + s), C::kConv);
             mbar_init(bar(V_FULL + s), C::kConv);
             mbar_init(bar(K_FREE + s), 1);
@@ -268,218 +274,315 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_con
             mbar_init(bar(W_FULL + s), 128);
             mbar_init(bar(O_DONE + s), 1);
         }
+        for (int s = 0; s < 2; ++s) {
+            mbar_init(bar(Q_FULL + s), 128);
+            mbar_init(bar(O_FREE + s), 128);
+        }
         mbar_init(bar(O_LAST), 1);
         fence_mbar_init();
     }
+    bool good = true;
+    for (int64_t n = tid; n < a.num_seqs; n += kTcThreads) good = good && lengths_hold(a, n);
+    const bool ok = __syncthreads_and(good);
+    if (tid == 0 && blockIdx.x == 0) *a.status = ok ? GDR_OK : GDR_ERR_BAD_SEQLENS;
+    if (!ok) return;
     if (warp == 12) {
         tmem_alloc(smem_u32(&tmem_slot), 512);
         tmem_relinquish();
-    }
-    float row_up = 1.f;
-    if (warp < C::kSoft / 32) {
-        // ---- queries: this thread's row in fp16 with a power of two, its sign that of the scale
-        const int r = tid, at = row0 + r;
-        const uint32_t to = sq + (r >> 7) * kParts * C::kQ;
-        const bool live = r < nrows;
-        const T *src = live ? (const T *)a.q + (int64_t)(item.first + at / a.group) * a.qs + (int64_t)(head * a.group + at % a.group) * D : nullptr;
-        // 256 bytes of the row at a time in registers, all of them under way together; longer rows come twice
-        constexpr int kPiece = 256 / sizeof(T), kPieces = (D + kPiece - 1) / kPiece, kVecs = (D < kPiece ? D : kPiece) * sizeof(T) / 16;
-        constexpr int kVec = 16 / sizeof(T);
-        uint4 w[kVecs];
-        auto fetch = [&](int piece) {
-#pragma unroll
-            for (int i = 0; i < kVecs; ++i) w[i] = live ? ld_nc(src + piece * kPiece + i * kVec) : make_uint4(0, 0, 0, 0);
-        };
-        uint32_t most = 0;
-#pragma unroll 1
-        for (int piece = kPieces - 1; piece >= 0; --piece) {
-            fetch(piece);
-#pragma unroll
-            for (int i = 0; i < kVecs; ++i) {
-                const T *e = (const T *)&w[i];
-#pragma unroll
-                for (int x = 0; x < kVec; ++x) most = max(most, __float_as_uint(to_f32<T>(e[x])) & 0x7fffffffu);
-            }
-        }
-        const int shift = row_shift(most);
-        const float up = a.scale < 0.f ? -two_to(shift) : two_to(shift);
-        row_up = two_to(-shift) * fabsf(a.scale);
-#pragma unroll 1
-        for (int piece = 0; piece < kPieces; ++piece) {
-            if (piece > 0) fetch(piece);
-#pragma unroll
-            for (int c = 0; c < kVecs * kVec; c += 8) {
-                uint32_t hi[4], lo[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int e = c + 2 * i;
-                    const float x = to_f32<T>(((const T *)&w[e / kVec])[e % kVec]) * up, y = to_f32<T>(((const T *)&w[(e + 1) / kVec])[(e + 1) % kVec]) * up;
-                    hi[i] = f16_pair(x, y);
-                    const float2 f = f16_values(hi[i]);
-                    lo[i] = f16_pair(x - f.x, y - f.y);
-                }
-                const int d = piece * kPiece + c;
-                const uint32_t dst = to + (d >> 6) * 16384 + sw128_offset(r & 127, d & 63);
-                store16(dst, hi[0], hi[1], hi[2], hi[3]);
-                if (kParts == 2) store16(dst + C::kQ, lo[0], lo[1], lo[2], lo[3]);
-            }
-        }
-        fence_async_smem();
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = tmem_slot;
     bool fine = true;
+    TcItem item;
+    int64_t turn = 0;  // items of this block that have been looked at
+    int gi0 = 0;       // tiles of keys before this item
 
     if (warp < C::kSoft / 32) {
         // ---------------------------------------------------------------- softmax
+        set_registers_up<C::kSoftRegs>();
         const int tile = warp >> 2;  // row tile
         const uint32_t lanes = (uint32_t)(warp & 3) << 21;
-        const int at = row0 + tid;
-        const int p = past + at / a.group, lim = a.causal ? min(len, p + 1) : len;
-        const int sure = a.causal ? min(len, past + (row0 + tile * 128) / a.group + 1) : len;
         const uint32_t out = tmem + lanes + C::kO + tile * D;
-        const bool live = tid < nrows;
-        const int64_t row = (int64_t)(item.first + at / a.group) * a.heads + head * a.group + at % a.group;
-        TcPart<C::kRows, D> *const part = (TcPart<C::kRows, D> *)plan.parts + (((int64_t)head * plan.tiles + blockIdx.x) * plan.splits + split);
-        float *const row_out = plan.splits > 1 ? part->o[tid] : (float *)a.o + row * D;  // (fp32 only without splits)
-        const float slope = kMode == kBiased && a.slopes && live ? __ldg(a.slopes + head * a.group + at % a.group) : 0.f;
         const float cap = kMode == kPlain ? 0.f : a.softcap, inv_cap = cap > 0.f ? 1.f / cap : 0.f;
-        const float up2 = row_up * (kMode == kPlain ? kLog2e : 1.f);
-        float ref = 0.f, l = 0.f;
-        float sum_ref = 0.f, sum_l = 0.f;  // kParts == 2: of what has left TMEM
-
-        // The tensor cores cut the sums in TMEM instead of rounding them, some 2^-24 of them per step and always
-        // towards zero: fp32 results take the outputs of kFlush tiles at a time out and add them up in memory.
-        auto flush = [&] {
-            const bool some = sum_l != 0.f;
-            const float by = some ? ex2(sum_ref - ref) : 0.f;
-#pragma unroll 1
-            for (int c = 0; c < D; c += 32) {
-                float v[32];
-                tmem_load32(out + c, v);
-                if (!live) continue;
+        using P = TcPart<C::kRows, D>;
+        auto row_of = [&](const TcItem &t) {
+            const int at = t.row0 + tid;
+            return (int64_t)(t.first + at / a.group) * a.heads + t.head * a.group + at % a.group;
+        };
+        auto query_of = [&](const TcItem &t) {
+            const int at = t.row0 + tid;
+            return (const T *)a.q + (int64_t)(t.first + at / a.group) * a.qs + (int64_t)(t.head * a.group + at % a.group) * D;
+        };
+        // The next item that has keys to look at; those before it that have none get their zeros.
+        auto next_item = [&](TcItem &t) {
+            while (get_item<C::kRows, C::kKeys>(a, plan, turn, t)) {
+                ++turn;
+                if (t.count) return true;
+                if (tid >= t.rows) continue;
+                P *const part = (P *)plan.parts + t.part;
+                const int64_t row = row_of(t);
+                if (plan.splits > 1) part->lse2[tid] = -INFINITY;
+                else if (a.lse) a.lse[row] = -INFINITY;
+                uint4 *const to = plan.splits > 1 ? (uint4 *)part->o[tid] : (uint4 *)((T *)a.o + row * D);
+                const int vecs = (plan.splits > 1 ? 4 : (int)sizeof(T)) * D / 16;
+                for (int e = 0; e < vecs; ++e) to[e] = make_uint4(0, 0, 0, 0);
+            }
+            return false;
+        };
+        // This thread's row of queries in fp16 with a power of two, its sign that of the scale; returns what
+        // products with it are to be multiplied by. 256 bytes of the row are under way together; longer rows come
+        // twice, the second time from near by.
+        auto put_queries = [&](const TcItem &t) {
+            const bool live = tid < t.rows;
+            const T *const src = query_of(t);
+            const uint32_t to = sq + tile * kParts * C::kQ;
+            constexpr int kVec = 16 / sizeof(T), kPiece = 256 / sizeof(T) < D ? 256 / sizeof(T) : D, kPieces = D / kPiece, kVecs = kPiece / kVec;
+            uint4 w[kVecs];
+            auto fetch = [&](int piece) {
 #pragma unroll
-                for (int e = 0; e < 32; e += 4) {
-                    float4 o = some ? *(const float4 *)(row_out + c + e) : make_float4(0.f, 0.f, 0.f, 0.f);
-                    o = make_float4(fmaf(o.x, by, v[e]), fmaf(o.y, by, v[e + 1]), fmaf(o.z, by, v[e + 2]), fmaf(o.w, by, v[e + 3]));
-                    *(float4 *)(row_out + c + e) = o;
+                for (int i = 0; i < kVecs; ++i) w[i] = live ? ld_nc(src + piece * kPiece + i * kVec) : make_uint4(0, 0, 0, 0);
+            };
+            uint32_t most = 0;
+#pragma unroll 1
+            for (int piece = kPieces - 1; piece >= 0; --piece) {
+                fetch(piece);
+#pragma unroll
+                for (int i = 0; i < kVecs; ++i) {
+                    if constexpr (sizeof(T) == 2) {
+                        most = __vmaxu2(most, __vmaxu2(__vmaxu2(w[i].x & 0x7fff7fffu, w[i].y & 0x7fff7fffu), __vmaxu2(w[i].z & 0x7fff7fffu, w[i].w & 0x7fff7fffu)));
+                    } else {
+                        most = max(most, max(max(w[i].x & 0x7fffffffu, w[i].y & 0x7fffffffu), max(w[i].z & 0x7fffffffu, w[i].w & 0x7fffffffu)));
+                    }
                 }
             }
-            sum_l = fmaf(sum_l, by, l);
-            sum_ref = ref;
-            l = 0.f;
+            if (sizeof(T) == 2) most = max(most & 0xffffu, most >> 16) << 16;
+            const int shift = row_shift(most);
+            const float up = a.scale < 0.f ? -two_to(shift) : two_to(shift);
+            const float2 up_pair = make_float2(up, up);
+            auto pair_of = [&](int e) {  // entries e and e + 1 of the piece
+                const uint4 &q = w[e / kVec];
+                const uint32_t word = (e / (kVec / 4)) % 4 == 0 ? q.x : (e / (kVec / 4)) % 4 == 1 ? q.y : (e / (kVec / 4)) % 4 == 2 ? q.z : q.w;
+                if constexpr (sizeof(T) == 2) return make_float2(__uint_as_float(word << 16), __uint_as_float(word & 0xffff0000u));
+                return make_float2(__uint_as_float(word), __uint_as_float(e % 4 == 0 ? q.y : q.w));
+            };
+#pragma unroll 1
+            for (int piece = 0; piece < kPieces; ++piece) {
+                if (kPieces > 1) fetch(piece);
+#pragma unroll
+                for (int c = 0; c < kPiece; c += 8) {
+                    uint32_t hi[4], lo[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float2 z = mul2(pair_of(c + 2 * i), up_pair);
+                        hi[i] = f16_pair(z.x, z.y);
+                        if (kParts == 2) {
+                            const float2 f = f16_values(hi[i]);
+                            lo[i] = f16_pair(z.x - f.x, z.y - f.y);
+                        }
+                    }
+                    const int d = piece * kPiece + c;
+                    const uint32_t dst = to + (d >> 6) * 16384 + sw128_offset(tid & 127, d & 63);
+                    store16(dst, hi[0], hi[1], hi[2], hi[3]);
+                    if (kParts == 2) store16(dst + C::kQ, lo[0], lo[1], lo[2], lo[3]);
+                }
+            }
+            fence_async_smem();
+            mbar_arrive(bar(Q_FULL + tile));
+            return two_to(-shift) * fabsf(a.scale);
         };
 
-        for (int i = 0; i < count && fine; ++i) {
-            const int slot = C::kTiles == 2 ? tile : i & 1, use = C::kTiles == 2 ? i : i >> 1;
-            const uint32_t s_at = tmem + lanes + slot * C::kS;
-            if (!mbar_wait(bar(S_FULL + slot), use & 1)) {
-                fine = false;
-                break;
-            }
-            // The outputs of the tiles before. With two row tiles the scores' barrier says that they are there; with
-            // one it does so of the last but one tile, and the last has a barrier that even and odd tiles share in turn.
-            auto outputs_done = [&] {
-                if (C::kTiles == 1 && !mbar_wait(bar(O_DONE + ((i - 1) & 1)), ((i - 1) >> 1) & 1)) fine = false;
+        bool have = next_item(item);
+        float row_up = have ? put_queries(item) : 0.f;
+        for (int done = 0; have && fine; ++done) {
+            const int at = item.row0 + tid;
+            const int p = item.past + at / a.group, lim = a.causal ? min(item.len, p + 1) : item.len;
+            const int sure = a.causal ? min(item.len, item.past + (item.row0 + tile * 128) / a.group + 1) : item.len;
+            const bool live = tid < item.rows;
+            const int64_t row = row_of(item);
+            P *const part = (P *)plan.parts + item.part;
+            float *const row_out = plan.splits > 1 ? part->o[tid] : (float *)a.o + row * D;  // (fp32 only without splits)
+            const float slope = kMode == kBiased && a.slopes && live ? __ldg(a.slopes + item.head * a.group + at % a.group) : 0.f;
+            const float up2 = row_up * (kMode == kPlain ? kLog2e : 1.f);
+            float ref = 0.f, l = 0.f;
+            float sum_ref = 0.f, sum_l = 0.f;  // kParts == 2: of what has left TMEM
+            const int count = item.count, j0 = item.j0;
+            TcItem then;
+            have = next_item(then);
+            if (have && tid < then.rows)
+                for (int e = 0; e < D * (int)sizeof(T); e += 128) asm volatile("prefetch.global.L2 [%0];" ::"l"((const char *)query_of(then) + e));
+
+            // The tensor cores cut the sums in TMEM instead of rounding them, some 2^-24 of them per step and always
+            // towards zero: fp32 results take the outputs of kFlush tiles at a time out and add them up in memory.
+            auto flush = [&] {
+                const bool some = sum_l != 0.f;
+                const float by = some ? ex2(sum_ref - ref) : 0.f;
+#pragma unroll 1
+                for (int c = 0; c < D; c += 32) {
+                    float v[32];
+                    tmem_load32(out + c, v);
+                    if (!live) continue;
+#pragma unroll
+                    for (int e = 0; e < 32; e += 4) {
+                        float4 o = some ? *(const float4 *)(row_out + c + e) : make_float4(0.f, 0.f, 0.f, 0.f);
+                        o = make_float4(fmaf(o.x, by, v[e]), fmaf(o.y, by, v[e + 1]), fmaf(o.z, by, v[e + 2]), fmaf(o.w, by, v[e + 3]));
+                        *(float4 *)(row_out + c + e) = o;
+                    }
+                }
+                sum_l = fmaf(sum_l, by, l);
+                sum_ref = ref;
+                l = 0.f;
+            };
+
+#pragma unroll 1
+            for (int i = 0; i < count && fine; ++i) {
+                const int gi = gi0 + i, slot = 2 * tile + (gi & 1);
+                const uint32_t s_at = tmem + lanes + slot * C::kKeys;
+                if (!mbar_wait(bar(S_FULL + slot), (gi >> 1) & 1)) {
+                    fine = false;
+                    break;
+                }
+                // The outputs of the tiles before: the scores' barrier says that those of the last but one are there,
+                // and those of the last have a barrier that even and odd tiles share in turn.
+                auto outputs_done = [&] {
+                    if (!mbar_wait(bar(O_DONE + 2 * tile + ((gi - 1) & 1)), ((gi - 1) >> 1) & 1)) fine = false;
+                    __syncwarp();
+                    tc_fence_after();
+                };
                 __syncwarp();
                 tc_fence_after();
-            };
-            __syncwarp();
-            tc_fence_after();
-            const bool anew = kParts == 2 && i % kFlush == 0;  // (this tile's product begins the outputs)
-            if (anew && i > 0) {
-                outputs_done();
-                if (!__all_sync(~0u, fine)) break;
-                flush();
-            }
-            const int tok = (j0 + i) * C::kKeys;
-            const float4 *const sc = scales[(j0 + i) % kRing];
-            const bool edge = tok + C::kKeys > sure;
+                const bool anew = kParts == 2 && i % kFlush == 0;  // (this tile's product begins the outputs)
+                if (anew && i > 0) {
+                    outputs_done();
+                    if (!__all_sync(~0u, fine)) break;
+                    flush();
+                }
+                const int tok = (j0 + i) * C::kKeys;
+                const float4 *const sc = scales[gi % kRing];
+                const bool edge = tok + C::kKeys > sure;
 
-            // Weights with the row's reference as it is, 16 keys at a time, and the largest exponent. The first tile
-            // (a row that sees none of its keys sees no later ones), or an exponent that is too large, moves the
-            // reference, and the outputs so far with it; then the weights are taken again.
-            uint32_t hi[C::kKeys / 2], lo[kParts == 2 ? C::kKeys / 2 : 1];
-            float sum = 0.f, top = -INFINITY;
-            auto weigh = [&](auto at_edge) {
-                constexpr bool kEdge = decltype(at_edge)::value;
-                float2 all = make_float2(0.f, 0.f);
-                top = -INFINITY;
-                uint32_t x[2][16];
-                tmem_fetch16(s_at, x[0]);
-#pragma unroll
-                for (int g = 0; g < C::kKeys / 16; ++g) {
-                    uint32_t(&y)[16] = x[g & 1];
-                    tmem_arrive16(y);
-                    if (g + 1 < C::kKeys / 16) tmem_fetch16(s_at + 16 * (g + 1), x[(g + 1) & 1]);
+                // Weights with the row's reference as it is, 16 keys at a time, kept in registers until it is known that
+                // none is too large. Else, and for the first tile and those that some row sees in part, slowly: the
+                // largest exponent first, the reference moved with the outputs so far, then the weights. (A row that
+                // sees no key of the first tile sees no later ones.)
+                auto shape_of = [&](int g) {
                     const float4 f = sc[g];
-                    const Shape<kMode, kParts == 2> shape(f.x * up2, f.y - ref, cap, inv_cap, slope, (float)(p - tok - 16 * g));
-                    float2 some = make_float2(0.f, 0.f);
+                    return Shape<kMode, kParts == 2>(f.x * up2, f.y - ref, cap, inv_cap, slope, (float)(p - tok - 16 * g));
+                };
+                bool slow = i == 0 || edge;
+                if (!slow) {
+                    uint32_t hi[C::kKeys / 2], lo[kParts == 2 ? C::kKeys / 2 : 1];
+                    float2 all = make_float2(0.f, 0.f);
+                    float top = -INFINITY;
+                    uint32_t x[2][16];
+                    tmem_fetch16(s_at, x[0]);
 #pragma unroll
-                    for (int e = 0; e < 16; e += 2) {
-                        float2 w = shape(make_float2(__uint_as_float(y[e]), __uint_as_float(y[e + 1])), e);
-                        if (kEdge) {
+                    for (int g = 0; g < C::kKeys / 16; ++g) {
+                        uint32_t(&y)[16] = x[g & 1];
+                        tmem_arrive16(y);
+                        if (g + 1 < C::kKeys / 16) tmem_fetch16(s_at + 16 * (g + 1), x[(g + 1) & 1]);
+                        const auto shape = shape_of(g);
+                        float2 some = make_float2(0.f, 0.f);
+#pragma unroll
+                        for (int e = 0; e < 16; e += 2) {
+                            float2 w = shape(make_float2(__uint_as_float(y[e]), __uint_as_float(y[e + 1])), e);
+                            top = fmaxf(top, fmaxf(w.x, w.y));
+                            w.x = ex2(w.x);
+                            w.y = ex2(w.y);
+                            some = add2(some, w);
+                            const int q = 8 * g + e / 2;
+                            hi[q] = f16_pair(w.x, w.y);
+                            if (kParts == 2) {
+                                const float2 v = f16_values(hi[q]);
+                                lo[q] = f16_pair(w.x - v.x, w.y - v.y);
+                            }
+                        }
+                        const float rv = sc[g].z;
+                        all = fma2(some, make_float2(rv, rv), all);
+                    }
+                    slow = __any_sync(~0u, top > kSpan + kSlack);
+                    if (!slow) {
+                        l += all.x + all.y;
+#pragma unroll
+                        for (int c = 0; c < C::kKeys / 2; c += 16) {
+                            tmem_put16(s_at + c, hi + c);
+                            if constexpr (kParts == 2) tmem_put16(tmem + lanes + C::kLow + (gi & 1) * C::kLowStep + c, lo + c);
+                        }
+                    }
+                }
+                if (slow) {
+                    float top = -INFINITY;
+                    auto exponents = [&](int g, float (&t)[16]) {
+                        uint32_t y[16];
+                        tmem_fetch16(s_at + 16 * g, y);
+                        tmem_arrive16(y);
+                        const auto shape = shape_of(g);
+#pragma unroll
+                        for (int e = 0; e < 16; e += 2) {
+                            const float2 w = shape(make_float2(__uint_as_float(y[e]), __uint_as_float(y[e + 1])), e);
                             const int j = tok + 16 * g + e;
-                            if (j >= lim) w.x = -INFINITY;
-                            if (j + 1 >= lim) w.y = -INFINITY;
+                            t[e] = j < lim ? w.x : -INFINITY;
+                            t[e + 1] = j + 1 < lim ? w.y : -INFINITY;
                         }
-                        top = fmaxf(top, fmaxf(w.x, w.y));
-                        w.x = ex2(w.x);
-                        w.y = ex2(w.y);
-                        some = add2(some, w);
-                        const int q = 8 * g + e / 2;
-                        hi[q] = f16_pair(w.x, w.y);
-                        if (kParts == 2) {
-                            const float2 v = f16_values(hi[q]);
-                            lo[q] = f16_pair(w.x - v.x, w.y - v.y);
-                        }
-                    }
-                    all = fma2(some, make_float2(f.z, f.z), all);
-                }
-                sum = all.x + all.y;
-            };
-            for (bool settled = false;; settled = true) {
-                if (edge) weigh(std::true_type{});
-                else weigh(std::false_type{});
-                if (settled || (i > 0 && !__any_sync(~0u, top > kSpan + kSlack))) break;
-                const bool move = i == 0 ? top > -INFINITY : top > kSpan + kSlack;
-                if (move) ref += top - kSpan;
-                if (i > 0) {
-                    const float by = move ? ex2(kSpan - top) : 1.f;
-                    l *= by;
-                    if (!anew) {
-                        outputs_done();
+                    };
 #pragma unroll 1
-                        for (int c = 0; c < D; c += 32) {
-                            float v[32];
-                            tmem_load32(out + c, v);
+                    for (int g = 0; g < C::kKeys / 16; ++g) {
+                        float t[16];
+                        exponents(g, t);
 #pragma unroll
-                            for (int e = 0; e < 32; ++e) v[e] *= by;
-                            tmem_store32(out + c, v);
+                        for (int e = 0; e < 16; ++e) top = fmaxf(top, t[e]);
+                    }
+                    const bool move = i == 0 ? top > -INFINITY : top > kSpan + kSlack;
+                    if (move) ref += top - kSpan;
+                    if (i > 0 && __any_sync(~0u, move)) {
+                        const float by = move ? ex2(kSpan - top) : 1.f;
+                        l *= by;
+                        if (!anew) {
+                            outputs_done();
+#pragma unroll 1
+                            for (int c = 0; c < D; c += 16) {
+                                float v[16];
+                                tmem_load16(out + c, v);
+                                uint32_t u[16];
+#pragma unroll
+                                for (int e = 0; e < 16; ++e) u[e] = __float_as_uint(v[e] * by);
+                                tmem_put16(out + c, u);
+                            }
                         }
                     }
-                }
-            }
-            l += sum;
+#pragma unroll 1
+                    for (int g = 0; g < C::kKeys / 16; ++g) {
+                        float t[16];
+                        uint32_t hi[8], lo[8];
+                        exponents(g, t);
+                        float some = 0.f;
 #pragma unroll
-            for (int c = 0; c < C::kKeys / 2; c += 16) {
-                tmem_put16(s_at + c, hi + c);
-                if constexpr (kParts == 2) tmem_put16(tmem + lanes + C::kLow + slot * C::kLowStep + c, lo + c);
+                        for (int e = 0; e < 16; e += 2) {
+                            const float w0 = ex2(t[e]), w1 = ex2(t[e + 1]);
+                            some += w0 + w1;
+                            hi[e / 2] = f16_pair(w0, w1);
+                            const float2 v = f16_values(hi[e / 2]);
+                            lo[e / 2] = f16_pair(w0 - v.x, w1 - v.y);
+                        }
+                        l = fmaf(some, sc[g].z, l);
+                        // (in the scores' place: columns 8g .. 8g + 7, which have been read)
+                        tmem_put8(s_at + 8 * g, hi);
+                        if (kParts == 2) tmem_put8(tmem + lanes + C::kLow + (gi & 1) * C::kLowStep + 8 * g, lo);
+                    }
+                }
+                tmem_stored();
+    tc_fence_before();
+                mbar_arrive(bar(W_FULL + slot));
             }
-            tmem_stored();
-            tc_fence_before();
-            mbar_arrive(bar(W_FULL + slot));
-        }
-        // ---- results
-        if (count > 0 && fine) {
-            fine = mbar_wait(bar(O_LAST), 0);
+            gi0 += count;
+            if (fine) fine = mbar_wait(bar(O_LAST), done & 1);
             __syncwarp();
             tc_fence_after();
-        }
-        // (a warp reads its lanes together, whichever rows are live)
-        if (__all_sync(~0u, fine)) {
+            // ---- the next item's queries (the products with the last ones are done), then the results. A warp reads its
+            // lanes together, whichever rows are live.
+            if (!__all_sync(~0u, fine)) break;
+            if (have) row_up = put_queries(then);
             const float by = kParts == 2 ? ex2(sum_ref - ref) : 0.f;
             const bool older = kParts == 2 && sum_l != 0.f;
             if (older) l = fmaf(sum_l, by, l);
@@ -493,12 +596,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_con
 #pragma unroll 1
             for (int c = 0; c < D; c += 32) {
                 float v[32];
-                if (count > 0) {
-                    tmem_load32(out + c, v);
-                } else {
-#pragma unroll
-                    for (int e = 0; e < 32; ++e) v[e] = 0.f;
-                }
+                tmem_load32(out + c, v);
                 if (!live) continue;
                 if (older) {
 #pragma unroll
@@ -529,9 +627,13 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_con
                     }
                 }
             }
+            tc_fence_before();
+            mbar_arrive(bar(O_FREE + tile));
+            item = then;
         }
     } else if (warp < 12) {
         // ---------------------------------------------------------------- codes to fp16
+        set_registers_down<C::kConvRegs>();
         const int ct = tid - C::kSoft, cw = ct >> 5;
         constexpr int kBlocks = D / 64;                     // 64 dims to a swizzled block of rows
         constexpr int kWarpRows = 8 / kBlocks;              // rows of a warp's pass of 512 bytes
@@ -540,160 +642,166 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_con
         // Eight lanes in turn write 16-byte chunks 2x of two rows, one even and one odd: no two in the same banks.
         const int x = lane & 3, blk = (lane >> 3) & (kBlocks - 1), row_lo = (lane >> 2) & 1;
         const int row = cw * kWarpRows + row_lo + 2 * (lane >> (3 + (kBlocks == 4 ? 2 : kBlocks == 2 ? 1 : 0)));
-        const int in_page = (1 << a.log_page) - 1, lane_off = (row & 15) * D + blk * 64 + x * 16;
-        // Lane g < 8 knows 16 keys of a tile: their page (-1 behind the last token, -2 outside the cache), and
-        // where their codes begin.
-        struct Keys {
-            int page;
-            int64_t at;
-        };
-        auto keys_of = [&](int i) {
-            const int tok = (j0 + i) * C::kKeys + (lane & 7) * 16;
-            if (i >= count || (lane & 7) * 16 >= C::kKeys || tok >= len) return Keys{-1, 0};
-            int pg = __ldg(a.table + (int64_t)n * a.width + (tok >> a.log_page));
-            if (pg < 0 || pg >= a.pages) pg = -2;
-            return Keys{pg, (((int64_t)pg * a.kv_heads + head) * (in_page + 1) + (tok & in_page)) * D};
-        };
-        auto load = [&](const uint8_t *cache, int i, const Keys &keys, uint4 (&v)[kPasses]) {
-            const bool full = (j0 + i + 1) * C::kKeys <= len && __all_sync(~0u, keys.page >= 0 || (lane & 7) * 16 >= C::kKeys);
+        const int in_page = (1 << a.log_page) - 1;
+        const uint32_t page_bytes = (uint32_t)(a.kv_heads * (in_page + 1)) * D;
+        const uint32_t chunk0 = (uint32_t)((2 * x) ^ (row & 7)) << 4;  // its first 16-byte chunk; the second is one bit away
+        const uint32_t to0 = blk * (C::kKeys * 128) + row * 128;
+        while (fine && get_item<C::kRows, C::kKeys>(a, plan, turn, item)) {
+            ++turn;
+            if (!item.count) continue;
+            const int count = item.count, j0 = item.j0, len = item.len;
+            const int64_t lane_at = (int64_t)item.head * (in_page + 1) * D + (row & 15) * D + blk * 64 + x * 16;
+            const uint8_t *const kc = a.kc + lane_at, *const vc = a.vc + lane_at;
+            const int32_t *const table = a.table + (int64_t)item.n * a.width;
+            // Lane g < 8 knows the page of 16 keys of a tile: -1 behind the last token, -2 outside the cache.
+            auto pages_of = [&](int i) {
+                const int tok = (j0 + i) * C::kKeys + (lane & 7) * 16;
+                if (i >= count || (lane & 7) * 16 >= C::kKeys || tok >= len) return -1;
+                const int pg = __ldg(table + (tok >> a.log_page));
+                return pg >= 0 && pg < a.pages ? pg : -2;
+            };
+            auto scales_of = [&](int pg) {
+                if (pg < 0) return make_float2(pg == -1 ? 1.f : __int_as_float(0x7fffffff), pg == -1 ? 1.f : __int_as_float(0x7fffffff));
+                const int64_t at = (int64_t)pg * a.kv_heads + item.head;
+                return make_float2(__ldg(a.ks + at), __ldg(a.vs + at));
+            };
+            // As soon as a pass is converted its registers are loaded again, for the same pass of the next tile.
+            int page_of_pass[kPasses];
+            bool full;
+            auto look_at = [&](int i, int pages) {
+                full = (j0 + i + 1) * C::kKeys <= len && __all_sync(~0u, pages >= 0 || (lane & 7) * 16 >= C::kKeys);
 #pragma unroll
-            for (int ps = 0; ps < kPasses; ++ps) {
-                const int g = (ps * kPass + cw * kWarpRows) >> 4;  // (a warp's rows of a pass lie in one of the 16s)
-                const uint8_t *const from = cache + (__shfl_sync(~0u, keys.at, g) + lane_off);
-                if (full) {
-                    v[ps] = ld_nc(from);
-                } else {
-                    const int pg = __shfl_sync(~0u, keys.page, g);
-                    v[ps] = make_uint4(0, 0, 0, 0);
-                    if (pg >= 0 && (j0 + i) * C::kKeys + ps * kPass + row < len) v[ps] = ld_nc(from);
+                for (int ps = 0; ps < kPasses; ++ps)  // (a warp's rows of a pass lie in one of the 16s)
+                    page_of_pass[ps] = __shfl_sync(~0u, pages, (ps * kPass + cw * kWarpRows) >> 4);
+            };
+            auto load = [&](const uint8_t *cache, int tok, int ps) {
+                const int pg = page_of_pass[ps], first = tok + ps * kPass + ((cw * kWarpRows) & ~15);
+                if (full || (pg >= 0 && tok + ps * kPass + row < len))
+                    return ld_nc(cache + (uint64_t)(uint32_t)pg * page_bytes + (first & in_page) * D);
+                return make_uint4(0, 0, 0, 0);
+            };
+            int next = pages_of(0);
+            uint4 k[kPasses], v[kPasses];
+            look_at(0, next);
+#pragma unroll
+            for (int ps = 0; ps < kPasses; ++ps) k[ps] = load(kc, j0 * C::kKeys, ps);
+#pragma unroll
+            for (int ps = 0; ps < kPasses; ++ps) v[ps] = load(vc, j0 * C::kKeys, ps);
+            float2 scale = scales_of(next);
+            next = pages_of(1);
+#pragma unroll 1
+            for (int i = 0; i < count; ++i) {
+                const int gi = gi0 + i, st = gi % C::kStages, free = ((gi / C::kStages) & 1) ^ 1;
+                const int tok = (j0 + i + 1) * C::kKeys;  // of the next tile
+                const bool more = i + 1 < count;
+                if (cw == 0 && lane < C::kKeys / 16)
+                    scales[gi % kRing][lane] = make_float4(scale.x, lg2(scale.y), scale.y == scale.y ? __fdividef(1.f, scale.y) : 1.f, 0.f);
+                look_at(i + 1, next);
+                if (cw == 0) scale = scales_of(next);
+                next = pages_of(i + 2);
+                auto convert = [&](uint32_t to, uint4 (&w)[kPasses], const uint8_t *cache) {
+#pragma unroll
+                    for (int ps = 0; ps < kPasses; ++ps) {
+                        uint32_t f[8];
+                        codes::to_f16x4<kCode>(w[ps].x, f[0], f[1]);
+                        codes::to_f16x4<kCode>(w[ps].y, f[2], f[3]);
+                        codes::to_f16x4<kCode>(w[ps].z, f[4], f[5]);
+                        codes::to_f16x4<kCode>(w[ps].w, f[6], f[7]);
+                        // (kPass is a multiple of 8: a thread's rows have one place in the swizzle)
+                        store16(to + ps * kPass * 128 + chunk0, f[0], f[1], f[2], f[3]);
+                        store16(to + ps * kPass * 128 + (chunk0 ^ 16), f[4], f[5], f[6], f[7]);
+                        if (more) w[ps] = load(cache, tok, ps);
+                    }
+                    fence_async_smem();
+                };
+                if (!mbar_wait(bar(K_FREE + st), free)) {
+                    fine = false;
+                    break;
                 }
-            }
-        };
-        auto put = [&](uint32_t to, const uint4 (&v)[kPasses]) {
-#pragma unroll
-            for (int ps = 0; ps < kPasses; ++ps) {
-                const int r = ps * kPass + row;
-                const uint32_t w[4] = {v[ps].x, v[ps].y, v[ps].z, v[ps].w};
-                uint32_t h[8];
-                if (code == GDR_CODE_E4M3) {
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) codes::to_f16x4<GDR_CODE_E4M3>(w[e], h[2 * e], h[2 * e + 1]);
-                } else {
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) codes::to_f16x4<GDR_CODE_INT8>(w[e], h[2 * e], h[2 * e + 1]);
+                convert(sk + st * C::kKv + to0, k, kc);
+                mbar_arrive(bar(K_FULL + st));
+                if (!mbar_wait(bar(V_FREE + st), free)) {
+                    fine = false;
+                    break;
                 }
-                const uint32_t at = to + blk * (C::kKeys * 128) + r * 128;
-                store16(at + (((2 * x) ^ (r & 7)) << 4), h[0], h[1], h[2], h[3]);
-                store16(at + (((2 * x + 1) ^ (r & 7)) << 4), h[4], h[5], h[6], h[7]);
+                convert(sv + st * C::kKv + to0, v, vc);
+                mbar_arrive(bar(V_FULL + st));
             }
-            fence_async_smem();
-        };
-        Keys keys = keys_of(0), next = keys_of(1);
-        uint4 k[kPasses], v[kPasses];
-        load(a.kc, 0, keys, k);
-        for (int i = 0; i < count; ++i) {
-            const int st = i % C::kStages, turn = (i / C::kStages) & 1;
-            load(a.vc, i, keys, v);
-            if (cw == 0 && lane < C::kKeys / 16) {
-                float4 f = make_float4(0.f, 0.f, 1.f, 0.f);  // (behind the last token: masked)
-                if (keys.page != -1) {
-                    const float bad = __int_as_float(0x7fffffff);
-                    const float ks = keys.page < 0 ? bad : __ldg(a.ks + (int64_t)keys.page * a.kv_heads + head);
-                    const float vs = keys.page < 0 ? bad : __ldg(a.vs + (int64_t)keys.page * a.kv_heads + head);
-                    f = make_float4(ks, lg2(vs), vs == vs ? __fdividef(1.f, vs) : 1.f, 0.f);
-                }
-                scales[(j0 + i) % kRing][lane] = f;
-            }
-            if (!mbar_wait(bar(K_FREE + st), turn ^ 1)) {
-                fine = false;
-                break;
-            }
-            put(sk + st * C::kKv, k);
-            mbar_arrive(bar(K_FULL + st));
-            keys = next;
-            next = keys_of(i + 2);
-            load(a.kc, i + 1, keys, k);
-            if (!mbar_wait(bar(V_FREE + st), turn ^ 1)) {
-                fine = false;
-                break;
-            }
-            put(sv + st * C::kKv, v);
-            mbar_arrive(bar(V_FULL + st));
+            gi0 += count;
         }
-    } else if (lane == 0) {
+    } else {
         // ---------------------------------------------------------------- products
         const uint32_t id_s = idesc_f16(128, C::kKeys, 0), id_o = idesc_f16(128, D, 1);
         // (the low parts first: a sum is cut while it is small)
-        auto scores = [&](int i, int tile, int slot) {
-            const uint32_t kt = desc_k(sk + (i % C::kStages) * C::kKv), qt = desc_k(sq + tile * kParts * C::kQ);
+        auto scores = [&](int gi, int tile) {
+            const int slot = 2 * tile + (gi & 1);
+            const uint32_t kt = desc_k(sk + (gi % C::kStages) * C::kKv), qt = desc_k(sq + tile * kParts * C::kQ);
+            if (elect()) {
 #pragma unroll
             for (int x = kParts - 1; x >= 0; --x)
 #pragma unroll
                 for (int kk = 0; kk < D / 16; ++kk)
-                    mma_ss(tmem + slot * C::kS, qt + ((x * C::kQ + (kk >> 2) * 16384 + (kk & 3) * 32) >> 4),
+                    mma_ss(tmem + slot * C::kKeys, qt + ((x * C::kQ + (kk >> 2) * 16384 + (kk & 3) * 32) >> 4),
                            kt + (((kk >> 2) * (C::kKeys * 128) + (kk & 3) * 32) >> 4), id_s, x < kParts - 1 || kk > 0);
             mma_commit(bar(S_FULL + slot));
+            }
+            __syncwarp();
         };
-        auto outputs = [&](int i, int tile, int slot) {
-            const uint32_t vt = desc_mn(sv + (i % C::kStages) * C::kKv, C::kKeys * 128);
+        auto outputs = [&](int gi, int i, int tile) {
+            const int slot = 2 * tile + (gi & 1);
+            const uint32_t vt = desc_mn(sv + (gi % C::kStages) * C::kKv, C::kKeys * 128);
             const bool add = (kParts == 2 ? i % kFlush : i) > 0;
+            if (elect()) {
 #pragma unroll
             for (int x = kParts - 1; x >= 0; --x)
 #pragma unroll
                 for (int kk = 0; kk < C::kKeys / 16; ++kk)
-                    mma_ts(tmem + C::kO + tile * D, (x == 0 ? tmem + slot * C::kS : tmem + C::kLow + slot * C::kLowStep) + 8 * kk,
+                    mma_ts(tmem + C::kO + tile * D, (x == 0 ? tmem + slot * C::kKeys : tmem + C::kLow + (gi & 1) * C::kLowStep) + 8 * kk,
                            vt + ((kk * 2048) >> 4), id_o, add || x < kParts - 1 || kk > 0);
+            mma_commit(bar(O_DONE + slot));
+            }
+            __syncwarp();
         };
-        auto turn = [&](int i) { return (uint32_t)(i / C::kStages) & 1u; };
         auto wait = [&](int b, uint32_t parity) {
-            if (fine) fine = mbar_wait(bar(b), parity);
-            tc_fence_after();
+            if (fine) fine = mbar_wait(bar(b), parity & 1);
+            if (b >= W_FULL) tc_fence_after();
             return fine;
         };
-        if (C::kTiles == 2) {
-            if (count > 0 && wait(K_FULL, 0)) {
-                scores(0, 0, 0);
-                scores(0, 1, 1);
-                mma_commit(bar(K_FREE));
-            }
-            for (int i = 0; i < count && fine; ++i) {
-                const int st = i % C::kStages, st1 = (i + 1) % C::kStages;
-                if (!wait(V_FULL + st, turn(i))) break;
+        int done = 0;
+        while (fine && get_item<C::kRows, C::kKeys>(a, plan, turn, item)) {
+            ++turn;
+            const int count = item.count;
+            if (!count) continue;
+            for (int tile = 0; tile < C::kTiles; ++tile) wait(Q_FULL + tile, done);
+            // (each product is written once: warps far apart in the code cost instruction fetches)
 #pragma unroll 1
-                for (int tile = 0; tile < 2; ++tile) {
-                    if (!wait(W_FULL + tile, i & 1)) break;
-                    outputs(i, tile, tile);
-                    if (tile == 1) mma_commit(bar(V_FREE + st));
-                    if (i + 1 < count) {
-                        if (tile == 0 && !wait(K_FULL + st1, turn(i + 1))) break;
-                        scores(i + 1, tile, tile);
-                        if (tile == 1) mma_commit(bar(K_FREE + st1));
-                    }
-                }
-            }
-        } else {
-            if (count > 0 && wait(K_FULL, 0)) {
-                scores(0, 0, 0);
-                mma_commit(bar(K_FREE));
-            }
-            for (int i = 0; i < count && fine; ++i) {
-                const int st = i % C::kStages, st1 = (i + 1) % C::kStages;
+            for (int i = -1; i < count && fine; ++i) {
+                const int gi = gi0 + i;
                 if (i + 1 < count) {
-                    if (!wait(K_FULL + st1, turn(i + 1))) break;
-                    scores(i + 1, 0, (i + 1) & 1);
-                    mma_commit(bar(K_FREE + st1));
+                    const int st = (gi + 1) % C::kStages;
+                    if (!wait(K_FULL + st, (gi + 1) / C::kStages)) break;
+#pragma unroll 1
+                    for (int tile = 0; tile < C::kTiles; ++tile) scores(gi + 1, tile);
+                    if (elect()) mma_commit(bar(K_FREE + st));
                 }
-                if (!wait(V_FULL + st, turn(i)) || !wait(W_FULL + (i & 1), (i >> 1) & 1)) break;
-                outputs(i, 0, i & 1);
-                mma_commit(bar(V_FREE + st));
-                mma_commit(bar(O_DONE + (i & 1)));
+                if (i >= 0) {
+                    const int st = gi % C::kStages;
+                    if (!wait(V_FULL + st, gi / C::kStages)) break;
+#pragma unroll 1
+                    for (int tile = 0; tile < C::kTiles && fine; ++tile) {
+                        if (!wait(W_FULL + 2 * tile + (gi & 1), gi >> 1)) break;
+                        if (i == 0 && done > 0 && !wait(O_FREE + tile, done - 1)) break;
+                        outputs(gi, i, tile);
+                    }
+                    if (elect()) mma_commit(bar(V_FREE + st));
+                }
             }
+            if (elect()) mma_commit(bar(O_LAST));
+            gi0 += count;
+            ++done;
         }
         // (also after a wait that ran out: what was issued ends before the TMEM goes)
-        if (count > 0) {
-            mma_commit(bar(O_LAST));
-            if (!fine) mbar_wait(bar(O_LAST), 0);
-        }
+        if (!fine) mbar_wait(bar(O_LAST), (done - 1) & 1);
     }
     if (!fine) gave_up = 1;
     tc_fence_before();
@@ -707,46 +815,24 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_con
 template <typename T, int D, int kParts> __global__ void __launch_bounds__(256) join_splits_kernel(const __grid_constant__ Attn a, const TcPlan plan) {
     using C = TcConfig<D, kParts>;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    if (*(volatile int32_t *)a.status == GDR_ERR_BAD_SEQLENS) return;
-    // a row of q and its head: the block of the item that it belongs to
-    const int64_t row = (int64_t)blockIdx.x * 8 + warp;
+    if (*(volatile int32_t *)a.status != GDR_OK) return;
+    const int64_t row = (int64_t)blockIdx.x * 8 + warp;  // of o
     const int64_t t = row / a.heads;
     if (t >= a.tokens) return;
     const int h = (int)(row - t * a.heads), head = h / a.group;
-    int64_t n, first, tiles_before = 0, total = 0;
-    if (!a.cu) {
-        n = t / a.max_q;
-        first = n * a.max_q;
-    } else {
+    int64_t n = a.cu ? 0 : t / a.max_q;
+    if (a.cu) {
         if (t >= __ldg(a.cu + a.num_seqs)) return;
-        int64_t lo = 0, hi = a.num_seqs - 1;  // the last request that begins at t or before and has t
-        while (lo < hi) {
-            const int64_t mid = (lo + hi) / 2;
+        int64_t hi = a.num_seqs - 1;  // the first request that ends behind t
+        while (n < hi) {
+            const int64_t mid = (n + hi) / 2;
             if (__ldg(a.cu + mid + 1) > t) hi = mid;
-            else lo = mid + 1;
-        }
-        n = lo;
-        first = __ldg(a.cu + n);
-        for (int64_t m = lane; m < a.num_seqs; m += 32) {
-            const int64_t k = ((int64_t)rows_of(a, m).y * a.group + C::kRows - 1) / C::kRows;
-            total += k;
-            if (m < n) tiles_before += k;
-        }
-#pragma unroll
-        for (int d = 1; d < 32; d *= 2) {
-            total += __shfl_xor_sync(~0u, total, d);
-            tiles_before += __shfl_xor_sync(~0u, tiles_before, d);
+            else n = mid + 1;
         }
     }
-    const int64_t r = (t - first) * a.group + h % a.group, tile = r / C::kRows;
-    int64_t x;
-    if (!a.cu) {
-        const int64_t each = (a.max_q * a.group + C::kRows - 1) / C::kRows;
-        x = (each - 1 - tile) * a.num_seqs + n;
-    } else {
-        x = total - 1 - (tiles_before + tile);
-    }
-    const TcPart<C::kRows, D> *const parts = (const TcPart<C::kRows, D> *)plan.parts + ((int64_t)head * plan.tiles + x) * plan.splits;
+    const int64_t r = (t - rows_of(a, n).x) * a.group + h % a.group, tile = r / C::kRows;
+    const TcPart<C::kRows, D> *const parts =
+        (const TcPart<C::kRows, D> *)plan.parts + ((first_tile<C::kRows>(a, n) + tile) * a.kv_heads + head) * plan.splits;
     const int at = (int)(r - tile * C::kRows);
     float top = -INFINITY;
     for (int i = 0; i < plan.splits; ++i) top = fmaxf(top, parts[i].lse2[at]);
@@ -772,12 +858,8 @@ template <typename T, int D, int kParts> __global__ void __launch_bounds__(256) 
 template <int D, int kParts> TcPlan tc_plan(const Attn &a, bool packed) {
     using C = TcConfig<D, kParts>;
     const int64_t rows = a.max_q * a.group;
-    int64_t tiles = a.num_seqs * ((rows + C::kRows - 1) / C::kRows);
-    if (packed) {
-        const int64_t most = a.tokens * a.group / C::kRows + a.num_seqs;
-        if (most < tiles) tiles = most;
-    }
-    TcPlan p = {nullptr, (int)tiles, 1};
+    const int64_t tiles = packed ? a.tokens * a.group / C::kRows + a.num_seqs : a.num_seqs * ((rows + C::kRows - 1) / C::kRows);
+    TcPlan p = {nullptr, tiles, 1};
     const int64_t items = tiles * a.kv_heads, keys = ((a.width << a.log_page) + C::kKeys - 1) / C::kKeys;
     double best = 1e300;
     for (int s = 1; s <= 64 && (s == 1 || (items * s <= 8 * 152 && keys >= 4 * s)); ++s) {
@@ -804,13 +886,14 @@ template <int D> size_t tc_bytes_d(const Attn &a, int dtype) {
     return most;
 }
 
-template <typename T, int D, int kParts, int kMode> int launch_tc_kernel(const Attn &a, int code, void *ws, cudaStream_t s) {
+template <typename T, int D, int kParts, int kMode> int launch_tc_kernel(const Attn &a, int codes, void *ws, cudaStream_t s) {
     using C = TcConfig<D, kParts>;
     TcPlan plan = tc_plan<D, kParts>(a, a.cu != nullptr);
     plan.parts = (char *)ws;
-    const auto kernel = attn_tc_kernel<T, D, kParts, kMode>;
+    const auto kernel = codes == GDR_CODE_E4M3 ? attn_tc_kernel<T, D, kParts, kMode, GDR_CODE_E4M3> : attn_tc_kernel<T, D, kParts, kMode, GDR_CODE_INT8>;
     if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem) != cudaSuccess) return GDR_ERR_CUDA;
-    kernel<<<dim3((unsigned)plan.tiles, (unsigned)a.kv_heads, (unsigned)plan.splits), kTcThreads, C::kSmem, s>>>(a, plan, code);
+    const int64_t items = plan.tiles * a.kv_heads * plan.splits;
+    kernel<<<(unsigned)(items < 152 ? items : 152), kTcThreads, C::kSmem, s>>>(a, plan);
     if (cudaGetLastError() != cudaSuccess) return GDR_ERR_CUDA;
     if (plan.splits > 1)
         join_splits_kernel<T, D, kParts><<<(unsigned)((a.tokens * a.heads + 7) / 8), 256, 0, s>>>(a, plan);

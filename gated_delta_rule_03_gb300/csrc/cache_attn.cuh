@@ -68,9 +68,9 @@ __device__ __forceinline__ float lg2(float x) {
 // The score of a token in powers of two, from a product that is already scaled; away = |p - j|.
 // tanh(x) = 1 - 2 / (1 + e^2x) is off by some 1e-7 in all, and the cap times that in the score: enough
 // for bf16 results; fp32 ones take the library's.
-template <bool kExact> __device__ __forceinline__ float shaped(float z, float softcap, float slope, float away) {
+template <bool kExact> __device__ __forceinline__ float shaped(float z, float softcap, float inv_cap, float slope, float away) {
     if (softcap > 0.f) {
-        const float x = z / softcap;
+        const float x = z * inv_cap;
         z = softcap * (kExact ? tanhf(x) : 1.f - __fdividef(2.f, 1.f + ex2(2.f * kLog2e * x)));
     }
     return fmaf(-slope, away, z);

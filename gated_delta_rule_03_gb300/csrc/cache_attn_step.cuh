@@ -7,13 +7,14 @@
 // their operands are registers, so codes go from the copy in shared memory to an operand without
 // a turn through it. The order of the contraction is free: thread c of a quad takes 16 consecutive
 // bytes of a key as the k indices of four steps (queries are laid out alike), and dims 16 g + u of a value as
-// column g of step u, which makes every copy 16 bytes wide.
+// column g of step u, so that shared memory is read 16 bytes at a time.
 // The tensor cores are far from busy (a tenth at 8 heads a group); the 5th-generation ones would need
 // the codes converted through shared memory, rows filled up to 128, and the same bytes.
 //
 // Bound by memory: each cached byte is read once per 16 rows. A warp streams tiles of 16 tokens
-// through a ring of its own in shared memory (cp.async, kStages deep, each thread reads back only what
-// it copied: no barrier between warps until an item ends).
+// through a ring of its own in shared memory (cp.async of whole lines, kStages deep: no barrier between warps
+// until an item ends). Copies in the order that the products take them, 32 bytes of a line at a time,
+// stopped at 4.4 TB/s.
 //
 // Split. All items' keys, in units of kUnit tokens, are laid end to end and shared out equally
 // among the resident blocks, whatever the requests' lengths. A block that ends inside an
@@ -46,8 +47,13 @@ template <int D, int kParts> struct StepConfig {
 __device__ __forceinline__ void cp16(uint32_t dst, const void *src) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
-__device__ __forceinline__ void cp8(uint32_t dst, const void *src) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
+// Where a row's 16-byte chunk lies in its row in shared memory: eight lanes read chunks 4j .. 4j + 3 of two
+// neighbouring rows of keys, and two chunks of four even (or odd) rows of values, without a bank twice.
+template <int D> __device__ __forceinline__ int key_place(int row, int chunk) {
+    return (D == 64 ? chunk : chunk ^ ((row & 1) << 2)) * 16;
+}
+template <int D> __device__ __forceinline__ int value_place(int row, int chunk) {
+    return (D == 64 ? chunk ^ ((row >> 2) & 1) << 1 : chunk ^ (row & 6)) * 16;
 }
 __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
     asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
@@ -136,7 +142,7 @@ __global__ void __launch_bounds__(kStepWarps * 32, (StepConfig<D, kParts>::kBloc
     }
 
     char *const ring = smem + warp * C::kStages * C::kStage;
-    const uint32_t ring_s = sm100::smem_u32(ring) + lane * 16;
+    const uint32_t ring_s = sm100::smem_u32(ring);
     uint32_t *const qfrag = (uint32_t *)(smem + C::kRing);
 
     int64_t u = (int64_t)blockIdx.x * per, n = share.n, before = share.before;
@@ -185,20 +191,10 @@ __global__ void __launch_bounds__(kStepWarps * 32, (StepConfig<D, kParts>::kBloc
                 if (lane == 0) scales[warp][slot] = make_float2(k1, v1);
                 const uint32_t dst = ring_s + slot * C::kStage;
 #pragma unroll
-                for (int t = 0; t < 2; ++t)
-#pragma unroll
-                    for (int j = 0; j < D / 64; ++j)
-                        cp16(dst + (t * (D / 64) + j) * 512, a.kc + at + (8 * t + g) * D + 64 * j + 16 * c);
-#pragma unroll
-                for (int t = 0; t < 4; ++t) {
-                    const int row = 2 * c + (t & 1) + 8 * (t >> 1);
-                    if constexpr (D == 64) {
-                        cp8(dst - lane * 8 + 16 * D + t * 256, a.vc + at + row * D + 8 * g);
-                    } else {
-#pragma unroll
-                        for (int j = 0; j < D / 128; ++j)
-                            cp16(dst + 16 * D + (t * (D / 128) + j) * 512, a.vc + at + row * D + 128 * j + 16 * g);
-                    }
+                for (int x = 0; x < 16 * D; x += 512) {  // a warp's 512 bytes: whole lines
+                    const int r = (x + lane * 16) / D, chunk = (x + lane * 16) % D / 16;
+                    cp16(dst + r * D + key_place<D>(r, chunk), a.kc + at + x + lane * 16);
+                    cp16(dst + 16 * D + r * D + value_place<D>(r, chunk), a.vc + at + x + lane * 16);
                 }
             }
             asm volatile("cp.async.commit_group;" ::: "memory");
@@ -264,15 +260,17 @@ __global__ void __launch_bounds__(kStepWarps * 32, (StepConfig<D, kParts>::kBloc
         const int lim0 = a.causal ? min(len, p0 + 1) : len, lim1 = a.causal ? min(len, p1 + 1) : len;
         const int sure = a.causal ? min(len, past + row0 / a.group + 1) : len;  // seen by every row
 
+        const float inv_cap = kShaped && a.softcap > 0.f ? 1.f / a.softcap : 0.f;
         float ref0 = kNoRef, ref1 = kNoRef, l0 = 0.f, l1 = 0.f;
         float acc[D / 8][4];
 #pragma unroll
         for (int i = 0; i < D / 8; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
 
         for (int i = 0; i < count; ++i) {
+            __syncwarp();  // (the place in the ring has been read)
             fetch(i + C::kStages - 1);
             asm volatile("cp.async.wait_group %0;" ::"n"(C::kStages - 1) : "memory");
-            __syncwarp();  // (scales)
+            __syncwarp();  // (what the others have copied)
             const int slot = i % C::kStages;
             const char *const at = ring + slot * C::kStage;
             const float2 sc = scales[warp][slot];
@@ -284,7 +282,7 @@ __global__ void __launch_bounds__(kStepWarps * 32, (StepConfig<D, kParts>::kBloc
             for (int j = 0; j < D / 64; ++j) {
                 uint4 k[2];
 #pragma unroll
-                for (int t = 0; t < 2; ++t) k[t] = *(const uint4 *)(at + (t * (D / 64) + j) * 512 + lane * 16);
+                for (int t = 0; t < 2; ++t) k[t] = *(const uint4 *)(at + (8 * t + g) * D + key_place<D>(g, 4 * j + c));
 #pragma unroll
                 for (int w = 0; w < 4; ++w) {
                     const int step = j * 4 + w;
@@ -318,7 +316,7 @@ __global__ void __launch_bounds__(kStepWarps * 32, (StepConfig<D, kParts>::kBloc
                 for (int e = 0; e < 4; ++e) {
                     const int j = tok + 8 * t + 2 * c + (e & 1);
                     float z = s[t][e] * (e < 2 ? m0 : m1);
-                    if (kShaped) z = shaped<kParts == 2>(z, a.softcap, e < 2 ? slope0 : slope1, fabsf((float)((e < 2 ? p0 : p1) - j)));
+                    if (kShaped) z = shaped<kParts == 2>(z, a.softcap, inv_cap, e < 2 ? slope0 : slope1, fabsf((float)((e < 2 ? p0 : p1) - j)));
                     s[t][e] = fmaf(z, kLog2e, lv);
                 }
             const bool edge = tok + 16 > sure;
@@ -376,11 +374,13 @@ __global__ void __launch_bounds__(kStepWarps * 32, (StepConfig<D, kParts>::kBloc
                 uint32_t v[4][kWords];
 #pragma unroll
                 for (int t = 0; t < 4; ++t) {
+                    const int r = 2 * c + (t & 1) + 8 * (t >> 1);
+                    const char *const from = at + 16 * D + r * D;
                     if constexpr (D == 64) {
-                        const uint2 w = *(const uint2 *)(at + 16 * D + t * 256 + lane * 8);
+                        const uint2 w = *(const uint2 *)(from + value_place<D>(r, g >> 1) + (g & 1) * 8);
                         v[t][0] = w.x, v[t][1] = w.y;
                     } else {
-                        const uint4 w = *(const uint4 *)(at + 16 * D + (t * (D / 128) + j) * 512 + lane * 16);
+                        const uint4 w = *(const uint4 *)(from + value_place<D>(r, 8 * j + g));
                         v[t][0] = w.x, v[t][1] = w.y, v[t][2] = w.z, v[t][3] = w.w;
                     }
                     if (unsure && (sc.y != sc.y || tok + 2 * c + (t & 1) + 8 * (t >> 1) >= len)) {

@@ -12,14 +12,16 @@
 // the codes converted through shared memory, rows filled up to 128, and the same bytes.
 //
 // Bound by memory: each cached byte is read once per 16 rows. A warp streams tiles of 16 tokens
-// through a ring of its own in shared memory (cp.async of whole lines, kStages deep: no barrier between warps
-// until an item ends). Copies in the order that the products take them, 32 bytes of a line at a time,
-// stopped at 4.4 TB/s.
+// through a ring of its own in shared memory (tensor copies, kStages deep: no barrier between warps until an
+// item ends). 16-byte copies by threads stopped at 4.4 TB/s in the order that the products take them, 32 bytes
+// of a line at a time, and at 5.3 TB/s by whole lines.
 //
 // Split. All items' keys, in units of kUnit tokens, are laid end to end and shared out equally
 // among the resident blocks, whatever the requests' lengths. A block that ends inside an
 // item leaves its part in the workspace; join_parts_kernel adds them in order.
 #pragma once
+
+#include <mutex>
 
 #include "cache_attn.cuh"
 #include "sm100.cuh"
@@ -40,21 +42,20 @@ template <int D, int kParts> struct StepConfig {
     static constexpr int kRing = kStepWarps * kStages * kStage;
     static constexpr int kQ = kParts * kSteps * 32 * 16;
     static constexpr bool kInRegs = D * kParts <= 128;    // queries stay in registers
-    static constexpr int kSmem = kRing + kQ;
+    static constexpr int kSmem = kRing + kQ + 1024;
     static_assert(kStepWarps * 16 * D * 4 <= kRing, "outputs of the warps meet in the ring");
 };
 
-__device__ __forceinline__ void cp16(uint32_t dst, const void *src) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+// Where a row's 16-byte chunk lies among the 16 rows that a tensor copy brings, in blocks of 128 bytes a row
+// (64 for D = 64) that are swizzled by the row: eight lanes read chunks c, c + 2, .. c + 6 of two neighbouring rows
+// of keys, and two chunks of four even (or odd) rows of values, without a bank twice (D = 64: twice).
+template <int D> __device__ __forceinline__ int place(int row, int chunk) {
+    if (D == 64) return row * 64 + (chunk ^ ((row >> 1) & 3)) * 16;
+    return (chunk >> 3) * 2048 + row * 128 + ((chunk ^ row) & 7) * 16;
 }
-// Where a row's 16-byte chunk lies in its row in shared memory: eight lanes read chunks 4j .. 4j + 3 of two
-// neighbouring rows of keys, and two chunks of four even (or odd) rows of values, without a bank twice.
-template <int D> __device__ __forceinline__ int key_place(int row, int chunk) {
-    return (D == 64 ? chunk : chunk ^ ((row & 1) << 2)) * 16;
-}
-template <int D> __device__ __forceinline__ int value_place(int row, int chunk) {
-    return (D == 64 ? chunk ^ ((row >> 2) & 1) << 1 : chunk ^ (row & 6)) * 16;
-}
+// The chunk of a key that thread c of a quad takes as its j-th, for steps 4j .. 4j + 3 of the first product.
+template <int D> __device__ __forceinline__ int key_chunk(int j, int c) { return D == 64 ? c : (j >> 1) * 8 + 2 * c + (j & 1); }
+
 __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
     asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
@@ -70,6 +71,7 @@ __device__ __forceinline__ float2 unpack_f16(uint32_t r) { return __half22float2
 struct StepPlan {
     int32_t *tasks;  // [blocks][4]: the item whose parts begin with this block's: request (-1: none), head, tile, blocks
     char *parts;     // [blocks][2] Part
+    CUtensorMap maps[2];  // keys, values: 16 rows of one page and head at a time
 };
 
 // Where unit `u` lies: request n and the units before it.
@@ -120,16 +122,22 @@ __device__ inline Share find_share(const Attn &a, int64_t *sums, int64_t *found,
 }
 
 template <typename T, int D, int kCode, int kParts, bool kShaped>
-__global__ void __launch_bounds__(kStepWarps * 32, (StepConfig<D, kParts>::kBlocks)) attn_step_kernel(Attn a, StepPlan plan) {
+__global__ void __launch_bounds__(kStepWarps * 32, (StepConfig<D, kParts>::kBlocks)) attn_step_kernel(const __grid_constant__ Attn a, const __grid_constant__ StepPlan plan) {
     using C = StepConfig<D, kParts>;
     using P = Part<16, D>;
-    extern __shared__ __align__(16) char smem[];
+    extern __shared__ char unaligned[];
+    char *const smem = (char *)(((uintptr_t)unaligned + 1023) & ~(uintptr_t)1023);
     __shared__ int64_t sums[kStepWarps], found[2];
     __shared__ float2 scales[kStepWarps][C::kStages];
+    __shared__ __align__(8) uint64_t bars[kStepWarps][C::kStages];
     __shared__ float row_factor[16], row_slope[16];
     __shared__ float warp_ref[kStepWarps][16], warp_sum[kStepWarps][16];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
     const int in_page = (1 << a.log_page) - 1;
+
+    if (lane < C::kStages) sm100::mbar_init(sm100::smem_u32(&bars[warp][lane]), 1);
+    sm100::fence_mbar_init();
+    bool fine = true;
 
     int64_t per;
     const Share share = find_share(a, sums, found, &per);
@@ -145,6 +153,7 @@ __global__ void __launch_bounds__(kStepWarps * 32, (StepConfig<D, kParts>::kBloc
     const uint32_t ring_s = sm100::smem_u32(ring);
     uint32_t *const qfrag = (uint32_t *)(smem + C::kRing);
 
+    int fetched = 0, fetched_turn = 0, used = 0, turn = 0;  // places in the ring, and the parity of the turn round it
     int64_t u = (int64_t)blockIdx.x * per, n = share.n, before = share.before;
     const int64_t end_u = min(share.total, u + per);
     while (u < end_u) {
@@ -186,18 +195,19 @@ __global__ void __launch_bounds__(kStepWarps * 32, (StepConfig<D, kParts>::kBloc
                 const int64_t pg = __shfl_sync(~0u, page, i & 31);
                 const float k1 = __shfl_sync(~0u, ks, i & 31), v1 = __shfl_sync(~0u, vs, i & 31);
                 const int tok = first + (warp + i * kStepWarps) * 16;
-                const int64_t at = (((pg * a.kv_heads + head) << a.log_page) + (tok & in_page)) * D;
-                const int slot = i % C::kStages;
-                if (lane == 0) scales[warp][slot] = make_float2(k1, v1);
-                const uint32_t dst = ring_s + slot * C::kStage;
+                if (lane == 0) {
+                    scales[warp][fetched] = make_float2(k1, v1);
+                    const uint32_t dst = ring_s + fetched * C::kStage, bar = sm100::smem_u32(&bars[warp][fetched]);
+                    sm100::mbar_arrive_expect_tx(bar, C::kStage);
+                    const int row = head * (in_page + 1) + (tok & in_page);
 #pragma unroll
-                for (int x = 0; x < 16 * D; x += 512) {  // a warp's 512 bytes: whole lines
-                    const int r = (x + lane * 16) / D, chunk = (x + lane * 16) % D / 16;
-                    cp16(dst + r * D + key_place<D>(r, chunk), a.kc + at + x + lane * 16);
-                    cp16(dst + 16 * D + r * D + value_place<D>(r, chunk), a.vc + at + x + lane * 16);
+                    for (int x = 0; x < D; x += 128) {
+                        sm100::tma_load_3d(dst + x * 16, &plan.maps[0], bar, x, row, (int)pg);
+                        sm100::tma_load_3d(dst + 16 * D + x * 16, &plan.maps[1], bar, x, row, (int)pg);
+                    }
                 }
+                if (++fetched == C::kStages) fetched = 0;
             }
-            asm volatile("cp.async.commit_group;" ::: "memory");
         };
 #pragma unroll
         for (int i = 0; i < C::kStages - 1; ++i) fetch(i);
@@ -235,7 +245,9 @@ __global__ void __launch_bounds__(kStepWarps * 32, (StepConfig<D, kParts>::kBloc
 #pragma unroll
             for (int i = 0; i < kMine; i += 2) {
                 const int d = part * kMine + i;
-                const int step = (d >> 6) * 4 + ((d & 15) >> 2), cc = (d & 63) >> 4, pair = (d & 3) >> 1;
+                // chunk d / 16 is the j-th of thread cc
+                const int chunk = d >> 4, j = D == 64 ? 0 : (chunk >> 3) * 2 + (chunk & 1), cc = D == 64 ? chunk : (chunk & 7) >> 1;
+                const int step = j * 4 + ((d & 15) >> 2), pair = (d & 3) >> 1;
                 uint32_t *const to = qfrag + (step * 32 + (r & 7) * 4 + cc) * 4 + (r >> 3) + 2 * pair;
                 const float x = v[i] * up, y = v[i + 1] * up;
                 const uint32_t hi = pack_f16(x, y);
@@ -269,11 +281,14 @@ __global__ void __launch_bounds__(kStepWarps * 32, (StepConfig<D, kParts>::kBloc
         for (int i = 0; i < count; ++i) {
             __syncwarp();  // (the place in the ring has been read)
             fetch(i + C::kStages - 1);
-            asm volatile("cp.async.wait_group %0;" ::"n"(C::kStages - 1) : "memory");
-            __syncwarp();  // (what the others have copied)
-            const int slot = i % C::kStages;
-            const char *const at = ring + slot * C::kStage;
-            const float2 sc = scales[warp][slot];
+            fine = fine && sm100::mbar_wait(sm100::smem_u32(&bars[warp][used]), turn);
+            __syncwarp();
+            const char *const at = ring + used * C::kStage;
+            const float2 sc = scales[warp][used];
+            if (++used == C::kStages) {
+                used = 0;
+                turn ^= 1;
+            }
             const int tok = first + (warp + i * kStepWarps) * 16;
             float s[2][4];
 #pragma unroll
@@ -282,7 +297,7 @@ __global__ void __launch_bounds__(kStepWarps * 32, (StepConfig<D, kParts>::kBloc
             for (int j = 0; j < D / 64; ++j) {
                 uint4 k[2];
 #pragma unroll
-                for (int t = 0; t < 2; ++t) k[t] = *(const uint4 *)(at + (8 * t + g) * D + key_place<D>(g, 4 * j + c));
+                for (int t = 0; t < 2; ++t) k[t] = *(const uint4 *)(at + place<D>(8 * t + g, key_chunk<D>(j, c)));
 #pragma unroll
                 for (int w = 0; w < 4; ++w) {
                     const int step = j * 4 + w;
@@ -375,12 +390,11 @@ __global__ void __launch_bounds__(kStepWarps * 32, (StepConfig<D, kParts>::kBloc
 #pragma unroll
                 for (int t = 0; t < 4; ++t) {
                     const int r = 2 * c + (t & 1) + 8 * (t >> 1);
-                    const char *const from = at + 16 * D + r * D;
                     if constexpr (D == 64) {
-                        const uint2 w = *(const uint2 *)(from + value_place<D>(r, g >> 1) + (g & 1) * 8);
+                        const uint2 w = *(const uint2 *)(at + 16 * D + place<D>(r, g >> 1) + (g & 1) * 8);
                         v[t][0] = w.x, v[t][1] = w.y;
                     } else {
-                        const uint4 w = *(const uint4 *)(from + value_place<D>(r, 8 * j + g));
+                        const uint4 w = *(const uint4 *)(at + 16 * D + place<D>(r, 8 * j + g));
                         v[t][0] = w.x, v[t][1] = w.y, v[t][2] = w.z, v[t][3] = w.w;
                     }
                     if (unsure && (sc.y != sc.y || tok + 2 * c + (t & 1) + 8 * (t >> 1) >= len)) {
@@ -403,8 +417,6 @@ __global__ void __launch_bounds__(kStepWarps * 32, (StepConfig<D, kParts>::kBloc
                 }
             }
         }
-        asm volatile("cp.async.wait_group 0;" ::: "memory");
-
         // ---- the warps' parts meet
 #pragma unroll
         for (int d = 1; d < 4; d *= 2) {
@@ -474,14 +486,16 @@ __global__ void __launch_bounds__(kStepWarps * 32, (StepConfig<D, kParts>::kBloc
             task = make_int4((int)n, head, tile, (int)(stop / per - blockIdx.x + 1));
         }
         u += ub - ua;
+        sm100::fence_async_smem();  // (before copies into the ring again)
         __syncthreads();
     }
     if (plan.tasks && tid == 0) ((int4 *)plan.tasks)[blockIdx.x] = task;
+    if (!fine) *a.status = GDR_ERR_DEVICE_TIMEOUT;
 }
 
 // Adds the parts of items that several blocks worked on: a block for each that begins one, a
 // warp for each of its rows, the parts in order.
-template <typename T, int D> __global__ void __launch_bounds__(256) join_parts_kernel(Attn a, StepPlan plan) {
+template <typename T, int D> __global__ void __launch_bounds__(256) join_parts_kernel(const __grid_constant__ Attn a, const __grid_constant__ StepPlan plan) {
     using P = Part<16, D>;
     sm100::griddep_wait();
     const int4 task = ((const int4 *)plan.tasks)[blockIdx.x];
@@ -527,6 +541,26 @@ template <typename T, int D> __global__ void __launch_bounds__(256) join_parts_k
     }
 }
 
+// 16 rows of one page and head of a cache, 128 bytes of them at most, swizzled.
+inline bool map_cache(CUtensorMap *map, const void *cache, const Attn &a, int D) {
+    static decltype(&cuTensorMapEncodeTiled) encode = nullptr;
+    static std::once_flag once;
+    std::call_once(once, [] {
+        void *f = nullptr;
+        cudaDriverEntryPointQueryResult found;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &found) == cudaSuccess &&
+            found == cudaDriverEntryPointSuccess)
+            encode = reinterpret_cast<decltype(encode)>(f);
+    });
+    if (!encode) return false;
+    const cuuint64_t rows = (cuuint64_t)a.kv_heads << a.log_page;
+    const cuuint64_t dims[3] = {(cuuint64_t)D, rows, (cuuint64_t)a.pages}, strides[2] = {(cuuint64_t)D, rows * D};
+    const cuuint32_t box[3] = {(cuuint32_t)(D < 128 ? D : 128), 16, 1}, each[3] = {1, 1, 1};
+    return encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void *>(cache), dims, strides, box, each,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, D == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 template <typename T, int D, int kCode, int kParts, bool kShaped>
 int launch_step_kernel(const Attn &a, const StepPlan &plan, bool join, cudaStream_t s) {
     using C = StepConfig<D, kParts>;
@@ -555,6 +589,7 @@ template <int D> int launch_step_d(const Attn &a, int codes, int dtype, void *ws
     StepPlan plan;
     plan.tasks = join ? (int32_t *)ws : nullptr;
     plan.parts = (char *)ws + ((size_t)kSms * 4 * sizeof(int4) + 255) / 256 * 256;
+    if (!map_cache(&plan.maps[0], a.kc, a, D) || !map_cache(&plan.maps[1], a.vc, a, D)) return GDR_ERR_CUDA;
     const bool shaped = a.softcap > 0.f || a.slopes;
     const bool e4m3 = codes == GDR_CODE_E4M3;
 #define GDR_STEP(T, CODE, PARTS) \

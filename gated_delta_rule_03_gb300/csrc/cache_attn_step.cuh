@@ -1,11 +1,12 @@
 // cache_attn_step.cuh -- attention over a paged 8-bit cache for few rows: single tokens.
 //
 // Rows. The queries of one request that share a head of the cache (its group of heads, times its
-// new tokens) are the rows of 16-row tiles: an item is (request, head of the cache, tile).
+// new tokens) are the rows of tiles of kR: an item is (request, head of the cache, tile).
 //
-// Products. Warp-level 16x8x16 MMAs in fp16 with fp32 sums: a tile of 16 rows is what they take, and
-// their operands are registers, so codes go from the copy in shared memory to an operand without
-// a turn through it. The order of the contraction is free: thread c of a quad takes 16 consecutive
+// Products. Warp-level 16x8x16 MMAs in fp16 with fp32 sums, whose operands are registers, so that codes go from
+// the copy in shared memory to an operand without a turn through it. Up to 8 rows (kR = 8) are the 8 columns and
+// tokens and dims the 16 rows, half as many products and registers as with 16 rows against 8 tokens or
+// dims (kR = 16, only for 9 rows and more). The order of the contraction is free: thread c of a quad takes 16 consecutive
 // bytes of a key as the k indices of four steps (queries are laid out alike), and dims 16 g + u of a value as
 // column g of step u, so that shared memory is read 16 bytes at a time.
 // The tensor cores are far from busy (a tenth at 8 heads a group); the 5th-generation ones would need
@@ -34,16 +35,16 @@ constexpr int kUnit = 16 * kStepWarps;  // tokens
 constexpr int kMinUnits = 4;            // a block's least share
 constexpr int kSms = 152;
 
-template <int D, int kParts> struct StepConfig {
+template <int D, int kParts, int kR> struct StepConfig {
     static constexpr int kSteps = D / 16;                 // k steps of the first product
-    static constexpr int kStages = D == 64 ? 6 : (D == 256 ? (kParts == 2 ? 2 : 3) : 4);
-    static constexpr int kBlocks = D == 64 ? (kParts == 2 ? 3 : 4) : (D == 128 ? (kParts == 2 ? 2 : 3) : 2);  // per SM
+    static constexpr int kStages = D == 64 ? 6 : D == 256 ? (kParts == 2 ? 2 : 3) : kR == 8 && kParts == 1 ? 3 : 4;
+    static constexpr int kBlocks = D == 64 ? (kParts == 2 ? 3 : 4) : D == 256 ? 2 : kParts == 2 ? (kR == 8 ? 3 : 2) : kR == 8 ? 4 : 3;  // per SM
     static constexpr int kStage = 2 * 16 * D;             // bytes: keys, then values
     static constexpr int kRing = kStepWarps * kStages * kStage;
-    static constexpr int kQ = kParts * kSteps * 32 * 16;
-    static constexpr bool kInRegs = D * kParts <= 128;    // queries stay in registers
+    static constexpr int kQ = kParts * kSteps * 32 * kR;
+    static constexpr bool kInRegs = D * kParts * kR <= 2048;  // queries stay in registers
     static constexpr int kSmem = kRing + kQ + 1024;
-    static_assert(kStepWarps * 16 * D * 4 <= kRing, "outputs of the warps meet in the ring");
+    static_assert(kStepWarps * kR * D * 4 <= kRing, "outputs of the warps meet in the ring");
 };
 
 // Where a row's 16-byte chunk lies among the 16 rows that a tensor copy brings, in blocks of 128 bytes a row
@@ -82,15 +83,15 @@ struct Share {
 __device__ __forceinline__ int64_t units_of(const Attn &a, int64_t n) {
     return max((__ldg(a.kv_lens + n) + kUnit - 1) / kUnit, 1);
 }
-__device__ __forceinline__ int tiles_of(const Attn &a, int rows) { return (int)(((int64_t)rows * a.group + 15) / 16); }
+template <int kR> __device__ __forceinline__ int tiles_of(const Attn &a, int rows) { return (int)(((int64_t)rows * a.group + kR - 1) / kR); }
 
 // The request of the first unit of this block's share, and the share itself.
-__device__ inline Share find_share(const Attn &a, int64_t *sums, int64_t *found, int64_t *per) {
+template <int kR> __device__ Share find_share(const Attn &a, int64_t *sums, int64_t *found, int64_t *per) {
     constexpr int kThreads = kStepWarps * 32;
     const int tid = threadIdx.x;
     int64_t mine = 0;
     bool ok = true;
-    auto weight = [&](int64_t n) { return (int64_t)a.kv_heads * tiles_of(a, rows_of(a, n).y) * units_of(a, n); };
+    auto weight = [&](int64_t n) { return (int64_t)a.kv_heads * tiles_of<kR>(a, rows_of(a, n).y) * units_of(a, n); };
     for (int64_t n = tid; n < a.num_seqs; n += kThreads) {
         if (lengths_hold(a, n)) mine += weight(n);
         else ok = false;
@@ -121,18 +122,19 @@ __device__ inline Share find_share(const Attn &a, int64_t *sums, int64_t *found,
     return s;
 }
 
-template <typename T, int D, int kCode, int kParts, bool kShaped>
-__global__ void __launch_bounds__(kStepWarps * 32, (StepConfig<D, kParts>::kBlocks)) attn_step_kernel(const __grid_constant__ Attn a, const __grid_constant__ StepPlan plan) {
-    using C = StepConfig<D, kParts>;
-    using P = Part<16, D>;
+template <typename T, int D, int kCode, int kParts, bool kShaped, int kR>
+__global__ void __launch_bounds__(kStepWarps * 32, (StepConfig<D, kParts, kR>::kBlocks)) attn_step_kernel(const __grid_constant__ Attn a, const __grid_constant__ StepPlan plan) {
+    using C = StepConfig<D, kParts, kR>;
+    using P = Part<kR, D>;
     extern __shared__ char unaligned[];
     char *const smem = (char *)(((uintptr_t)unaligned + 1023) & ~(uintptr_t)1023);
     __shared__ int64_t sums[kStepWarps], found[2];
     __shared__ float2 scales[kStepWarps][C::kStages];
     __shared__ __align__(8) uint64_t bars[kStepWarps][C::kStages];
-    __shared__ float row_factor[16], row_slope[16];
-    __shared__ float warp_ref[kStepWarps][16], warp_sum[kStepWarps][16];
+    __shared__ float row_factor[kR], row_slope[kR];
+    __shared__ float warp_ref[kStepWarps][kR], warp_sum[kStepWarps][kR];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
+    const int R0 = kR == 16 ? g : 2 * c, R1 = kR == 16 ? g + 8 : 2 * c + 1;  // this thread's rows
     const int in_page = (1 << a.log_page) - 1;
 
     if (lane < C::kStages) sm100::mbar_init(sm100::smem_u32(&bars[warp][lane]), 1);
@@ -140,7 +142,7 @@ __global__ void __launch_bounds__(kStepWarps * 32, (StepConfig<D, kParts>::kBloc
     bool fine = true;
 
     int64_t per;
-    const Share share = find_share(a, sums, found, &per);
+    const Share share = find_share<kR>(a, sums, found, &per);
     if (blockIdx.x == 0 && tid == 0) *a.status = share.ok ? GDR_OK : GDR_ERR_BAD_SEQLENS;
     int4 task = make_int4(-1, 0, 0, 0);
     sm100::griddep_launch_dependents();
@@ -158,7 +160,7 @@ __global__ void __launch_bounds__(kStepWarps * 32, (StepConfig<D, kParts>::kBloc
     const int64_t end_u = min(share.total, u + per);
     while (u < end_u) {
         const int2 rows = rows_of(a, n);
-        const int tiles = tiles_of(a, rows.y);
+        const int tiles = tiles_of<kR>(a, rows.y);
         const int len = __ldg(a.kv_lens + n);
         const int64_t units = units_of(a, n), weight = (int64_t)a.kv_heads * tiles * units;
         if (u >= before + weight) {  // (also a request without new tokens)
@@ -169,7 +171,7 @@ __global__ void __launch_bounds__(kStepWarps * 32, (StepConfig<D, kParts>::kBloc
         const int64_t rel = u - before, item = rel / units;
         const int ua = (int)(rel - item * units), ub = (int)min(units, ua + (end_u - u));
         const int tile = (int)(item % tiles), head = (int)(item / tiles);
-        const int row0 = tile * 16, nrows = min(16, rows.y * a.group - row0);
+        const int row0 = tile * kR, nrows = min(kR, rows.y * a.group - row0);
         // the tokens that the last row may see
         const int past = len - rows.y;  // position of the first new token
         const int far = a.causal ? max(0, min(len, past + (row0 + nrows - 1) / a.group + 1)) : len;
@@ -213,7 +215,7 @@ __global__ void __launch_bounds__(kStepWarps * 32, (StepConfig<D, kParts>::kBloc
         for (int i = 0; i < C::kStages - 1; ++i) fetch(i);
 
         // ---- queries: fp16 with a power of two per row, in the order of the first product
-        {
+        if (tid < 8 * kR) {
             const int r = tid >> 3, part = tid & 7, at = row0 + r;
             constexpr int kMine = D / 8;
             float v[kMine];
@@ -248,35 +250,42 @@ __global__ void __launch_bounds__(kStepWarps * 32, (StepConfig<D, kParts>::kBloc
                 // chunk d / 16 is the j-th of thread cc
                 const int chunk = d >> 4, j = D == 64 ? 0 : (chunk >> 3) * 2 + (chunk & 1), cc = D == 64 ? chunk : (chunk & 7) >> 1;
                 const int step = j * 4 + ((d & 15) >> 2), pair = (d & 3) >> 1;
-                uint32_t *const to = qfrag + (step * 32 + (r & 7) * 4 + cc) * 4 + (r >> 3) + 2 * pair;
+                uint32_t *const to = kR == 16 ? qfrag + (step * 32 + (r & 7) * 4 + cc) * 4 + (r >> 3) + 2 * pair : qfrag + (step * 32 + r * 4 + cc) * 2 + pair;
                 const float x = v[i] * up, y = v[i + 1] * up;
                 const uint32_t hi = pack_f16(x, y);
                 *to = hi;
                 if (kParts == 2) {
                     const float2 f = unpack_f16(hi);
-                    to[C::kSteps * 128] = pack_f16(x - f.x, y - f.y);
+                    to[C::kSteps * 8 * kR] = pack_f16(x - f.x, y - f.y);
                 }
             }
         }
         __syncthreads();
-        uint32_t qreg[C::kInRegs ? kParts * C::kSteps : 1][4];
+        constexpr int kQRegs = kR / 4;  // of a step
+        uint32_t qreg[C::kInRegs ? kParts * C::kSteps : 1][kQRegs];
+        auto query = [&](int s, uint32_t (&q)[kQRegs]) {
+            if constexpr (kR == 16) {
+                const uint4 w = *(const uint4 *)(qfrag + (s * 32 + lane) * 4);
+                q[0] = w.x, q[1] = w.y, q[2] = w.z, q[3] = w.w;
+            } else {
+                const uint2 w = *(const uint2 *)(qfrag + (s * 32 + lane) * 2);
+                q[0] = w.x, q[1] = w.y;
+            }
+        };
         if (C::kInRegs) {
 #pragma unroll
-            for (int s = 0; s < kParts * C::kSteps; ++s) {
-                const uint4 w = *(const uint4 *)(qfrag + (s * 32 + lane) * 4);
-                qreg[s][0] = w.x, qreg[s][1] = w.y, qreg[s][2] = w.z, qreg[s][3] = w.w;
-            }
+            for (int s = 0; s < kParts * C::kSteps; ++s) query(s, qreg[s]);
         }
-        const float f0 = row_factor[g], f1 = row_factor[g + 8], slope0 = row_slope[g], slope1 = row_slope[g + 8];
-        const int p0 = past + (row0 + g) / a.group, p1 = past + (row0 + g + 8) / a.group;
+        const float f0 = row_factor[R0], f1 = row_factor[R1], slope0 = row_slope[R0], slope1 = row_slope[R1];
+        const int p0 = past + (row0 + R0) / a.group, p1 = past + (row0 + R1) / a.group;
         const int lim0 = a.causal ? min(len, p0 + 1) : len, lim1 = a.causal ? min(len, p1 + 1) : len;
         const int sure = a.causal ? min(len, past + row0 / a.group + 1) : len;  // seen by every row
 
         const float inv_cap = kShaped && a.softcap > 0.f ? 1.f / a.softcap : 0.f;
         float ref0 = kNoRef, ref1 = kNoRef, l0 = 0.f, l1 = 0.f;
-        float acc[D / 8][4];
+        float acc[D * kR / 128][4];
 #pragma unroll
-        for (int i = 0; i < D / 8; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
+        for (int i = 0; i < D * kR / 128; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
 
         for (int i = 0; i < count; ++i) {
             __syncwarp();  // (the place in the ring has been read)
@@ -290,6 +299,7 @@ __global__ void __launch_bounds__(kStepWarps * 32, (StepConfig<D, kParts>::kBloc
                 turn ^= 1;
             }
             const int tok = first + (warp + i * kStepWarps) * 16;
+            // scores: kR = 16: [8 tokens][token, row]; kR = 8: sums of even and of odd steps, [token][row]
             float s[2][4];
 #pragma unroll
             for (int t = 0; t < 2; ++t) s[t][0] = s[t][1] = s[t][2] = s[t][3] = 0.f;
@@ -301,53 +311,62 @@ __global__ void __launch_bounds__(kStepWarps * 32, (StepConfig<D, kParts>::kBloc
 #pragma unroll
                 for (int w = 0; w < 4; ++w) {
                     const int step = j * 4 + w;
-                    uint32_t q[kParts][4];
+                    uint32_t q[kParts][kQRegs];
 #pragma unroll
                     for (int x = 0; x < kParts; ++x) {
                         if (C::kInRegs) {
 #pragma unroll
-                            for (int y = 0; y < 4; ++y) q[x][y] = qreg[x * C::kSteps + step][y];
+                            for (int y = 0; y < kQRegs; ++y) q[x][y] = qreg[x * C::kSteps + step][y];
                         } else {
-                            const uint4 z = *(const uint4 *)(qfrag + ((x * C::kSteps + step) * 32 + lane) * 4);
-                            q[x][0] = z.x, q[x][1] = z.y, q[x][2] = z.z, q[x][3] = z.w;
+                            query(x * C::kSteps + step, q[x]);
                         }
                     }
+                    uint32_t lo[2], hi[2];
 #pragma unroll
-                    for (int t = 0; t < 2; ++t) {
-                        const uint32_t word = w == 0 ? k[t].x : w == 1 ? k[t].y : w == 2 ? k[t].z : k[t].w;
-                        uint32_t lo, hi;
-                        codes::to_f16x4<kCode>(word, lo, hi);
+                    for (int t = 0; t < 2; ++t)
+                        codes::to_f16x4<kCode>(w == 0 ? k[t].x : w == 1 ? k[t].y : w == 2 ? k[t].z : k[t].w, lo[t], hi[t]);
 #pragma unroll
-                        for (int x = kParts - 1; x >= 0; --x) mma_f16(s[t], q[x], lo, hi);
+                    for (int x = kParts - 1; x >= 0; --x) {
+                        if constexpr (kR == 16) {
+                            mma_f16(s[0], q[x], lo[0], hi[0]);
+                            mma_f16(s[1], q[x], lo[1], hi[1]);
+                        } else {
+                            const uint32_t tokens[4] = {lo[0], lo[1], hi[0], hi[1]};
+                            mma_f16(s[w & 1], tokens, q[x][0], q[x][1]);
+                        }
                     }
                 }
             }
+            if (kR == 8) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) s[0][e] += s[1][e];
+            }
+            // this thread's scores x: the token behind tok, and whether its row is R1
+            constexpr int kMine = kR / 2;
+            auto token = [&](int x) { return kR == 16 ? 8 * (x >> 2) + 2 * c + (x & 1) : g + 8 * (x >> 1); };
+            auto second = [](int x) { return kR == 16 ? (x & 2) != 0 : (x & 1) != 0; };
+            float w[kMine];
             // scores in powers of two, with the value scale's
             const float lv = lg2(sc.y), rv = sc.y == sc.y ? __fdividef(1.f, sc.y) : 1.f;  // (a weight there is NaN, or 0 if masked)
-            const float m0 = f0 * sc.x, m1 = f1 * sc.x;
-#pragma unroll
-            for (int t = 0; t < 2; ++t)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int j = tok + 8 * t + 2 * c + (e & 1);
-                    float z = s[t][e] * (e < 2 ? m0 : m1);
-                    if (kShaped) z = shaped<kParts == 2>(z, a.softcap, inv_cap, e < 2 ? slope0 : slope1, fabsf((float)((e < 2 ? p0 : p1) - j)));
-                    s[t][e] = fmaf(z, kLog2e, lv);
-                }
+            const float m0 = f0 * sc.x * (kShaped ? 1.f : kLog2e), m1 = f1 * sc.x * (kShaped ? 1.f : kLog2e);
             const bool edge = tok + 16 > sure;
-            if (edge) {
+            float top0 = -INFINITY, top1 = -INFINITY;
 #pragma unroll
-                for (int t = 0; t < 2; ++t)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        if (tok + 8 * t + 2 * c + (e & 1) >= (e < 2 ? lim0 : lim1)) s[t][e] = -INFINITY;
+            for (int x = 0; x < kMine; ++x) {
+                const float z = s[x >> 2][x & 3];
+                const int j = tok + token(x);
+                if (kShaped)
+                    w[x] = fmaf(shaped<kParts == 2>(z * (second(x) ? m1 : m0), a.softcap, inv_cap, second(x) ? slope1 : slope0,
+                                                    fabsf((float)((second(x) ? p1 : p0) - j))), kLog2e, lv);
+                else
+                    w[x] = fmaf(z, second(x) ? m1 : m0, lv);
+                if (edge && j >= (second(x) ? lim1 : lim0)) w[x] = -INFINITY;
+                (second(x) ? top1 : top0) = fmaxf(second(x) ? top1 : top0, w[x]);
             }
-            const float top0 = fmaxf(fmaxf(s[0][0], s[0][1]), fmaxf(s[1][0], s[1][1]));
-            const float top1 = fmaxf(fmaxf(s[0][2], s[0][3]), fmaxf(s[1][2], s[1][3]));
             if (__any_sync(~0u, top0 > ref0 + (kSpan + kSlack) || top1 > ref1 + (kSpan + kSlack))) {
                 float t0 = top0, t1 = top1;
 #pragma unroll
-                for (int d = 1; d < 4; d *= 2) {
+                for (int d = kR == 16 ? 1 : 4; d < (kR == 16 ? 4 : 32); d *= 2) {  // the threads of the same rows
                     t0 = fmaxf(t0, __shfl_xor_sync(~0u, t0, d));
                     t1 = fmaxf(t1, __shfl_xor_sync(~0u, t1, d));
                 }
@@ -358,28 +377,33 @@ __global__ void __launch_bounds__(kStepWarps * 32, (StepConfig<D, kParts>::kBloc
                 l0 *= d0;
                 l1 *= d1;
 #pragma unroll
-                for (int x = 0; x < D / 8; ++x) {
-                    acc[x][0] *= d0;
-                    acc[x][1] *= d0;
-                    acc[x][2] *= d1;
-                    acc[x][3] *= d1;
-                }
+                for (int x = 0; x < D * kR / 128; ++x)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) acc[x][e] *= (kR == 16 ? e >= 2 : e & 1) ? d1 : d0;
             }
+            float sum0 = 0.f, sum1 = 0.f;
 #pragma unroll
-            for (int t = 0; t < 2; ++t)
+            for (int x = 0; x < kMine; ++x) {
+                w[x] = ex2(w[x] - (second(x) ? ref1 : ref0));
+                (second(x) ? sum1 : sum0) += w[x];
+            }
+            l0 = fmaf(sum0, rv, l0);
+            l1 = fmaf(sum1, rv, l1);
+            // weights as an operand: kR = 16 as they lie; kR = 8 turned, from tokens by rows to rows by tokens
+            uint32_t p[kParts][kMine / 2];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) s[t][e] = ex2(s[t][e] - (e < 2 ? ref0 : ref1));
-            l0 = fmaf((s[0][0] + s[0][1]) + (s[1][0] + s[1][1]), rv, l0);
-            l1 = fmaf((s[0][2] + s[0][3]) + (s[1][2] + s[1][3]), rv, l1);
-            uint32_t p[kParts][4];
-#pragma unroll
-            for (int y = 0; y < 4; ++y) {
-                const float x0 = s[y >> 1][(y & 1) * 2], x1 = s[y >> 1][(y & 1) * 2 + 1];
-                p[0][y] = pack_f16(x0, x1);
+            for (int y = 0; y < kMine / 2; ++y) {
+                p[0][y] = pack_f16(w[2 * y], w[2 * y + 1]);
                 if (kParts == 2) {
                     const float2 f = unpack_f16(p[0][y]);
-                    p[kParts - 1][y] = pack_f16(x0 - f.x, x1 - f.y);
+                    p[kParts - 1][y] = pack_f16(w[2 * y] - f.x, w[2 * y + 1] - f.y);
                 }
+            }
+            if (kR == 8) {
+#pragma unroll
+                for (int x = 0; x < kParts; ++x)
+#pragma unroll
+                    for (int y = 0; y < 2; ++y) asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %0;" : "+r"(p[x][y]));
             }
             // bytes behind the last token, and those that stand in for a page that is none, may be anything
             const bool unsure = tok + 16 > len || sc.y != sc.y;
@@ -391,62 +415,77 @@ __global__ void __launch_bounds__(kStepWarps * 32, (StepConfig<D, kParts>::kBloc
                 for (int t = 0; t < 4; ++t) {
                     const int r = 2 * c + (t & 1) + 8 * (t >> 1);
                     if constexpr (D == 64) {
-                        const uint2 w = *(const uint2 *)(at + 16 * D + place<D>(r, g >> 1) + (g & 1) * 8);
-                        v[t][0] = w.x, v[t][1] = w.y;
+                        const uint2 z = *(const uint2 *)(at + 16 * D + place<D>(r, g >> 1) + (g & 1) * 8);
+                        v[t][0] = z.x, v[t][1] = z.y;
                     } else {
-                        const uint4 w = *(const uint4 *)(at + 16 * D + place<D>(r, 8 * j + g));
-                        v[t][0] = w.x, v[t][1] = w.y, v[t][2] = w.z, v[t][3] = w.w;
+                        const uint4 z = *(const uint4 *)(at + 16 * D + place<D>(r, 8 * j + g));
+                        v[t][0] = z.x, v[t][1] = z.y, v[t][2] = z.z, v[t][3] = z.w;
                     }
-                    if (unsure && (sc.y != sc.y || tok + 2 * c + (t & 1) + 8 * (t >> 1) >= len)) {
+                    if (unsure && (sc.y != sc.y || tok + r >= len)) {
 #pragma unroll
-                        for (int w = 0; w < kWords; ++w) v[t][w] = 0;
+                        for (int z = 0; z < kWords; ++z) v[t][z] = 0;
                     }
                 }
 #pragma unroll
-                for (int w = 0; w < kWords; ++w) {
+                for (int z = 0; z < kWords; ++z) {
                     uint32_t b[2][4];  // [token pair][dim of the word]
 #pragma unroll
                     for (int t = 0; t < 2; ++t) {
-                        codes::to_f16x4<kCode>(__byte_perm(v[2 * t][w], v[2 * t + 1][w], 0x5140), b[t][0], b[t][1]);
-                        codes::to_f16x4<kCode>(__byte_perm(v[2 * t][w], v[2 * t + 1][w], 0x7362), b[t][2], b[t][3]);
+                        codes::to_f16x4<kCode>(__byte_perm(v[2 * t][z], v[2 * t + 1][z], 0x5140), b[t][0], b[t][1]);
+                        codes::to_f16x4<kCode>(__byte_perm(v[2 * t][z], v[2 * t + 1][z], 0x7362), b[t][2], b[t][3]);
                     }
+                    const int u = j * 4 * kWords + z * 4;
 #pragma unroll
-                    for (int x = 0; x < 4; ++x)
+                    for (int y = kParts - 1; y >= 0; --y) {
+                        if constexpr (kR == 16) {
 #pragma unroll
-                        for (int y = kParts - 1; y >= 0; --y) mma_f16(acc[j * 4 * kWords + w * 4 + x], p[y], b[0][x], b[1][x]);
+                            for (int x = 0; x < 4; ++x) mma_f16(acc[u + x], p[y], b[0][x], b[1][x]);
+                        } else {
+#pragma unroll
+                            for (int x = 0; x < 4; x += 2) {
+                                const uint32_t dims[4] = {b[0][x], b[0][x + 1], b[1][x], b[1][x + 1]};
+                                mma_f16(acc[(u + x) / 2], dims, p[y][0], p[y][1]);
+                            }
+                        }
+                    }
                 }
             }
         }
         // ---- the warps' parts meet
 #pragma unroll
-        for (int d = 1; d < 4; d *= 2) {
+        for (int d = kR == 16 ? 1 : 4; d < (kR == 16 ? 4 : 32); d *= 2) {
             l0 += __shfl_xor_sync(~0u, l0, d);
             l1 += __shfl_xor_sync(~0u, l1, d);
         }
-        if (c == 0) {
-            warp_ref[warp][g] = ref0;
-            warp_ref[warp][g + 8] = ref1;
-            warp_sum[warp][g] = l0;
-            warp_sum[warp][g + 8] = l1;
+        if (kR == 16 ? c == 0 : g == 0) {
+            warp_ref[warp][R0] = ref0;
+            warp_ref[warp][R1] = ref1;
+            warp_sum[warp][R0] = l0;
+            warp_sum[warp][R1] = l1;
         }
         __syncthreads();
-        float *const outs = (float *)smem;  // [warp][16][D]
+        float *const outs = (float *)smem;  // [warp][kR][D]
         constexpr int kU = D == 64 ? 8 : 16;  // dims of a thread in a row of 8 groups
 #pragma unroll
         for (int x = 0; x < D / 8; ++x) {
-            // column n of the MMA's 8 is dim (x / kU) 128 + kU n + x % kU
-            const int dim = (x / kU) * 128 + kU * (2 * c) + x % kU;
-            float *const to = outs + (warp * 16 + g) * D + dim;
-            to[0] = acc[x][0];
-            to[kU] = acc[x][1];
-            to[8 * D] = acc[x][2];
-            to[8 * D + kU] = acc[x][3];
+            const int dim = (x / kU) * 128 + x % kU;
+            if constexpr (kR == 16) {  // column n of 8 is dim + kU n
+                float *const to = outs + (warp * 16 + g) * D + dim + kU * (2 * c);
+                to[0] = acc[x][0];
+                to[kU] = acc[x][1];
+                to[8 * D] = acc[x][2];
+                to[8 * D + kU] = acc[x][3];
+            } else {  // row n of 8 is
+                float *const to = outs + (warp * 8 + 2 * c) * D + dim + kU * g;
+                to[0] = acc[x / 2][2 * (x & 1)];
+                to[D] = acc[x / 2][2 * (x & 1) + 1];
+            }
         }
         __syncthreads();
         const bool whole = ua == 0 && ub == units;
         P *const part = whole ? nullptr : (P *)plan.parts + (2 * (int64_t)blockIdx.x + (ua == 0));
         constexpr int kQuads = D / 4;
-        for (int x = tid; x < 16 * kQuads; x += kStepWarps * 32) {
+        for (int x = tid; x < kR * kQuads; x += kStepWarps * 32) {
             const int r = x / kQuads, d = (x % kQuads) * 4;
             if (r >= nrows) break;
             float top = kNoRef;
@@ -457,7 +496,7 @@ __global__ void __launch_bounds__(kStepWarps * 32, (StepConfig<D, kParts>::kBloc
 #pragma unroll
             for (int w = 0; w < kStepWarps; ++w) {
                 const float f = ex2(warp_ref[w][r] - top);
-                const float4 y = *(const float4 *)(outs + (w * 16 + r) * D + d);
+                const float4 y = *(const float4 *)(outs + (w * kR + r) * D + d);
                 l = fmaf(warp_sum[w][r], f, l);
                 o.x = fmaf(y.x, f, o.x);
                 o.y = fmaf(y.y, f, o.y);
@@ -495,15 +534,15 @@ __global__ void __launch_bounds__(kStepWarps * 32, (StepConfig<D, kParts>::kBloc
 
 // Adds the parts of items that several blocks worked on: a block for each that begins one, a
 // warp for each of its rows, the parts in order.
-template <typename T, int D> __global__ void __launch_bounds__(256) join_parts_kernel(const __grid_constant__ Attn a, const __grid_constant__ StepPlan plan) {
-    using P = Part<16, D>;
+template <typename T, int D, int kR> __global__ void __launch_bounds__(256) join_parts_kernel(const __grid_constant__ Attn a, const __grid_constant__ StepPlan plan) {
+    using P = Part<kR, D>;
     sm100::griddep_wait();
     const int4 task = ((const int4 *)plan.tasks)[blockIdx.x];
     if (task.x < 0) return;
     const int64_t n = task.x;
-    const int head = task.y, row0 = task.z * 16, blocks = task.w;
+    const int head = task.y, row0 = task.z * kR, blocks = task.w;
     const int2 rows = rows_of(a, n);
-    const int nrows = min(16, rows.y * a.group - row0);
+    const int nrows = min(kR, rows.y * a.group - row0);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const P *const parts = (const P *)plan.parts;
     // the first block's part is its second one, that of the others their first
@@ -561,11 +600,11 @@ inline bool map_cache(CUtensorMap *map, const void *cache, const Attn &a, int D)
                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <typename T, int D, int kCode, int kParts, bool kShaped>
+template <typename T, int D, int kCode, int kParts, bool kShaped, int kR>
 int launch_step_kernel(const Attn &a, const StepPlan &plan, bool join, cudaStream_t s) {
-    using C = StepConfig<D, kParts>;
+    using C = StepConfig<D, kParts, kR>;
     constexpr int kBlocks = kSms * C::kBlocks;
-    const auto kernel = attn_step_kernel<T, D, kCode, kParts, kShaped>;
+    const auto kernel = attn_step_kernel<T, D, kCode, kParts, kShaped, kR>;
     static const cudaError_t sized = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
     if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem) != cudaSuccess) return GDR_ERR_CUDA;
     kernel<<<kBlocks, kStepWarps * 32, C::kSmem, s>>>(a, plan);
@@ -580,7 +619,7 @@ int launch_step_kernel(const Attn &a, const StepPlan &plan, bool join, cudaStrea
     attr.val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    return cuda_status(cudaLaunchKernelEx(&cfg, join_parts_kernel<T, D>, a, plan));
+    return cuda_status(cudaLaunchKernelEx(&cfg, join_parts_kernel<T, D, kR>, a, plan));
 }
 
 template <int D> int launch_step_d(const Attn &a, int codes, int dtype, void *ws, cudaStream_t s) {
@@ -592,8 +631,10 @@ template <int D> int launch_step_d(const Attn &a, int codes, int dtype, void *ws
     if (!map_cache(&plan.maps[0], a.kc, a, D) || !map_cache(&plan.maps[1], a.vc, a, D)) return GDR_ERR_CUDA;
     const bool shaped = a.softcap > 0.f || a.slopes;
     const bool e4m3 = codes == GDR_CODE_E4M3;
-#define GDR_STEP(T, CODE, PARTS) \
-    return shaped ? launch_step_kernel<T, D, CODE, PARTS, true>(a, plan, join, s) : launch_step_kernel<T, D, CODE, PARTS, false>(a, plan, join, s)
+    const bool few = a.max_q * a.group <= 8;
+#define GDR_STEP_ROWS(T, CODE, PARTS, ROWS) \
+    (shaped ? launch_step_kernel<T, D, CODE, PARTS, true, ROWS>(a, plan, join, s) : launch_step_kernel<T, D, CODE, PARTS, false, ROWS>(a, plan, join, s))
+#define GDR_STEP(T, CODE, PARTS) return few ? GDR_STEP_ROWS(T, CODE, PARTS, 8) : GDR_STEP_ROWS(T, CODE, PARTS, 16)
     if (dtype == GDR_F32) {
         if (e4m3) GDR_STEP(float, GDR_CODE_E4M3, 2);
         GDR_STEP(float, GDR_CODE_INT8, 2);
@@ -601,10 +642,11 @@ template <int D> int launch_step_d(const Attn &a, int codes, int dtype, void *ws
     if (e4m3) GDR_STEP(__nv_bfloat16, GDR_CODE_E4M3, 1);
     GDR_STEP(__nv_bfloat16, GDR_CODE_INT8, 1);
 #undef GDR_STEP
+#undef GDR_STEP_ROWS
 }
 
 template <int D> size_t step_bytes_d() {
-    return ((size_t)kSms * 4 * sizeof(int4) + 255) / 256 * 256 + (size_t)kSms * StepConfig<D, 1>::kBlocks * 2 * sizeof(Part<16, D>);
+    return ((size_t)kSms * 4 * sizeof(int4) + 255) / 256 * 256 + (size_t)kSms * 4 * 2 * sizeof(Part<16, D>);  // (at most 4 blocks an SM)
 }
 
 }  // namespace cattn

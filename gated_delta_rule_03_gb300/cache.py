@@ -17,7 +17,8 @@ import functools
 import torch
 
 from . import ops
-from .linattn import _addr, _dense, _new, _rows
+from .described import dense, describe, named, new_like, rows_stride
+from .linattn import _addr
 from .ops import _DTYPES, _launch, _need
 
 _CODES = {torch.float8_e4m3fn: 0, torch.int8: 1}
@@ -45,38 +46,38 @@ class CacheAttnShape(ctypes.Structure):
                 ("softcap", ctypes.c_float)]
 
 
-@functools.lru_cache(maxsize=256)
-def _page_shape(fields):
-    return ctypes.byref(PageShape(*fields))
+def _opt(t, name):
+    return None if t is None else describe(t, name)
 
 
-@functools.lru_cache(maxsize=256)
-def _cache_shape(fields):
-    return ctypes.byref(CacheShape(*fields))
-
-
-@functools.lru_cache(maxsize=256)
-def _attn_shape(cache, fields):
-    return ctypes.byref(CacheAttnShape(CacheShape(*cache), *fields))
-
-
-@functools.lru_cache(maxsize=256)
-def _attn_workspace_bytes(cache, fields):
-    return int(ops._load().gdr_cache_attn_workspace_size(_attn_shape(cache, fields)))
-
-
-def _table(block_table):
-    _need(block_table, "block_table", torch.int32)
-    if block_table.dim() != 2:
+def _table(t):
+    dense(t, "block_table", torch.int32)
+    if len(t.shape) != 2:
         raise ValueError("block_table must have shape [num_seqs, width]")
-    return block_table.device, block_table.shape[0], block_table.shape[1]
+    return t.device, t.shape[0], t.shape[1]
 
 
-def _vector(t, name, n, dtype, device):
-    _need(t, name, dtype, device)
-    if t.dim() != 1 or t.shape[0] != n:
-        raise ValueError(f"{name} must have shape ({n},), got {tuple(t.shape)}")
-    return t
+@functools.lru_cache(maxsize=256)
+def _checked_plan(block_table, kv_lens, free_pages, free_count, q_lens, rows, page, outs):
+    block_table, kv_lens, free_pages, free_count, q_lens = named(block_table, kv_lens, free_pages, free_count, q_lens)
+    outs = named(*outs)
+    dev, n, width = _table(block_table)
+    i32 = torch.int32
+    dense(kv_lens, "kv_lens", i32, dev, (n,))
+    dense(free_pages, "free_pages", i32, dev)
+    dense(free_count, "free_count", i32, dev, (1,))
+    if q_lens is not None:
+        dense(q_lens, "q_lens", i32, dev, (n,))
+        if rows is None:
+            raise ValueError("q_lens needs rows, the tokens of the packed batch")
+    rows = n if rows is None else rows
+    if rows < 0:
+        raise ValueError(f"rows must not be negative, got {rows}")
+    sizes = (n, 1, n + 1, n, rows, rows)
+    for t, name, size in zip(outs, ("kv_lens_out", "free_count_out", "cu_q", "start", "positions", "slots"), sizes):
+        if t is not None:
+            dense(t, name, i32, dev, (size,))
+    return ctypes.byref(PageShape(n, width, rows, free_pages.shape.numel(), page)), sizes, all(t is None for t in outs)
 
 
 def page_plan(block_table, kv_lens, free_pages, free_count, page, q_lens=None, rows=None, kv_lens_out=None,
@@ -85,62 +86,74 @@ def page_plan(block_table, kv_lens, free_pages, free_count, page, q_lens=None, r
     [num_seqs, width], kv_lens [num_seqs], free_pages [num_pages] and free_count [1] int32; q_lens
     [num_seqs] int32 or None for one token each; rows: tokens of the packed batch, padding included
     (default num_seqs; needed with q_lens). The table gets its new entries in place. Returns a
-    PagePlan (kv_lens, free_count, cu_q, start, positions, slots) of new tensors or those given; kv_lens_out
-    may be kv_lens and free_count_out may be free_count. start is -1 for a refused request."""
+    PagePlan (kv_lens, free_count, cu_q, start, positions, slots) of new tensors (parts of one) or those
+    given; kv_lens_out may be kv_lens and free_count_out may be free_count. start is -1 for a refused request."""
     lib = ops._load()
+    outs = (kv_lens_out, free_count_out, cu_q, start, positions, slots)
+    shape, sizes, fresh = _checked_plan(
+        describe(block_table, "block_table"), describe(kv_lens, "kv_lens"), describe(free_pages, "free_pages"),
+        describe(free_count, "free_count"), _opt(q_lens, "q_lens"), None if rows is None else int(rows), int(page),
+        tuple(None if t is None else describe(t, "an output") for t in outs))
+    if fresh:
+        outs = new_like(kv_lens, stream, (sum(sizes),)).split_with_sizes(sizes)
+    else:
+        outs = [new_like(kv_lens, stream, (n,)) if t is None else t for t, n in zip(outs, sizes)]
+    _launch(lib.gdr_page_plan, "gdr_page_plan", kv_lens.device, stream, shape, _addr(q_lens), kv_lens.data_ptr(),
+            free_pages.data_ptr(), free_count.data_ptr(), block_table.data_ptr(), *[t.data_ptr() for t in outs])
+    return PagePlan(*outs)
+
+
+@functools.lru_cache(maxsize=256)
+def _checked_release(block_table, kv_lens, done, free_pages, free_count, page):
+    block_table, kv_lens, done, free_pages, free_count = named(block_table, kv_lens, done, free_pages, free_count)
     dev, n, width = _table(block_table)
-    _vector(kv_lens, "kv_lens", n, torch.int32, dev)
-    _need(free_pages, "free_pages", torch.int32, dev)
-    _vector(free_count, "free_count", 1, torch.int32, dev)
-    if q_lens is not None:
-        _vector(q_lens, "q_lens", n, torch.int32, dev)
-        if rows is None:
-            raise ValueError("q_lens needs rows, the tokens of the packed batch")
-    rows = n if rows is None else int(rows)
-    i32 = torch.int32
-    kv_lens_out = _dense(kv_lens_out, "kv_lens_out", (n,), i32, dev, stream)
-    free_count_out = _dense(free_count_out, "free_count_out", (1,), i32, dev, stream)
-    cu_q = _dense(cu_q, "cu_q", (n + 1,), i32, dev, stream)
-    start = _dense(start, "start", (n,), i32, dev, stream)
-    positions = _dense(positions, "positions", (rows,), i32, dev, stream)
-    slots = _dense(slots, "slots", (rows,), i32, dev, stream)
-    _launch(lib.gdr_page_plan, "gdr_page_plan", dev, stream, _page_shape((n, width, rows, free_pages.numel(), int(page))),
-            _addr(q_lens), kv_lens.data_ptr(), free_pages.data_ptr(), free_count.data_ptr(), block_table.data_ptr(),
-            kv_lens_out.data_ptr(), free_count_out.data_ptr(), cu_q.data_ptr(), start.data_ptr(), positions.data_ptr(),
-            slots.data_ptr())
-    return PagePlan(kv_lens_out, free_count_out, cu_q, start, positions, slots)
+    dense(kv_lens, "kv_lens", torch.int32, dev, (n,))
+    if done.dtype not in (torch.bool, torch.uint8):
+        raise TypeError("done must be a torch.bool or torch.uint8 tensor")
+    dense(done, "done", done.dtype, dev, (n,))
+    dense(free_pages, "free_pages", torch.int32, dev)
+    dense(free_count, "free_count", torch.int32, dev, (1,))
+    return ctypes.byref(PageShape(n, width, 0, free_pages.shape.numel(), page))
 
 
 def page_release(block_table, kv_lens, done, free_pages, free_count, page, stream=None):
     """Gives the pages of ended requests back (gdr_page_release): done [num_seqs] bool or uint8. The
     table, kv_lens, free_pages and free_count are changed in place."""
     lib = ops._load()
-    dev, n, width = _table(block_table)
-    _vector(kv_lens, "kv_lens", n, torch.int32, dev)
-    if not isinstance(done, torch.Tensor) or done.dtype not in (torch.bool, torch.uint8):
-        raise TypeError("done must be a torch.bool or torch.uint8 tensor")
-    _vector(done, "done", n, done.dtype, dev)
-    _need(free_pages, "free_pages", torch.int32, dev)
-    _vector(free_count, "free_count", 1, torch.int32, dev)
-    _launch(lib.gdr_page_release, "gdr_page_release", dev, stream, _page_shape((n, width, 0, free_pages.numel(), int(page))),
-            done.data_ptr(), kv_lens.data_ptr(), block_table.data_ptr(), free_pages.data_ptr(), free_count.data_ptr())
+    shape = _checked_release(describe(block_table, "block_table"), describe(kv_lens, "kv_lens"), describe(done, "done"),
+                             describe(free_pages, "free_pages"), describe(free_count, "free_count"), int(page))
+    _launch(lib.gdr_page_release, "gdr_page_release", kv_lens.device, stream, shape, done.data_ptr(), kv_lens.data_ptr(),
+            block_table.data_ptr(), free_pages.data_ptr(), free_count.data_ptr())
 
 
-def _cache(k_cache, v_cache, k_scale, v_scale, device, dtype):
+def _cache_fields(k_cache, v_cache, k_scale, v_scale, device, dtype):
     """The fields of CacheShape."""
-    if not isinstance(k_cache, torch.Tensor) or k_cache.dtype not in _CODES:
-        raise TypeError(f"unsupported k_cache: {getattr(k_cache, 'dtype', type(k_cache))}; torch.float8_e4m3fn or torch.int8")
-    _need(k_cache, "k_cache", None, device)
-    if k_cache.dim() != 4:
+    if k_cache.dtype not in _CODES:
+        raise TypeError(f"unsupported k_cache: {k_cache.dtype}; torch.float8_e4m3fn or torch.int8")
+    dense(k_cache, "k_cache", None, device)
+    if len(k_cache.shape) != 4:
         raise ValueError("k_cache must have shape [num_pages, kv_heads, page, d]")
     shape = k_cache.shape
-    for t, name, want, of in ((v_cache, "v_cache", shape, k_cache.dtype), (k_scale, "k_scale", shape[:2], torch.float32),
-                              (v_scale, "v_scale", shape[:2], torch.float32)):
-        _need(t, name, of, device)
-        if t.shape != want:
-            raise ValueError(f"{name} must have shape {tuple(want)}, got {tuple(t.shape)}")
+    dense(v_cache, "v_cache", k_cache.dtype, device, shape)
+    dense(k_scale, "k_scale", torch.float32, device, shape[:2])
+    dense(v_scale, "v_scale", torch.float32, device, shape[:2])
     pages, heads, page, d = shape
     return pages, heads, page, d, _CODES[k_cache.dtype], _DTYPES[dtype]
+
+
+@functools.lru_cache(maxsize=256)
+def _checked_append(k, v, slots, *caches):
+    k, v, slots, *caches = named(k, v, slots, *caches)
+    if k.dtype not in _DTYPES or len(k.shape) != 3:
+        raise TypeError(f"unsupported k: {k.dtype}, {len(k.shape)} dimensions")
+    dev, T = k.device, k.shape[0]
+    ks, vs = rows_stride(k, "k", k.dtype, dev, T), rows_stride(v, "v", k.dtype, dev, T)
+    cache = _cache_fields(*caches, dev, k.dtype)
+    for t, name in ((k, "k"), (v, "v")):
+        if t.shape[1] != cache[1] or t.shape[2] != cache[3]:
+            raise ValueError(f"{name} must have shape ({T}, {cache[1]}, {cache[3]}), got {tuple(t.shape)}")
+    dense(slots, "slots", torch.int32, dev, (T,))
+    return ctypes.byref(CacheShape(*cache)), ks, vs
 
 
 def cache_append(k, v, slots, k_cache, v_cache, k_scale, v_scale, stream=None):
@@ -148,17 +161,18 @@ def cache_append(k, v, slots, k_cache, v_cache, k_scale, v_scale, stream=None):
     their slots [T] int32 (gdr_cache_append); rows with slot -1 are skipped. The caches and scales are
     changed in place."""
     lib = ops._load()
-    if not isinstance(k, torch.Tensor) or k.dtype not in _DTYPES or k.dim() != 3:
-        raise TypeError(f"unsupported k: {getattr(k, 'dtype', type(k))}")
-    dev, T = k.device, k.shape[0]
-    ks, vs = _rows(k, "k", k.dtype, dev, T), _rows(v, "v", k.dtype, dev, T)
-    cache = _cache(k_cache, v_cache, k_scale, v_scale, dev, k.dtype)
-    for t, name in ((k, "k"), (v, "v")):
-        if t.shape[1] != cache[1] or t.shape[2] != cache[3]:
-            raise ValueError(f"{name} must have shape ({T}, {cache[1]}, {cache[3]}), got {tuple(t.shape)}")
-    _vector(slots, "slots", T, torch.int32, dev)
-    _launch(lib.gdr_cache_append, "gdr_cache_append", dev, stream, _cache_shape(cache), T, k.data_ptr(), ks, v.data_ptr(),
-            vs, slots.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr())
+    shape, ks, vs = _checked_append(
+        describe(k, "k"), describe(v, "v"), describe(slots, "slots"), describe(k_cache, "k_cache"),
+        describe(v_cache, "v_cache"), describe(k_scale, "k_scale"), describe(v_scale, "v_scale"))
+    _launch(lib.gdr_cache_append, "gdr_cache_append", k.device, stream, shape, k.shape[0], k.data_ptr(), ks, v.data_ptr(), vs,
+            slots.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr())
+
+
+@functools.lru_cache(maxsize=256)
+def _attn_call(cache, fields):
+    """A reference to the struct of these fields, and the workspace bytes that it takes."""
+    shape = ctypes.byref(CacheAttnShape(CacheShape(*cache), *fields))
+    return shape, int(ops._load().gdr_cache_attn_workspace_size(shape))
 
 
 def cache_attn_workspace_size(num_seqs, total_tokens, heads, kv_heads, d, page, width, num_pages, max_q=None,
@@ -166,8 +180,34 @@ def cache_attn_workspace_size(num_seqs, total_tokens, heads, kv_heads, d, page, 
     """Workspace bytes of cache_attn (0 if the sizes are unsupported)."""
     if max_q is None:
         max_q = total_tokens
-    return _attn_workspace_bytes((int(num_pages), kv_heads, page, d, _CODES[codes], _DTYPES[dtype]),
-                                 (int(num_seqs), int(total_tokens), int(max_q), int(width), 0, heads, 1, 1.0, 0.0))
+    return _attn_call((int(num_pages), kv_heads, page, d, _CODES[codes], _DTYPES[dtype]),
+                      (int(num_seqs), int(total_tokens), int(max_q), int(width), 0, heads, 1, 1.0, 0.0))[1]
+
+
+@functools.lru_cache(maxsize=256)
+def _checked_attn(q, caches, block_table, kv_lens, cu_q, slopes, o, lse, max_q, scale, softcap, causal):
+    q, block_table, kv_lens, cu_q, slopes, o, lse = named(q, block_table, kv_lens, cu_q, slopes, o, lse)
+    caches = named(*caches)
+    if q.dtype not in _DTYPES or len(q.shape) != 3:
+        raise TypeError(f"unsupported q: {q.dtype}, {len(q.shape)} dimensions")
+    dev, dtype, (T, heads, d) = q.device, q.dtype, q.shape
+    qs = rows_stride(q, "q", dtype, dev, T)
+    cache = _cache_fields(*caches, dev, dtype)
+    if cache[3] != d:
+        raise ValueError(f"q has heads of {d}, the cache of {cache[3]}")
+    _, n, width = _table(block_table)
+    dense(block_table, "block_table", None, dev)
+    dense(kv_lens, "kv_lens", torch.int32, dev, (n,))
+    if cu_q is not None:
+        dense(cu_q, "cu_q", torch.int32, dev, (n + 1,))
+    if slopes is not None:
+        dense(slopes, "slopes", torch.float32, dev, (heads,))
+    if o is not None:
+        dense(o, "o", dtype, dev, q.shape)
+    if lse is not None:
+        dense(lse, "lse", torch.float32, dev, (T, heads))
+    return _attn_call(cache, (n, T, T if max_q is None else max_q, width, qs, heads, causal, d ** -0.5 if scale is None else scale,
+                              softcap))
 
 
 def cache_attn(q, k_cache, v_cache, k_scale, v_scale, block_table, kv_lens, cu_q=None, max_q=None, scale=None,
@@ -179,31 +219,22 @@ def cache_attn(q, k_cache, v_cache, k_scale, v_scale, block_table, kv_lens, cu_q
     slopes [heads] fp32: scores lowered by slope times the distance. Returns o [T, heads, d], with
     return_lse (o, lse [T, heads] fp32)."""
     lib = ops._load()
-    if not isinstance(q, torch.Tensor) or q.dtype not in _DTYPES or q.dim() != 3:
-        raise TypeError(f"unsupported q: {getattr(q, 'dtype', type(q))}")
-    dev, dtype, (T, heads, d) = q.device, q.dtype, q.shape
-    qs = _rows(q, "q", dtype, dev, T)
-    cache = _cache(k_cache, v_cache, k_scale, v_scale, dev, dtype)
-    if cache[3] != d:
-        raise ValueError(f"q has heads of {d}, the cache of {cache[3]}")
-    _need(block_table, "block_table", torch.int32, dev)
-    if block_table.dim() != 2:
-        raise ValueError("block_table must have shape [num_seqs, width]")
-    n, width = block_table.shape
-    _vector(kv_lens, "kv_lens", n, torch.int32, dev)
-    if cu_q is not None:
-        _vector(cu_q, "cu_q", n + 1, torch.int32, dev)
-    if slopes is not None:
-        _vector(slopes, "slopes", heads, torch.float32, dev)
-    fields = (n, T, T if max_q is None else int(max_q), width, qs, heads, int(bool(causal)),
-              d ** -0.5 if scale is None else float(scale), float(softcap))
-    o = _dense(o, "o", q.shape, dtype, dev, stream)
-    if return_lse or lse is not None:
-        lse = _dense(lse, "lse", (T, heads), torch.float32, dev, stream)
+    shape, bytes_ = _checked_attn(
+        describe(q, "q"), (describe(k_cache, "k_cache"), describe(v_cache, "v_cache"), describe(k_scale, "k_scale"),
+                           describe(v_scale, "v_scale")),
+        describe(block_table, "block_table"), describe(kv_lens, "kv_lens"), _opt(cu_q, "cu_q"), _opt(slopes, "slopes"),
+        _opt(o, "o"), _opt(lse, "lse"), None if max_q is None else int(max_q), None if scale is None else float(scale),
+        float(softcap), int(bool(causal)))
+    if o is None:
+        o = new_like(q, stream)
+    if return_lse and lse is None:
+        lse = new_like(q, stream, q.shape[:2], torch.float32)
     if workspace is None:
-        workspace = _new(max(_attn_workspace_bytes(cache, fields), 256), torch.uint8, dev, stream)
-    _need(workspace, "workspace", device=dev)
-    _launch(lib.gdr_cache_attn, "gdr_cache_attn", dev, stream, _attn_shape(cache, fields), q.data_ptr(), k_cache.data_ptr(),
+        workspace = new_like(q, stream, (max(bytes_, 256),), torch.uint8)
+    else:
+        _need(workspace, "workspace", device=q.device)
+        bytes_ = workspace.nbytes
+    _launch(lib.gdr_cache_attn, "gdr_cache_attn", q.device, stream, shape, q.data_ptr(), k_cache.data_ptr(),
             v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), block_table.data_ptr(), kv_lens.data_ptr(),
-            _addr(cu_q), _addr(slopes), o.data_ptr(), _addr(lse), workspace.data_ptr(), workspace.nbytes)
+            _addr(cu_q), _addr(slopes), o.data_ptr(), _addr(lse), workspace.data_ptr(), bytes_)
     return (o, lse) if return_lse else o

@@ -176,8 +176,10 @@ def _stream_handle(stream, device):
     return ctypes.c_void_p(s.cuda_stream)
 
 
-# the current stream's handle without a Stream object around it (2 us of a small call)
+# the current stream's handle without a Stream object around it (2 us of a small call), and the current device
+# without the check that CUDA has been initialised (the tensors of a call are on it)
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_get_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _launch(f, what, device, stream, *args):
@@ -188,7 +190,7 @@ def _launch(f, what, device, stream, *args):
         handle = _raw_stream(device.index)
     else:
         handle = torch.cuda.current_stream(device).cuda_stream
-    if torch.cuda.current_device() == device.index:
+    if _get_device() == device.index:
         status = f(*args, handle)
     else:
         with torch.cuda.device(device):

@@ -12,8 +12,9 @@ import math
 import torch
 
 from . import ops
-from .linattn import _addr, _new, _rows
-from .ops import _DTYPES, _launch, _need
+from .described import dense, describe, named, new_like, rows_stride
+from .linattn import _addr
+from .ops import _DTYPES, _launch
 
 
 class RotaryShape(ctypes.Structure):
@@ -23,12 +24,6 @@ class RotaryShape(ctypes.Structure):
                 ("neighbours", ctypes.c_int), ("amplitude", ctypes.c_float),
                 ("q_stride", ctypes.c_int64), ("k_stride", ctypes.c_int64),
                 ("q_out_stride", ctypes.c_int64), ("k_out_stride", ctypes.c_int64)]
-
-
-@functools.lru_cache(maxsize=256)
-def _shape(fields):
-    """A reference to the struct of these fields."""
-    return ctypes.byref(RotaryShape(*fields))
 
 
 def rotary_rates(rot_dim, base=10000.0, factor=1.0, trained_length=None, fast_turns=32.0, slow_turns=1.0,
@@ -64,43 +59,52 @@ def rotary_amplitude(factor):
     return 1.0 if factor <= 1 else 0.1 * math.log(factor) + 1.0
 
 
-def _out(t, name, like, stream):
-    """A given output of `like`'s shape and its token stride, or a new dense one."""
-    if t is None:
-        return _new(like.shape, like.dtype, like.device, stream), 0
-    stride = _rows(t, name, like.dtype, like.device, like.shape[0])
-    if t.shape != like.shape:
-        raise ValueError(f"{name} must have shape {tuple(like.shape)}, got {tuple(t.shape)}")
-    return t, stride
-
-
-def _rotary(f, what, names, q, k, positions, rates, neighbours, amplitude, q_out, k_out, stream):
-    if not isinstance(q, torch.Tensor) or q.dtype not in _DTYPES or q.dim() != 3:
-        raise TypeError(f"unsupported {names[0]}: {getattr(q, 'dtype', type(q))}")
+@functools.lru_cache(maxsize=256)
+def _checked(names, q, k, positions, rates, q_out, k_out, neighbours, amplitude):
+    """Checks tensors by what `describe` says of them; a reference to the struct of the call."""
+    q, k, positions, rates, q_out, k_out = named(q, k, positions, rates, q_out, k_out)
+    if q.dtype not in _DTYPES or len(q.shape) != 3:
+        raise TypeError(f"unsupported {names[0]}: {q.dtype}, {len(q.shape)} dimensions")
     dev, dtype, (T, q_heads, d) = q.device, q.dtype, q.shape
-    qs = _rows(q, names[0], dtype, dev, T)
-    ks, k_heads = 0, 0
+    qs = rows_stride(q, names[0], dtype, dev, T)
+    ks, kos, k_heads = 0, 0, 0
     if k is not None:
-        ks = _rows(k, names[1], dtype, dev, T)
+        ks = rows_stride(k, names[1], dtype, dev, T)
         k_heads = k.shape[1]
         if k.shape[2] != d:
             raise ValueError(f"{names[1]} has heads of {k.shape[2]}, {names[0]} of {d}")
-    _need(positions, "positions", torch.int32, dev)
-    _need(rates, "rates", torch.int64, dev)
-    if positions.dim() != 1 or positions.shape[0] != T:
-        raise ValueError(f"positions must have shape ({T},), got {tuple(positions.shape)}")
-    if rates.dim() != 1:
+    dense(positions, "positions", torch.int32, dev, (T,))
+    dense(rates, "rates", torch.int64, dev)
+    if len(rates.shape) != 1:
         raise ValueError("rates must have shape [rot_dim / 2]")
-    q_out, qos = _out(q_out, names[2], q, stream)
-    kos = 0
+
+    def out_stride(t, name, like):
+        if t is None:
+            return 0
+        stride = rows_stride(t, name, dtype, dev, T)
+        if t.shape != like.shape:
+            raise ValueError(f"{name} must have shape {tuple(like.shape)}, got {tuple(t.shape)}")
+        return stride
+
+    qos = out_stride(q_out, names[2], q)
     if k is not None:
-        k_out, kos = _out(k_out, names[3], k, stream)
+        kos = out_stride(k_out, names[3], k)
     elif k_out is not None:
         raise ValueError(f"{names[3]} needs {names[1]}")
-    _launch(f, what, dev, stream,
-            _shape((T, q_heads, k_heads, d, 2 * rates.shape[0], _DTYPES[dtype], int(bool(neighbours)), float(amplitude),
-                    qs, ks, qos, kos)),
-            q.data_ptr(), _addr(k), positions.data_ptr(), rates.data_ptr(), q_out.data_ptr(), _addr(k_out))
+    return ctypes.byref(RotaryShape(T, q_heads, k_heads, d, 2 * rates.shape[0], _DTYPES[dtype], neighbours, amplitude, qs, ks,
+                                    qos, kos))
+
+
+def _rotary(f, what, names, q, k, positions, rates, neighbours, amplitude, q_out, k_out, stream):
+    shape = _checked(names, describe(q, names[0]), k if k is None else describe(k, names[1]), describe(positions, "positions"),
+                     describe(rates, "rates"), q_out if q_out is None else describe(q_out, names[2]),
+                     k_out if k_out is None else describe(k_out, names[3]), int(bool(neighbours)), float(amplitude))
+    if q_out is None:
+        q_out = new_like(q, stream)
+    if k is not None and k_out is None:
+        k_out = new_like(k, stream)
+    _launch(f, what, q.device, stream, shape, q.data_ptr(), _addr(k), positions.data_ptr(), rates.data_ptr(),
+            q_out.data_ptr(), _addr(k_out))
     return q_out, k_out
 
 

@@ -25,7 +25,7 @@ struct Append {
 };
 
 constexpr int kWarps = 4;
-constexpr int kHold = 8;
+constexpr int kHold = 4;
 
 // 8 consecutive entries.
 template <typename T> struct Eight;
@@ -70,13 +70,15 @@ template <int kCode> __device__ __forceinline__ uint2 encode(const float (&v)[8]
     return r;
 }
 
-// One run by kThreads threads (a warp, or the block with `sums` between its warps): rows
-// t .. t + len - 1 of the tensor into page `page` from place `off` on.
+// One run by kThreads threads (a warp, or the block with `shared` between its warps): rows t .. of the tensor into
+// page `page` from place `off` on, at most `room` of them. A warp is told their number `len`; the block finds it while
+// the first rows are on their way (a few too many at a run's end).
 template <typename T, int kCode, int kThreads>
-__device__ __forceinline__ void put_run(const Append &a, int which, int h, int64_t t, int len, int64_t page, int off, uint32_t *sums) {
-    const int tid = threadIdx.x & (kThreads - 1);
-    const int row_vecs = a.d >> 3, vecs = len * row_vecs;  // of 8 entries
-    const int shift = 31 - __clz(row_vecs);
+__device__ __forceinline__ void put_run(const Append &a, int which, int h, int64_t t, int32_t slot, int room, int len, uint32_t *shared) {
+    const int tid = threadIdx.x & (kThreads - 1), lane = threadIdx.x & 31;
+    const int64_t page = slot >> a.log_page;
+    const int off = slot & ((1 << a.log_page) - 1);
+    const int row_vecs = a.d >> 3, shift = 31 - __clz(row_vecs);  // of 8 entries
     const int64_t stride = which ? a.xs[1] : a.xs[0];
     const T *src = (const T *)(which ? a.x[1] : a.x[0]) + t * stride + (int64_t)h * a.d;
     auto from = [&](int i) { return src + (int64_t)(i >> shift) * stride + (i & (row_vecs - 1)) * 8; };
@@ -84,13 +86,25 @@ __device__ __forceinline__ void put_run(const Append &a, int which, int h, int64
     uint8_t *const out = (which ? a.cache[1] : a.cache[0]) + (((page * a.heads + h) << a.log_page) + off) * a.d;
     const float before = off > 0 ? *scale : 0.f;
 
+    int vecs = (kThreads > 32 ? room : len) << shift;
     Eight<T> held[kHold];
-    uint32_t most = 0;
 #pragma unroll
     for (int j = 0; j < kHold; ++j) {
         const int i = tid + j * kThreads;
         if (i < vecs) held[j].load(from(i));
     }
+    if (kThreads > 32) {
+        const bool follows = tid < room && __ldg(a.slots + t + tid) == slot + tid;
+        const uint32_t some = __ballot_sync(~0u, follows);
+        if (lane == 0) shared[threadIdx.x >> 5] = some;
+        __syncthreads();
+        len = 0;
+#pragma unroll
+        for (int w = 0; w < kThreads / 32; ++w)
+            if (len == 32 * w) len += shared[w] == ~0u ? 32 : __ffs(~shared[w]) - 1;
+        vecs = len << shift;
+    }
+    uint32_t most = 0;
 #pragma unroll
     for (int j = 0; j < kHold; ++j)
         if (tid + j * kThreads < vecs) most = max(most, held[j].largest());
@@ -101,7 +115,8 @@ __device__ __forceinline__ void put_run(const Append &a, int which, int h, int64
     }
     most = __reduce_max_sync(~0u, most);
     if (kThreads > 32) {
-        if ((threadIdx.x & 31) == 0) sums[threadIdx.x >> 5] = most;
+        uint32_t *const sums = shared + kThreads / 32;
+        if (lane == 0) sums[threadIdx.x >> 5] = most;
         __syncthreads();
 #pragma unroll
         for (int i = 0; i < kThreads / 32; ++i) most = max(most, sums[i]);
@@ -148,48 +163,51 @@ __device__ __forceinline__ void put_run(const Append &a, int which, int h, int64
         x.load(from(i));
         put(i, x);
     }
-    if (kThreads > 32) __syncthreads();  // (sums is used again by the next run)
+    if (kThreads > 32) __syncthreads();  // (shared is used again by the next run)
 }
 
-// A block takes the runs that begin in its `group` rows, for one head of one tensor: a single run
-// by all its warps, several by a warp each.
-template <typename T, int kCode> __global__ void __launch_bounds__(kWarps * 32) append_kernel(Append a) {
-    __shared__ uint32_t sums[kWarps];
-    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+// A block takes the runs that begin in its `group` rows, for one head of one tensor: long ones by all its warps one
+// after the other, many short ones by a warp each.
+template <typename T, int kCode> __global__ void __launch_bounds__(kWarps * 32, sizeof(T) == 2 ? 6 : 4) append_kernel(Append a) {
+    __shared__ uint32_t shared[2 * kWarps], starts[kWarps];
+    const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
     const int64_t t0 = (int64_t)blockIdx.x * a.group;
     const int h = blockIdx.y, which = blockIdx.z;
     const int in_page = (1 << a.log_page) - 1;
     auto slot_of = [&](int64_t t) { return t < a.tokens ? __ldg(a.slots + t) : -1; };
-    auto valid = [&](int64_t s) { return s >= 0 && s < a.limit; };
     bool begins = false;
-    if (lane < a.group) {
-        const int32_t s = slot_of(t0 + lane);
-        if (valid(s)) {
-            const int64_t t = t0 + lane;
-            begins = t == 0 || (s & in_page) == 0 || __ldg(a.slots + t - 1) != s - 1;
-        }
+    if (tid < a.group) {
+        const int64_t t = t0 + tid;
+        const int32_t s = slot_of(t), last = t > 0 ? slot_of(t - 1) : -1;
+        begins = s >= 0 && s < a.limit && (t == 0 || (s & in_page) == 0 || last != s - 1);
     }
-    uint32_t starts = __ballot_sync(~0u, begins);
-    const int runs = __popc(starts);
-    for (int r = 0; starts; ++r) {
-        const int at = __ffs(starts) - 1;
-        starts &= starts - 1;
-        if (runs > 1 && r % kWarps != w) continue;
-        const int64_t t = t0 + at;
-        const int32_t s = slot_of(t);
-        const int off = s & in_page, room = in_page + 1 - off;
-        int len = 0;
-        while (len < room) {  // rows of the run: 32 at a time, up to the first that does not follow
-            const int i = len + lane;
-            const uint32_t ok = __ballot_sync(~0u, i < room && slot_of(t + i) == s + i);
-            len += ok == ~0u ? 32 : __ffs(~ok) - 1;
-            if (ok != ~0u) break;
+    const uint32_t mine = __ballot_sync(~0u, begins);
+    if (lane == 0) starts[w] = mine;
+    __syncthreads();
+    int runs = 0;
+#pragma unroll
+    for (int i = 0; i < kWarps; ++i) runs += __popc(starts[i]);
+    const bool together = runs * 8 <= a.group;
+    int r = 0;
+    for (int i = 0; i < kWarps; ++i) {
+        for (uint32_t m = starts[i]; m; m &= m - 1, ++r) {
+            if (!together && r % kWarps != w) continue;
+            const int64_t t = t0 + 32 * i + __ffs(m) - 1;
+            const int32_t s = slot_of(t);
+            const int room = (int)min((int64_t)(in_page + 1 - (s & in_page)), a.tokens - t);
+            if (together) {
+                put_run<T, kCode, kWarps * 32>(a, which, h, t, s, room, 0, shared);
+            } else {
+                int len = 0;
+                while (len < room) {  // 32 rows at a time, up to the first that does not follow
+                    const int j = len + lane;
+                    const uint32_t ok = __ballot_sync(~0u, j < room && slot_of(t + j) == s + j);
+                    len += ok == ~0u ? 32 : __ffs(~ok) - 1;
+                    if (ok != ~0u) break;
+                }
+                put_run<T, kCode, 32>(a, which, h, t, s, room, len, nullptr);
+            }
         }
-        const int64_t page = s >> a.log_page;
-        if (runs > 1)
-            put_run<T, kCode, 32>(a, which, h, t, len, page, off, nullptr);
-        else
-            put_run<T, kCode, kWarps * 32>(a, which, h, t, len, page, off, sums);
     }
 }
 
@@ -247,8 +265,8 @@ extern "C" int gdr_cache_append(const gdr_cache_shape *shape, int64_t tokens, co
     a.heads = shape->kv_heads;
     a.d = shape->d;
     // Rows per block: single tokens of many requests are a run each, a warp's work; many rows are
-    // runs of whole pages, and a block looks for them in as many rows as a page has (at most 32).
-    a.group = tokens <= 2048 ? kWarps : shape->page < 32 ? shape->page : 32;
+    // runs of whole pages, and a block looks for them in as many rows as a page has.
+    a.group = tokens <= 2048 ? kWarps : shape->page;
     if (shape->dtype == GDR_F32)
         launch_append<float>(a, shape->codes, (cudaStream_t)stream);
     else

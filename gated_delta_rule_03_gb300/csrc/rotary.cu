@@ -33,7 +33,7 @@ template <typename T, int V> struct alignas(sizeof(T) * V) Vec {
 
 // V elements to a vector, two vectors to a thread: lane a < turning holds pairs a V .. a V + V - 1,
 // the lanes behind copy what is not turned.
-template <typename T, int V, bool kNeighbours> __global__ void __launch_bounds__(256) rotary_kernel(Rotary r) {
+template <typename T, int V, bool kNeighbours> __global__ void __launch_bounds__(256, 4) rotary_kernel(Rotary r) {
     const int64_t u = (int64_t)blockIdx.x * 256 + threadIdx.x;
     if (u >= r.units) return;
     const int64_t t = r.units < INT32_MAX ? (int64_t)((uint32_t)u / (uint32_t)r.lanes) : u / r.lanes;
@@ -70,7 +70,7 @@ template <typename T, int V, bool kNeighbours> __global__ void __launch_bounds__
         from = (const T *)(k ? r.x[1] : r.x[0]) + t * (k ? r.xs[1] : r.xs[0]) + (int64_t)at * r.d;
         to = (T *)(k ? r.y[1] : r.y[0]) + t * (k ? r.ys[1] : r.ys[0]) + (int64_t)at * r.d;
     };
-    constexpr int kAhead = 4;  // heads whose loads are under way together
+    constexpr int kAhead = 2;  // heads whose loads are under way together
     for (int h = h0; h < h1; h += kAhead) {
         W x[kAhead], y[kAhead];
 #pragma unroll
@@ -120,10 +120,10 @@ template <typename T, int V> int launch_rotary(Rotary r, int64_t tokens, bool in
     const int rest = (r.d - r.rot + 2 * V - 1) / (2 * V);
     r.lanes = r.turning + (in_place ? 0 : rest);
     r.units = tokens * r.lanes;
-    // Enough threads to fill the GPU (152 SMs of 1024 threads), each with as many heads as that
+    // Enough threads to fill the GPU (152 SMs of 2048 threads), each with as many heads as that
     // leaves: the sines of a pair are taken once for all of them.
     const int all = r.heads[0] + r.heads[1];
-    const int64_t want = 152 * 1024;
+    const int64_t want = 152 * 2048;
     int64_t parts = (want + r.units - 1) / r.units;
     if (parts > all) parts = all;
     r.step = (int)((all + parts - 1) / parts);

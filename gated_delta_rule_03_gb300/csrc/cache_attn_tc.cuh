@@ -10,8 +10,8 @@
 // which is K-major for the first product and MN-major for the second, so that both are written alike.
 // Loads of codes go to registers a tile ahead, as they have to pass through them.
 //
-// Roles (416 threads): kTiles groups of 128 threads for the softmax, a row to a thread; the rest of
-// 384 convert; one thread of the last warp issues the products. Scores have two buffers, so that the next
+// Roles (448 threads): kTiles groups of 128 threads for the softmax, a row to a thread; the rest of
+// 384 convert; a thread of each of the last two warps issues the products of a row tile. Scores have two buffers, so that the next
 // tile's are there when a tile's weights are done. A block stays and goes from item to item: the next
 // item's queries and first keys are on their way while the outputs of the last leave. (A block for each
 // item took 32 thousand cycles more per item, as much as six tiles of 128 keys.)
@@ -30,7 +30,7 @@ namespace cattn {
 
 using namespace sm100;
 
-constexpr int kTcThreads = 416;
+constexpr int kTcThreads = 448;
 constexpr int kRing = 8;   // tiles of scales
 constexpr int kFlush = 4;  // tiles whose outputs are added up in TMEM (fp32)
 
@@ -42,7 +42,7 @@ template <int D, int kParts> struct TcConfig {
     static constexpr int kRows = 128 * kTiles;
     static constexpr int kSoft = 128 * kTiles;         // threads
     static constexpr int kConv = 384 - kSoft;
-    // Registers of a thread: 13 warps are launched with 128 each; what the converters give up the softmax
+    // Registers of a thread: 14 warps are launched with 128 each; what the converters give up the softmax
     // gets (kSoft kSoftRegs + kConv kConvRegs = 384 x 128).
     static constexpr int kConvRegs = 112, kSoftRegs = kTiles == 2 ? 136 : 160;
     static_assert(kSoft * kSoftRegs + kConv * kConvRegs <= 384 * 128, "registers of the launch");
@@ -257,8 +257,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_con
     __shared__ float4 scales[kRing][8];  // of 16 keys: key scale, log2 and reciprocal of the value scale
     __shared__ uint32_t tmem_slot;
     __shared__ int gave_up;
-    // Of the stages of keys and values; of the scores' slots (2 tile + parity of the key tile); per row tile; one
-    enum { K_FULL = 0, K_FREE = 4, V_FULL = 8, V_FREE = 12, S_FULL = 16, W_FULL = 20, O_DONE = 24, Q_FULL = 28, O_FREE = 30, O_LAST = 32, BARS = 33 };
+    // Of the stages of keys and values; of the scores' slots (2 tile + parity of the key tile); per row tile
+    enum { K_FULL = 0, K_FREE = 4, V_FULL = 8, V_FREE = 12, S_FULL = 16, W_FULL = 20, O_DONE = 24, Q_FULL = 28, O_FREE = 30, O_LAST = 32, BARS = 34 };
     __shared__ __align__(8) uint64_t bars[BARS];
     auto bar = [&](int i) { return smem_u32(&bars[i]); };
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -268,8 +268,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_con
         for (int s = 0; s < 4; ++s) {
             mbar_init(bar(K_FULL + s), C::kConv);
             mbar_init(bar(V_FULL + s), C::kConv);
-            mbar_init(bar(K_FREE + s), 1);
-            mbar_init(bar(V_FREE + s), 1);
+            mbar_init(bar(K_FREE + s), C::kTiles);
+            mbar_init(bar(V_FREE + s), C::kTiles);
             mbar_init(bar(S_FULL + s), 1);
             mbar_init(bar(W_FULL + s), 128);
             mbar_init(bar(O_DONE + s), 1);
@@ -277,8 +277,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_con
         for (int s = 0; s < 2; ++s) {
             mbar_init(bar(Q_FULL + s), 128);
             mbar_init(bar(O_FREE + s), 128);
+            mbar_init(bar(O_LAST + s), 1);
         }
-        mbar_init(bar(O_LAST), 1);
         fence_mbar_init();
     }
     bool good = true;
@@ -475,13 +475,20 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_con
                     uint32_t hi[C::kKeys / 2], lo[kParts == 2 ? C::kKeys / 2 : 1];
                     float2 all = make_float2(0.f, 0.f);
                     float top = -INFINITY;
-                    uint32_t x[2][16];
+                    uint32_t x[4][16];
                     tmem_fetch16(s_at, x[0]);
+                    tmem_fetch16(s_at + 16, x[1]);
 #pragma unroll
                     for (int g = 0; g < C::kKeys / 16; ++g) {
-                        uint32_t(&y)[16] = x[g & 1];
-                        tmem_arrive16(y);
-                        if (g + 1 < C::kKeys / 16) tmem_fetch16(s_at + 16 * (g + 1), x[(g + 1) & 1]);
+                        uint32_t(&y)[16] = x[g & 3];
+                        if (g % 2 == 0) {
+                            tmem_arrive16(y);
+                            tmem_arrive16(x[(g + 1) & 3]);
+                            if (g + 2 < C::kKeys / 16) {
+                                tmem_fetch16(s_at + 16 * (g + 2), x[(g + 2) & 3]);
+                                tmem_fetch16(s_at + 16 * (g + 3), x[(g + 3) & 3]);
+                            }
+                        }
                         const auto shape = shape_of(g);
                         float2 some = make_float2(0.f, 0.f);
 #pragma unroll
@@ -576,7 +583,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_con
                 mbar_arrive(bar(W_FULL + slot));
             }
             gi0 += count;
-            if (fine) fine = mbar_wait(bar(O_LAST), done & 1);
+            if (fine) fine = mbar_wait(bar(O_LAST + tile), done & 1);
             __syncwarp();
             tc_fence_after();
             // ---- the next item's queries (the products with the last ones are done), then the results. A warp reads its
@@ -729,11 +736,12 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_con
             }
             gi0 += count;
         }
-    } else {
+    } else if (warp < 12 + C::kTiles) {
         // ---------------------------------------------------------------- products
+        const int tile = warp - 12;  // row tile
         const uint32_t id_s = idesc_f16(128, C::kKeys, 0), id_o = idesc_f16(128, D, 1);
         // (the low parts first: a sum is cut while it is small)
-        auto scores = [&](int gi, int tile) {
+        auto scores = [&](int gi) {
             const int slot = 2 * tile + (gi & 1);
             const uint32_t kt = desc_k(sk + (gi % C::kStages) * C::kKv), qt = desc_k(sq + tile * kParts * C::kQ);
             if (elect()) {
@@ -747,7 +755,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_con
             }
             __syncwarp();
         };
-        auto outputs = [&](int gi, int i, int tile) {
+        auto outputs = [&](int gi, int i) {
             const int slot = 2 * tile + (gi & 1);
             const uint32_t vt = desc_mn(sv + (gi % C::kStages) * C::kKv, C::kKeys * 128);
             const bool add = (kParts == 2 ? i % kFlush : i) > 0;
@@ -772,7 +780,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_con
             ++turn;
             const int count = item.count;
             if (!count) continue;
-            for (int tile = 0; tile < C::kTiles; ++tile) wait(Q_FULL + tile, done);
+            wait(Q_FULL + tile, done);
             // (each product is written once: warps far apart in the code cost instruction fetches)
 #pragma unroll 1
             for (int i = -1; i < count && fine; ++i) {
@@ -780,28 +788,24 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_con
                 if (i + 1 < count) {
                     const int st = (gi + 1) % C::kStages;
                     if (!wait(K_FULL + st, (gi + 1) / C::kStages)) break;
-#pragma unroll 1
-                    for (int tile = 0; tile < C::kTiles; ++tile) scores(gi + 1, tile);
+                    scores(gi + 1);
                     if (elect()) mma_commit(bar(K_FREE + st));
                 }
                 if (i >= 0) {
                     const int st = gi % C::kStages;
                     if (!wait(V_FULL + st, gi / C::kStages)) break;
-#pragma unroll 1
-                    for (int tile = 0; tile < C::kTiles && fine; ++tile) {
-                        if (!wait(W_FULL + 2 * tile + (gi & 1), gi >> 1)) break;
-                        if (i == 0 && done > 0 && !wait(O_FREE + tile, done - 1)) break;
-                        outputs(gi, i, tile);
-                    }
+                    if (!wait(W_FULL + 2 * tile + (gi & 1), gi >> 1)) break;
+                    if (i == 0 && done > 0 && !wait(O_FREE + tile, done - 1)) break;
+                    outputs(gi, i);
                     if (elect()) mma_commit(bar(V_FREE + st));
                 }
             }
-            if (elect()) mma_commit(bar(O_LAST));
+            if (elect()) mma_commit(bar(O_LAST + tile));
             gi0 += count;
             ++done;
         }
         // (also after a wait that ran out: what was issued ends before the TMEM goes)
-        if (!fine) mbar_wait(bar(O_LAST), (done - 1) & 1);
+        if (!fine) mbar_wait(bar(O_LAST + tile), (done - 1) & 1);
     }
     if (!fine) gave_up = 1;
     tc_fence_before();

@@ -10,8 +10,11 @@
 // bits down to 2^-21 of the largest and are dropped below 2^-32.
 #pragma once
 
+#include <cuda.h>
 #include <cuda_fp16.h>
 #include <math.h>
+
+#include <mutex>
 
 #include "codes.cuh"
 #include "internal.h"
@@ -108,6 +111,28 @@ template <int kThreads> __device__ int64_t block_sums(int64_t x, int64_t *sums, 
     }
     *total = all;
     return x + before;
+}
+
+// Tensor map of boxes of up to `most` rows of one page and head of a cache, 128 bytes of each at most, swizzled by as
+// many or not.
+inline bool map_cache(CUtensorMap *map, const void *cache, const Attn &a, int D, int most, bool swizzled) {
+    const int wide = D < 128 ? D : 128, page = 1 << a.log_page;
+    static decltype(&cuTensorMapEncodeTiled) encode = nullptr;
+    static std::once_flag once;
+    std::call_once(once, [] {
+        void *f = nullptr;
+        cudaDriverEntryPointQueryResult found;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &found) == cudaSuccess &&
+            found == cudaDriverEntryPointSuccess)
+            encode = reinterpret_cast<decltype(encode)>(f);
+    });
+    if (!encode) return false;
+    const cuuint64_t rows = (cuuint64_t)a.kv_heads << a.log_page;
+    const cuuint64_t dims[3] = {(cuuint64_t)D, rows, (cuuint64_t)a.pages}, strides[2] = {(cuuint64_t)D, rows * D};
+    const cuuint32_t box[3] = {(cuuint32_t)wide, (cuuint32_t)(page < most ? page : most), 1}, each[3] = {1, 1, 1};
+    return encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void *>(cache), dims, strides, box, each,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, !swizzled ? CU_TENSOR_MAP_SWIZZLE_NONE : wide == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 // A part of one item's keys, for a join of several: log2 of its sum, then its outputs (divided by it).

@@ -22,8 +22,6 @@
 // item leaves its part in the workspace; join_parts_kernel adds them in order.
 #pragma once
 
-#include <mutex>
-
 #include "cache_attn.cuh"
 #include "sm100.cuh"
 
@@ -613,26 +611,6 @@ template <typename T, int D, int kR> __global__ void __launch_bounds__(256) join
     }
 }
 
-// 16 rows of one page and head of a cache, 128 bytes of them at most, swizzled.
-inline bool map_cache(CUtensorMap *map, const void *cache, const Attn &a, int D) {
-    static decltype(&cuTensorMapEncodeTiled) encode = nullptr;
-    static std::once_flag once;
-    std::call_once(once, [] {
-        void *f = nullptr;
-        cudaDriverEntryPointQueryResult found;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &found) == cudaSuccess &&
-            found == cudaDriverEntryPointSuccess)
-            encode = reinterpret_cast<decltype(encode)>(f);
-    });
-    if (!encode) return false;
-    const cuuint64_t rows = (cuuint64_t)a.kv_heads << a.log_page;
-    const cuuint64_t dims[3] = {(cuuint64_t)D, rows, (cuuint64_t)a.pages}, strides[2] = {(cuuint64_t)D, rows * D};
-    const cuuint32_t box[3] = {(cuuint32_t)(D < 128 ? D : 128), 16, 1}, each[3] = {1, 1, 1};
-    return encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void *>(cache), dims, strides, box, each,
-                  CU_TENSOR_MAP_INTERLEAVE_NONE, D == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
-                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 template <typename T, int D, int kCode, int kParts, bool kShaped, int kR>
 int launch_step_kernel(const Attn &a, const StepPlan &plan, bool join, cudaStream_t s) {
     using C = StepConfig<D, kParts, kR>;
@@ -661,7 +639,7 @@ template <int D> int launch_step_d(const Attn &a, int codes, int dtype, void *ws
     StepPlan plan;
     plan.tasks = join ? (int32_t *)ws : nullptr;
     plan.parts = (char *)ws + ((size_t)kSms * 4 * sizeof(int4) + 255) / 256 * 256;
-    if (!map_cache(&plan.maps[0], a.kc, a, D) || !map_cache(&plan.maps[1], a.vc, a, D)) return GDR_ERR_CUDA;
+    if (!map_cache(&plan.maps[0], a.kc, a, D, 16, true) || !map_cache(&plan.maps[1], a.vc, a, D, 16, true)) return GDR_ERR_CUDA;
     const bool shaped = a.softcap > 0.f || a.slopes;
     const bool e4m3 = codes == GDR_CODE_E4M3;
     const bool few = a.max_q * a.group <= 8;

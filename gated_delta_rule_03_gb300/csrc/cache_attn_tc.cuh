@@ -6,12 +6,13 @@
 //
 // Products on the 5th-generation tensor cores in fp16 with fp32 sums in TMEM: scores = Q K^T from shared
 // memory, outputs += W codes with the weights W read from TMEM, where they take their scores' place.
-// Converter warps turn codes into fp16 tiles in the 128-byte-swizzled layout: a tile's row is a token,
-// which is K-major for the first product and MN-major for the second, so that both are written alike.
-// Loads of codes go to registers a tile ahead, as they have to pass through them.
+// Codes come into shared memory by tensor copies, up to 64 keys of a page at a time, and converter warps turn them
+// into fp16 tiles in the 128-byte-swizzled layout: a tile's row is a token, which is K-major for the first product
+// and MN-major for the second, so that both are written alike. (Codes loaded into the converters' registers a tile
+// ahead: 330 us for 4 x 4096 tokens of 16 heads, of which 70 were waits for them.)
 //
-// Roles (448 threads): kTiles groups of 128 threads for the softmax, a row to a thread; the rest of
-// 384 convert; a thread of each of the last two warps issues the products of a row tile. Scores have two buffers, so that the next
+// Roles (480 threads): kTiles groups of 128 threads for the softmax, a row to a thread; the rest of
+// 384 convert; a thread of a warp for each row tile issues its products; a warp issues the copies. Scores have two buffers, so that the next
 // tile's are there when a tile's weights are done. A block stays and goes from item to item: the next
 // item's queries and first keys are on their way while the outputs of the last leave. (A block for each
 // item took 32 thousand cycles more per item, as much as six tiles of 128 keys.)
@@ -30,8 +31,9 @@ namespace cattn {
 
 using namespace sm100;
 
-constexpr int kTcThreads = 448;
+constexpr int kTcThreads = 480;
 constexpr int kRing = 8;   // tiles of scales
+constexpr int kAll = 16 | 16 << 5 | 16 << 10 | 16 << 15;  // rows of a whole tile
 constexpr int kFlush = 4;  // tiles whose outputs are added up in TMEM (fp32)
 
 template <int D, int kParts> struct TcConfig {
@@ -42,17 +44,18 @@ template <int D, int kParts> struct TcConfig {
     static constexpr int kRows = 128 * kTiles;
     static constexpr int kSoft = 128 * kTiles;         // threads
     static constexpr int kConv = 384 - kSoft;
-    // Registers of a thread: 14 warps are launched with 128 each; what the converters give up the softmax
+    // Registers of a thread: 15 warps are launched with 128 each; what the converters give up the softmax
     // gets (kSoft kSoftRegs + kConv kConvRegs = 384 x 128).
-    static constexpr int kConvRegs = 112, kSoftRegs = kTiles == 2 ? 136 : 160;
+    static constexpr int kConvRegs = kTiles == 2 ? 80 : 96, kSoftRegs = kTiles == 2 ? 152 : 192;
     static_assert(kSoft * kSoftRegs + kConv * kConvRegs <= 384 * 128, "registers of the launch");
     static constexpr int kQ = 128 * D * 2;             // bytes of a part of a row tile
     static constexpr int kKv = kKeys * D * 2;          // of a tile of keys or values
-    static constexpr int kStages = D == 256 ? (kParts == 2 ? 1 : 2) : 4;
-    static constexpr int kSmem = kTiles * kParts * kQ + 2 * kStages * kKv + 1024;
+    static constexpr int kStages = D == 256 ? (kParts == 2 ? 1 : 2) : 3;
+    static constexpr int kRaw = D == 256 ? 1 : 3;      // tiles of codes
+    static constexpr int kSmem = kTiles * kParts * kQ + 2 * kStages * kKv + kRaw * kKv + 1024;
     // TMEM columns: scores of two slots per row tile (weights in their place), low parts of weights, outputs
     static constexpr uint32_t kLow = 128, kLowStep = kKeys / 2, kO = 256;
-    static_assert(kSmem <= 232448 - 2048, "shared memory");
+    static_assert(kSmem <= 232448 - 2000, "shared memory");
     static_assert(kO + kTiles * D <= 512 && kTiles * 2 * kKeys + (kParts == 2 ? 2 * kLowStep : 0) <= kO, "TMEM");
 };
 
@@ -230,6 +233,11 @@ __device__ __forceinline__ uint32_t f16_pair(float lo, float hi) {
     return r;
 }
 __device__ __forceinline__ float2 f16_values(uint32_t r) { return __half22float2(reinterpret_cast<const __half2 &>(r)); }
+__device__ __forceinline__ uint4 load16(uint32_t saddr) {
+    uint4 v;
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(saddr) : "memory");
+    return v;
+}
 // Issued where it stands: a load that the compiler may move ends up next to its use.
 __device__ __forceinline__ uint4 ld_nc(const void *p) {
     uint4 v;
@@ -249,16 +257,17 @@ template <int kRegs> __device__ __forceinline__ void set_registers_up() { asm vo
 template <int kRegs> __device__ __forceinline__ void set_registers_down() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs)); }
 
 template <typename T, int D, int kParts, int kMode, int kCode>
-__global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_constant__ Attn a, const __grid_constant__ TcPlan plan) {
+__global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_constant__ Attn a, const __grid_constant__ TcPlan plan, const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map) {
     using C = TcConfig<D, kParts>;
     extern __shared__ unsigned char sm[];
     const uint32_t base = (smem_u32(sm) + 1023u) & ~1023u;
-    const uint32_t sq = base, sk = base + C::kTiles * kParts * C::kQ, sv = sk + C::kStages * C::kKv;
-    __shared__ float4 scales[kRing][8];  // of 16 keys: key scale, log2 and reciprocal of the value scale
+    const uint32_t sq = base, sk = base + C::kTiles * kParts * C::kQ, sv = sk + C::kStages * C::kKv, sr = sv + C::kStages * C::kKv;
+    __shared__ float4 scales[kRing][4];  // of 16 keys: key scale, log2 and reciprocal of the value scale
     __shared__ uint32_t tmem_slot;
     __shared__ int gave_up;
-    // Of the stages of keys and values; of the scores' slots (2 tile + parity of the key tile); per row tile
-    enum { K_FULL = 0, K_FREE = 4, V_FULL = 8, V_FREE = 12, S_FULL = 16, W_FULL = 20, O_DONE = 24, Q_FULL = 28, O_FREE = 30, O_LAST = 32, BARS = 34 };
+    __shared__ int held[kRing];  // 5 bits for each 16 keys: the rows that there are
+    // Of the stages of keys and values, and of their codes (R); of the scores' slots (2 tile + parity of the key tile); per row tile
+    enum { K_FULL = 0, K_FREE = 4, V_FULL = 8, V_FREE = 12, S_FULL = 16, W_FULL = 20, O_DONE = 24, Q_FULL = 28, O_FREE = 30, O_LAST = 32, RK_FULL = 34, RK_FREE = 37, RV_FULL = 40, RV_FREE = 43, BARS = 46 };
     __shared__ __align__(8) uint64_t bars[BARS];
     auto bar = [&](int i) { return smem_u32(&bars[i]); };
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -278,6 +287,12 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_con
             mbar_init(bar(Q_FULL + s), 128);
             mbar_init(bar(O_FREE + s), 128);
             mbar_init(bar(O_LAST + s), 1);
+        }
+        for (int s = 0; s < 3; ++s) {
+            mbar_init(bar(RK_FULL + s), 1);
+            mbar_init(bar(RV_FULL + s), 1);
+            mbar_init(bar(RK_FREE + s), C::kConv / 32);
+            mbar_init(bar(RV_FREE + s), C::kConv / 32);
         }
         fence_mbar_init();
     }
@@ -646,93 +661,53 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_con
         constexpr int kWarpRows = 8 / kBlocks;              // rows of a warp's pass of 512 bytes
         constexpr int kPass = kWarpRows * (C::kConv / 32);  // rows of a pass
         constexpr int kPasses = C::kKeys / kPass;
-        // Eight lanes in turn write 16-byte chunks 2x of two rows, one even and one odd: no two in the same banks.
-        const int x = lane & 3, blk = (lane >> 3) & (kBlocks - 1), row_lo = (lane >> 2) & 1;
-        const int row = cw * kWarpRows + row_lo + 2 * (lane >> (3 + (kBlocks == 4 ? 2 : kBlocks == 2 ? 1 : 0)));
-        const int in_page = (1 << a.log_page) - 1;
-        const uint32_t page_bytes = (uint32_t)(a.kv_heads * (in_page + 1)) * D;
+        // Eight lanes in turn read chunks x of codes and write chunks 2x and 2x + 1 of two rows. In 128-byte-swizzled
+        // rows r and r ^ 5 no two of them meet in a bank, either way; D = 64, whose codes lie in plain rows of 64 bytes,
+        // takes r and r + 1.
+        const int x = lane & 3, blk = (lane >> 3) & (kBlocks - 1), odd = (lane >> 2) & 1;
+        const int pair = kBlocks == 4 ? cw & 3 : (cw & 1) * 2 + (lane >> 4);
+        const int row = kBlocks == 1 ? cw * 8 + odd + 2 * (lane >> 3) : cw / (kBlocks == 4 ? 4 : 2) * 8 + (odd ? pair ^ 5 : pair);
         const uint32_t chunk0 = (uint32_t)((2 * x) ^ (row & 7)) << 4;  // its first 16-byte chunk; the second is one bit away
-        const uint32_t to0 = blk * (C::kKeys * 128) + row * 128;
+        const uint32_t to0 = blk * (C::kKeys * 128) + row * 128, 
+                       from0 = kBlocks == 1 ? row * 64 + x * 16 : (blk >> 1) * (C::kKeys * 128) + row * 128 + (((blk & 1) * 4 + x) ^ (row & 7)) * 16;
         while (fine && get_item<C::kRows, C::kKeys>(a, plan, turn, item)) {
             ++turn;
-            if (!item.count) continue;
-            const int count = item.count, j0 = item.j0, len = item.len;
-            const int64_t lane_at = (int64_t)item.head * (in_page + 1) * D + (row & 15) * D + blk * 64 + x * 16;
-            const uint8_t *const kc = a.kc + lane_at, *const vc = a.vc + lane_at;
-            const int32_t *const table = a.table + (int64_t)item.n * a.width;
-            // Lane g < 8 knows the page of 16 keys of a tile: -1 behind the last token, -2 outside the cache.
-            auto pages_of = [&](int i) {
-                const int tok = (j0 + i) * C::kKeys + (lane & 7) * 16;
-                if (i >= count || (lane & 7) * 16 >= C::kKeys || tok >= len) return -1;
-                const int pg = __ldg(table + (tok >> a.log_page));
-                return pg >= 0 && pg < a.pages ? pg : -2;
-            };
-            auto scales_of = [&](int pg) {
-                if (pg < 0) return make_float2(pg == -1 ? 1.f : __int_as_float(0x7fffffff), pg == -1 ? 1.f : __int_as_float(0x7fffffff));
-                const int64_t at = (int64_t)pg * a.kv_heads + item.head;
-                return make_float2(__ldg(a.ks + at), __ldg(a.vs + at));
-            };
-            // As soon as a pass is converted its registers are loaded again, for the same pass of the next tile.
-            int page_of_pass[kPasses];
-            bool full;
-            auto look_at = [&](int i, int pages) {
-                full = (j0 + i + 1) * C::kKeys <= len && __all_sync(~0u, pages >= 0 || (lane & 7) * 16 >= C::kKeys);
-#pragma unroll
-                for (int ps = 0; ps < kPasses; ++ps)  // (a warp's rows of a pass lie in one of the 16s)
-                    page_of_pass[ps] = __shfl_sync(~0u, pages, (ps * kPass + cw * kWarpRows) >> 4);
-            };
-            auto load = [&](const uint8_t *cache, int tok, int ps) {
-                const int pg = page_of_pass[ps], first = tok + ps * kPass + ((cw * kWarpRows) & ~15);
-                if (full || (pg >= 0 && tok + ps * kPass + row < len))
-                    return ld_nc(cache + (uint64_t)(uint32_t)pg * page_bytes + (first & in_page) * D);
-                return make_uint4(0, 0, 0, 0);
-            };
-            int next = pages_of(0);
-            uint4 k[kPasses], v[kPasses];
-            look_at(0, next);
-#pragma unroll
-            for (int ps = 0; ps < kPasses; ++ps) k[ps] = load(kc, j0 * C::kKeys, ps);
-#pragma unroll
-            for (int ps = 0; ps < kPasses; ++ps) v[ps] = load(vc, j0 * C::kKeys, ps);
-            float2 scale = scales_of(next);
-            next = pages_of(1);
+            const int count = item.count;
 #pragma unroll 1
-            for (int i = 0; i < count; ++i) {
-                const int gi = gi0 + i, st = gi % C::kStages, free = ((gi / C::kStages) & 1) ^ 1;
-                const int tok = (j0 + i + 1) * C::kKeys;  // of the next tile
-                const bool more = i + 1 < count;
-                if (cw == 0 && lane < C::kKeys / 16)
-                    scales[gi % kRing][lane] = make_float4(scale.x, lg2(scale.y), scale.y == scale.y ? __fdividef(1.f, scale.y) : 1.f, 0.f);
-                look_at(i + 1, next);
-                if (cw == 0) scale = scales_of(next);
-                next = pages_of(i + 2);
-                auto convert = [&](uint32_t to, uint4 (&w)[kPasses], const uint8_t *cache) {
+            for (int t = 0; t < 2 * count; ++t) {  // keys and values in turn
+                const int gi = gi0 + (t >> 1), is_v = t & 1, st = gi % C::kStages, raw = gi % C::kRaw;
+                if (!mbar_wait(bar((is_v ? RV_FULL : RK_FULL) + raw), (gi / C::kRaw) & 1) ||
+                    !mbar_wait(bar((is_v ? V_FREE : K_FREE) + st), ((gi / C::kStages) & 1) ^ 1)) {
+                    fine = false;
+                    break;
+                }
+                const uint32_t from = sr + raw * C::kKv + is_v * (C::kKv / 2) + from0, to = (is_v ? sv : sk) + st * C::kKv + to0;
+                uint4 w[kPasses];
+#pragma unroll
+                for (int ps = 0; ps < kPasses; ++ps) w[ps] = load16(from + ps * kPass * (kBlocks == 1 ? 64 : 128));
+                const int rows = held[gi % kRing];
+                if (rows != kAll) {  // places of no token, or of a page that is none
 #pragma unroll
                     for (int ps = 0; ps < kPasses; ++ps) {
-                        uint32_t f[8];
-                        codes::to_f16x4<kCode>(w[ps].x, f[0], f[1]);
-                        codes::to_f16x4<kCode>(w[ps].y, f[2], f[3]);
-                        codes::to_f16x4<kCode>(w[ps].z, f[4], f[5]);
-                        codes::to_f16x4<kCode>(w[ps].w, f[6], f[7]);
-                        // (kPass is a multiple of 8: a thread's rows have one place in the swizzle)
-                        store16(to + ps * kPass * 128 + chunk0, f[0], f[1], f[2], f[3]);
-                        store16(to + ps * kPass * 128 + (chunk0 ^ 16), f[4], f[5], f[6], f[7]);
-                        if (more) w[ps] = load(cache, tok, ps);
+                        const int r = ps * kPass + row;
+                        if ((r & 15) >= ((rows >> (r / 16 * 5)) & 31)) w[ps] = make_uint4(0, 0, 0, 0);
                     }
-                    fence_async_smem();
-                };
-                if (!mbar_wait(bar(K_FREE + st), free)) {
-                    fine = false;
-                    break;
                 }
-                convert(sk + st * C::kKv + to0, k, kc);
-                mbar_arrive(bar(K_FULL + st));
-                if (!mbar_wait(bar(V_FREE + st), free)) {
-                    fine = false;
-                    break;
+#pragma unroll
+                for (int ps = 0; ps < kPasses; ++ps) {
+                    uint32_t f[8];
+                    codes::to_f16x4<kCode>(w[ps].x, f[0], f[1]);
+                    codes::to_f16x4<kCode>(w[ps].y, f[2], f[3]);
+                    codes::to_f16x4<kCode>(w[ps].z, f[4], f[5]);
+                    codes::to_f16x4<kCode>(w[ps].w, f[6], f[7]);
+                    // (kPass is a multiple of 8: a thread's rows have one place in the swizzle)
+                    store16(to + ps * kPass * 128 + chunk0, f[0], f[1], f[2], f[3]);
+                    store16(to + ps * kPass * 128 + (chunk0 ^ 16), f[4], f[5], f[6], f[7]);
                 }
-                convert(sv + st * C::kKv + to0, v, vc);
-                mbar_arrive(bar(V_FULL + st));
+                fence_async_smem();
+                mbar_arrive(bar((is_v ? V_FULL : K_FULL) + st));
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar((is_v ? RV_FREE : RK_FREE) + raw));
             }
             gi0 += count;
         }
@@ -806,6 +781,62 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_con
         }
         // (also after a wait that ran out: what was issued ends before the TMEM goes)
         if (!fine) mbar_wait(bar(O_LAST + tile), (done - 1) & 1);
+    } else if (warp == 12 + C::kTiles) {
+        // ---------------------------------------------------------------- copies
+        const int in_page = (1 << a.log_page) - 1, box = min(C::kKeys, in_page + 1);
+        while (fine && get_item<C::kRows, C::kKeys>(a, plan, turn, item)) {
+            ++turn;
+            const int count = item.count, j0 = item.j0, len = item.len;
+            const int32_t *const table = a.table + (int64_t)item.n * a.width;
+            // Lane g < 4 sees to 16 keys of a tile. Their page: -1 behind the last token, -2 outside the cache.
+            auto page_of = [&](int i) {
+                const int tok = (j0 + i) * C::kKeys + lane * 16;
+                if (i >= count || lane >= 4 || tok >= len) return -1;
+                const int pg = __ldg(table + (tok >> a.log_page));
+                return pg >= 0 && pg < a.pages ? pg : -2;
+            };
+            auto scale_of = [&](int pg) {
+                if (pg < 0) return make_float2(pg == -1 ? 1.f : __int_as_float(0x7fffffff), pg == -1 ? 1.f : __int_as_float(0x7fffffff));
+                const int64_t at = (int64_t)pg * a.kv_heads + item.head;
+                return make_float2(__ldg(a.ks + at), __ldg(a.vs + at));
+            };
+            int page = page_of(0), next = page_of(1);
+            float2 scale = scale_of(page);
+#pragma unroll 1
+            for (int i = 0; i < count && fine; ++i) {
+                const int gi = gi0 + i, raw = gi % C::kRaw, tok = (j0 + i) * C::kKeys + lane * 16;
+                const float2 coming = scale_of(next);
+                const int later = page_of(i + 2);
+                const int rows = page >= 0 ? min(16, len - tok) : 0;
+                const int all = __shfl_sync(~0u, rows, 0) | __shfl_sync(~0u, rows, 1) << 5 | __shfl_sync(~0u, rows, 2) << 10 | __shfl_sync(~0u, rows, 3) << 15;
+                // a copy brings as many rows as a page and a tile have in common, all of one page
+                const bool copies = rows > 0 && lane * 16 % box == 0;
+                const int boxes = __popc(__ballot_sync(~0u, copies));
+                if (lane < 4)
+                    scales[gi % kRing][lane] = make_float4(scale.x, lg2(scale.y), scale.y == scale.y ? __fdividef(1.f, scale.y) : 1.f, 0.f);
+                if (lane == 0) held[gi % kRing] = all;
+                __syncwarp();
+#pragma unroll 1
+                for (int is_v = 0; is_v < 2; ++is_v) {
+                    const uint32_t full = bar((is_v ? RV_FULL : RK_FULL) + raw);
+                    if (!mbar_wait(bar((is_v ? RV_FREE : RK_FREE) + raw), ((gi / C::kRaw) & 1) ^ 1)) fine = false;
+                    fine = __all_sync(~0u, fine);
+                    if (!fine) break;
+                    if (lane == 0) mbar_arrive_expect_tx(full, boxes * box * D);
+                    __syncwarp();
+                    if (copies) {
+                        const int at = item.head * (in_page + 1) + (tok & in_page);
+                        const uint32_t to = sr + raw * C::kKv + is_v * (C::kKv / 2) + lane * 16 * (D < 128 ? D : 128);
+#pragma unroll
+                        for (int x = 0; x < D; x += 128) tma_load_3d(to + x * C::kKeys, is_v ? &v_map : &k_map, full, x, at, page);
+                    }
+                }
+                page = next;
+                next = later;
+                scale = coming;
+            }
+            gi0 += count;
+        }
     }
     if (!fine) gave_up = 1;
     tc_fence_before();
@@ -897,7 +928,9 @@ template <typename T, int D, int kParts, int kMode> int launch_tc_kernel(const A
     const auto kernel = codes == GDR_CODE_E4M3 ? attn_tc_kernel<T, D, kParts, kMode, GDR_CODE_E4M3> : attn_tc_kernel<T, D, kParts, kMode, GDR_CODE_INT8>;
     if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem) != cudaSuccess) return GDR_ERR_CUDA;
     const int64_t items = plan.tiles * a.kv_heads * plan.splits;
-    kernel<<<(unsigned)(items < 152 ? items : 152), kTcThreads, C::kSmem, s>>>(a, plan);
+    CUtensorMap maps[2];
+    if (!map_cache(&maps[0], a.kc, a, D, C::kKeys, D >= 128) || !map_cache(&maps[1], a.vc, a, D, C::kKeys, D >= 128)) return GDR_ERR_CUDA;
+    kernel<<<(unsigned)(items < 152 ? items : 152), kTcThreads, C::kSmem, s>>>(a, plan, maps[0], maps[1]);
     if (cudaGetLastError() != cudaSuccess) return GDR_ERR_CUDA;
     if (plan.splits > 1)
         join_splits_kernel<T, D, kParts><<<(unsigned)((a.tokens * a.heads + 7) / 8), 256, 0, s>>>(a, plan);

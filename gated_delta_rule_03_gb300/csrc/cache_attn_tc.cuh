@@ -477,88 +477,42 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_con
                 const float4 *const sc = scales[gi % kRing];
                 const bool edge = tok + C::kKeys > sure;
 
-                // Weights with the row's reference as it is, 16 keys at a time, kept in registers until it is known that
-                // none is too large. Else, and for the first tile and those that some row sees in part, slowly: the
-                // largest exponent first, the reference moved with the outputs so far, then the weights. (A row that
-                // sees no key of the first tile sees no later ones.)
-                auto shape_of = [&](int g) {
-                    const float4 f = sc[g];
-                    return Shape<kMode, kParts == 2>(f.x * up2, f.y - ref, cap, inv_cap, slope, (float)(p - tok - 16 * g));
-                };
-                bool slow = i == 0 || edge;
-                if (!slow) {
-                    uint32_t hi[C::kKeys / 2], lo[kParts == 2 ? C::kKeys / 2 : 1];
-                    float2 all = make_float2(0.f, 0.f);
-                    float top = -INFINITY;
-                    uint32_t x[4][16];
-                    tmem_fetch16(s_at, x[0]);
-                    tmem_fetch16(s_at + 16, x[1]);
+                // Exponents of all weights first, relative to the row's reference: the first tile, or one that is too large,
+                // moves the reference, and the outputs so far with it. (A row that sees no key of the first tile sees
+                // no later ones.)
+                float2 t[C::kKeys / 2];
+                {
+                    uint32_t x[C::kKeys / 16][16];
+#pragma unroll
+                    for (int g = 0; g < C::kKeys / 16; ++g) tmem_fetch16(s_at + 16 * g, x[g]);
 #pragma unroll
                     for (int g = 0; g < C::kKeys / 16; ++g) {
-                        uint32_t(&y)[16] = x[g & 3];
-                        if (g % 2 == 0) {
-                            tmem_arrive16(y);
-                            tmem_arrive16(x[(g + 1) & 3]);
-                            if (g + 2 < C::kKeys / 16) {
-                                tmem_fetch16(s_at + 16 * (g + 2), x[(g + 2) & 3]);
-                                tmem_fetch16(s_at + 16 * (g + 3), x[(g + 3) & 3]);
-                            }
-                        }
-                        const auto shape = shape_of(g);
-                        float2 some = make_float2(0.f, 0.f);
+                        tmem_arrive16(x[g]);
+                        const float4 f = sc[g];
+                        const Shape<kMode, kParts == 2> shape(f.x * up2, f.y - ref, cap, inv_cap, slope, (float)(p - tok - 16 * g));
 #pragma unroll
-                        for (int e = 0; e < 16; e += 2) {
-                            float2 w = shape(make_float2(__uint_as_float(y[e]), __uint_as_float(y[e + 1])), e);
-                            top = fmaxf(top, fmaxf(w.x, w.y));
-                            w.x = ex2(w.x);
-                            w.y = ex2(w.y);
-                            some = add2(some, w);
-                            const int q = 8 * g + e / 2;
-                            hi[q] = f16_pair(w.x, w.y);
-                            if (kParts == 2) {
-                                const float2 v = f16_values(hi[q]);
-                                lo[q] = f16_pair(w.x - v.x, w.y - v.y);
-                            }
-                        }
-                        const float rv = sc[g].z;
-                        all = fma2(some, make_float2(rv, rv), all);
-                    }
-                    slow = __any_sync(~0u, top > kSpan + kSlack);
-                    if (!slow) {
-                        l += all.x + all.y;
-#pragma unroll
-                        for (int c = 0; c < C::kKeys / 2; c += 16) {
-                            tmem_put16(s_at + c, hi + c);
-                            if constexpr (kParts == 2) tmem_put16(tmem + lanes + C::kLow + (gi & 1) * C::kLowStep + c, lo + c);
-                        }
+                        for (int e = 0; e < 16; e += 2)
+                            t[8 * g + e / 2] = shape(make_float2(__uint_as_float(x[g][e]), __uint_as_float(x[g][e + 1])), e);
                     }
                 }
-                if (slow) {
-                    float top = -INFINITY;
-                    auto exponents = [&](int g, float (&t)[16]) {
-                        uint32_t y[16];
-                        tmem_fetch16(s_at + 16 * g, y);
-                        tmem_arrive16(y);
-                        const auto shape = shape_of(g);
+                if (edge) {
 #pragma unroll
-                        for (int e = 0; e < 16; e += 2) {
-                            const float2 w = shape(make_float2(__uint_as_float(y[e]), __uint_as_float(y[e + 1])), e);
-                            const int j = tok + 16 * g + e;
-                            t[e] = j < lim ? w.x : -INFINITY;
-                            t[e + 1] = j + 1 < lim ? w.y : -INFINITY;
-                        }
-                    };
-#pragma unroll 1
-                    for (int g = 0; g < C::kKeys / 16; ++g) {
-                        float t[16];
-                        exponents(g, t);
-#pragma unroll
-                        for (int e = 0; e < 16; ++e) top = fmaxf(top, t[e]);
+                    for (int e = 0; e < C::kKeys; e += 2) {
+                        if (tok + e >= lim) t[e / 2].x = -INFINITY;
+                        if (tok + e + 1 >= lim) t[e / 2].y = -INFINITY;
                     }
-                    const bool move = i == 0 ? top > -INFINITY : top > kSpan + kSlack;
-                    if (move) ref += top - kSpan;
-                    if (i > 0 && __any_sync(~0u, move)) {
-                        const float by = move ? ex2(kSpan - top) : 1.f;
+                }
+                float top = -INFINITY;
+#pragma unroll
+                for (int e = 0; e < C::kKeys / 2; ++e) top = fmaxf(top, fmaxf(t[e].x, t[e].y));
+                const bool move = i == 0 ? top > -INFINITY : top > kSpan + kSlack;
+                if (__any_sync(~0u, move)) {
+                    const float up = move ? top - kSpan : 0.f;
+                    ref += up;
+#pragma unroll
+                    for (int e = 0; e < C::kKeys / 2; ++e) t[e] = add2(t[e], make_float2(-up, -up));
+                    if (i > 0) {
+                        const float by = ex2(-up);
                         l *= by;
                         if (!anew) {
                             outputs_done();
@@ -573,28 +527,29 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_con
                             }
                         }
                     }
-#pragma unroll 1
-                    for (int g = 0; g < C::kKeys / 16; ++g) {
-                        float t[16];
-                        uint32_t hi[8], lo[8];
-                        exponents(g, t);
-                        float some = 0.f;
+                }
+                // the weights, in the scores' place
 #pragma unroll
-                        for (int e = 0; e < 16; e += 2) {
-                            const float w0 = ex2(t[e]), w1 = ex2(t[e + 1]);
-                            some += w0 + w1;
-                            hi[e / 2] = f16_pair(w0, w1);
-                            const float2 v = f16_values(hi[e / 2]);
-                            lo[e / 2] = f16_pair(w0 - v.x, w1 - v.y);
+                for (int c = 0; c < C::kKeys / 2; c += 16) {
+                    uint32_t hi[16], lo[kParts == 2 ? 16 : 1];
+                    float2 some[2];
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) {
+                        const float2 w = make_float2(ex2(t[c + e].x), ex2(t[c + e].y));
+                        some[e / 8] = e % 8 ? add2(some[e / 8], w) : w;
+                        hi[e] = f16_pair(w.x, w.y);
+                        if (kParts == 2) {
+                            const float2 v = f16_values(hi[e]);
+                            lo[e] = f16_pair(w.x - v.x, w.y - v.y);
                         }
-                        l = fmaf(some, sc[g].z, l);
-                        // (in the scores' place: columns 8g .. 8g + 7, which have been read)
-                        tmem_put8(s_at + 8 * g, hi);
-                        if (kParts == 2) tmem_put8(tmem + lanes + C::kLow + (gi & 1) * C::kLowStep + 8 * g, lo);
                     }
+                    tmem_put16(s_at + c, hi);
+                    if constexpr (kParts == 2) tmem_put16(tmem + lanes + C::kLow + (gi & 1) * C::kLowStep + c, lo);
+                    l = fmaf(some[0].x + some[0].y, sc[c / 8].z, l);
+                    l = fmaf(some[1].x + some[1].y, sc[c / 8 + 1].z, l);
                 }
                 tmem_stored();
-    tc_fence_before();
+                tc_fence_before();
                 mbar_arrive(bar(W_FULL + slot));
             }
             gi0 += count;

@@ -37,8 +37,12 @@ struct Attn {
     int32_t *status;
     int64_t num_seqs, tokens, max_q, width, qs, pages;
     int heads, kv_heads, group, log_page, causal;
+    int group_shift;  // log2 of group, -1 if it is no power of two
     float scale, softcap;
 };
+
+// Token of row r of a head of the cache, and its head in the group.
+__device__ __forceinline__ int token_of(const Attn &a, int r) { return a.group_shift >= 0 ? r >> a.group_shift : r / a.group; }
 
 // New tokens of request n: the first row and their number.
 __device__ __forceinline__ int2 rows_of(const Attn &a, int64_t n) {

@@ -41,6 +41,9 @@ int check_shape(const gdr_cache_attn_shape *s, Call *c) {
     a.kv_heads = s->cache.kv_heads;
     a.group = s->heads / s->cache.kv_heads;
     a.causal = s->causal != 0;
+    a.group_shift = -1;
+    for (int i = 0; i < 17; ++i)
+        if (a.group == 1 << i) a.group_shift = i;
     if (a.max_q > (INT32_MAX - 256) / a.group) return GDR_ERR_INVALID_ARG;  // (rows of an item are 32-bit numbers)
     a.scale = s->scale;
     a.softcap = s->softcap;

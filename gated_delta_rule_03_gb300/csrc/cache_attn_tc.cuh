@@ -145,7 +145,7 @@ template <int kRows, int kKeys> __device__ __forceinline__ bool get_item(const A
     t.row0 = (int)(tile * kRows);
     t.rows = left <= 0 ? 0 : (int)(left < kRows ? left : kRows);
     // keys that the last row sees, and this split's tiles of them
-    const int far = a.causal ? max(0, min(t.len, t.past + (t.row0 + t.rows - 1) / a.group + 1)) : t.len;
+    const int far = a.causal ? max(0, min(t.len, t.past + token_of(a, t.row0 + t.rows - 1) + 1)) : t.len;
     const int all = t.rows ? (far + kKeys - 1) / kKeys : 0, per = (all + plan.splits - 1) / plan.splits;
     t.j0 = min(all, split * per);
     t.count = min(all, t.j0 + per) - t.j0;
@@ -323,12 +323,12 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_con
         const float cap = kMode == kPlain ? 0.f : a.softcap, inv_cap = cap > 0.f ? 1.f / cap : 0.f;
         using P = TcPart<C::kRows, D>;
         auto row_of = [&](const TcItem &t) {
-            const int at = t.row0 + tid;
-            return (int64_t)(t.first + at / a.group) * a.heads + t.head * a.group + at % a.group;
+            const int at = t.row0 + tid, token = token_of(a, at);
+            return (int64_t)(t.first + token) * a.heads + t.head * a.group + at - token * a.group;
         };
         auto query_of = [&](const TcItem &t) {
-            const int at = t.row0 + tid;
-            return (const T *)a.q + (int64_t)(t.first + at / a.group) * a.qs + (int64_t)(t.head * a.group + at % a.group) * D;
+            const int at = t.row0 + tid, token = token_of(a, at);
+            return (const T *)a.q + (int64_t)(t.first + token) * a.qs + (int64_t)(t.head * a.group + at - token * a.group) * D;
         };
         // The next item that has keys to look at; those before it that have none get their zeros.
         auto next_item = [&](TcItem &t) {
@@ -412,13 +412,13 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_con
         float row_up = have ? put_queries(item) : 0.f;
         for (int done = 0; have && fine; ++done) {
             const int at = item.row0 + tid;
-            const int p = item.past + at / a.group, lim = a.causal ? min(item.len, p + 1) : item.len;
-            const int sure = a.causal ? min(item.len, item.past + (item.row0 + tile * 128) / a.group + 1) : item.len;
+            const int p = item.past + token_of(a, at), lim = a.causal ? min(item.len, p + 1) : item.len;
+            const int sure = a.causal ? min(item.len, item.past + token_of(a, item.row0 + tile * 128) + 1) : item.len;
             const bool live = tid < item.rows;
             const int64_t row = row_of(item);
             P *const part = (P *)plan.parts + item.part;
             float *const row_out = plan.splits > 1 ? part->o[tid] : (float *)a.o + row * D;  // (fp32 only without splits)
-            const float slope = kMode == kBiased && a.slopes && live ? __ldg(a.slopes + item.head * a.group + at % a.group) : 0.f;
+            const float slope = kMode == kBiased && a.slopes && live ? __ldg(a.slopes + item.head * a.group + at - token_of(a, at) * a.group) : 0.f;
             const float up2 = row_up * (kMode == kPlain ? kLog2e : 1.f);
             float ref = 0.f, l = 0.f;
             float sum_ref = 0.f, sum_l = 0.f;  // kParts == 2: of what has left TMEM
@@ -502,9 +502,10 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_con
                         if (tok + e + 1 >= lim) t[e / 2].y = -INFINITY;
                     }
                 }
-                float top = -INFINITY;
+                float tops[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                for (int e = 0; e < C::kKeys / 2; ++e) top = fmaxf(top, fmaxf(t[e].x, t[e].y));
+                for (int e = 0; e < C::kKeys / 2; ++e) tops[e & 3] = fmaxf(tops[e & 3], fmaxf(t[e].x, t[e].y));
+                const float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
                 const bool move = i == 0 ? top > -INFINITY : top > kSpan + kSlack;
                 if (__any_sync(~0u, move)) {
                     const float up = move ? top - kSpan : 0.f;
@@ -553,13 +554,16 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_con
                 mbar_arrive(bar(W_FULL + slot));
             }
             gi0 += count;
-            if (fine) fine = mbar_wait(bar(O_LAST + tile), done & 1);
-            __syncwarp();
-            tc_fence_after();
-            // ---- the next item's queries (the products with the last ones are done), then the results. A warp reads its
-            // lanes together, whichever rows are live.
+            // ---- the next item's queries (the scores of the last tile are there, and were the last to need these), then the
+            // results. A warp reads its lanes together, whichever rows are live.
             if (!__all_sync(~0u, fine)) break;
             if (have) row_up = put_queries(then);
+            fine = mbar_wait(bar(O_LAST + tile), done & 1);
+            if (!__all_sync(~0u, fine)) {
+                fine = false;
+                break;
+            }
+            tc_fence_after();
             const float by = kParts == 2 ? ex2(sum_ref - ref) : 0.f;
             const bool older = kParts == 2 && sum_l != 0.f;
             if (older) l = fmaf(sum_l, by, l);
@@ -586,7 +590,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_con
                     }
                 }
 #pragma unroll
-                for (int e = 0; e < 32; ++e) v[e] = some ? v[e] * inv : 0.f;
+                for (int e = 0; e < 32; ++e) v[e] *= inv;
                 if (plan.splits > 1 || sizeof(T) == 4) {
 #pragma unroll
                     for (int e = 0; e < 32; e += 4) *(float4 *)(row_out + c + e) = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);

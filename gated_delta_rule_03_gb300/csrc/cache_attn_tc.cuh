@@ -216,14 +216,33 @@ template <int kMode, bool kExact> struct Shape {
         if (kMode == kBiased) z = fmaf(-slope, fabsf(away - (float)e), z);
         return fmaf(z, kLog2e, off);
     }
-    __device__ __forceinline__ float2 operator()(float2 z, int e) const {
-        if (kMode == kPlain) return fma2(z, make_float2(m, m), make_float2(off, off));
-        if (kMode == kCapped && !kExact) {
-            float2 x = mul2(z, make_float2(m, m));
-            x = add2(make_float2(ex2(x.x), ex2(x.y)), make_float2(1.f, 1.f));
-            return fma2(make_float2(rcp(x.x), rcp(x.y)), make_float2(k, k), make_float2(off, off));
+    // Keys e .. e + 3.
+    __device__ __forceinline__ void operator()(const uint32_t *bits, int e, float2 &t0, float2 &t1) const {
+        const float2 z0 = make_float2(__uint_as_float(bits[0]), __uint_as_float(bits[1]));
+        const float2 z1 = make_float2(__uint_as_float(bits[2]), __uint_as_float(bits[3]));
+        if (kMode == kPlain) {
+            t0 = fma2(z0, make_float2(m, m), make_float2(off, off));
+            t1 = fma2(z1, make_float2(m, m), make_float2(off, off));
+        } else if (kMode == kCapped && !kExact) {
+            // four reciprocals from one (the special functions bound capped scores: 12 cycles of theirs a key with one
+            // each, 6 so): exponents are held below 30, where tanh is 1, so that no product overflows
+            const float2 x0 = mul2(z0, make_float2(m, m)), x1 = mul2(z1, make_float2(m, m));
+            const float2 a = add2(make_float2(ex2(below(x0.x)), ex2(below(x1.x))), make_float2(1.f, 1.f));
+            const float2 b = add2(make_float2(ex2(below(x0.y)), ex2(below(x1.y))), make_float2(1.f, 1.f));
+            const float2 ab = mul2(a, b);
+            const float r = rcp(ab.x * ab.y);
+            const float2 q = mul2(make_float2(r, r), make_float2(ab.y, ab.x));  // reciprocals of ab
+            t0 = fma2(mul2(make_float2(q.x, q.x), make_float2(b.x, a.x)), make_float2(k, k), make_float2(off, off));
+            t1 = fma2(mul2(make_float2(q.y, q.y), make_float2(b.y, a.y)), make_float2(k, k), make_float2(off, off));
+        } else {
+            t0 = make_float2(one(z0.x, e), one(z0.y, e + 1));
+            t1 = make_float2(one(z1.x, e + 2), one(z1.y, e + 3));
         }
-        return make_float2(one(z.x, e), one(z.y, e + 1));
+    }
+    static __device__ __forceinline__ float below(float x) {  // (NaN stays NaN)
+        float y;
+        asm("min.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(x), "f"(30.f));
+        return y;
     }
 };
 
@@ -491,8 +510,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_con
                         const float4 f = sc[g];
                         const Shape<kMode, kParts == 2> shape(f.x * up2, f.y - ref, cap, inv_cap, slope, (float)(p - tok - 16 * g));
 #pragma unroll
-                        for (int e = 0; e < 16; e += 2)
-                            t[8 * g + e / 2] = shape(make_float2(__uint_as_float(x[g][e]), __uint_as_float(x[g][e + 1])), e);
+                        for (int e = 0; e < 16; e += 4) shape(x[g] + e, e, t[8 * g + e / 2], t[8 * g + e / 2 + 1]);
                     }
                 }
                 if (edge) {

@@ -77,7 +77,7 @@ def _checked_plan(block_table, kv_lens, free_pages, free_count, q_lens, rows, pa
     for t, name, size in zip(outs, ("kv_lens_out", "free_count_out", "cu_q", "start", "positions", "slots"), sizes):
         if t is not None:
             dense(t, name, i32, dev, (size,))
-    return ctypes.byref(PageShape(n, width, rows, free_pages.shape.numel(), page)), sizes, all(t is None for t in outs)
+    return ctypes.byref(PageShape(n, width, rows, free_pages.shape.numel(), page)), sizes
 
 
 def page_plan(block_table, kv_lens, free_pages, free_count, page, q_lens=None, rows=None, kv_lens_out=None,
@@ -86,18 +86,15 @@ def page_plan(block_table, kv_lens, free_pages, free_count, page, q_lens=None, r
     [num_seqs, width], kv_lens [num_seqs], free_pages [num_pages] and free_count [1] int32; q_lens
     [num_seqs] int32 or None for one token each; rows: tokens of the packed batch, padding included
     (default num_seqs; needed with q_lens). The table gets its new entries in place. Returns a
-    PagePlan (kv_lens, free_count, cu_q, start, positions, slots) of new tensors (parts of one) or those
+    PagePlan (kv_lens, free_count, cu_q, start, positions, slots) of new tensors or those
     given; kv_lens_out may be kv_lens and free_count_out may be free_count. start is -1 for a refused request."""
     lib = ops._load()
     outs = (kv_lens_out, free_count_out, cu_q, start, positions, slots)
-    shape, sizes, fresh = _checked_plan(
+    shape, sizes = _checked_plan(
         describe(block_table, "block_table"), describe(kv_lens, "kv_lens"), describe(free_pages, "free_pages"),
         describe(free_count, "free_count"), _opt(q_lens, "q_lens"), None if rows is None else int(rows), int(page),
-        tuple(None if t is None else describe(t, "an output") for t in outs))
-    if fresh:
-        outs = new_like(kv_lens, stream, (sum(sizes),)).split_with_sizes(sizes)
-    else:
-        outs = [new_like(kv_lens, stream, (n,)) if t is None else t for t, n in zip(outs, sizes)]
+        tuple([None if t is None else describe(t, "an output") for t in outs]))
+    outs = [new_like(kv_lens, stream, (n,)) if t is None else t for t, n in zip(outs, sizes)]
     _launch(lib.gdr_page_plan, "gdr_page_plan", kv_lens.device, stream, shape, _addr(q_lens), kv_lens.data_ptr(),
             free_pages.data_ptr(), free_count.data_ptr(), block_table.data_ptr(), *[t.data_ptr() for t in outs])
     return PagePlan(*outs)

@@ -8,14 +8,16 @@ import collections
 
 import torch
 
+empty = torch.empty
 Described = collections.namedtuple("Described", "dtype shape stride device")
 
 
 def describe(t, name):
     """A plain tuple, half the time of the named one, which `named` makes of it."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    return t.dtype, t.shape, t.stride(), t.device
+    try:
+        return t.dtype, t.shape, t.stride(), t.device
+    except AttributeError:
+        raise TypeError(f"{name} must be a torch.Tensor") from None
 
 
 def named(*descriptions):
@@ -74,6 +76,6 @@ def rows_stride(t, name, dtype, device, tokens):
 def new_like(t, stream, shape=None, dtype=None):
     """A dense tensor to be written on `stream`: memory of that stream."""
     if stream is None:
-        return torch.empty(t.shape if shape is None else shape, dtype=dtype or t.dtype, device=t.device)
+        return empty(t.shape if shape is None else shape, dtype=dtype or t.dtype, device=t.device)
     with torch.cuda.stream(stream):
-        return torch.empty(t.shape if shape is None else shape, dtype=dtype or t.dtype, device=t.device)
+        return empty(t.shape if shape is None else shape, dtype=dtype or t.dtype, device=t.device)

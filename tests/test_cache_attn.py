@@ -161,6 +161,39 @@ def test_a_long_cache(new):
 
 
 @gpu
+@pytest.mark.parametrize("dtype", [BF16, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_keys_of_few_rows_are_shared_out(d, dtype):
+    """A long cache that many blocks work on for one request, a short one beside it, one without new tokens and one
+    without cached ones; for a few rows and for many."""
+    for new in ([1, 1, 0, 1], [40, 3, 0, 2]):
+        c = make(new, [9000, 70, 500, 0], 6, 2, d, 128, dtype, INT8, seed=11, behind=1)
+        check(c)
+        check(c, softcap=3.0, slopes=torch.full((6,), 0.01, device="cuda"))
+
+
+@gpu
+@pytest.mark.parametrize("dtype", [BF16, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_more_items_than_the_gpu_has_blocks(d, dtype):
+    """Blocks go from item to item: of several tiles of rows, of few and of none."""
+    c = make([300, 0, 17, 1, 129], [350, 40, 17, 900, 200], 64, 32, d, 16, dtype, E4M3, seed=12, behind=2)
+    check(c)
+    c = make([3, 1, 2] * 20, [50, 0, 300] * 20, 32, 32, d, 32, dtype, E4M3, seed=13)
+    check(c)
+
+
+@gpu
+def test_calls_without_rows():
+    from gated_delta_rule_03_gb300 import cache_attn
+    c = make([0, 0], [30, 0], 4, 2, 64, 16, BF16, E4M3)
+    for cu in (c["cu"], None):
+        o, lse = cache_attn(c["q"], c["kc"], c["vc"], c["ks"], c["vs"], c["table"], c["kv"], cu_q=cu, return_lse=True)
+        torch.cuda.synchronize()
+        assert o.shape == (0, 4, 64) and lse.shape == (0, 4)
+
+
+@gpu
 @pytest.mark.parametrize("new", [1, 90])
 def test_a_cache_behind_two_to_the_31_bytes(new):
     from gated_delta_rule_03_gb300 import cache_attn

@@ -203,6 +203,8 @@ def _checked_attn(q, caches, block_table, kv_lens, cu_q, slopes, o, lse, max_q, 
         dense(o, "o", dtype, dev, q.shape)
     if lse is not None:
         dense(lse, "lse", torch.float32, dev, (T, heads))
+    if cu_q is None and n:
+        max_q = T // n  # (T that n does not divide is refused)
     return _attn_call(cache, (n, T, T if max_q is None else max_q, width, qs, heads, causal, d ** -0.5 if scale is None else scale,
                               softcap))
 

@@ -27,6 +27,7 @@ int check_shape(const gdr_cache_attn_shape *s, Call *c) {
     if (s->max_q < 0 || s->max_q > INT32_MAX || s->width < 1 || s->width > INT32_MAX / s->cache.page) return GDR_ERR_INVALID_ARG;
     if (s->heads < 1 || s->heads > 1 << 16 || s->heads % s->cache.kv_heads) return GDR_ERR_INVALID_ARG;
     if (!isfinite(s->scale) || !isfinite(s->softcap) || s->softcap < 0.f) return GDR_ERR_INVALID_ARG;
+    if (s->softcap > 0.f && s->softcap < 1e-18f) return GDR_ERR_INVALID_ARG;  // (its reciprocal is used)
     c->d = s->cache.d;
     c->codes = s->cache.codes;
     c->dtype = s->cache.dtype;
@@ -87,6 +88,7 @@ int gdr_cache_attn(const gdr_cache_attn_shape *shape, const void *q, const void 
     if (st != GDR_OK) return st;
     Attn &a = c.a;
     if (!cu_q && a.tokens % a.num_seqs) return GDR_ERR_INVALID_ARG;
+    if (!cu_q) a.max_q = a.tokens / a.num_seqs;
     if (!workspace) return GDR_ERR_WORKSPACE;
     const size_t need = workspace_bytes(c);
     if (workspace_bytes_given < need) return GDR_ERR_WORKSPACE;
@@ -121,7 +123,6 @@ int gdr_cache_attn(const gdr_cache_attn_shape *shape, const void *q, const void 
     a.o = o;
     a.lse = lse;
     a.status = (int32_t *)workspace;
-    if (!cu_q) a.max_q = a.tokens / a.num_seqs;
     void *const ws = (char *)workspace + kHead;
     const cudaStream_t s = (cudaStream_t)stream;
     if (few_rows(a))

@@ -342,7 +342,7 @@ def test_refusals_on_the_host():
         return lib.gdr_cache_attn(s, *args, size(s) if ws_bytes is None else ws_bytes, None)
 
     for kw in (dict(num_pages=0), dict(kv_heads=0), dict(heads=5), dict(heads=0), dict(num_seqs=0), dict(total_tokens=-1), dict(max_q=-1), dict(width=0),
-               dict(scale=math.inf), dict(softcap=-1.0), dict(softcap=math.nan), dict(q_stride=128)):
+               dict(scale=math.inf), dict(softcap=-1.0), dict(softcap=1e-20), dict(softcap=math.nan), dict(q_stride=128)):
         assert size(shape(**kw)) == 0 and call(1 << 40, **kw) == -1, kw
     for kw in (dict(page=8), dict(d=96), dict(codes=2), dict(dtype=5)):
         assert size(shape(**kw)) == 0 and call(1 << 40, **kw) == -2, kw

@@ -31,7 +31,7 @@ namespace cattn {
 
 using namespace sm100;
 
-constexpr int kTcThreads = 480;
+constexpr int kTcThreads = 480, kTcRegs = 128;
 constexpr int kRing = 8;   // tiles of scales
 constexpr int kAll = 16 | 16 << 5 | 16 << 10 | 16 << 15;  // rows of a whole tile
 constexpr int kFlush = 4;  // tiles whose outputs are added up in TMEM (fp32)
@@ -44,10 +44,10 @@ template <int D, int kParts> struct TcConfig {
     static constexpr int kRows = 128 * kTiles;
     static constexpr int kSoft = 128 * kTiles;         // threads
     static constexpr int kConv = 384 - kSoft;
-    // Registers of a thread: 15 warps are launched with 128 each; what the converters give up the softmax
-    // gets (kSoft kSoftRegs + kConv kConvRegs = 384 x 128).
+    // Registers of a thread: 15 warps are launched with kTcRegs each; what the converters give up the softmax
+    // gets (kSoft kSoftRegs + kConv kConvRegs = 384 x kTcRegs).
     static constexpr int kConvRegs = kTiles == 2 ? 80 : 96, kSoftRegs = kTiles == 2 ? 152 : 192;
-    static_assert(kSoft * kSoftRegs + kConv * kConvRegs <= 384 * 128, "registers of the launch");
+    static_assert(kSoft * kSoftRegs + kConv * kConvRegs <= 384 * kTcRegs, "registers of the launch");
     static constexpr int kQ = 128 * D * 2;             // bytes of a part of a row tile
     static constexpr int kKv = kKeys * D * 2;          // of a tile of keys or values
     static constexpr int kStages = D == 256 ? (kParts == 2 ? 1 : 2) : 3;
@@ -903,6 +903,9 @@ template <typename T, int D, int kParts, int kMode> int launch_tc_kernel(const A
     TcPlan plan = tc_plan<D, kParts>(a, a.cu != nullptr);
     plan.parts = (char *)ws;
     const auto kernel = codes == GDR_CODE_E4M3 ? attn_tc_kernel<T, D, kParts, kMode, GDR_CODE_E4M3> : attn_tc_kernel<T, D, kParts, kMode, GDR_CODE_INT8>;
+    // The roles' shares of registers add up to what the block is launched with, if the compiler gave it that many.
+    cudaFuncAttributes attr;
+    if (cudaFuncGetAttributes(&attr, kernel) != cudaSuccess || attr.numRegs != kTcRegs) return GDR_ERR_CUDA;
     if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem) != cudaSuccess) return GDR_ERR_CUDA;
     const int64_t items = plan.tiles * a.kv_heads * plan.splits;
     CUtensorMap maps[2];

@@ -500,36 +500,37 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_con
                 // moves the reference, and the outputs so far with it. (A row that sees no key of the first tile sees
                 // no later ones.)
                 float2 t[C::kKeys / 2];
-                {
-                    uint32_t x[C::kKeys / 16][16];
+#pragma unroll 1
+                for (bool again = i > 0;;) {
+                    {
+                        uint32_t x[C::kKeys / 16][16];
 #pragma unroll
-                    for (int g = 0; g < C::kKeys / 16; ++g) tmem_fetch16(s_at + 16 * g, x[g]);
+                        for (int g = 0; g < C::kKeys / 16; ++g) tmem_fetch16(s_at + 16 * g, x[g]);
 #pragma unroll
-                    for (int g = 0; g < C::kKeys / 16; ++g) {
-                        tmem_arrive16(x[g]);
-                        const float4 f = sc[g];
-                        const Shape<kMode, kParts == 2> shape(f.x * up2, f.y - ref, cap, inv_cap, slope, (float)(p - tok - 16 * g));
+                        for (int g = 0; g < C::kKeys / 16; ++g) {
+                            tmem_arrive16(x[g]);
+                            const float4 f = sc[g];
+                            const Shape<kMode, kParts == 2> shape(f.x * up2, f.y - ref, cap, inv_cap, slope, (float)(p - tok - 16 * g));
 #pragma unroll
-                        for (int e = 0; e < 16; e += 4) shape(x[g] + e, e, t[8 * g + e / 2], t[8 * g + e / 2 + 1]);
+                            for (int e = 0; e < 16; e += 4) shape(x[g] + e, e, t[8 * g + e / 2], t[8 * g + e / 2 + 1]);
+                        }
                     }
-                }
-                if (edge) {
+                    if (edge) {
 #pragma unroll
-                    for (int e = 0; e < C::kKeys; e += 2) {
-                        if (tok + e >= lim) t[e / 2].x = -INFINITY;
-                        if (tok + e + 1 >= lim) t[e / 2].y = -INFINITY;
+                        for (int e = 0; e < C::kKeys; e += 2) {
+                            if (tok + e >= lim) t[e / 2].x = -INFINITY;
+                            if (tok + e + 1 >= lim) t[e / 2].y = -INFINITY;
+                        }
                     }
-                }
-                float tops[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                    float tops[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                for (int e = 0; e < C::kKeys / 2; ++e) tops[e & 3] = fmaxf(tops[e & 3], fmaxf(t[e].x, t[e].y));
-                const float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
-                const bool move = i == 0 ? top > -INFINITY : top > kSpan + kSlack;
-                if (__any_sync(~0u, move)) {
-                    const float up = move ? top - kSpan : 0.f;
+                    for (int e = 0; e < C::kKeys / 2; ++e) tops[e & 3] = fmaxf(tops[e & 3], fmaxf(t[e].x, t[e].y));
+                    const float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
+                    const bool move = i == 0 ? top > -INFINITY : top > kSpan + kSlack;
+                    if (!__any_sync(~0u, move)) break;
+                    // (a whole number: references below 2^24 move without a rounding)
+                    const float up = move ? rintf(top) - kSpan : 0.f;
                     ref += up;
-#pragma unroll
-                    for (int e = 0; e < C::kKeys / 2; ++e) t[e] = add2(t[e], make_float2(-up, -up));
                     if (i > 0) {
                         const float by = ex2(-up);
                         l *= by;
@@ -544,8 +545,18 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_con
                                 for (int e = 0; e < 16; ++e) u[e] = __float_as_uint(v[e] * by);
                                 tmem_put16(out + c, u);
                             }
+                            tmem_stored();
                         }
                     }
+                    // An exponent far above the old reference (a bias by distance lifts it so from tile to tile) has lost bits to
+                    // rounding, 2^-25 of its height: beyond 2^-15 of a weight (fp32: 2^-20) all are taken anew.
+                    if (again && __any_sync(~0u, up > (kParts == 2 ? 32.f : 1024.f))) {
+                        again = false;
+                        continue;
+                    }
+#pragma unroll
+                    for (int e = 0; e < C::kKeys / 2; ++e) t[e] = add2(t[e], make_float2(-up, -up));
+                    break;
                 }
                 // the weights, in the scores' place
 #pragma unroll

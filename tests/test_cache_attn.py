@@ -375,3 +375,23 @@ def test_refusals_of_tensors():
                     (dict(lse=torch.zeros(2, 3, device="cuda")), ValueError), (dict(q=c["q"][..., ::2]), ValueError)):
         with pytest.raises(err):
             cache_attn(**dict(good, **kw))
+
+
+@gpu
+@pytest.mark.parametrize("dtype", [BF16, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("new", [1, 200])
+def test_a_bias_by_distance_far_behind_a_row(new, dtype):
+    """Of the scores only those near a row's own place weigh anything, and those are small: how far the others
+    fall may not count in the error. So the size of a score in the bound is that of tokens with 2^-30 of the
+    largest weight or more: those behind them have less than 2^-24 together (the slopes fall by 2^-30 within
+    1100 tokens), and 2^-24 times their scores' errors is nothing beside the rest."""
+    H = 6
+    slopes = torch.tensor([0.02, 0.5, 1.0, 37.0, 1000.0, 30000.0], device="cuda")
+    c = make([new], [20000], H, 2, 128, 64, dtype, E4M3, seed=5)
+    o, lse = run(c, slopes=slopes)
+    want = ref.attend(c["q"], c["kc"], c["vc"], c["ks"], c["vs"], c["table"], c["held"], c["cu_list"], c["d"] ** -0.5, 0.0, slopes)
+    # such a token's bias is at most 30 ln 2 and the products' difference, 2 dots; its |s| one more
+    want["most"] = 3 * want["dots"] + 30 * math.log(2)
+    bo, bl = ref.attend_bounds(want, dtype, 128, 20000)
+    ref.check("lse", lse, want["lse"], bl)
+    ref.check("o", o, want["o"], bo)

@@ -57,7 +57,7 @@ __device__ __forceinline__ void place(const Plan &p, int64_t t, int64_t n, int64
     if (first >= 0) {
         pos = (int32_t)(first + i);
         const int32_t page = p.table[n * p.width + (pos >> p.log_page)];
-        slot = (page << p.log_page) + (pos & ((1 << p.log_page) - 1));
+        if ((uint32_t)page <= (uint32_t)INT32_MAX >> p.log_page) slot = (page << p.log_page) + (pos & ((1 << p.log_page) - 1));
     }
     p.positions[t] = pos;
     p.slots[t] = slot;

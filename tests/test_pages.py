@@ -158,3 +158,13 @@ def test_refusals_on_the_host():
         assert release(i, None) == -1
     assert release(2, A[1]) == -1 and release(3, A[0]) == -1
     assert lib.gdr_page_plan(None, *A, None) == -1 and lib.gdr_page_release(None, *A[:5], None) == -1
+
+
+@gpu
+def test_entries_that_can_be_no_page_give_no_slot():
+    """The next tokens of four requests whose last page is half full, by a table that holds no page there."""
+    from gated_delta_rule_03_gb300 import page_plan
+    page = 16
+    table = torch.tensor([[0, 3], [-7, -1], [2 ** 27, 0], [2 ** 28, 0], [2 ** 31 - 1, 0], [2 ** 27 - 1, 0]], dtype=I32, device="cuda")
+    plan = page_plan(table, ints([8] * 6), ints([5]), ints([1]), page)
+    assert plan.slots.tolist() == [8, -1, -1, -1, -1, 2 ** 31 - 8] and plan.positions.tolist() == [8] * 6 and plan.free_count.tolist() == [1]

@@ -126,6 +126,7 @@ template <typename T, int V> int launch_rotary(Rotary r, int64_t tokens, bool in
     const int64_t want = 152 * 2048;
     int64_t parts = (want + r.units - 1) / r.units;
     if (parts > all) parts = all;
+    if (parts > 65535) parts = 65535;  // (of a grid)
     r.step = (int)((all + parts - 1) / parts);
     const dim3 grid((unsigned)((r.units + 255) / 256), (unsigned)((all + r.step - 1) / r.step));
     if (r.neighbours)

@@ -189,3 +189,13 @@ def test_refusals_on_the_host():
         row = dict(q_stride=1024, k_stride=1024, q_out_stride=1024, k_out_stride=1024)
         assert call(f, k=A[0] + 4 * 64 * 2 - 16, qo=A[0], ko=A[5], **row) == -1
         assert call(f, tokens=0) == 0
+
+
+@gpu
+def test_more_heads_than_a_grid_is_high():
+    from gated_delta_rule_03_gb300 import rotary_fwd, rotary_rates
+    q, k, pos = make(1, 65536, 65536, 16, BF16)
+    rates = rotary_rates(16)
+    for t, y in zip((q, k), rotary_fwd(q, k, pos, rates)):
+        want = ref.rotary(t, pos, rates.cpu(), False, 1.0)
+        ref.check("heads", y.cpu(), want, bound(t, BF16, 1.0)(want, sizes(t, 16, False)))

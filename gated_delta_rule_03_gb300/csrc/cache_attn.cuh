@@ -24,7 +24,7 @@ namespace cattn {
 
 constexpr float kSpan = 7.f, kSlack = 8.f;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
-constexpr float kNoRef = -1e30f;  // of a row that has seen nothing
+constexpr float kNoRef = -3.4028234663852886e38f;  // of a row that has seen nothing: the lowest number
 
 struct Attn {
     const void *q;
@@ -72,14 +72,23 @@ __device__ __forceinline__ float lg2(float x) {
     return y;
 }
 
-// The score of a token in powers of two, from a product that is already scaled; away = |p - j|.
-// tanh(x) = 1 - 2 / (1 + e^2x) is off by some 1e-7 in all, and the cap times that in the score: enough
-// for bf16 results; fp32 ones take the library's.
+// tanh(x) = 1 - 2 / (1 + e^2x) is off by some 2e-7 in all, and the cap times that in the score. Near 0 two terms of
+// its series are off by 2 x^5 / 15, relative 1e-7 where they are taken, so that a score far below its cap keeps
+// its bits whatever the cap: 2^-16 relative in all, enough for bf16 results; fp32 ones take the library's.
+__device__ __forceinline__ float reciprocal(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+template <bool kExact> __device__ __forceinline__ float cap_of(float x) {
+    if (kExact) return tanhf(x);
+    const float far = fmaf(-2.f, reciprocal(1.f + ex2(2.f * kLog2e * x)), 1.f), near = fmaf(x * x, x * (-1.f / 3.f), x);
+    return fabsf(x) < 0.03f ? near : far;
+}
+
+// The score of a token from a product that is already scaled; away = |p - j|.
 template <bool kExact> __device__ __forceinline__ float shaped(float z, float softcap, float inv_cap, float slope, float away) {
-    if (softcap > 0.f) {
-        const float x = z * inv_cap;
-        z = softcap * (kExact ? tanhf(x) : 1.f - __fdividef(2.f, 1.f + ex2(2.f * kLog2e * x)));
-    }
+    if (softcap > 0.f) z = softcap * cap_of<kExact>(z * inv_cap);
     return fmaf(-slope, away, z);
 }
 

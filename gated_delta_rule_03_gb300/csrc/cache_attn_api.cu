@@ -17,6 +17,8 @@ struct Call {
     size_t e;
 };
 
+constexpr int kBeyond = 4096;  // places behind a request's last that the kernels look ahead, as 32-bit numbers
+
 int check_shape(const gdr_cache_attn_shape *s, Call *c) {
     if (!s) return GDR_ERR_INVALID_ARG;
     Attn &a = c->a;
@@ -24,7 +26,7 @@ int check_shape(const gdr_cache_attn_shape *s, Call *c) {
     int st = check_cache(&s->cache, &a.log_page);
     if (st != GDR_OK) return st;
     if (s->num_seqs < 1 || s->num_seqs > INT32_MAX / 2 || s->total_tokens < 0 || s->total_tokens > INT32_MAX) return GDR_ERR_INVALID_ARG;
-    if (s->max_q < 0 || s->max_q > INT32_MAX || s->width < 1 || s->width > INT32_MAX / s->cache.page) return GDR_ERR_INVALID_ARG;
+    if (s->max_q < 0 || s->max_q > INT32_MAX || s->width < 1 || s->width > (INT32_MAX - kBeyond) / s->cache.page) return GDR_ERR_INVALID_ARG;
     if (s->heads < 1 || s->heads > 1 << 16 || s->heads % s->cache.kv_heads) return GDR_ERR_INVALID_ARG;
     if (!isfinite(s->scale) || !isfinite(s->softcap) || s->softcap < 0.f) return GDR_ERR_INVALID_ARG;
     if (s->softcap > 0.f && s->softcap < 1e-18f) return GDR_ERR_INVALID_ARG;  // (its reciprocal is used)

@@ -616,7 +616,6 @@ int launch_step_kernel(const Attn &a, const StepPlan &plan, bool join, cudaStrea
     using C = StepConfig<D, kParts, kR>;
     constexpr int kBlocks = kSms * C::kBlocks;
     const auto kernel = attn_step_kernel<T, D, kCode, kParts, kShaped, kR>;
-    static const cudaError_t sized = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
     if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem) != cudaSuccess) return GDR_ERR_CUDA;
     kernel<<<kBlocks, kStepWarps * 32, C::kSmem, s>>>(a, plan);
     if (cudaGetLastError() != cudaSuccess) return GDR_ERR_CUDA;

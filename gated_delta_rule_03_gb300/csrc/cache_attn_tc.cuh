@@ -187,7 +187,9 @@ __device__ __forceinline__ void tmem_put8(uint32_t taddr, const uint32_t (&r)[8]
 }
 __device__ __forceinline__ void tmem_stored() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-// What becomes of scores: nothing more, a cap, or a bias by distance with or without a cap.
+// What becomes of scores: nothing more, a cap, or a bias by distance with or without a cap. (bf16: a cap above kCaps,
+// of which the quick form's 2e-7 would be too much, goes the third way.)
+constexpr float kCaps = 1024.f;
 enum { kPlain = 0, kCapped = 1, kBiased = 2 };
 
 // Exponents of 16 keys' weights from products with their codes: m scales a product (log2(e) in it if
@@ -205,14 +207,9 @@ template <int kMode, bool kExact> struct Shape {
             k = inv_cap;
         }
     }
-    static __device__ __forceinline__ float rcp(float x) {
-        float y;
-        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-        return y;
-    }
     __device__ __forceinline__ float one(float z, int e) const {
         z *= m;
-        if (cap > 0.f) z = cap * (kExact ? tanhf(z * k) : fmaf(-2.f, rcp(1.f + ex2(z * k * (2.f * kLog2e))), 1.f));
+        if (cap > 0.f) z = cap * cap_of<kExact>(z * k);
         if (kMode == kBiased) z = fmaf(-slope, fabsf(away - (float)e), z);
         return fmaf(z, kLog2e, off);
     }
@@ -230,7 +227,7 @@ template <int kMode, bool kExact> struct Shape {
             const float2 a = add2(make_float2(ex2(below(x0.x)), ex2(below(x1.x))), make_float2(1.f, 1.f));
             const float2 b = add2(make_float2(ex2(below(x0.y)), ex2(below(x1.y))), make_float2(1.f, 1.f));
             const float2 ab = mul2(a, b);
-            const float r = rcp(ab.x * ab.y);
+            const float r = reciprocal(ab.x * ab.y);
             const float2 q = mul2(make_float2(r, r), make_float2(ab.y, ab.x));  // reciprocals of ab
             t0 = fma2(mul2(make_float2(q.x, q.x), make_float2(b.x, a.x)), make_float2(k, k), make_float2(off, off));
             t1 = fma2(mul2(make_float2(q.y, q.y), make_float2(b.y, a.y)), make_float2(k, k), make_float2(off, off));
@@ -929,7 +926,7 @@ template <typename T, int D, int kParts, int kMode> int launch_tc_kernel(const A
 }
 
 template <int D> int launch_tc_d(const Attn &a, int code, int dtype, void *ws, cudaStream_t s) {
-    const int mode = a.slopes ? kBiased : a.softcap > 0.f ? kCapped : kPlain;
+    const int mode = a.slopes || (dtype == GDR_BF16 && a.softcap > kCaps) ? kBiased : a.softcap > 0.f ? kCapped : kPlain;
     if (dtype == GDR_F32)
         return mode == kPlain    ? launch_tc_kernel<float, D, 2, kPlain>(a, code, ws, s)
                : mode == kCapped ? launch_tc_kernel<float, D, 2, kCapped>(a, code, ws, s)

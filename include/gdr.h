@@ -568,7 +568,7 @@ int gdr_block_norm_bwd(const gdr_block_norm_shape *shape, const void *dx_out, co
  *
  * Shape of a call (a HOST struct):
  *   tokens          rows of every tensor (>= 0)
- *   q_heads >= 1, k_heads >= 0 (0: no keys)
+ *   q_heads >= 1, k_heads >= 0 (0: no keys), each at most 65536
  *   d               a multiple of 8 in [8, 256];  rot_dim even, in [2, d]
  *   dtype           gdr_dtype of all tensors
  *   neighbours      nonzero: a pair is two neighbours
@@ -617,7 +617,8 @@ int gdr_rotary_bwd(const gdr_rotary_shape *shape, const void *dq_out, const void
  *   cu_q         [num_seqs + 1] int32: offsets of the requests' new tokens, cut off at rows
  *   start        [num_seqs] int32: position of a request's first new token, -1 if refused
  *   positions    [rows] int32: every new token's position, 0 if there is none
- *   slots        [rows] int32: page * (tokens per page) + place in it, -1 if there is none
+ *   slots        [rows] int32: page * (tokens per page) + place in it, -1 if there is none or the
+ *                table's entry can be no page (negative, or its slots not 32-bit numbers)
  * sizes: num_seqs >= 1, rows >= 0, width >= 1, page a power of two in [16, 128],
  * num_pages * page < 2^31 (the caller's entries are not checked here; users of slots and block
  * tables check theirs). One or two launches, no workspace; the same results every time.
@@ -694,10 +695,10 @@ int gdr_cache_append(const gdr_cache_shape *shape, int64_t tokens, const void *k
  *   num_seqs, total_tokens   requests (>= 1) and rows of q
  *   max_q     the most new tokens of one request (with cu_q; else total_tokens / num_seqs)
  *   heads     a multiple of kv_heads, at most 65536
- *   width     block_table [num_seqs, width]
+ *   width     block_table [num_seqs, width]; width * page at most 2^31 - 4097
  *   q_stride  elements from a token's first head to the next token's; 0: dense
  *   causal    nonzero: causal
- *   scale     finite; softcap finite, >= 0 (0: none)
+ *   scale     finite; softcap finite, 0 (none) or at least 1e-18
  */
 typedef struct gdr_cache_attn_shape {
     gdr_cache_shape cache;
@@ -718,7 +719,7 @@ size_t gdr_cache_attn_workspace_size(const gdr_cache_attn_shape *shape);
  *   cu_q         [num_seqs + 1] int32 offsets from 0, non-decreasing, the last at most
  *                total_tokens (rows behind it are neither read nor written), no request longer
  *                than max_q; or NULL for total_tokens / num_seqs tokens each
- *   slopes       [heads] fp32 or NULL
+ *   slopes       [heads] fp32 or NULL; slope times distance within fp32
  *   o            [total_tokens, heads, d] dtype, dense (written)
  *   lse          [total_tokens, heads] fp32 (written), or NULL
  *   workspace    16-byte aligned; calls that share one must be ordered on one stream
@@ -726,9 +727,12 @@ size_t gdr_cache_attn_workspace_size(const gdr_cache_attn_shape *shape);
  * workspace's status word (gdr_read_device_status) and nothing else is written.
  * Scores, maxima, sums and outputs are fp32 until o is rounded. bf16: a query is held in fp16
  * with a power of two per row (exact for entries within 2^-24 of its largest), the weights of a
- * tile in fp16 relative to a running maximum. fp32: both as two fp16 parts (22 bits).
- * What is masked or behind len is never used: NaN there stays there. A NaN within a page reaches
- * the tokens that look at the page's scale. The same results every time.
+ * tile in fp16 relative to a running maximum. fp32: both as two fp16 parts (22 bits). Weights below
+ * 2^-32 of a row's largest contribution may be dropped from o (not from lse).
+ * What is behind len is never used: NaN there stays there. A page's scale that is NaN reaches the
+ * tokens that see one of the page's, no others. Codes of cached tokens are numbers, as gdr_cache_append
+ * leaves them; an e4m3 NaN code within len may also reach rows that do not see it. The same
+ * results every time.
  */
 int gdr_cache_attn(const gdr_cache_attn_shape *shape, const void *q, const void *k_cache,
                    const void *v_cache, const float *k_scale, const float *v_scale,

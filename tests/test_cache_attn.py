@@ -395,3 +395,43 @@ def test_a_bias_by_distance_far_behind_a_row(new, dtype):
     bo, bl = ref.attend_bounds(want, dtype, 128, 20000)
     ref.check("lse", lse, want["lse"], bl)
     ref.check("o", o, want["o"], bo)
+
+
+@gpu
+@pytest.mark.parametrize("dtype", [BF16, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("new", [1, 20])
+def test_a_score_of_any_size_is_a_score(new, dtype):
+    """The last token sees one key, at a score of some 1e33 of either sign: it takes its value."""
+    c = make([new], [1], 4, 2, 128, 16, dtype, E4M3, seed=12)
+    for scale in (1e32, -1e32):
+        o, lse = run(c, scale=scale)
+        want = ref.attend(c["q"], c["kc"], c["vc"], c["ks"], c["vs"], c["table"], c["held"], c["cu_list"], scale)
+        assert float(want["lse"][-1].abs().min()) > 1e31 and bool((o[:-1] == 0).all()) and bool((lse[:-1] == -math.inf).all())
+        # o: a weight over itself, and the value scale's logarithm lost beside the score, twice ...
+        ref.check("o", o[-1:], want["o"][-1:], (2 * ref.HALF_STEP[dtype] + 2.0 ** -10) * want["o"][-1:].abs())
+        # ... lse: scores of 128 products, with roundings of 2^-23 of their sizes, queries of 22 bits
+        ref.check("lse", lse[-1:], want["lse"][-1:], 256 * 2.0 ** -23 * want["dots"][-1:] + 2.0 ** -20 * want["lse"][-1:].abs())
+
+
+@gpu
+@pytest.mark.parametrize("new", [1, 6, 70])
+@pytest.mark.parametrize("cap", [2000.0, 1e5, 1e9])
+def test_caps_far_above_the_scores(new, cap):
+    """A score far below its cap is off by 2^-16 of itself, not of the cap."""
+    for size in (1.0, 6.0):
+        c = make([new], [900], 8, 4, 128, 32, BF16, INT8, seed=13, size=size)
+        slopes = torch.exp2(-torch.arange(1.0, 9.0, device="cuda"))
+        for kw in (dict(), dict(slopes=slopes)):
+            o, lse = run(c, softcap=cap, **kw)
+            want = ref.attend(c["q"], c["kc"], c["vc"], c["ks"], c["vs"], c["table"], c["held"], c["cu_list"], 128 ** -0.5, cap, kw.get("slopes"))
+            bo, bl = ref.attend_bounds(want, BF16, 128, 900)
+            capped = 2.0 ** -16 * want["dots"]  # |s| before a bias is below this sum of sizes
+            ref.check("lse", lse, want["lse"], bl + capped)
+            ref.check("o", o, want["o"], bo + 2 * capped[..., None] * want["size"])
+
+
+def test_tables_whose_tokens_pass_32_bits_are_refused():
+    from gated_delta_rule_03_gb300 import ops
+    size = ops._load().gdr_cache_attn_workspace_size
+    most = (2 ** 31 - 4097) // 16
+    assert size(shape(width=most)) > 0 and size(shape(width=most + 1)) == 0 and size(shape(width=(2 ** 31 - 1) // 16)) == 0

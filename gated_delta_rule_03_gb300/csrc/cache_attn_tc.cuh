@@ -52,7 +52,8 @@ template <int D, int kParts> struct TcConfig {
     static constexpr int kKv = kKeys * D * 2;          // of a tile of keys or values
     static constexpr int kStages = D == 256 ? (kParts == 2 ? 1 : 2) : 3;
     static constexpr int kRaw = D == 256 ? 1 : 3;      // tiles of codes
-    static constexpr int kSmem = kTiles * kParts * kQ + 2 * kStages * kKv + kRaw * kKv + 1024;
+    static constexpr int kStage = D == 256 ? 0 : kSoft / 32 * 2048;  // 64 bytes of every row on their way out (D = 256: no room)
+    static constexpr int kSmem = kTiles * kParts * kQ + 2 * kStages * kKv + kRaw * kKv + kStage + 1024;
     // TMEM columns: scores of two slots per row tile (weights in their place), low parts of weights, outputs
     static constexpr uint32_t kLow = 128, kLowStep = kKeys / 2, kO = 256;
     static_assert(kSmem <= 232448 - 2000, "shared memory");
@@ -264,6 +265,10 @@ __device__ __forceinline__ void store16(uint32_t saddr, uint32_t x, uint32_t y, 
     asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(saddr), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
 }
 
+__device__ __forceinline__ void store8(uint32_t saddr, uint32_t x, uint32_t y) {
+    asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(saddr), "r"(x), "r"(y) : "memory");
+}
+
 __device__ __forceinline__ bool elect() {
     uint32_t one;
     asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(one));
@@ -362,66 +367,78 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_con
             }
             return false;
         };
-        // This thread's row of queries in fp16 with a power of two, its sign that of the scale; returns what
-        // products with it are to be multiplied by. 256 bytes of the row are under way together; longer rows come
-        // twice, the second time from near by.
+        // This warp's 32 rows of queries in fp16 with a power of two each, its sign that of the scale; returns what products
+        // with this thread's are to be multiplied by. Lanes share a row, so that a load takes whole lines of few rows (a row
+        // to a thread: 32 lines a load, 4096 cycles of them for an item of two row tiles).
         auto put_queries = [&](const TcItem &t) {
-            const bool live = tid < t.rows;
-            const T *const src = query_of(t);
+            constexpr int kVecs = D * (int)sizeof(T) / 16, kLanes = kVecs < 32 ? kVecs : 32, kPieces = kVecs / kLanes;
+            constexpr int kAtOnce = 32 / kLanes, kBatch = 16 / kPieces < kLanes ? 16 / kPieces : kLanes;  // rows of a load; loads under way
+            const uint64_t mine = (uint64_t)query_of(t);
+            const uint32_t alive = __ballot_sync(~0u, tid < t.rows);
             const uint32_t to = sq + tile * kParts * C::kQ;
-            constexpr int kVec = 16 / sizeof(T), kPiece = 256 / sizeof(T) < D ? 256 / sizeof(T) : D, kPieces = D / kPiece, kVecs = kPiece / kVec;
-            uint4 w[kVecs];
-            auto fetch = [&](int piece) {
-#pragma unroll
-                for (int i = 0; i < kVecs; ++i) w[i] = live ? ld_nc(src + piece * kPiece + i * kVec) : make_uint4(0, 0, 0, 0);
-            };
-            uint32_t most = 0;
+            const int sub = lane % kLanes;
+            int my_shift = 0;
 #pragma unroll 1
-            for (int piece = kPieces - 1; piece >= 0; --piece) {
-                fetch(piece);
+            for (int j0 = 0; j0 < kLanes; j0 += kBatch) {
+                uint4 w[kBatch][kPieces];
 #pragma unroll
-                for (int i = 0; i < kVecs; ++i) {
-                    if constexpr (sizeof(T) == 2) {
-                        most = __vmaxu2(most, __vmaxu2(__vmaxu2(w[i].x & 0x7fff7fffu, w[i].y & 0x7fff7fffu), __vmaxu2(w[i].z & 0x7fff7fffu, w[i].w & 0x7fff7fffu)));
-                    } else {
-                        most = max(most, max(max(w[i].x & 0x7fffffffu, w[i].y & 0x7fffffffu), max(w[i].z & 0x7fffffffu, w[i].w & 0x7fffffffu)));
-                    }
+                for (int j = 0; j < kBatch; ++j) {
+                    const int r = (j0 + j) * kAtOnce + lane / kLanes;
+                    const char *const src = (const char *)__shfl_sync(~0u, mine, r);
+#pragma unroll
+                    for (int x = 0; x < kPieces; ++x) w[j][x] = alive >> r & 1 ? ld_nc(src + (x * 32 + sub) * 16) : make_uint4(0, 0, 0, 0);
                 }
-            }
-            if (sizeof(T) == 2) most = max(most & 0xffffu, most >> 16) << 16;
-            const int shift = row_shift(most);
-            const float up = a.scale < 0.f ? -two_to(shift) : two_to(shift);
-            const float2 up_pair = make_float2(up, up);
-            auto pair_of = [&](int e) {  // entries e and e + 1 of the piece
-                const uint4 &q = w[e / kVec];
-                const uint32_t word = (e / (kVec / 4)) % 4 == 0 ? q.x : (e / (kVec / 4)) % 4 == 1 ? q.y : (e / (kVec / 4)) % 4 == 2 ? q.z : q.w;
-                if constexpr (sizeof(T) == 2) return make_float2(__uint_as_float(word << 16), __uint_as_float(word & 0xffff0000u));
-                return make_float2(__uint_as_float(word), __uint_as_float(e % 4 == 0 ? q.y : q.w));
-            };
-#pragma unroll 1
-            for (int piece = 0; piece < kPieces; ++piece) {
-                if (kPieces > 1) fetch(piece);
 #pragma unroll
-                for (int c = 0; c < kPiece; c += 8) {
-                    uint32_t hi[4], lo[4];
+                for (int j = 0; j < kBatch; ++j) {
+                    const int r = (j0 + j) * kAtOnce + lane / kLanes;
+                    uint32_t most = 0;
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const float2 z = mul2(pair_of(c + 2 * i), up_pair);
-                        hi[i] = f16_pair(z.x, z.y);
-                        if (kParts == 2) {
-                            const float2 f = f16_values(hi[i]);
-                            lo[i] = f16_pair(z.x - f.x, z.y - f.y);
+                    for (int x = 0; x < kPieces; ++x) {
+                        const uint4 &q = w[j][x];
+                        if constexpr (sizeof(T) == 2) {
+                            most = __vmaxu2(__vmaxu2(q.x & 0x7fff7fffu, q.y & 0x7fff7fffu), __vmaxu2(q.z & 0x7fff7fffu, q.w & 0x7fff7fffu));
+                            most = max(most & 0xffffu, most >> 16) << 16;
+                        } else {
+                            most = max(most, max(max(q.x & 0x7fffffffu, q.y & 0x7fffffffu), max(q.z & 0x7fffffffu, q.w & 0x7fffffffu)));
                         }
                     }
-                    const int d = piece * kPiece + c;
-                    const uint32_t dst = to + (d >> 6) * 16384 + sw128_offset(tid & 127, d & 63);
-                    store16(dst, hi[0], hi[1], hi[2], hi[3]);
-                    if (kParts == 2) store16(dst + C::kQ, lo[0], lo[1], lo[2], lo[3]);
+#pragma unroll
+                    for (int d = 1; d < kLanes; d *= 2) most = max(most, __shfl_xor_sync(~0u, most, d));
+                    const int shift = row_shift(most), its = __shfl_sync(~0u, shift, lane % kAtOnce * kLanes);
+                    if (lane / kAtOnce == j0 + j) my_shift = its;
+                    const float up = a.scale < 0.f ? -two_to(shift) : two_to(shift);
+                    const float2 up_pair = make_float2(up, up);
+#pragma unroll
+                    for (int x = 0; x < kPieces; ++x) {
+                        const uint32_t in[4] = {w[j][x].x, w[j][x].y, w[j][x].z, w[j][x].w};
+                        constexpr int kPairs = 8 / (int)sizeof(T);
+                        uint32_t hi[kPairs], lo[kPairs];
+#pragma unroll
+                        for (int i = 0; i < kPairs; ++i) {
+                            float2 z;
+                            if constexpr (sizeof(T) == 2) z = make_float2(__uint_as_float(in[i] << 16), __uint_as_float(in[i] & 0xffff0000u));
+                            else z = make_float2(__uint_as_float(in[2 * i]), __uint_as_float(in[2 * i + 1]));
+                            z = mul2(z, up_pair);
+                            hi[i] = f16_pair(z.x, z.y);
+                            if (kParts == 2) {
+                                const float2 f = f16_values(hi[i]);
+                                lo[i] = f16_pair(z.x - f.x, z.y - f.y);
+                            }
+                        }
+                        const int d = (x * 32 + sub) * (16 / (int)sizeof(T));
+                        const uint32_t dst = to + (d >> 6) * 16384 + sw128_offset((warp & 3) * 32 + r, d & 63);
+                        if constexpr (sizeof(T) == 2) {
+                            store16(dst, hi[0], hi[1], hi[2], hi[3]);
+                        } else {
+                            store8(dst, hi[0], hi[1]);
+                            store8(dst + C::kQ, lo[0], lo[1]);
+                        }
+                    }
                 }
             }
             fence_async_smem();
             mbar_arrive(bar(Q_FULL + tile));
-            return two_to(-shift) * fabsf(a.scale);
+            return two_to(-my_shift) * fabsf(a.scale);
         };
 
         bool have = next_item(item);
@@ -600,12 +617,34 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_con
                 if (plan.splits > 1) part->lse2[tid] = sum2;
                 else if (a.lse) a.lse[row] = sum2 * kLn2;
             }
+            // 64 bytes of every row: through shared memory, four lanes to a row (a row to a thread: 32 lines a store)
+            char *const mine = plan.splits > 1 ? (char *)part->o[tid] : (char *)((T *)a.o + row * D);
+            const uint32_t alive = __ballot_sync(~0u, live);
+            auto hand_out = [&](const uint32_t *w, int at) {
+                if constexpr (C::kStage == 0) {
+                    if (!live) return;
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) *(uint4 *)(mine + at + 16 * x) = make_uint4(w[4 * x], w[4 * x + 1], w[4 * x + 2], w[4 * x + 3]);
+                } else {
+                    const uint32_t stage = sr + C::kRaw * C::kKv + warp * 2048;
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) store16(stage + lane * 64 + ((x ^ (lane >> 1)) & 3) * 16, w[4 * x], w[4 * x + 1], w[4 * x + 2], w[4 * x + 3]);
+                    __syncwarp();
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) {
+                        const int r = x * 8 + (lane >> 2);
+                        const uint4 y = load16(stage + r * 64 + ((lane ^ (r >> 1)) & 3) * 16);
+                        char *const to = (char *)__shfl_sync(~0u, (uint64_t)mine, r);
+                        if (alive >> r & 1) *(uint4 *)(to + at + (lane & 3) * 16) = y;
+                    }
+                    __syncwarp();
+                }
+            };
 #pragma unroll 1
             for (int c = 0; c < D; c += 32) {
                 float v[32];
                 tmem_load32(out + c, v);
-                if (!live) continue;
-                if (older) {
+                if (older && live) {
 #pragma unroll
                     for (int e = 0; e < 32; e += 4) {
                         const float4 o = *(const float4 *)(row_out + c + e);
@@ -619,19 +658,20 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_con
                 for (int e = 0; e < 32; ++e) v[e] *= inv;
                 if (plan.splits > 1 || sizeof(T) == 4) {
 #pragma unroll
-                    for (int e = 0; e < 32; e += 4) *(float4 *)(row_out + c + e) = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
-                } else {
-                    __nv_bfloat16 *const to = (__nv_bfloat16 *)a.o + row * D + c;
+                    for (int e = 0; e < 32; e += 16) {
+                        uint32_t w[16];
 #pragma unroll
-                    for (int e = 0; e < 32; e += 8) {
-                        uint32_t w[4];
-#pragma unroll
-                        for (int x = 0; x < 4; ++x) {
-                            const __nv_bfloat162 b = __floats2bfloat162_rn(v[e + 2 * x], v[e + 2 * x + 1]);
-                            w[x] = reinterpret_cast<const uint32_t &>(b);
-                        }
-                        *(uint4 *)(to + e) = make_uint4(w[0], w[1], w[2], w[3]);
+                        for (int x = 0; x < 16; ++x) w[x] = __float_as_uint(v[e + x]);
+                        hand_out(w, (c + e) * 4);
                     }
+                } else {
+                    uint32_t w[16];
+#pragma unroll
+                    for (int x = 0; x < 16; ++x) {
+                        const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * x], v[2 * x + 1]);
+                        w[x] = reinterpret_cast<const uint32_t &>(b);
+                    }
+                    hand_out(w, c * 2);
                 }
             }
             tc_fence_before();

@@ -550,14 +550,16 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_con
                         l *= by;
                         if (!anew) {
                             outputs_done();
+                            // (32 columns a time: 4 x 4096 tokens 250 us, by 16 260)
 #pragma unroll 1
-                            for (int c = 0; c < D; c += 16) {
-                                float v[16];
-                                tmem_load16(out + c, v);
-                                uint32_t u[16];
+                            for (int c = 0; c < D; c += 32) {
+                                float v[32];
+                                tmem_load32(out + c, v);
+                                uint32_t u[32];
 #pragma unroll
-                                for (int e = 0; e < 16; ++e) u[e] = __float_as_uint(v[e] * by);
+                                for (int e = 0; e < 32; ++e) u[e] = __float_as_uint(v[e] * by);
                                 tmem_put16(out + c, u);
+                                tmem_put16(out + c + 16, u + 16);
                             }
                             tmem_stored();
                         }

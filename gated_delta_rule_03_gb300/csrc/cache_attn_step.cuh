@@ -32,6 +32,7 @@ constexpr int kStepWarps = 4;
 constexpr int kUnit = 16 * kStepWarps;  // tokens
 constexpr int kMinUnits = 4;            // a block's least share
 constexpr int kSms = 152;
+constexpr size_t kTaskBytes = kSms * 4 * 2 * sizeof(int4);  // (at most 4 blocks an SM)
 
 template <int D, int kParts, int kR> struct StepConfig {
     static constexpr int kSteps = D / 16;                 // k steps of the first product
@@ -68,7 +69,7 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
 __device__ __forceinline__ float2 unpack_f16(uint32_t r) { return __half22float2(reinterpret_cast<const __half2 &>(r)); }
 
 struct StepPlan {
-    int32_t *tasks;  // [blocks][4]: the item whose parts begin with this block's: request (-1: none), head, tile, blocks
+    int4 *tasks;     // [blocks][2]: the items that begin in this block and that began before it and go on in it: request (-1: none), head, tile, blocks of it + 2^16 (blocks before this one)
     char *parts;     // [blocks][2] Part
     CUtensorMap maps[2];  // keys, values: 16 rows of one page and head at a time
 };
@@ -142,12 +143,9 @@ __global__ void __launch_bounds__(kStepWarps * 32, (StepConfig<D, kParts, kR>::k
     int64_t per;
     const Share share = find_share<kR>(a, sums, found, &per);
     if (blockIdx.x == 0 && tid == 0) *a.status = share.ok ? GDR_OK : GDR_ERR_BAD_SEQLENS;
-    int4 task = make_int4(-1, 0, 0, 0);
+    if (plan.tasks && tid < 2) plan.tasks[2 * blockIdx.x + tid] = make_int4(-1, 0, 0, 0);
     sm100::griddep_launch_dependents();
-    if (!share.ok) {
-        if (plan.tasks && tid == 0) ((int4 *)plan.tasks)[blockIdx.x] = task;
-        return;
-    }
+    if (!share.ok) return;
 
     char *const ring = smem + warp * C::kStages * C::kStage;
     const uint32_t ring_s = sm100::smem_u32(ring);
@@ -518,96 +516,93 @@ __global__ void __launch_bounds__(kStepWarps * 32, (StepConfig<D, kParts, kR>::k
                 if (d == 0 && a.lse) a.lse[row] = sum2 * kLn2;
             }
         }
-        if (!whole && ua == 0) {
-            const int64_t stop = u - ua + units - 1;  // the item's last unit
-            task = make_int4((int)n, head, tile, (int)(stop / per - blockIdx.x + 1));
+        if (!whole && tid == (ua == 0 ? 0 : 1)) {
+            const int from = (int)((u - ua) / per), to = (int)((u - ua + units - 1) / per);  // blocks
+            plan.tasks[2 * blockIdx.x + tid] = make_int4((int)n, head, tile, (to - from + 1) | ((int)blockIdx.x - from) << 16);
         }
         u += ub - ua;
         sm100::fence_async_smem();  // (before copies into the ring again)
         __syncthreads();
     }
-    if (plan.tasks && tid == 0) ((int4 *)plan.tasks)[blockIdx.x] = task;
     if (!fine) *a.status = GDR_ERR_DEVICE_TIMEOUT;
 }
 
-// Adds the parts of items that several blocks worked on: a block for each that begins one. Its warps take the parts in
-// turn (a row by one warp, part after part, took 20 us for the 76 parts of a long cache), 4 rows at a time, and
-// meet in shared memory; every sum is in a fixed order.
+// Adds the parts of items that several blocks worked on, 64 columns of a row at a time. Bound by latency: a thread's loads
+// are under way together. Up to kAtOnce parts are a warp's work, and the block that begins the item does it all
+// (shared out, 64 requests took 6 us longer). More are shared out to all blocks that had a part, and the warps
+// take the parts in turn and meet in shared memory (one token behind 131,072 has 8 items of 76 parts, which 8 blocks took
+// 12 us to read). Every sum is in a fixed order.
 template <typename T, int D, int kR> __global__ void __launch_bounds__(256) join_parts_kernel(const __grid_constant__ Attn a, const __grid_constant__ StepPlan plan) {
     using P = Part<kR, D>;
-    constexpr int kRows = 4, kCols = D / 32;  // rows at a time, columns of a lane
-    __shared__ float base[kR], bad[kR], sum[8][kRows];
-    __shared__ float out[8][kRows][D];
-    sm100::griddep_wait();
-    const int4 task = ((const int4 *)plan.tasks)[blockIdx.x];
-    if (task.x < 0) return;
-    const int64_t n = task.x;
-    const int head = task.y, row0 = task.z * kR, blocks = task.w;
-    const int2 rows = rows_of(a, n);
-    const int nrows = min(kR, rows.y * a.group - row0);
+    constexpr int kCols = D / 64, kAtOnce = 8;
+    __shared__ float tops[8], sums[8], outs[8][64];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const P *const parts = (const P *)plan.parts;
-    // the first block's part is its second one, that of the others their first
-    auto part = [&](int i) { return parts + 2 * ((int64_t)blockIdx.x + i) + (i == 0); };
-    for (int r = warp; r < nrows; r += 8) {
-        float top = -INFINITY, nan = 0.f;
-        for (int i = lane; i < blocks; i += 32) {
-            const float x = part(i)->lse2[r];
-            top = fmaxf(top, x);
-            if (x != x) nan = x;
-        }
+    sm100::griddep_wait();
+    const int4 tasks[2] = {plan.tasks[2 * blockIdx.x], plan.tasks[2 * blockIdx.x + 1]};
+#pragma unroll 1
+    for (int which = 0; which < 2; ++which) {
+        const int4 task = which ? tasks[1] : tasks[0];
+        if (task.x < 0) continue;
+        const int head = task.y, row0 = task.z * kR, blocks = task.w & 0xffff, mine = task.w >> 16;
+        const int2 rows = rows_of(a, task.x);
+        const int units = min(kR, rows.y * a.group - row0) * kCols;
+        const bool many = blocks > kAtOnce;
+        if (!many && mine > 0) continue;
+        const int ways = many ? 8 : 1, abreast = 8 / ways, step = many ? blocks : abreast;  // warps for the parts of a unit; units at a time
+        // the first block's part is its second one, that of the others their first
+        const P *const parts = (const P *)plan.parts + 2 * ((int64_t)blockIdx.x - mine);
+        for (int u0 = mine; u0 < units; u0 += step) {
+            const int u = u0 + warp / ways, r = u / kCols, d = u % kCols * 64 + lane * 2;
+            float top = -INFINITY, l = 0.f;
+            float2 o = make_float2(0.f, 0.f);
+#pragma unroll 1
+            for (int i0 = warp % ways; u < units && i0 < blocks; i0 += ways * kAtOnce) {
+                float lse[kAtOnce];
+                float2 y[kAtOnce];
 #pragma unroll
-        for (int d = 1; d < 32; d *= 2) {
-            top = fmaxf(top, __shfl_xor_sync(~0u, top, d));
-            nan += __shfl_xor_sync(~0u, nan, d);
-        }
-        if (lane == 0) {
-            base[r] = top == -INFINITY ? 0.f : top;
-            bad[r] = nan;
-        }
-    }
-    __syncthreads();
-    for (int r0 = 0; r0 < nrows; r0 += kRows) {
-        float o[kRows][kCols], l[kRows];
+                for (int j = 0; j < kAtOnce; ++j) {
+                    const int i = i0 + ways * j;
+                    const P *const p = parts + 2 * i + (i == 0);
+                    lse[j] = i < blocks ? p->lse2[r] : -INFINITY;
+                    y[j] = i < blocks ? *(const float2 *)&p->o[r][d] : make_float2(0.f, 0.f);
+                }
+                float most = top;
 #pragma unroll
-        for (int r = 0; r < kRows; ++r) {
-            l[r] = 0.f;
+                for (int j = 0; j < kAtOnce; ++j) most = fmaxf(most, lse[j]);
+                const float base = most == -INFINITY ? 0.f : most, by = ex2(top - base);
+                top = most;
+                l *= by;
+                o = make_float2(o.x * by, o.y * by);
 #pragma unroll
-            for (int x = 0; x < kCols; ++x) o[r][x] = 0.f;
-        }
-#pragma unroll 2
-        for (int i = warp; i < blocks; i += 8) {
-            const P *const p = part(i);
-#pragma unroll
-            for (int r = 0; r < kRows; ++r) {
-                if (r0 + r >= nrows) break;
-                const float f = ex2(p->lse2[r0 + r] - base[r0 + r]);
-                l[r] += f;
-#pragma unroll
-                for (int x = 0; x < kCols; ++x) o[r][x] = fmaf(p->o[r0 + r][x * 32 + lane], f, o[r][x]);
+                for (int j = 0; j < kAtOnce; ++j) {
+                    const float f = ex2(lse[j] - base);
+                    l += f;
+                    o = make_float2(fmaf(y[j].x, f, o.x), fmaf(y[j].y, f, o.y));
+                }
             }
-        }
-#pragma unroll
-        for (int r = 0; r < kRows; ++r) {
-            if (lane == 0) sum[warp][r] = l[r];
-#pragma unroll
-            for (int x = 0; x < kCols; ++x) out[warp][r][x * 32 + lane] = o[r][x];
-        }
-        __syncthreads();
-        for (int x = threadIdx.x; x < kRows * D; x += 256) {
-            const int r = x / D, d = x % D;
-            if (r0 + r >= nrows) break;
-            float l1 = bad[r0 + r], o1 = 0.f;
-#pragma unroll
-            for (int w = 0; w < 8; ++w) {
-                l1 += sum[w][r];
-                o1 += out[w][r][d];
+            *(float2 *)&outs[warp][lane * 2] = o;
+            if (lane == 0) {
+                tops[warp] = top;
+                sums[warp] = l;
             }
-            const int64_t row = (int64_t)(rows.x + (row0 + r0 + r) / a.group) * a.heads + head * a.group + (row0 + r0 + r) % a.group;
-            ((T *)a.o)[row * D + d] = from_f32<T>(l1 == 0.f ? 0.f : o1 * (1.f / l1));
-            if (d == 0 && a.lse) a.lse[row] = (l1 == 0.f ? -INFINITY : log2f(l1) + base[r0 + r]) * kLn2;
+            __syncthreads();
+            for (int x = threadIdx.x; x < abreast * 64 && u0 + x / 64 < units; x += 256) {
+                const int first = x / 64 * ways, unit = u0 + x / 64;
+                float most = -INFINITY, sum = 0.f, z = 0.f;
+                for (int w = first; w < first + ways; ++w) most = fmaxf(most, tops[w]);
+                const float base = most == -INFINITY ? 0.f : most;
+                for (int w = first; w < first + ways; ++w) {
+                    const float f = ex2(tops[w] - base);
+                    sum = fmaf(sums[w], f, sum);
+                    z = fmaf(outs[w][x % 64], f, z);
+                }
+                const int at = row0 + unit / kCols, dim = unit % kCols * 64 + x % 64;
+                const int64_t row = (int64_t)(rows.x + at / a.group) * a.heads + head * a.group + at % a.group;
+                ((T *)a.o)[row * D + dim] = from_f32<T>(sum == 0.f ? 0.f : z * (1.f / sum));
+                if (dim == 0 && a.lse) a.lse[row] = (sum == 0.f ? -INFINITY : log2f(sum) + base) * kLn2;
+            }
+            __syncthreads();
         }
-        __syncthreads();
     }
 }
 
@@ -636,8 +631,8 @@ template <int D> int launch_step_d(const Attn &a, int codes, int dtype, void *ws
     // The least share of a block is kMinUnits: no request can have more, no item is split
     const bool join = ((a.width << a.log_page) + kUnit - 1) / kUnit > 1;
     StepPlan plan;
-    plan.tasks = join ? (int32_t *)ws : nullptr;
-    plan.parts = (char *)ws + ((size_t)kSms * 4 * sizeof(int4) + 255) / 256 * 256;
+    plan.tasks = join ? (int4 *)ws : nullptr;
+    plan.parts = (char *)ws + kTaskBytes;
     if (!map_cache(&plan.maps[0], a.kc, a, D, 16, true) || !map_cache(&plan.maps[1], a.vc, a, D, 16, true)) return GDR_ERR_CUDA;
     const bool shaped = a.softcap > 0.f || a.slopes;
     const bool e4m3 = codes == GDR_CODE_E4M3;
@@ -656,7 +651,7 @@ template <int D> int launch_step_d(const Attn &a, int codes, int dtype, void *ws
 }
 
 template <int D> size_t step_bytes_d() {
-    return ((size_t)kSms * 4 * sizeof(int4) + 255) / 256 * 256 + (size_t)kSms * 4 * 2 * sizeof(Part<16, D>);  // (at most 4 blocks an SM)
+    return kTaskBytes + (size_t)kSms * 4 * 2 * sizeof(Part<16, D>);
 }
 
 }  // namespace cattn

@@ -948,14 +948,21 @@ template <int D> size_t tc_bytes_d(const Attn &a, int dtype) {
     return most;
 }
 
+template <typename K> int registers_of(K kernel) {
+    cudaFuncAttributes attr;
+    return cudaFuncGetAttributes(&attr, kernel) == cudaSuccess ? attr.numRegs : -1;
+}
+
 template <typename T, int D, int kParts, int kMode> int launch_tc_kernel(const Attn &a, int codes, void *ws, cudaStream_t s) {
     using C = TcConfig<D, kParts>;
     TcPlan plan = tc_plan<D, kParts>(a, a.cu != nullptr);
     plan.parts = (char *)ws;
     const auto kernel = codes == GDR_CODE_E4M3 ? attn_tc_kernel<T, D, kParts, kMode, GDR_CODE_E4M3> : attn_tc_kernel<T, D, kParts, kMode, GDR_CODE_INT8>;
-    // The roles' shares of registers add up to what the block is launched with, if the compiler gave it that many.
-    cudaFuncAttributes attr;
-    if (cudaFuncGetAttributes(&attr, kernel) != cudaSuccess || attr.numRegs != kTcRegs) return GDR_ERR_CUDA;
+    // The roles' shares of registers add up to what the block is launched with, if the compiler gave it that many
+    // (asked once, 2 us a call).
+    static const bool shares_hold = registers_of(attn_tc_kernel<T, D, kParts, kMode, GDR_CODE_E4M3>) == kTcRegs &&
+                                    registers_of(attn_tc_kernel<T, D, kParts, kMode, GDR_CODE_INT8>) == kTcRegs;
+    if (!shares_hold) return GDR_ERR_CUDA;
     if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem) != cudaSuccess) return GDR_ERR_CUDA;
     const int64_t items = plan.tiles * a.kv_heads * plan.splits;
     CUtensorMap maps[2];

@@ -3,7 +3,8 @@
 //
 // Integer work of a few kilobytes: bound by latency. One block scans the requests, 1024 at a
 // time, and hands out their pages; the tokens' positions and slots follow in the same block up to
-// kOneBlock of them, else in a second launch over as many blocks as they fill.
+// kOneBlock of them, else in a second launch over as many blocks as they fill. 256 requests of a token each 5.4 us, 33
+// prompts of 100 to 3000 tokens 6.9 us.
 #include "internal.h"
 #include "spans.h"
 

@@ -4,7 +4,9 @@
 // product drops whole turns exactly, so a far position costs no precision, and no 64-bit
 // floating arithmetic is needed (the card has little of it). A thread takes the pairs of two
 // 16-byte vectors of a token and goes through several heads with one set of sines and cosines.
-// Bound by memory: every value is read and written once.
+// Bound by memory: every value is read and written once. 16384 tokens of 20 bf16 heads, 168 MB: 33.7 us, 5.0 TB/s; 4099
+// tokens of 10 fp32 heads of 256, 84 MB: 13.4 us. Two heads' loads are under way together, in 64 registers, so
+// that four blocks share an SM: one head after the other took 47 us for the first.
 #include <math.h>
 
 #include "internal.h"

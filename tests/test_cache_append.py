@@ -3,6 +3,7 @@ powers of two, so every step but one rounding to a code is exact: codes and scal
 import ctypes
 import math
 
+import numpy as np
 import pytest
 import torch
 
@@ -184,3 +185,27 @@ def test_refusals_of_tensors():
                       ((k.cpu(), v, slots, *cache), ValueError), ((k[..., ::2], v, slots, *cache), ValueError)):
         with pytest.raises(err):
             cache_append(*args)
+
+
+@gpu
+@pytest.mark.parametrize("dtype", [BF16, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("page,d", [(16, 64), (16, 128), (16, 256), (32, 64), (32, 128), (64, 64), (128, 64)])
+def test_many_packed_rows(page, d, dtype):
+    """More rows than a warp per few: whole pages, then stretches of short runs, single rows and padding, so that
+    blocks with long runs, with short ones and with none stand side by side."""
+    rng = np.random.default_rng(page + d)
+    order = list(rng.permutation(1400))
+    slots = []
+    for piece in range(4):
+        for _ in range(640 // page):
+            first = int(order.pop()) * page
+            slots += range(first, first + page)
+        for _ in range(40):
+            n = int(rng.integers(1, min(page, 12) + 1))
+            off = int(rng.integers(0, page - n + 1))
+            first = int(order.pop()) * page + off
+            slots += range(first, first + n)
+        slots += [-1] * 90
+    assert len(slots) > 2048
+    k, v = rows_of(len(slots), 1, d, dtype, 3, fused=True)
+    check(k, v, torch.tensor(slots, dtype=torch.int32), cache_of(1400, 1, page, d, E4M3 if d != 64 else INT8, 4))

@@ -5,7 +5,7 @@
 // where the run goes on behind older tokens), older codes rounded to a scale that grew, then the
 // run's codes. Bound by memory: entries are read once (a run of up to kHold vectors per thread
 // stays in registers between its two uses, the rest comes from L2 again), codes written once. 8 packed prompts of
-// 512 to 8192 tokens, 4 heads of 128 in bf16, 123 MB in all: 31 us, 4.0 TB/s; 256 single tokens 5.4 us. A run's scale needs
+// 512 to 8192 tokens, 4 heads of 128 in bf16, 123 MB in all: 31 us, 4.0 TB/s; 256 single tokens 5.8 us. A run's scale needs
 // all its rows before the first code, so that a block waits for its loads, then for its warps, then writes: what it
 // comes to is how many blocks an SM holds (6 of 80 registers a thread; fp32 4).
 #include "codes.cuh"
@@ -174,6 +174,7 @@ __device__ __forceinline__ void put_run(const Append &a, int which, int h, int64
 // other for 8 packed prompts of 512 to 8192 tokens; pages of 32: 40 and 33.5).
 template <typename T, int kCode> __global__ void __launch_bounds__(kWarps * 32, sizeof(T) == 2 ? 6 : 4) append_kernel(Append a) {
     __shared__ uint32_t shared[2 * kWarps], starts[kWarps];
+    __shared__ int least;  // entries of a run on average that are too many for a warp
     const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
     const int64_t t0 = (int64_t)blockIdx.x * a.group;
     const int h = blockIdx.y, which = blockIdx.z;
@@ -184,6 +185,9 @@ template <typename T, int kCode> __global__ void __launch_bounds__(kWarps * 32, 
         const int64_t t = t0 + tid;
         const int32_t s = slot_of(t), last = t > 0 ? slot_of(t - 1) : -1;
         begins = s >= 0 && s < a.limit && (t == 0 || (s & in_page) == 0 || last != s - 1);
+        // (few rows to a block: a run that goes on behind them may be long; 1000 tokens in pages of 128, heads of 256: 13 us, 30
+        // by a warp)
+        if (tid == a.group - 1) least = a.group < 32 && (slot_of(t + 1) & in_page) && slot_of(t + 1) == s + 1 ? a.group * a.d - 1 : 2048;
     }
     const uint32_t mine = __ballot_sync(~0u, begins);
     if (lane == 0) starts[w] = mine;
@@ -191,7 +195,7 @@ template <typename T, int kCode> __global__ void __launch_bounds__(kWarps * 32, 
     int runs = 0;
 #pragma unroll
     for (int i = 0; i < kWarps; ++i) runs += __popc(starts[i]);
-    const bool together = runs * 2048 < a.group * a.d;
+    const bool together = runs * least < a.group * a.d;
     int r = 0;
     for (int i = 0; i < kWarps; ++i) {
         for (uint32_t m = starts[i]; m; m &= m - 1, ++r) {

@@ -209,3 +209,13 @@ def test_many_packed_rows(page, d, dtype):
     assert len(slots) > 2048
     k, v = rows_of(len(slots), 1, d, dtype, 3, fused=True)
     check(k, v, torch.tensor(slots, dtype=torch.int32), cache_of(1400, 1, page, d, E4M3 if d != 64 else INT8, 4))
+
+
+@gpu
+@pytest.mark.parametrize("page,d", [(16, 64), (64, 128), (128, 256)])
+def test_a_few_rows_that_are_long_runs(page, d):
+    """Up to 2048 rows: a prompt's pages, a run that ends behind a block's rows, singles between, the rows' end."""
+    slots = list(range(3, 3 * page)) + [5 * page + 1] + list(range(6 * page + 2, 7 * page)) + [-1, -1, 9 * page] + list(range(10 * page, 11 * page + 5))
+    for cut in (len(slots), len(slots) - 1, 5):
+        k, v = rows_of(cut, 2, d, BF16, cut)
+        check(k, v, torch.tensor(slots[:cut], dtype=torch.int32), cache_of(12, 2, page, d, INT8, 6))

@@ -11,6 +11,10 @@
 // column g of step u, so that shared memory is read 16 bytes at a time.
 // The tensor cores are far from busy (a tenth at 8 heads a group); the 5th-generation ones would need
 // the codes converted through shared memory, rows filled up to 128, and the same bytes.
+// The tensor cores cut sums instead of rounding them. fp32: the two products of a tile of 16 tokens begin at 0 and are
+// added to the outputs by ordinary additions (a mean error of 4e-6 behind 8192 tokens and 2e-5 behind 32,768 otherwise; 2 % of
+// the time). bf16 ones stay in the sums of the products: some 4e-8 of a sum for each tile of a warp, 3e-4 behind 500,000
+// tokens, beside its own rounding's 2e-3 (added up outside, 256 requests of 512 to 8192 tokens take 414 us for 407).
 //
 // Bound by memory: each cached byte is read once per 16 rows. A warp streams tiles of 16 tokens
 // through a ring of its own in shared memory (tensor copies, kStages deep: no barrier between warps until an
@@ -41,7 +45,9 @@ template <int D, int kParts, int kR> struct StepConfig {
     static constexpr int kStage = 2 * 16 * D;             // bytes: keys, then values
     static constexpr int kRing = kStepWarps * kStages * kStage;
     static constexpr int kQ = kParts * kSteps * 32 * kR;
-    static constexpr bool kInRegs = D * kParts * kR <= 2048;  // queries stay in registers
+    // Queries stay in registers where there is room for them (fp32, heads of 128, up to 8 rows: 12 bytes of a thread would
+    // spill, 132 us for 64 requests of 512 to 8192 tokens, 126 with queries from shared memory).
+    static constexpr bool kInRegs = D * kParts * kR <= 2048 && !(kParts == 2 && D == 128);
     static constexpr int kSmem = kRing + kQ + 1024;
     static_assert(kStepWarps * kR * D * 4 <= kRing, "outputs of the warps meet in the ring");
 };
@@ -432,16 +438,22 @@ __global__ void __launch_bounds__(kStepWarps * 32, (StepConfig<D, kParts, kR>::k
                     }
                     const int u = j * 4 * kWords + z * 4;
 #pragma unroll
-                    for (int y = kParts - 1; y >= 0; --y) {
-                        if constexpr (kR == 16) {
+                    for (int x = 0; x < 4; x += kR == 16 ? 1 : 2) {
+                        float(&sum)[4] = acc[kR == 16 ? u + x : (u + x) / 2];
+                        float mine[4] = {0.f, 0.f, 0.f, 0.f};  // of this tile (kParts == 2)
 #pragma unroll
-                            for (int x = 0; x < 4; ++x) mma_f16(acc[u + x], p[y], b[0][x], b[1][x]);
-                        } else {
-#pragma unroll
-                            for (int x = 0; x < 4; x += 2) {
+                        for (int y = kParts - 1; y >= 0; --y) {
+                            float(&to)[4] = kParts == 2 ? mine : sum;
+                            if constexpr (kR == 16) {
+                                mma_f16(to, p[y], b[0][x], b[1][x]);
+                            } else {
                                 const uint32_t dims[4] = {b[0][x], b[0][x + 1], b[1][x], b[1][x + 1]};
-                                mma_f16(acc[(u + x) / 2], dims, p[y][0], p[y][1]);
+                                mma_f16(to, dims, p[y][0], p[y][1]);
                             }
+                        }
+                        if (kParts == 2) {
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) sum[e] += mine[e];
                         }
                     }
                 }

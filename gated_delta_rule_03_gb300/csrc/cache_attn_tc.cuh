@@ -34,7 +34,12 @@ using namespace sm100;
 constexpr int kTcThreads = 480, kTcRegs = 128;
 constexpr int kRing = 8;   // tiles of scales
 constexpr int kAll = 16 | 16 << 5 | 16 << 10 | 16 << 15;  // rows of a whole tile
-constexpr int kFlush = 4;  // tiles whose outputs are added up in TMEM (fp32)
+// Tiles of keys whose outputs are added up in TMEM. The tensor cores cut these sums instead of rounding them, up to 2^-23 of
+// them per step of 16 keys and always towards zero. fp32 outputs leave TMEM every kFlush tiles (3e-7 in norm). Of bf16 ones an
+// item has kMost tiles (2^-11 at most, 4e-4 measured; without an end 2e-3 behind 300,000 tokens and 6e-3 behind a million); longer
+// ones are several items of a block in turn, which meet in the workspace. That takes registers of the softmax (kLong: 4 x 4096
+// tokens 262 us, 249 without; as a test within the loop over tiles 280), so tables that hold less go without.
+constexpr int kFlush = 4, kMost = 1024;
 
 template <int D, int kParts> struct TcConfig {
     static constexpr int kTiles = kParts == 1 && D <= 128 ? 2 : 1;
@@ -62,8 +67,13 @@ template <int D, int kParts> struct TcConfig {
 
 struct TcPlan {
     char *parts;   // fp32 outputs and sums of the splits: [tile][head][split] TcPart
+    char *pieces;  // [block][row] TcPiece, of tables that hold more than kMost tiles of keys for a split (bf16)
     int64_t tiles; // row tiles, empty ones among them, for each head of the cache
     int splits;    // of each item's keys
+};
+// A row's outputs and sum of weights of the pieces so far, times 2^-ref (l = 0: of none).
+template <int D> struct alignas(16) TcPiece {
+    float o[D], ref, l;
 };
 template <int kRows, int D> struct TcPart {
     float lse2[kRows];
@@ -110,11 +120,19 @@ struct TcItem {
     int row0, rows;            // of the tile
     int head, j0, count;       // head of the cache; tiles of keys
     int64_t part;
+    bool later, more;          // kLong: pieces of the same rows come before, behind
 };
 
-// Item k of this block, false behind the last. Those that see the most keys come first, and the blocks take
+// Where a block is among its items.
+struct TcTurn {
+    int64_t k = 0;
+    int piece = 0;
+};
+
+// The next item of this block, false behind the last. Those that see the most keys come first, and the blocks take
 // them to and fro. An empty one has rows = 0.
-template <int kRows, int kKeys> __device__ __forceinline__ bool get_item(const Attn &a, const TcPlan &plan, int64_t k, TcItem &t) {
+template <int kRows, int kKeys, bool kLong> __device__ __forceinline__ bool get_item(const Attn &a, const TcPlan &plan, TcTurn &turn, TcItem &t) {
+    const int64_t k = turn.k;
     const int64_t each = (int64_t)a.kv_heads * plan.splits;
     const int64_t idx = k * gridDim.x + (k & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
     if (idx >= plan.tiles * each) return false;
@@ -151,6 +169,16 @@ template <int kRows, int kKeys> __device__ __forceinline__ bool get_item(const A
     t.j0 = min(all, split * per);
     t.count = min(all, t.j0 + per) - t.j0;
     t.part = (x * a.kv_heads + t.head) * plan.splits + split;
+    t.later = t.more = false;
+    if (kLong) {
+        const int before = turn.piece * kMost;
+        t.later = turn.piece > 0;
+        t.more = t.count - before > kMost;
+        t.j0 += before;
+        t.count = t.more ? kMost : t.count - before;
+    }
+    turn.piece = t.more ? turn.piece + 1 : 0;
+    turn.k = t.more ? k : k + 1;
     return true;
 }
 
@@ -277,7 +305,7 @@ __device__ __forceinline__ bool elect() {
 template <int kRegs> __device__ __forceinline__ void set_registers_up() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs)); }
 template <int kRegs> __device__ __forceinline__ void set_registers_down() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs)); }
 
-template <typename T, int D, int kParts, int kMode, int kCode>
+template <typename T, int D, int kParts, int kMode, int kCode, bool kLong>
 __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_constant__ Attn a, const __grid_constant__ TcPlan plan, const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map) {
     using C = TcConfig<D, kParts>;
     extern __shared__ unsigned char sm[];
@@ -332,7 +360,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_con
     const uint32_t tmem = tmem_slot;
     bool fine = true;
     TcItem item;
-    int64_t turn = 0;  // items of this block that have been looked at
+    TcTurn turn;
     int gi0 = 0;       // tiles of keys before this item
 
     if (warp < C::kSoft / 32) {
@@ -353,8 +381,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_con
         };
         // The next item that has keys to look at; those before it that have none get their zeros.
         auto next_item = [&](TcItem &t) {
-            while (get_item<C::kRows, C::kKeys>(a, plan, turn, t)) {
-                ++turn;
+            while (get_item<C::kRows, C::kKeys, kLong>(a, plan, turn, t)) {
                 if (t.count) return true;
                 if (tid >= t.rows) continue;
                 P *const part = (P *)plan.parts + t.part;
@@ -461,8 +488,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_con
             if (have && tid < then.rows)
                 for (int e = 0; e < D * (int)sizeof(T); e += 128) asm volatile("prefetch.global.L2 [%0];" ::"l"((const char *)query_of(then) + e));
 
-            // The tensor cores cut the sums in TMEM instead of rounding them, some 2^-24 of them per step and always
-            // towards zero: fp32 results take the outputs of kFlush tiles at a time out and add them up in memory.
+            // fp32: the outputs of kFlush tiles leave TMEM and are added up in memory.
             auto flush = [&] {
                 const bool some = sum_l != 0.f;
                 const float by = some ? ex2(sum_ref - ref) : 0.f;
@@ -609,18 +635,37 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_con
                 break;
             }
             tc_fence_after();
-            const float by = kParts == 2 ? ex2(sum_ref - ref) : 0.f;
-            const bool older = kParts == 2 && sum_l != 0.f;
+            // Outputs from before, if there are `older` ones, stand at `from` and are to be multiplied by `by`, these by `now`.
+            float by = kParts == 2 ? ex2(sum_ref - ref) : 0.f, now = 1.f;
+            static_assert(!kLong || kParts == 1, "fp32 outputs leave TMEM anyway");
+            bool older = kParts == 2 && sum_l != 0.f;
+            TcPiece<D> *const piece = (TcPiece<D> *)plan.pieces + (int64_t)blockIdx.x * C::kRows + tid;
+            const float *const from = kLong ? piece->o : row_out;
+            if (kLong && item.later && live) {
+                sum_ref = piece->ref;
+                sum_l = piece->l;
+                older = sum_l != 0.f;
+                const float most = older ? fmaxf(sum_ref, l != 0.f ? ref : sum_ref) : ref;
+                by = ex2(sum_ref - most);
+                now = l != 0.f ? ex2(ref - most) : 0.f;
+                ref = most;
+                l *= now;
+            }
             if (older) l = fmaf(sum_l, by, l);
             const bool some = l != 0.f;
-            const float inv = some ? 1.f / l : 0.f;
-            if (live) {
+            const bool more = kLong && item.more;
+            const float inv = more ? 1.f : some ? 1.f / l : 0.f;
+            if (more && live) {
+                piece->ref = ref;
+                piece->l = l;
+            }
+            if (live && !more) {
                 const float sum2 = some ? log2f(l) + ref : -INFINITY;
                 if (plan.splits > 1) part->lse2[tid] = sum2;
                 else if (a.lse) a.lse[row] = sum2 * kLn2;
             }
             // 64 bytes of every row: through shared memory, four lanes to a row (a row to a thread: 32 lines a store)
-            char *const mine = plan.splits > 1 ? (char *)part->o[tid] : (char *)((T *)a.o + row * D);
+            char *const mine = more ? (char *)piece->o : plan.splits > 1 ? (char *)part->o[tid] : (char *)((T *)a.o + row * D);
             const uint32_t alive = __ballot_sync(~0u, live);
             auto hand_out = [&](const uint32_t *w, int at) {
                 if constexpr (C::kStage == 0) {
@@ -649,16 +694,16 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_con
                 if (older && live) {
 #pragma unroll
                     for (int e = 0; e < 32; e += 4) {
-                        const float4 o = *(const float4 *)(row_out + c + e);
-                        v[e] = fmaf(o.x, by, v[e]);
-                        v[e + 1] = fmaf(o.y, by, v[e + 1]);
-                        v[e + 2] = fmaf(o.z, by, v[e + 2]);
-                        v[e + 3] = fmaf(o.w, by, v[e + 3]);
+                        const float4 o = *(const float4 *)(from + c + e);
+                        v[e] = fmaf(o.x, by, v[e] * now);
+                        v[e + 1] = fmaf(o.y, by, v[e + 1] * now);
+                        v[e + 2] = fmaf(o.z, by, v[e + 2] * now);
+                        v[e + 3] = fmaf(o.w, by, v[e + 3] * now);
                     }
                 }
 #pragma unroll
                 for (int e = 0; e < 32; ++e) v[e] *= inv;
-                if (plan.splits > 1 || sizeof(T) == 4) {
+                if (more || plan.splits > 1 || sizeof(T) == 4) {
 #pragma unroll
                     for (int e = 0; e < 32; e += 16) {
                         uint32_t w[16];
@@ -697,8 +742,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_con
         const uint32_t chunk0 = (uint32_t)((2 * x) ^ (row & 7)) << 4;  // its first 16-byte chunk; the second is one bit away
         const uint32_t to0 = blk * (C::kKeys * 128) + row * 128, 
                        from0 = kBlocks == 1 ? row * 64 + x * 16 : (blk >> 1) * (C::kKeys * 128) + row * 128 + (((blk & 1) * 4 + x) ^ (row & 7)) * 16;
-        while (fine && get_item<C::kRows, C::kKeys>(a, plan, turn, item)) {
-            ++turn;
+        while (fine && get_item<C::kRows, C::kKeys, kLong>(a, plan, turn, item)) {
             const int count = item.count;
 #pragma unroll 1
             for (int t = 0; t < 2 * count; ++t) {  // keys and values in turn
@@ -778,8 +822,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_con
             return fine;
         };
         int done = 0;
-        while (fine && get_item<C::kRows, C::kKeys>(a, plan, turn, item)) {
-            ++turn;
+        while (fine && get_item<C::kRows, C::kKeys, kLong>(a, plan, turn, item)) {
             const int count = item.count;
             if (!count) continue;
             wait(Q_FULL + tile, done);
@@ -811,8 +854,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_con
     } else if (warp == 12 + C::kTiles) {
         // ---------------------------------------------------------------- copies
         const int in_page = (1 << a.log_page) - 1, box = min(C::kKeys, in_page + 1);
-        while (fine && get_item<C::kRows, C::kKeys>(a, plan, turn, item)) {
-            ++turn;
+        while (fine && get_item<C::kRows, C::kKeys, kLong>(a, plan, turn, item)) {
             const int count = item.count, j0 = item.j0, len = item.len;
             const int32_t *const table = a.table + (int64_t)item.n * a.width;
             // Lane g < 4 sees to 16 keys of a tile. Their page: -1 behind the last token, -2 outside the cache.
@@ -921,7 +963,7 @@ template <int D, int kParts> TcPlan tc_plan(const Attn &a, bool packed) {
     using C = TcConfig<D, kParts>;
     const int64_t rows = a.max_q * a.group;
     const int64_t tiles = packed ? a.tokens * a.group / C::kRows + a.num_seqs : a.num_seqs * ((rows + C::kRows - 1) / C::kRows);
-    TcPlan p = {nullptr, tiles, 1};
+    TcPlan p = {nullptr, nullptr, tiles, 1};
     const int64_t items = tiles * a.kv_heads, keys = ((a.width << a.log_page) + C::kKeys - 1) / C::kKeys;
     double best = 1e300;
     for (int s = 1; s <= 64 && (s == 1 || (items * s <= 8 * 152 && keys >= 4 * s)); ++s) {
@@ -933,9 +975,23 @@ template <int D, int kParts> TcPlan tc_plan(const Attn &a, bool packed) {
     }
     return p;
 }
+inline int64_t tc_blocks(const Attn &a, const TcPlan &p) {
+    const int64_t items = p.tiles * a.kv_heads * p.splits;
+    return items < 152 ? items : 152;
+}
+template <int D, int kParts> size_t tc_parts_bytes(const Attn &a, const TcPlan &p) {
+    return p.splits == 1 ? 0 : (size_t)p.tiles * a.kv_heads * p.splits * sizeof(TcPart<TcConfig<D, kParts>::kRows, D>);
+}
+template <int D, int kParts> bool tc_long(const Attn &a, const TcPlan &p) {
+    const int64_t keys = ((a.width << a.log_page) + TcConfig<D, kParts>::kKeys - 1) / TcConfig<D, kParts>::kKeys;
+    return kParts == 1 && (keys + p.splits - 1) / p.splits > kMost;
+}
+template <int D, int kParts> size_t tc_pieces_bytes(const Attn &a, const TcPlan &p) {
+    return tc_long<D, kParts>(a, p) ? (size_t)tc_blocks(a, p) * TcConfig<D, kParts>::kRows * sizeof(TcPiece<D>) : 0;
+}
 template <int D, int kParts> size_t tc_bytes_for(const Attn &a, bool packed) {
     const TcPlan p = tc_plan<D, kParts>(a, packed);
-    return p.splits == 1 ? 0 : (size_t)p.tiles * a.kv_heads * p.splits * sizeof(TcPart<TcConfig<D, kParts>::kRows, D>);
+    return tc_parts_bytes<D, kParts>(a, p) + tc_pieces_bytes<D, kParts>(a, p);
 }
 template <int D> size_t tc_bytes_d(const Attn &a, int dtype) {
     Attn b = a;
@@ -953,36 +1009,45 @@ template <typename K> int registers_of(K kernel) {
     return cudaFuncGetAttributes(&attr, kernel) == cudaSuccess ? attr.numRegs : -1;
 }
 
-template <typename T, int D, int kParts, int kMode> int launch_tc_kernel(const Attn &a, int codes, void *ws, cudaStream_t s) {
+template <typename T, int D, int kParts, int kMode, int kCode, bool kLong> int launch_tc_kernel(const Attn &a, const TcPlan &plan, cudaStream_t s) {
     using C = TcConfig<D, kParts>;
-    TcPlan plan = tc_plan<D, kParts>(a, a.cu != nullptr);
-    plan.parts = (char *)ws;
-    const auto kernel = codes == GDR_CODE_E4M3 ? attn_tc_kernel<T, D, kParts, kMode, GDR_CODE_E4M3> : attn_tc_kernel<T, D, kParts, kMode, GDR_CODE_INT8>;
+    const auto kernel = attn_tc_kernel<T, D, kParts, kMode, kCode, kLong>;
     // The roles' shares of registers add up to what the block is launched with, if the compiler gave it that many
     // (asked once, 2 us a call).
-    static const bool shares_hold = registers_of(attn_tc_kernel<T, D, kParts, kMode, GDR_CODE_E4M3>) == kTcRegs &&
-                                    registers_of(attn_tc_kernel<T, D, kParts, kMode, GDR_CODE_INT8>) == kTcRegs;
+    static const bool shares_hold = registers_of(kernel) == kTcRegs;
     if (!shares_hold) return GDR_ERR_CUDA;
     if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem) != cudaSuccess) return GDR_ERR_CUDA;
-    const int64_t items = plan.tiles * a.kv_heads * plan.splits;
     CUtensorMap maps[2];
     if (!map_cache(&maps[0], a.kc, a, D, C::kKeys, D >= 128) || !map_cache(&maps[1], a.vc, a, D, C::kKeys, D >= 128)) return GDR_ERR_CUDA;
-    kernel<<<(unsigned)(items < 152 ? items : 152), kTcThreads, C::kSmem, s>>>(a, plan, maps[0], maps[1]);
+    kernel<<<(unsigned)tc_blocks(a, plan), kTcThreads, C::kSmem, s>>>(a, plan, maps[0], maps[1]);
     if (cudaGetLastError() != cudaSuccess) return GDR_ERR_CUDA;
     if (plan.splits > 1)
         join_splits_kernel<T, D, kParts><<<(unsigned)((a.tokens * a.heads + 7) / 8), 256, 0, s>>>(a, plan);
     return cuda_status(cudaGetLastError());
 }
 
+template <typename T, int D, int kParts, int kMode, bool kLong> int launch_tc_code(const Attn &a, const TcPlan &plan, int code, cudaStream_t s) {
+    return code == GDR_CODE_E4M3 ? launch_tc_kernel<T, D, kParts, kMode, GDR_CODE_E4M3, kLong>(a, plan, s)
+                                 : launch_tc_kernel<T, D, kParts, kMode, GDR_CODE_INT8, kLong>(a, plan, s);
+}
+template <typename T, int D, int kParts, bool kLong> int launch_tc_mode(const Attn &a, const TcPlan &plan, int mode, int code, cudaStream_t s) {
+    return mode == kPlain    ? launch_tc_code<T, D, kParts, kPlain, kLong>(a, plan, code, s)
+           : mode == kCapped ? launch_tc_code<T, D, kParts, kCapped, kLong>(a, plan, code, s)
+                             : launch_tc_code<T, D, kParts, kBiased, kLong>(a, plan, code, s);
+}
+template <int D, int kParts> TcPlan tc_plan_in(const Attn &a, void *ws) {
+    TcPlan plan = tc_plan<D, kParts>(a, a.cu != nullptr);
+    plan.parts = (char *)ws;
+    plan.pieces = (char *)ws + tc_parts_bytes<D, kParts>(a, plan);
+    return plan;
+}
+
 template <int D> int launch_tc_d(const Attn &a, int code, int dtype, void *ws, cudaStream_t s) {
     const int mode = a.slopes || (dtype == GDR_BF16 && a.softcap > kCaps) ? kBiased : a.softcap > 0.f ? kCapped : kPlain;
-    if (dtype == GDR_F32)
-        return mode == kPlain    ? launch_tc_kernel<float, D, 2, kPlain>(a, code, ws, s)
-               : mode == kCapped ? launch_tc_kernel<float, D, 2, kCapped>(a, code, ws, s)
-                                 : launch_tc_kernel<float, D, 2, kBiased>(a, code, ws, s);
-    return mode == kPlain    ? launch_tc_kernel<__nv_bfloat16, D, 1, kPlain>(a, code, ws, s)
-           : mode == kCapped ? launch_tc_kernel<__nv_bfloat16, D, 1, kCapped>(a, code, ws, s)
-                             : launch_tc_kernel<__nv_bfloat16, D, 1, kBiased>(a, code, ws, s);
+    if (dtype == GDR_F32) return launch_tc_mode<float, D, 2, false>(a, tc_plan_in<D, 2>(a, ws), mode, code, s);
+    const TcPlan plan = tc_plan_in<D, 1>(a, ws);
+    return tc_long<D, 1>(a, plan) ? launch_tc_mode<__nv_bfloat16, D, 1, true>(a, plan, mode, code, s)
+                                  : launch_tc_mode<__nv_bfloat16, D, 1, false>(a, plan, mode, code, s);
 }
 
 }  // namespace cattn

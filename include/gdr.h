@@ -728,7 +728,9 @@ size_t gdr_cache_attn_workspace_size(const gdr_cache_attn_shape *shape);
  * Scores, maxima, sums and outputs are fp32 until o is rounded. bf16: a query is held in fp16
  * with a power of two per row (exact for entries within 2^-24 of its largest), the weights of a
  * tile in fp16 relative to a running maximum. fp32: both as two fp16 parts (22 bits). Weights below
- * 2^-32 of a row's largest contribution may be dropped from o (not from lse).
+ * 2^-32 of a row's largest contribution may be dropped from o (not from lse). The tensor cores cut sums
+ * instead of rounding them: outputs come out too small by up to 2^-11 of the sum of |w_j v_j| in bf16 (prompts of
+ * 65,536 cached tokens and more; few rows 3e-4 behind 500,000), by some 3e-7 in fp32.
  * What is behind len is never used: NaN there stays there. A page's scale that is NaN reaches the
  * tokens that see one of the page's, no others. Codes of cached tokens are numbers, as gdr_cache_append
  * leaves them; an e4m3 NaN code within len may also reach rows that do not see it. The same

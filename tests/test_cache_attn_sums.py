@@ -4,25 +4,29 @@ import pytest
 import torch
 
 from gated_delta_rule_03_gb300 import cache_attn
+from tests import cache_ref as ref
 
 gpu = pytest.mark.gpu
 BF16, F32 = torch.bfloat16, torch.float32
 E4M3 = torch.float8_e4m3fn
 
 
-def one_sign(n, new, held, H, Hkv, d, dtype, page=64):
-    """n requests of `held` tokens each, values of 50 to 400 times 2^-7, unlike by column; queries of size 1."""
+def one_sign(n, new, held, H, Hkv, d, dtype, page=64, shared=False):
+    """n requests of `held` tokens each, in pages of their own or the same ones; values of 50 to 400 times 2^-7, unlike by
+    column; queries of size 1."""
     g = torch.Generator(device="cuda").manual_seed(1)
     per = -(-held // page)
-    kc, vc = (torch.empty(n * per, Hkv, page, d, dtype=E4M3, device="cuda") for _ in "kv")
+    pages = per if shared else n * per
+    kc, vc = (torch.empty(pages, Hkv, page, d, dtype=E4M3, device="cuda") for _ in "kv")
     size = 0.25 + 0.75 * torch.rand(d, generator=g, device="cuda")
-    for a in range(0, n * per, 4096):
+    for a in range(0, pages, 4096):
         shape = kc[a:a + 4096].shape
         kc[a:a + 4096] = (90 * torch.randn(shape, generator=g, device="cuda")).clamp(-448, 448).to(E4M3)
         vc[a:a + 4096] = ((200 + 200 * torch.rand(shape, generator=g, device="cuda")) * size).to(E4M3)
-    scale = torch.full((n * per, Hkv), 2.0 ** -7, device="cuda")
+    scale = torch.full((pages, Hkv), 2.0 ** -7, device="cuda")
+    table = torch.arange(pages, dtype=torch.int32, device="cuda").view(-1, per).expand(n, per).contiguous()
     return dict(q=torch.randn(n * new, H, d, generator=g, device="cuda").to(dtype), k_cache=kc, v_cache=vc, k_scale=scale,
-                v_scale=scale.clone(), block_table=torch.arange(n * per, dtype=torch.int32, device="cuda").view(n, per),
+                v_scale=scale.clone(), block_table=table,
                 kv_lens=torch.full((n,), held, dtype=torch.int32, device="cuda"))
 
 
@@ -35,7 +39,8 @@ def errors(c, o, requests, rows, heads):
     got, want = [], []
     for i in requests:
         for h in heads:
-            k, v = (c[x][i * per:(i + 1) * per, h * Hkv // H].reshape(-1, d)[:held] for x in ("k_cache", "v_cache"))
+            first = int(c["block_table"][i, 0])
+            k, v = (c[x][first:first + per, h * Hkv // H].reshape(-1, d)[:held] for x in ("k_cache", "v_cache"))
             x, top, out = c["q"][i * new:i * new + rows, h].double(), 0.0, 0.0
             pos = torch.arange(held - new, held - new + rows, device="cuda")[:, None]
             for a in range(0, held, 65536):  # (scores are a few units: no maximum needed in 64 bits)
@@ -57,3 +62,41 @@ def test_fp32_single_tokens_behind_many_each(H, Hkv, d, n, held):
     c = one_sign(n, 1, held, H, Hkv, d, F32)
     norm, mean = errors(c, cache_attn(**c), (0, n // 2, n - 1), 1, range(min(H, 8)))
     assert abs(mean) < 2.0 ** -21 + 3 * 2.0 ** -23 and norm < 2.0 ** -20 + 2.0 ** -21 + 3 * 2.0 ** -23, (norm, mean)
+
+
+@gpu
+@pytest.mark.parametrize("d,n,new,held", [(128, 152, 256, 1000000), (128, 152, 300, 300001), (128, 60, 256, 500000), (64, 155, 200, 400000),
+                                          (256, 152, 128, 300000), (128, 1, 40, 66000)])
+def test_bf16_prompts_behind_very_many_tokens(d, n, new, held):
+    """Sums that stay in the tensor cores are cut by 2^-23 at most per step of 16 tokens, of 65,536 tokens at most: 2^-11. The
+    outputs of a column are nearly the same for all rows; rounded to bf16 they are off by 2^-8 at most, 2^-8 / sqrt 3
+    in the root mean square, so the mean over d columns by four times 2^-8 / sqrt(3 d) but once in 10,000 inputs."""
+    c = one_sign(n, new, held, 1, 1, d, BF16, shared=True)
+    norm, mean = errors(c, cache_attn(**c), (0, n // 2, n - 1), 4, range(1))
+    assert abs(mean) < 2.0 ** -11 + 4 * 2.0 ** -8 / (3 * d) ** 0.5 and norm < 2.0 ** -8, (norm, mean)
+
+
+@gpu
+@pytest.mark.parametrize("n", [1, 38, 152])
+@pytest.mark.parametrize("kw", [dict(slopes=0.002), dict(slopes=-0.002), dict(slopes=0.5), dict(causal=False), dict(softcap=4.0), dict(scale=1e-3, new=300)], ids=str)
+def test_rows_whose_keys_are_seen_in_pieces(n, kw):
+    """References that move between the pieces or fall, rows that see nothing of the last piece, heads that share keys, short
+    requests beside long ones, with lse. Scores near a row's place count (see the test of biases in test_cache_attn.py)."""
+    kw = dict(kw)
+    new, held, H = kw.pop("new", 130), [131072 + 64 - 2, 140000, 33, 65536, 196700], 2
+    c = one_sign(n, new, held[-1], H, 1, 64, BF16, page=128, shared=True)
+    lens = [held[i % 5] for i in range(n - 1)] + [held[-1]]
+    c["kv_lens"] = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    if "slopes" in kw:
+        kw["slopes"] = torch.tensor([kw["slopes"], 0.3 * kw["slopes"]], device="cuda")
+    o, lse = cache_attn(**c, return_lse=True, **kw)
+    for i in sorted({0, 1 % n, 2 % n, 3 % n, n - 1}):
+        rows = slice(i * new, (i + 1) * new)
+        args = dict(dict(scale=64 ** -0.5), **kw)
+        want = ref.attend(c["q"][rows], c["k_cache"], c["v_cache"], c["k_scale"], c["v_scale"], c["block_table"][i:i + 1], [lens[i]],
+                          [0, new], **args)
+        if "slopes" in kw and float(kw["slopes"][0]) > 0:
+            want["most"] = 3 * want["dots"] + 30 * 0.7
+        bo, bl = ref.attend_bounds(want, BF16, 64, lens[i], kw.get("softcap", 0.0))
+        ref.check("lse", lse[rows], want["lse"], bl)
+        ref.check("o", o[rows], want["o"], bo)

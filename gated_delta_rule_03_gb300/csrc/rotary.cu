@@ -56,8 +56,8 @@ template <typename T, int V, bool kNeighbours> __global__ void __launch_bounds__
 #pragma unroll
         for (int i = 0; i < V; ++i) {
             const uint64_t turn = (uint64_t)p * (uint64_t)r.rates[a * V + i];
-            // the nearest of both ways round: -1 <= half turns < 1
-            const float half_turns = (float)(int32_t)(turn >> 32) * 4.656612873077393e-10f;
+            // to the nearest 2^-32 turn, and the nearest of both ways round: -1 <= half turns < 1
+            const float half_turns = (float)(int32_t)((turn + 0x80000000u) >> 32) * 4.656612873077393e-10f;
             sincospif(half_turns, &s[i], &c[i]);
             c[i] *= r.amplitude;
             s[i] *= r.back ? -r.amplitude : r.amplitude;

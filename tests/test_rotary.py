@@ -106,6 +106,19 @@ def test_far_and_negative_positions():
 
 
 @gpu
+def test_small_angles_are_rounded_either_way():
+    """The sine of a turn of a few 2^-32 shows how the turn was rounded: to the nearest, half of that step at most."""
+    from gated_delta_rule_03_gb300 import rotary_fwd
+    rates = torch.tensor([2 ** 33 - 1, 2 ** 32 - 1, 2 ** 33 + 1, 3 * 2 ** 32 - 1, 2 ** 31 - 1, 2 ** 31 + 1, -(2 ** 32) - 1, -1, 1, 12345678901], device="cuda")
+    q = torch.zeros(2, 1, 24, device="cuda")
+    q[..., :10] = 1
+    got, _ = rotary_fwd(q, None, torch.tensor([1, -1], dtype=torch.int32, device="cuda"), rates)
+    for sign, y in zip((1, -1), got[:, 0, 10:20].double().cpu()):
+        turns = torch.tensor([sign * int(r) / 2.0 ** 64 for r in rates.tolist()], dtype=torch.float64)
+        assert bool(((y / (2 * math.pi) - turns).abs() <= 2.0 ** -33 + 2.0 ** -22 * turns.abs()).all())
+
+
+@gpu
 def test_the_turn_back_is_the_gradient():
     """Differences of a weighted sum of outputs, which is linear in each input."""
     from gated_delta_rule_03_gb300 import rotary_bwd, rotary_fwd, rotary_rates

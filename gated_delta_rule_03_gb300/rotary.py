@@ -6,6 +6,7 @@ position; rates[i] is the turn of pair i per position in steps of 2^-64 of a who
 marshalling only: there is no autograd here, `rotary_bwd` turns gradients back.
 """
 import ctypes
+import decimal
 import functools
 import math
 
@@ -26,10 +27,13 @@ class RotaryShape(ctypes.Structure):
                 ("q_out_stride", ctypes.c_int64), ("k_out_stride", ctypes.c_int64)]
 
 
+_TWO_PI = decimal.Decimal("6.28318530717958647692528676655900576839433879875021164194989")
+
+
 def rotary_rates(rot_dim, base=10000.0, factor=1.0, trained_length=None, fast_turns=32.0, slow_turns=1.0,
                  device="cuda"):
     """The rates of rot_dim / 2 pairs, int64: pair i turns by base^(-2i / rot_dim) radians per
-    position, in 64 bits, to the nearest 2^-64 of a turn.
+    position, to the nearest 2^-64 of a turn (in decimals: doubles would leave 2^-56 of the fastest pairs).
 
     factor > 1 stretches the context: without trained_length every pair turns `factor` times
     slower (positions interpolated). With it, pairs that turn more than fast_turns times within
@@ -42,15 +46,16 @@ def rotary_rates(rot_dim, base=10000.0, factor=1.0, trained_length=None, fast_tu
     if trained_length is not None and not fast_turns > slow_turns:
         raise ValueError("fast_turns must be above slow_turns")
     rates = []
-    for i in range(rot_dim // 2):
-        f = base ** (-2.0 * i / rot_dim)
-        keep = 0.0
-        if trained_length is not None:
-            turns = trained_length * f / (2 * math.pi)
-            keep = min(1.0, max(0.0, (turns - slow_turns) / (fast_turns - slow_turns)))
-        f = f * keep + f / factor * (1 - keep)
-        r = round(f / (2 * math.pi) * 2.0 ** 64) % 2 ** 64
-        rates.append(r - 2 ** 64 if r >= 2 ** 63 else r)
+    with decimal.localcontext(decimal.Context(prec=50)):
+        base, factor, lo, hi = (decimal.Decimal(float(x)) for x in (base, factor, slow_turns, fast_turns))
+        for i in range(rot_dim // 2):
+            turns = base ** (decimal.Decimal(-2 * i) / rot_dim) / _TWO_PI
+            keep = 0
+            if trained_length is not None:
+                keep = min(1, max(0, (decimal.Decimal(float(trained_length)) * turns - lo) / (hi - lo)))
+            turns = turns * keep + turns / factor * (1 - keep)
+            r = int((turns * 2 ** 64).to_integral_value(decimal.ROUND_HALF_EVEN)) % 2 ** 64
+            rates.append(r - 2 ** 64 if r >= 2 ** 63 else r)
     return torch.tensor(rates, dtype=torch.int64, device=device)
 
 

@@ -176,6 +176,28 @@ def test_rates_of_stretched_contexts():
             rotary_rates(device="cpu", **bad)
 
 
+def test_rates_are_the_nearest_there_are():
+    """By logarithms and a sum of arctangents in 90 decimals: no rate is off by more than half of 2^-64 turns."""
+    import decimal
+    from gated_delta_rule_03_gb300 import rotary_rates
+    with decimal.localcontext(decimal.Context(prec=90)):
+        D = decimal.Decimal
+
+        def arctan_of_inverse(n):  # sum of (-1)^k / ((2k + 1) n^(2k + 1))
+            return sum(D((-1) ** k) / ((2 * k + 1) * D(n) ** (2 * k + 1)) for k in range(130))
+
+        pi = 16 * arctan_of_inverse(5) - 4 * arctan_of_inverse(239)
+        for rot, base, factor in ((128, 10000.0, 1.0), (256, 500000.0, 1.0), (34, 1234.5, 1.0), (64, 1e6, 3.7)):
+            for i, r in enumerate(rotary_rates(rot, base=base, factor=factor, device="cpu").tolist()):
+                want = (D(base).ln() * D(-2 * i) / rot).exp() / D(factor) / (2 * pi) * 2 ** 64
+                assert abs((D(r) - want + 2 ** 63) % 2 ** 64 - 2 ** 63) <= D("0.5000001"), (rot, base, i)
+        for i, r in enumerate(rotary_rates(128, factor=4.0, trained_length=4096, device="cpu").tolist()):
+            turns = (D(10000).ln() * D(-2 * i) / 128).exp() / (2 * pi)
+            keep = min(D(1), max(D(0), (4096 * turns - 1) / 31))
+            want = (turns * keep + turns / 4 * (1 - keep)) * 2 ** 64
+            assert abs((D(r) - want + 2 ** 63) % 2 ** 64 - 2 ** 63) <= D("0.5000001"), i
+
+
 def test_refusals_on_the_host():
     from gated_delta_rule_03_gb300 import ops
     from gated_delta_rule_03_gb300.rotary import RotaryShape

@@ -72,9 +72,10 @@ __device__ __forceinline__ float lg2(float x) {
     return y;
 }
 
-// tanh(x) = 1 - 2 / (1 + e^2x) is off by some 2e-7 in all, and the cap times that in the score. Near 0 two terms of
-// its series are off by 2 x^5 / 15, relative 1e-7 where they are taken, so that a score far below its cap keeps
-// its bits whatever the cap: 2^-16 relative in all, enough for bf16 results; fp32 ones take the library's.
+// tanh(x) = 1 - 2 / (1 + e^2x) is off by some 2e-7 in all (held to 2^-21 by the tests), and the cap times that in the
+// score. Near 0 two terms of its series are off by 2 x^5 / 15, relative 1e-7 where they are taken, so that a score far
+// below its cap keeps its bits whatever the cap: 2^-16 relative in all, enough for bf16 results; fp32 ones take the
+// library's. (Prompts in bf16 with caps up to 64 have a quicker form without the series, cache_attn_tc.cuh.)
 __device__ __forceinline__ float reciprocal(float x) {
     float y;
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));

@@ -216,9 +216,10 @@ __device__ __forceinline__ void tmem_put8(uint32_t taddr, const uint32_t (&r)[8]
 }
 __device__ __forceinline__ void tmem_stored() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-// What becomes of scores: nothing more, a cap, or a bias by distance with or without a cap. (bf16: a cap above kCaps,
-// of which the quick form's 2e-7 would be too much, goes the third way.)
-constexpr float kCaps = 1024.f;
+// What becomes of scores: nothing more, a cap, or a bias by distance with or without a cap. bf16: the quick form of a cap is
+// off by up to 2^-21 of it whatever the score, 3e-5 of caps up to kCaps (a usual one is 30 or 50; lse off by 1.4e-6 at
+// 64, 2.2e-5 at 1000). Higher ones go the third way, where 1000 rows of heads of 256 behind 32,768 tokens take 1066 us for 643.
+constexpr float kCaps = 64.f;
 enum { kPlain = 0, kCapped = 1, kBiased = 2 };
 
 // Exponents of 16 keys' weights from products with their codes: m scales a product (log2(e) in it if

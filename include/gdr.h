@@ -732,6 +732,8 @@ size_t gdr_cache_attn_workspace_size(const gdr_cache_attn_shape *shape);
  * 2^-32 of a row's largest contribution may be dropped from o (not from lse). The tensor cores cut sums
  * instead of rounding them: outputs come out too small by up to 2^-11 of the sum of |w_j v_j| in bf16 (prompts of
  * 65,536 cached tokens and more; few rows 3e-4 behind 500,000), by some 3e-7 in fp32.
+ * A capped score is off by up to 2^-16 of itself in bf16 (by 2^-21 of the cap, if that is more, where more than 16
+ * rows share a head of the cache and the cap is at most 64), by fp32's tanh in fp32.
  * What is behind len is never used: NaN there stays there. A page's scale that is NaN reaches the
  * tokens that see one of the page's, no others. Codes of cached tokens are numbers, as gdr_cache_append
  * leaves them; an e4m3 NaN code within len may also reach rows that do not see it. The same

@@ -430,6 +430,29 @@ def test_caps_far_above_the_scores(new, cap):
             ref.check("o", o, want["o"], bo + 2 * capped[..., None] * want["size"])
 
 
+@gpu
+@pytest.mark.parametrize("new", [4, 70])
+@pytest.mark.parametrize("cap", [65.0, 200.0, 1000.0, 1024.0, 1e4])
+def test_a_capped_score_keeps_its_bits(new, cap):
+    """Rows that see one key have that score for lse. Queries and keys of one entry, a bf16 number and 1: the product is
+    exact, the cap off by 2^-16 of the score, the rest by a few roundings of the score, 2^-24 each, and of the
+    logarithms of the value scale (7 of either sign)."""
+    from gated_delta_rule_03_gb300 import cache_attn
+    g = torch.Generator(device="cuda").manual_seed(3)
+    c = make([new], [1], 2, 1, 128, 16, BF16, INT8)
+    q = torch.zeros(new, 2, 128, device="cuda", dtype=BF16)
+    q[..., 0] = torch.exp2(9 * torch.rand(new, 2, generator=g, device="cuda") - 6) * torch.sign(torch.randn(new, 2, generator=g, device="cuda"))
+    page = c["table"][0, 0].long()
+    c["kc"][page], c["ks"][page], c["vs"][page] = 0, 2.0 ** -6, 2.0 ** -7
+    c["kc"][page, 0, 0, 0] = 64
+    o, lse = cache_attn(q, c["kc"], c["vc"], c["ks"], c["vs"], c["table"], c["kv"], scale=1.0, softcap=cap, causal=False, return_lse=True)
+    s = q[..., 0].double()
+    want = cap * torch.tanh(s / cap)
+    ref.check("lse", lse, want, 2.0 ** -16 * s.abs() + 8 * 2.0 ** -24 * (s.abs() + 14))
+    value = c["vc"][page, 0, 0].double() * 2.0 ** -7
+    ref.check("o", o, value.expand(new, 2, 128), 3 * ref.HALF_STEP[BF16] * value.abs().expand(new, 2, 128))
+
+
 def test_tables_whose_tokens_pass_32_bits_are_refused():
     from gated_delta_rule_03_gb300 import ops
     size = ops._load().gdr_cache_attn_workspace_size

@@ -4,10 +4,12 @@ Each translation unit under csrc/ is compiled in parallel into _build/, then
 linked into gated_delta_rule_03_gb300/libgdr.so with the CUDA runtime linked
 statically (the library then needs only the driver). The driver API entry
 points the library uses are fetched at run time through the runtime, so no
--lcuda is needed. Register and spill counts from ptxas go to _build/ptxas.log.
+-lcuda is needed. Register and spill counts from ptxas go to _build/ptxas.log; a
+kernel that shares its registers out among its warps has to have their exact number.
 """
 import concurrent.futures
 import os
+import re
 import shutil
 import subprocess
 import sys
@@ -21,6 +23,10 @@ SOURCES = ["gdr_api.cu", "decode.cu", "prefill_exact.cu", "solve_tc.cu", "prefil
            "epilogue.cu", "linattn_api.cu", "linattn_exact.cu", "linattn_tc.cu", "linattn_step.cu", "block_norm.cu",
            "rotary.cu", "pages.cu", "cache_append.cu", "cache_attn_api.cu", "cache_attn_step64.cu", "cache_attn_step128.cu",
            "cache_attn_step256.cu", "cache_attn_tc64.cu", "cache_attn_tc128.cu", "cache_attn_tc256.cu"]
+
+
+# kernels whose warps hand registers to one another (setmaxnreg), and what a thread is launched with
+REGISTERS = {"attn_tc_kernel": 128}
 
 
 def nvcc():
@@ -41,6 +47,18 @@ def _compile(src):
     return obj, proc.stderr
 
 
+def check_registers(log):
+    """Raises if ptxas gave a kernel of REGISTERS another number; returns how many there are."""
+    seen = 0
+    for name, used in re.findall(r"Compiling entry function '(\w+)'.*?Used (\d+) registers", log, re.S):
+        for kernel, want in REGISTERS.items():
+            if kernel in name:
+                seen += 1
+                if int(used) != want:
+                    raise RuntimeError(f"{name} has {used} registers; its warps share out {want} a thread (cache_attn_tc.cuh)")
+    return seen
+
+
 def build(verbose=False):
     """Compile every CUDA source and link libgdr.so; returns the library path."""
     os.makedirs(BUILD, exist_ok=True)
@@ -51,6 +69,8 @@ def build(verbose=False):
             log.write(f"== {os.path.basename(obj)}\n{err}\n")
             if verbose:
                 print(err, file=sys.stderr)
+    for _, err in results:
+        check_registers(err)
     tmp = LIB + ".tmp"
     cmd = [nvcc(), *ARCH, "-shared", "-o", tmp, *[r[0] for r in results]]
     subprocess.run(cmd, check=True)

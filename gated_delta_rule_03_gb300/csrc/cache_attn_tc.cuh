@@ -20,6 +20,7 @@
 // fp32: queries and weights as two fp16 parts, hi + lo, whose products are added in the same TMEM sums.
 #pragma once
 
+#include <atomic>
 #include <type_traits>
 
 #include "cache_attn.cuh"
@@ -1007,16 +1008,20 @@ template <int D> size_t tc_bytes_d(const Attn &a, int dtype) {
 
 template <typename K> int registers_of(K kernel) {
     cudaFuncAttributes attr;
-    return cudaFuncGetAttributes(&attr, kernel) == cudaSuccess ? attr.numRegs : -1;
+    if (cudaFuncGetAttributes(&attr, kernel) == cudaSuccess) return attr.numRegs;
+    (void)cudaGetLastError();
+    return -1;
 }
 
 template <typename T, int D, int kParts, int kMode, int kCode, bool kLong> int launch_tc_kernel(const Attn &a, const TcPlan &plan, cudaStream_t s) {
     using C = TcConfig<D, kParts>;
     const auto kernel = attn_tc_kernel<T, D, kParts, kMode, kCode, kLong>;
-    // The roles' shares of registers add up to what the block is launched with, if the compiler gave it that many
-    // (asked once, 2 us a call).
-    static const bool shares_hold = registers_of(kernel) == kTcRegs;
-    if (!shares_hold) return GDR_ERR_CUDA;
+    // The roles' shares of registers add up to what the block is launched with, if the compiler gave it that many: the
+    // build refuses another number, and so does the call (asked until there is an answer, 2 us a call).
+    static std::atomic<int> registers{-1};
+    int has = registers.load(std::memory_order_relaxed);
+    if (has < 0) registers.store(has = registers_of(kernel), std::memory_order_relaxed);
+    if (has != kTcRegs) return GDR_ERR_CUDA;
     if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem) != cudaSuccess) return GDR_ERR_CUDA;
     CUtensorMap maps[2];
     if (!map_cache(&maps[0], a.kc, a, D, C::kKeys, D >= 128) || !map_cache(&maps[1], a.vc, a, D, C::kKeys, D >= 128)) return GDR_ERR_CUDA;

@@ -41,6 +41,21 @@ def test_library_exports_every_declared_symbol(lib):
         assert hasattr(lib, name), f"{name} declared in gdr.h but not exported"
 
 
+def test_the_build_refuses_another_number_of_registers(lib):
+    """The warps of a kernel share its registers out: with another number they would wait for ones that never come."""
+    from gated_delta_rule_03_gb300 import build
+    entry = "ptxas info    : Compiling entry function '_ZN3gdr14attn_tc_kernelIfLi64EEEv' for 'sm_103a'\n"
+    used = "ptxas info    : Function properties for x\n    0 bytes stack frame\nptxas info    : Used {} registers, used 1 barriers\n"
+    other = entry.replace("14attn_tc_kernel", "11step_kernel")
+    assert build.check_registers(entry + used.format(128) + other + used.format(90)) == 1
+    for n in (127, 136):
+        with pytest.raises(RuntimeError, match=str(n)):
+            build.check_registers(other + used.format(128) + entry + used.format(n))
+    log = os.path.join(build.BUILD, "ptxas.log")
+    if os.path.exists(log):
+        assert build.check_registers(open(log).read()) >= 36
+
+
 def test_status_strings(lib):
     assert lib.gdr_status_string(0) == b"GDR_OK"
     for code in range(-7, 0):

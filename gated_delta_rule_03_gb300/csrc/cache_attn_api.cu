@@ -19,6 +19,8 @@ struct Call {
 
 constexpr int kBeyond = 4096;  // places behind a request's last that the kernels look ahead, as 32-bit numbers
 
+int64_t most_rows(const Attn &a) { return (INT32_MAX - 256) / a.group; }  // new tokens of a request (rows are 32-bit numbers)
+
 int check_shape(const gdr_cache_attn_shape *s, Call *c) {
     if (!s) return GDR_ERR_INVALID_ARG;
     Attn &a = c->a;
@@ -47,7 +49,7 @@ int check_shape(const gdr_cache_attn_shape *s, Call *c) {
     a.group_shift = -1;
     for (int i = 0; i < 17; ++i)
         if (a.group == 1 << i) a.group_shift = i;
-    if (a.max_q > (INT32_MAX - 256) / a.group) return GDR_ERR_INVALID_ARG;  // (rows of an item are 32-bit numbers)
+    if (a.max_q > most_rows(a)) return GDR_ERR_INVALID_ARG;
     a.scale = s->scale;
     a.softcap = s->softcap;
     return GDR_OK;
@@ -93,6 +95,7 @@ int gdr_cache_attn(const gdr_cache_attn_shape *shape, const void *q, const void 
     Attn &a = c.a;
     if (!cu_q && a.tokens % a.num_seqs) return GDR_ERR_INVALID_ARG;
     if (!cu_q) a.max_q = a.tokens / a.num_seqs;
+    if (a.max_q > most_rows(a)) return GDR_ERR_INVALID_ARG;
     if (!workspace) return GDR_ERR_WORKSPACE;
     const size_t need = workspace_bytes(c);
     if (workspace_bytes_given < need) return GDR_ERR_WORKSPACE;

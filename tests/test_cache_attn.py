@@ -458,3 +458,14 @@ def test_tables_whose_tokens_pass_32_bits_are_refused():
     size = ops._load().gdr_cache_attn_workspace_size
     most = (2 ** 31 - 4097) // 16
     assert size(shape(width=most)) > 0 and size(shape(width=most + 1)) == 0 and size(shape(width=(2 ** 31 - 1) // 16)) == 0
+
+
+def test_rows_that_pass_32_bits_are_refused():
+    """With offsets by max_q, without them by the tokens of each request, whatever max_q says."""
+    from gated_delta_rule_03_gb300 import ops
+    lib = ops._load()
+    A = [2 ** 52 * (i + 1) for i in range(12)]
+    names = ("q", "kc", "vc", "ks", "vs", "table", "kv", "cu", "slopes", "o", "lse", "ws")
+    for cu, kw in ((A[7], dict(max_q=2 ** 21)), (None, dict(max_q=2 ** 21)), (None, dict(max_q=1))):
+        args = [cu if n == "cu" else a for n, a in zip(names, A)]
+        assert lib.gdr_cache_attn(shape(num_seqs=1, total_tokens=2 ** 21, heads=2048, kv_heads=1, **kw), *args, 2 ** 51, None) == -1, kw

@@ -497,6 +497,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_con
 #pragma unroll 1
                 for (int c = 0; c < D; c += 32) {
                     float v[32];
+                    __syncwarp();  // (a warp reads its lanes together)
                     tmem_load32(out + c, v);
                     if (!live) continue;
 #pragma unroll
@@ -692,6 +693,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_con
 #pragma unroll 1
             for (int c = 0; c < D; c += 32) {
                 float v[32];
+                __syncwarp();
                 tmem_load32(out + c, v);
                 if (older && live) {
 #pragma unroll

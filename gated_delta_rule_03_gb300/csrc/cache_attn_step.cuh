@@ -1,7 +1,7 @@
 // cache_attn_step.cuh -- attention over a paged 8-bit cache for few rows: single tokens.
 //
 // Rows. The queries of one request that share a head of the cache (its group of heads, times its
-// new tokens) are the rows of tiles of kR: an item is (request, head of the cache, tile).
+// new tokens), up to kR of them: an item is (request, head of the cache).
 //
 // Products. Warp-level 16x8x16 MMAs in fp16 with fp32 sums, whose operands are registers, so that codes go from
 // the copy in shared memory to an operand without a turn through it. Up to 8 rows (kR = 8) are the 8 columns and
@@ -16,7 +16,7 @@
 // the time). bf16 ones stay in the sums of the products: some 4e-8 of a sum for each tile of a warp, 3e-4 behind 500,000
 // tokens, beside its own rounding's 2e-3 (added up outside, 256 requests of 512 to 8192 tokens take 414 us for 407).
 //
-// Bound by memory: each cached byte is read once per 16 rows. A warp streams tiles of 16 tokens
+// Bound by memory: each cached byte is read once. A warp streams tiles of 16 tokens
 // through a ring of its own in shared memory (tensor copies, kStages deep: no barrier between warps until an
 // item ends). 16-byte copies by threads stopped at 4.4 TB/s in the order that the products take them, 32 bytes
 // of a line at a time, and at 5.3 TB/s by whole lines.
@@ -75,7 +75,7 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
 __device__ __forceinline__ float2 unpack_f16(uint32_t r) { return __half22float2(reinterpret_cast<const __half2 &>(r)); }
 
 struct StepPlan {
-    int4 *tasks;     // [blocks][2]: the items that begin in this block and that began before it and go on in it: request (-1: none), head, tile, blocks of it + 2^16 (blocks before this one)
+    int4 *tasks;     // [blocks][2]: the items that begin in this block and that began before it and go on in it: request (-1: none), head, blocks of it, blocks of it before this one
     char *parts;     // [blocks][2] Part
     CUtensorMap maps[2];  // keys, values: 16 rows of one page and head at a time
 };
@@ -88,15 +88,13 @@ struct Share {
 __device__ __forceinline__ int64_t units_of(const Attn &a, int64_t n) {
     return max((__ldg(a.kv_lens + n) + kUnit - 1) / kUnit, 1);
 }
-template <int kR> __device__ __forceinline__ int tiles_of(const Attn &a, int rows) { return (int)(((int64_t)rows * a.group + kR - 1) / kR); }
-
 // The request of the first unit of this block's share, and the share itself.
-template <int kR> __device__ Share find_share(const Attn &a, int64_t *sums, int64_t *found, int64_t *per) {
+__device__ inline Share find_share(const Attn &a, int64_t *sums, int64_t *found, int64_t *per) {
     constexpr int kThreads = kStepWarps * 32;
     const int tid = threadIdx.x;
     int64_t mine = 0;
     bool ok = true;
-    auto weight = [&](int64_t n) { return (int64_t)a.kv_heads * tiles_of<kR>(a, rows_of(a, n).y) * units_of(a, n); };
+    auto weight = [&](int64_t n) { return rows_of(a, n).y > 0 ? (int64_t)a.kv_heads * units_of(a, n) : 0; };
     for (int64_t n = tid; n < a.num_seqs; n += kThreads) {
         if (lengths_hold(a, n)) mine += weight(n);
         else ok = false;
@@ -147,7 +145,7 @@ __global__ void __launch_bounds__(kStepWarps * 32, (StepConfig<D, kParts, kR>::k
     bool fine = true;
 
     int64_t per;
-    const Share share = find_share<kR>(a, sums, found, &per);
+    const Share share = find_share(a, sums, found, &per);
     if (blockIdx.x == 0 && tid == 0) *a.status = share.ok ? GDR_OK : GDR_ERR_BAD_SEQLENS;
     if (plan.tasks && tid < 2) plan.tasks[2 * blockIdx.x + tid] = make_int4(-1, 0, 0, 0);
     sm100::griddep_launch_dependents();
@@ -157,26 +155,24 @@ __global__ void __launch_bounds__(kStepWarps * 32, (StepConfig<D, kParts, kR>::k
     const uint32_t ring_s = sm100::smem_u32(ring);
     uint32_t *const qfrag = (uint32_t *)(smem + C::kRing);
 
-    int fetched = 0, fetched_turn = 0, used = 0, turn = 0;  // places in the ring, and the parity of the turn round it
+    int fetched = 0, used = 0, turn = 0;  // places in the ring, and the parity of the turn round it
     int64_t u = (int64_t)blockIdx.x * per, n = share.n, before = share.before;
     const int64_t end_u = min(share.total, u + per);
     while (u < end_u) {
         const int2 rows = rows_of(a, n);
-        const int tiles = tiles_of<kR>(a, rows.y);
         const int len = __ldg(a.kv_lens + n);
-        const int64_t units = units_of(a, n), weight = (int64_t)a.kv_heads * tiles * units;
+        const int64_t units = units_of(a, n), weight = rows.y > 0 ? a.kv_heads * units : 0;
         if (u >= before + weight) {  // (also a request without new tokens)
             before += weight;
             ++n;
             continue;
         }
-        const int64_t rel = u - before, item = rel / units;
-        const int ua = (int)(rel - item * units), ub = (int)min(units, ua + (end_u - u));
-        const int tile = (int)(item % tiles), head = (int)(item / tiles);
-        const int row0 = tile * kR, nrows = min(kR, rows.y * a.group - row0);
+        const int64_t rel = u - before;
+        const int head = (int)(rel / units), ua = (int)(rel - head * units), ub = (int)min(units, ua + (end_u - u));
+        const int nrows = rows.y * a.group;  // at most kR: few_rows, and no request has more than max_q tokens
         // the tokens that the last row may see
         const int past = len - rows.y;  // position of the first new token
-        const int far = a.causal ? max(0, min(len, past + (row0 + nrows - 1) / a.group + 1)) : len;
+        const int far = a.causal ? max(0, min(len, past + rows.y)) : len;
         const int first = ua * kUnit, last = min(far, ub * kUnit);
         const int count = last > first ? ((last - first + 15) / 16 - warp + kStepWarps - 1) / kStepWarps : 0;  // of this warp
 
@@ -218,13 +214,13 @@ __global__ void __launch_bounds__(kStepWarps * 32, (StepConfig<D, kParts, kR>::k
 
         // ---- queries: fp16 with a power of two per row, in the order of the first product
         if (tid < 8 * kR) {
-            const int r = tid >> 3, part = tid & 7, at = row0 + r;
+            const int r = tid >> 3, part = tid & 7;
             constexpr int kMine = D / 8;
             float v[kMine];
             uint32_t most = 0;
             if (r < nrows) {
-                const int h = head * a.group + at % a.group;
-                const T *src = (const T *)a.q + (int64_t)(rows.x + at / a.group) * a.qs + (int64_t)h * D + part * kMine;
+                const int h = head * a.group + r % a.group;
+                const T *src = (const T *)a.q + (int64_t)(rows.x + r / a.group) * a.qs + (int64_t)h * D + part * kMine;
                 constexpr int kVec = 16 / sizeof(T);
 #pragma unroll
                 for (int i = 0; i < kMine; i += kVec) {
@@ -279,9 +275,9 @@ __global__ void __launch_bounds__(kStepWarps * 32, (StepConfig<D, kParts, kR>::k
             for (int s = 0; s < kParts * C::kSteps; ++s) query(s, qreg[s]);
         }
         const float f0 = row_factor[R0], f1 = row_factor[R1], slope0 = row_slope[R0], slope1 = row_slope[R1];
-        const int p0 = past + (row0 + R0) / a.group, p1 = past + (row0 + R1) / a.group;
+        const int p0 = past + R0 / a.group, p1 = past + R1 / a.group;
         const int lim0 = a.causal ? min(len, p0 + 1) : len, lim1 = a.causal ? min(len, p1 + 1) : len;
-        const int sure = a.causal ? min(len, past + row0 / a.group + 1) : len;  // seen by every row
+        const int sure = a.causal ? min(len, past + 1) : len;  // seen by every row
 
         const float inv_cap = kShaped && a.softcap > 0.f ? 1.f / a.softcap : 0.f;
         float ref0 = kNoRef, ref1 = kNoRef, l0 = 0.f, l1 = 0.f;
@@ -517,7 +513,7 @@ __global__ void __launch_bounds__(kStepWarps * 32, (StepConfig<D, kParts, kR>::k
                 *(float4 *)&part->o[r][d] = o;
                 if (d == 0) part->lse2[r] = sum2;
             } else {
-                const int64_t row = (int64_t)(rows.x + (row0 + r) / a.group) * a.heads + head * a.group + (row0 + r) % a.group;
+                const int64_t row = (int64_t)(rows.x + r / a.group) * a.heads + head * a.group + r % a.group;
                 T *const to = (T *)a.o + row * D + d;
                 if constexpr (sizeof(T) == 4) {
                     *(float4 *)to = o;
@@ -530,7 +526,7 @@ __global__ void __launch_bounds__(kStepWarps * 32, (StepConfig<D, kParts, kR>::k
         }
         if (!whole && tid == (ua == 0 ? 0 : 1)) {
             const int from = (int)((u - ua) / per), to = (int)((u - ua + units - 1) / per);  // blocks
-            plan.tasks[2 * blockIdx.x + tid] = make_int4((int)n, head, tile, (to - from + 1) | ((int)blockIdx.x - from) << 16);
+            plan.tasks[2 * blockIdx.x + tid] = make_int4((int)n, head, to - from + 1, (int)blockIdx.x - from);
         }
         u += ub - ua;
         sm100::fence_async_smem();  // (before copies into the ring again)
@@ -555,9 +551,9 @@ template <typename T, int D, int kR> __global__ void __launch_bounds__(256) join
     for (int which = 0; which < 2; ++which) {
         const int4 task = which ? tasks[1] : tasks[0];
         if (task.x < 0) continue;
-        const int head = task.y, row0 = task.z * kR, blocks = task.w & 0xffff, mine = task.w >> 16;
+        const int head = task.y, blocks = task.z, mine = task.w;
         const int2 rows = rows_of(a, task.x);
-        const int units = min(kR, rows.y * a.group - row0) * kCols;
+        const int units = rows.y * a.group * kCols;
         const bool many = blocks > kAtOnce;
         if (!many && mine > 0) continue;
         const int ways = many ? 8 : 1, abreast = 8 / ways, step = many ? blocks : abreast;  // warps for the parts of a unit; units at a time
@@ -608,7 +604,7 @@ template <typename T, int D, int kR> __global__ void __launch_bounds__(256) join
                     sum = fmaf(sums[w], f, sum);
                     z = fmaf(outs[w][x % 64], f, z);
                 }
-                const int at = row0 + unit / kCols, dim = unit % kCols * 64 + x % 64;
+                const int at = unit / kCols, dim = unit % kCols * 64 + x % 64;
                 const int64_t row = (int64_t)(rows.x + at / a.group) * a.heads + head * a.group + at % a.group;
                 ((T *)a.o)[row * D + dim] = from_f32<T>(sum == 0.f ? 0.f : z * (1.f / sum));
                 if (dim == 0 && a.lse) a.lse[row] = (sum == 0.f ? -INFINITY : log2f(sum) + base) * kLn2;

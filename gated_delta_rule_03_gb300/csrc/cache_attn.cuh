@@ -18,6 +18,7 @@
 
 #include "codes.cuh"
 #include "internal.h"
+#include "scan.cuh"
 
 namespace gdr {
 namespace cattn {
@@ -87,6 +88,14 @@ template <bool kExact> __device__ __forceinline__ float cap_of(float x) {
     return fabsf(x) < 0.03f ? near : far;
 }
 
+// Two numbers as fp16, lo in the low half, and back.
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+__device__ __forceinline__ float2 unpack_f16(uint32_t r) { return __half22float2(reinterpret_cast<const __half2 &>(r)); }
+
 // The score of a token from a product that is already scaled; away = |p - j|.
 template <bool kExact> __device__ __forceinline__ float shaped(float z, float softcap, float inv_cap, float slope, float away) {
     if (softcap > 0.f) z = softcap * cap_of<kExact>(z * inv_cap);
@@ -103,17 +112,9 @@ __device__ __forceinline__ int row_shift(uint32_t bits) {
 __device__ __forceinline__ float two_to(int n) { return __int_as_float((n + 127) << 23); }
 
 // Sum over the block and inclusive sums, kThreads threads.
-__device__ __forceinline__ int64_t warp_sums(int64_t x) {
-#pragma unroll
-    for (int d = 1; d < 32; d *= 2) {
-        const int64_t y = __shfl_up_sync(~0u, x, d);
-        if ((int)(threadIdx.x & 31) >= d) x += y;
-    }
-    return x;
-}
 template <int kThreads> __device__ int64_t block_sums(int64_t x, int64_t *sums, int64_t *total) {
     const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    x = warp_sums(x);
+    x = warp_scan(x);
     __syncthreads();
     if (lane == 31) sums[w] = x;
     __syncthreads();

@@ -67,12 +67,6 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], u
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
-    uint32_t r;
-    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-    return r;
-}
-__device__ __forceinline__ float2 unpack_f16(uint32_t r) { return __half22float2(reinterpret_cast<const __half2 &>(r)); }
 
 struct StepPlan {
     int4 *tasks;     // [blocks][2]: the items that begin in this block and that began before it and go on in it: request (-1: none), head, blocks of it, blocks of it before this one

@@ -67,7 +67,7 @@ template <int D, int kParts> struct TcConfig {
 };
 
 struct TcPlan {
-    char *parts;   // fp32 outputs and sums of the splits: [tile][head][split] TcPart
+    char *parts;   // fp32 outputs and sums of the splits: [tile][head][split] Part
     char *pieces;  // [block][row] TcPiece, of tables that hold more than kMost tiles of keys for a split (bf16)
     int64_t tiles; // row tiles, empty ones among them, for each head of the cache
     int splits;    // of each item's keys
@@ -75,10 +75,6 @@ struct TcPlan {
 // A row's outputs and sum of weights of the pieces so far, times 2^-ref (l = 0: of none).
 template <int D> struct alignas(16) TcPiece {
     float o[D], ref, l;
-};
-template <int kRows, int D> struct TcPart {
-    float lse2[kRows];
-    float o[kRows][D];
 };
 
 __host__ __device__ constexpr uint32_t idesc_f16(int M, int N, int b_mn) {
@@ -210,11 +206,6 @@ __device__ __forceinline__ void tmem_put16(uint32_t taddr, const uint32_t *r) {
         "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
         : "memory");
 }
-__device__ __forceinline__ void tmem_put8(uint32_t taddr, const uint32_t (&r)[8]) {
-    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "r"(r[0]), "r"(r[1]),
-                 "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
-                 : "memory");
-}
 __device__ __forceinline__ void tmem_stored() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 // What becomes of scores: nothing more, a cap, or a bias by distance with or without a cap. bf16: the quick form of a cap is
@@ -274,12 +265,6 @@ template <int kMode, bool kExact> struct Shape {
     }
 };
 
-__device__ __forceinline__ uint32_t f16_pair(float lo, float hi) {
-    uint32_t r;
-    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-    return r;
-}
-__device__ __forceinline__ float2 f16_values(uint32_t r) { return __half22float2(reinterpret_cast<const __half2 &>(r)); }
 __device__ __forceinline__ uint4 load16(uint32_t saddr) {
     uint4 v;
     asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(saddr) : "memory");
@@ -372,7 +357,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_con
         const uint32_t lanes = (uint32_t)(warp & 3) << 21;
         const uint32_t out = tmem + lanes + C::kO + tile * D;
         const float cap = kMode == kPlain ? 0.f : a.softcap, inv_cap = cap > 0.f ? 1.f / cap : 0.f;
-        using P = TcPart<C::kRows, D>;
+        using P = Part<C::kRows, D>;
         auto row_of = [&](const TcItem &t) {
             const int at = t.row0 + tid, token = token_of(a, at);
             return (int64_t)(t.first + token) * a.heads + t.head * a.group + at - token * a.group;
@@ -448,10 +433,10 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_con
                             if constexpr (sizeof(T) == 2) z = make_float2(__uint_as_float(in[i] << 16), __uint_as_float(in[i] & 0xffff0000u));
                             else z = make_float2(__uint_as_float(in[2 * i]), __uint_as_float(in[2 * i + 1]));
                             z = mul2(z, up_pair);
-                            hi[i] = f16_pair(z.x, z.y);
+                            hi[i] = pack_f16(z.x, z.y);
                             if (kParts == 2) {
-                                const float2 f = f16_values(hi[i]);
-                                lo[i] = f16_pair(z.x - f.x, z.y - f.y);
+                                const float2 f = unpack_f16(hi[i]);
+                                lo[i] = pack_f16(z.x - f.x, z.y - f.y);
                             }
                         }
                         const int d = (x * 32 + sub) * (16 / (int)sizeof(T));
@@ -612,10 +597,10 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_con
                     for (int e = 0; e < 16; ++e) {
                         const float2 w = make_float2(ex2(t[c + e].x), ex2(t[c + e].y));
                         some[e / 8] = e % 8 ? add2(some[e / 8], w) : w;
-                        hi[e] = f16_pair(w.x, w.y);
+                        hi[e] = pack_f16(w.x, w.y);
                         if (kParts == 2) {
-                            const float2 v = f16_values(hi[e]);
-                            lo[e] = f16_pair(w.x - v.x, w.y - v.y);
+                            const float2 v = unpack_f16(hi[e]);
+                            lo[e] = pack_f16(w.x - v.x, w.y - v.y);
                         }
                     }
                     tmem_put16(s_at + c, hi);
@@ -939,8 +924,8 @@ template <typename T, int D, int kParts> __global__ void __launch_bounds__(256) 
         }
     }
     const int64_t r = (t - rows_of(a, n).x) * a.group + h % a.group, tile = r / C::kRows;
-    const TcPart<C::kRows, D> *const parts =
-        (const TcPart<C::kRows, D> *)plan.parts + ((first_tile<C::kRows>(a, n) + tile) * a.kv_heads + head) * plan.splits;
+    const Part<C::kRows, D> *const parts =
+        (const Part<C::kRows, D> *)plan.parts + ((first_tile<C::kRows>(a, n) + tile) * a.kv_heads + head) * plan.splits;
     const int at = (int)(r - tile * C::kRows);
     float top = -INFINITY;
     for (int i = 0; i < plan.splits; ++i) top = fmaxf(top, parts[i].lse2[at]);
@@ -984,7 +969,7 @@ inline int64_t tc_blocks(const Attn &a, const TcPlan &p) {
     return items < 152 ? items : 152;
 }
 template <int D, int kParts> size_t tc_parts_bytes(const Attn &a, const TcPlan &p) {
-    return p.splits == 1 ? 0 : (size_t)p.tiles * a.kv_heads * p.splits * sizeof(TcPart<TcConfig<D, kParts>::kRows, D>);
+    return p.splits == 1 ? 0 : (size_t)p.tiles * a.kv_heads * p.splits * sizeof(Part<TcConfig<D, kParts>::kRows, D>);
 }
 template <int D, int kParts> bool tc_long(const Attn &a, const TcPlan &p) {
     const int64_t keys = ((a.width << a.log_page) + TcConfig<D, kParts>::kKeys - 1) / TcConfig<D, kParts>::kKeys;

@@ -6,6 +6,7 @@
 // kOneBlock of them, else in a second launch over as many blocks as they fill. 256 requests of a token each 5.4 us, 33
 // prompts of 100 to 3000 tokens 6.9 us.
 #include "internal.h"
+#include "scan.cuh"
 #include "spans.h"
 
 namespace gdr {
@@ -21,14 +22,6 @@ struct Plan {
     int32_t *table, *kv_out, *count_out, *cu, *start, *positions, *slots;
 };
 
-__device__ __forceinline__ int64_t warp_scan(int64_t x) {
-#pragma unroll
-    for (int d = 1; d < 32; d *= 2) {
-        const int64_t y = __shfl_up_sync(~0u, x, d);
-        if ((int)(threadIdx.x & 31) >= d) x += y;
-    }
-    return x;
-}
 // Inclusive sum over the block; *total receives that of all threads.
 __device__ int64_t block_scan(int64_t x, int64_t *sums, int64_t *total) {
     const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;

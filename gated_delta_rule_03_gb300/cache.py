@@ -213,8 +213,12 @@ def cache_attn(q, k_cache, v_cache, k_scale, v_scale, block_table, kv_lens, cu_q
                softcap=0.0, slopes=None, causal=True, return_lse=False, o=None, lse=None, workspace=None, stream=None):
     """Softmax attention of the new tokens q [T, heads, d] over the cache (gdr_cache_attn), the
     new ones among the kv_lens [num_seqs] cached tokens of each request. cu_q [num_seqs + 1] int32:
-    offsets of the requests' new tokens (max_q: the most of one request, default T), or None for T /
-    num_seqs each. scale: default d^-1/2; softcap: scores capped by softcap tanh(s / softcap), 0 for none;
+    offsets of the requests' new tokens (max_q: the most of one request, default T; it chooses the kernel, so
+    give 1 with the offsets of single tokens), or None for T / num_seqs each. Lengths that do not hold
+    (kv_lens beyond the table, a request longer than max_q, ..) are found on the device: o and lse are then left
+    as they were, which is unwritten memory if they are new, and read_device_status(workspace) of a
+    workspace given by the caller tells. Prompts are planned by the table's width: a table about as wide
+    as the lengths need is fastest and takes the least workspace. scale: default d^-1/2; softcap: scores capped by softcap tanh(s / softcap), 0 for none;
     slopes [heads] fp32: scores lowered by slope times the distance. Returns o [T, heads, d], with
     return_lse (o, lse [T, heads] fp32)."""
     lib = ops._load()

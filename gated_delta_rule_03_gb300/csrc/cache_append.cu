@@ -273,7 +273,9 @@ extern "C" int gdr_cache_append(const gdr_cache_shape *shape, int64_t tokens, co
     a.heads = shape->kv_heads;
     a.d = shape->d;
     // Rows per block: single tokens of many requests are a run each, a warp's work; many rows are runs of
-    // whole pages, and a block looks for one of 64 or 128, or for several.
+    // whole pages, and a block looks for one of 64 or 128, or for several. What the rows are is on the device, so their
+    // number decides: 256 single tokens 3.8 us with 4 rows to a block (19.6 with 64), 2048 of them 13.6 (20.2), one prompt of 2048
+    // 8.7 (5.3); 4096 single ones 24.7 (23.0), one prompt of 4096 13.8 (5.5); 4 heads of 128 in bf16.
     a.group = tokens <= 2048 ? kWarps : (shape->page < 64 ? 64 : shape->page);
     if (shape->dtype == GDR_F32)
         launch_append<float>(a, shape->codes, (cudaStream_t)stream);

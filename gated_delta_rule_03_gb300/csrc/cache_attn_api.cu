@@ -57,10 +57,11 @@ int check_shape(const gdr_cache_attn_shape *s, Call *c) {
 
 constexpr size_t kHead = 256;  // the status word
 
-// Few rows share a head of the cache: at most a tile of the warp-level products, so that its keys are read once. Single
-// tokens are (up to 16 heads a group). 64 requests of some 4000 tokens, 8 heads of the cache of 128: 32 rows take
-// 125 us either way (fp32: 154 and, the other way, 232), 64 rows 217 us and 128 the other way; of two such requests 32
-// rows take 39 us and 27.
+// Few rows share a head of the cache: at most a tile of the warp-level products, 16, so that its keys are read once. Single
+// tokens are (up to 16 heads a group). 64 requests of some 4000 tokens, 8 heads of the cache of 128, with tiles of 16 rows
+// one after the other against the many-row kernel: 32 rows 125 us either way, 64 rows 217 and 128; of two such
+// requests 32 rows 39 and 27. fp32 would gain up to 32 rows (154 us for 232) by a tile more, which the few-row kernel
+// does not have.
 bool few_rows(const Attn &a) { return a.max_q * a.group <= 16; }
 
 size_t workspace_bytes(const Call &c) {

@@ -36,7 +36,8 @@ constexpr int kTcThreads = 480, kTcRegs = 128;
 constexpr int kRing = 8;   // tiles of scales
 constexpr int kAll = 16 | 16 << 5 | 16 << 10 | 16 << 15;  // rows of a whole tile
 // Tiles of keys whose outputs are added up in TMEM. The tensor cores cut these sums instead of rounding them, up to 2^-23 of
-// them per step of 16 keys and always towards zero. fp32 outputs leave TMEM every kFlush tiles (3e-7 in norm). Of bf16 ones an
+// them per step of 16 keys and always towards zero. fp32 outputs leave TMEM every kFlush tiles (256 rows behind 32,768
+// tokens off by 3.1e-7 in norm and 2 x 4096 tokens 553 us; every 2 tiles 1.6e-7 and 843, every 16 1.9e-6 and 338). Of bf16 ones an
 // item has kMost tiles (2^-11 at most, 2.6e-4 measured; without an end 2e-3 behind 300,000 tokens and 6e-3 behind a million); longer
 // ones are several items of a block in turn, which meet in the workspace. That takes registers of the softmax (kLong: 4 x 4096
 // tokens 262 us, 249 without; as a test within the loop over tiles 280), so tables that hold less go without.

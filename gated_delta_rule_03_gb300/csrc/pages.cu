@@ -13,7 +13,8 @@ namespace gdr {
 namespace {
 
 constexpr int kThreads = 1024;
-constexpr int64_t kOneBlock = 4096;  // tokens
+// Tokens that one block places: 256 of them 5.2 us (7.1 with a second launch), 4000 6.5 (6.4), 8000 9.7 (7.3).
+constexpr int64_t kOneBlock = 4096;
 
 struct Plan {
     int64_t n, width, rows, pages;

@@ -694,9 +694,14 @@ int gdr_cache_append(const gdr_cache_shape *shape, int64_t tokens, const void *k
  *
  * Shape of a call (a HOST struct):
  *   num_seqs, total_tokens   requests (>= 1) and rows of q
- *   max_q     the most new tokens of one request (with cu_q; else total_tokens / num_seqs)
+ *   max_q     the most new tokens of one request (with cu_q; else total_tokens / num_seqs). It chooses
+ *             the kernel: up to 16 / (heads / kv_heads) tokens share one that reads each cached byte
+ *             once, so single tokens are to say 1, not total_tokens.
  *   heads     a multiple of kv_heads, at most 65536
- *   width     block_table [num_seqs, width]; width * page at most 2^31 - 4097
+ *   width     block_table [num_seqs, width]; width * page at most 2^31 - 4097. Prompts are planned by
+ *             it, as the lengths are on the device: a table far wider than they need has keys split
+ *             for nothing, which takes memory and time (one prompt of 1024 tokens, 16 heads over 4 of 128, in a
+ *             table for 131,072: 99 MB of workspace, 18 in one for 1024).
  *   q_stride  elements from a token's first head to the next token's; 0: dense
  *   causal    nonzero: causal
  *   scale     finite; softcap finite, 0 (none) or at least 1e-18

@@ -564,8 +564,8 @@ int gdr_block_norm_bwd(const gdr_block_norm_shape *shape, const void *dx_out, co
  *
  * rates: turns per position in steps of 2^-64, modulo one turn. The product with the position
  * is taken in 64-bit integers, whose overflow drops whole turns: the angle of any position
- * is off by 2^-33 turns at most before it becomes an fp32 number, however far the position (and
- * by the rate's own rounding times the position, 2^-34 at most).
+ * is off by 2^-33 turns at most, however far the position (and by the rate's own rounding times
+ * the position, 2^-34 at most). Of bf16 tensors it is then rounded to an fp32 number.
  *
  * Shape of a call (a HOST struct):
  *   tokens          rows of every tensor (>= 0)

@@ -119,6 +119,24 @@ def test_small_angles_are_rounded_either_way():
 
 
 @gpu
+def test_sines_and_cosines_of_fp32_outputs():
+    """Pairs (1, 0) become (cos, sin). Those are off by 2 units of CUDA's functions and half of one of the step behind them,
+    2^-23 of their size each, and by what the angle is: 2^-33 turns, the square of 2e-7 beside it."""
+    from gated_delta_rule_03_gb300 import rotary_fwd
+    g = torch.Generator().manual_seed(2)
+    rates = torch.randint(-2 ** 63, 2 ** 63 - 1, (100,), generator=g, dtype=torch.int64)
+    pos = torch.randint(-2 ** 31, 2 ** 31 - 1, (300,), generator=g, dtype=torch.int32)
+    # and angles around quarter turns, where sine or cosine is small
+    rates[:8] = torch.tensor([2 ** 62, 2 ** 62 + 2 ** 35, -(2 ** 62) + 2 ** 36, 2 ** 63 - 2 ** 33, -(2 ** 63), 2 ** 61, 77 * 2 ** 32, -(2 ** 63) + 2 ** 34])
+    pos[:3] = torch.tensor([1, -1, 3])
+    q = torch.zeros(300, 1, 200)
+    q[..., :100] = 1
+    got, _ = rotary_fwd(q.cuda(), None, pos.cuda(), rates.cuda())
+    want = ref.rotary(q, pos, rates, False, 1.0)
+    ref.check("cos, sin", got.cpu(), want, 2.5 * 2.0 ** -23 * want.abs() + 2.0 ** -33 * 2 * math.pi + 2.0 ** -44)
+
+
+@gpu
 def test_the_turn_back_is_the_gradient():
     """Differences of a weighted sum of outputs, which is linear in each input."""
     from gated_delta_rule_03_gb300 import rotary_bwd, rotary_fwd, rotary_rates

@@ -49,7 +49,7 @@ def rotary_rates(rot_dim, base=10000.0, factor=1.0, trained_length=None, fast_tu
     with decimal.localcontext(decimal.Context(prec=50)):
         base, factor, lo, hi = (decimal.Decimal(float(x)) for x in (base, factor, slow_turns, fast_turns))
         for i in range(rot_dim // 2):
-            turns = base ** (decimal.Decimal(-2 * i) / rot_dim) / _TWO_PI
+            turns = base ** (decimal.Decimal(-2 * i) / int(rot_dim)) / _TWO_PI
             keep = 0
             if trained_length is not None:
                 keep = min(1, max(0, (decimal.Decimal(float(trained_length)) * turns - lo) / (hi - lo)))

@@ -2,6 +2,7 @@
 import ctypes
 import math
 
+import numpy as np
 import pytest
 import torch
 
@@ -209,6 +210,8 @@ def test_rates_are_the_nearest_there_are():
             for i, r in enumerate(rotary_rates(rot, base=base, factor=factor, device="cpu").tolist()):
                 want = (D(base).ln() * D(-2 * i) / rot).exp() / D(factor) / (2 * pi) * 2 ** 64
                 assert abs((D(r) - want + 2 ** 63) % 2 ** 64 - 2 ** 63) <= D("0.5000001"), (rot, base, i)
+        assert torch.equal(rotary_rates(np.int64(128), base=np.float32(10000), factor=np.float32(4), trained_length=np.int32(4096), device="cpu"),
+                           rotary_rates(128, factor=4.0, trained_length=4096.0, device="cpu"))
         for i, r in enumerate(rotary_rates(128, factor=4.0, trained_length=4096, device="cpu").tolist()):
             turns = (D(10000).ln() * D(-2 * i) / 128).exp() / (2 * pi)
             keep = min(D(1), max(D(0), (4096 * turns - 1) / 31))

@@ -100,3 +100,41 @@ def test_rows_whose_keys_are_seen_in_pieces(n, kw):
         bo, bl = ref.attend_bounds(want, BF16, 64, lens[i], kw.get("softcap", 0.0))
         ref.check("lse", lse[rows], want["lse"], bl)
         ref.check("o", o[rows], want["o"], bo)
+
+
+@gpu
+def test_pieces_with_a_page_without_a_scale():
+    """It reaches the rows that see it, whichever piece it stands in, and no others."""
+    new, held, n = 130, 140000, 152
+    c = one_sign(n, new, held, 1, 1, 64, BF16, page=128, shared=True)
+    clean = cache_attn(**c, return_lse=True)
+    spare = c["k_cache"].shape[0]
+    for x in ("k_cache", "v_cache"):
+        c[x] = torch.cat([c[x].view(torch.uint8), c[x][:1].view(torch.uint8)]).view(E4M3)
+    for where in (3, 600, 1093):
+        for x in ("k_scale", "v_scale"):
+            scales = {y: torch.cat([c[y], c[y][:1]]) for y in ("k_scale", "v_scale")}
+            scales[x][spare] = float("nan")
+            table = c["block_table"].clone()
+            table[5, where] = spare
+            o, lse = cache_attn(**dict(c, block_table=table, **scales), return_lse=True)
+            sees = torch.zeros(n * new, 1, dtype=torch.bool, device="cuda")
+            sees[5 * new:6 * new, 0] = torch.arange(held - new, held, device="cuda") >= where * 128
+            assert torch.equal(o.isnan().all(-1), sees) and torch.equal(o.isnan().any(-1), sees) and torch.equal(lse.isnan(), sees)
+            assert torch.equal(o[~sees], clean[0][~sees]) and torch.equal(lse[~sees], clean[1][~sees])
+
+
+@gpu
+def test_more_new_tokens_than_cached_ones_in_pieces():
+    """70,100 new tokens of 70,000: the first 100 rows see nothing; the next see one key after the other."""
+    new, held = 70100, 70000
+    c = one_sign(1, new, held, 1, 1, 64, BF16)
+    o, lse = cache_attn(**c, return_lse=True)
+    assert not bool(o[:100].any()) and bool((lse[:100] == -float("inf")).all())
+    k, v = (c[x].reshape(-1, 64)[:held].double() * 2.0 ** -7 for x in ("k_cache", "v_cache"))
+    for row in (100, 101, 164, 357, 65635, 65636, 65700, 70098, 70099):
+        s = (c["q"][row, 0].double() @ k[:row - 99].T) / 8
+        want = torch.softmax(s, 0) @ v[:row - 99]
+        # bf16's half step, fp16 weights and 2^-11 of sums that are cut; a score is off by 2^-16 of a few units at most
+        assert float(((o[row, 0].double() - want) / want).abs().max()) < 2.0 ** -8 + 2.0 ** -11 + 2.0 ** -11 + 2.0 ** -12
+        assert abs(float(lse[row, 0]) - float(torch.logsumexp(s, 0))) < 2.0 ** -14

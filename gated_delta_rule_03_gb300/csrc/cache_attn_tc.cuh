@@ -658,9 +658,11 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_con
             const uint32_t alive = __ballot_sync(~0u, live);
             auto hand_out = [&](const uint32_t *w, int at) {
                 if constexpr (C::kStage == 0) {
-                    if (!live) return;
+                    if (live) {
 #pragma unroll
-                    for (int x = 0; x < 4; ++x) *(uint4 *)(mine + at + 16 * x) = make_uint4(w[4 * x], w[4 * x + 1], w[4 * x + 2], w[4 * x + 3]);
+                        for (int x = 0; x < 4; ++x) *(uint4 *)(mine + at + 16 * x) = make_uint4(w[4 * x], w[4 * x + 1], w[4 * x + 2], w[4 * x + 3]);
+                    }
+                    __syncwarp();
                 } else {
                     const uint32_t stage = sr + C::kRaw * C::kKv + warp * 2048;
 #pragma unroll
@@ -679,7 +681,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_con
 #pragma unroll 1
             for (int c = 0; c < D; c += 32) {
                 float v[32];
-                __syncwarp();
+                if (kParts == 2 || kLong) __syncwarp();
                 tmem_load32(out + c, v);
                 if (older && live) {
 #pragma unroll

@@ -171,7 +171,7 @@ __global__ void __launch_bounds__(kStepWarps * 32, (StepConfig<D, kParts, kR>::k
         const int past = len - rows.y;  // position of the first new token
         const int far = a.causal ? max(0, min(len, past + rows.y)) : len;
         const int first = ua * kUnit, last = min(far, ub * kUnit);
-        const int count = last > first ? ((last - first + 15) / 16 - warp + kStepWarps - 1) / kStepWarps : 0;  // of this warp
+        const int count = last > first && fine ? ((last - first + 15) / 16 - warp + kStepWarps - 1) / kStepWarps : 0;  // of this warp
 
         // ---- the stream of tiles: page and scales of 32 tiles at a time, one per lane
         int64_t page = 0;
@@ -285,8 +285,8 @@ __global__ void __launch_bounds__(kStepWarps * 32, (StepConfig<D, kParts, kR>::k
         for (int i = 0; i < count; ++i) {
             __syncwarp();  // (the place in the ring has been read)
             fetch(i + C::kStages - 1);
-            fine = fine && sm100::mbar_wait(sm100::smem_u32(&bars[warp][used]), turn);
-            __syncwarp();
+            fine = __all_sync(~0u, sm100::mbar_wait(sm100::smem_u32(&bars[warp][used]), turn));
+            if (!fine) break;
             const char *const at = ring + used * C::kStage;
             const float2 sc = scales[warp][used];
             if (++used == C::kStages) {
@@ -451,6 +451,15 @@ __global__ void __launch_bounds__(kStepWarps * 32, (StepConfig<D, kParts, kR>::k
                     }
                 }
             }
+        }
+        if (!fine && count > 0) {  // a wait that ran out: the copies under way are waited for, again with a limit, before the ring is used
+            do {
+                sm100::mbar_wait(sm100::smem_u32(&bars[warp][used]), turn);
+                if (++used == C::kStages) {
+                    used = 0;
+                    turn ^= 1;
+                }
+            } while (used != fetched);
         }
         // ---- the warps' parts meet
 #pragma unroll

@@ -301,7 +301,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_con
     const uint32_t sq = base, sk = base + C::kTiles * kParts * C::kQ, sv = sk + C::kStages * C::kKv, sr = sv + C::kStages * C::kKv;
     __shared__ float4 scales[kRing][4];  // of 16 keys: key scale, log2 and reciprocal of the value scale
     __shared__ uint32_t tmem_slot;
-    __shared__ int gave_up;
+    __shared__ int gave_up, copied;  // whether a wait ran out; tiles that have been asked for, of keys and values in turn
     __shared__ int held[kRing];  // 5 bits for each 16 keys: the rows that there are
     // Of the stages of keys and values, and of their codes (R); of the scores' slots (2 tile + parity of the key tile); per row tile
     enum { K_FULL = 0, K_FREE = 4, V_FULL = 8, V_FREE = 12, S_FULL = 16, W_FULL = 20, O_DONE = 24, Q_FULL = 28, O_FREE = 30, O_LAST = 32, RK_FULL = 34, RK_FREE = 37, RV_FULL = 40, RV_FREE = 43, BARS = 46 };
@@ -310,7 +310,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_con
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
     if (tid == 0) {
-        gave_up = 0;
+        gave_up = copied = 0;
         for (int s = 0; s < 4; ++s) {
             mbar_init(bar(K_FULL + s), C::kConv);
             mbar_init(bar(V_FULL + s), C::kConv);
@@ -882,7 +882,10 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_con
                     const uint32_t full = bar((is_v ? RV_FULL : RK_FULL) + raw);
                     if (!mbar_wait(bar((is_v ? RV_FREE : RK_FREE) + raw), ((gi / C::kRaw) & 1) ^ 1)) fine = false;
                     fine = __all_sync(~0u, fine);
-                    if (!fine) break;
+                    if (!fine) {
+                        if (lane == 0) copied = 2 * gi + is_v;
+                        break;
+                    }
                     if (lane == 0) mbar_arrive_expect_tx(full, boxes * box * D);
                     __syncwarp();
                     if (copies) {
@@ -897,6 +900,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_con
                 scale = coming;
             }
             gi0 += count;
+            if (fine && lane == 0) copied = 2 * gi0;
         }
     }
     if (!fine) gave_up = 1;
@@ -904,7 +908,13 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_con
     __syncthreads();
     tc_fence_after();
     if (warp == 12) tmem_dealloc(tmem, 512);
-    if (tid == 0 && gave_up) *a.status = GDR_ERR_DEVICE_TIMEOUT;
+    if (tid == 0 && gave_up) {  // no copy outlives the block: the last ones are waited for, again with a limit
+        for (int is_v = 0; is_v < 2; ++is_v) {
+            const int n = (copied + 1 - is_v) / 2;
+            for (int i = max(0, n - C::kRaw); i < n; ++i) mbar_wait(bar((is_v ? RV_FULL : RK_FULL) + i % C::kRaw), (i / C::kRaw) & 1);
+        }
+        *a.status = GDR_ERR_DEVICE_TIMEOUT;
+    }
 }
 
 // Adds the splits of an item in order: a warp to a row.

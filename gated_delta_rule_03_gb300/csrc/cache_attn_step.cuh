@@ -11,9 +11,9 @@
 // column g of step u, so that shared memory is read 16 bytes at a time.
 // The tensor cores are far from busy (a tenth at 8 heads a group); the 5th-generation ones would need
 // the codes converted through shared memory, rows filled up to 128, and the same bytes.
-// The tensor cores cut sums instead of rounding them. fp32: the two products of a tile of 16 tokens begin at 0 and are
-// added to the outputs by ordinary additions (a mean error of 4e-6 behind 8192 tokens and 2e-5 behind 32,768 otherwise; 2 % of
-// the time). bf16 ones stay in the sums of the products: some 4e-8 of a sum for each tile of a warp, 3e-4 behind 500,000
+// The tensor cores cut sums instead of rounding them. fp32: the two products of a tile of 16 tokens, and of 16 dims of a
+// score, begin at 0 and are added up by ordinary additions (otherwise outputs have a mean error of 4e-6 behind 8192 tokens and
+// 2e-5 behind 32,768, and with heads of 256 7.8e-7 of scores alone, 3.0e-7 so; 1 to 3 % of the time). bf16 ones stay in the sums of the products: some 4e-8 of a sum for each tile of a warp, 3e-4 behind 500,000
 // tokens, beside its own rounding's 2e-3 (added up outside, 256 requests of 512 to 8192 tokens take 414 us for 407).
 //
 // Bound by memory: each cached byte is read once. A warp streams tiles of 16 tokens
@@ -320,15 +320,23 @@ __global__ void __launch_bounds__(kStepWarps * 32, (StepConfig<D, kParts, kR>::k
 #pragma unroll
                     for (int t = 0; t < 2; ++t)
                         codes::to_f16x4<kCode>(w == 0 ? k[t].x : w == 1 ? k[t].y : w == 2 ? k[t].z : k[t].w, lo[t], hi[t]);
+                    float mine[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};  // of this step (kParts == 2)
 #pragma unroll
                     for (int x = kParts - 1; x >= 0; --x) {
                         if constexpr (kR == 16) {
-                            mma_f16(s[0], q[x], lo[0], hi[0]);
-                            mma_f16(s[1], q[x], lo[1], hi[1]);
+                            mma_f16(kParts == 2 ? mine[0] : s[0], q[x], lo[0], hi[0]);
+                            mma_f16(kParts == 2 ? mine[1] : s[1], q[x], lo[1], hi[1]);
                         } else {
                             const uint32_t tokens[4] = {lo[0], lo[1], hi[0], hi[1]};
-                            mma_f16(s[w & 1], tokens, q[x][0], q[x][1]);
+                            mma_f16(kParts == 2 ? mine[w & 1] : s[w & 1], tokens, q[x][0], q[x][1]);
                         }
+                    }
+                    if (kParts == 2) {
+#pragma unroll
+                        for (int t = 0; t < 2; ++t)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                if (kR == 16 || t == (w & 1)) s[t][e] += mine[t][e];
                     }
                 }
             }

@@ -65,6 +65,25 @@ def test_fp32_single_tokens_behind_many_each(H, Hkv, d, n, held):
 
 
 @gpu
+@pytest.mark.parametrize("H,d", [(8, 64), (8, 128), (8, 256), (96, 256)])
+def test_fp32_scores_of_single_tokens(H, d):
+    """Queries and keys of one sign, scores of some 50: a sum over d whose steps were all cut would be too small by d / 8 cuts of
+    half a 2^-23. Cut are the two products of a step of 16 by 2^-23 of their sum each, 2^-22 of the score; the steps' sum,
+    queries in 22 bits and what comes after are rounded either way, which leaves the mean over 200 rows and 300 keys."""
+    c = one_sign(200, 1, 300, H, 8, d, F32)
+    c["q"] = c["q"].abs()
+    c["k_cache"] = (c["k_cache"].view(torch.uint8) & 0x7f).view(E4M3)
+    scale = 128 / d
+    lse = cache_attn(**c, scale=scale, return_lse=True)[1]
+    k = c["k_cache"].view(200, -1, 8, 64, d).double().transpose(1, 2).reshape(200, 8, -1, d)[:, :, :300] * 2.0 ** -7
+    s = torch.einsum("nhd,nhjd->nhj", c["q"].double(), k.repeat_interleave(H // 8, 1)) * scale
+    want = torch.logsumexp(s, -1)
+    assert 20 < float(want.mean()) < 200
+    mean = float(((lse.double() - want) / want).mean())
+    assert abs(mean) < 2.0 ** -22 + 2.0 ** -23, mean
+
+
+@gpu
 @pytest.mark.parametrize("d,n,new,held", [(128, 152, 256, 1000000), (128, 152, 300, 300001), (128, 60, 256, 500000), (64, 155, 200, 400000),
                                           (256, 152, 128, 300000), (128, 1, 40, 66000)])
 def test_bf16_prompts_behind_very_many_tokens(d, n, new, held):

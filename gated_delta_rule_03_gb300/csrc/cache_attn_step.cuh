@@ -42,7 +42,7 @@ template <int D, int kParts, int kR> struct StepConfig {
     static constexpr int kSteps = D / 16;                 // k steps of the first product
     // Tiles under way for each warp, and blocks of an SM. 64 requests of 512 to 8192 tokens, 32 heads over 8: heads of 128 in
     // bf16 116 us, with a block less an SM 115, a stage less 112; heads of 64 75, 78 and 74; of 256 222, 253 and 210; 12
-    // heads a group 147, 153 and 146; fp32, heads of 128 122, 136 and 120.
+    // heads a group 147, 153 and 146; fp32, heads of 128 124, 138 and 122.
     static constexpr int kStages = D == 64 ? 6 : D == 256 ? (kParts == 2 ? 2 : 3) : kR == 8 && kParts == 1 ? 3 : 4;
     static constexpr int kBlocks = D == 64 ? (kParts == 2 ? 3 : 4) : D == 256 ? 2 : kParts == 2 ? (kR == 8 ? 3 : 2) : kR == 8 ? 4 : 3;  // per SM
     static constexpr int kStage = 2 * 16 * D;             // bytes: keys, then values
